@@ -7,6 +7,7 @@ module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 import os
@@ -24,10 +25,12 @@ ERR_WAIT_TIMEOUT, ERR_BAD_METADATA, ERR_TMEM_ALLOC = 1, 2, 4
 EXPORTED = [
     "msa_status_string", "msa_last_error", "msa_workspace_size", "msa_index_scores", "msa_select_blocks",
     "msa_attend_decode", "msa_attend_prefill", "msa_forward", "msa_forward_marked", "msa_forward_launches",
-    "msa_attend_decode_noalloc", "msa_check_wait_timeout",
+    "msa_attend_decode_noalloc", "msa_check_wait_timeout", "msa_append_cache", "msa_dense_workspace_size",
+    "msa_dense_forward",
 ]
 
 
+APPEND_WORKSPACE_BYTES = 256  # MSA_APPEND_WORKSPACE_BYTES
 DECODE_MAX_ROWS = 8  # sequences with up to this many rows take the decode kernels
 
 
@@ -43,6 +46,20 @@ class MsaProblem(C.Structure):
         ("page_size", C.c_int32), ("index_key_heads", C.c_int32), ("kv_dtype", C.c_int32),
         ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("num_decode_rows", C.c_int32),
     ]
+
+
+class MsaRope(C.Structure):
+    """Mirror of struct msa_rope."""
+    _fields_ = [("dim", C.c_int32), ("index_dim", C.c_int32), ("axes", C.c_int32), ("interleaved", C.c_int32),
+                ("turns", C.c_void_p), ("index_turns", C.c_void_p), ("axis", C.c_void_p), ("index_axis", C.c_void_p),
+                ("positions", C.c_void_p)]
+
+
+class MsaAppend(C.Structure):
+    """Mirror of struct msa_append."""
+    _fields_ = [(n, C.c_void_p) for n in ("k", "v", "ik", "q", "iq")] + \
+        [(n, C.c_int64) for n in ("k_stride", "v_stride", "ik_stride", "q_stride", "iq_stride")] + \
+        [(n, C.c_void_p) for n in ("k_cache", "v_cache", "ik_cache", "k_scale", "v_scale", "q_out", "iq_out")]
 
 
 class MsaError(RuntimeError):
@@ -72,11 +89,15 @@ def _load():
     lib.msa_forward_marked.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, C.c_size_t, vp,
                                        C.POINTER(vp), i32]
     lib.msa_forward_launches.argtypes = [P]
+    lib.msa_append_cache.argtypes = [P, C.POINTER(MsaAppend), C.POINTER(MsaRope), vp, C.c_size_t, vp]
+    lib.msa_dense_workspace_size.argtypes = [P, C.POINTER(C.c_size_t)]
+    lib.msa_dense_forward.argtypes = [P, vp, vp, vp, vp, vp, C.c_size_t, vp]
     lib.msa_check_wait_timeout.argtypes = [vp, C.c_size_t, C.c_uint32, vp]
     lib.msa_forward_launches.restype = i32
     for name in ["msa_workspace_size", "msa_index_scores", "msa_select_blocks", "msa_attend_decode",
                  "msa_attend_decode_noalloc", "msa_check_wait_timeout",
-                 "msa_attend_prefill", "msa_forward", "msa_forward_marked"]:
+                 "msa_attend_prefill", "msa_forward", "msa_forward_marked", "msa_append_cache",
+                 "msa_dense_workspace_size", "msa_dense_forward"]:
         getattr(lib, name).restype = C.c_int
     return lib
 
@@ -103,6 +124,11 @@ def _ptr(t):
 
 def _stream(device):
     return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(device):
+    """The device of a call made current for its launches (free when it already is)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _need(t, name, dtype, device, shape=None):
@@ -204,6 +230,14 @@ class Problem:
 
     def workspace(self) -> torch.Tensor:
         return torch.empty(self.workspace_size(), dtype=torch.uint8, device=self.device)
+
+    def dense_workspace_size(self) -> int:
+        n = C.c_size_t(0)
+        _check(_lib.msa_dense_workspace_size(C.byref(self.c), C.byref(n)))
+        return int(n.value)
+
+    def dense_workspace(self) -> torch.Tensor:
+        return torch.empty(self.dense_workspace_size(), dtype=torch.uint8, device=self.device)
 
     def forward_launches(self) -> int:
         return int(_lib.msa_forward_launches(C.byref(self.c)))
@@ -318,6 +352,120 @@ def forward(pb: Problem, q, iq, k, v, ik, out=None, sel=None, nsel=None, workspa
     return out, sel, nsel
 
 
+class Rope:
+    """Rotary positions for append_cache: the tables of struct msa_rope.
+
+    dim, index_dim: rotated dimensions of the q/k heads and of the iq/ik heads (0: none; multiples of 16).
+    theta: pair j of dim turns by theta ** (-2j / dim) radians per position.
+    axes, axis, index_axis: with several position axes, the axis of each pair ([dim / 2] and [index_dim / 2] int32).
+    interleaved: pairs are (2j, 2j + 1) instead of (j, j + dim / 2).
+    """
+
+    def __init__(self, dim, index_dim=0, theta=10000.0, device="cuda", axes=1, axis=None, index_axis=None,
+                 interleaved=False):
+        self.dim, self.index_dim, self.axes, self.interleaved = int(dim), int(index_dim), int(axes), bool(interleaved)
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+
+        def turns(n):  # turns per position in units of 2^-64, as the bits of an int64
+            t = [int(theta ** (-2.0 * j / n) / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for j in range(n // 2)]
+            return torch.tensor([x - (1 << 64) if x >> 63 else x for x in t], dtype=torch.int64, device=self.device)
+
+        def axis_of(x, n, name):
+            if self.axes == 1 or n == 0:
+                return None
+            if x is None:
+                raise ValueError(f"{name} must be given with several axes")
+            x = torch.as_tensor(x, dtype=torch.int32).to(self.device).contiguous()
+            if tuple(x.shape) != (n // 2,):
+                raise ValueError(f"{name} must have shape ({n // 2},), got {tuple(x.shape)}")
+            return x
+
+        self.turns, self.index_turns = turns(self.dim), turns(self.index_dim)
+        self.axis = axis_of(axis, self.dim, "axis")
+        self.index_axis = axis_of(index_axis, self.index_dim, "index_axis")
+
+
+def _rows(t, name, shape, device):
+    """Checks a bf16 [rows, heads, dim] view whose heads lie side by side; returns its row stride in elements."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise ValueError(f"{name}'s heads must lie side by side in each row")
+    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+
+
+def append_cache(pb: Problem, new_k, new_v, k, v, new_ik=None, ik=None, q=None, iq=None, rope=None, positions=None,
+                 workspace=None):
+    """msa_append_cache: rotates the new rows (rope) and stores new_k, new_v, new_ik in the caches k, v, ik.
+
+    New rows may be views of a wider projection (any row stride that is a multiple of 8).  positions: int32
+    [axes, rows], or None for each row's position in its sequence.  With an int8 cache the scales go to pb.k_scale
+    and pb.v_scale.  Returns (q, iq) rotated, each None when not given."""
+    a = MsaAppend()
+    R, HG = pb.total_rows, pb.H * pb.G
+    pb._check_cache(k, "k", pb.D)
+    pb._check_cache(v, "v", pb.D)
+    if (new_ik is None) != (ik is None):
+        raise ValueError("new_ik and ik go together")
+    q_out = iq_out = None
+    for name, t, shape in (("k", new_k, (R, pb.H, pb.D)), ("v", new_v, (R, pb.H, pb.D)), ("ik", new_ik, (R, pb.KH, pb.Di)),
+                           ("q", q, (R, HG, pb.D)), ("iq", iq, (R, pb.H, pb.Di))):
+        if t is not None:
+            setattr(a, name + "_stride", _rows(t, name if name in ("q", "iq") else "new_" + name, shape, pb.device))
+            setattr(a, name, t.data_ptr())
+    if ik is not None:
+        pb._check_cache(ik, "ik", pb.Di, pb.KH)
+        a.ik_cache = ik.data_ptr()
+    if q is not None:
+        q_out = torch.empty(R, HG, pb.D, dtype=torch.bfloat16, device=pb.device)
+        a.q_out = q_out.data_ptr()
+    if iq is not None:
+        iq_out = torch.empty(R, pb.H, pb.Di, dtype=torch.bfloat16, device=pb.device)
+        a.iq_out = iq_out.data_ptr()
+    a.k_cache, a.v_cache = k.data_ptr(), v.data_ptr()
+    if pb.k_scale is not None:
+        a.k_scale, a.v_scale = pb.k_scale.data_ptr(), pb.v_scale.data_ptr()
+    c_rope = None
+    if rope is not None:
+        if rope.device != pb.device:
+            raise ValueError(f"rope must be on {pb.device}, got {rope.device}")
+        c_rope = MsaRope(rope.dim, rope.index_dim, rope.axes, int(rope.interleaved), rope.turns.data_ptr(),
+                         rope.index_turns.data_ptr(), None if rope.axis is None else rope.axis.data_ptr(),
+                         None if rope.index_axis is None else rope.index_axis.data_ptr())
+        if positions is not None:
+            _need(positions, "positions", torch.int32, pb.device, (rope.axes, R))
+            c_rope.positions = positions.data_ptr()
+    elif positions is not None:
+        raise ValueError("positions need a rope")
+    ws = torch.empty(APPEND_WORKSPACE_BYTES, dtype=torch.uint8, device=pb.device) if workspace is None else workspace
+    _need(ws, "workspace", torch.uint8, pb.device)
+    with _on(pb.device):
+        _check(_lib.msa_append_cache(C.byref(pb.c), C.byref(a), None if c_rope is None else C.byref(c_rope), _ptr(ws),
+                                     ws.numel(), _stream(pb.device)))
+    return q_out, iq_out
+
+
+def dense_forward(pb: Problem, q, k, v, out=None, workspace=None):
+    """msa_dense_forward: attention of every row over all of its sequence's positions up to its own."""
+    pb._check_q(q)
+    pb._check_cache(k, "k", pb.D)
+    pb._check_cache(v, "v", pb.D)
+    out = pb.new_out() if out is None else out
+    _need(out, "out", pb.out_dtype, pb.device, (pb.total_rows, pb.H * pb.G, pb.D))
+    ws = pb.dense_workspace() if workspace is None else workspace
+    _need(ws, "workspace", torch.uint8, pb.device)
+    with _on(pb.device):
+        _check(_lib.msa_dense_forward(C.byref(pb.c), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(ws), ws.numel(),
+                                      _stream(pb.device)))
+    return out
+
+
 def check_wait_timeout(workspace, limit_us: int = 20000):
     """msa_check_wait_timeout: one bounded wait of the library runs out on purpose
     and sets the timeout bit (ERR_WAIT_TIMEOUT) of the workspace's error word."""
@@ -330,6 +478,6 @@ def error_word(workspace) -> int:
     return int(workspace[:4].view(torch.int32).item())
 
 
-__all__ = ["Problem", "MsaProblem", "MsaError", "index_scores", "select_blocks", "attend_decode", "attend_prefill",
+__all__ = ["Problem", "MsaProblem", "MsaAppend", "MsaRope", "Rope", "append_cache", "dense_forward", "MsaError", "index_scores", "select_blocks", "attend_decode", "attend_prefill",
            "attend_decode_noalloc", "check_wait_timeout",
            "forward", "error_word", "lib", "LIB_PATH", "EXPORTED"]

@@ -174,6 +174,44 @@ struct WidenArgs {
 };
 cudaError_t run_widen_kv(const WidenArgs& a, cudaStream_t stream);
 
+// Cache writer: the new rows of a call, rotated and stored (msa_append, msa_rope of the ABI).
+struct AppendArgs {
+    const uint16_t *k, *v, *ik, *q, *iq;
+    int64_t k_stride, v_stride, ik_stride, q_stride, iq_stride;  // elements
+    void *k_cache, *v_cache;
+    uint16_t* ik_cache;
+    float *k_scale, *v_scale;
+    uint16_t *q_out, *iq_out;
+    int rope_dim, rope_index_dim, axes, interleaved;
+    const uint64_t *turns, *index_turns;
+    const int32_t *axis, *index_axis, *positions;
+    const int32_t* cu_rows;
+    const int32_t* cache_lens;
+    CacheRows cache;
+    int num_seqs, H, G, KH, total_rows, max_rows_per_seq, max_cache_len, kv_int8;
+    int64_t cache_tokens;
+    uint32_t* err;
+};
+cudaError_t run_append_cache(const AppendArgs& a, cudaStream_t stream);
+
+// Attention over every cached position.
+struct DenseArgs {
+    const uint16_t* q;
+    const void* k;
+    const void* v;
+    const float* k_scale;  // int8 caches: [T, H]
+    const float* v_scale;
+    void* out;
+    const int32_t* cu_rows;
+    const int32_t* cache_lens;
+    CacheRows cache;
+    int num_seqs, H, G, total_rows, max_rows_per_seq, max_cache_len, kv_int8, out_bf16;
+    int64_t cache_tokens;
+    float scale_log2;  // softmax scale * log2(e)
+    uint32_t* err;
+};
+cudaError_t run_dense_simple(const DenseArgs& a, cudaStream_t stream);
+
 // Allocation-free decode attention: scratch in a file-scope device array
 // sized for at most kNoAllocMaxPairs (sequence, KV head) pairs per call.
 constexpr int kNoAllocMaxPairs = 32;

@@ -213,6 +213,16 @@ Layout layout_of(const msa_problem* p) {
     return l;
 }
 
+struct DenseLayout {
+    size_t err = 0, total = 0;
+};
+
+DenseLayout dense_layout(const msa_problem*) {
+    DenseLayout l;
+    l.total = 256;
+    return l;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -738,6 +748,167 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
         if ((s = marks.mark(3)) != MSA_OK || (s = marks.mark(4)) != MSA_OK) return s;
     }
     return MSA_OK;
+}
+
+static msa_status check_rows(const void* x, int64_t stride, int64_t width, const char* name) {
+    msa_status s = check_ptr(x, name);
+    if (s != MSA_OK) return s;
+    if (stride < width || stride % 8 != 0)
+        return fail(MSA_ERR_INVALID_ARG, "%s_stride must be a multiple of 8 and at least %lld (got %lld)", name,
+                    static_cast<long long>(width), static_cast<long long>(stride));
+    return MSA_OK;
+}
+
+static msa_status check_rope(const msa_problem* p, const msa_rope* r) {
+    if (r->dim < 0 || r->dim > p->head_dim || r->dim % 16 != 0)
+        return fail(MSA_ERR_UNSUPPORTED, "rope dim must be a multiple of 16 in [0, head_dim] (got %d)", r->dim);
+    if (r->index_dim < 0 || r->index_dim > p->index_dim || r->index_dim % 16 != 0)
+        return fail(MSA_ERR_UNSUPPORTED, "rope index_dim must be a multiple of 16 in [0, index_dim] (got %d)", r->index_dim);
+    if (r->axes < 1 || r->axes > 4) return fail(MSA_ERR_UNSUPPORTED, "rope axes must be 1 to 4 (got %d)", r->axes);
+    if (r->interleaved != 0 && r->interleaved != 1) return fail(MSA_ERR_INVALID_ARG, "rope interleaved must be 0 or 1");
+    if (r->dim > 0 && (!r->turns || (r->axes > 1 && !r->axis)))
+        return fail(MSA_ERR_INVALID_ARG, "rope turns (and axis, with several axes) must be given");
+    if (r->index_dim > 0 && (!r->index_turns || (r->axes > 1 && !r->index_axis)))
+        return fail(MSA_ERR_INVALID_ARG, "rope index_turns (and index_axis, with several axes) must be given");
+    if ((reinterpret_cast<uintptr_t>(r->turns) & 7u) || (reinterpret_cast<uintptr_t>(r->index_turns) & 7u) ||
+        (reinterpret_cast<uintptr_t>(r->axis) & 3u) || (reinterpret_cast<uintptr_t>(r->index_axis) & 3u) ||
+        (reinterpret_cast<uintptr_t>(r->positions) & 3u))
+        return fail(MSA_ERR_INVALID_ARG, "a rope array is misaligned");
+    return MSA_OK;
+}
+
+msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa_rope* rope, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    g_last_error.clear();
+    msa_status s;
+    if ((s = check_problem(p)) != MSA_OK) return s;
+    if (!a) return fail(MSA_ERR_INVALID_ARG, "append is null");
+    const int64_t H = p->num_kv_heads, HG = H * p->group_size, KH = ik_shared(p) ? 1 : H, D = p->head_dim, Di = p->index_dim;
+    if ((s = check_rows(a->k, a->k_stride, H * D, "k")) != MSA_OK || (s = check_rows(a->v, a->v_stride, H * D, "v")) != MSA_OK ||
+        (s = check_ptr(a->k_cache, "k_cache")) != MSA_OK || (s = check_ptr(a->v_cache, "v_cache")) != MSA_OK)
+        return s;
+    if ((a->ik == nullptr) != (a->ik_cache == nullptr) || (a->q == nullptr) != (a->q_out == nullptr) ||
+        (a->iq == nullptr) != (a->iq_out == nullptr))
+        return fail(MSA_ERR_INVALID_ARG, "ik and ik_cache, q and q_out, iq and iq_out go together");
+    if (a->ik && ((s = check_rows(a->ik, a->ik_stride, KH * Di, "ik")) != MSA_OK ||
+                  (s = check_ptr(a->ik_cache, "ik_cache")) != MSA_OK))
+        return s;
+    if (a->q && ((s = check_rows(a->q, a->q_stride, HG * D, "q")) != MSA_OK || (s = check_ptr(a->q_out, "q_out")) != MSA_OK))
+        return s;
+    if (a->iq && ((s = check_rows(a->iq, a->iq_stride, H * Di, "iq")) != MSA_OK ||
+                  (s = check_ptr(a->iq_out, "iq_out")) != MSA_OK))
+        return s;
+    if ((a->q && a->q_out == a->q && a->q_stride != HG * D) || (a->iq && a->iq_out == a->iq && a->iq_stride != H * Di))
+        return fail(MSA_ERR_INVALID_ARG, "q and iq can be rotated in place only where their rows are contiguous");
+    const bool i8 = p->kv_dtype == MSA_KV_INT8;
+    if (i8 != (a->k_scale != nullptr) || i8 != (a->v_scale != nullptr))
+        return fail(MSA_ERR_INVALID_ARG, "k_scale and v_scale are given for an int8 cache and for no other");
+    if ((reinterpret_cast<uintptr_t>(a->k_scale) & 3u) || (reinterpret_cast<uintptr_t>(a->v_scale) & 3u))
+        return fail(MSA_ERR_INVALID_ARG, "k_scale or v_scale is not 4-byte aligned");
+    if (rope && (s = check_rope(p, rope)) != MSA_OK) return s;
+    if (workspace == nullptr) return fail(MSA_ERR_WORKSPACE, "workspace is null");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (workspace_bytes < MSA_APPEND_WORKSPACE_BYTES)
+        return fail(MSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %d", workspace_bytes, MSA_APPEND_WORKSPACE_BYTES);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(uint32_t), st);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    msa::AppendArgs x{};
+    x.k = static_cast<const uint16_t*>(a->k);
+    x.v = static_cast<const uint16_t*>(a->v);
+    x.ik = static_cast<const uint16_t*>(a->ik);
+    x.q = static_cast<const uint16_t*>(a->q);
+    x.iq = static_cast<const uint16_t*>(a->iq);
+    x.k_stride = a->k_stride;
+    x.v_stride = a->v_stride;
+    x.ik_stride = a->ik_stride;
+    x.q_stride = a->q_stride;
+    x.iq_stride = a->iq_stride;
+    x.k_cache = a->k_cache;
+    x.v_cache = a->v_cache;
+    x.ik_cache = static_cast<uint16_t*>(a->ik_cache);
+    x.k_scale = a->k_scale;
+    x.v_scale = a->v_scale;
+    x.q_out = static_cast<uint16_t*>(a->q_out);
+    x.iq_out = static_cast<uint16_t*>(a->iq_out);
+    x.axes = 1;
+    if (rope) {
+        x.rope_dim = rope->dim;
+        x.rope_index_dim = rope->index_dim;
+        x.axes = rope->axes;
+        x.interleaved = rope->interleaved;
+        x.turns = rope->turns;
+        x.index_turns = rope->index_turns;
+        x.axis = rope->axes > 1 ? rope->axis : nullptr;
+        x.index_axis = rope->axes > 1 ? rope->index_axis : nullptr;
+        x.positions = rope->positions;
+    }
+    x.cu_rows = p->cu_rows;
+    x.cache_lens = p->cache_lens;
+    x.cache = cache_rows_of(p);
+    x.num_seqs = p->num_seqs;
+    x.H = p->num_kv_heads;
+    x.G = p->group_size;
+    x.KH = static_cast<int>(KH);
+    x.total_rows = p->total_rows;
+    x.max_rows_per_seq = p->max_rows_per_seq;
+    x.max_cache_len = p->max_cache_len;
+    x.kv_int8 = i8;
+    x.cache_tokens = p->cache_tokens;
+    x.err = static_cast<uint32_t*>(workspace);
+    e = msa::run_append_cache(x, st);
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "cache writer launch");
+}
+
+msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes) {
+    g_last_error.clear();
+    msa_status s = check_problem(p);
+    if (s != MSA_OK) return s;
+    if (!bytes) return fail(MSA_ERR_INVALID_ARG, "bytes is null");
+    *bytes = dense_layout(p).total;
+    return MSA_OK;
+}
+
+msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_cache, const void* v_cache, void* out,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error.clear();
+    msa_status s;
+    if ((s = check_problem(p)) != MSA_OK) return s;
+    if ((s = check_ptr(q, "q")) != MSA_OK || (s = check_ptr(k_cache, "k_cache")) != MSA_OK ||
+        (s = check_ptr(v_cache, "v_cache")) != MSA_OK || (s = check_ptr(out, "out")) != MSA_OK)
+        return s;
+    const DenseLayout l = dense_layout(p);
+    if (workspace == nullptr) return fail(MSA_ERR_WORKSPACE, "workspace is null");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (workspace_bytes < l.total)
+        return fail(MSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, l.total);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    msa::DenseArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = k_cache;
+    a.v = v_cache;
+    a.kv_int8 = p->kv_dtype == MSA_KV_INT8;
+    a.k_scale = a.kv_int8 ? p->k_scale : nullptr;
+    a.v_scale = a.kv_int8 ? p->v_scale : nullptr;
+    a.out = out;
+    a.out_bf16 = p->out_dtype == MSA_OUT_BF16;
+    a.cu_rows = p->cu_rows;
+    a.cache_lens = p->cache_lens;
+    a.cache = cache_rows_of(p);
+    a.num_seqs = p->num_seqs;
+    a.H = p->num_kv_heads;
+    a.G = p->group_size;
+    a.total_rows = p->total_rows;
+    a.max_rows_per_seq = p->max_rows_per_seq;
+    a.max_cache_len = p->max_cache_len;
+    a.cache_tokens = p->cache_tokens;
+    a.scale_log2 = scale_log2(p);
+    a.err = reinterpret_cast<uint32_t*>(ws + l.err);
+    e = msa::run_dense_simple(a, st);
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "dense attention launch");
 }
 
 msa_status msa_check_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t limit_us, void* stream) {

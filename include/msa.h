@@ -294,6 +294,89 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
  * mechanics, no counterpart in the pages). */
 int32_t msa_forward_launches(const msa_problem* p);
 
+/* ------------------------------------------------------------------------
+ * The caches' writer, and the attention over every cached position.  A model
+ * of this kind keeps every key in some of its layers and lets the indexer
+ * choose in the others; both read the caches that the writer fills.  The
+ * pages define neither interface; the formulas stand at each entry point. */
+
+/* Bytes of scratch that msa_append_cache needs: the error word alone. */
+#define MSA_APPEND_WORKSPACE_BYTES 256
+
+/* Rotary positions of msa_append_cache.  Pair j of a head (dimensions j and
+ * j + dim/2, or 2j and 2j+1 with `interleaved`) turns by the angle
+ *   2 pi frac(x * turns[j] / 2^64),   x = positions[axis[j]][r]
+ * (a 64-bit product modulo 2^64, so far positions lose nothing); dimensions
+ * from `dim` on stay as they are. */
+typedef struct msa_rope {
+    int32_t dim;         /* rotated dimensions of q and k heads: 0 (none) or a multiple of 16 <= head_dim   */
+    int32_t index_dim;   /* the same of iq and ik heads, <= index_dim of the problem                        */
+    int32_t axes;        /* 1 to 4 position axes (for example time, height, width)                          */
+    int32_t interleaved; /* 0: pairs (j, j + dim/2); 1: pairs (2j, 2j + 1)                                  */
+    const uint64_t* turns;       /* device [dim/2]: turns per position, in units of 2^-64 turn              */
+    const uint64_t* index_turns; /* device [index_dim/2]                                                    */
+    const int32_t* axis;         /* device [dim/2], each in [0, axes); NULL with one axis                   */
+    const int32_t* index_axis;   /* device [index_dim/2]; NULL with one axis                                */
+    const int32_t* positions;    /* device [axes, total_rows] (any sign); NULL: the row's position in its
+                                    sequence, on every axis                                                 */
+} msa_rope;
+
+/* What msa_append_cache reads and writes.  New rows are bf16; row r of x
+ * starts at x + r * x_stride elements and holds its heads side by side, so
+ * the parts of one fused projection can be passed as they lie.  Strides are
+ * multiples of 8 elements, at least the row's width; pointers are 16-byte
+ * aligned.  The caches are those of the problem (layout, paging, kv_dtype). */
+typedef struct msa_append {
+    const void* k;  /* [total_rows, H, D]; k, v and both caches are required */
+    const void* v;
+    const void* ik; /* [total_rows, KH, Di] (KH = 1 with a shared index key, else H), or NULL (then ik_cache is NULL) */
+    const void* q;  /* [total_rows, H*G, D], or NULL (then q_out is NULL)    */
+    const void* iq; /* [total_rows, H, Di], or NULL (then iq_out is NULL)    */
+    int64_t k_stride, v_stride, ik_stride, q_stride, iq_stride;
+    void* k_cache;
+    void* v_cache;
+    void* ik_cache;
+    float* k_scale; /* MSA_KV_INT8: [cache_tokens, H], written; else NULL    */
+    float* v_scale;
+    void* q_out;    /* [total_rows, H*G, D] bf16, contiguous; may be q itself when q_stride = H*G*D */
+    void* iq_out;   /* [total_rows, H, Di] bf16, contiguous; may be iq likewise                      */
+} msa_append;
+
+/* Rotates the new rows (rope NULL: no rotation) and stores them in the
+ * caches.  Row i of sequence b (n rows, length L) is position p = L - n + i
+ * and goes to that position's cache row.  Keys and index keys are rotated,
+ * values are not; q and iq are rotated into q_out and iq_out.  Rotation is
+ * done in fp32 and rounded once, to bf16 or to the int8 cache's codes:
+ *   scale = max_d |y_d| / 127,   code_d = round-to-nearest-even(y_d / scale)
+ * (clamped to [-127, 127]; zero codes for a zero head; a head that holds a
+ * NaN or an infinity gets a NaN or infinite scale and zero codes, which read
+ * back as NaN).  Cache rows of other positions are left as they were, and so
+ * are rows of q_out and iq_out at or past cu_rows[num_seqs].  Two positions
+ * that share a cache row (a page listed twice) are the caller's error.
+ * Metadata errors go to the error word in the workspace's first 4 bytes, as
+ * for msa_workspace_size's workspace; a row with bad metadata is not stored. */
+msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa_rope* rope, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Bytes of scratch that msa_dense_forward needs for problem p (host only;
+ * same conventions and error word as msa_workspace_size). */
+msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
+
+/* Attention over every cached position (top_k plays no part):
+ *   out[r, h*G+g] = softmax_t(softmax_scale * q[r,h*G+g] . k[t,h]) . v[t,h]
+ *                   over t = 0 .. p
+ * for decode rows, drafted windows and prompt chunks (packed sequences of
+ * different lengths, each with its cached prefix) in one call; contiguous or
+ * paged caches, bf16 or int8 with scales.  Rows of a sequence share each
+ * read of a key or value.  Cache rows past a sequence's length may hold
+ * anything, NaN included.  Rows of out at or past cu_rows[num_seqs] are left
+ * as they were; a sequence of no rows is skipped.
+ * With fp32 outputs the softmax weights enter the products with V as three
+ * bf16 parts (all 24 bits); with bf16 outputs as one part (prompt chunks) or
+ * two (decode rows). */
+msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_cache, const void* v_cache,
+                             void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Diagnostics of the failure path (library mechanics, no counterpart in the
  * pages).  Every barrier wait in the library's
  * kernels gives up after a time limit, sets bit 1 of the device error word
