@@ -1,0 +1,698 @@
+// Attention over every cached position, decode family (1 to 8 rows a sequence).
+//   out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m),  x_t = scale log2(e) q.k_t,  m = max_t x_t
+// in one pass: a running maximum m, sum l and unnormalised output O per (row, query head), rescaled by
+// 2^(m - m') when the maximum grows, and the parts of a sequence that several CTAs walk joined by the same rule.
+//
+// Bound by memory: each cached position is H x 512 bytes (264 with an int8 cache) that are read once for all query
+// heads of the sequence's rows.  The cache is split over its length: one CTA per SM takes an even share of all
+// 64-position blocks of all sequences (from the lengths on the device, so ragged batches balance) and streams them
+// through a ring of shared-memory stages, one (block, KV head) tile of K and V each, by TMA boxes issued by a
+// producer warp.  Heads of a block are neighbours in the ring, so memory is read in whole 64 H-row runs.  Eight
+// consumer warps take the tiles in turn; 8 is a multiple of H, so a warp stays with one head and keeps its queries (A
+// operand, 16 (row, head) pairs) and O (accumulators) in registers.  S = Q K^T and O += P V run on mma.sync
+// m16n8k16: 16 rows are all a tile has (tcgen05 wants 128), and 12 to 16 FLOP a byte are well within its rate.
+//
+// P enters the second product as two bf16 parts (2^-16 of a weight; bf16 outputs) or three (2^-24; fp32 outputs),
+// taken from the accumulators of the first as they lie.  int8 tiles are widened in registers, exactly (an int8 value
+// has 8 significant bits): the order of the dimensions inside a dot product and of the output columns is free, so
+// each lane takes 16-byte runs of its keys and needs no transposition.  The key scale multiplies the score and the
+// value scale the weight.
+//
+// Where a sequence begins and ends inside one CTA, the CTA writes its output; else each CTA leaves its part (O, m,
+// l) in the workspace, at most two a CTA, and dense_combine_kernel joins them.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace msa {
+
+constexpr int kDdConsumers = 8;
+// Two warpgroups of consumers and one whose first warp is the producer.  Registers move from the last to the others:
+// launched with 168 a thread (64,512), 256 x 208 + 128 x 88 = 64,512 after the split.
+constexpr int kDdThreads = 384;
+constexpr int kDdMergeWords = 64 + 4;  // O, m and l of a lane
+
+// Tile i lands in stage i % kStages and completes barrier i % 16.  16 is a multiple of the consumers, so each of them
+// sees its barriers' phases one after the other (a warp that saw only some of a stage's phases could not tell them
+// apart by their parity), and with at most 16 stages no barrier is armed again before its last phase was seen.
+constexpr int kDdFull = 16;
+
+template <bool kInt8>
+struct DdCfg {
+    static constexpr int kPlane = kInt8 ? kBlock * kHeadDim : kBlock * kHeadDim * 2;  // K or V of a tile
+    static constexpr int kStageBytes = 2 * kPlane + (kInt8 ? 1024 : 0);               // int8: 64 key, 64 value scales
+    static constexpr int kStages = kInt8 ? 9 : 5;
+    static constexpr int kMergeBytes = 4 * kDdMergeWords * 32 * 4;
+    static_assert(kStages <= kDdFull, "a tile's barrier must not be armed twice ahead of its consumer");
+    static constexpr int kBarArrivals = kInt8 ? 33 : 1;  // the producer lane, and the scale copies of the 32 lanes
+};
+
+__device__ __forceinline__ void dd_ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void dd_ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void dd_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float dd_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint4 dd_lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+// Two int8 values, in the low bytes of t's halves, as two bf16: (128 + low 7 bits) - (128, or 256 with the sign bit).
+__device__ __forceinline__ uint32_t dd_widen2(uint32_t t) {
+    const uint32_t x = (t & 0x007F007Fu) | 0x43004300u, y = (t & 0x00800080u) | 0x43004300u;
+    __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ void dd_sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// A sequence's place in the work: its blocks, tiles of 16 (row, head) pairs, and what its rows need.
+struct DdSeq {
+    int b, c0, n, L, blocks, tiles;
+};
+
+__device__ __forceinline__ int dd_blocks(int L) { return (L + kBlock - 1) / kBlock; }
+
+// Units (blocks x tiles) of sequence b; 0 if it is not of the decode family or its metadata is bad.
+__device__ __forceinline__ int dd_units(const DenseArgs& a, int b, bool& bad) {
+    bad = false;
+    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0;
+    if (n == 0 || n > kDecodeMaxRows) return 0;
+    const int L = a.cache_lens[b];
+    if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
+        !seq_rows_ok(a.cache, b, L, a.cache_tokens)) {
+        bad = true;
+        return 0;
+    }
+    return dd_blocks(L) * ((n * a.G + 15) / 16);
+}
+
+__device__ __forceinline__ DdSeq dd_seq(const DenseArgs& a, int b) {
+    DdSeq s;
+    s.b = b;
+    s.c0 = a.cu_rows[b];
+    s.n = a.cu_rows[b + 1] - s.c0;
+    s.L = a.cache_lens[b];
+    s.blocks = dd_blocks(s.L);
+    s.tiles = (s.n * a.G + 15) / 16;
+    return s;
+}
+
+// Writes two neighbouring outputs of (row, head) pair m of a sequence, heads of KV head h.
+__device__ __forceinline__ void dd_store2(const DenseArgs& a, const DdSeq& s, int h, int m, int d, float x, float y) {
+    const int i = m / a.G, g = m - i * a.G;
+    const int64_t o = ((static_cast<int64_t>(s.c0 + i) * a.H + h) * a.G + g) * kHeadDim + d;
+    if (a.out_bf16)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o) = pack_bf16x2(x, y);
+    else
+        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o) = make_float2(x, y);
+}
+
+template <int H, bool kInt8, int kParts>
+__global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __grid_constant__ CUtensorMap k_map,
+                                                                    const __grid_constant__ CUtensorMap v_map,
+                                                                    const DenseArgs a) {
+    using Cfg = DdCfg<kInt8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* merge = reinterpret_cast<float*>(ring + Cfg::kStages * Cfg::kStageBytes);
+    int32_t* prefix = reinterpret_cast<int32_t*>(ring + Cfg::kStages * Cfg::kStageBytes + Cfg::kMergeBytes);  // [num_seqs + 1]
+    __shared__ uint64_t full[kDdFull], empty[Cfg::kStages];
+    __shared__ int warp_tot[kDdThreads / 32];
+    __shared__ uint32_t err;
+    __shared__ float tail_w[kDdConsumers][16][kDecodeMaxRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < kDdFull; ++s) mbar_init(&full[s], Cfg::kBarArrivals);
+        for (int s = 0; s < Cfg::kStages; ++s) mbar_init(&empty[s], 1);
+        fence_mbar_init();
+        err = 0;
+        prefetch_tmap(&k_map);
+        prefetch_tmap(&v_map);
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // ---- exclusive prefix of the sequences' units (a block-wide scan, kDdThreads sequences at a time)
+    int carry = 0;
+    for (int base = 0; base < a.num_seqs; base += kDdThreads) {
+        const int b = base + tid;
+        bool bad = false;
+        const int units = b < a.num_seqs ? dd_units(a, b, bad) : 0;
+        if (bad && blockIdx.x == 0) atomicOr(&err, kErrBadMetadata);
+        int incl = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_tot[warp] = incl;
+        __syncthreads();
+        int before = 0, total = 0;
+        for (int w = 0; w < kDdThreads / 32; ++w) {
+            if (w < warp) before += warp_tot[w];
+            total += warp_tot[w];
+        }
+        if (b < a.num_seqs) prefix[b] = carry + before + incl - units;
+        __syncthreads();
+        carry += total;
+    }
+    if (tid == 0) prefix[a.num_seqs] = carry;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= a.num_seqs; b += kDdThreads) a.unit_prefix[b] = prefix[b];
+    const int64_t total = carry;
+    const int u0 = static_cast<int>(total * blockIdx.x / gridDim.x), u1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+    int first_b = 0;
+    {
+        int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= u0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (prefix[mid] <= u0) lo = mid; else hi = mid;
+        }
+        first_b = lo;
+    }
+
+    if (warp >= kDdConsumers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kDdConsumers) {
+        // ---------------- producer: 32 blocks' cache rows at a time, one lane each, then their tiles in order
+        int b = first_b, tile = 0;
+        bool alive = true;
+        for (int base = u0; base < u1 && alive; base += 32) {
+            const int u = base + lane;
+            int64_t row = -1;
+            int live = 0;
+            if (u < u1) {
+                while (u >= prefix[b + 1]) ++b;
+                const int L = a.cache_lens[b], blocks = dd_blocks(L);
+                const int j = (u - prefix[b]) % blocks;
+                live = min(kBlock, L - j * kBlock);
+                row = block_row(a.cache, b, static_cast<int64_t>(j) * kBlock);
+                if (row < 0) {  // page outside the pool: nothing of it is read (a box past the cache is zeros)
+                    atomicOr(&err, kErrBadMetadata);
+                    row = a.cache_tokens;
+                    live = 0;
+                }
+            }
+            const int count = min(32, u1 - base);
+            for (int i = 0; i < count && alive; ++i) {
+                const int64_t r = __shfl_sync(0xffffffffu, row, i);
+                const int n = __shfl_sync(0xffffffffu, live, i);
+#pragma unroll 1
+                for (int h = 0; h < H; ++h, ++tile) {
+                    const int s = tile % Cfg::kStages;
+                    int ok = 1;
+                    if (lane == 0 && tile >= Cfg::kStages) ok = mbar_wait(&empty[s], ((tile / Cfg::kStages) - 1) & 1, &err);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        alive = false;
+                        break;
+                    }
+                    uint8_t* st = ring + s * Cfg::kStageBytes;
+                    uint64_t* bar = &full[tile % kDdFull];
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, 2 * Cfg::kPlane);
+                        if constexpr (kInt8) {
+                            tma_load_3d(st, &k_map, bar, 0, h, static_cast<int>(r));
+                            tma_load_3d(st + Cfg::kPlane, &v_map, bar, 0, h, static_cast<int>(r));
+                        } else {
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+                                tma_load_3d(st + half * (Cfg::kPlane / 2), &k_map, bar, 64 * half, h, static_cast<int>(r));
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+                                tma_load_3d(st + Cfg::kPlane + half * (Cfg::kPlane / 2), &v_map, bar, 64 * half, h,
+                                            static_cast<int>(r));
+                        }
+                    }
+                    if constexpr (kInt8) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {  // 64 key scales, 64 value scales; those past the length are not read
+                            const int key = (c & 1) * 32 + lane;
+                            const float* src = (c < 2 ? a.k_scale : a.v_scale) + (r + key) * H + h;
+                            const uint32_t dst = smem_u32(st + 2 * Cfg::kPlane + (c >> 1) * 256 + key * 4);
+                            if (key < n) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+                        }
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+                    }
+                }
+            }
+        }
+        // no copy of this warp may be in flight when the CTA ends
+        if (lane == 0)
+            for (int s = 0; s < kDdFull && s < tile; ++s) mbar_wait(&full[s], ((tile - 1 - s) / kDdFull) & 1, &err);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ---------------- consumer warp: tiles warp, warp + 8, ... of the CTA, all of head warp % H
+        const int grp = lane >> 2, tig = lane & 3, h = warp % H;
+        bool alive = true;
+        int i = warp, b = first_b;
+        for (int u = u0; u < u1;) {
+            while (u >= prefix[b + 1]) ++b;
+            const DdSeq s = dd_seq(a, b);
+            const int mt = (u - prefix[b]) / s.blocks, seg0 = prefix[b] + mt * s.blocks, seg1 = seg0 + s.blocks;
+            const int end = min(u1, seg1);  // this CTA's part of the tile: units [u, end)
+            const int pairs = min(16, s.n * a.G - 16 * mt);
+            // rows grp and grp + 8 of the tile: (row, head) pair, position, whether it exists
+            int pos[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) pos[e] = s.L - s.n + min(16 * mt + grp + 8 * e, s.n * a.G - 1) / a.G;
+            const int first_pos = s.L - s.n + 16 * mt / a.G;  // the tile's earliest row
+            uint32_t qa[8][4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int m = 16 * mt + min(grp + 8 * e, pairs - 1), qi = m / a.G, g = m - qi * a.G;
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                    a.q + ((static_cast<int64_t>(s.c0 + qi) * H + h) * a.G + g) * kHeadDim);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    // bf16: dims 16 ks + 2 tig, + 8; int8: dims 32 tig + 4 ks, + 2 (the order the lane's key bytes have)
+                    qa[ks][e] = src[kInt8 ? 16 * tig + 2 * ks : 8 * ks + tig];
+                    qa[ks][2 + e] = src[kInt8 ? 16 * tig + 2 * ks + 1 : 8 * ks + 4 + tig];
+                }
+            }
+            float o[16][4], mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < 16; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+
+            for (; i < (end - u0) * H; i += kDdConsumers) {
+                const int st = i % Cfg::kStages, j = u0 + i / H - seg0, t0 = j * kBlock;
+                if (alive) alive = mbar_wait(&full[i % kDdFull], (i / kDdFull) & 1, &err);
+                if (!alive) continue;
+                uint8_t* stage = ring + st * Cfg::kStageBytes;
+                const uint32_t kb = smem_u32(stage), vb = kb + Cfg::kPlane;
+                const bool edge = t0 + kBlock > first_pos + 1;  // some key is hidden from some row
+                float c[8][4];
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+                    if constexpr (kInt8) {
+                        const int row = nt * 8 + grp;
+                        const uint4 w0 = dd_lds128(kb + row * 128 + (((2 * tig) ^ (row & 7)) << 4));
+                        const uint4 w1 = dd_lds128(kb + row * 128 + (((2 * tig + 1) ^ (row & 7)) << 4));
+                        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            dd_mma(c[nt], qa[ks], dd_widen2(__byte_perm(w[ks], 0, 0x4140)), dd_widen2(__byte_perm(w[ks], 0, 0x4342)));
+                    } else {
+                        const int row = nt * 8 + (lane & 7);
+#pragma unroll
+                        for (int k2 = 0; k2 < 4; ++k2) {  // 32 dims: chunks of 8 dims 4 (k2 & 1) .. + 3 of a half
+                            uint32_t r[4];
+                            const int chunk = (k2 & 1) * 4 + (lane >> 3);
+                            dd_ldsm_x4(kb + (k2 >> 1) * (Cfg::kPlane / 2) + row * 128 + ((chunk ^ (row & 7)) << 4), r);
+                            dd_mma(c[nt], qa[2 * k2], r[0], r[1]);
+                            dd_mma(c[nt], qa[2 * k2 + 1], r[2], r[3]);
+                        }
+                    }
+                }
+                // scores in the log2 domain; hidden keys -inf
+                float vs[8][2];
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    float f0 = a.scale_log2, f1 = a.scale_log2;
+                    if constexpr (kInt8) {
+                        const float2 ks = *reinterpret_cast<const float2*>(stage + 2 * Cfg::kPlane + (nt * 8 + 2 * tig) * 4);
+                        const float2 v2 = *reinterpret_cast<const float2*>(stage + 2 * Cfg::kPlane + 256 + (nt * 8 + 2 * tig) * 4);
+                        f0 *= ks.x;
+                        f1 *= ks.y;
+                        vs[nt][0] = v2.x;
+                        vs[nt][1] = v2.y;
+                    }
+                    c[nt][0] *= f0;
+                    c[nt][1] *= f1;
+                    c[nt][2] *= f0;
+                    c[nt][3] *= f1;
+                    if (edge) {
+                        const int t = t0 + nt * 8 + 2 * tig;
+                        if (t > pos[0]) c[nt][0] = -INFINITY;
+                        if (t + 1 > pos[0]) c[nt][1] = -INFINITY;
+                        if (t > pos[1]) c[nt][2] = -INFINITY;
+                        if (t + 1 > pos[1]) c[nt][3] = -INFINITY;
+                    }
+                }
+                float top[2] = {mrun[0], mrun[1]};
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    top[0] = fmaxf(top[0], fmaxf(c[nt][0], c[nt][1]));
+                    top[1] = fmaxf(top[1], fmaxf(c[nt][2], c[nt][3]));
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                }
+                if (__any_sync(0xffffffffu, top[0] > mrun[0] || top[1] > mrun[1])) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = mrun[e] == -INFINITY ? 0.f : dd_exp2(mrun[e] - top[e]);
+                        lrun[e] *= f;
+                        mrun[e] = top[e];
+#pragma unroll
+                        for (int nt = 0; nt < 16; ++nt) {
+                            o[nt][2 * e] *= f;
+                            o[nt][2 * e + 1] *= f;
+                        }
+                    }
+                }
+                const float base0 = mrun[0] == -INFINITY ? 0.f : mrun[0], base1 = mrun[1] == -INFINITY ? 0.f : mrun[1];
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    c[nt][0] = dd_exp2(c[nt][0] - base0);
+                    c[nt][1] = dd_exp2(c[nt][1] - base0);
+                    c[nt][2] = dd_exp2(c[nt][2] - base1);
+                    c[nt][3] = dd_exp2(c[nt][3] - base1);
+                }
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    sum[0] += c[nt][0] + c[nt][1];
+                    sum[1] += c[nt][2] + c[nt][3];
+                }
+                lrun[0] += sum[0];
+                lrun[1] += sum[1];
+                if constexpr (kInt8) {
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt) {
+                        // a hidden key's weight stays 0 whatever its scale is
+                        c[nt][0] = edge && c[nt][0] == 0.f ? 0.f : c[nt][0] * vs[nt][0];
+                        c[nt][1] = edge && c[nt][1] == 0.f ? 0.f : c[nt][1] * vs[nt][1];
+                        c[nt][2] = edge && c[nt][2] == 0.f ? 0.f : c[nt][2] * vs[nt][0];
+                        c[nt][3] = edge && c[nt][3] == 0.f ? 0.f : c[nt][3] * vs[nt][1];
+                    }
+                } else if (edge) {
+                    // Keys hidden from some row may hold anything: their values leave the products (zeroed in
+                    // the stage) and those that later rows do see are added one by one below.
+                    const int first = max(0, first_pos + 1 - t0);  // first such key of the block
+                    const int last = min(kBlock, s.L - t0);         // keys from `last` on belong to no row
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = nt * 8 + 2 * tig + (e & 1);
+                            if (key >= first) {
+                                if (key < last) tail_w[warp][grp + 8 * (e >> 1)][key - first] = c[nt][e];
+                                c[nt][e] = 0.f;
+                            }
+                        }
+                    __syncwarp();
+                    for (int key = first; key < last; ++key) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (t0 + key > pos[e]) continue;
+                            const float w = tail_w[warp][grp + 8 * e][key - first];
+#pragma unroll
+                            for (int nt = 0; nt < 16; ++nt) {
+                                const int chunk = nt & 7;
+                                const uint32_t v2 = *reinterpret_cast<const uint32_t*>(
+                                    stage + Cfg::kPlane + (nt >> 3) * (Cfg::kPlane / 2) + key * 128 +
+                                    ((chunk ^ (key & 7)) << 4) + 4 * tig);
+                                o[nt][2 * e] = fmaf(w, bf16_lo(v2), o[nt][2 * e]);
+                                o[nt][2 * e + 1] = fmaf(w, bf16_hi(v2), o[nt][2 * e + 1]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    for (int x = first * 16 + lane; x < kBlock * 16; x += 32) {
+                        const int key = x >> 4, chunk = x & 15;
+                        *reinterpret_cast<uint4*>(stage + Cfg::kPlane + (chunk >> 3) * (Cfg::kPlane / 2) + key * 128 +
+                                                  (((chunk & 7) ^ (key & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
+                    __syncwarp();
+                }
+                // O += P V, 16 keys a step
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    uint32_t pa[kParts][4];
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        float x = c[2 * kk + (f >> 1)][2 * (f & 1)], y = c[2 * kk + (f >> 1)][2 * (f & 1) + 1];
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) {
+                            pa[part][f] = pack_bf16x2(x, y);
+                            x -= bf16_lo(pa[part][f]);
+                            y -= bf16_hi(pa[part][f]);
+                        }
+                    }
+                    if constexpr (kInt8) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int key = 16 * kk + 2 * tig + (q & 1) + 8 * (q >> 1);
+                            w[q] = dd_lds128(vb + key * 128 + ((grp ^ (key & 7)) << 4));
+                        }
+                        const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+                        const uint32_t w2[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, w3[4] = {w[3].x, w[3].y, w[3].z, w[3].w};
+#pragma unroll
+                        for (int nt = 0; nt < 16; ++nt) {  // output column grp of n-tile nt is dim 16 grp + nt
+                            const uint32_t sel = (nt & 3) | ((4 + (nt & 3)) << 8);
+                            const uint32_t b0 = dd_widen2(__byte_perm(w0[nt >> 2], w1[nt >> 2], sel));
+                            const uint32_t b1 = dd_widen2(__byte_perm(w2[nt >> 2], w3[nt >> 2], sel));
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part) dd_mma(o[nt], pa[part], b0, b1);
+                        }
+                    } else {
+                        const int key = 16 * kk + (lane & 15);
+#pragma unroll
+                        for (int n2 = 0; n2 < 8; ++n2) {  // 16 dims
+                            uint32_t r[4];
+                            const int chunk = (n2 & 3) * 2 + (lane >> 4);
+                            dd_ldsm_x4_t(vb + (n2 >> 2) * (Cfg::kPlane / 2) + key * 128 + ((chunk ^ (key & 7)) << 4), r);
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part) {
+                                dd_mma(o[2 * n2], pa[part], r[0], r[1]);
+                                dd_mma(o[2 * n2 + 1], pa[part], r[2], r[3]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
+            }
+
+            // ---- the warps of a head join their parts (8 / H of them, by halves)
+#pragma unroll
+            for (int half = kDdConsumers / 2; half >= H; half >>= 1) {
+                dd_sync_consumers();
+                if (warp >= half && warp < 2 * half) {
+                    float* dst = merge + (warp - half) * (kDdMergeWords * 32) + lane;
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) dst[x * 32] = o[x >> 2][x & 3];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        dst[(64 + e) * 32] = mrun[e];
+                        dst[(66 + e) * 32] = lrun[e];
+                    }
+                }
+                dd_sync_consumers();
+                if (warp < half) {
+                    const float* src = merge + warp * (kDdMergeWords * 32) + lane;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float m2 = src[(64 + e) * 32], m = fmaxf(mrun[e], m2);
+                        const float f1 = mrun[e] == -INFINITY ? 0.f : dd_exp2(mrun[e] - m);
+                        const float f2 = m2 == -INFINITY ? 0.f : dd_exp2(m2 - m);
+                        mrun[e] = m;
+                        lrun[e] = lrun[e] * f1 + src[(66 + e) * 32] * f2;
+#pragma unroll
+                        for (int nt = 0; nt < 16; ++nt)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                o[nt][2 * e + y] = o[nt][2 * e + y] * f1 + src[(nt * 4 + 2 * e + y) * 32] * f2;
+                    }
+                }
+            }
+            if (warp < H) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    lrun[e] += __shfl_xor_sync(0xffffffffu, lrun[e], 1);
+                    lrun[e] += __shfl_xor_sync(0xffffffffu, lrun[e], 2);
+                }
+                const bool whole = u == seg0 && end == seg1;
+                const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * H + h;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int m = grp + 8 * e;
+                    if (m >= pairs) continue;
+                    float* part = a.part_o + (slot * 16 + m) * kHeadDim;
+                    const float f = whole ? 1.f / lrun[e] : 1.f;
+                    if (!whole && tig == 0)
+                        *reinterpret_cast<float2*>(a.part_ml + (slot * 16 + m) * 2) = make_float2(mrun[e], lrun[e]);
+#pragma unroll
+                    for (int nt = 0; nt < 16; ++nt) {
+                        float x = o[nt][2 * e] * f, y = o[nt][2 * e + 1] * f;
+                        int d = nt * 8 + 2 * tig;
+                        if constexpr (kInt8) {
+                            // columns 2 tig and 2 tig + 1 are dims 32 tig + nt and 32 tig + 16 + nt: two n-tiles make pairs
+                            if (nt & 1) continue;
+                            const float x1 = o[nt + 1][2 * e] * f, y1 = o[nt + 1][2 * e + 1] * f;
+                            d = 32 * tig + nt;
+                            if (whole) {
+                                dd_store2(a, s, h, 16 * mt + m, d, x, x1);
+                                dd_store2(a, s, h, 16 * mt + m, d + 16, y, y1);
+                            } else {
+                                *reinterpret_cast<float2*>(part + d) = make_float2(x, x1);
+                                *reinterpret_cast<float2*>(part + d + 16) = make_float2(y, y1);
+                            }
+                        } else if (whole) {
+                            dd_store2(a, s, h, 16 * mt + m, d, x, y);
+                        } else {
+                            *reinterpret_cast<float2*>(part + d) = make_float2(x, y);
+                        }
+                    }
+                }
+            }
+            u = end;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) a.err_slots[blockIdx.x] = err;
+}
+
+// Joins the parts of the sequences that several CTAs walked.  CTA (c, h) takes the (sequence, tile) in which boundary
+// c + 1 of the shares is the first to fall, if any; a warp takes one (row, head) pair: the parts' maxima and sums
+// first, then 2^(m_i - m) O_i summed in the parts' order (the same every time), 4 of the 128 values a lane.
+constexpr int kDcThreads = 512;
+__global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseArgs a, int shares) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0 && h == 0 && warp == 0) {  // what the shares' CTAs found wrong
+        uint32_t e = 0;
+        for (int c = lane; c < shares; c += 32) e |= a.err_slots[c];
+        e = __reduce_or_sync(0xffffffffu, e);
+        if (lane == 0) {
+            if (a.err_store) *a.err = e;
+            else if (e) atomicOr(a.err, e);
+        }
+    }
+    const int64_t total = a.unit_prefix[a.num_seqs];
+    const int c = blockIdx.x;  // boundary between shares c and c + 1
+    if (c + 1 >= shares) return;
+    const int cut = static_cast<int>(total * (c + 1) / shares);
+    if (cut <= 0 || cut >= total) return;
+    int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= cut
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.unit_prefix[mid] <= cut) lo = mid; else hi = mid;
+    }
+    const DdSeq s = dd_seq(a, lo);
+    const int mt = (cut - a.unit_prefix[lo]) / s.blocks, seg0 = a.unit_prefix[lo] + mt * s.blocks, seg1 = seg0 + s.blocks;
+    if (cut == seg0) return;  // the boundary lies between two of them
+    // an earlier boundary inside the same one (strictly): its CTA joins them
+    if (c > 0 && static_cast<int>(total * c / shares) > seg0) return;
+    int last = c + 1;  // last share that holds a part of it
+    while (last + 1 < shares && static_cast<int>(total * (last + 1) / shares) < seg1) ++last;
+    const int count = last - c + 1;
+    const int pairs = min(16, s.n * a.G - 16 * mt);
+    if (warp >= pairs) return;
+    // share c's part began inside the share unless it began with it; the others' begin with their shares.  A share
+    // of no units (more shares than units) has no part.
+    auto slot_of = [&](int i) {
+        const int sh = c + i;
+        return (2 * static_cast<int64_t>(sh) + (i == 0 && static_cast<int>(total * sh / shares) < seg0 ? 1 : 0)) * a.H + h;
+    };
+    auto empty = [&](int i) { return total * (c + i) / shares == total * (c + i + 1) / shares; };
+    float m = -INFINITY;
+    for (int i = lane; i < count; i += 32)
+        if (!empty(i)) m = fmaxf(m, a.part_ml[(slot_of(i) * 16 + warp) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < count; i0 += 32) {
+        float f = 0.f;
+        int64_t at = 0;
+        if (i0 + lane < count && !empty(i0 + lane)) {
+            at = slot_of(i0 + lane) * 16 + warp;
+            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+            f = ml.x == -INFINITY ? 0.f : dd_exp2(ml.x - m);
+            l += ml.y * f;
+        }
+        const int n = min(32, count - i0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i);
+            const int64_t from = __shfl_sync(0xffffffffu, at, i);
+            const float4 v = *reinterpret_cast<const float4*>(a.part_o + from * kHeadDim + 4 * lane);
+            if (w != 0.f) {
+                x[0] = fmaf(w, v.x, x[0]);
+                x[1] = fmaf(w, v.y, x[1]);
+                x[2] = fmaf(w, v.z, x[2]);
+                x[3] = fmaf(w, v.w, x[3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = 1.f / l;
+    dd_store2(a, s, h, 16 * mt + warp, 4 * lane, x[0] * inv, x[1] * inv);
+    dd_store2(a, s, h, 16 * mt + warp, 4 * lane + 2, x[2] * inv, x[3] * inv);
+}
+
+template <int H, bool kInt8, int kParts>
+static cudaError_t launch_dense_decode(const DenseArgs& a, int grid, cudaStream_t stream) {
+    using Cfg = DdCfg<kInt8>;
+    const size_t smem = 1024 + static_cast<size_t>(Cfg::kStages) * Cfg::kStageBytes + Cfg::kMergeBytes +
+                        static_cast<size_t>(a.num_seqs + 1) * sizeof(int32_t);
+    auto* kernel = dense_decode_kernel<H, kInt8, kParts>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kDdThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, *a.k_map, *a.v_map, a)) != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(a.H), 1);
+    cfg.blockDim = dim3(kDcThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, dense_combine_kernel, a, grid);
+}
+
+int dense_decode_shares(int64_t units) {
+    const int64_t sms = std::min(device_sm_count(), kDenseMaxShares);
+    return static_cast<int>(units < 1 ? 1 : (units < sms ? units : sms));
+}
+
+template <int H>
+static cudaError_t launch_dense_decode_h(const DenseArgs& a, int grid, cudaStream_t stream) {
+    if (a.kv_int8)
+        return a.out_bf16 ? launch_dense_decode<H, true, 2>(a, grid, stream) : launch_dense_decode<H, true, 3>(a, grid, stream);
+    return a.out_bf16 ? launch_dense_decode<H, false, 2>(a, grid, stream) : launch_dense_decode<H, false, 3>(a, grid, stream);
+}
+
+cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream) {
+    switch (a.H) {
+        case 1: return launch_dense_decode_h<1>(a, shares, stream);
+        case 2: return launch_dense_decode_h<2>(a, shares, stream);
+        case 4: return launch_dense_decode_h<4>(a, shares, stream);
+        case 8: return launch_dense_decode_h<8>(a, shares, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace msa

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kDsThreads) dense_simple_kernel(const DenseArg
     __shared__ float ks[kDsKeys][kHeadDim], vs[kDsKeys][kHeadDim];
     const int b = blockIdx.x / tiles, tile = blockIdx.x - b * tiles, h = blockIdx.y, tid = threadIdx.x;
     const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0, L = a.cache_lens[b];
-    if (n == 0) return;
+    if (n == 0 || (a.only_multi_row && n > 0 && n <= kDecodeMaxRows)) return;
     if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
         !seq_rows_ok(a.cache, b, L, a.cache_tokens)) {
         if (tid == 0) atomicOr(a.err, kErrBadMetadata);

@@ -208,9 +208,20 @@ struct DenseArgs {
     int num_seqs, H, G, total_rows, max_rows_per_seq, max_cache_len, kv_int8, out_bf16;
     int64_t cache_tokens;
     float scale_log2;  // softmax scale * log2(e)
+    int only_multi_row;  // 1: the prompt kernel skips decode-family sequences
+    const CUtensorMap* k_map;  // host copies of the cache maps (kv_map)
+    const CUtensorMap* v_map;
+    int32_t* unit_prefix;  // [num_seqs + 1] decode family: units before each sequence
+    float* part_o;         // [2 shares, H, 16, 128] parts of sequences that several CTAs walk
+    float* part_ml;        // [2 shares, H, 16, 2]
+    uint32_t* err_slots;   // [shares] error bits of the decode family's CTAs
+    int err_store;         // 1: the combine stores the error word, 0: it adds to it
     uint32_t* err;
 };
+constexpr int kDenseMaxShares = 160;  // most CTAs that share the decode family's cache walk
 cudaError_t run_dense_simple(const DenseArgs& a, cudaStream_t stream);
+int dense_decode_shares(int64_t units);  // CTAs for so many blocks
+cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream);
 
 // Allocation-free decode attention: scratch in a file-scope device array
 // sized for at most kNoAllocMaxPairs (sequence, KV head) pairs per call.

@@ -214,12 +214,24 @@ Layout layout_of(const msa_problem* p) {
 }
 
 struct DenseLayout {
-    size_t err = 0, total = 0;
+    size_t err = 0, err_slots = 0, unit_prefix = 0, part_ml = 0, part_o = 0, total = 0;
 };
 
-DenseLayout dense_layout(const msa_problem*) {
+DenseLayout dense_layout(const msa_problem* p) {
     DenseLayout l;
-    l.total = 256;
+    const size_t parts = 2 * msa::kDenseMaxShares * static_cast<size_t>(p->num_kv_heads) * 16;
+    size_t off = 256;
+    l.err_slots = off;
+    off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
+    l.unit_prefix = off;
+    off = align256(off + (static_cast<size_t>(p->num_seqs) + 1) * sizeof(int32_t));
+    if (p->num_decode_seqs != 0) {
+        l.part_ml = off;
+        off = align256(off + parts * 2 * sizeof(float));
+        l.part_o = off;
+        off = align256(off + parts * msa::kHeadDim * sizeof(float));
+    }
+    l.total = off;
     return l;
 }
 
@@ -884,9 +896,19 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
         return fail(MSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, l.total);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    const bool dec = decode_family(p), pre = prefill_family(p);
+    cudaError_t e;
     msa::DenseArgs a{};
+    CUtensorMap km, vm;
+    if ((s = kv_map(&km, p, k_cache, "k_cache")) != MSA_OK || (s = kv_map(&vm, p, v_cache, "v_cache")) != MSA_OK) return s;
+    a.k_map = &km;
+    a.v_map = &vm;
+    a.unit_prefix = reinterpret_cast<int32_t*>(ws + l.unit_prefix);
+    a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+    a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+    a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
+    a.err_store = !pre;  // with prompt chunks the word is cleared first and every kernel adds to it
+    a.only_multi_row = dec;
     a.q = static_cast<const uint16_t*>(q);
     a.k = k_cache;
     a.v = v_cache;
@@ -907,8 +929,16 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.cache_tokens = p->cache_tokens;
     a.scale_log2 = scale_log2(p);
     a.err = reinterpret_cast<uint32_t*>(ws + l.err);
-    e = msa::run_dense_simple(a, st);
-    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "dense attention launch");
+    if (pre && (e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    if (dec) {
+        const int64_t seqs = p->num_decode_seqs > 0 ? p->num_decode_seqs : p->num_seqs;
+        const int64_t tiles = (static_cast<int64_t>(decode_rows_per_seq(p)) * p->group_size + 15) / 16;
+        const int64_t blocks = (p->max_cache_len + msa::kBlock - 1) / msa::kBlock;
+        if ((e = msa::run_dense_decode(a, msa::dense_decode_shares(seqs * tiles * blocks), st)) != cudaSuccess)
+            return cuda_fail(e, "dense decode attention launch");
+    }
+    if (pre && (e = msa::run_dense_simple(a, st)) != cudaSuccess) return cuda_fail(e, "dense prompt attention launch");
+    return MSA_OK;
 }
 
 msa_status msa_check_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t limit_us, void* stream) {
