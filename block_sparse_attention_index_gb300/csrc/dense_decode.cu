@@ -94,7 +94,7 @@ __device__ __forceinline__ int dd_blocks(int L) { return (L + kBlock - 1) / kBlo
 __device__ __forceinline__ int dd_units(const DenseArgs& a, int b, bool& bad) {
     bad = false;
     const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0;
-    if (n == 0 || n > kDecodeMaxRows) return 0;
+    if (n == 0 || n > kDecodeMaxRows || (a.tile_windows && n * a.G > 16)) return 0;
     const int L = a.cache_lens[b];
     if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
         !seq_rows_ok(a.cache, b, L, a.cache_tokens)) {
@@ -440,49 +440,73 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
                     __syncwarp();
                 }
-                // O += P V, 16 keys a step
+                // O += P V, 16 keys a step.  The tensor cores cut what an addition loses (a bias of about 2^-25 each,
+                // 1.5e-4 after 33,280 keys), so with fp32 outputs a tile is summed by itself and then added to O.
+                uint32_t pa[4][kParts][4];
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    uint32_t pa[kParts][4];
+                for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
                         float x = c[2 * kk + (f >> 1)][2 * (f & 1)], y = c[2 * kk + (f >> 1)][2 * (f & 1) + 1];
 #pragma unroll
                         for (int part = 0; part < kParts; ++part) {
-                            pa[part][f] = pack_bf16x2(x, y);
-                            x -= bf16_lo(pa[part][f]);
-                            y -= bf16_hi(pa[part][f]);
+                            pa[kk][part][f] = pack_bf16x2(x, y);
+                            x -= bf16_lo(pa[kk][part][f]);
+                            y -= bf16_hi(pa[kk][part][f]);
                         }
                     }
-                    if constexpr (kInt8) {
-                        uint4 w[4];
+                if constexpr (kInt8) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int key = 16 * kk + 2 * tig + (q & 1) + 8 * (q >> 1);
-                            w[q] = dd_lds128(vb + key * 128 + ((grp ^ (key & 7)) << 4));
+                    for (int n4 = 0; n4 < 4; ++n4) {  // n-tiles 4 n4 ..: output column grp of n-tile nt is dim 16 grp + nt
+                        float t[4][4];
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int key = 16 * kk + 2 * tig + (q & 1) + 8 * (q >> 1);
+                                w[q] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kPlane + key * 128 + ((grp ^ (key & 7)) << 4) + 4 * n4);
+                            }
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                const uint32_t sel = n | ((4 + n) << 8);
+                                const uint32_t b0 = dd_widen2(__byte_perm(w[0], w[1], sel));
+                                const uint32_t b1 = dd_widen2(__byte_perm(w[2], w[3], sel));
+#pragma unroll
+                                for (int part = 0; part < kParts; ++part) dd_mma(kParts == 3 ? t[n] : o[4 * n4 + n], pa[kk][part], b0, b1);
+                            }
                         }
-                        const uint32_t w0[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, w1[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
-                        const uint32_t w2[4] = {w[2].x, w[2].y, w[2].z, w[2].w}, w3[4] = {w[3].x, w[3].y, w[3].z, w[3].w};
+                        if constexpr (kParts == 3) {
 #pragma unroll
-                        for (int nt = 0; nt < 16; ++nt) {  // output column grp of n-tile nt is dim 16 grp + nt
-                            const uint32_t sel = (nt & 3) | ((4 + (nt & 3)) << 8);
-                            const uint32_t b0 = dd_widen2(__byte_perm(w0[nt >> 2], w1[nt >> 2], sel));
-                            const uint32_t b1 = dd_widen2(__byte_perm(w2[nt >> 2], w3[nt >> 2], sel));
+                            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                            for (int part = 0; part < kParts; ++part) dd_mma(o[nt], pa[part], b0, b1);
+                                for (int e = 0; e < 4; ++e) o[4 * n4 + n][e] += t[n][e];
                         }
-                    } else {
-                        const int key = 16 * kk + (lane & 15);
+                    }
+                } else {
 #pragma unroll
-                        for (int n2 = 0; n2 < 8; ++n2) {  // 16 dims
+                    for (int n2 = 0; n2 < 8; ++n2) {  // 16 dims
+                        float t[2][4];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
                             uint32_t r[4];
-                            const int chunk = (n2 & 3) * 2 + (lane >> 4);
+                            const int key = 16 * kk + (lane & 15), chunk = (n2 & 3) * 2 + (lane >> 4);
                             dd_ldsm_x4_t(vb + (n2 >> 2) * (Cfg::kPlane / 2) + key * 128 + ((chunk ^ (key & 7)) << 4), r);
 #pragma unroll
                             for (int part = 0; part < kParts; ++part) {
-                                dd_mma(o[2 * n2], pa[part], r[0], r[1]);
-                                dd_mma(o[2 * n2 + 1], pa[part], r[2], r[3]);
+                                dd_mma(kParts == 3 ? t[0] : o[2 * n2], pa[kk][part], r[0], r[1]);
+                                dd_mma(kParts == 3 ? t[1] : o[2 * n2 + 1], pa[kk][part], r[2], r[3]);
                             }
+                        }
+                        if constexpr (kParts == 3) {
+#pragma unroll
+                            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[2 * n2 + n][e] += t[n][e];
                         }
                     }
                 }

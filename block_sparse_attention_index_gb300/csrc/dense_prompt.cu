@@ -1,0 +1,840 @@
+// Attention over every cached position on tcgen05: prompt chunks (more than 8 rows a sequence), causal, packed, with
+// cached prefixes; and windows of several drafted rows.
+//   out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m),  x_t = scale log2(e) q.k_t over t <= p
+// in one pass over the keys with a running maximum.
+//
+// The G query heads of a KV head and P = 128 / G neighbouring positions make the 128 rows of an M tile (row = position
+// x G + head), so a tile's rows share every key and value and the causal edge crosses few key tiles.  A CTA holds two
+// such tiles ("stages") and walks the keys in tiles of NK:
+//   S_s[128, NK] = Q_s K^T     both operands from shared memory (TMA, 128-byte swizzle), S in tensor memory
+//   P_s = 2^(x - m)            softmax group s: one thread a row, S read from and P written over tensor memory
+//   O_s[128, 128] += P_s V     P from tensor memory, V as it lies ([key][dim], MN-major), O in tensor memory
+// While group 0 works on S_0 the tensor cores run P_1 V and S_1, and the other way round: 1,024 tensor cycles and two
+// softmax passes of 128 x 128 a tile pair.  Tensor memory is full: S_0, S_1, O_0, O_1 of 128 columns each.
+//
+// The running maximum is only raised when it would grow by more than 8 (a factor of 256 in the weights, which fp32
+// sums and bf16 weights carry without loss); the group that owns O then multiplies it in tensor memory.  So most tiles
+// rescale nothing.
+//
+// With bf16 outputs a weight enters P V as one bf16 (2^-9 relative, at random, about the output's own rounding); with
+// fp32 outputs as three parts (2^-24), NK = 64 then, so that the parts fit over S.  The tensor cores cut what an
+// addition loses instead of rounding it, a bias of about 2^-25 per addition (1.5e-4 after 33,280 keys, measured), so
+// with fp32 outputs O_s holds one key tile's product only and the softmax group adds it to its rows in registers.
+//
+// Drafted windows (kAlt): one M tile, and the two stages take alternate key tiles, each with its own running state.
+// When tiles alone leave SMs idle the key range is split as well; the parts are joined by dense_join_kernel.
+//
+// int8 caches are read from a copy widened once per call (run_widen_kv), scales beside it: the key scale multiplies
+// the score, the value scale the weight.
+//
+// Values that no row of the tile may see: positions past the length are zeroed in the last value tile (warp 10), so
+// stale cache rows do not matter.  A later token of the same chunk meets weights of zero; if its value is not finite
+// the product is NaN, so a row whose result is not finite is computed again key by key (dp_row_again).
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace msa {
+
+constexpr int kDpThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 copies, 9 matrix instructions, 10 last value tile
+constexpr int kDpQBytes = 128 * kHeadDim * 2;
+constexpr int kDpScaleSlots = 4;
+constexpr float kDpSlack = 8.f;  // log2 by which the running maximum may lag
+
+template <int kParts, bool kWide>
+struct DpCfg {
+    static constexpr int NK = kParts == 1 ? 128 : 64;
+    static constexpr int kTile = NK * kHeadDim * 2;  // bytes of a K or V tile
+    static constexpr int kStages = (kWide ? 4 : 5) * (128 / NK);
+};
+
+template <int kParts, bool kWide>
+struct __align__(1024) DpSmem {
+    using Cfg = DpCfg<kParts, kWide>;
+    uint8_t q[2][kDpQBytes];
+    uint8_t ring[Cfg::kStages][Cfg::kTile];
+    float sc[kWide ? kDpScaleSlots : 1][2][kWide ? 128 : 4];  // key and value scales of a tile
+    uint64_t full[Cfg::kStages], empty[Cfg::kStages];
+    uint64_t sc_full[kDpScaleSlots], sc_empty[kDpScaleSlots];
+    uint64_t q_full, v_last;
+    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem;
+    int32_t scan[kDpThreads / 32];
+    int32_t found[4];
+    float2 other_ml[128];  // drafted windows: maxima and sums of the second stream
+};
+static_assert(sizeof(DpSmem<1, false>) + 1024 <= 227 * 1024, "prompt attention exceeds 227 KB of shared memory");
+static_assert(sizeof(DpSmem<1, true>) + 1024 <= 227 * 1024, "prompt attention (int8) exceeds 227 KB of shared memory");
+static_assert(sizeof(DpSmem<3, false>) + 1024 <= 227 * 1024, "prompt attention (fp32) exceeds 227 KB of shared memory");
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void dp_ld32(uint32_t addr, float* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void dp_st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void dp_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float dp_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void dp_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Work of a launch: M tile pairs (kAlt: single tiles) of the sequences it takes.
+struct DpItem {
+    int b, tile;  // b < 0: none
+};
+
+template <bool kAlt>
+__device__ __forceinline__ int dp_tiles(const DenseArgs& a, int b, bool& bad) {
+    bad = false;
+    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0;
+    if (n == 0) return 0;
+    if (kAlt ? n < 0 || n > kDecodeMaxRows || n * a.G <= 16 : a.only_multi_row && n > 0 && n <= kDecodeMaxRows) return 0;
+    const int L = a.cache_lens[b];
+    if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
+        !seq_rows_ok(a.seq_cache, b, L, a.seq_cache_tokens)) {
+        bad = true;
+        return 0;
+    }
+    if (a.cache.table == nullptr && a.cache.starts[b] < 0) return 0;  // widened in another pass
+    const int rows = (128 / a.G) * (kAlt ? 1 : 2);
+    return (n + rows - 1) / rows;
+}
+
+// The block finds its item: the tiles of all sequences counted by a block-wide scan, the longest first (the last tile
+// of a sequence has the most keys).  Ends with every thread holding the same answer.
+template <bool kAlt, int kThreads>
+__device__ DpItem dp_find(const DenseArgs& a, int index, int items, int32_t* scan, int32_t* found) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.num_seqs + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, a.num_seqs), b1 = min(b0 + per, a.num_seqs);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        bool bad;
+        mine += dp_tiles<kAlt>(a, b, bad);
+        if (bad && blockIdx.x == 0) atomicOr(a.err, kErrBadMetadata);
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    int before = incl - mine, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    // more tiles than the host's row counts allow for: the first of them go without
+    if (total > items && blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrBadMetadata);
+    int want = total - 1 - index - before;
+    if (index < total && want >= 0 && want < mine) {
+        for (int b = b0; b < b1; ++b) {
+            bool bad;
+            const int t = dp_tiles<kAlt>(a, b, bad);
+            if (want < t) {
+                found[1] = want;
+                found[0] = b;
+                break;
+            }
+            want -= t;
+        }
+    }
+    __syncthreads();
+    return DpItem{found[0], found[1]};
+}
+
+// What an item covers.
+struct DpWork {
+    int b, c0, n, L, i0;      // sequence, its first row, rows, length; first row of the item in the sequence
+    int P;                    // positions of an M tile
+    int first;                // first key tile of this part
+    int count[2];             // key tiles of each stage
+    int total;                // key tiles loaded
+};
+
+template <bool kAlt, int NK>
+__device__ __forceinline__ DpWork dp_work(const DenseArgs& a, const DpItem& it, int split, int nsplit) {
+    DpWork w;
+    w.b = it.b;
+    w.c0 = a.cu_rows[it.b];
+    w.n = a.cu_rows[it.b + 1] - w.c0;
+    w.L = a.cache_lens[it.b];
+    w.P = 128 / a.G;
+    w.i0 = it.tile * w.P * (kAlt ? 1 : 2);
+    const int p0 = w.L - w.n;
+    // keys up to the last row of each M tile
+    const int end0 = p0 + min(w.n, w.i0 + w.P), end1 = p0 + min(w.n, w.i0 + 2 * w.P);
+    const int all = (max(end0, end1) + NK - 1) / NK;
+    w.first = static_cast<int>(static_cast<int64_t>(all) * split / nsplit);
+    const int last = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / nsplit);
+    w.total = last - w.first;
+    if (kAlt) {
+        w.count[0] = (w.total + 1) / 2;
+        w.count[1] = w.total / 2;
+    } else {
+        w.count[0] = max(0, min(last, (end0 + NK - 1) / NK) - w.first);
+        w.count[1] = w.i0 + w.P < w.n ? w.total : 0;
+        w.total = max(w.count[0], w.count[1]);
+    }
+    return w;
+}
+
+// One row again over keys [first, end), key by key (a whole warp; 4 dimensions a lane).  Used where a product with a later token's infinite or NaN value spoiled the row.
+__device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int64_t q_row, int first, int end, float (&o)[4],
+                                          float& m, float& l) {
+    const int lane = threadIdx.x & 31;
+    o[0] = o[1] = o[2] = o[3] = l = 0.f;
+    m = -INFINITY;
+    for (int u0 = first; u0 < end; u0 += 32) {
+        const int t = u0 + lane;
+        float x = -INFINITY;
+        int64_t row = 0;
+        if (t < end) {
+            row = block_row(a.cache, b, t & ~(kBlock - 1));
+            row = row < 0 ? 0 : (row + (t & (kBlock - 1))) * a.H + h;
+            const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + row * kHeadDim);
+            const uint4* q = reinterpret_cast<const uint4*>(a.q + q_row * kHeadDim);
+            float acc = 0.f;
+            for (int i = 0; i < kHeadDim / 8; ++i) {
+                const uint4 kv = k[i], qv = q[i];
+                acc += bf16_lo(kv.x) * bf16_lo(qv.x) + bf16_hi(kv.x) * bf16_hi(qv.x) + bf16_lo(kv.y) * bf16_lo(qv.y) +
+                       bf16_hi(kv.y) * bf16_hi(qv.y) + bf16_lo(kv.z) * bf16_lo(qv.z) + bf16_hi(kv.z) * bf16_hi(qv.z) +
+                       bf16_lo(kv.w) * bf16_lo(qv.w) + bf16_hi(kv.w) * bf16_hi(qv.w);
+            }
+            x = acc * a.scale_log2;
+        }
+        float top = x;
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = fmaxf(top, m);
+        const float f = m == -INFINITY ? 0.f : dp_exp2(m - top), p = t < end ? dp_exp2(x - top) : 0.f;
+        l *= f;
+        for (int e = 0; e < 4; ++e) o[e] *= f;
+        m = top;
+        for (int i = 0; i < 32 && u0 + i < end; ++i) {
+            const float pi = __shfl_sync(0xffffffffu, p, i);
+            const int64_t ri = __shfl_sync(0xffffffffu, row, i);
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + ri * kHeadDim + 4 * lane);
+            l += pi;
+            o[0] = fmaf(pi, bf16_lo(v.x), o[0]);
+            o[1] = fmaf(pi, bf16_hi(v.x), o[1]);
+            o[2] = fmaf(pi, bf16_lo(v.y), o[2]);
+            o[3] = fmaf(pi, bf16_hi(v.y), o[3]);
+        }
+    }
+}
+
+template <int kParts, bool kWide, bool kAlt>
+__global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                    const __grid_constant__ CUtensorMap k_map,
+                                                                    const __grid_constant__ CUtensorMap v_map,
+                                                                    const DenseArgs a, int nsplit) {
+    using Cfg = DpCfg<kParts, kWide>;
+    constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2;
+    extern __shared__ uint8_t smem_raw[];
+    using Smem = DpSmem<kParts, kWide>;
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H, split = blockIdx.x / a.H % nsplit, index = blockIdx.x / (a.H * nsplit);
+    const DpItem item = dp_find<kAlt, kDpThreads>(a, index, gridDim.x / (a.H * nsplit), sm.scan, sm.found);
+    if (item.b < 0) return;
+    const DpWork w = dp_work<kAlt, NK>(a, item, split, nsplit);
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int s = 0; s < kDpScaleSlots; ++s) {
+            mbar_init(&sm.sc_full[s], 1);
+            mbar_init(&sm.sc_empty[s], kAlt ? 4 : (w.count[0] > 0 ? 4 : 0) + (w.count[1] > 0 ? 4 : 0));
+        }
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.v_last, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.s_full[s], 1);
+            mbar_init(&sm.p_full[s], 4);
+            mbar_init(&sm.o_full[s], 1);
+        }
+        mbar_init(&sm.drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    // the value tile that holds the end of the sequence, if its last rows are nobody's
+    const int v_end = w.L / NK;
+    const bool fix = w.L % NK != 0 && v_end >= w.first && v_end < w.first + w.total;
+
+    if (warp >= 8) {
+        if constexpr (kParts == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 8) {
+            // ---------------- copies: queries, then K and V tiles in the order the matrix instructions take them
+            if (lane == 0) {
+                const int tiles = kAlt ? 1 : (w.count[1] > 0 ? 2 : 1);
+                mbar_arrive_expect_tx(&sm.q_full, tiles * 2 * w.P * a.G * 128);
+                for (int s = 0; s < tiles; ++s)
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_3d(sm.q[s] + half * (kDpQBytes / 2), &q_map, &sm.q_full, 64 * half, h * a.G,
+                                    w.c0 + w.i0 + s * w.P);
+            }
+            int64_t row = 0;
+            int slot = 0;
+            bool alive = true;
+            // a copy step i loads K tile i (if any) and V tile i - lag: the order K0 V0 K1 V1 ... (two stages a tile) or
+            // K0 K1 V0 K2 V1 ... (alternate tiles)
+            constexpr int kLag = kAlt ? 1 : 0;
+            constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
+            int64_t row_before = 0;                     // the previous batch's (a V tile may still need its last one)
+            for (int i = 0; i < w.total + kLag && alive; ++i) {
+                if (i % kBatch == 0) {
+                    row_before = row;
+                    const int64_t t = (static_cast<int64_t>(w.first) + i) * NK + lane * kBlock;
+                    row = a.cache_tokens;  // past the length: a box past the cache is zeros
+                    if (t < w.L && t < static_cast<int64_t>(w.first + w.total) * NK) {
+                        row = block_row(a.cache, w.b, t);
+                        if (row < 0) {  // page outside the pool
+                            atomicOr(a.err, kErrBadMetadata);
+                            row = a.cache_tokens;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int kind = 0; kind < 2; ++kind) {  // K, V
+                    const int j = kind == 0 ? i : i - kLag;
+                    if (j < 0 || j >= w.total) continue;
+                    const int st = slot % kStages;
+                    int ok = 1;
+                    if (lane == 0 && slot >= kStages) ok = mbar_wait(&sm.empty[st], ((slot / kStages) - 1) & 1, a.err);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        alive = false;
+                        break;
+                    }
+                    const bool old = kind == 1 && kLag == 1 && i % kBatch == 0;
+                    int64_t r[NK / kBlock];
+#pragma unroll
+                    for (int c = 0; c < NK / kBlock; ++c)
+                        r[c] = __shfl_sync(0xffffffffu, old ? row_before : row, (j % kBatch) * (NK / kBlock) + c);
+                    if (lane == 0) {
+                        // the last value tile completes a barrier of its own: warp 10 zeroes its tail and passes it on
+                        uint64_t* bar = kind == 1 && fix && w.first + j == v_end ? &sm.v_last : &sm.full[st];
+                        mbar_arrive_expect_tx(bar, Cfg::kTile);
+#pragma unroll
+                        for (int c = 0; c < NK / kBlock; ++c)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half)
+                                tma_load_3d(sm.ring[st] + half * kHalf + c * (kBlock * 128), kind == 0 ? &k_map : &v_map, bar,
+                                            64 * half, h, static_cast<int>(r[c]));
+                        if (kWide && kind == 0) {  // the tile's scales
+                            const int e = j % kDpScaleSlots;
+                            if (j >= kDpScaleSlots && !mbar_wait(&sm.sc_empty[e], ((j / kDpScaleSlots) - 1) & 1, a.err)) ok = 0;
+                            if (ok) {
+                                const int64_t from = static_cast<int64_t>(h) * a.cache_tokens + a.cache.starts[w.b] +
+                                                     static_cast<int64_t>(w.first + j) * NK;
+                                mbar_arrive_expect_tx(&sm.sc_full[e], 2 * NK * 4);
+                                dp_bulk(sm.sc[e][0], a.k_scale + from, NK * 4, &sm.sc_full[e]);
+                                dp_bulk(sm.sc[e][1], a.v_scale + from, NK * 4, &sm.sc_full[e]);
+                            }
+                        }
+                    }
+                    ++slot;
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) {
+                        alive = false;
+                        break;
+                    }
+                }
+            }
+            if (lane == 0) {  // no copy in flight at the end (the last value tile's barrier is warp 10's to wait for)
+                mbar_wait(&sm.q_full, 0, a.err);
+                for (int st = 0; st < kStages && st < slot; ++st)
+                    mbar_wait(&sm.full[st], ((slot - 1 - st) / kStages) & 1, a.err);
+                if (kWide && alive)
+                    for (int e = 0; e < kDpScaleSlots && e < w.total; ++e)
+                        mbar_wait(&sm.sc_full[e], ((w.total - 1 - e) / kDpScaleSlots) & 1, a.err);
+            }
+        } else if (warp == 9) {
+            // ---------------- matrix instructions, one thread
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(128, NK, 0, 0), idesc_o = idesc_bf16_f32(128, kHeadDim, 0, 1);
+                uint64_t qd[2];
+                qd[0] = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+                qd[1] = kAlt ? qd[0] : smem_desc_sw128(smem_u32(sm.q[1]), 16, 1024);
+                const uint64_t kd = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
+                const uint64_t vd = smem_desc_sw128(smem_u32(sm.ring[0]), kHalf, 1024);
+                int slot = 0;  // ring slots taken so far
+                auto take = [&]() {
+                    const bool ok = mbar_wait(&sm.full[slot % kStages], (slot / kStages) & 1, a.err);
+                    return ok ? slot++ % kStages : -1;
+                };
+                auto scores = [&](int s, int st) {  // S_s = Q_s K^T
+                    const uint64_t kb = kd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_ss(tmem + s * 128, qd[s] + static_cast<uint64_t>(((k >> 2) * (kDpQBytes / 2) + (k & 3) * 32) >> 4),
+                                  kb + static_cast<uint64_t>(((k >> 2) * kHalf + (k & 3) * 32) >> 4), idesc_s, k > 0);
+                    tc_commit(&sm.s_full[s]);
+                };
+                auto values = [&](int s, int st, bool first) {  // O_s += P_s V
+                    const uint64_t vb = vd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                        for (int k = 0; k < NK / 16; ++k)
+                            dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + k * 8,
+                                      vb + static_cast<uint64_t>(k * 2048 >> 4), idesc_o, !(first && part == 0 && k == 0));
+                };
+                bool ok = mbar_wait(&sm.q_full, 0, a.err), issued = false;
+                tc_fence_after();
+                if constexpr (kAlt) {
+                    // K0 K1 | V0 K2 V1 K3 ...: tile j belongs to stage j & 1
+                    for (int j = 0; ok && j < 2 && j < w.total; ++j) {
+                        const int st = take();
+                        ok = st >= 0;
+                        if (!ok) break;
+                        scores(j, st);
+                        tc_commit(&sm.empty[st]);
+                        issued = true;
+                        if (j == 0 && w.total == 1) break;
+                        if (j == 1) break;
+                    }
+                    // after the first two K tiles the ring holds V0 K2 V1 K3 ... (K1 lies behind K0)
+                    for (int j = 0; ok && j < w.total; ++j) {
+                        const int s = j & 1, st = take();
+                        ok = st >= 0 && mbar_wait(&sm.p_full[s], (j >> 1) & 1, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(s, st, kParts > 1 || j < 2);
+                        tc_commit(&sm.empty[st]);
+                        if (j + 2 >= w.total) tc_commit(&sm.o_full[s]);
+                        if (j + 2 < w.total) {
+                            const int sk = take();
+                            ok = sk >= 0;
+                            if (!ok) break;
+                            scores(s, sk);
+                            tc_commit(&sm.empty[sk]);
+                        }
+                    }
+                } else if (w.total > 0) {  // (a part of a short sequence may have no key tile)
+                    int sk = ok ? take() : -1;  // K tile of the next scores
+                    ok = ok && sk >= 0;
+                    if (ok) {
+                        for (int s = 0; s < 2; ++s)
+                            if (w.count[s] > 0) scores(s, sk);
+                        tc_commit(&sm.empty[sk]);
+                        issued = true;
+                    }
+                    for (int j = 0; ok && j < w.total; ++j) {
+                        const int sv = take();
+                        ok = sv >= 0;
+                        sk = -1;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (!ok || j >= w.count[s]) continue;
+                            ok = mbar_wait(&sm.p_full[s], j & 1, a.err);
+                            if (!ok) continue;
+                            tc_fence_after();
+                            values(s, sv, kParts > 1 || j == 0);
+                            if (j + 1 == w.count[s]) {
+                                tc_commit(&sm.o_full[s]);
+                            } else {
+                                if (sk < 0) sk = take();
+                                ok = sk >= 0;
+                                if (!ok) continue;
+                                scores(s, sk);
+                            }
+                        }
+                        if (!ok) break;
+                        tc_commit(&sm.empty[sv]);
+                        if (sk >= 0) tc_commit(&sm.empty[sk]);
+                        else if (j + 1 < w.total) ok = false;
+                    }
+                }
+                if (issued) {  // every matrix instruction done before tensor memory is given back
+                    tc_commit(&sm.drain);
+                    mbar_wait(&sm.drain, 0, a.err);
+                }
+            }
+        } else if (warp == 10 && fix) {
+            // ---------------- last value tile: rows past the length become zero
+            const int j = v_end - w.first;
+            // its ring slot: K0 V0 K1 V1 ..., or K0 K1 V0 K2 V1 ... (the last V has no K before it)
+            const int slot = kAlt ? (j + 1 < w.total ? 2 * j + 2 : 2 * j + 1) : 2 * j + 1, st = slot % kStages;
+            if (mbar_wait(&sm.v_last, 0, a.err)) {
+                const int first = w.L - v_end * NK;
+                for (int x = first * 16 + lane; x < NK * 16; x += 32) {
+                    const int key = x >> 4, c = x & 15;  // 16-byte chunk c & 7 of half c >> 3 (a whole row: no swizzle to undo)
+                    *reinterpret_cast<uint4*>(sm.ring[st] + (c >> 3) * kHalf + key * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.full[st]);
+            }
+        }
+    } else {
+        // 168 x 384 registers at launch: 208 x 256 + 88 x 128, or 232 x 256 + 40 x 128
+        if constexpr (kParts == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        // ---------------- softmax group s: thread = row of M tile s
+        const int s = warp >> 2, m = tid & 127;
+        const int i = w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, g = m % a.G;
+        const bool mine = m < w.P * a.G && i < w.n;
+        const int pos = w.L - w.n + min(i, w.n - 1);
+        // the tile's earliest position: key tiles up to it hide nothing
+        const int early = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P), w.n - 1);
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 (warp % 4)) << 16
+        const uint32_t s_addr = tmem + s * 128 + lanes, o_addr = tmem + 256 + s * 128 + lanes;
+        const int count = w.count[s];
+        float top = -INFINITY, sum = 0.f;  // maximum in use (log2 domain), sum of weights
+        float acc[kParts > 1 ? kHeadDim : 1];  // fp32 outputs: O of the row
+        if constexpr (kParts > 1) {
+#pragma unroll
+            for (int k = 0; k < kHeadDim; ++k) acc[k] = 0.f;
+        }
+        auto collect = [&]() {  // adds the last tile's product to it
+            if constexpr (kParts > 1) {
+#pragma unroll
+                for (int q = 0; q < kHeadDim / 16; ++q) {
+                    uint32_t y[16];
+                    tmem_ld16(o_addr + 16 * q, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) acc[16 * q + k] += __uint_as_float(y[k]);
+                }
+            }
+        };
+        bool alive = true;
+        for (int c = 0; c < count; ++c) {
+            const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
+            alive = mbar_wait(&sm.s_full[s], c & 1, a.err);
+            if (!alive) break;
+            tc_fence_after();
+            if (c > 0) collect();
+            float x[NK];
+#pragma unroll
+            for (int q = 0; q < NK / 32; ++q) dp_ld32(s_addr + 32 * q, x + 32 * q);
+            float f = a.scale_log2;  // x f is the score in the log2 domain
+            const int e = j % kDpScaleSlots;
+            if constexpr (kWide) {
+                alive = mbar_wait(&sm.sc_full[e], (j / kDpScaleSlots) & 1, a.err);
+                if (!alive) break;
+            }
+            tmem_ld_wait();
+            if constexpr (kWide) {
+#pragma unroll
+                for (int k = 0; k < NK; k += 4) {
+                    const float4 ks = *reinterpret_cast<const float4*>(&sm.sc[e][0][k]);
+                    x[k] *= ks.x;
+                    x[k + 1] *= ks.y;
+                    x[k + 2] *= ks.z;
+                    x[k + 3] *= ks.w;
+                }
+            }
+            const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
+            if (edge) {
+                const int seen = pos + 1 - t0;
+#pragma unroll
+                for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * f : -INFINITY;
+                f = 1.f;
+            }
+            float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < NK; k += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) big[y] = fmaxf(big[y], fmaxf(x[k + y], x[k + 4 + y]));
+            const float now = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f;
+            if (c == 0) {
+                top = now;
+            } else if (__any_sync(0xffffffffu, now > top + kDpSlack)) {
+                // the maximum grew: the warp's rows of O in tensor memory (no product runs on it now: S of this tile
+                // was computed after the last one) and their sums move to the new one
+                const float next = now > top + kDpSlack ? now : top;
+                const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
+                if constexpr (kParts > 1) {
+#pragma unroll
+                    for (int k = 0; k < kHeadDim; ++k) acc[k] *= r;
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < kHeadDim / 32; ++q) {
+                        float y[32];
+                        dp_ld32(o_addr + 32 * q, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) y[k] *= r;
+                        dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
+                    }
+                }
+                sum *= r;
+                top = next;
+            }
+            const float base = top == -INFINITY ? 0.f : top;
+            float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                x[k] = dp_exp2(fmaf(x[k], f, -base));
+                add[k & 3] += x[k];
+            }
+            sum += (add[0] + add[1]) + (add[2] + add[3]);
+            if constexpr (kWide) {
+#pragma unroll
+                for (int k = 0; k < NK; k += 4) {
+                    const float4 vs = *reinterpret_cast<const float4*>(&sm.sc[e][1][k]);
+                    // a hidden key's weight stays 0 whatever its scale is
+                    x[k] = edge && x[k] == 0.f ? 0.f : x[k] * vs.x;
+                    x[k + 1] = edge && x[k + 1] == 0.f ? 0.f : x[k + 1] * vs.y;
+                    x[k + 2] = edge && x[k + 2] == 0.f ? 0.f : x[k + 2] * vs.z;
+                    x[k + 3] = edge && x[k + 3] == 0.f ? 0.f : x[k + 3] * vs.w;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.sc_empty[e]);
+            }
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int q = 0; q < NK / 64; ++q) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        pk[k] = pack_bf16x2(x[64 * q + 2 * k], x[64 * q + 2 * k + 1]);
+                        if (part + 1 < kParts) {
+                            x[64 * q + 2 * k] -= bf16_lo(pk[k]);
+                            x[64 * q + 2 * k + 1] -= bf16_hi(pk[k]);
+                        }
+                    }
+                    dp_st32(s_addr + part * (NK / 2) + 32 * q, pk);
+                }
+            }
+            dp_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[s]);
+        }
+        // ---------------- epilogue
+        bool have = count > 0;
+        if (alive && have) alive = mbar_wait(&sm.o_full[s], 0, a.err);
+        tc_fence_after();
+        if (alive && have) collect();
+        auto row_of_o = [&](int q, float (&y)[32]) {  // 32 values of the row
+            if constexpr (kParts > 1) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) y[k] = acc[32 * q + k];
+            } else {
+                dp_ld32(o_addr + 32 * q, y);
+                tmem_ld_wait();
+            }
+        };
+        float f0 = 1.f, f1 = 0.f;
+        float* other = reinterpret_cast<float*>(&sm.q[0][0]);  // [128 dims][128 rows]
+        if constexpr (kAlt) {
+            // the second stream's state goes through the query buffers (every score product is done by now)
+            if (s == 1 && have && alive) {
+#pragma unroll(kParts > 1 ? 4 : 1)
+                for (int q = 0; q < kHeadDim / 32; ++q) {
+                    float y[32];
+                    row_of_o(q, y);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) other[(32 * q + k) * 128 + m] = y[k];
+                }
+            }
+            if (s == 1) sm.other_ml[m] = make_float2(have ? top : -INFINITY, have ? sum : 0.f);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (s == 0 && w.count[1] > 0) {
+                const float2 ml = sm.other_ml[m];
+                const float t2 = fmaxf(top, ml.x);
+                f0 = top == -INFINITY ? 0.f : dp_exp2(top - t2);
+                f1 = ml.x == -INFINITY ? 0.f : dp_exp2(ml.x - t2);
+                sum = sum * f0 + ml.y * f1;
+                top = t2;
+            }
+            if (s == 1) alive = false;  // group 0 writes
+        }
+        if (alive && (have || nsplit > 1)) {
+            constexpr int kRows = kAlt ? 128 : 256;  // rows of an item's part
+            const int64_t q_row = (static_cast<int64_t>(w.c0 + min(i, w.n - 1)) * a.H + h) * a.G + g;
+            const int64_t part_row = ((static_cast<int64_t>(index) * a.H + h) * nsplit + split) * kRows + s * 128 + m;
+            const bool split_up = nsplit > 1;
+            bool spoiled = kAlt && !(fabsf(sum) < INFINITY);  // a product with a value past the row's position that is not finite
+            const float inv = 1.f / sum;
+            if (have) {
+#pragma unroll(kParts > 1 ? 4 : 1)
+                for (int q = 0; q < kHeadDim / 32; ++q) {
+                    float y[32];
+                    row_of_o(q, y);
+                    if constexpr (kAlt) {
+                        if (w.count[1] > 0)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) y[k] = y[k] * f0 + other[(32 * q + k) * 128 + m] * f1;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) spoiled |= !(fabsf(y[k]) < INFINITY);
+                    if (!mine) continue;
+                    if (split_up) {
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 32 * q);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    } else if (a.out_bf16) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_row * kHeadDim + 32 * q);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            dst[k] = make_uint4(pack_bf16x2(y[8 * k] * inv, y[8 * k + 1] * inv),
+                                                pack_bf16x2(y[8 * k + 2] * inv, y[8 * k + 3] * inv),
+                                                pack_bf16x2(y[8 * k + 4] * inv, y[8 * k + 5] * inv),
+                                                pack_bf16x2(y[8 * k + 6] * inv, y[8 * k + 7] * inv));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + q_row * kHeadDim + 32 * q);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            dst[k] = make_float4(y[4 * k] * inv, y[4 * k + 1] * inv, y[4 * k + 2] * inv, y[4 * k + 3] * inv);
+                    }
+                }
+            }
+            if (split_up && mine) *reinterpret_cast<float2*>(a.part_ml + part_row * 2) = make_float2(top, sum);
+            if constexpr (!kWide) {
+                uint32_t again = __ballot_sync(0xffffffffu, mine && spoiled && have);
+                const int end = min(pos + 1, (w.first + (kAlt ? w.total : count)) * NK);
+                while (again) {  // these rows once more, by the whole warp
+                    const int from = __ffs(again) - 1;
+                    again &= again - 1;
+                    const int64_t qr = __shfl_sync(0xffffffffu, q_row, from), pr = __shfl_sync(0xffffffffu, part_row, from);
+                    float y[4], m2, l2;
+                    dp_row_again(a, w.b, h, qr, w.first * NK, __shfl_sync(0xffffffffu, end, from), y, m2, l2);
+                    const float f = split_up ? 1.f : 1.f / l2;
+                    if (split_up) {
+                        *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
+                        if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m2, l2);
+                    } else if (a.out_bf16) {
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qr * kHeadDim + 4 * lane) =
+                            make_uint2(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f));
+                    } else {
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + qr * kHeadDim + 4 * lane) =
+                            make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of split items: CTA (item, head), a warp per row at a time; the parts in order, the same every time.
+constexpr int kDjThreads = 512;
+template <bool kAlt>
+__global__ void __launch_bounds__(kDjThreads) dense_join_kernel(const DenseArgs a, int nsplit) {
+    __shared__ int32_t scan[kDjThreads / 32], found[4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H, index = blockIdx.x / a.H;
+    const DpItem it = dp_find<kAlt, kDjThreads>(a, index, gridDim.x / a.H, scan, found);
+    if (it.b < 0) return;
+    const int c0 = a.cu_rows[it.b], n = a.cu_rows[it.b + 1] - c0, P = 128 / a.G, i0 = it.tile * P * (kAlt ? 1 : 2);
+    constexpr int kRows = kAlt ? 128 : 256;
+    const int64_t base = (static_cast<int64_t>(index) * a.H + h) * nsplit * kRows;
+    for (int x = blockIdx.y * (kDjThreads / 32) + warp; x < kRows; x += gridDim.y * (kDjThreads / 32)) {
+        const int s = x >> 7, m = x & 127, i = i0 + s * P + m / a.G, g = m % a.G;
+        if (m >= P * a.G || i >= n) continue;
+        auto row_of = [&](int y) { return base + static_cast<int64_t>(y) * kRows + x; };
+        float top = -INFINITY;
+        for (int y = lane; y < nsplit; y += 32) top = fmaxf(top, a.part_ml[row_of(y) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int y0 = 0; y0 < nsplit; y0 += 32) {
+            float f = 0.f;
+            if (y0 + lane < nsplit) {
+                const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + row_of(y0 + lane) * 2);
+                f = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : dp_exp2(ml.x - top);
+                l += f * ml.y;
+            }
+            const int count = min(32, nsplit - y0);
+#pragma unroll 4
+            for (int y = 0; y < count; ++y) {
+                const float wt = __shfl_sync(0xffffffffu, f, y);
+                const float4 p = *reinterpret_cast<const float4*>(a.part_o + row_of(y0 + y) * kHeadDim + 4 * lane);
+                if (wt != 0.f) {
+                    v[0] = fmaf(wt, p.x, v[0]);
+                    v[1] = fmaf(wt, p.y, v[1]);
+                    v[2] = fmaf(wt, p.z, v[2]);
+                    v[3] = fmaf(wt, p.w, v[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const float inv = 1.f / l;
+        const int64_t out = (((static_cast<int64_t>(c0 + i) * a.H + h) * a.G) + g) * kHeadDim + 4 * lane;
+        if (a.out_bf16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out) =
+                make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+        else
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out) =
+                make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    }
+}
+
+template <int kParts, bool kWide, bool kAlt>
+static cudaError_t launch_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
+    auto* kernel = dense_prompt_kernel<kParts, kWide, kAlt>;
+    const size_t smem = sizeof(DpSmem<kParts, kWide>) + 1024;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(items) * a.H * nsplit, kDpThreads, smem, stream>>>(*a.q_map, *a.k_map, *a.v_map, a, nsplit);
+    if ((e = cudaGetLastError()) != cudaSuccess || (nsplit == 1)) return e;
+    dense_join_kernel<kAlt><<<dim3(static_cast<unsigned>(items) * a.H, 4), kDjThreads, 0, stream>>>(a, nsplit);
+    return cudaGetLastError();
+}
+
+cudaError_t run_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
+    if (a.kv_int8)
+        return a.out_bf16 ? launch_dense_prompt<1, true, false>(a, items, nsplit, stream)
+                          : launch_dense_prompt<3, true, false>(a, items, nsplit, stream);
+    return a.out_bf16 ? launch_dense_prompt<1, false, false>(a, items, nsplit, stream)
+                      : launch_dense_prompt<3, false, false>(a, items, nsplit, stream);
+}
+
+cudaError_t run_dense_window(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
+    return a.out_bf16 ? launch_dense_prompt<1, false, true>(a, items, nsplit, stream)
+                      : launch_dense_prompt<3, false, true>(a, items, nsplit, stream);
+}
+
+}  // namespace msa

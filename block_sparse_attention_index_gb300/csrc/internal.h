@@ -163,6 +163,8 @@ struct WidenArgs {
     int num_seqs, H, max_cache_len;
     int64_t cache_tokens;
     int only_multi_row;  // 1: sequences with more than kDecodeMaxRows rows only (fused path); 0: all
+    int first_slot;      // first widened sequence of this pass, in order
+    int total_slots;     // most widened sequences of all passes
     int max_slots;       // sequences the copy has room for
     int slot_rows;       // rows per slot: max_cache_len rounded up to a multiple of kBlock
     uint16_t* kw;        // bf16 [max_slots * slot_rows, H, D]
@@ -209,17 +211,24 @@ struct DenseArgs {
     int64_t cache_tokens;
     float scale_log2;  // softmax scale * log2(e)
     int only_multi_row;  // 1: the prompt kernel skips decode-family sequences
-    const CUtensorMap* k_map;  // host copies of the cache maps (kv_map)
+    int tile_windows;    // 1: run_dense_window takes the decode-family sequences of more than 16 (row, head) pairs
+    const CUtensorMap* q_map;  // host copies: q as (D, H*G, rows), box 64 x G x 128 / G; the cache maps (kv_map)
+    const CUtensorMap* k_map;
     const CUtensorMap* v_map;
+    CacheRows seq_cache;       // the caches as the problem gives them (cache: the widened copy for int8 prompts)
+    int64_t seq_cache_tokens;
     int32_t* unit_prefix;  // [num_seqs + 1] decode family: units before each sequence
-    float* part_o;         // [2 shares, H, 16, 128] parts of sequences that several CTAs walk
-    float* part_ml;        // [2 shares, H, 16, 2]
+    float* part_o;         // parts of what several CTAs walk: O [.., 128], decode family [2 shares, H, 16]
+    float* part_ml;        // and their maxima and sums [.., 2]
     uint32_t* err_slots;   // [shares] error bits of the decode family's CTAs
     int err_store;         // 1: the combine stores the error word, 0: it adds to it
     uint32_t* err;
 };
 constexpr int kDenseMaxShares = 160;  // most CTAs that share the decode family's cache walk
-cudaError_t run_dense_simple(const DenseArgs& a, cudaStream_t stream);
+constexpr int kDenseMaxSplit = 32;    // most key ranges of an M tile
+// Prompt chunks (M tile pairs of 2 (128 / G) rows) and drafted windows (one M tile a sequence); items: host bound.
+cudaError_t run_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream);
+cudaError_t run_dense_window(const DenseArgs& a, int items, int nsplit, cudaStream_t stream);
 int dense_decode_shares(int64_t units);  // CTAs for so many blocks
 cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream);
 

@@ -213,23 +213,90 @@ Layout layout_of(const msa_problem* p) {
     return l;
 }
 
-struct DenseLayout {
-    size_t err = 0, err_slots = 0, unit_prefix = 0, part_ml = 0, part_o = 0, total = 0;
+// How msa_dense_forward divides a problem (host counts alone).
+struct DensePlan {
+    bool stream = false;   // decode-family sequences of at most 16 (row, head) pairs (all of them with an int8 cache)
+    bool windows = false;  // the others of the decode family, on tcgen05
+    bool prompts = false;
+    int64_t window_items = 0, prompt_items = 0;  // bounds of the M tiles (prompts: pairs of them)
+    int window_split = 1, prompt_split = 1;      // key ranges an M tile is split into
+    int64_t wide_slots = 0, wide_total = 0, slot_rows = 0;  // int8 prompts: sequences widened a pass, in all; rows of each
 };
 
-DenseLayout dense_layout(const msa_problem* p) {
+// Key ranges for so many CTAs: enough to fill the GPU, at least eight 128-key tiles each.
+int dense_split(int64_t ctas, int max_cache_len) {
+    const int64_t tiles = (static_cast<int64_t>(max_cache_len) + 127) / 128;
+    int64_t n = 152 / std::max<int64_t>(ctas, 1);
+    n = std::min<int64_t>(n, tiles / 8);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, msa::kDenseMaxSplit)));
+}
+
+bool decode_family(const msa_problem* p) { return p->num_decode_seqs != 0; }
+bool prefill_family(const msa_problem* p) {
+    return p->max_rows_per_seq > msa::kDecodeMaxRows && p->num_decode_seqs != p->num_seqs;
+}
+
+DensePlan dense_plan(const msa_problem* p) {
+    DensePlan d;
+    const int64_t H = p->num_kv_heads, G = p->group_size;
+    const int64_t known = p->num_decode_seqs;  // -1: unknown
+    if (decode_family(p)) {
+        const int64_t rows = static_cast<int64_t>(decode_rows_per_seq(p)), seqs = known >= 0 ? known : p->num_seqs;
+        const bool one_row = known >= 0 && p->num_decode_rows == known;  // every sequence
+        const bool full = known >= 0 && p->num_decode_rows == known * rows;
+        d.windows = p->kv_dtype == MSA_KV_BF16 && rows * G > 16 && !one_row;
+        d.stream = !(d.windows && full);
+        d.window_items = seqs;
+        d.window_split = dense_split(seqs * H, p->max_cache_len);
+    }
+    d.prompts = prefill_family(p);
+    if (d.prompts) {
+        const int64_t rows = p->total_rows - std::max(p->num_decode_rows, 0);
+        int64_t seqs = known >= 0 ? p->num_seqs - known : p->num_seqs;
+        seqs = std::max<int64_t>(1, std::min<int64_t>(seqs, p->total_rows / (msa::kDecodeMaxRows + 1)));
+        d.prompt_items = rows / (2 * (128 / G)) + seqs;
+        d.prompt_split = dense_split(d.prompt_items * H, p->max_cache_len);
+        if (p->kv_dtype == MSA_KV_INT8) {
+            d.slot_rows = (static_cast<int64_t>(p->max_cache_len) + msa::kBlock - 1) / msa::kBlock * msa::kBlock;
+            d.wide_total = seqs;
+            d.wide_slots = std::max<int64_t>(1, std::min(seqs, kWidenMaxBytes / (d.slot_rows * widen_bytes_per_row(p))));
+        }
+    }
+    return d;
+}
+
+struct DenseLayout {
+    size_t err = 0, err_slots = 0, unit_prefix = 0, part_ml = 0, part_o = 0, wide_starts = 0, wide_k = 0, wide_v = 0,
+           wide_ks = 0, wide_vs = 0, total = 0;
+};
+
+DenseLayout dense_layout(const msa_problem* p, const DensePlan& d) {
     DenseLayout l;
-    const size_t parts = 2 * msa::kDenseMaxShares * static_cast<size_t>(p->num_kv_heads) * 16;
+    const size_t H = p->num_kv_heads;
+    size_t parts = d.stream ? 2 * msa::kDenseMaxShares * H * 16 : 0;  // the three launches follow one another: one buffer
+    if (d.windows && d.window_split > 1) parts = std::max(parts, static_cast<size_t>(d.window_items) * H * d.window_split * 128);
+    if (d.prompts && d.prompt_split > 1) parts = std::max(parts, static_cast<size_t>(d.prompt_items) * H * d.prompt_split * 256);
     size_t off = 256;
     l.err_slots = off;
     off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
     l.unit_prefix = off;
     off = align256(off + (static_cast<size_t>(p->num_seqs) + 1) * sizeof(int32_t));
-    if (p->num_decode_seqs != 0) {
-        l.part_ml = off;
-        off = align256(off + parts * 2 * sizeof(float));
-        l.part_o = off;
-        off = align256(off + parts * msa::kHeadDim * sizeof(float));
+    l.part_ml = off;
+    off = align256(off + parts * 2 * sizeof(float));
+    l.part_o = off;
+    off = align256(off + parts * msa::kHeadDim * sizeof(float));
+    if (d.wide_slots > 0) {
+        const size_t rows = static_cast<size_t>(d.wide_slots * d.slot_rows);
+        l.wide_starts = off;
+        off = align256(off + static_cast<size_t>(p->num_seqs) * sizeof(int64_t));
+        l.wide_k = off;
+        off = align256(off + rows * H * msa::kHeadDim * 2);
+        l.wide_v = off;
+        off = align256(off + rows * H * msa::kHeadDim * 2);
+        l.wide_ks = off;
+        off = align256(off + rows * H * sizeof(float));
+        l.wide_vs = off;
+        off = align256(off + rows * H * sizeof(float) + 256);  // the last tile's scales are copied as a whole tile
     }
     l.total = off;
     return l;
@@ -314,16 +381,11 @@ msa_status kv_map(CUtensorMap* map, const msa_problem* p, const void* base, cons
     return make_map(map, base, 128, H, T, 64, 1, 64, name);
 }
 
-bool decode_family(const msa_problem* p) { return p->num_decode_seqs != 0; }
-
 // The decode attention's grid covers the host's count of decode-family rows
 // (when given and smaller than the row slots) instead of every row slot.
 bool compact_decode_grid(const msa_problem* p) {
     return p->num_decode_rows > 0 &&
            static_cast<int64_t>(p->num_decode_rows) < static_cast<int64_t>(p->num_seqs) * decode_rows_per_seq(p);
-}
-bool prefill_family(const msa_problem* p) {
-    return p->max_rows_per_seq > msa::kDecodeMaxRows && p->num_decode_seqs != p->num_seqs;
 }
 
 }  // namespace
@@ -552,7 +614,7 @@ static msa_status widen_for_attention(const msa_problem* p, const WidenPlan& w, 
     wa.max_cache_len = p->max_cache_len;
     wa.cache_tokens = p->cache_tokens;
     wa.only_multi_row = only_multi_row ? 1 : 0;
-    wa.max_slots = static_cast<int>(w.slots);
+    wa.max_slots = wa.total_slots = static_cast<int>(w.slots);
     wa.slot_rows = static_cast<int>(w.slot_rows);
     wa.kw = reinterpret_cast<uint16_t*>(ws + l.wide_k);
     wa.vw = reinterpret_cast<uint16_t*>(ws + l.wide_v);
@@ -877,7 +939,7 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes) {
     msa_status s = check_problem(p);
     if (s != MSA_OK) return s;
     if (!bytes) return fail(MSA_ERR_INVALID_ARG, "bytes is null");
-    *bytes = dense_layout(p).total;
+    *bytes = dense_layout(p, dense_plan(p)).total;
     return MSA_OK;
 }
 
@@ -889,26 +951,31 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     if ((s = check_ptr(q, "q")) != MSA_OK || (s = check_ptr(k_cache, "k_cache")) != MSA_OK ||
         (s = check_ptr(v_cache, "v_cache")) != MSA_OK || (s = check_ptr(out, "out")) != MSA_OK)
         return s;
-    const DenseLayout l = dense_layout(p);
+    const DensePlan d = dense_plan(p);
+    const DenseLayout l = dense_layout(p, d);
     if (workspace == nullptr) return fail(MSA_ERR_WORKSPACE, "workspace is null");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
     if (workspace_bytes < l.total)
         return fail(MSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, l.total);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const bool dec = decode_family(p), pre = prefill_family(p);
     cudaError_t e;
     msa::DenseArgs a{};
-    CUtensorMap km, vm;
+    CUtensorMap qm, km, vm;
     if ((s = kv_map(&km, p, k_cache, "k_cache")) != MSA_OK || (s = kv_map(&vm, p, v_cache, "v_cache")) != MSA_OK) return s;
+    const uint32_t G = p->group_size;
+    if ((d.windows || d.prompts) && (s = make_map(&qm, q, 128, static_cast<uint64_t>(p->num_kv_heads) * G, p->total_rows, 64, G,
+                                                  128 / G, "q")) != MSA_OK)
+        return s;
+    a.q_map = &qm;
     a.k_map = &km;
     a.v_map = &vm;
     a.unit_prefix = reinterpret_cast<int32_t*>(ws + l.unit_prefix);
     a.part_o = reinterpret_cast<float*>(ws + l.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
     a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
-    a.err_store = !pre;  // with prompt chunks the word is cleared first and every kernel adds to it
-    a.only_multi_row = dec;
+    a.tile_windows = d.windows;
+    a.only_multi_row = decode_family(p);
     a.q = static_cast<const uint16_t*>(q);
     a.k = k_cache;
     a.v = v_cache;
@@ -919,25 +986,74 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.out_bf16 = p->out_dtype == MSA_OUT_BF16;
     a.cu_rows = p->cu_rows;
     a.cache_lens = p->cache_lens;
-    a.cache = cache_rows_of(p);
+    a.cache = a.seq_cache = cache_rows_of(p);
     a.num_seqs = p->num_seqs;
     a.H = p->num_kv_heads;
     a.G = p->group_size;
     a.total_rows = p->total_rows;
     a.max_rows_per_seq = p->max_rows_per_seq;
     a.max_cache_len = p->max_cache_len;
-    a.cache_tokens = p->cache_tokens;
+    a.cache_tokens = a.seq_cache_tokens = p->cache_tokens;
     a.scale_log2 = scale_log2(p);
     a.err = reinterpret_cast<uint32_t*>(ws + l.err);
-    if (pre && (e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
-    if (dec) {
+    // the decode family's combine stores the error word; before any other kernel it is cleared
+    a.err_store = d.stream && !d.prompts && !d.windows;
+    if (!a.err_store && (e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    if (d.stream) {
         const int64_t seqs = p->num_decode_seqs > 0 ? p->num_decode_seqs : p->num_seqs;
-        const int64_t tiles = (static_cast<int64_t>(decode_rows_per_seq(p)) * p->group_size + 15) / 16;
+        const int64_t tiles = d.windows ? 1 : (static_cast<int64_t>(decode_rows_per_seq(p)) * p->group_size + 15) / 16;
         const int64_t blocks = (p->max_cache_len + msa::kBlock - 1) / msa::kBlock;
         if ((e = msa::run_dense_decode(a, msa::dense_decode_shares(seqs * tiles * blocks), st)) != cudaSuccess)
             return cuda_fail(e, "dense decode attention launch");
     }
-    if (pre && (e = msa::run_dense_simple(a, st)) != cudaSuccess) return cuda_fail(e, "dense prompt attention launch");
+    if (d.windows && (e = msa::run_dense_window(a, static_cast<int>(d.window_items), d.window_split, st)) != cudaSuccess)
+        return cuda_fail(e, "dense window attention launch");
+    if (d.prompts && !a.kv_int8) {
+        if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), d.prompt_split, st)) != cudaSuccess)
+            return cuda_fail(e, "dense prompt attention launch");
+    } else if (d.prompts) {
+        // int8: the prompts' positions widened into the workspace, as many sequences a pass as it holds
+        msa::WidenArgs wa{};
+        wa.k8 = static_cast<const uint8_t*>(k_cache);
+        wa.v8 = static_cast<const uint8_t*>(v_cache);
+        wa.k_scale = p->k_scale;
+        wa.v_scale = p->v_scale;
+        wa.cu_rows = p->cu_rows;
+        wa.cache_lens = p->cache_lens;
+        wa.cache = a.seq_cache;
+        wa.num_seqs = p->num_seqs;
+        wa.H = p->num_kv_heads;
+        wa.max_cache_len = p->max_cache_len;
+        wa.cache_tokens = p->cache_tokens;
+        wa.only_multi_row = a.only_multi_row;
+        wa.max_slots = static_cast<int>(d.wide_slots);
+        wa.total_slots = static_cast<int>(d.wide_total);
+        wa.slot_rows = static_cast<int>(d.slot_rows);
+        wa.kw = reinterpret_cast<uint16_t*>(ws + l.wide_k);
+        wa.vw = reinterpret_cast<uint16_t*>(ws + l.wide_v);
+        wa.ksw = reinterpret_cast<float*>(ws + l.wide_ks);
+        wa.vsw = reinterpret_cast<float*>(ws + l.wide_vs);
+        wa.wide_starts = reinterpret_cast<int64_t*>(ws + l.wide_starts);
+        wa.err = a.err;
+        const uint64_t T = static_cast<uint64_t>(d.wide_slots * d.slot_rows), H = p->num_kv_heads;
+        CUtensorMap kw, vw;
+        if ((s = make_map(&kw, wa.kw, 128, H, T, 64, 1, 64, "widened k")) != MSA_OK ||
+            (s = make_map(&vw, wa.vw, 128, H, T, 64, 1, 64, "widened v")) != MSA_OK)
+            return s;
+        a.k_map = &kw;
+        a.v_map = &vw;
+        a.cache = msa::CacheRows{};
+        a.cache.starts = wa.wide_starts;
+        a.cache_tokens = static_cast<int64_t>(T);
+        a.k_scale = wa.ksw;
+        a.v_scale = wa.vsw;
+        for (int64_t first = 0; first < d.wide_total; first += d.wide_slots) {
+            wa.first_slot = static_cast<int>(first);
+            if ((e = msa::run_widen_kv(wa, st)) != cudaSuccess) return cuda_fail(e, "key/value widening launch");
+            if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), d.prompt_split, st)) != cudaSuccess)
+                return cuda_fail(e, "dense prompt attention launch");
+        }
+    }
     return MSA_OK;
 }
 

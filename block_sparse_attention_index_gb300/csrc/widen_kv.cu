@@ -19,7 +19,7 @@
 // written as zeros: keys past a row's position are masked, and a zero value
 // keeps 0 x value out of the P V products.  Row starts per sequence go to
 // `wide_starts` (0 for a sequence that is not widened, -1 for one past the
-// slots the workspace holds, which the attention then rejects).
+// slots the workspace holds, which the attention then rejects, or for one that another pass widens).
 #include "common.cuh"
 #include "internal.h"
 
@@ -64,13 +64,17 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kv_kernel(const WidenArgs
     __syncthreads();
     int excl = x - cnt;
     for (int i = 0; i < warp; ++i) excl += warp_tot[i];
-    for (int b = b_lo; b < b_hi; ++b) slot_of[b] = slot_of[b] ? excl++ : -1;
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int s = slot_of[b] ? excl++ : -1;
+        // another pass widens it; past every pass's slots: more such sequences than the host counted
+        slot_of[b] = s < 0 ? -1 : (s >= a.total_slots ? -2 : (s < a.first_slot || s >= a.first_slot + a.max_slots ? -3 : s - a.first_slot));
+    }
     __syncthreads();
     if (blockIdx.x == 0) {
         for (int b = tid; b < B; b += kWidenThreads) {
             const int s = slot_of[b];
-            a.wide_starts[b] = s < 0 ? 0 : (s < a.max_slots ? static_cast<int64_t>(s) * a.slot_rows : -1);
-            if (s >= a.max_slots) atomicOr(a.err, kErrBadMetadata);  // more such sequences than the host counted
+            a.wide_starts[b] = s == -1 ? 0 : (s < 0 ? -1 : static_cast<int64_t>(s) * a.slot_rows);
+            if (s == -2) atomicOr(a.err, kErrBadMetadata);
         }
     }
 
@@ -85,7 +89,7 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kv_kernel(const WidenArgs
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int b = static_cast<int>(u / groups), grp = static_cast<int>(u - static_cast<int64_t>(b) * groups);
         const int slot = slot_of[b];
-        if (slot < 0 || slot >= a.max_slots) continue;
+        if (slot < 0) continue;
         const int L = a.cache_lens[b];
         const int t0 = grp * kWidenPos, tb = t0 & ~(kBlock - 1);  // first position, its block's
         if (L < 1 || L > a.max_cache_len || tb >= L) continue;  // the attention rejects such a sequence

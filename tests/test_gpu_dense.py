@@ -183,19 +183,16 @@ def test_cache_rows_past_the_length_may_hold_anything(n, int8, page):
 def test_later_tokens_do_not_reach_earlier_rows(n):
     """A NaN or an infinity in the key and value of a later token of the same chunk."""
     b = Batch([(n, 200)], 2, 16, False, 0, torch.bfloat16, seed=1)
-    before = b.run()
+    # a spoiled row is computed again in another order of the same operations, with fp32 weights, so it stays within
+    # the bound of the formula (which allows bf16 weights) rather than the same bits
+    ref, bound = b.ref()
     at = n - 2
     row = b.rows_of(0, torch.tensor(200 - n + at)).item()
-    b.k[row] = float("nan")
-    b.v[row] = float("nan")
-    after = b.run()
-    assert torch.equal(before[:at], after[:at])
-    assert not torch.isfinite(after[at:]).any()
-    b.k[row] = 0
-    b.v[row] = float("inf")
-    after = b.run()
-    assert torch.equal(before[:at], after[:at])
-    assert not torch.isfinite(after[at:]).any()
+    for key, value in ((float("nan"), float("nan")), (0, float("inf")), (0, -float("inf"))):
+        b.k[row], b.v[row] = key, value
+        after = b.run()
+        assert ((after[:at].double() - ref[:at]).abs() <= bound[:at]).all()
+        assert not torch.isfinite(after[at:]).any()
 
 
 def test_rows_behind_the_last_sequence_stay():
