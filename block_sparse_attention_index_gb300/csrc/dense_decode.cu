@@ -13,14 +13,22 @@
 // m16n8k16: 16 rows are all a tile has (tcgen05 wants 128), and 12 to 16 FLOP a byte are well within its rate.
 //
 // P enters the second product as two bf16 parts (2^-16 of a weight; bf16 outputs) or three (2^-24; fp32 outputs),
-// taken from the accumulators of the first as they lie.  int8 tiles are widened in registers, exactly (an int8 value
-// has 8 significant bits): the order of the dimensions inside a dot product and of the output columns is free, so
-// each lane takes 16-byte runs of its keys and needs no transposition.  The key scale multiplies the score and the
-// value scale the weight.
+// taken from the accumulators of the first as they lie.
+//
+// int8 caches: the tiles are widened in registers to f16, exactly, by 1.25 instructions a value (bf16, whose 8 bits
+// cannot hold the bias that such a conversion adds, takes 2): byte b, its sign bit flipped, under the exponent of
+// 1024 is 1152 + b.  The order of the dimensions inside a dot product is free, so a lane takes 16-byte runs of its
+// keys, and the second product's pairs of keys come from transposed loads of byte pairs.  Queries become f16 times a
+// power of two for each row (its largest value in [2^8, 2^9): bf16's 8 bits fit; what lies 2^-22 below the row's
+// largest loses bits).  The key scale multiplies the score and the value scale the weight.  A weight is 2^14 2^(x - m)
+// times the value scale over a power of two not below any of the scales so far, in one f16 part (2^-12; bf16
+// outputs) or two (2^-23; fp32): at most 2^14, and full precision down to 2^-28 of the largest.
 //
 // Where a sequence begins and ends inside one CTA, the CTA writes its output; else each CTA leaves its part (O, m,
 // l) in the workspace, at most two a CTA, and dense_combine_kernel joins them.
 #include <algorithm>
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -75,10 +83,22 @@ __device__ __forceinline__ uint4 dd_lds128(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-// Two int8 values, in the low bytes of t's halves, as two bf16: (128 + low 7 bits) - (128, or 256 with the sign bit).
-__device__ __forceinline__ uint32_t dd_widen2(uint32_t t) {
-    const uint32_t x = (t & 0x007F007Fu) | 0x43004300u, y = (t & 0x00800080u) | 0x43004300u;
-    __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+__device__ __forceinline__ void dd_mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Bytes 0 and 2 of w (signed) as two f16: with the sign bit flipped and the exponent of 1024 above it a byte b reads
+// as 1152 + b, exactly.
+__device__ __forceinline__ uint32_t dd_even_f16(uint32_t w) {
+    const uint32_t u = (w & 0x00FF00FFu) ^ 0x64806480u, bias = 0x64806480u;
+    __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&bias));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t dd_pack_f16(float lo, float hi) {
+    __half2 r = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&r);
 }
 __device__ __forceinline__ void dd_sync_consumers() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -114,6 +134,9 @@ __device__ __forceinline__ DdSeq dd_seq(const DenseArgs& a, int b) {
     s.tiles = (s.n * a.G + 15) / 16;
     return s;
 }
+
+// CTAs that take a share of the units: share c is units [total c / shares, total (c + 1) / shares), none of them empty.
+__device__ __forceinline__ int dd_shares(int total, int grid) { return min(total, grid); }
 
 // Writes two neighbouring outputs of (row, head) pair m of a sequence, heads of KV head h.
 __device__ __forceinline__ void dd_store2(const DenseArgs& a, const DdSeq& s, int h, int m, int d, float x, float y) {
@@ -179,7 +202,10 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     if (blockIdx.x == 0)
         for (int b = tid; b <= a.num_seqs; b += kDdThreads) a.unit_prefix[b] = prefix[b];
     const int64_t total = carry;
-    const int u0 = static_cast<int>(total * blockIdx.x / gridDim.x), u1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+    const int shares = dd_shares(carry, gridDim.x);  // CTAs with work
+    const bool idle = static_cast<int>(blockIdx.x) >= shares;
+    const int u0 = idle ? 0 : static_cast<int>(total * blockIdx.x / shares);
+    const int u1 = idle ? 0 : static_cast<int>(total * (blockIdx.x + 1) / shares);
     int first_b = 0;
     {
         int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= u0
@@ -278,18 +304,42 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
             for (int e = 0; e < 2; ++e) pos[e] = s.L - s.n + min(16 * mt + grp + 8 * e, s.n * a.G - 1) / a.G;
             const int first_pos = s.L - s.n + 16 * mt / a.G;  // the tile's earliest row
             uint32_t qa[8][4];
+            float qf[2];  // factor from the product to the log2 domain, rows grp and grp + 8
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int m = 16 * mt + min(grp + 8 * e, pairs - 1), qi = m / a.G, g = m - qi * a.G;
                 const uint32_t* src = reinterpret_cast<const uint32_t*>(
                     a.q + ((static_cast<int64_t>(s.c0 + qi) * H + h) * a.G + g) * kHeadDim);
+                qf[e] = a.scale_log2;
+                if constexpr (kInt8) {
+                    // dims 32 tig + 4 ks + {0, 2} and {1, 3}: the order in which a word of four key bytes is widened
+                    float v[32], top = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    // bf16: dims 16 ks + 2 tig, + 8; int8: dims 32 tig + 4 ks, + 2 (the order the lane's key bytes have)
-                    qa[ks][e] = src[kInt8 ? 16 * tig + 2 * ks : 8 * ks + tig];
-                    qa[ks][2 + e] = src[kInt8 ? 16 * tig + 2 * ks + 1 : 8 * ks + 4 + tig];
+                    for (int x = 0; x < 16; ++x) {
+                        const uint32_t w = src[16 * tig + x];
+                        v[2 * x] = bf16_lo(w);
+                        v[2 * x + 1] = bf16_hi(w);
+                        top = fmaxf(top, fmaxf(fabsf(v[2 * x]), fabsf(v[2 * x + 1])));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const uint32_t ex = min(max(__float_as_uint(top) >> 23, 9u), 253u);
+                    const float f = __uint_as_float((262u - ex) << 23);  // 2^(8 - exponent of the row's largest)
+                    qf[e] *= __uint_as_float((ex - 8u) << 23);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        qa[ks][e] = dd_pack_f16(v[4 * ks] * f, v[4 * ks + 2] * f);
+                        qa[ks][2 + e] = dd_pack_f16(v[4 * ks + 1] * f, v[4 * ks + 3] * f);
+                    }
+                } else {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {  // dims 16 ks + 2 tig, + 8
+                        qa[ks][e] = src[8 * ks + tig];
+                        qa[ks][2 + e] = src[8 * ks + 4 + tig];
+                    }
                 }
             }
+            float vref = 0.f, vinv = 0.f;  // int8: the power of two that the value scales are divided by, its inverse
             float o[16][4], mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < 16; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
@@ -311,8 +361,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                         const uint4 w1 = dd_lds128(kb + row * 128 + (((2 * tig + 1) ^ (row & 7)) << 4));
                         const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            dd_mma(c[nt], qa[ks], dd_widen2(__byte_perm(w[ks], 0, 0x4140)), dd_widen2(__byte_perm(w[ks], 0, 0x4342)));
+                        for (int ks = 0; ks < 8; ++ks) dd_mma_f16(c[nt], qa[ks], dd_even_f16(w[ks]), dd_even_f16(w[ks] >> 8));
                     } else {
                         const int row = nt * 8 + (lane & 7);
 #pragma unroll
@@ -325,62 +374,81 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                         }
                     }
                 }
-                // scores in the log2 domain; hidden keys -inf
+                // hidden keys -inf; int8: times the key scales, and the value scales of the lane's 16 keys
                 float vs[8][2];
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt) {
-                    float f0 = a.scale_log2, f1 = a.scale_log2;
+                    const int t = t0 + nt * 8 + 2 * tig;
                     if constexpr (kInt8) {
                         const float2 ks = *reinterpret_cast<const float2*>(stage + 2 * Cfg::kPlane + (nt * 8 + 2 * tig) * 4);
                         const float2 v2 = *reinterpret_cast<const float2*>(stage + 2 * Cfg::kPlane + 256 + (nt * 8 + 2 * tig) * 4);
-                        f0 *= ks.x;
-                        f1 *= ks.y;
-                        vs[nt][0] = v2.x;
-                        vs[nt][1] = v2.y;
+                        c[nt][0] *= ks.x;
+                        c[nt][1] *= ks.y;
+                        c[nt][2] *= ks.x;
+                        c[nt][3] *= ks.y;
+                        vs[nt][0] = edge && t >= s.L ? 0.f : v2.x;
+                        vs[nt][1] = edge && t + 1 >= s.L ? 0.f : v2.y;
                     }
-                    c[nt][0] *= f0;
-                    c[nt][1] *= f1;
-                    c[nt][2] *= f0;
-                    c[nt][3] *= f1;
-                    if (edge) {
-                        const int t = t0 + nt * 8 + 2 * tig;
-                        if (t > pos[0]) c[nt][0] = -INFINITY;
-                        if (t + 1 > pos[0]) c[nt][1] = -INFINITY;
-                        if (t > pos[1]) c[nt][2] = -INFINITY;
-                        if (t + 1 > pos[1]) c[nt][3] = -INFINITY;
+                    if (edge) {  // (scaled here: a scale of zero must not meet an infinity)
+                        c[nt][0] = t > pos[0] ? -INFINITY : c[nt][0] * qf[0];
+                        c[nt][1] = t + 1 > pos[0] ? -INFINITY : c[nt][1] * qf[0];
+                        c[nt][2] = t > pos[1] ? -INFINITY : c[nt][2] * qf[1];
+                        c[nt][3] = t + 1 > pos[1] ? -INFINITY : c[nt][3] * qf[1];
                     }
                 }
-                float top[2] = {mrun[0], mrun[1]};
+                const float f0 = edge ? 1.f : qf[0], f1 = edge ? 1.f : qf[1];  // what is left to multiply by
+                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt) {
                     top[0] = fmaxf(top[0], fmaxf(c[nt][0], c[nt][1]));
                     top[1] = fmaxf(top[1], fmaxf(c[nt][2], c[nt][3]));
                 }
+                top[0] *= f0;
+                top[1] *= f1;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
                     top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+                    top[e] = fmaxf(top[e], mrun[e]);
                 }
-                if (__any_sync(0xffffffffu, top[0] > mrun[0] || top[1] > mrun[1])) {
+                bool grew = top[0] > mrun[0] || top[1] > mrun[1];
+                float vnew = vref;
+                if constexpr (kInt8) {
+                    float big = 0.f;
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt) big = fmaxf(big, fmaxf(fabsf(vs[nt][0]), fabsf(vs[nt][1])));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    if (big > vref && big < INFINITY) {  // the same in every lane; the next power of two, at most 2^127
+                        vnew = __uint_as_float(min((__float_as_uint(big) + 0x007FFFFFu) & 0x7F800000u, 0x7F000000u));
+                        grew = true;
+                    }
+                }
+                if (__any_sync(0xffffffffu, grew)) {
+                    const float fv = kInt8 ? (vnew > 0.f ? vref / vnew : 1.f) : 1.f;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float f = mrun[e] == -INFINITY ? 0.f : dd_exp2(mrun[e] - top[e]);
+                        const float f = mrun[e] == -INFINITY ? 0.f : dd_exp2(mrun[e] - top[e]), fo = f * fv;
                         lrun[e] *= f;
                         mrun[e] = top[e];
 #pragma unroll
                         for (int nt = 0; nt < 16; ++nt) {
-                            o[nt][2 * e] *= f;
-                            o[nt][2 * e + 1] *= f;
+                            o[nt][2 * e] *= fo;
+                            o[nt][2 * e + 1] *= fo;
                         }
                     }
+                    vref = vnew;
+                    vinv = vnew > 0.f ? 1.f / vnew : 0.f;
                 }
-                const float base0 = mrun[0] == -INFINITY ? 0.f : mrun[0], base1 = mrun[1] == -INFINITY ? 0.f : mrun[1];
+                constexpr float kLift = kInt8 ? 14.f : 0.f;  // f16 weights: 2^14 at most
+                const float base0 = (mrun[0] == -INFINITY ? 0.f : mrun[0]) - kLift;
+                const float base1 = (mrun[1] == -INFINITY ? 0.f : mrun[1]) - kLift;
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt) {
-                    c[nt][0] = dd_exp2(c[nt][0] - base0);
-                    c[nt][1] = dd_exp2(c[nt][1] - base0);
-                    c[nt][2] = dd_exp2(c[nt][2] - base1);
-                    c[nt][3] = dd_exp2(c[nt][3] - base1);
+                    c[nt][0] = dd_exp2(fmaf(c[nt][0], f0, -base0));
+                    c[nt][1] = dd_exp2(fmaf(c[nt][1], f0, -base0));
+                    c[nt][2] = dd_exp2(fmaf(c[nt][2], f1, -base1));
+                    c[nt][3] = dd_exp2(fmaf(c[nt][3], f1, -base1));
                 }
                 float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -393,6 +461,8 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                 if constexpr (kInt8) {
 #pragma unroll
                     for (int nt = 0; nt < 8; ++nt) {
+                        vs[nt][0] *= vinv;
+                        vs[nt][1] *= vinv;
                         // a hidden key's weight stays 0 whatever its scale is
                         c[nt][0] = edge && c[nt][0] == 0.f ? 0.f : c[nt][0] * vs[nt][0];
                         c[nt][1] = edge && c[nt][1] == 0.f ? 0.f : c[nt][1] * vs[nt][1];
@@ -450,35 +520,42 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                         float x = c[2 * kk + (f >> 1)][2 * (f & 1)], y = c[2 * kk + (f >> 1)][2 * (f & 1) + 1];
 #pragma unroll
                         for (int part = 0; part < kParts; ++part) {
-                            pa[kk][part][f] = pack_bf16x2(x, y);
-                            x -= bf16_lo(pa[kk][part][f]);
-                            y -= bf16_hi(pa[kk][part][f]);
+                            if constexpr (kInt8) {
+                                pa[kk][part][f] = dd_pack_f16(x, y);
+                                const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&pa[kk][part][f]));
+                                x -= r.x;
+                                y -= r.y;
+                            } else {
+                                pa[kk][part][f] = pack_bf16x2(x, y);
+                                x -= bf16_lo(pa[kk][part][f]);
+                                y -= bf16_hi(pa[kk][part][f]);
+                            }
                         }
                     }
+                constexpr bool kApart = kParts == (kInt8 ? 2 : 3);  // fp32 outputs: a tile's product by itself
                 if constexpr (kInt8) {
 #pragma unroll
-                    for (int n4 = 0; n4 < 4; ++n4) {  // n-tiles 4 n4 ..: output column grp of n-tile nt is dim 16 grp + nt
+                    for (int n4 = 0; n4 < 4; ++n4) {
+                        // 32 dims: n-tile 2 x + y (x: 16-byte chunk 2 n4 + x, y: parity) has dim 16 chunk + 2 grp + y in column grp
                         float t[4][4];
 #pragma unroll
                         for (int n = 0; n < 4; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int key = 16 * kk + 2 * tig + (q & 1) + 8 * (q >> 1);
-                                w[q] = *reinterpret_cast<const uint32_t*>(stage + Cfg::kPlane + key * 128 + ((grp ^ (key & 7)) << 4) + 4 * n4);
-                            }
+                            // byte pairs (dims 2 grp, + 1) of keys 16 kk + 2 tig, + 1 and those 8 further, chunks 2 n4 and + 1
+                            uint32_t r[4];
+                            const int key = 16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7), chunk = 2 * n4 + (lane >> 4);
+                            dd_ldsm_x4_t(vb + key * 128 + ((chunk ^ (key & 7)) << 4), r);
 #pragma unroll
                             for (int n = 0; n < 4; ++n) {
-                                const uint32_t sel = n | ((4 + n) << 8);
-                                const uint32_t b0 = dd_widen2(__byte_perm(w[0], w[1], sel));
-                                const uint32_t b1 = dd_widen2(__byte_perm(w[2], w[3], sel));
+                                const int sh = (n & 1) * 8, at = (n >> 1) * 2;
+                                const uint32_t b0 = dd_even_f16(r[at] >> sh), b1 = dd_even_f16(r[at + 1] >> sh);
 #pragma unroll
-                                for (int part = 0; part < kParts; ++part) dd_mma(kParts == 3 ? t[n] : o[4 * n4 + n], pa[kk][part], b0, b1);
+                                for (int part = 0; part < kParts; ++part)
+                                    dd_mma_f16(kApart ? t[n] : o[4 * n4 + n], pa[kk][part], b0, b1);
                             }
                         }
-                        if constexpr (kParts == 3) {
+                        if constexpr (kApart) {
 #pragma unroll
                             for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -498,11 +575,11 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                             dd_ldsm_x4_t(vb + (n2 >> 2) * (Cfg::kPlane / 2) + key * 128 + ((chunk ^ (key & 7)) << 4), r);
 #pragma unroll
                             for (int part = 0; part < kParts; ++part) {
-                                dd_mma(kParts == 3 ? t[0] : o[2 * n2], pa[kk][part], r[0], r[1]);
-                                dd_mma(kParts == 3 ? t[1] : o[2 * n2 + 1], pa[kk][part], r[2], r[3]);
+                                dd_mma(kApart ? t[0] : o[2 * n2], pa[kk][part], r[0], r[1]);
+                                dd_mma(kApart ? t[1] : o[2 * n2 + 1], pa[kk][part], r[2], r[3]);
                             }
                         }
-                        if constexpr (kParts == 3) {
+                        if constexpr (kApart) {
 #pragma unroll
                             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -514,6 +591,12 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                 if (lane == 0) mbar_arrive(&empty[st]);
             }
 
+            if constexpr (kInt8) {
+#pragma unroll
+                for (int nt = 0; nt < 16; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nt][e] *= vref;
+            }
             // ---- the warps of a head join their parts (8 / H of them, by halves)
 #pragma unroll
             for (int half = kDdConsumers / 2; half >= H; half >>= 1) {
@@ -563,25 +646,18 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     if (!whole && tig == 0)
                         *reinterpret_cast<float2*>(a.part_ml + (slot * 16 + m) * 2) = make_float2(mrun[e], lrun[e]);
 #pragma unroll
-                    for (int nt = 0; nt < 16; ++nt) {
-                        float x = o[nt][2 * e] * f, y = o[nt][2 * e + 1] * f;
-                        int d = nt * 8 + 2 * tig;
-                        if constexpr (kInt8) {
-                            // columns 2 tig and 2 tig + 1 are dims 32 tig + nt and 32 tig + 16 + nt: two n-tiles make pairs
-                            if (nt & 1) continue;
-                            const float x1 = o[nt + 1][2 * e] * f, y1 = o[nt + 1][2 * e + 1] * f;
-                            d = 32 * tig + nt;
-                            if (whole) {
-                                dd_store2(a, s, h, 16 * mt + m, d, x, x1);
-                                dd_store2(a, s, h, 16 * mt + m, d + 16, y, y1);
-                            } else {
-                                *reinterpret_cast<float2*>(part + d) = make_float2(x, x1);
-                                *reinterpret_cast<float2*>(part + d + 16) = make_float2(y, y1);
-                            }
-                        } else if (whole) {
-                            dd_store2(a, s, h, 16 * mt + m, d, x, y);
+                    for (int nt = 0; nt < 16; nt += 2) {
+                        // two pairs of neighbouring dims.  bf16: columns 2 tig, + 1 of each n-tile; int8: the two n-tiles of a
+                        // chunk have dims 16 chunk + 4 tig + {0, 2} and {1, 3} in the lane's columns
+                        const float p0 = o[nt][2 * e] * f, p1 = (kInt8 ? o[nt + 1][2 * e] : o[nt][2 * e + 1]) * f;
+                        const float p2 = (kInt8 ? o[nt][2 * e + 1] : o[nt + 1][2 * e]) * f, p3 = o[nt + 1][2 * e + 1] * f;
+                        const int d0 = kInt8 ? 8 * nt + 4 * tig : 8 * nt + 2 * tig, d1 = kInt8 ? d0 + 2 : d0 + 8;
+                        if (whole) {
+                            dd_store2(a, s, h, 16 * mt + m, d0, p0, p1);
+                            dd_store2(a, s, h, 16 * mt + m, d1, p2, p3);
                         } else {
-                            *reinterpret_cast<float2*>(part + d) = make_float2(x, y);
+                            *reinterpret_cast<float2*>(part + d0) = make_float2(p0, p1);
+                            *reinterpret_cast<float2*>(part + d1) = make_float2(p2, p3);
                         }
                     }
                 }
@@ -597,12 +673,12 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 // c + 1 of the shares is the first to fall, if any; a warp takes one (row, head) pair: the parts' maxima and sums
 // first, then 2^(m_i - m) O_i summed in the parts' order (the same every time), 4 of the 128 values a lane.
 constexpr int kDcThreads = 512;
-__global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseArgs a, int shares) {
+__global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseArgs a, int grid) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (blockIdx.x == 0 && h == 0 && warp == 0) {  // what the shares' CTAs found wrong
         uint32_t e = 0;
-        for (int c = lane; c < shares; c += 32) e |= a.err_slots[c];
+        for (int c = lane; c < grid; c += 32) e |= a.err_slots[c];
         e = __reduce_or_sync(0xffffffffu, e);
         if (lane == 0) {
             if (a.err_store) *a.err = e;
@@ -610,10 +686,10 @@ __global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseAr
         }
     }
     const int64_t total = a.unit_prefix[a.num_seqs];
+    const int shares = dd_shares(static_cast<int>(total), grid);
     const int c = blockIdx.x;  // boundary between shares c and c + 1
     if (c + 1 >= shares) return;
-    const int cut = static_cast<int>(total * (c + 1) / shares);
-    if (cut <= 0 || cut >= total) return;
+    const int start = static_cast<int>(total * c / shares), cut = static_cast<int>(total * (c + 1) / shares);
     int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= cut
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -621,47 +697,43 @@ __global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseAr
     }
     const DdSeq s = dd_seq(a, lo);
     const int mt = (cut - a.unit_prefix[lo]) / s.blocks, seg0 = a.unit_prefix[lo] + mt * s.blocks, seg1 = seg0 + s.blocks;
-    if (cut == seg0) return;  // the boundary lies between two of them
-    // an earlier boundary inside the same one (strictly): its CTA joins them
-    if (c > 0 && static_cast<int>(total * c / shares) > seg0) return;
-    int last = c + 1;  // last share that holds a part of it
-    while (last + 1 < shares && static_cast<int>(total * (last + 1) / shares) < seg1) ++last;
+    // the boundary lies between two of them, or an earlier boundary inside the same one has a CTA that joins it
+    if (cut == seg0 || start > seg0) return;
+    // the share that holds its last unit: the largest c with total c / shares <= seg1 - 1
+    const int last = static_cast<int>((static_cast<int64_t>(seg1) * shares - 1) / total);
     const int count = last - c + 1;
     const int pairs = min(16, s.n * a.G - 16 * mt);
     if (warp >= pairs) return;
-    // share c's part began inside the share unless it began with it; the others' begin with their shares.  A share
-    // of no units (more shares than units) has no part.
-    auto slot_of = [&](int i) {
-        const int sh = c + i;
-        return (2 * static_cast<int64_t>(sh) + (i == 0 && static_cast<int>(total * sh / shares) < seg0 ? 1 : 0)) * a.H + h;
-    };
-    auto empty = [&](int i) { return total * (c + i) / shares == total * (c + i + 1) / shares; };
+    // share c's part is its second one unless the share began with it; the others' are the first of their shares
+    const int slot0 = 2 * c + (start < seg0 ? 1 : 0);
+    auto row_of = [&](int i) { return (static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * a.H + h) * 16 + warp; };
     float m = -INFINITY;
-    for (int i = lane; i < count; i += 32)
-        if (!empty(i)) m = fmaxf(m, a.part_ml[(slot_of(i) * 16 + warp) * 2]);
+    for (int i = lane; i < count; i += 32) m = fmaxf(m, a.part_ml[row_of(i) * 2]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
     for (int i0 = 0; i0 < count; i0 += 32) {
         float f = 0.f;
-        int64_t at = 0;
-        if (i0 + lane < count && !empty(i0 + lane)) {
-            at = slot_of(i0 + lane) * 16 + warp;
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+        if (i0 + lane < count) {
+            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + row_of(i0 + lane) * 2);
             f = ml.x == -INFINITY ? 0.f : dd_exp2(ml.x - m);
             l += ml.y * f;
         }
         const int n = min(32, count - i0);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float w = __shfl_sync(0xffffffffu, f, i);
-            const int64_t from = __shfl_sync(0xffffffffu, at, i);
-            const float4 v = *reinterpret_cast<const float4*>(a.part_o + from * kHeadDim + 4 * lane);
-            if (w != 0.f) {
-                x[0] = fmaf(w, v.x, x[0]);
-                x[1] = fmaf(w, v.y, x[1]);
-                x[2] = fmaf(w, v.z, x[2]);
-                x[3] = fmaf(w, v.w, x[3]);
+        for (int i = 0; i < n; i += 8) {  // eight parts' loads in flight
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] = *reinterpret_cast<const float4*>(a.part_o + row_of(i0 + min(i + u, n - 1)) * kHeadDim + 4 * lane);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float w = __shfl_sync(0xffffffffu, f, min(i + u, 31));
+                if (i + u < n && w != 0.f) {
+                    x[0] = fmaf(w, v[u].x, x[0]);
+                    x[1] = fmaf(w, v[u].y, x[1]);
+                    x[2] = fmaf(w, v[u].z, x[2]);
+                    x[3] = fmaf(w, v[u].w, x[3]);
+                }
             }
         }
     }
@@ -705,7 +777,7 @@ int dense_decode_shares(int64_t units) {
 template <int H>
 static cudaError_t launch_dense_decode_h(const DenseArgs& a, int grid, cudaStream_t stream) {
     if (a.kv_int8)
-        return a.out_bf16 ? launch_dense_decode<H, true, 2>(a, grid, stream) : launch_dense_decode<H, true, 3>(a, grid, stream);
+        return a.out_bf16 ? launch_dense_decode<H, true, 1>(a, grid, stream) : launch_dense_decode<H, true, 2>(a, grid, stream);
     return a.out_bf16 ? launch_dense_decode<H, false, 2>(a, grid, stream) : launch_dense_decode<H, false, 3>(a, grid, stream);
 }
 
