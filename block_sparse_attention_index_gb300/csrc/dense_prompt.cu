@@ -58,7 +58,7 @@ struct __align__(1024) DpSmem {
     uint64_t full[Cfg::kStages], empty[Cfg::kStages];
     uint64_t sc_full[kDpScaleSlots], sc_empty[kDpScaleSlots];
     uint64_t q_full, v_last;
-    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint64_t s_full[2], p_full[2][2], o_full[2], drain;  // P: by halves of the key tile
     uint32_t tmem;
     int32_t scan[kDpThreads / 32];
     int32_t found[4];
@@ -85,6 +85,22 @@ __device__ __forceinline__ void dp_ld32(uint32_t addr, float* r) {
           "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
           "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
         : "r"(addr));
+}
+// 64 columns of the thread's row and their maximum, taken as they are read (tcgen05.ld.red, an sm_103a instruction).
+__device__ __forceinline__ void dp_ld64_max(uint32_t addr, float* v, float& m) {
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, %64, [%65];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63]),
+          "=f"(m)
+        : "r"(addr));
+}
+__device__ __forceinline__ void dp_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 __device__ __forceinline__ void dp_st32(uint32_t addr, const uint32_t* r) {
     asm volatile(
@@ -286,7 +302,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         mbar_init(&sm.v_last, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.s_full[s], 1);
-            mbar_init(&sm.p_full[s], 4);
+            mbar_init(&sm.p_full[s][0], 4);
+            mbar_init(&sm.p_full[s][1], 4);
             mbar_init(&sm.o_full[s], 1);
         }
         mbar_init(&sm.drain, 1);
@@ -412,14 +429,21 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                                   kb + static_cast<uint64_t>(((k >> 2) * kHalf + (k & 3) * 32) >> 4), idesc_s, k > 0);
                     tc_commit(&sm.s_full[s]);
                 };
-                auto values = [&](int s, int st, bool first) {  // O_s += P_s V
+                // O_s += P_s V, each 64 keys as soon as their weights are there; false: they never came
+                auto values = [&](int s, int st, uint32_t phase, bool first) {
                     const uint64_t vb = vd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part)
+                    for (int h2 = 0; h2 < NK / 64; ++h2) {
+                        if (!mbar_wait(&sm.p_full[s][h2], phase, a.err)) return false;
+                        tc_fence_after();
 #pragma unroll
-                        for (int k = 0; k < NK / 16; ++k)
-                            dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + k * 8,
-                                      vb + static_cast<uint64_t>(k * 2048 >> 4), idesc_o, !(first && part == 0 && k == 0));
+                        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                            for (int k = 4 * h2; k < 4 * h2 + 4; ++k)
+                                dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + k * 8,
+                                          vb + static_cast<uint64_t>(k * 2048 >> 4), idesc_o, !(first && part == 0 && k == 0));
+                    }
+                    return true;
                 };
                 bool ok = mbar_wait(&sm.q_full, 0, a.err), issued = false;
                 tc_fence_after();
@@ -438,10 +462,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     // after the first two K tiles the ring holds V0 K2 V1 K3 ... (K1 lies behind K0)
                     for (int j = 0; ok && j < w.total; ++j) {
                         const int s = j & 1, st = take();
-                        ok = st >= 0 && mbar_wait(&sm.p_full[s], (j >> 1) & 1, a.err);
+                        ok = st >= 0 && values(s, st, (j >> 1) & 1, kParts > 1 || j < 2);
                         if (!ok) break;
-                        tc_fence_after();
-                        values(s, st, kParts > 1 || j < 2);
                         tc_commit(&sm.empty[st]);
                         if (j + 2 >= w.total) tc_commit(&sm.o_full[s]);
                         if (j + 2 < w.total) {
@@ -468,10 +490,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             if (!ok || j >= w.count[s]) continue;
-                            ok = mbar_wait(&sm.p_full[s], j & 1, a.err);
+                            ok = values(s, sv, j & 1, kParts > 1 || j == 0);
                             if (!ok) continue;
-                            tc_fence_after();
-                            values(s, sv, kParts > 1 || j == 0);
                             if (j + 1 == w.count[s]) {
                                 tc_commit(&sm.o_full[s]);
                             } else {
@@ -547,9 +567,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             if (!alive) break;
             tc_fence_after();
             if (c > 0) collect();
-            float x[NK];
+            float x[NK], big[NK / 64];
 #pragma unroll
-            for (int q = 0; q < NK / 32; ++q) dp_ld32(s_addr + 32 * q, x + 32 * q);
+            for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
             float f = a.scale_log2;  // x f is the score in the log2 domain
             const int e = j % kDpScaleSlots;
             if constexpr (kWide) {
@@ -574,12 +594,16 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * f : -INFINITY;
                 f = 1.f;
             }
-            float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float now = NK == 128 ? fmaxf(big[0], big[NK / 64 - 1]) : big[0];
+            if (kWide || edge) {  // the scores are not those that the load took the maximum of
+                float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 0; k < NK; k += 8)
+                for (int k = 0; k < NK; k += 8)
 #pragma unroll
-                for (int y = 0; y < 4; ++y) big[y] = fmaxf(big[y], fmaxf(x[k + y], x[k + 4 + y]));
-            const float now = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * f;
+                    for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], fmaxf(x[k + z], x[k + 4 + z]));
+                now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+            }
+            now *= f;
             if (c == 0) {
                 top = now;
             } else if (__any_sync(0xffffffffu, now > top + kDpSlack)) {
@@ -605,46 +629,54 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 top = next;
             }
             const float base = top == -INFINITY ? 0.f : top;
-            float add[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+            float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                x[k] = dp_exp2(fmaf(x[k], f, -base));
-                add[k & 3] += x[k];
-            }
-            sum += (add[0] + add[1]) + (add[2] + add[3]);
-            if constexpr (kWide) {
+            for (int h2 = 0; h2 < NK / 64; ++h2) {  // 64 keys at a time: the products with them start while the next are made
 #pragma unroll
-                for (int k = 0; k < NK; k += 4) {
-                    const float4 vs = *reinterpret_cast<const float4*>(&sm.sc[e][1][k]);
-                    // a hidden key's weight stays 0 whatever its scale is
-                    x[k] = edge && x[k] == 0.f ? 0.f : x[k] * vs.x;
-                    x[k + 1] = edge && x[k + 1] == 0.f ? 0.f : x[k + 1] * vs.y;
-                    x[k + 2] = edge && x[k + 2] == 0.f ? 0.f : x[k + 2] * vs.z;
-                    x[k + 3] = edge && x[k + 3] == 0.f ? 0.f : x[k + 3] * vs.w;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.sc_empty[e]);
-            }
+                for (int q = 0; q < 2; ++q) {
+                    float* z = x + 64 * h2 + 32 * q;
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) {
-                uint32_t pk[32];
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 y = __ffma2_rn(make_float2(z[2 * k], z[2 * k + 1]), ff, nb);
+                        z[2 * k] = dp_exp2(y.x);
+                        z[2 * k + 1] = dp_exp2(y.y);
+                        add[k & 1] = __fadd2_rn(add[k & 1], make_float2(z[2 * k], z[2 * k + 1]));
+                    }
+                    if constexpr (kWide) {
 #pragma unroll
-                for (int q = 0; q < NK / 64; ++q) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        pk[k] = pack_bf16x2(x[64 * q + 2 * k], x[64 * q + 2 * k + 1]);
-                        if (part + 1 < kParts) {
-                            x[64 * q + 2 * k] -= bf16_lo(pk[k]);
-                            x[64 * q + 2 * k + 1] -= bf16_hi(pk[k]);
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 vs = *reinterpret_cast<const float4*>(&sm.sc[e][1][64 * h2 + 32 * q + k]);
+                            // a hidden key's weight stays 0 whatever its scale is
+                            z[k] = edge && z[k] == 0.f ? 0.f : z[k] * vs.x;
+                            z[k + 1] = edge && z[k + 1] == 0.f ? 0.f : z[k + 1] * vs.y;
+                            z[k + 2] = edge && z[k + 2] == 0.f ? 0.f : z[k + 2] * vs.z;
+                            z[k + 3] = edge && z[k + 3] == 0.f ? 0.f : z[k + 3] * vs.w;
                         }
                     }
-                    dp_st32(s_addr + part * (NK / 2) + 32 * q, pk);
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            pk[k] = pack_bf16x2(z[2 * k], z[2 * k + 1]);
+                            if (part + 1 < kParts) {
+                                z[2 * k] -= bf16_lo(pk[k]);
+                                z[2 * k + 1] -= bf16_hi(pk[k]);
+                            }
+                        }
+                        dp_st16(s_addr + part * (NK / 2) + 32 * h2 + 16 * q, pk);
+                    }
                 }
+                dp_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[s][h2]);
             }
-            dp_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[s]);
+            sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
+            if constexpr (kWide) {
+                if (lane == 0) mbar_arrive(&sm.sc_empty[e]);  // (after the warp's last barrier: every lane has read them)
+            }
         }
         // ---------------- epilogue
         bool have = count > 0;
