@@ -9,8 +9,10 @@
 //   S_s[128, NK] = Q_s K^T     both operands from shared memory (TMA, 128-byte swizzle), S in tensor memory
 //   P_s = 2^(x - m)            softmax group s: one thread a row, S read from and P written over tensor memory
 //   O_s[128, 128] += P_s V     P from tensor memory, V as it lies ([key][dim], MN-major), O in tensor memory
-// While group 0 works on S_0 the tensor cores run P_1 V and S_1, and the other way round: 1,024 tensor cycles and two
-// softmax passes of 128 x 128 a tile pair.  Tensor memory is full: S_0, S_1, O_0, O_1 of 128 columns each.
+// While group 0 works on S_0 the tensor cores run P_1 V and S_1, and the other way round: 2,048 tensor cycles and two
+// softmax passes of 128 x 128 a tile pair.  Tensor memory is full: S_0, S_1, O_0, O_1 of 128 columns each.  Each stage
+// has an issuing thread of its own: the tensor pipe queues little, so a thread's test of a barrier (75 cycles even
+// where the barrier is complete) or commit would leave it idle, eight of them in a pair's 32 instructions.
 //
 // The running maximum is only raised when it would grow by more than 8 (a factor of 256 in the weights, which fp32
 // sums and bf16 weights carry without loss); the group that owns O then multiplies it in tensor memory.  So most tiles
@@ -37,7 +39,7 @@
 
 namespace msa {
 
-constexpr int kDpThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 copies, 9 matrix instructions, 10 last value tile
+constexpr int kDpThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 copies, 9 and 11 matrix instructions, 10 last value tile
 constexpr int kDpQBytes = 128 * kHeadDim * 2;
 constexpr int kDpScaleSlots = 4;
 constexpr float kDpSlack = 8.f;  // log2 by which the running maximum may lag
@@ -55,10 +57,13 @@ struct __align__(1024) DpSmem {
     uint8_t q[2][kDpQBytes];
     uint8_t ring[Cfg::kStages][Cfg::kTile];
     float sc[kWide ? kDpScaleSlots : 1][2][kWide ? 128 : 4];  // key and value scales of a tile
-    uint64_t full[Cfg::kStages], empty[Cfg::kStages];
+    // Copies landed.  Two stages a tile: [0][ring slot], every slot seen by both issuers.  Alternate tiles: issuer s's
+    // n-th copy completes [s][n % kStages], so that each issuer sees its barriers' phases one after the other (a slot's
+    // phases would belong to either, and a wait that skipped one could not tell by parity that it had).
+    uint64_t full[2][Cfg::kStages], empty[Cfg::kStages];
     uint64_t sc_full[kDpScaleSlots], sc_empty[kDpScaleSlots];
     uint64_t q_full, v_last;
-    uint64_t s_full[2], p_full[2][2], o_full[2], drain;  // P: by halves of the key tile
+    uint64_t s_full[2], p_full[2][2], o_full[2], drain[2];  // P: by halves of the key tile
     uint32_t tmem;
     int32_t scan[kDpThreads / 32];
     int32_t found[4];
@@ -291,12 +296,13 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], 1);
+            mbar_init(&sm.full[0][s], 1);
+            mbar_init(&sm.full[1][s], 1);
+            mbar_init(&sm.empty[s], kAlt ? 1 : max(1, (w.count[0] > 0) + (w.count[1] > 0)));  // the stages that read it
         }
         for (int s = 0; s < kDpScaleSlots; ++s) {
             mbar_init(&sm.sc_full[s], 1);
-            mbar_init(&sm.sc_empty[s], kAlt ? 4 : (w.count[0] > 0 ? 4 : 0) + (w.count[1] > 0 ? 4 : 0));
+            mbar_init(&sm.sc_empty[s], 4 * max(1, (w.count[0] > 0) + (w.count[1] > 0)));
         }
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.v_last, 1);
@@ -305,8 +311,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             mbar_init(&sm.p_full[s][0], 4);
             mbar_init(&sm.p_full[s][1], 4);
             mbar_init(&sm.o_full[s], 1);
+            mbar_init(&sm.drain[s], 1);
         }
-        mbar_init(&sm.drain, 1);
         fence_mbar_init();
     }
     if (warp == 9) tmem_alloc(&sm.tmem, 512);
@@ -317,6 +323,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     // the value tile that holds the end of the sequence, if its last rows are nobody's
     const int v_end = w.L / NK;
     const bool fix = w.L % NK != 0 && v_end >= w.first && v_end < w.first + w.total;
+
+    auto full_index = [&](int j, int kind) { return kAlt ? 2 * (j >> 1) + kind : 2 * j + kind; };  // of tile j's K (0) or V (1)
+    auto full_bar = [&](int j, int kind) { return &sm.full[kAlt ? j & 1 : 0][full_index(j, kind) % kStages]; };
 
     if (warp >= 8) {
         if constexpr (kParts == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                                     w.c0 + w.i0 + s * w.P);
             }
             int64_t row = 0;
-            int slot = 0;
+            int slot = 0, sent[2] = {0, 0};  // copies so far, and by barrier row
             bool alive = true;
             // a copy step i loads K tile i (if any) and V tile i - lag: the order K0 V0 K1 V1 ... (two stages a tile) or
             // K0 K1 V0 K2 V1 ... (alternate tiles)
@@ -371,7 +380,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         r[c] = __shfl_sync(0xffffffffu, old ? row_before : row, (j % kBatch) * (NK / kBlock) + c);
                     if (lane == 0) {
                         // the last value tile completes a barrier of its own: warp 10 zeroes its tail and passes it on
-                        uint64_t* bar = kind == 1 && fix && w.first + j == v_end ? &sm.v_last : &sm.full[st];
+                        uint64_t* bar = kind == 1 && fix && w.first + j == v_end ? &sm.v_last : full_bar(j, kind);
                         mbar_arrive_expect_tx(bar, Cfg::kTile);
 #pragma unroll
                         for (int c = 0; c < NK / kBlock; ++c)
@@ -392,6 +401,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         }
                     }
                     ++slot;
+                    if (kAlt && (j & 1)) ++sent[1];
+                    else ++sent[0];
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (!ok) {
                         alive = false;
@@ -401,37 +412,36 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             }
             if (lane == 0) {  // no copy in flight at the end (the last value tile's barrier is warp 10's to wait for)
                 mbar_wait(&sm.q_full, 0, a.err);
-                for (int st = 0; st < kStages && st < slot; ++st)
-                    mbar_wait(&sm.full[st], ((slot - 1 - st) / kStages) & 1, a.err);
+                for (int s = 0; s < (kAlt ? 2 : 1); ++s)
+                    for (int b = 0; b < kStages && b < sent[s]; ++b)
+                        mbar_wait(&sm.full[s][b], ((sent[s] - 1 - b) / kStages) & 1, a.err);
                 if (kWide && alive)
                     for (int e = 0; e < kDpScaleSlots && e < w.total; ++e)
                         mbar_wait(&sm.sc_full[e], ((w.total - 1 - e) / kDpScaleSlots) & 1, a.err);
             }
-        } else if (warp == 9) {
-            // ---------------- matrix instructions, one thread
-            if (lane == 0) {
+        } else if (warp == 9 || warp == 11) {
+            // ---------------- matrix instructions of stage s, one thread
+            const int s = warp == 9 ? 0 : 1;
+            if (lane == 0 && w.count[s] > 0) {
                 constexpr uint32_t idesc_s = idesc_bf16_f32(128, NK, 0, 0), idesc_o = idesc_bf16_f32(128, kHeadDim, 0, 1);
-                uint64_t qd[2];
-                qd[0] = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-                qd[1] = kAlt ? qd[0] : smem_desc_sw128(smem_u32(sm.q[1]), 16, 1024);
+                const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[kAlt ? 0 : s]), 16, 1024);
                 const uint64_t kd = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
                 const uint64_t vd = smem_desc_sw128(smem_u32(sm.ring[0]), kHalf, 1024);
-                int slot = 0;  // ring slots taken so far
-                auto take = [&]() {
-                    const bool ok = mbar_wait(&sm.full[slot % kStages], (slot / kStages) & 1, a.err);
-                    return ok ? slot++ % kStages : -1;
-                };
-                auto scores = [&](int s, int st) {  // S_s = Q_s K^T
-                    const uint64_t kb = kd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
+                // ring slots of key tile j: K0 V0 K1 V1 ..., or (alternate tiles) K0 K1 V0 K2 V1 ...
+                auto slot_k = [&](int j) { return kAlt ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
+                auto slot_v = [&](int j) { return kAlt ? (j + 1 < w.total ? 2 * j + 2 : 2 * j + 1) : 2 * j + 1; };
+                auto landed = [&](int j, int kind) { return mbar_wait(full_bar(j, kind), (full_index(j, kind) / kStages) & 1, a.err); };
+                auto scores = [&](int slot) {  // S_s = Q_s K^T
+                    const uint64_t kb = kd + static_cast<uint64_t>((slot % kStages) * (Cfg::kTile >> 4));
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        tc_mma_ss(tmem + s * 128, qd[s] + static_cast<uint64_t>(((k >> 2) * (kDpQBytes / 2) + (k & 3) * 32) >> 4),
+                        tc_mma_ss(tmem + s * 128, qd + static_cast<uint64_t>(((k >> 2) * (kDpQBytes / 2) + (k & 3) * 32) >> 4),
                                   kb + static_cast<uint64_t>(((k >> 2) * kHalf + (k & 3) * 32) >> 4), idesc_s, k > 0);
                     tc_commit(&sm.s_full[s]);
                 };
                 // O_s += P_s V, each 64 keys as soon as their weights are there; false: they never came
-                auto values = [&](int s, int st, uint32_t phase, bool first) {
-                    const uint64_t vb = vd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
+                auto values = [&](int slot, uint32_t phase, bool first) {
+                    const uint64_t vb = vd + static_cast<uint64_t>((slot % kStages) * (Cfg::kTile >> 4));
 #pragma unroll
                     for (int h2 = 0; h2 < NK / 64; ++h2) {
                         if (!mbar_wait(&sm.p_full[s][h2], phase, a.err)) return false;
@@ -445,71 +455,39 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     }
                     return true;
                 };
-                bool ok = mbar_wait(&sm.q_full, 0, a.err), issued = false;
+                constexpr int kStep = kAlt ? 2 : 1;
+                const int j0 = kAlt ? s : 0;
+                bool ok = mbar_wait(&sm.q_full, 0, a.err) && landed(j0, 0);
+                const bool issued = ok;
                 tc_fence_after();
-                if constexpr (kAlt) {
-                    // K0 K1 | V0 K2 V1 K3 ...: tile j belongs to stage j & 1
-                    for (int j = 0; ok && j < 2 && j < w.total; ++j) {
-                        const int st = take();
-                        ok = st >= 0;
+                if (ok) {
+                    scores(slot_k(j0));
+                    tc_commit(&sm.empty[slot_k(j0) % kStages]);
+                }
+                for (int c = 0; ok && c < w.count[s]; ++c) {
+                    const int j = j0 + kStep * c;
+                    ok = landed(j, 1) && values(slot_v(j), c & 1, kParts > 1 || c == 0);
+                    if (!ok) break;
+                    if (c + 1 < w.count[s]) {
+                        ok = landed(j + kStep, 0);
                         if (!ok) break;
-                        scores(j, st);
-                        tc_commit(&sm.empty[st]);
-                        issued = true;
-                        if (j == 0 && w.total == 1) break;
-                        if (j == 1) break;
+                        scores(slot_k(j + kStep));
+                        tc_commit(&sm.empty[slot_k(j + kStep) % kStages]);
+                    } else {
+                        tc_commit(&sm.o_full[s]);
                     }
-                    // after the first two K tiles the ring holds V0 K2 V1 K3 ... (K1 lies behind K0)
-                    for (int j = 0; ok && j < w.total; ++j) {
-                        const int s = j & 1, st = take();
-                        ok = st >= 0 && values(s, st, (j >> 1) & 1, kParts > 1 || j < 2);
-                        if (!ok) break;
-                        tc_commit(&sm.empty[st]);
-                        if (j + 2 >= w.total) tc_commit(&sm.o_full[s]);
-                        if (j + 2 < w.total) {
-                            const int sk = take();
-                            ok = sk >= 0;
-                            if (!ok) break;
-                            scores(s, sk);
-                            tc_commit(&sm.empty[sk]);
+                    tc_commit(&sm.empty[slot_v(j) % kStages]);
+                }
+                if constexpr (!kAlt) {  // tiles that only the other stage needs
+                    for (int j = w.count[s]; ok && j < w.total; ++j)
+                        for (int kind = 0; ok && kind < 2; ++kind) {
+                            ok = landed(j, kind);
+                            if (ok) mbar_arrive(&sm.empty[(2 * j + kind) % kStages]);
                         }
-                    }
-                } else if (w.total > 0) {  // (a part of a short sequence may have no key tile)
-                    int sk = ok ? take() : -1;  // K tile of the next scores
-                    ok = ok && sk >= 0;
-                    if (ok) {
-                        for (int s = 0; s < 2; ++s)
-                            if (w.count[s] > 0) scores(s, sk);
-                        tc_commit(&sm.empty[sk]);
-                        issued = true;
-                    }
-                    for (int j = 0; ok && j < w.total; ++j) {
-                        const int sv = take();
-                        ok = sv >= 0;
-                        sk = -1;
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            if (!ok || j >= w.count[s]) continue;
-                            ok = values(s, sv, j & 1, kParts > 1 || j == 0);
-                            if (!ok) continue;
-                            if (j + 1 == w.count[s]) {
-                                tc_commit(&sm.o_full[s]);
-                            } else {
-                                if (sk < 0) sk = take();
-                                ok = sk >= 0;
-                                if (!ok) continue;
-                                scores(s, sk);
-                            }
-                        }
-                        if (!ok) break;
-                        tc_commit(&sm.empty[sv]);
-                        if (sk >= 0) tc_commit(&sm.empty[sk]);
-                        else if (j + 1 < w.total) ok = false;
-                    }
                 }
                 if (issued) {  // every matrix instruction done before tensor memory is given back
-                    tc_commit(&sm.drain);
-                    mbar_wait(&sm.drain, 0, a.err);
+                    tc_commit(&sm.drain[s]);
+                    mbar_wait(&sm.drain[s], 0, a.err);
                 }
             }
         } else if (warp == 10 && fix) {
@@ -525,7 +503,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.full[st]);
+                if (lane == 0) mbar_arrive(full_bar(j, 1));
             }
         }
     } else {
@@ -563,7 +541,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         bool alive = true;
         for (int c = 0; c < count; ++c) {
             const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
-            alive = mbar_wait(&sm.s_full[s], c & 1, a.err);
+            alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], c & 1, a.err));
             if (!alive) break;
             tc_fence_after();
             if (c > 0) collect();
@@ -573,7 +551,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             float f = a.scale_log2;  // x f is the score in the log2 domain
             const int e = j % kDpScaleSlots;
             if constexpr (kWide) {
-                alive = mbar_wait(&sm.sc_full[e], (j / kDpScaleSlots) & 1, a.err);
+                alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], (j / kDpScaleSlots) & 1, a.err));
                 if (!alive) break;
             }
             tmem_ld_wait();
@@ -680,7 +658,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         }
         // ---------------- epilogue
         bool have = count > 0;
-        if (alive && have) alive = mbar_wait(&sm.o_full[s], 0, a.err);
+        if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], 0, a.err));
         tc_fence_after();
         if (alive && have) collect();
         auto row_of_o = [&](int q, float (&y)[32]) {  // 32 values of the row
@@ -695,7 +673,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         float f0 = 1.f, f1 = 0.f;
         float* other = reinterpret_cast<float*>(&sm.q[0][0]);  // [128 dims][128 rows]
         if constexpr (kAlt) {
-            // the second stream's state goes through the query buffers (every score product is done by now)
+            // the second stream's state goes through the query buffers, once both streams' products are done
+            asm volatile("bar.sync 1, 256;" ::: "memory");
             if (s == 1 && have && alive) {
 #pragma unroll(kParts > 1 ? 4 : 1)
                 for (int q = 0; q < kHeadDim / 32; ++q) {
@@ -736,8 +715,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) spoiled |= !(fabsf(y[k]) < INFINITY);
-                    if (!mine) continue;
-                    if (split_up) {
+                    if (!mine) {
+                        // (a row of the tile that no query has)
+                    } else if (split_up) {
                         float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 32 * q);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
@@ -755,6 +735,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         for (int k = 0; k < 8; ++k)
                             dst[k] = make_float4(y[4 * k] * inv, y[4 * k + 1] * inv, y[4 * k + 2] * inv, y[4 * k + 3] * inv);
                     }
+                    __syncwarp();  // the next load is the whole warp's
                 }
             }
             if (split_up && mine) *reinterpret_cast<float2*>(a.part_ml + part_row * 2) = make_float2(top, sum);
