@@ -12,7 +12,9 @@
 // While group 0 works on S_0 the tensor cores run P_1 V and S_1, and the other way round: 2,048 tensor cycles and two
 // softmax passes of 128 x 128 a tile pair.  Tensor memory is full: S_0, S_1, O_0, O_1 of 128 columns each.  Each stage
 // has an issuing thread of its own: the tensor pipe queues little, so a thread's test of a barrier (75 cycles even
-// where the barrier is complete) or commit would leave it idle, eight of them in a pair's 32 instructions.
+// where the barrier is complete) or commit would leave it idle, eight of them in a pair's 32 instructions.  The two
+// take turns, so that one stage's softmax falls into the other's products (left alone they fall into step: both
+// softmaxes, then both stages' products).
 //
 // The running maximum is only raised when it would grow by more than 8 (a factor of 256 in the weights, which fp32
 // sums and bf16 weights carry without loss); the group that owns O then multiplies it in tensor memory.  So most tiles
@@ -63,7 +65,7 @@ struct __align__(1024) DpSmem {
     uint64_t full[2][Cfg::kStages], empty[Cfg::kStages];
     uint64_t sc_full[kDpScaleSlots], sc_empty[kDpScaleSlots];
     uint64_t q_full, v_last;
-    uint64_t s_full[2], p_full[2][2], o_full[2], drain[2];  // P: by halves of the key tile
+    uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
     uint32_t tmem;
     int32_t scan[kDpThreads / 32];
     int32_t found[4];
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             mbar_init(&sm.p_full[s][0], 4);
             mbar_init(&sm.p_full[s][1], 4);
             mbar_init(&sm.o_full[s], 1);
+            mbar_init(&sm.turn[s], 1);
             mbar_init(&sm.drain[s], 1);
         }
         fence_mbar_init();
@@ -431,49 +434,57 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 auto slot_k = [&](int j) { return kAlt ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
                 auto slot_v = [&](int j) { return kAlt ? (j + 1 < w.total ? 2 * j + 2 : 2 * j + 1) : 2 * j + 1; };
                 auto landed = [&](int j, int kind) { return mbar_wait(full_bar(j, kind), (full_index(j, kind) / kStages) & 1, a.err); };
-                auto scores = [&](int slot) {  // S_s = Q_s K^T
+                // S_s = Q_s K^T; `pass`: the other stage's turn begins while the last of them run
+                auto scores = [&](int slot, bool pass) {
                     const uint64_t kb = kd + static_cast<uint64_t>((slot % kStages) * (Cfg::kTile >> 4));
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
+                    for (int k = 0; k < 8; ++k) {
                         tc_mma_ss(tmem + s * 128, qd + static_cast<uint64_t>(((k >> 2) * (kDpQBytes / 2) + (k & 3) * 32) >> 4),
                                   kb + static_cast<uint64_t>(((k >> 2) * kHalf + (k & 3) * 32) >> 4), idesc_s, k > 0);
+                        if (k == 5 && pass) mbar_arrive(&sm.turn[s ^ 1]);
+                    }
                     tc_commit(&sm.s_full[s]);
                 };
-                // O_s += P_s V, each 64 keys as soon as their weights are there; false: they never came
-                auto values = [&](int slot, uint32_t phase, bool first) {
-                    const uint64_t vb = vd + static_cast<uint64_t>((slot % kStages) * (Cfg::kTile >> 4));
+                constexpr int kStep = kAlt ? 2 : 1;
+                const int j0 = kAlt ? s : 0, count = w.count[s], others = w.count[s ^ 1];
+                bool ok = mbar_wait(&sm.q_full, 0, a.err) && landed(j0, 0);
+                const bool issued = ok;
+                tc_fence_after();
+                if (ok) {
+                    scores(slot_k(j0), false);
+                    tc_commit(&sm.empty[slot_k(j0) % kStages]);
+                }
+                for (int c = 0; ok && c < count; ++c) {
+                    // the stages take turns: values of tile c, scores of the next (whatever can be waited for is, first)
+                    const int j = j0 + kStep * c;
+                    const bool next = c + 1 < count;
+                    ok = landed(j, 1) && (!next || landed(j + kStep, 0)) && mbar_wait(&sm.p_full[s][0], c & 1, a.err);
+                    if (ok && (s == 0 ? c > 0 && c <= others : c < others)) ok = mbar_wait(&sm.turn[s], (s == 0 ? c - 1 : c) & 1, a.err);
+                    if (!ok) break;
+                    const bool pass = s == 0 ? c < others : c + 1 < others;
+                    const uint64_t vb = vd + static_cast<uint64_t>((slot_v(j) % kStages) * (Cfg::kTile >> 4));
+                    tc_fence_after();
 #pragma unroll
-                    for (int h2 = 0; h2 < NK / 64; ++h2) {
-                        if (!mbar_wait(&sm.p_full[s][h2], phase, a.err)) return false;
-                        tc_fence_after();
+                    for (int h2 = 0; h2 < NK / 64; ++h2) {  // O_s += P_s V, the second 64 keys as soon as their weights are there
+                        if (h2 == 1) {
+                            ok = mbar_wait(&sm.p_full[s][1], c & 1, a.err);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
 #pragma unroll
                         for (int part = 0; part < kParts; ++part)
 #pragma unroll
                             for (int k = 4 * h2; k < 4 * h2 + 4; ++k)
                                 dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + k * 8,
-                                          vb + static_cast<uint64_t>(k * 2048 >> 4), idesc_o, !(first && part == 0 && k == 0));
+                                          vb + static_cast<uint64_t>(k * 2048 >> 4), idesc_o,
+                                          !((kParts > 1 || c == 0) && part == 0 && k == 0));
                     }
-                    return true;
-                };
-                constexpr int kStep = kAlt ? 2 : 1;
-                const int j0 = kAlt ? s : 0;
-                bool ok = mbar_wait(&sm.q_full, 0, a.err) && landed(j0, 0);
-                const bool issued = ok;
-                tc_fence_after();
-                if (ok) {
-                    scores(slot_k(j0));
-                    tc_commit(&sm.empty[slot_k(j0) % kStages]);
-                }
-                for (int c = 0; ok && c < w.count[s]; ++c) {
-                    const int j = j0 + kStep * c;
-                    ok = landed(j, 1) && values(slot_v(j), c & 1, kParts > 1 || c == 0);
                     if (!ok) break;
-                    if (c + 1 < w.count[s]) {
-                        ok = landed(j + kStep, 0);
-                        if (!ok) break;
-                        scores(slot_k(j + kStep));
+                    if (next) {
+                        scores(slot_k(j + kStep), pass);
                         tc_commit(&sm.empty[slot_k(j + kStep) % kStages]);
                     } else {
+                        if (pass) mbar_arrive(&sm.turn[s ^ 1]);
                         tc_commit(&sm.o_full[s]);
                     }
                     tc_commit(&sm.empty[slot_v(j) % kStages]);
