@@ -126,9 +126,18 @@ def _stream(device):
     return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _on(device):
     """The device of a call made current for its launches (free when it already is)."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _NOTHING if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _raw_stream(index):
+    """The handle of torch's current stream on device `index` (what current_stream().cuda_stream gives, without the
+    stream object: half the host time of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _need(t, name, dtype, device, shape=None):
@@ -138,7 +147,7 @@ def _need(t, name, dtype, device, shape=None):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -202,6 +211,7 @@ class Problem:
             self.cache_starts.data_ptr() if self.block_table is None else None,
             None if self.block_table is None else self.block_table.data_ptr(),
             0 if self.block_table is None else int(self.block_table.shape[1]), int(page_size), int(ik_heads))
+        self._ref = C.byref(self.c)
         if num_decode_rows == "auto":  # rows of the decode-family sequences (1 to 8 rows each)
             num_decode_rows = sum(n for n in rows if n <= DECODE_MAX_ROWS)
         self.c.num_decode_rows = int(num_decode_rows)
@@ -386,18 +396,25 @@ class Rope:
         self.axis = axis_of(axis, self.dim, "axis")
         self.index_axis = axis_of(index_axis, self.index_dim, "index_axis")
 
+    def _struct(self, positions):
+        return MsaRope(self.dim, self.index_dim, self.axes, int(self.interleaved), self.turns.data_ptr(),
+                       self.index_turns.data_ptr(), None if self.axis is None else self.axis.data_ptr(),
+                       None if self.index_axis is None else self.index_axis.data_ptr(),
+                       None if positions is None else positions.data_ptr())
 
-def _rows(t, name, shape, device):
+
+def _rows(t, name, R, heads, dim, device):
     """Checks a bf16 [rows, heads, dim] view whose heads lie side by side; returns its row stride in elements."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+    if t.shape != (R, heads, dim):
+        raise ValueError(f"{name} must have shape {(R, heads, dim)}, got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name}'s heads must lie side by side in each row")
-    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+    return row if R > 1 else heads * dim
 
 
 def append_cache(pb: Problem, new_k, new_v, k, v, new_ik=None, ik=None, q=None, iq=None, rope=None, positions=None,
@@ -407,47 +424,42 @@ def append_cache(pb: Problem, new_k, new_v, k, v, new_ik=None, ik=None, q=None, 
     New rows may be views of a wider projection (any row stride that is a multiple of 8).  positions: int32
     [axes, rows], or None for each row's position in its sequence.  With an int8 cache the scales go to pb.k_scale
     and pb.v_scale.  Returns (q, iq) rotated, each None when not given."""
-    a = MsaAppend()
-    R, HG = pb.total_rows, pb.H * pb.G
-    pb._check_cache(k, "k", pb.D)
-    pb._check_cache(v, "v", pb.D)
+    R, H, D, Di, dev = pb.total_rows, pb.H, pb.D, pb.Di, pb.device
+    pb._check_cache(k, "k", D)
+    pb._check_cache(v, "v", D)
+    ks, vs = _rows(new_k, "new_k", R, H, D, dev), _rows(new_v, "new_v", R, H, D, dev)
+    ikp = ikc = qp = iqp = qo = iqo = None
+    iks = qs = iqs = 0
+    q_out = iq_out = None
     if (new_ik is None) != (ik is None):
         raise ValueError("new_ik and ik go together")
-    q_out = iq_out = None
-    for name, t, shape in (("k", new_k, (R, pb.H, pb.D)), ("v", new_v, (R, pb.H, pb.D)), ("ik", new_ik, (R, pb.KH, pb.Di)),
-                           ("q", q, (R, HG, pb.D)), ("iq", iq, (R, pb.H, pb.Di))):
-        if t is not None:
-            setattr(a, name + "_stride", _rows(t, name if name in ("q", "iq") else "new_" + name, shape, pb.device))
-            setattr(a, name, t.data_ptr())
     if ik is not None:
-        pb._check_cache(ik, "ik", pb.Di, pb.KH)
-        a.ik_cache = ik.data_ptr()
+        iks = _rows(new_ik, "new_ik", R, pb.KH, Di, dev)
+        pb._check_cache(ik, "ik", Di, pb.KH)
+        ikp, ikc = new_ik.data_ptr(), ik.data_ptr()
     if q is not None:
-        q_out = torch.empty(R, HG, pb.D, dtype=torch.bfloat16, device=pb.device)
-        a.q_out = q_out.data_ptr()
+        qs = _rows(q, "q", R, H * pb.G, D, dev)
+        q_out = torch.empty((R, H * pb.G, D), dtype=torch.bfloat16, device=dev)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     if iq is not None:
-        iq_out = torch.empty(R, pb.H, pb.Di, dtype=torch.bfloat16, device=pb.device)
-        a.iq_out = iq_out.data_ptr()
-    a.k_cache, a.v_cache = k.data_ptr(), v.data_ptr()
-    if pb.k_scale is not None:
-        a.k_scale, a.v_scale = pb.k_scale.data_ptr(), pb.v_scale.data_ptr()
+        iqs = _rows(iq, "iq", R, H, Di, dev)
+        iq_out = torch.empty((R, H, Di), dtype=torch.bfloat16, device=dev)
+        iqp, iqo = iq.data_ptr(), iq_out.data_ptr()
     c_rope = None
     if rope is not None:
-        if rope.device != pb.device:
-            raise ValueError(f"rope must be on {pb.device}, got {rope.device}")
-        c_rope = MsaRope(rope.dim, rope.index_dim, rope.axes, int(rope.interleaved), rope.turns.data_ptr(),
-                         rope.index_turns.data_ptr(), None if rope.axis is None else rope.axis.data_ptr(),
-                         None if rope.index_axis is None else rope.index_axis.data_ptr())
+        if rope.device != dev:
+            raise ValueError(f"rope must be on {dev}, got {rope.device}")
         if positions is not None:
-            _need(positions, "positions", torch.int32, pb.device, (rope.axes, R))
-            c_rope.positions = positions.data_ptr()
+            _need(positions, "positions", torch.int32, dev, (rope.axes, R))
+        c_rope = C.byref(rope._struct(positions))
     elif positions is not None:
         raise ValueError("positions need a rope")
-    ws = torch.empty(APPEND_WORKSPACE_BYTES, dtype=torch.uint8, device=pb.device) if workspace is None else workspace
-    _need(ws, "workspace", torch.uint8, pb.device)
-    with _on(pb.device):
-        _check(_lib.msa_append_cache(C.byref(pb.c), C.byref(a), None if c_rope is None else C.byref(c_rope), _ptr(ws),
-                                     ws.numel(), _stream(pb.device)))
+    a = MsaAppend(new_k.data_ptr(), new_v.data_ptr(), ikp, qp, iqp, ks, vs, iks, qs, iqs, k.data_ptr(), v.data_ptr(), ikc,
+                  pb.c.k_scale, pb.c.v_scale, qo, iqo)
+    ws = torch.empty(APPEND_WORKSPACE_BYTES, dtype=torch.uint8, device=dev) if workspace is None else workspace
+    _need(ws, "workspace", torch.uint8, dev)
+    with _on(dev):
+        _check(_lib.msa_append_cache(pb._ref, C.byref(a), c_rope, ws.data_ptr(), ws.numel(), _raw_stream(dev.index)))
     return q_out, iq_out
 
 
@@ -456,13 +468,15 @@ def dense_forward(pb: Problem, q, k, v, out=None, workspace=None):
     pb._check_q(q)
     pb._check_cache(k, "k", pb.D)
     pb._check_cache(v, "v", pb.D)
-    out = pb.new_out() if out is None else out
-    _need(out, "out", pb.out_dtype, pb.device, (pb.total_rows, pb.H * pb.G, pb.D))
+    if out is None:
+        out = pb.new_out()
+    else:
+        _need(out, "out", pb.out_dtype, pb.device, (pb.total_rows, pb.H * pb.G, pb.D))
     ws = pb.dense_workspace() if workspace is None else workspace
     _need(ws, "workspace", torch.uint8, pb.device)
     with _on(pb.device):
-        _check(_lib.msa_dense_forward(C.byref(pb.c), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(ws), ws.numel(),
-                                      _stream(pb.device)))
+        _check(_lib.msa_dense_forward(pb._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                                      ws.numel(), _raw_stream(pb.device.index)))
     return out
 
 

@@ -884,9 +884,6 @@ msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
     if (workspace_bytes < MSA_APPEND_WORKSPACE_BYTES)
         return fail(MSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %d", workspace_bytes, MSA_APPEND_WORKSPACE_BYTES);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(uint32_t), st);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
     msa::AppendArgs x{};
     x.k = static_cast<const uint16_t*>(a->k);
     x.v = static_cast<const uint16_t*>(a->v);
@@ -930,7 +927,7 @@ msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa
     x.kv_int8 = i8;
     x.cache_tokens = p->cache_tokens;
     x.err = static_cast<uint32_t*>(workspace);
-    e = msa::run_append_cache(x, st);
+    const cudaError_t e = msa::run_append_cache(x, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MSA_OK : cuda_fail(e, "cache writer launch");
 }
 
