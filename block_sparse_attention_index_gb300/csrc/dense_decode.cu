@@ -67,7 +67,7 @@ __device__ __forceinline__ void dd_ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr));
 }
 __device__ __forceinline__ void dd_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -84,7 +84,7 @@ __device__ __forceinline__ uint4 dd_lds128(uint32_t addr) {
     return v;
 }
 __device__ __forceinline__ void dd_mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     }
                 }
             }
+            const int i_first = (u - u0) * H, tiles = (end - u) * H;  // of this part
             float vref = 0.f, vinv = 0.f;  // int8: the power of two that the value scales are divided by, its inverse
             float o[16][4], mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
 #pragma unroll
@@ -563,27 +564,32 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                         }
                     }
                 } else {
+                    // 32 dims at a time, four accumulators in turn (each product waits for the last on its accumulator)
 #pragma unroll
-                    for (int n2 = 0; n2 < 8; ++n2) {  // 16 dims
-                        float t[2][4];
+                    for (int n4 = 0; n4 < 4; ++n4) {
+                        float t[4][4];
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+                        for (int n = 0; n < 4; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            uint32_t r[4];
-                            const int key = 16 * kk + (lane & 15), chunk = (n2 & 3) * 2 + (lane >> 4);
-                            dd_ldsm_x4_t(vb + (n2 >> 2) * (Cfg::kPlane / 2) + key * 128 + ((chunk ^ (key & 7)) << 4), r);
+                            uint32_t r[2][4];
+                            const int key = 16 * kk + (lane & 15);
 #pragma unroll
-                            for (int part = 0; part < kParts; ++part) {
-                                dd_mma(kApart ? t[0] : o[2 * n2], pa[kk][part], r[0], r[1]);
-                                dd_mma(kApart ? t[1] : o[2 * n2 + 1], pa[kk][part], r[2], r[3]);
+                            for (int y = 0; y < 2; ++y) {
+                                const int n2 = 2 * n4 + y, chunk = (n2 & 3) * 2 + (lane >> 4);
+                                dd_ldsm_x4_t(vb + (n2 >> 2) * (Cfg::kPlane / 2) + key * 128 + ((chunk ^ (key & 7)) << 4), r[y]);
                             }
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                                for (int n = 0; n < 4; ++n)
+                                    dd_mma(kApart ? t[n] : o[4 * n4 + n], pa[kk][part], r[n >> 1][2 * (n & 1)], r[n >> 1][2 * (n & 1) + 1]);
                         }
                         if constexpr (kApart) {
 #pragma unroll
-                            for (int n = 0; n < 2; ++n)
+                            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) o[2 * n2 + n][e] += t[n][e];
+                                for (int e = 0; e < 4; ++e) o[4 * n4 + n][e] += t[n][e];
                         }
                     }
                 }
@@ -600,6 +606,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
             // ---- the warps of a head join their parts (8 / H of them, by halves)
 #pragma unroll
             for (int half = kDdConsumers / 2; half >= H; half >>= 1) {
+                if (i_first % kDdConsumers == 0 && tiles <= half) continue;  // warps from `half` on had no tile
                 dd_sync_consumers();
                 if (warp >= half && warp < 2 * half) {
                     float* dst = merge + (warp - half) * (kDdMergeWords * 32) + lane;
@@ -669,14 +676,20 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     if (tid == 0) a.err_slots[blockIdx.x] = err;
 }
 
-// Joins the parts of the sequences that several CTAs walked.  CTA (c, h) takes the (sequence, tile) in which boundary
-// c + 1 of the shares is the first to fall, if any; a warp takes one (row, head) pair: the parts' maxima and sums
-// first, then 2^(m_i - m) O_i summed in the parts' order (the same every time), 4 of the 128 values a lane.
+// Joins the parts of the sequences that several CTAs walked.  CTA (x, h, z) takes a (sequence, tile), x itself where
+// they are no more than the shares (by_tile: tiles a sequence may have), else the one in which boundary x + 1 of the
+// shares is the first to fall, if any; and four of its (row, head) pairs; four warps share a pair,
+// each a quarter of the parts (their loads all in flight: one warp a pair took 5.5 us for 64 parts), 4 of the 128 values
+// a lane.  The parts' maximum first, then 2^(m_i - m) O_i summed in the parts' order within each warp and the warps'
+// order after that: the same every time.
 constexpr int kDcThreads = 512;
-__global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseArgs a, int grid) {
+__global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseArgs a, int grid, int by_tile) {
+    __shared__ float4 sum_o[4][4][32];
+    __shared__ float sum_l[4][4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+    const int pair = blockIdx.z * 4 + (warp >> 2), quarter = warp & 3;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (blockIdx.x == 0 && h == 0 && warp == 0) {  // what the shares' CTAs found wrong
+    if (blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the shares' CTAs found wrong
         uint32_t e = 0;
         for (int c = lane; c < grid; c += 32) e |= a.err_slots[c];
         e = __reduce_or_sync(0xffffffffu, e);
@@ -687,61 +700,85 @@ __global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseAr
     }
     const int64_t total = a.unit_prefix[a.num_seqs];
     const int shares = dd_shares(static_cast<int>(total), grid);
-    const int c = blockIdx.x;  // boundary between shares c and c + 1
-    if (c + 1 >= shares) return;
-    const int start = static_cast<int>(total * c / shares), cut = static_cast<int>(total * (c + 1) / shares);
-    int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= cut
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.unit_prefix[mid] <= cut) lo = mid; else hi = mid;
+    if (shares == 0) return;
+    int c = 0, lo, mt, start;  // first share of the parts, sequence, tile; first unit of that share
+    if (by_tile > 0) {
+        lo = blockIdx.x / by_tile;
+        mt = blockIdx.x - lo * by_tile;
+        if (a.unit_prefix[lo + 1] == a.unit_prefix[lo]) return;
+    } else {
+        c = blockIdx.x;  // boundary between shares c and c + 1
+        if (c + 1 >= shares) return;
+        const int cut = static_cast<int>(total * (c + 1) / shares);
+        lo = 0;
+        int hi = a.num_seqs;  // largest b with prefix[b] <= cut
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.unit_prefix[mid] <= cut) lo = mid; else hi = mid;
+        }
+        mt = (cut - a.unit_prefix[lo]) / dd_blocks(a.cache_lens[lo]);
     }
     const DdSeq s = dd_seq(a, lo);
-    const int mt = (cut - a.unit_prefix[lo]) / s.blocks, seg0 = a.unit_prefix[lo] + mt * s.blocks, seg1 = seg0 + s.blocks;
-    // the boundary lies between two of them, or an earlier boundary inside the same one has a CTA that joins it
-    if (cut == seg0 || start > seg0) return;
-    // the share that holds its last unit: the largest c with total c / shares <= seg1 - 1
+    if (mt >= s.tiles) return;
+    const int seg0 = a.unit_prefix[lo] + mt * s.blocks, seg1 = seg0 + s.blocks;
+    // the shares that hold its first and last units: the largest c with total c / shares <= unit
+    const int first = static_cast<int>((static_cast<int64_t>(seg0 + 1) * shares - 1) / total);
     const int last = static_cast<int>((static_cast<int64_t>(seg1) * shares - 1) / total);
+    // one share wrote it whole; the boundary lies between two tiles, or an earlier one inside the tile has its CTA
+    if (first == last || (by_tile == 0 && first != c)) return;
+    c = first;
+    start = static_cast<int>(total * c / shares);
     const int count = last - c + 1;
-    const int pairs = min(16, s.n * a.G - 16 * mt);
-    if (warp >= pairs) return;
+    if (static_cast<int>(blockIdx.z) * 4 >= min(16, s.n * a.G - 16 * mt)) return;
+    const bool live = pair < min(16, s.n * a.G - 16 * mt);
     // share c's part is its second one unless the share began with it; the others' are the first of their shares
     const int slot0 = 2 * c + (start < seg0 ? 1 : 0);
-    auto row_of = [&](int i) { return (static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * a.H + h) * 16 + warp; };
+    auto row_of = [&](int i) { return (static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * a.H + h) * 16 + (live ? pair : 0); };
     float m = -INFINITY;
     for (int i = lane; i < count; i += 32) m = fmaxf(m, a.part_ml[row_of(i) * 2]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < count; i0 += 32) {
-        float f = 0.f;
-        if (i0 + lane < count) {
-            const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + row_of(i0 + lane) * 2);
-            f = ml.x == -INFINITY ? 0.f : dd_exp2(ml.x - m);
-            l += ml.y * f;
+    const int i_begin = count * quarter / 4, i_end = count * (quarter + 1) / 4;
+    float l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = i_begin; i0 < i_end; i0 += 8) {  // eight parts' loads in flight
+        float4 v[8];
+        float2 ml[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int64_t at = row_of(min(i0 + u, i_end - 1));
+            ml[u] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+            v[u] = *reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + 4 * lane);
         }
-        const int n = min(32, count - i0);
-        for (int i = 0; i < n; i += 8) {  // eight parts' loads in flight
-            float4 v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                v[u] = *reinterpret_cast<const float4*>(a.part_o + row_of(i0 + min(i + u, n - 1)) * kHeadDim + 4 * lane);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float w = __shfl_sync(0xffffffffu, f, min(i + u, 31));
-                if (i + u < n && w != 0.f) {
-                    x[0] = fmaf(w, v[u].x, x[0]);
-                    x[1] = fmaf(w, v[u].y, x[1]);
-                    x[2] = fmaf(w, v[u].z, x[2]);
-                    x[3] = fmaf(w, v[u].w, x[3]);
-                }
+        for (int u = 0; u < 8; ++u) {
+            if (i0 + u >= i_end) break;
+            const float w = ml[u].x == -INFINITY ? (ml[u].y == ml[u].y ? 0.f : ml[u].y) : dd_exp2(ml[u].x - m);
+            if (w != 0.f) {
+                l = fmaf(w, ml[u].y, l);
+                x.x = fmaf(w, v[u].x, x.x);
+                x.y = fmaf(w, v[u].y, x.y);
+                x.z = fmaf(w, v[u].z, x.z);
+                x.w = fmaf(w, v[u].w, x.w);
             }
         }
     }
+    sum_o[warp >> 2][quarter][lane] = x;
+    if (lane == 0) sum_l[warp >> 2][quarter] = l;
+    __syncthreads();
+    if (quarter != 0 || !live) return;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int q = 1; q < 4; ++q) {
+        const float4 y = sum_o[warp >> 2][q][lane];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+        l += sum_l[warp >> 2][q];
+    }
     const float inv = 1.f / l;
-    dd_store2(a, s, h, 16 * mt + warp, 4 * lane, x[0] * inv, x[1] * inv);
-    dd_store2(a, s, h, 16 * mt + warp, 4 * lane + 2, x[2] * inv, x[3] * inv);
+    dd_store2(a, s, h, 16 * mt + pair, 4 * lane, x.x * inv, x.y * inv);
+    dd_store2(a, s, h, 16 * mt + pair, 4 * lane + 2, x.z * inv, x.w * inv);
 }
 
 template <int H, bool kInt8, int kParts>
@@ -763,15 +800,21 @@ static cudaError_t launch_dense_decode(const DenseArgs& a, int grid, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, *a.k_map, *a.v_map, a)) != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(a.H), 1);
+    // tiles or boundaries, heads, groups of four (row, head) pairs
+    const int tiles = (a.pairs_most + 15) / 16;
+    const int by_tile = a.num_seqs * tiles <= grid ? tiles : 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(by_tile > 0 ? a.num_seqs * tiles : grid), static_cast<unsigned>(a.H),
+                       (std::min(16, a.pairs_most) + 3) / 4);
     cfg.blockDim = dim3(kDcThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, dense_combine_kernel, a, grid);
+    return cudaLaunchKernelEx(&cfg, dense_combine_kernel, a, grid, by_tile);
 }
 
-int dense_decode_shares(int64_t units) {
+// CTAs for so many units: one a SM at most, and at least two tiles each (fewer parts to join, the same latency).
+int dense_decode_shares(int64_t units, int H) {
     const int64_t sms = std::min(device_sm_count(), kDenseMaxShares);
-    return static_cast<int>(units < 1 ? 1 : (units < sms ? units : sms));
+    const int64_t n = std::min(units, std::max<int64_t>(1, units * H / 2));
+    return static_cast<int>(n < 1 ? 1 : (n < sms ? n : sms));
 }
 
 template <int H>

@@ -217,6 +217,7 @@ struct DenseArgs {
     const CUtensorMap* v_map;
     CacheRows seq_cache;       // the caches as the problem gives them (cache: the widened copy for int8 prompts)
     int64_t seq_cache_tokens;
+    int pairs_most;        // decode family: most (row, head) pairs of a sequence that its kernel takes
     int32_t* unit_prefix;  // [num_seqs + 1] decode family: units before each sequence
     float* part_o;         // parts of what several CTAs walk: O [.., 128], decode family [2 shares, H, 16]
     float* part_ml;        // and their maxima and sums [.., 2]
@@ -229,7 +230,7 @@ constexpr int kDenseMaxSplit = 32;    // most key ranges of an M tile
 // Prompt chunks (M tile pairs of 2 (128 / G) rows) and drafted windows (one M tile a sequence); items: host bound.
 cudaError_t run_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream);
 cudaError_t run_dense_window(const DenseArgs& a, int items, int nsplit, cudaStream_t stream);
-int dense_decode_shares(int64_t units);  // CTAs for so many blocks
+int dense_decode_shares(int64_t units, int H);  // CTAs for so many blocks
 cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream);
 
 // Allocation-free decode attention: scratch in a file-scope device array

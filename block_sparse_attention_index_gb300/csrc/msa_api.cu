@@ -972,6 +972,7 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
     a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
     a.tile_windows = d.windows;
+    a.pairs_most = d.windows ? 16 : static_cast<int>(decode_rows_per_seq(p)) * p->group_size;
     a.only_multi_row = decode_family(p);
     a.q = static_cast<const uint16_t*>(q);
     a.k = k_cache;
@@ -1000,7 +1001,7 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
         const int64_t seqs = p->num_decode_seqs > 0 ? p->num_decode_seqs : p->num_seqs;
         const int64_t tiles = d.windows ? 1 : (static_cast<int64_t>(decode_rows_per_seq(p)) * p->group_size + 15) / 16;
         const int64_t blocks = (p->max_cache_len + msa::kBlock - 1) / msa::kBlock;
-        if ((e = msa::run_dense_decode(a, msa::dense_decode_shares(seqs * tiles * blocks), st)) != cudaSuccess)
+        if ((e = msa::run_dense_decode(a, msa::dense_decode_shares(seqs * tiles * blocks, p->num_kv_heads), st)) != cudaSuccess)
             return cuda_fail(e, "dense decode attention launch");
     }
     if (d.windows && (e = msa::run_dense_window(a, static_cast<int>(d.window_items), d.window_split, st)) != cudaSuccess)
