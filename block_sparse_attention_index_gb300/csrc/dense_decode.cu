@@ -6,8 +6,8 @@
 // Bound by memory: each cached position is H x 512 bytes (264 with an int8 cache) that are read once for all query
 // heads of the sequence's rows.  The cache is split over its length: one CTA per SM takes an even share of all
 // 64-position blocks of all sequences (from the lengths on the device, so ragged batches balance) and streams them
-// through a ring of shared-memory stages, one (block, KV head) tile of K and V each, by TMA boxes issued by a
-// producer warp.  Heads of a block are neighbours in the ring, so memory is read in whole 64 H-row runs.  Eight
+// through a ring of shared-memory stages, one (block, KV head) tile of K and V each, by TMA boxes issued by two
+// producer warps.  Heads of a block are neighbours in the ring, so memory is read in whole 64 H-row runs.  Eight
 // consumer warps take the tiles in turn; 8 is a multiple of H, so a warp stays with one head and keeps its queries (A
 // operand, 16 (row, head) pairs) and O (accumulators) in registers.  S = Q K^T and O += P V run on mma.sync
 // m16n8k16: 16 rows are all a tile has (tcgen05 wants 128), and 12 to 16 FLOP a byte are well within its rate.
@@ -36,10 +36,11 @@
 namespace msa {
 
 constexpr int kDdConsumers = 8;
-// Two warpgroups of consumers and one whose first warp is the producer.  Registers move from the last to the others:
+// Two warpgroups of consumers and one whose first two warps are the producers.  Registers move from the last to the others:
 // launched with 168 a thread (64,512), 256 x 208 + 128 x 88 = 64,512 after the split.
 constexpr int kDdThreads = 384;
-constexpr int kDdMergeWords = 64 + 4;  // O, m and l of a lane
+constexpr int kDdMergeWords = 32 + 4;  // half of O, m and l of a lane
+constexpr int kDdPrefix = 512;         // sequences whose unit prefix is kept in shared memory (more: in the workspace)
 
 // Tile i lands in stage i % kStages and completes barrier i % 16.  16 is a multiple of the consumers, so each of them
 // sees its barriers' phases one after the other (a warp that saw only some of a stage's phases could not tell them
@@ -50,7 +51,7 @@ template <bool kInt8>
 struct DdCfg {
     static constexpr int kPlane = kInt8 ? kBlock * kHeadDim : kBlock * kHeadDim * 2;  // K or V of a tile
     static constexpr int kStageBytes = 2 * kPlane + (kInt8 ? 1024 : 0);               // int8: 64 key, 64 value scales
-    static constexpr int kStages = kInt8 ? 9 : 5;
+    static constexpr int kStages = kInt8 ? 12 : 6;  // even: see the producers
     static constexpr int kMergeBytes = 4 * kDdMergeWords * 32 * 4;
     static_assert(kStages <= kDdFull, "a tile's barrier must not be armed twice ahead of its consumer");
     static constexpr int kBarArrivals = kInt8 ? 33 : 1;  // the producer lane, and the scale copies of the 32 lanes
@@ -97,6 +98,8 @@ __device__ __forceinline__ uint32_t dd_even_f16(uint32_t w) {
     __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&bias));
     return *reinterpret_cast<uint32_t*>(&r);
 }
+// The same without taking the 1152 off.
+__device__ __forceinline__ uint32_t dd_even_biased(uint32_t w) { return (w & 0x00FF00FFu) ^ 0x64806480u; }
 __device__ __forceinline__ uint32_t dd_pack_f16(float lo, float hi) {
     __half2 r = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&r);
@@ -113,11 +116,10 @@ __device__ __forceinline__ int dd_blocks(int L) { return (L + kBlock - 1) / kBlo
 // Units (blocks x tiles) of sequence b; 0 if it is not of the decode family or its metadata is bad.
 __device__ __forceinline__ int dd_units(const DenseArgs& a, int b, bool& bad) {
     bad = false;
-    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0;
+    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0, L = a.cache_lens[b];
+    const bool placed = seq_rows_ok(a.cache, b, L, a.cache_tokens);  // (loads that need not wait for one another)
     if (n == 0 || n > kDecodeMaxRows || (a.tile_windows && n * a.G > 16)) return 0;
-    const int L = a.cache_lens[b];
-    if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
-        !seq_rows_ok(a.cache, b, L, a.cache_tokens)) {
+    if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len || !placed) {
         bad = true;
         return 0;
     }
@@ -156,7 +158,9 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* merge = reinterpret_cast<float*>(ring + Cfg::kStages * Cfg::kStageBytes);
-    int32_t* prefix = reinterpret_cast<int32_t*>(ring + Cfg::kStages * Cfg::kStageBytes + Cfg::kMergeBytes);  // [num_seqs + 1]
+    // [num_seqs + 1]; in the workspace every CTA writes the same values
+    int32_t* prefix = a.num_seqs < kDdPrefix ? reinterpret_cast<int32_t*>(ring + Cfg::kStages * Cfg::kStageBytes + Cfg::kMergeBytes)
+                                             : a.unit_prefix;
     __shared__ uint64_t full[kDdFull], empty[Cfg::kStages];
     __shared__ int warp_tot[kDdThreads / 32];
     __shared__ uint32_t err;
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     }
     if (tid == 0) prefix[a.num_seqs] = carry;
     __syncthreads();
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && a.num_seqs < kDdPrefix)
         for (int b = tid; b <= a.num_seqs; b += kDdThreads) a.unit_prefix[b] = prefix[b];
     const int64_t total = carry;
     const int shares = dd_shares(carry, gridDim.x);  // CTAs with work
@@ -218,8 +222,12 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 
     if (warp >= kDdConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == kDdConsumers) {
-        // ---------------- producer: 32 blocks' cache rows at a time, one lane each, then their tiles in order
+        if (warp < kDdConsumers + 2) {
+        // ---------------- two producers, the even and the odd tiles (one warp's barrier tests, copies and scale copies,
+        // 870 cycles an int8 tile, held 8 ragged int8 sequences to 59 us).  With an even number of stages each of them
+        // sees every phase of its stages.  32 blocks' cache rows at a time, one lane each, then their tiles in order.
+        static_assert(Cfg::kStages % 2 == 0, "a producer must see every phase of its stages");
+        const int odd = warp - kDdConsumers;
         int b = first_b, tile = 0;
         bool alive = true;
         for (int base = u0; base < u1 && alive; base += 32) {
@@ -244,6 +252,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                 const int n = __shfl_sync(0xffffffffu, live, i);
 #pragma unroll 1
                 for (int h = 0; h < H; ++h, ++tile) {
+                    if ((tile & 1) != odd) continue;
                     const int s = tile % Cfg::kStages;
                     int ok = 1;
                     if (lane == 0 && tile >= Cfg::kStages) ok = mbar_wait(&empty[s], ((tile / Cfg::kStages) - 1) & 1, &err);
@@ -284,12 +293,15 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
         }
         // no copy of this warp may be in flight when the CTA ends
         if (lane == 0)
-            for (int s = 0; s < kDdFull && s < tile; ++s) mbar_wait(&full[s], ((tile - 1 - s) / kDdFull) & 1, &err);
+            for (int s = odd; s < kDdFull && s < tile; s += 2) mbar_wait(&full[s], ((tile - 1 - s) / kDdFull) & 1, &err);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------- consumer warp: tiles warp, warp + 8, ... of the CTA, all of head warp % H
         const int grp = lane >> 2, tig = lane & 3, h = warp % H;
+        // int8, bf16 outputs: the keys keep their bias and the accumulators begin at -1152 sum q (its cancellation costs
+        // some 1e-5 of a score's spread, far below the outputs' rounding; fp32 outputs take the bias off)
+        constexpr bool kBiased = kInt8 && kParts == 1;
         bool alive = true;
         int i = warp, b = first_b;
         for (int u = u0; u < u1;) {
@@ -305,6 +317,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
             const int first_pos = s.L - s.n + 16 * mt / a.G;  // the tile's earliest row
             uint32_t qa[8][4];
             float qf[2];  // factor from the product to the log2 domain, rows grp and grp + 8
+            float qsum[2] = {0.f, 0.f};  // int8, biased keys: what the bias adds to the rows' products, negated
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int m = 16 * mt + min(grp + 8 * e, pairs - 1), qi = m / a.G, g = m - qi * a.G;
@@ -315,22 +328,34 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     // dims 32 tig + 4 ks + {0, 2} and {1, 3}: the order in which a word of four key bytes is widened
                     float v[32], top = 0.f;
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const uint32_t w = src[16 * tig + x];
-                        v[2 * x] = bf16_lo(w);
-                        v[2 * x + 1] = bf16_hi(w);
-                        top = fmaxf(top, fmaxf(fabsf(v[2 * x]), fabsf(v[2 * x + 1])));
+                    for (int x4 = 0; x4 < 4; ++x4) {
+                        const uint4 w4 = *reinterpret_cast<const uint4*>(src + 16 * tig + 4 * x4);
+                        const uint32_t ws[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int x = 4 * x4 + y;
+                            v[2 * x] = bf16_lo(ws[y]);
+                            v[2 * x + 1] = bf16_hi(ws[y]);
+                            top = fmaxf(top, fmaxf(fabsf(v[2 * x]), fabsf(v[2 * x + 1])));
+                        }
                     }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const uint32_t ex = min(max(__float_as_uint(top) >> 23, 9u), 253u);
                     const float f = __uint_as_float((262u - ex) << 23);  // 2^(8 - exponent of the row's largest)
                     qf[e] *= __uint_as_float((ex - 8u) << 23);
+                    float all = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         qa[ks][e] = dd_pack_f16(v[4 * ks] * f, v[4 * ks + 2] * f);
                         qa[ks][2 + e] = dd_pack_f16(v[4 * ks + 1] * f, v[4 * ks + 3] * f);
+                        const float2 q02 = __half22float2(*reinterpret_cast<const __half2*>(&qa[ks][e]));
+                        const float2 q13 = __half22float2(*reinterpret_cast<const __half2*>(&qa[ks][2 + e]));
+                        all += (q02.x + q02.y) + (q13.x + q13.y);
                     }
+                    all += __shfl_xor_sync(0xffffffffu, all, 1);
+                    all += __shfl_xor_sync(0xffffffffu, all, 2);
+                    qsum[e] = kBiased ? -1152.f * all : 0.f;
                 } else {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {  // dims 16 ks + 2 tig, + 8
@@ -355,14 +380,18 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                 float c[8][4];
 #pragma unroll
                 for (int nt = 0; nt < 8; ++nt) {
-                    c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
+                    c[nt][0] = c[nt][1] = qsum[0];
+                    c[nt][2] = c[nt][3] = qsum[1];
                     if constexpr (kInt8) {
                         const int row = nt * 8 + grp;
                         const uint4 w0 = dd_lds128(kb + row * 128 + (((2 * tig) ^ (row & 7)) << 4));
                         const uint4 w1 = dd_lds128(kb + row * 128 + (((2 * tig + 1) ^ (row & 7)) << 4));
                         const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) dd_mma_f16(c[nt], qa[ks], dd_even_f16(w[ks]), dd_even_f16(w[ks] >> 8));
+                        for (int ks = 0; ks < 8; ++ks) {
+                            if constexpr (kBiased) dd_mma_f16(c[nt], qa[ks], dd_even_biased(w[ks]), dd_even_biased(w[ks] >> 8));
+                            else dd_mma_f16(c[nt], qa[ks], dd_even_f16(w[ks]), dd_even_f16(w[ks] >> 8));
+                        }
                     } else {
                         const int row = nt * 8 + (lane & 7);
 #pragma unroll
@@ -375,26 +404,33 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                         }
                     }
                 }
-                // hidden keys -inf; int8: times the key scales, and the value scales of the lane's 16 keys
-                float vs[8][2];
+                // int8: times the key scales; the value scales of the lane's 16 keys
+                float2 vs[8];
+                if constexpr (kInt8) {
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                    const int t = t0 + nt * 8 + 2 * tig;
-                    if constexpr (kInt8) {
+                    for (int nt = 0; nt < 8; ++nt) {
                         const float2 ks = *reinterpret_cast<const float2*>(stage + 2 * Cfg::kPlane + (nt * 8 + 2 * tig) * 4);
-                        const float2 v2 = *reinterpret_cast<const float2*>(stage + 2 * Cfg::kPlane + 256 + (nt * 8 + 2 * tig) * 4);
-                        c[nt][0] *= ks.x;
-                        c[nt][1] *= ks.y;
-                        c[nt][2] *= ks.x;
-                        c[nt][3] *= ks.y;
-                        vs[nt][0] = edge && t >= s.L ? 0.f : v2.x;
-                        vs[nt][1] = edge && t + 1 >= s.L ? 0.f : v2.y;
+                        vs[nt] = *reinterpret_cast<const float2*>(stage + 2 * Cfg::kPlane + 256 + (nt * 8 + 2 * tig) * 4);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 x = __fmul2_rn(make_float2(c[nt][2 * e], c[nt][2 * e + 1]), ks);
+                            c[nt][2 * e] = x.x;
+                            c[nt][2 * e + 1] = x.y;
+                        }
                     }
-                    if (edge) {  // (scaled here: a scale of zero must not meet an infinity)
+                }
+                if (edge) {  // hidden keys -inf (scaled here: a scale of zero must not meet an infinity)
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt) {
+                        const int t = t0 + nt * 8 + 2 * tig;
                         c[nt][0] = t > pos[0] ? -INFINITY : c[nt][0] * qf[0];
                         c[nt][1] = t + 1 > pos[0] ? -INFINITY : c[nt][1] * qf[0];
                         c[nt][2] = t > pos[1] ? -INFINITY : c[nt][2] * qf[1];
                         c[nt][3] = t + 1 > pos[1] ? -INFINITY : c[nt][3] * qf[1];
+                        if constexpr (kInt8) {
+                            if (t >= s.L) vs[nt].x = 0.f;
+                            if (t + 1 >= s.L) vs[nt].y = 0.f;
+                        }
                     }
                 }
                 const float f0 = edge ? 1.f : qf[0], f1 = edge ? 1.f : qf[1];  // what is left to multiply by
@@ -417,15 +453,17 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                 if constexpr (kInt8) {
                     float big = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < 8; ++nt) big = fmaxf(big, fmaxf(fabsf(vs[nt][0]), fabsf(vs[nt][1])));
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                    if (big > vref && big < INFINITY) {  // the same in every lane; the next power of two, at most 2^127
+                    for (int nt = 0; nt < 8; ++nt) big = fmaxf(big, fmaxf(fabsf(vs[nt].x), fabsf(vs[nt].y)));
+                    if (big > vref && big < INFINITY) {  // the next power of two, at most 2^127
                         vnew = __uint_as_float(min((__float_as_uint(big) + 0x007FFFFFu) & 0x7F800000u, 0x7F000000u));
                         grew = true;
                     }
                 }
                 if (__any_sync(0xffffffffu, grew)) {
+                    if constexpr (kInt8) {  // the same in every lane
+                        vnew = fmaxf(vnew, __shfl_xor_sync(0xffffffffu, vnew, 1));
+                        vnew = fmaxf(vnew, __shfl_xor_sync(0xffffffffu, vnew, 2));
+                    }
                     const float fv = kInt8 ? (vnew > 0.f ? vref / vnew : 1.f) : 1.f;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -442,33 +480,43 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     vinv = vnew > 0.f ? 1.f / vnew : 0.f;
                 }
                 constexpr float kLift = kInt8 ? 14.f : 0.f;  // f16 weights: 2^14 at most
-                const float base0 = (mrun[0] == -INFINITY ? 0.f : mrun[0]) - kLift;
-                const float base1 = (mrun[1] == -INFINITY ? 0.f : mrun[1]) - kLift;
+                {
+                    const float b0 = kLift - (mrun[0] == -INFINITY ? 0.f : mrun[0]), b1 = kLift - (mrun[1] == -INFINITY ? 0.f : mrun[1]);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                    c[nt][0] = dd_exp2(fmaf(c[nt][0], f0, -base0));
-                    c[nt][1] = dd_exp2(fmaf(c[nt][1], f0, -base0));
-                    c[nt][2] = dd_exp2(fmaf(c[nt][2], f1, -base1));
-                    c[nt][3] = dd_exp2(fmaf(c[nt][3], f1, -base1));
-                }
-                float sum[2] = {0.f, 0.f};
+                    for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                    sum[0] += c[nt][0] + c[nt][1];
-                    sum[1] += c[nt][2] + c[nt][3];
+                        for (int e = 0; e < 2; ++e) {
+                            const float f = e ? f1 : f0, b = e ? b1 : b0;
+                            float2 x = __ffma2_rn(make_float2(c[nt][2 * e], c[nt][2 * e + 1]), make_float2(f, f), make_float2(b, b));
+                            x = make_float2(dd_exp2(x.x), dd_exp2(x.y));
+                            sum[e] = __fadd2_rn(sum[e], x);
+                            c[nt][2 * e] = x.x;
+                            c[nt][2 * e + 1] = x.y;
+                        }
+                    lrun[0] += sum[0].x + sum[0].y;
+                    lrun[1] += sum[1].x + sum[1].y;
                 }
-                lrun[0] += sum[0];
-                lrun[1] += sum[1];
                 if constexpr (kInt8) {
+                    if (edge) {  // a hidden key's weight stays 0 whatever its scale is
 #pragma unroll
-                    for (int nt = 0; nt < 8; ++nt) {
-                        vs[nt][0] *= vinv;
-                        vs[nt][1] *= vinv;
-                        // a hidden key's weight stays 0 whatever its scale is
-                        c[nt][0] = edge && c[nt][0] == 0.f ? 0.f : c[nt][0] * vs[nt][0];
-                        c[nt][1] = edge && c[nt][1] == 0.f ? 0.f : c[nt][1] * vs[nt][1];
-                        c[nt][2] = edge && c[nt][2] == 0.f ? 0.f : c[nt][2] * vs[nt][0];
-                        c[nt][3] = edge && c[nt][3] == 0.f ? 0.f : c[nt][3] * vs[nt][1];
+                        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float v = (e & 1 ? vs[nt].y : vs[nt].x) * vinv;
+                                c[nt][e] = c[nt][e] == 0.f ? 0.f : c[nt][e] * v;
+                            }
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < 8; ++nt) {
+                            const float2 v = __fmul2_rn(vs[nt], make_float2(vinv, vinv));
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float2 x = __fmul2_rn(make_float2(c[nt][2 * e], c[nt][2 * e + 1]), v);
+                                c[nt][2 * e] = x.x;
+                                c[nt][2 * e + 1] = x.y;
+                            }
+                        }
                     }
                 } else if (edge) {
                     // Keys hidden from some row may hold anything: their values leave the products (zeroed in
@@ -607,32 +655,39 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 #pragma unroll
             for (int half = kDdConsumers / 2; half >= H; half >>= 1) {
                 if (i_first % kDdConsumers == 0 && tiles <= half) continue;  // warps from `half` on had no tile
-                dd_sync_consumers();
-                if (warp >= half && warp < 2 * half) {
-                    float* dst = merge + (warp - half) * (kDdMergeWords * 32) + lane;
+                float f1[2], f2[2];
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) dst[x * 32] = o[x >> 2][x & 3];
+                for (int part = 0; part < 2; ++part) {  // half of O at a time
+                    dd_sync_consumers();
+                    if (warp >= half && warp < 2 * half) {
+                        float* dst = merge + (warp - half) * (kDdMergeWords * 32) + lane;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        dst[(64 + e) * 32] = mrun[e];
-                        dst[(66 + e) * 32] = lrun[e];
+                        for (int x = 0; x < 32; ++x) dst[x * 32] = o[8 * part + (x >> 2)][x & 3];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            dst[(32 + e) * 32] = mrun[e];
+                            dst[(34 + e) * 32] = lrun[e];
+                        }
                     }
-                }
-                dd_sync_consumers();
-                if (warp < half) {
-                    const float* src = merge + warp * (kDdMergeWords * 32) + lane;
+                    dd_sync_consumers();
+                    if (warp < half) {
+                        const float* src = merge + warp * (kDdMergeWords * 32) + lane;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float m2 = src[(64 + e) * 32], m = fmaxf(mrun[e], m2);
-                        const float f1 = mrun[e] == -INFINITY ? 0.f : dd_exp2(mrun[e] - m);
-                        const float f2 = m2 == -INFINITY ? 0.f : dd_exp2(m2 - m);
-                        mrun[e] = m;
-                        lrun[e] = lrun[e] * f1 + src[(66 + e) * 32] * f2;
+                        for (int e = 0; e < 2; ++e) {
+                            if (part == 0) {
+                                const float m2 = src[(32 + e) * 32], m = fmaxf(mrun[e], m2);
+                                f1[e] = mrun[e] == -INFINITY ? 0.f : dd_exp2(mrun[e] - m);
+                                f2[e] = m2 == -INFINITY ? 0.f : dd_exp2(m2 - m);
+                                mrun[e] = m;
+                                lrun[e] = lrun[e] * f1[e] + src[(34 + e) * 32] * f2[e];
+                            }
 #pragma unroll
-                        for (int nt = 0; nt < 16; ++nt)
+                            for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                o[nt][2 * e + y] = o[nt][2 * e + y] * f1 + src[(nt * 4 + 2 * e + y) * 32] * f2;
+                                for (int y = 0; y < 2; ++y)
+                                    o[8 * part + nt][2 * e + y] =
+                                        o[8 * part + nt][2 * e + y] * f1[e] + src[(nt * 4 + 2 * e + y) * 32] * f2[e];
+                        }
                     }
                 }
             }
@@ -678,17 +733,17 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 
 // Joins the parts of the sequences that several CTAs walked.  CTA (x, h, z) takes a (sequence, tile), x itself where
 // they are no more than the shares (by_tile: tiles a sequence may have), else the one in which boundary x + 1 of the
-// shares is the first to fall, if any; and four of its (row, head) pairs; four warps share a pair,
-// each a quarter of the parts (their loads all in flight: one warp a pair took 5.5 us for 64 parts), 4 of the 128 values
-// a lane.  The parts' maximum first, then 2^(m_i - m) O_i summed in the parts' order within each warp and the warps'
-// order after that: the same every time.
-constexpr int kDcThreads = 512;
-__global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseArgs a, int grid, int by_tile) {
-    __shared__ float4 sum_o[4][4][32];
-    __shared__ float sum_l[4][4];
+// shares is the first to fall, if any; of its (row, head) pairs every gridDim.z-th.  Four warps share a pair, each a
+// quarter of the parts, eight parts' loads in flight and 4 of the 128 values a lane: a running maximum m and sum of
+// 2^(m_i - m) O_i in the parts' order within a warp, then over the warps: the same every time.  What bounds it is the
+// chain of dependent loads (metadata, parts), so everything that can go out together does.
+constexpr int kDcThreads = 128;
+__global__ void __launch_bounds__(kDcThreads, 8) dense_combine_kernel(const DenseArgs a, int grid, int by_tile) {
+    __shared__ float4 sum_o[4][32];
+    __shared__ float2 sum_ml[4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
-    const int pair = blockIdx.z * 4 + (warp >> 2), quarter = warp & 3;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the shares' CTAs found wrong
         uint32_t e = 0;
         for (int c = lane; c < grid; c += 32) e |= a.err_slots[c];
@@ -698,19 +753,12 @@ __global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseAr
             else if (e) atomicOr(a.err, e);
         }
     }
-    const int64_t total = a.unit_prefix[a.num_seqs];
-    const int shares = dd_shares(static_cast<int>(total), grid);
-    if (shares == 0) return;
-    int c = 0, lo, mt, start;  // first share of the parts, sequence, tile; first unit of that share
-    if (by_tile > 0) {
-        lo = blockIdx.x / by_tile;
-        mt = blockIdx.x - lo * by_tile;
-        if (a.unit_prefix[lo + 1] == a.unit_prefix[lo]) return;
-    } else {
-        c = blockIdx.x;  // boundary between shares c and c + 1
-        if (c + 1 >= shares) return;
-        const int cut = static_cast<int>(total * (c + 1) / shares);
-        lo = 0;
+    const int total = a.unit_prefix[a.num_seqs];
+    const int shares = dd_shares(total, grid);
+    int lo = by_tile > 0 ? blockIdx.x / by_tile : 0, mt = by_tile > 0 ? blockIdx.x % by_tile : 0;  // sequence, tile
+    if (by_tile == 0) {
+        if (static_cast<int>(blockIdx.x) + 1 >= shares) return;
+        const int cut = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / shares);
         int hi = a.num_seqs;  // largest b with prefix[b] <= cut
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -718,74 +766,88 @@ __global__ void __launch_bounds__(kDcThreads) dense_combine_kernel(const DenseAr
         }
         mt = (cut - a.unit_prefix[lo]) / dd_blocks(a.cache_lens[lo]);
     }
+    const int begin = a.unit_prefix[lo], units = a.unit_prefix[lo + 1] - begin;
     const DdSeq s = dd_seq(a, lo);
-    if (mt >= s.tiles) return;
-    const int seg0 = a.unit_prefix[lo] + mt * s.blocks, seg1 = seg0 + s.blocks;
+    if (units == 0 || mt >= s.tiles) return;
+    const int seg0 = begin + mt * s.blocks, seg1 = seg0 + s.blocks;
     // the shares that hold its first and last units: the largest c with total c / shares <= unit
     const int first = static_cast<int>((static_cast<int64_t>(seg0 + 1) * shares - 1) / total);
     const int last = static_cast<int>((static_cast<int64_t>(seg1) * shares - 1) / total);
     // one share wrote it whole; the boundary lies between two tiles, or an earlier one inside the tile has its CTA
-    if (first == last || (by_tile == 0 && first != c)) return;
-    c = first;
-    start = static_cast<int>(total * c / shares);
-    const int count = last - c + 1;
-    if (static_cast<int>(blockIdx.z) * 4 >= min(16, s.n * a.G - 16 * mt)) return;
-    const bool live = pair < min(16, s.n * a.G - 16 * mt);
-    // share c's part is its second one unless the share began with it; the others' are the first of their shares
-    const int slot0 = 2 * c + (start < seg0 ? 1 : 0);
-    auto row_of = [&](int i) { return (static_cast<int64_t>(i == 0 ? slot0 : 2 * (c + i)) * a.H + h) * 16 + (live ? pair : 0); };
-    float m = -INFINITY;
-    for (int i = lane; i < count; i += 32) m = fmaxf(m, a.part_ml[row_of(i) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int i_begin = count * quarter / 4, i_end = count * (quarter + 1) / 4;
-    float l = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = i_begin; i0 < i_end; i0 += 8) {  // eight parts' loads in flight
-        float4 v[8];
-        float2 ml[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int64_t at = row_of(min(i0 + u, i_end - 1));
-            ml[u] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-            v[u] = *reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + 4 * lane);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (i0 + u >= i_end) break;
-            const float w = ml[u].x == -INFINITY ? (ml[u].y == ml[u].y ? 0.f : ml[u].y) : dd_exp2(ml[u].x - m);
+    if (first == last || (by_tile == 0 && first != static_cast<int>(blockIdx.x))) return;
+    const int count = last - first + 1;
+    // the first share's part is its second one unless the share began with it; the others' are the first of their shares
+    const int slot0 = 2 * first + (static_cast<int>(static_cast<int64_t>(total) * first / shares) < seg0 ? 1 : 0);
+    const int i_begin = count * warp / 4, i_end = count * (warp + 1) / 4;
+    const int pairs = min(16, s.n * a.G - 16 * mt);
+    for (int pair = blockIdx.z; pair < pairs; pair += gridDim.z) {
+        float m = -INFINITY, l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
+        auto weight = [](float2 ml, float top) {
+            return ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : dd_exp2(ml.x - top);
+        };
+        auto add = [&](float w, float2 ml, float4 v) {
             if (w != 0.f) {
-                l = fmaf(w, ml[u].y, l);
-                x.x = fmaf(w, v[u].x, x.x);
-                x.y = fmaf(w, v[u].y, x.y);
-                x.z = fmaf(w, v[u].z, x.z);
-                x.w = fmaf(w, v[u].w, x.w);
+                l = fmaf(w, ml.y, l);
+                x.x = fmaf(w, v.x, x.x);
+                x.y = fmaf(w, v.y, x.y);
+                x.z = fmaf(w, v.z, x.z);
+                x.w = fmaf(w, v.w, x.w);
             }
-        }
-    }
-    sum_o[warp >> 2][quarter][lane] = x;
-    if (lane == 0) sum_l[warp >> 2][quarter] = l;
-    __syncthreads();
-    if (quarter != 0 || !live) return;
+        };
+        auto raise = [&](float top) {
+            const float f = m == -INFINITY ? 0.f : dd_exp2(m - top);
+            if (m != -INFINITY) {
+                l *= f;
+                x = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+            }
+            m = top;
+        };
+        for (int i0 = i_begin; i0 < i_end; i0 += 8) {
+            float4 v[8];
+            float2 ml[8];
 #pragma unroll
-    for (int q = 1; q < 4; ++q) {
-        const float4 y = sum_o[warp >> 2][q][lane];
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
-        l += sum_l[warp >> 2][q];
+            for (int u = 0; u < 8; ++u) {
+                const int i = min(i0 + u, i_end - 1);
+                const int64_t at = (static_cast<int64_t>(i == 0 ? slot0 : 2 * (first + i)) * a.H + h) * 16 + pair;
+                ml[u] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+                v[u] = *reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + 4 * lane);
+            }
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top = fmaxf(top, ml[u].x);
+            raise(top);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i0 + u < i_end) add(weight(ml[u], m), ml[u], v[u]);
+        }
+        sum_o[warp][lane] = x;
+        if (lane == 0) sum_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp == 0) {
+            float top = m;
+#pragma unroll
+            for (int q = 1; q < 4; ++q) top = fmaxf(top, sum_ml[q].x);
+            raise(top);
+#pragma unroll
+            for (int q = 1; q < 4; ++q) {
+                const float2 ml = sum_ml[q];
+                add(weight(ml, m), ml, sum_o[q][lane]);
+            }
+            const float inv = 1.f / l;
+            dd_store2(a, s, h, 16 * mt + pair, 4 * lane, x.x * inv, x.y * inv);
+            dd_store2(a, s, h, 16 * mt + pair, 4 * lane + 2, x.z * inv, x.w * inv);
+        }
+        __syncthreads();
     }
-    const float inv = 1.f / l;
-    dd_store2(a, s, h, 16 * mt + pair, 4 * lane, x.x * inv, x.y * inv);
-    dd_store2(a, s, h, 16 * mt + pair, 4 * lane + 2, x.z * inv, x.w * inv);
 }
 
 template <int H, bool kInt8, int kParts>
 static cudaError_t launch_dense_decode(const DenseArgs& a, int grid, cudaStream_t stream) {
     using Cfg = DdCfg<kInt8>;
     const size_t smem = 1024 + static_cast<size_t>(Cfg::kStages) * Cfg::kStageBytes + Cfg::kMergeBytes +
-                        static_cast<size_t>(a.num_seqs + 1) * sizeof(int32_t);
+                        kDdPrefix * sizeof(int32_t);
     auto* kernel = dense_decode_kernel<H, kInt8, kParts>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
@@ -800,11 +862,11 @@ static cudaError_t launch_dense_decode(const DenseArgs& a, int grid, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, *a.k_map, *a.v_map, a)) != cudaSuccess) return e;
-    // tiles or boundaries, heads, groups of four (row, head) pairs
-    const int tiles = (a.pairs_most + 15) / 16;
+    // tiles or boundaries, heads, (row, head) pairs
+    const int tiles = (a.pairs_most + 15) / 16, pairs = std::min(16, a.pairs_most);
     const int by_tile = a.num_seqs * tiles <= grid ? tiles : 0;
     cfg.gridDim = dim3(static_cast<unsigned>(by_tile > 0 ? a.num_seqs * tiles : grid), static_cast<unsigned>(a.H),
-                       (std::min(16, a.pairs_most) + 3) / 4);
+                       by_tile > 0 ? pairs : (pairs + 3) / 4);
     cfg.blockDim = dim3(kDcThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, dense_combine_kernel, a, grid, by_tile);
