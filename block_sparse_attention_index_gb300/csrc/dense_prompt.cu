@@ -28,12 +28,18 @@
 // Drafted windows (kAlt): one M tile, and the two stages take alternate key tiles, each with its own running state.
 // When tiles alone leave SMs idle the key range is split as well; the parts are joined by dense_join_kernel.
 //
-// int8 caches are read from a copy widened once per call (run_widen_kv), scales beside it: the key scale multiplies
-// the score, the value scale the weight.
+// int8 caches are read from a copy widened once per call.  bf16 outputs: f16 values with the scales in them, over a
+// power of two for each 64-position block (run_widen_f16), queries as f16 times a power of two for each row (converted
+// in shared memory by the softmax threads; bf16's 8 bits fit, what lies 2^-22 below the row's largest loses some) and
+// weights as one f16 (2^-12), at most 2^14: the blocks' powers of two are two scalars each for the softmax, where the
+// scales themselves, one for each key, were a third of its instructions (784 us for 2,048 rows at 8,192).  fp32 outputs:
+// bf16 integers, exact, scales beside them (run_widen_kv); the key scale multiplies the score, the value scale the weight.
 //
 // Values that no row of the tile may see: positions past the length are zeroed in the last value tile (warp 10), so
 // stale cache rows do not matter.  A later token of the same chunk meets weights of zero; if its value is not finite
 // the product is NaN, so a row whose result is not finite is computed again key by key (dp_row_again).
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -46,16 +52,19 @@ constexpr int kDpQBytes = 128 * kHeadDim * 2;
 constexpr int kDpScaleSlots = 4;
 constexpr float kDpSlack = 8.f;  // log2 by which the running maximum may lag
 
-template <int kParts, bool kWide>
+enum DpForm { kDpBf16 = 0, kDpInt = 1, kDpF16 = 2 };  // bf16 caches; int8: bf16 integers with scales; int8: f16 copy
+
+template <int kParts, int kForm>
 struct DpCfg {
     static constexpr int NK = kParts == 1 ? 128 : 64;
     static constexpr int kTile = NK * kHeadDim * 2;  // bytes of a K or V tile
-    static constexpr int kStages = (kWide ? 4 : 5) * (128 / NK);
+    static constexpr int kStages = (kForm == kDpInt ? 4 : 5) * (128 / NK);
 };
 
-template <int kParts, bool kWide>
+template <int kParts, int kForm>
 struct __align__(1024) DpSmem {
-    using Cfg = DpCfg<kParts, kWide>;
+    using Cfg = DpCfg<kParts, kForm>;
+    static constexpr bool kWide = kForm == kDpInt;
     uint8_t q[2][kDpQBytes];
     uint8_t ring[Cfg::kStages][Cfg::kTile];
     float sc[kWide ? kDpScaleSlots : 1][2][kWide ? 128 : 4];  // key and value scales of a tile
@@ -64,16 +73,25 @@ struct __align__(1024) DpSmem {
     // phases would belong to either, and a wait that skipped one could not tell by parity that it had).
     uint64_t full[2][Cfg::kStages], empty[Cfg::kStages];
     uint64_t sc_full[kDpScaleSlots], sc_empty[kDpScaleSlots];
-    uint64_t q_full, v_last;
+    uint64_t q_full, q_turned[2], v_last;  // q_turned: a stage's queries converted (f16 form)
     uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
     uint32_t tmem;
     int32_t scan[kDpThreads / 32];
     int32_t found[4];
     float2 other_ml[128];  // drafted windows: maxima and sums of the second stream
 };
-static_assert(sizeof(DpSmem<1, false>) + 1024 <= 227 * 1024, "prompt attention exceeds 227 KB of shared memory");
-static_assert(sizeof(DpSmem<1, true>) + 1024 <= 227 * 1024, "prompt attention (int8) exceeds 227 KB of shared memory");
-static_assert(sizeof(DpSmem<3, false>) + 1024 <= 227 * 1024, "prompt attention (fp32) exceeds 227 KB of shared memory");
+static_assert(sizeof(DpSmem<1, kDpBf16>) + 1024 <= 227 * 1024, "prompt attention exceeds 227 KB of shared memory");
+static_assert(sizeof(DpSmem<1, kDpF16>) + 1024 <= 227 * 1024, "prompt attention (f16 copy) exceeds 227 KB of shared memory");
+static_assert(sizeof(DpSmem<3, kDpInt>) + 1024 <= 227 * 1024, "prompt attention (int8, fp32) exceeds 227 KB of shared memory");
+static_assert(sizeof(DpSmem<3, kDpBf16>) + 1024 <= 227 * 1024, "prompt attention (fp32) exceeds 227 KB of shared memory");
+
+constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major) {  // as idesc_bf16_f32, f16 operands
+    return idesc_bf16_f32(M, N, 0, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+__device__ __forceinline__ uint32_t dp_pack_f16(float lo, float hi) {
+    __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&r);
+}
 
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void dp_mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
@@ -247,8 +265,15 @@ __device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int6
         float x = -INFINITY;
         int64_t row = 0;
         if (t < end) {
-            row = block_row(a.cache, b, t & ~(kBlock - 1));
+            row = block_row(a.seq_cache, b, t & ~(kBlock - 1));
             row = row < 0 ? 0 : (row + (t & (kBlock - 1))) * a.H + h;
+            if (a.kv_int8) {
+                float acc = 0.f;
+                for (int i = 0; i < kHeadDim; ++i)
+                    acc = fmaf(static_cast<float>(static_cast<const int8_t*>(a.k)[row * kHeadDim + i]),
+                               __uint_as_float(static_cast<uint32_t>(a.q[q_row * kHeadDim + i]) << 16), acc);
+                x = acc * a.seq_k_scale[row] * a.scale_log2;
+            } else {
             const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + row * kHeadDim);
             const uint4* q = reinterpret_cast<const uint4*>(a.q + q_row * kHeadDim);
             float acc = 0.f;
@@ -259,6 +284,7 @@ __device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int6
                        bf16_lo(kv.w) * bf16_lo(qv.w) + bf16_hi(kv.w) * bf16_hi(qv.w);
             }
             x = acc * a.scale_log2;
+            }
         }
         float top = x;
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -270,25 +296,37 @@ __device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int6
         for (int i = 0; i < 32 && u0 + i < end; ++i) {
             const float pi = __shfl_sync(0xffffffffu, p, i);
             const int64_t ri = __shfl_sync(0xffffffffu, row, i);
-            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + ri * kHeadDim + 4 * lane);
+            float v[4];
+            if (a.kv_int8) {
+                const char4 v8 = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.v) + ri * kHeadDim + 4 * lane);
+                const float f8 = a.seq_v_scale[ri];
+                v[0] = v8.x * f8;
+                v[1] = v8.y * f8;
+                v[2] = v8.z * f8;
+                v[3] = v8.w * f8;
+            } else {
+                const uint2 vw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + ri * kHeadDim + 4 * lane);
+                v[0] = bf16_lo(vw.x);
+                v[1] = bf16_hi(vw.x);
+                v[2] = bf16_lo(vw.y);
+                v[3] = bf16_hi(vw.y);
+            }
             l += pi;
-            o[0] = fmaf(pi, bf16_lo(v.x), o[0]);
-            o[1] = fmaf(pi, bf16_hi(v.x), o[1]);
-            o[2] = fmaf(pi, bf16_lo(v.y), o[2]);
-            o[3] = fmaf(pi, bf16_hi(v.y), o[3]);
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(pi, v[e], o[e]);
         }
     }
 }
 
-template <int kParts, bool kWide, bool kAlt>
+template <int kParts, int kForm, bool kAlt>
 __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                     const __grid_constant__ CUtensorMap k_map,
                                                                     const __grid_constant__ CUtensorMap v_map,
                                                                     const DenseArgs a, int nsplit) {
-    using Cfg = DpCfg<kParts, kWide>;
+    constexpr bool kWide = kForm == kDpInt, kF16 = kForm == kDpF16;
+    using Cfg = DpCfg<kParts, kForm>;
     constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2;
     extern __shared__ uint8_t smem_raw[];
-    using Smem = DpSmem<kParts, kWide>;
+    using Smem = DpSmem<kParts, kForm>;
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.H, split = blockIdx.x / a.H % nsplit, index = blockIdx.x / (a.H * nsplit);
@@ -309,6 +347,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.v_last, 1);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.q_turned[s], 4);
             mbar_init(&sm.s_full[s], 1);
             mbar_init(&sm.p_full[s][0], 4);
             mbar_init(&sm.p_full[s][1], 4);
@@ -426,7 +465,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             // ---------------- matrix instructions of stage s, one thread
             const int s = warp == 9 ? 0 : 1;
             if (lane == 0 && w.count[s] > 0) {
-                constexpr uint32_t idesc_s = idesc_bf16_f32(128, NK, 0, 0), idesc_o = idesc_bf16_f32(128, kHeadDim, 0, 1);
+                constexpr uint32_t idesc_s = kF16 ? idesc_f16_f32(128, NK, 0) : idesc_bf16_f32(128, NK, 0, 0);
+                constexpr uint32_t idesc_o = kF16 ? idesc_f16_f32(128, kHeadDim, 1) : idesc_bf16_f32(128, kHeadDim, 0, 1);
                 const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[kAlt ? 0 : s]), 16, 1024);
                 const uint64_t kd = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
                 const uint64_t vd = smem_desc_sw128(smem_u32(sm.ring[0]), kHalf, 1024);
@@ -447,7 +487,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 };
                 constexpr int kStep = kAlt ? 2 : 1;
                 const int j0 = kAlt ? s : 0, count = w.count[s], others = w.count[s ^ 1];
-                bool ok = mbar_wait(&sm.q_full, 0, a.err) && landed(j0, 0);
+                bool ok = mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, 0, a.err) && landed(j0, 0);
                 const bool issued = ok;
                 tc_fence_after();
                 if (ok) {
@@ -531,6 +571,49 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 (warp % 4)) << 16
         const uint32_t s_addr = tmem + s * 128 + lanes, o_addr = tmem + 256 + s * 128 + lanes;
         const int count = w.count[s];
+        float row_f = a.scale_log2;  // factor from the row's products to the log2 domain
+        bool alive = true;
+        if constexpr (kF16) {
+            // the row's queries to f16: its largest value into [2^8, 2^9)
+            if (count > 0) alive = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, a.err));
+            uint8_t* row = sm.q[s] + m * 128;
+            auto chunk = [&](int c) { return reinterpret_cast<uint4*>(row + (c >> 3) * (kDpQBytes / 2) + (((c & 7) ^ (m & 7)) << 4)); };
+            uint32_t big = 0;  // largest magnitude as bits
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c) {
+                const uint4 v = *chunk(c);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) big = max(big, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+            }
+            const uint32_t ex = min(max(big >> 23, 9u), 253u);
+            const float up = __uint_as_float((262u - ex) << 23);  // 2^(8 - exponent)
+            row_f *= __uint_as_float((ex - 8u) << 23);
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c) {
+                const uint4 v = *chunk(c);
+                *chunk(c) = make_uint4(dp_pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), dp_pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                                       dp_pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), dp_pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_turned[s]);
+        }
+        // f16 form: factors (products, value sums) of the key tile's blocks, loaded a tile ahead; the power of two that
+        // O is kept in units of (not below any value block's so far)
+        const float2* fac = kF16 ? a.wide_fac + (static_cast<int64_t>(h) * a.cache_tokens + a.cache.starts[w.b]) / kBlock : nullptr;
+        float2 fac_now[2], fac_next[2];
+        auto load_fac = [&](int c, float2 (&x)[2]) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int blk = 2 * (w.first + c) + y;
+                x[y] = blk * kBlock < w.L ? fac[blk] : make_float2(0.f, 0.f);
+            }
+        };
+        if constexpr (kF16) load_fac(0, fac_next);
+        float vref = 0.f;
+        bool coarse = false;  // some block's values were 2^-12 or less of another's: small weights may have lost bits
+        constexpr float kLift = kF16 ? 6.f : 0.f;  // f16 weights: at most 2^(6 + 8)
         float top = -INFINITY, sum = 0.f;  // maximum in use (log2 domain), sum of weights
         float acc[kParts > 1 ? kHeadDim : 1];  // fp32 outputs: O of the row
         if constexpr (kParts > 1) {
@@ -549,8 +632,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 }
             }
         };
-        bool alive = true;
-        for (int c = 0; c < count; ++c) {
+        for (int c = 0; alive && c < count; ++c) {
             const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
             alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], c & 1, a.err));
             if (!alive) break;
@@ -559,7 +641,12 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             float x[NK], big[NK / 64];
 #pragma unroll
             for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
-            float f = a.scale_log2;  // x f is the score in the log2 domain
+            float f = row_f;  // x f is the score in the log2 domain (f16 form: times the block's factor)
+            if constexpr (kF16) {
+                fac_now[0] = fac_next[0];
+                fac_now[1] = fac_next[1];
+                if (c + 1 < count) load_fac(c + 1, fac_next);
+            }
             const int e = j % kDpScaleSlots;
             if constexpr (kWide) {
                 alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], (j / kDpScaleSlots) & 1, a.err));
@@ -579,27 +666,40 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
             if (edge) {
                 const int seen = pos + 1 - t0;
+                if constexpr (kF16) {
 #pragma unroll
-                for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * f : -INFINITY;
+                    for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * (f * fac_now[k >> 6].x) : -INFINITY;
+                    fac_now[0].x = fac_now[1].x = 1.f;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * f : -INFINITY;
+                }
                 f = 1.f;
             }
-            float now = NK == 128 ? fmaxf(big[0], big[NK / 64 - 1]) : big[0];
+            float now;
             if (kWide || edge) {  // the scores are not those that the load took the maximum of
                 float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < NK; k += 8)
 #pragma unroll
                     for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], fmaxf(x[k + z], x[k + 4 + z]));
-                now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * f;
+            } else if constexpr (kF16) {
+                now = fmaxf(big[0] * fac_now[0].x, big[NK / 64 - 1] * fac_now[1].x) * f;
+            } else {
+                now = (NK == 128 ? fmaxf(big[0], big[NK / 64 - 1]) : big[0]) * f;
             }
-            now *= f;
+            float vnew = vref;
+            if constexpr (kF16) vnew = fmaxf(vref, fmaxf(fac_now[0].y, fac_now[1].y));  // the same for every row
             if (c == 0) {
                 top = now;
-            } else if (__any_sync(0xffffffffu, now > top + kDpSlack)) {
+            } else if (__any_sync(0xffffffffu, now > top + kDpSlack) || (kF16 && vnew > vref)) {
                 // the maximum grew: the warp's rows of O in tensor memory (no product runs on it now: S of this tile
                 // was computed after the last one) and their sums move to the new one
                 const float next = now > top + kDpSlack ? now : top;
                 const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
+                const float ro = kF16 ? r * (vref / vnew) : r;  // (vnew > 0: every block's is)
+                if constexpr (kF16) coarse |= vref < vnew * 2.4414063e-4f;
                 if constexpr (kParts > 1) {
 #pragma unroll
                     for (int k = 0; k < kHeadDim; ++k) acc[k] *= r;
@@ -610,18 +710,33 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         dp_ld32(o_addr + 32 * q, y);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] *= r;
+                        for (int k = 0; k < 32; ++k) y[k] *= ro;
                         dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
                     }
                 }
                 sum *= r;
                 top = next;
             }
+            if constexpr (kF16) vref = vnew;
             const float base = top == -INFINITY ? 0.f : top;
-            const float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+            float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+            float back[2] = {1.f, 1.f};  // f16 form: from a block's weights, in units of its values, to plain ones
             float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int h2 = 0; h2 < NK / 64; ++h2) {  // 64 keys at a time: the products with them start while the next are made
+                float unit = 1.f;  // f16 form: the block's value factor over vref
+                bool folded = true;
+                if constexpr (kF16) {
+                    // weight 2^(x - base + 6) times `unit`, a power of two: an exponent's addition, and taken out of the
+                    // sum again, unless it is too small for that (a block of tiny scales; the same for the whole CTA)
+                    if (fac_now[h2].y > 0.f) unit = fac_now[h2].y / vref;
+                    folded = unit >= 8.6736174e-19f;  // 2^-60
+                    coarse |= unit < 2.4414063e-4f;   // 2^-12
+                    const float up = kLift + (folded ? static_cast<float>(static_cast<int>(__float_as_uint(unit) >> 23) - 127) : 0.f);
+                    ff = make_float2(f * fac_now[h2].x, f * fac_now[h2].x);
+                    nb = make_float2(up - base, up - base);
+                    back[h2] = folded ? 1.f / unit : 1.f;
+                }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     float* z = x + 64 * h2 + 32 * q;
@@ -630,7 +745,11 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         const float2 y = __ffma2_rn(make_float2(z[2 * k], z[2 * k + 1]), ff, nb);
                         z[2 * k] = dp_exp2(y.x);
                         z[2 * k + 1] = dp_exp2(y.y);
-                        add[k & 1] = __fadd2_rn(add[k & 1], make_float2(z[2 * k], z[2 * k + 1]));
+                        add[kF16 ? h2 : k & 1] = __fadd2_rn(add[kF16 ? h2 : k & 1], make_float2(z[2 * k], z[2 * k + 1]));
+                    }
+                    if (kF16 && !folded) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) z[k] *= unit;
                     }
                     if constexpr (kWide) {
 #pragma unroll
@@ -648,7 +767,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         uint32_t pk[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            pk[k] = pack_bf16x2(z[2 * k], z[2 * k + 1]);
+                            pk[k] = kF16 ? dp_pack_f16(z[2 * k], z[2 * k + 1]) : pack_bf16x2(z[2 * k], z[2 * k + 1]);
                             if (part + 1 < kParts) {
                                 z[2 * k] -= bf16_lo(pk[k]);
                                 z[2 * k + 1] -= bf16_hi(pk[k]);
@@ -662,7 +781,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full[s][h2]);
             }
-            sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
+            sum += (add[0].x + add[0].y) * back[0] + (add[1].x + add[1].y) * back[1];
             if constexpr (kWide) {
                 if (lane == 0) mbar_arrive(&sm.sc_empty[e]);  // (after the warp's last barrier: every lane has read them)
             }
@@ -712,8 +831,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             const int64_t q_row = (static_cast<int64_t>(w.c0 + min(i, w.n - 1)) * a.H + h) * a.G + g;
             const int64_t part_row = ((static_cast<int64_t>(index) * a.H + h) * nsplit + split) * kRows + s * 128 + m;
             const bool split_up = nsplit > 1;
+            float most = 0.f;  // f16 form: the row's largest value, in units of w x V16
             bool spoiled = kAlt && !(fabsf(sum) < INFINITY);  // a product with a value past the row's position that is not finite
-            const float inv = 1.f / sum;
+            const float inv = kF16 ? vref / sum : 1.f / sum;  // (parts: O in plain units, as their join expects)
             if (have) {
 #pragma unroll(kParts > 1 ? 4 : 1)
                 for (int q = 0; q < kHeadDim / 32; ++q) {
@@ -725,7 +845,13 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                             for (int k = 0; k < 32; ++k) y[k] = y[k] * f0 + other[(32 * q + k) * 128 + m] * f1;
                     }
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) spoiled |= !(fabsf(y[k]) < INFINITY);
+                    for (int k = 0; k < 32; ++k) {
+                        spoiled |= !(fabsf(y[k]) < INFINITY);
+                        if constexpr (kF16) most = fmaxf(most, fabsf(y[k]));
+                    }
+                    if (kF16 && split_up)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) y[k] *= vref;
                     if (!mine) {
                         // (a row of the tile that no query has)
                     } else if (split_up) {
@@ -750,7 +876,11 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 }
             }
             if (split_up && mine) *reinterpret_cast<float2*>(a.part_ml + part_row * 2) = make_float2(top, sum);
-            if constexpr (!kWide) {
+            // f16 form: a row that lives on blocks whose values are tiny beside another block's (even one that it does
+            // not see) has small weights there, off by up to 2^-25 each, L^1/2 2^-12 in units where it has 2^10 or more
+            // when nothing was lost
+            if (kF16 && coarse && most < 1024.f) spoiled = true;
+            if constexpr (!kWide) {  // (bf16 integers are finite, and a hidden key's weight ignores its scale)
                 uint32_t again = __ballot_sync(0xffffffffu, mine && spoiled && have);
                 const int end = min(pos + 1, (w.first + (kAlt ? w.total : count)) * NK);
                 while (again) {  // these rows once more, by the whole warp
@@ -760,9 +890,11 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     float y[4], m2, l2;
                     dp_row_again(a, w.b, h, qr, w.first * NK, __shfl_sync(0xffffffffu, end, from), y, m2, l2);
                     const float f = split_up ? 1.f : 1.f / l2;
-                    if (split_up) {
-                        *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
-                        if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m2, l2);
+                    if (split_up) {  // (in the units of the other parts' sums)
+                        constexpr float kUnits = kF16 ? 64.f : 1.f;
+                        *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + 4 * lane) =
+                            make_float4(y[0] * kUnits, y[1] * kUnits, y[2] * kUnits, y[3] * kUnits);
+                        if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m2, l2 * kUnits);
                     } else if (a.out_bf16) {
                         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qr * kHeadDim + 4 * lane) =
                             make_uint2(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f));
@@ -836,10 +968,10 @@ __global__ void __launch_bounds__(kDjThreads) dense_join_kernel(const DenseArgs 
     }
 }
 
-template <int kParts, bool kWide, bool kAlt>
+template <int kParts, int kForm, bool kAlt>
 static cudaError_t launch_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
-    auto* kernel = dense_prompt_kernel<kParts, kWide, kAlt>;
-    const size_t smem = sizeof(DpSmem<kParts, kWide>) + 1024;
+    auto* kernel = dense_prompt_kernel<kParts, kForm, kAlt>;
+    const size_t smem = sizeof(DpSmem<kParts, kForm>) + 1024;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(items) * a.H * nsplit, kDpThreads, smem, stream>>>(*a.q_map, *a.k_map, *a.v_map, a, nsplit);
@@ -850,15 +982,15 @@ static cudaError_t launch_dense_prompt(const DenseArgs& a, int items, int nsplit
 
 cudaError_t run_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
     if (a.kv_int8)
-        return a.out_bf16 ? launch_dense_prompt<1, true, false>(a, items, nsplit, stream)
-                          : launch_dense_prompt<3, true, false>(a, items, nsplit, stream);
-    return a.out_bf16 ? launch_dense_prompt<1, false, false>(a, items, nsplit, stream)
-                      : launch_dense_prompt<3, false, false>(a, items, nsplit, stream);
+        return a.out_bf16 ? launch_dense_prompt<1, kDpF16, false>(a, items, nsplit, stream)
+                          : launch_dense_prompt<3, kDpInt, false>(a, items, nsplit, stream);
+    return a.out_bf16 ? launch_dense_prompt<1, kDpBf16, false>(a, items, nsplit, stream)
+                      : launch_dense_prompt<3, kDpBf16, false>(a, items, nsplit, stream);
 }
 
 cudaError_t run_dense_window(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
-    return a.out_bf16 ? launch_dense_prompt<1, false, true>(a, items, nsplit, stream)
-                      : launch_dense_prompt<3, false, true>(a, items, nsplit, stream);
+    return a.out_bf16 ? launch_dense_prompt<1, kDpBf16, true>(a, items, nsplit, stream)
+                      : launch_dense_prompt<3, kDpBf16, true>(a, items, nsplit, stream);
 }
 
 }  // namespace msa

@@ -175,6 +175,7 @@ struct WidenArgs {
     uint32_t* err;
 };
 cudaError_t run_widen_kv(const WidenArgs& a, cudaStream_t stream);
+cudaError_t run_widen_f16(const WidenArgs& a, float2* fac, cudaStream_t stream);
 
 // Cache writer: the new rows of a call, rotated and stored (msa_append, msa_rope of the ABI).
 struct AppendArgs {
@@ -217,6 +218,9 @@ struct DenseArgs {
     const CUtensorMap* v_map;
     CacheRows seq_cache;       // the caches as the problem gives them (cache: the widened copy for int8 prompts)
     int64_t seq_cache_tokens;
+    const float* seq_k_scale;  // int8 caches: the problem's scales
+    const float* seq_v_scale;
+    const float2* wide_fac;    // int8 prompts, bf16 outputs: factors of the f16 copy's blocks, [H, cache_tokens / 64]
     int pairs_most;        // decode family: most (row, head) pairs of a sequence that its kernel takes
     int32_t* unit_prefix;  // [num_seqs + 1] decode family: units before each sequence
     float* part_o;         // parts of what several CTAs walk: O [.., 128], decode family [2 shares, H, 16]

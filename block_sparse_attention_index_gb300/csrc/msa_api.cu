@@ -978,8 +978,8 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.k = k_cache;
     a.v = v_cache;
     a.kv_int8 = p->kv_dtype == MSA_KV_INT8;
-    a.k_scale = a.kv_int8 ? p->k_scale : nullptr;
-    a.v_scale = a.kv_int8 ? p->v_scale : nullptr;
+    a.k_scale = a.seq_k_scale = a.kv_int8 ? p->k_scale : nullptr;
+    a.v_scale = a.seq_v_scale = a.kv_int8 ? p->v_scale : nullptr;
     a.out = out;
     a.out_bf16 = p->out_dtype == MSA_OUT_BF16;
     a.cu_rows = p->cu_rows;
@@ -1045,9 +1045,12 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
         a.cache_tokens = static_cast<int64_t>(T);
         a.k_scale = wa.ksw;
         a.v_scale = wa.vsw;
+        float2* fac = reinterpret_cast<float2*>(wa.ksw);  // (the f16 copy has its scales in it)
+        a.wide_fac = fac;
         for (int64_t first = 0; first < d.wide_total; first += d.wide_slots) {
             wa.first_slot = static_cast<int>(first);
-            if ((e = msa::run_widen_kv(wa, st)) != cudaSuccess) return cuda_fail(e, "key/value widening launch");
+            e = a.out_bf16 ? msa::run_widen_f16(wa, fac, st) : msa::run_widen_kv(wa, st);
+            if (e != cudaSuccess) return cuda_fail(e, "key/value widening launch");
             if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), d.prompt_split, st)) != cudaSuccess)
                 return cuda_fail(e, "dense prompt attention launch");
         }

@@ -20,6 +20,8 @@
 // keeps 0 x value out of the P V products.  Row starts per sequence go to
 // `wide_starts` (0 for a sequence that is not widened, -1 for one past the
 // slots the workspace holds, which the attention then rejects, or for one that another pass widens).
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -38,9 +40,9 @@ __device__ __forceinline__ uint2 widen_i8x4(uint32_t w) {
     return make_uint2(pack_bf16x2(i8_at(w, 0), i8_at(w, 1)), pack_bf16x2(i8_at(w, 2), i8_at(w, 3)));
 }
 
-__global__ void __launch_bounds__(kWidenThreads) widen_kv_kernel(const WidenArgs a) {
-    extern __shared__ int32_t slot_of[];  // [num_seqs]: slot of sequence b, or -1 (not widened)
-    __shared__ int32_t warp_tot[kWidenThreads / 32];
+// slot_of[b]: the slot of sequence b in this pass, or negative (-1 not widened, -2 past every pass's slots, -3 another
+// pass widens it); CTA 0 writes the row starts.  The whole block calls it.
+__device__ void widen_slots(const WidenArgs& a, int32_t* slot_of, int32_t* warp_tot) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = a.num_seqs;
 
@@ -77,6 +79,13 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kv_kernel(const WidenArgs
             if (s == -2) atomicOr(a.err, kErrBadMetadata);
         }
     }
+}
+
+__global__ void __launch_bounds__(kWidenThreads) widen_kv_kernel(const WidenArgs a) {
+    extern __shared__ int32_t slot_of[];  // [num_seqs]: slot of sequence b, or -1 (not widened)
+    __shared__ int32_t warp_tot[kWidenThreads / 32];
+    const int tid = threadIdx.x, B = a.num_seqs;
+    widen_slots(a, slot_of, warp_tot);
 
     // ---- units: (sequence, 16 positions), all heads, K and V; a block's positions past L_b are
     // written as zeros, so the units run to the end of the last block
@@ -135,6 +144,96 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kv_kernel(const WidenArgs
             a.vsw[o] = live ? a.v_scale[src * H + c] : 0.f;
         }
     }
+}
+
+// The same for outputs of 16 bits in the dense attention: f16 values with the scales in them, over a power of two for
+// each 64-position block and head (so that nothing overflows and the block's values keep f16's 11 bits; a key is
+// then off by 2^-12 of itself at random, about a tenth of what the output's own rounding is).  fac[h][block] = (the
+// power of two to multiply key products by, the one to multiply the value sums by).  CTA: a block, all heads.
+__global__ void __launch_bounds__(kWidenThreads) widen_f16_kernel(const WidenArgs a, float2* fac) {
+    extern __shared__ int32_t slot_of[];  // [num_seqs]
+    __shared__ int32_t warp_tot[kWidenThreads / 32];
+    __shared__ float scale[2][kBlock * 8];  // key and value scales of the block, [position][head]
+    __shared__ float top[2][8];             // their powers of two
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.num_seqs, H = a.H;
+    widen_slots(a, slot_of, warp_tot);
+    const int blocks = a.slot_rows / kBlock;
+    const int64_t wide_blocks = static_cast<int64_t>(a.max_slots) * blocks;
+    const int row_chunks = H * (kHeadDim / 16), chunks = kBlock * row_chunks;
+    for (int64_t u = blockIdx.x; u < static_cast<int64_t>(B) * blocks; u += gridDim.x) {
+        const int b = static_cast<int>(u / blocks), blk = static_cast<int>(u - static_cast<int64_t>(b) * blocks);
+        const int slot = slot_of[b];
+        if (slot < 0) continue;
+        const int L = a.cache_lens[b], t0 = blk * kBlock;
+        if (L < 1 || L > a.max_cache_len || t0 >= L) continue;  // the attention rejects such a sequence
+        const int64_t src = seq_rows_ok(a.cache, b, L, a.cache_tokens) ? block_row(a.cache, b, t0) : -1;
+        if (src < 0 && tid == 0) atomicOr(a.err, kErrBadMetadata);  // the block is written as zeros
+        const int live = src < 0 ? 0 : min(kBlock, L - t0);
+        __syncthreads();  // the last block's scales are done with
+        for (int c = tid; c < kBlock * H; c += kWidenThreads) {
+            scale[0][c] = c < live * H ? a.k_scale[src * H + c] : 0.f;
+            scale[1][c] = c < live * H ? a.v_scale[src * H + c] : 0.f;
+        }
+        __syncthreads();
+        for (int c = warp; c < 2 * H; c += kWidenThreads / 32) {  // a warp a (kind, head): the largest finite scale
+            const int kind = c / H, h = c - kind * H;
+            float m = 0.f;
+            for (int pos = lane; pos < kBlock; pos += 32) {
+                const float x = fabsf(scale[kind][pos * H + h]);
+                if (x < INFINITY) m = fmaxf(m, x);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            // the next power of two, in [2^-110, 2^127]: 256 / it and it / 256 are normal numbers
+            const uint32_t bits = (__float_as_uint(m) + 0x007FFFFFu) & 0x7F800000u;
+            if (lane == 0) top[kind][h] = __uint_as_float(min(max(bits, 17u << 23), 0x7F000000u));
+        }
+        __syncthreads();
+        const int64_t dst = (static_cast<int64_t>(slot) * blocks + blk) * kBlock;
+        if (tid < H) fac[tid * wide_blocks + dst / kBlock] = make_float2(top[0][tid] / 256.f, top[1][tid] / 256.f);
+        const uint8_t* in[2] = {a.k8 + src * H * kHeadDim, a.v8 + src * H * kHeadDim};
+        uint16_t* out[2] = {a.kw + dst * H * kHeadDim, a.vw + dst * H * kHeadDim};
+        for (int c0 = tid; c0 < chunks; c0 += kWidenBatch * kWidenThreads) {
+            uint4 x[2][kWidenBatch];  // every load of the batch in flight before a store
+#pragma unroll
+            for (int j = 0; j < kWidenBatch; ++j) {
+                const int c = c0 + j * kWidenThreads;
+#pragma unroll
+                for (int kind = 0; kind < 2; ++kind)
+                    x[kind][j] = c < live * row_chunks ? ld_stream_v4(in[kind] + c * 16) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < kWidenBatch; ++j) {
+                const int c = c0 + j * kWidenThreads;
+                if (c >= chunks) break;
+                const int head = c / (kHeadDim / 16) % H;
+#pragma unroll
+                for (int kind = 0; kind < 2; ++kind) {
+                    const float f = scale[kind][c / (kHeadDim / 16)] * (256.f / top[kind][head]);
+                    const uint32_t w[4] = {x[kind][j].x, x[kind][j].y, x[kind][j].z, x[kind][j].w};
+                    uint32_t y[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const __half2 v = __floats2half2_rn(i8_at(w[i], 2 * e) * f, i8_at(w[i], 2 * e + 1) * f);
+                            y[2 * i + e] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                    uint4* d = reinterpret_cast<uint4*>(out[kind] + static_cast<int64_t>(c) * 16);
+                    d[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                    d[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+            }
+        }
+    }
+}
+
+cudaError_t run_widen_f16(const WidenArgs& a, float2* fac, cudaStream_t stream) {
+    const int64_t units = static_cast<int64_t>(a.num_seqs) * (a.slot_rows / kBlock);
+    const int64_t cap = 4 * static_cast<int64_t>(device_sm_count());
+    const int grid = static_cast<int>(units < cap ? (units > 0 ? units : 1) : cap);
+    widen_f16_kernel<<<grid, kWidenThreads, static_cast<size_t>(a.num_seqs) * sizeof(int32_t), stream>>>(a, fac);
+    return cudaGetLastError();
 }
 
 cudaError_t run_widen_kv(const WidenArgs& a, cudaStream_t stream) {

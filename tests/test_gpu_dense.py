@@ -195,6 +195,42 @@ def test_later_tokens_do_not_reach_earlier_rows(n):
         assert not torch.isfinite(after[at:]).any()
 
 
+@pytest.mark.parametrize("n", [1, 5, 40, 200])
+def test_int8_scales_of_any_size(n):
+    """Scales that differ by 2^-12 from token to token, blocks of zero, tiny and huge scales."""
+    b = Batch([(n, 500), (n, 1000)], 2, 16, True, 64, torch.bfloat16, seed=2)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    b.pb.v_scale.mul_(2.0 ** torch.randint(-12, 1, b.v_scale.shape, generator=g, device="cuda"))
+    b.pb.k_scale.mul_(2.0 ** torch.randint(-6, 1, b.k_scale.shape, generator=g, device="cuda"))
+    for seq in range(2):
+        rows = b.rows_of(seq, torch.arange(500, device="cuda"))
+        b.pb.v_scale[rows[64:128]] = 0
+        b.pb.v_scale[rows[130:200]] *= 2.0 ** -60
+        b.pb.k_scale[rows[256:320]] = 0
+        b.pb.v_scale[rows[320:384], 0] *= 2.0 ** 40
+        b.pb.k_scale[rows[200:250]] *= 2.0 ** -100
+    b.k_scale, b.v_scale = b.pb.k_scale, b.pb.v_scale
+    b.check()
+    b.pb.v_scale.mul_(2.0 ** -100)
+    b.check()
+    b.pb.v_scale.mul_(2.0 ** 100).mul_(2.0 ** 60)
+    b.check()
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_int8_later_tokens_do_not_reach_earlier_rows(n):
+    b = Batch([(n, 200)], 2, 16, True, 0, torch.bfloat16, seed=1)
+    ref, bound = b.ref()
+    at = n - 2
+    row = b.rows_of(0, torch.tensor(200 - n + at)).item()
+    for ks, vs in ((float("nan"), float("nan")), (0.01, float("inf")), (float("inf"), 0.01)):
+        b.pb.k_scale[row], b.pb.v_scale[row] = ks, vs
+        after = b.run()
+        assert ((after[:at].double() - ref[:at]).abs() <= bound[:at]).all()
+        if ks != float("inf"):  # (an infinite key scale makes a score of either sign: weight 0, or a NaN)
+            assert not torch.isfinite(after[at:]).all(-1).any()
+
+
 def test_rows_behind_the_last_sequence_stay():
     for seqs in ([(1, 100), (1, 30)], [(20, 100), (5, 30)], [(4, 100)]):
         b = Batch(seqs, 2, 8, spare_rows=7)
