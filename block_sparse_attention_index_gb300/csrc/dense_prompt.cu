@@ -23,7 +23,7 @@
 // With bf16 outputs a weight enters P V as one bf16 (2^-9 relative, at random, about the output's own rounding); with
 // fp32 outputs as three parts (2^-24), NK = 64 then, so that the parts fit over S.  The tensor cores cut what an
 // addition loses instead of rounding it, a bias of about 2^-25 per addition (1.5e-4 after 33,280 keys, measured), so
-// with fp32 outputs O_s holds one key tile's product only and the softmax group adds it to its rows in registers.
+// with fp32 outputs O_s holds two key tiles' products only and the softmax group adds them to its rows in registers.
 //
 // Drafted windows (kAlt): one M tile, and the two stages take alternate key tiles, each with its own running state.
 // When tiles alone leave SMs idle the key range is split as well; the parts are joined by dense_join_kernel.
@@ -59,6 +59,9 @@ struct DpCfg {
     static constexpr int NK = kParts == 1 ? 128 : 64;
     static constexpr int kTile = NK * kHeadDim * 2;  // bytes of a K or V tile
     static constexpr int kStages = (kForm == kDpInt ? 4 : 5) * (128 / NK);
+    // Column of S in its 128.  P's parts lie at columns 0, 32 and 64: with S from 64 on (fp32 outputs) a row's first 32
+    // scores can be read, made into weights and overwritten before its last 32 are read.
+    static constexpr int kSAt = kParts == 1 ? 0 : 64;
 };
 
 template <int kParts, int kForm>
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                                                                     const DenseArgs a, int nsplit) {
     constexpr bool kWide = kForm == kDpInt, kF16 = kForm == kDpF16;
     using Cfg = DpCfg<kParts, kForm>;
-    constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2;
+    constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2, kSAt = Cfg::kSAt;
     extern __shared__ uint8_t smem_raw[];
     using Smem = DpSmem<kParts, kForm>;
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     const uint64_t kb = kd + static_cast<uint64_t>((slot % kStages) * (Cfg::kTile >> 4));
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        tc_mma_ss(tmem + s * 128, qd + static_cast<uint64_t>(((k >> 2) * (kDpQBytes / 2) + (k & 3) * 32) >> 4),
+                        tc_mma_ss(tmem + s * 128 + kSAt, qd + static_cast<uint64_t>(((k >> 2) * (kDpQBytes / 2) + (k & 3) * 32) >> 4),
                                   kb + static_cast<uint64_t>(((k >> 2) * kHalf + (k & 3) * 32) >> 4), idesc_s, k > 0);
                         if (k == 5 && pass) mbar_arrive(&sm.turn[s ^ 1]);
                     }
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                             for (int k = 4 * h2; k < 4 * h2 + 4; ++k)
                                 dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + k * 8,
                                           vb + static_cast<uint64_t>(k * 2048 >> 4), idesc_o,
-                                          !((kParts > 1 || c == 0) && part == 0 && k == 0));
+                                          !((kParts > 1 ? (c & 1) == 0 : c == 0) && part == 0 && k == 0));
                     }
                     if (!ok) break;
                     if (next) {
@@ -620,7 +623,18 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
 #pragma unroll
             for (int k = 0; k < kHeadDim; ++k) acc[k] = 0.f;
         }
-        auto collect = [&]() {  // adds the last tile's product to it
+        auto rescale = [&](float r) {  // O in tensor memory times r
+#pragma unroll 1
+            for (int q = 0; q < kHeadDim / 32; ++q) {
+                float y[32];
+                dp_ld32(o_addr + 32 * q, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) y[k] *= r;
+                dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
+            }
+        };
+        auto collect = [&]() {  // adds the last two tiles' product to it
             if constexpr (kParts > 1) {
 #pragma unroll
                 for (int q = 0; q < kHeadDim / 16; ++q) {
@@ -637,7 +651,109 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], c & 1, a.err));
             if (!alive) break;
             tc_fence_after();
-            if (c > 0) collect();
+            if (c > 0 && (c & 1) == 0) collect();
+            if constexpr (kParts > 1) {  // ---- fp32 outputs: 32 scores at a time, O in registers (the code below has no room for it)
+                const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
+                const int e = j % kDpScaleSlots;
+                if constexpr (kWide) {
+                    alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], (j / kDpScaleSlots) & 1, a.err));
+                    if (!alive) break;
+                }
+                // the scores of keys 32 q .. of the tile in the log2 domain (f: what is left to multiply by)
+                const float f = kWide || edge ? 1.f : a.scale_log2;
+                auto scores_of = [&](int q, float (&x)[32]) {
+                    dp_ld32(s_addr + kSAt + 32 * q, x);
+                    tmem_ld_wait();
+                    if constexpr (kWide) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 ks = *reinterpret_cast<const float4*>(&sm.sc[e][0][32 * q + k]);
+                            x[k] *= ks.x * a.scale_log2;
+                            x[k + 1] *= ks.y * a.scale_log2;
+                            x[k + 2] *= ks.z * a.scale_log2;
+                            x[k + 3] *= ks.w * a.scale_log2;
+                        }
+                    }
+                    if (edge) {
+                        const int seen = pos + 1 - t0 - 32 * q;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = k < seen ? (kWide ? x[k] : x[k] * a.scale_log2) : -INFINITY;
+                    }
+                };
+                float now = -INFINITY;
+                if (kWide || edge) {
+#pragma unroll 1
+                    for (int q = 0; q < 2; ++q) {
+                        float x[32];
+                        scores_of(q, x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) now = fmaxf(now, x[k]);
+                    }
+                } else {
+                    tmem_ld_max64(s_addr + kSAt, now);
+                    tmem_ld_wait();
+                    now *= f;
+                }
+                if (c == 0) {
+                    top = now;
+                } else if (__any_sync(0xffffffffu, now > top + kDpSlack)) {
+                    const float next = now > top + kDpSlack ? now : top;
+                    const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
+#pragma unroll
+                    for (int k = 0; k < kHeadDim; ++k) acc[k] *= r;
+                    if (c & 1) rescale(r);
+                    sum *= r;
+                    top = next;
+                }
+                const float base = top == -INFINITY ? 0.f : top;
+                const float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+                float2 add = make_float2(0.f, 0.f);
+#pragma unroll 1
+                for (int q = 0; q < 2; ++q) {
+                    float x[32];
+                    scores_of(q, x);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), ff, nb);
+                        x[2 * k] = dp_exp2(y.x);
+                        x[2 * k + 1] = dp_exp2(y.y);
+                        add = __fadd2_rn(add, make_float2(x[2 * k], x[2 * k + 1]));
+                    }
+                    if constexpr (kWide) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            const float4 vs = *reinterpret_cast<const float4*>(&sm.sc[e][1][32 * q + k]);
+                            // a hidden key's weight stays 0 whatever its scale is
+                            x[k] = edge && x[k] == 0.f ? 0.f : x[k] * vs.x;
+                            x[k + 1] = edge && x[k + 1] == 0.f ? 0.f : x[k + 1] * vs.y;
+                            x[k + 2] = edge && x[k + 2] == 0.f ? 0.f : x[k + 2] * vs.z;
+                            x[k + 3] = edge && x[k + 3] == 0.f ? 0.f : x[k + 3] * vs.w;
+                        }
+                    }
+#pragma unroll
+                    for (int part = 0; part < kParts; ++part) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            pk[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                            if (part + 1 < kParts) {
+                                x[2 * k] -= bf16_lo(pk[k]);
+                                x[2 * k + 1] -= bf16_hi(pk[k]);
+                            }
+                        }
+                        dp_st16(s_addr + part * 32 + 16 * q, pk);
+                    }
+                }
+                sum += add.x + add.y;
+                dp_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.p_full[s][0]);
+                    if constexpr (kWide) mbar_arrive(&sm.sc_empty[e]);
+                }
+                continue;
+            } else {
             float x[NK], big[NK / 64];
 #pragma unroll
             for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
@@ -647,22 +763,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 fac_now[1] = fac_next[1];
                 if (c + 1 < count) load_fac(c + 1, fac_next);
             }
-            const int e = j % kDpScaleSlots;
-            if constexpr (kWide) {
-                alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], (j / kDpScaleSlots) & 1, a.err));
-                if (!alive) break;
-            }
             tmem_ld_wait();
-            if constexpr (kWide) {
-#pragma unroll
-                for (int k = 0; k < NK; k += 4) {
-                    const float4 ks = *reinterpret_cast<const float4*>(&sm.sc[e][0][k]);
-                    x[k] *= ks.x;
-                    x[k + 1] *= ks.y;
-                    x[k + 2] *= ks.z;
-                    x[k + 3] *= ks.w;
-                }
-            }
             const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
             if (edge) {
                 const int seen = pos + 1 - t0;
@@ -677,7 +778,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 f = 1.f;
             }
             float now;
-            if (kWide || edge) {  // the scores are not those that the load took the maximum of
+            if (edge) {  // the scores are not those that the load took the maximum of
                 float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < NK; k += 8)
@@ -700,20 +801,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
                 const float ro = kF16 ? r * (vref / vnew) : r;  // (vnew > 0: every block's is)
                 if constexpr (kF16) coarse |= vref < vnew * 2.4414063e-4f;
-                if constexpr (kParts > 1) {
-#pragma unroll
-                    for (int k = 0; k < kHeadDim; ++k) acc[k] *= r;
-                } else {
-#pragma unroll 1
-                    for (int q = 0; q < kHeadDim / 32; ++q) {
-                        float y[32];
-                        dp_ld32(o_addr + 32 * q, y);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] *= ro;
-                        dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
-                    }
-                }
+                rescale(ro);
                 sum *= r;
                 top = next;
             }
@@ -751,30 +839,11 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
 #pragma unroll
                         for (int k = 0; k < 32; ++k) z[k] *= unit;
                     }
-                    if constexpr (kWide) {
+                    uint32_t pk[16];
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 vs = *reinterpret_cast<const float4*>(&sm.sc[e][1][64 * h2 + 32 * q + k]);
-                            // a hidden key's weight stays 0 whatever its scale is
-                            z[k] = edge && z[k] == 0.f ? 0.f : z[k] * vs.x;
-                            z[k + 1] = edge && z[k + 1] == 0.f ? 0.f : z[k + 1] * vs.y;
-                            z[k + 2] = edge && z[k + 2] == 0.f ? 0.f : z[k + 2] * vs.z;
-                            z[k + 3] = edge && z[k + 3] == 0.f ? 0.f : z[k + 3] * vs.w;
-                        }
-                    }
-#pragma unroll
-                    for (int part = 0; part < kParts; ++part) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            pk[k] = kF16 ? dp_pack_f16(z[2 * k], z[2 * k + 1]) : pack_bf16x2(z[2 * k], z[2 * k + 1]);
-                            if (part + 1 < kParts) {
-                                z[2 * k] -= bf16_lo(pk[k]);
-                                z[2 * k + 1] -= bf16_hi(pk[k]);
-                            }
-                        }
-                        dp_st16(s_addr + part * (NK / 2) + 32 * h2 + 16 * q, pk);
-                    }
+                    for (int k = 0; k < 16; ++k)
+                        pk[k] = kF16 ? dp_pack_f16(z[2 * k], z[2 * k + 1]) : pack_bf16x2(z[2 * k], z[2 * k + 1]);
+                    dp_st16(s_addr + 32 * h2 + 16 * q, pk);
                 }
                 dp_st_wait();
                 tc_fence_before();
@@ -782,8 +851,6 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 if (lane == 0) mbar_arrive(&sm.p_full[s][h2]);
             }
             sum += (add[0].x + add[0].y) * back[0] + (add[1].x + add[1].y) * back[1];
-            if constexpr (kWide) {
-                if (lane == 0) mbar_arrive(&sm.sc_empty[e]);  // (after the warp's last barrier: every lane has read them)
             }
         }
         // ---------------- epilogue
