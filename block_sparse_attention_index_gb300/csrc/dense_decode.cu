@@ -137,8 +137,9 @@ __device__ __forceinline__ DdSeq dd_seq(const DenseArgs& a, int b) {
     return s;
 }
 
-// CTAs that take a share of the units: share c is units [total c / shares, total (c + 1) / shares), none of them empty.
-__device__ __forceinline__ int dd_shares(int total, int grid) { return min(total, grid); }
+// CTAs that take a share of the tiles (unit u, head h: tile u H + h): share c is tiles [total c / shares,
+// total (c + 1) / shares), none of them empty.
+__device__ __forceinline__ int dd_shares(int64_t total, int grid) { return static_cast<int>(min(total, static_cast<int64_t>(grid))); }
 
 // Writes two neighbouring outputs of (row, head) pair m of a sequence, heads of KV head h.
 __device__ __forceinline__ void dd_store2(const DenseArgs& a, const DdSeq& s, int h, int m, int d, float x, float y) {
@@ -205,11 +206,13 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     __syncthreads();
     if (blockIdx.x == 0 && a.num_seqs < kDdPrefix)
         for (int b = tid; b <= a.num_seqs; b += kDdThreads) a.unit_prefix[b] = prefix[b];
-    const int64_t total = carry;
-    const int shares = dd_shares(carry, gridDim.x);  // CTAs with work
+    // this CTA's tiles: [begin, begin + n) of all; the first is head h_off of unit u0
+    const int64_t total = static_cast<int64_t>(carry) * H;
+    const int shares = dd_shares(total, gridDim.x);  // CTAs with work
     const bool idle = static_cast<int>(blockIdx.x) >= shares;
-    const int u0 = idle ? 0 : static_cast<int>(total * blockIdx.x / shares);
-    const int u1 = idle ? 0 : static_cast<int>(total * (blockIdx.x + 1) / shares);
+    const int64_t begin = idle ? 0 : total * blockIdx.x / shares;
+    const int n_tiles = idle ? 0 : static_cast<int>(total * (blockIdx.x + 1) / shares - begin);
+    const int u0 = static_cast<int>(begin / H), h_off = static_cast<int>(begin % H), u1 = u0 + (h_off + n_tiles + H - 1) / H;
     int first_b = 0;
     {
         int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= u0
@@ -228,7 +231,8 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
         // sees every phase of its stages.  32 blocks' cache rows at a time, one lane each, then their tiles in order.
         static_assert(Cfg::kStages % 2 == 0, "a producer must see every phase of its stages");
         const int odd = warp - kDdConsumers;
-        int b = first_b, tile = 0;
+        int sent = 0;  // the CTA's tiles up to this warp's last copy
+        int b = first_b;
         bool alive = true;
         for (int base = u0; base < u1 && alive; base += 32) {
             const int u = base + lane;
@@ -251,8 +255,9 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                 const int64_t r = __shfl_sync(0xffffffffu, row, i);
                 const int n = __shfl_sync(0xffffffffu, live, i);
 #pragma unroll 1
-                for (int h = 0; h < H; ++h, ++tile) {
-                    if ((tile & 1) != odd) continue;
+                for (int h = 0; h < H; ++h) {
+                    const int tile = (base - u0 + i) * H + h - h_off;  // of the CTA's
+                    if (tile < 0 || tile >= n_tiles || (tile & 1) != odd) continue;
                     const int s = tile % Cfg::kStages;
                     int ok = 1;
                     if (lane == 0 && tile >= Cfg::kStages) ok = mbar_wait(&empty[s], ((tile / Cfg::kStages) - 1) & 1, &err);
@@ -263,6 +268,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     }
                     uint8_t* st = ring + s * Cfg::kStageBytes;
                     uint64_t* bar = &full[tile % kDdFull];
+                    sent = tile + 1;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar, 2 * Cfg::kPlane);
                         if constexpr (kInt8) {
@@ -293,22 +299,24 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
         }
         // no copy of this warp may be in flight when the CTA ends
         if (lane == 0)
-            for (int s = odd; s < kDdFull && s < tile; s += 2) mbar_wait(&full[s], ((tile - 1 - s) / kDdFull) & 1, &err);
+            for (int s = odd; s < kDdFull && s < sent; s += 2) mbar_wait(&full[s], ((sent - 1 - s) / kDdFull) & 1, &err);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        // ---------------- consumer warp: tiles warp, warp + 8, ... of the CTA, all of head warp % H
+        // ---------------- consumer warp: every 8th tile, all of head warp % H
         const int grp = lane >> 2, tig = lane & 3, h = warp % H;
         // int8, bf16 outputs: the keys keep their bias and the accumulators begin at -1152 sum q (its cancellation costs
         // some 1e-5 of a score's spread, far below the outputs' rounding; fp32 outputs take the bias off)
         constexpr bool kBiased = kInt8 && kParts == 1;
         bool alive = true;
-        int i = warp, b = first_b;
-        for (int u = u0; u < u1;) {
+        int i = (warp - static_cast<int>(begin % kDdConsumers)) & (kDdConsumers - 1), b = first_b;
+        for (int cur = 0; cur < n_tiles;) {
+            const int u = u0 + (cur + h_off) / H;
             while (u >= prefix[b + 1]) ++b;
             const DdSeq s = dd_seq(a, b);
             const int mt = (u - prefix[b]) / s.blocks, seg0 = prefix[b] + mt * s.blocks, seg1 = seg0 + s.blocks;
-            const int end = min(u1, seg1);  // this CTA's part of the tile: units [u, end)
+            // this CTA's part of the (sequence, 16 pairs): its tiles [cur, end)
+            const int seg_first = (seg0 - u0) * H - h_off, seg_last = (seg1 - u0) * H - h_off, end = min(n_tiles, seg_last);
             const int pairs = min(16, s.n * a.G - 16 * mt);
             // rows grp and grp + 8 of the tile: (row, head) pair, position, whether it exists
             int pos[2];
@@ -364,14 +372,13 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     }
                 }
             }
-            const int i_first = (u - u0) * H, tiles = (end - u) * H;  // of this part
             float vref = 0.f, vinv = 0.f;  // int8: the power of two that the value scales are divided by, its inverse
             float o[16][4], mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < 16; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
 
-            for (; i < (end - u0) * H; i += kDdConsumers) {
-                const int st = i % Cfg::kStages, j = u0 + i / H - seg0, t0 = j * kBlock;
+            for (; i < end; i += kDdConsumers) {
+                const int st = i % Cfg::kStages, j = u0 + (i + h_off) / H - seg0, t0 = j * kBlock;
                 if (alive) alive = mbar_wait(&full[i % kDdFull], (i / kDdFull) & 1, &err);
                 if (!alive) continue;
                 uint8_t* stage = ring + st * Cfg::kStageBytes;
@@ -654,7 +661,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
             // ---- the warps of a head join their parts (8 / H of them, by halves)
 #pragma unroll
             for (int half = kDdConsumers / 2; half >= H; half >>= 1) {
-                if (i_first % kDdConsumers == 0 && tiles <= half) continue;  // warps from `half` on had no tile
+                if ((begin + cur) % kDdConsumers == 0 && end - cur <= half) continue;  // warps from `half` on had no tile
                 float f1[2], f2[2];
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {  // half of O at a time
@@ -697,8 +704,8 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     lrun[e] += __shfl_xor_sync(0xffffffffu, lrun[e], 1);
                     lrun[e] += __shfl_xor_sync(0xffffffffu, lrun[e], 2);
                 }
-                const bool whole = u == seg0 && end == seg1;
-                const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1)) * H + h;
+                const bool whole = cur == seg_first && end == seg_last;
+                const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (cur == 0 ? 0 : 1)) * H + h;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int m = grp + 8 * e;
@@ -724,7 +731,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     }
                 }
             }
-            u = end;
+            cur = end;
         }
     }
     __syncthreads();
@@ -736,12 +743,39 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 // shares is the first to fall, if any; of its (row, head) pairs every gridDim.z-th.  Four warps share a pair, each a
 // quarter of the parts, eight parts' loads in flight and 4 of the 128 values a lane: a running maximum m and sum of
 // 2^(m_i - m) O_i in the parts' order within a warp, then over the warps: the same every time.  What bounds it is the
-// chain of dependent loads (metadata, parts), so everything that can go out together does.
+// chain of dependent loads (metadata, parts), so the metadata is read while the shares' CTAs still run.
 constexpr int kDcThreads = 128;
 __global__ void __launch_bounds__(kDcThreads, 8) dense_combine_kernel(const DenseArgs a, int grid, int by_tile) {
     __shared__ float4 sum_o[4][32];
     __shared__ float2 sum_ml[4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
+    // ---- which parts: from the inputs alone where a thread a sequence is enough (before the wait), else from the prefix
+    // that the shares' CTA 0 wrote
+    int lo = by_tile > 0 ? blockIdx.x / by_tile : 0, mt = by_tile > 0 ? blockIdx.x % by_tile : 0;  // sequence, tile
+    const bool early = by_tile > 0 && a.num_seqs <= kDcThreads;
+    int begin = 0, units = 0, carry = 0;  // units before the sequence, of it, of all
+    if (early) {
+        __shared__ int sums[3][4];
+        bool bad;
+        const int mine = tid < a.num_seqs ? dd_units(a, tid, bad) : 0;
+        const int before = __reduce_add_sync(0xffffffffu, tid < lo ? mine : 0);
+        const int here = __reduce_add_sync(0xffffffffu, tid == lo ? mine : 0);
+        const int all = __reduce_add_sync(0xffffffffu, mine);
+        if (lane == 0) {
+            sums[0][warp] = before;
+            sums[1][warp] = here;
+            sums[2][warp] = all;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            begin += sums[0][q];
+            units += sums[1][q];
+            carry += sums[2][q];
+        }
+    }
+    DdSeq s{};
+    if (early) s = dd_seq(a, lo);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the shares' CTAs found wrong
@@ -753,12 +787,12 @@ __global__ void __launch_bounds__(kDcThreads, 8) dense_combine_kernel(const Dens
             else if (e) atomicOr(a.err, e);
         }
     }
-    const int total = a.unit_prefix[a.num_seqs];
+    if (!early) carry = a.unit_prefix[a.num_seqs];
+    const int64_t total = static_cast<int64_t>(carry) * a.H;
     const int shares = dd_shares(total, grid);
-    int lo = by_tile > 0 ? blockIdx.x / by_tile : 0, mt = by_tile > 0 ? blockIdx.x % by_tile : 0;  // sequence, tile
     if (by_tile == 0) {
         if (static_cast<int>(blockIdx.x) + 1 >= shares) return;
-        const int cut = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / shares);
+        const int cut = static_cast<int>(total * (blockIdx.x + 1) / shares / a.H);  // the unit of the boundary's tile
         int hi = a.num_seqs;  // largest b with prefix[b] <= cut
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -766,18 +800,20 @@ __global__ void __launch_bounds__(kDcThreads, 8) dense_combine_kernel(const Dens
         }
         mt = (cut - a.unit_prefix[lo]) / dd_blocks(a.cache_lens[lo]);
     }
-    const int begin = a.unit_prefix[lo], units = a.unit_prefix[lo + 1] - begin;
-    const DdSeq s = dd_seq(a, lo);
+    if (!early) {
+        begin = a.unit_prefix[lo];
+        units = a.unit_prefix[lo + 1] - begin;
+        s = dd_seq(a, lo);
+    }
     if (units == 0 || mt >= s.tiles) return;
-    const int seg0 = begin + mt * s.blocks, seg1 = seg0 + s.blocks;
-    // the shares that hold its first and last units: the largest c with total c / shares <= unit
-    const int first = static_cast<int>((static_cast<int64_t>(seg0 + 1) * shares - 1) / total);
-    const int last = static_cast<int>((static_cast<int64_t>(seg1) * shares - 1) / total);
-    // one share wrote it whole; the boundary lies between two tiles, or an earlier one inside the tile has its CTA
+    const int64_t seg0 = static_cast<int64_t>(begin + mt * s.blocks) * a.H, seg1 = seg0 + static_cast<int64_t>(s.blocks) * a.H;
+    // the shares that hold its first and last tiles: the largest c with total c / shares <= tile
+    const int first = static_cast<int>(((seg0 + 1) * shares - 1) / total), last = static_cast<int>((seg1 * shares - 1) / total);
+    // one share wrote it whole; the boundary lies between two of them, or an earlier one inside it has its CTA
     if (first == last || (by_tile == 0 && first != static_cast<int>(blockIdx.x))) return;
     const int count = last - first + 1;
     // the first share's part is its second one unless the share began with it; the others' are the first of their shares
-    const int slot0 = 2 * first + (static_cast<int>(static_cast<int64_t>(total) * first / shares) < seg0 ? 1 : 0);
+    const int slot0 = 2 * first + (total * first / shares < seg0 ? 1 : 0);
     const int i_begin = count * warp / 4, i_end = count * (warp + 1) / 4;
     const int pairs = min(16, s.n * a.G - 16 * mt);
     for (int pair = blockIdx.z; pair < pairs; pair += gridDim.z) {
