@@ -26,7 +26,9 @@
 // with fp32 outputs O_s holds two key tiles' products only and the softmax group adds them to its rows in registers.
 //
 // Drafted windows (kAlt): one M tile, and the two stages take alternate key tiles, each with its own running state.
-// When tiles alone leave SMs idle the key range is split as well; the parts are joined by dense_join_kernel.
+// Items (a tile pair and a head) are one CTA each, the longest first; those of the last wave, which would leave SMs
+// idle, are split over their keys as well (2,048 int8 rows at 8,192: 512 items on 152 SMs ended between 432 and 562 us)
+// and their parts joined by dense_join_kernel.
 //
 // int8 caches are read from a copy widened once per call.  bf16 outputs: f16 values with the scales in them, over a
 // power of two for each 64-position block (run_widen_f16), queries as f16 times a power of two for each row (converted
@@ -51,6 +53,15 @@ constexpr int kDpThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 copies, 9 
 constexpr int kDpQBytes = 128 * kHeadDim * 2;
 constexpr int kDpScaleSlots = 4;
 constexpr float kDpSlack = 8.f;  // log2 by which the running maximum may lag
+
+// A CTA's work: one of the launch's items (an M tile pair, kAlt: a single tile, of a sequence; and a KV head), whole or
+// a part of its key range.
+struct DpItem {
+    int b, tile, h;            // b < 0: none
+    int c0, n, L;              // of the sequence: first row, rows, length
+    int split, nsplit, part;   // part `split` of `nsplit`; the part's place in the workspace
+    int item;                  // of those that are split: its number
+};
 
 enum DpForm { kDpBf16 = 0, kDpInt = 1, kDpF16 = 2 };  // bf16 caches; int8: bf16 integers with scales; int8: f16 copy
 
@@ -80,7 +91,8 @@ struct __align__(1024) DpSmem {
     uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
     uint32_t tmem;
     int32_t scan[kDpThreads / 32];
-    int32_t found[4];
+    float scan_keys[kDpThreads / 32];
+    DpItem found;
     float2 other_ml[128];  // drafted windows: maxima and sums of the second stream
 };
 static_assert(sizeof(DpSmem<1, kDpBf16>) + 1024 <= 227 * 1024, "prompt attention exceeds 227 KB of shared memory");
@@ -153,39 +165,63 @@ __device__ __forceinline__ void dp_bulk(void* dst, const void* src, uint32_t byt
                  : "memory");
 }
 
-// Work of a launch: M tile pairs (kAlt: single tiles) of the sequences it takes.
-struct DpItem {
-    int b, tile;  // b < 0: none
-};
-
+// Items of the sequence without its heads; its metadata; `keys`: its items' key tiles (128 positions).
 template <bool kAlt>
-__device__ __forceinline__ int dp_tiles(const DenseArgs& a, int b, bool& bad) {
+__device__ __forceinline__ int dp_tiles(const DenseArgs& a, int b, DpItem& it, float& keys, bool& bad) {
     bad = false;
-    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0;
+    keys = 0.f;
+    // (loads that need not wait for one another)
+    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0, L = a.cache_lens[b];
+    const bool placed = seq_rows_ok(a.seq_cache, b, L, a.seq_cache_tokens);
+    const bool here = a.cache.table != nullptr || a.cache.starts[b] >= 0;  // (else widened in another pass)
     if (n == 0) return 0;
     if (kAlt ? n < 0 || n > kDecodeMaxRows || n * a.G <= 16 : a.only_multi_row && n > 0 && n <= kDecodeMaxRows) return 0;
-    const int L = a.cache_lens[b];
-    if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
-        !seq_rows_ok(a.seq_cache, b, L, a.seq_cache_tokens)) {
+    if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len || !placed) {
         bad = true;
         return 0;
     }
-    if (a.cache.table == nullptr && a.cache.starts[b] < 0) return 0;  // widened in another pass
-    const int rows = (128 / a.G) * (kAlt ? 1 : 2);
-    return (n + rows - 1) / rows;
+    if (!here) return 0;
+    it.c0 = c0;
+    it.n = n;
+    it.L = L;
+    const int rows = (128 / a.G) * (kAlt ? 1 : 2), tiles = (n + rows - 1) / rows;
+    keys = tiles * (static_cast<float>(L) - 0.5f * n) * (1.f / 128.f);
+    return tiles;
 }
 
-// The block finds its item: the tiles of all sequences counted by a block-wide scan, the longest first (the last tile
-// of a sequence has the most keys).  Ends with every thread holding the same answer.
+// What `n` parts of each of the last wave's `rest` items cost, in key tiles: a wave of CTAs takes its tiles and what a
+// CTA costs besides (about six; parts ten, as they write 32-bit rows), and the parts are joined.
+__host__ __device__ constexpr float dp_cost(int rest, int places, float tiles, int n) {
+    return ((rest * n + places - 1) / places) * (tiles / n + (n > 1 ? 10.f : 6.f)) + (n > 1 ? 12.f : 0.f);
+}
+
+// Key ranges that the items of the last, unfilled wave are split into: `rest` items of `tiles` key tiles each on `places`
+// SMs, `most` parts at most; lane n - 1 weighs n parts.
+__device__ __forceinline__ int dp_split(int rest, int places, float tiles, int most) {
+    const int n = (threadIdx.x & 31) + 1;
+    const bool fits = n == 1 || (rest > 0 && rest * n <= most && tiles >= 4.f * n);
+    const uint32_t mine = fits ? static_cast<uint32_t>(dp_cost(rest, places, tiles, n) * 16.f) << 5 | (n - 1) : 0xffffffffu;
+    return static_cast<int>(__reduce_min_sync(0xffffffffu, mine) & 31u) + 1;
+}
+
+// The block finds its item: all sequences' tiles counted by a block-wide scan, the longest first (the last tile of a
+// sequence has the most keys).  Whole waves of items go whole; those of the last wave may be split.  Ends with every
+// thread holding the same answer.
 template <bool kAlt, int kThreads>
-__device__ DpItem dp_find(const DenseArgs& a, int index, int items, int32_t* scan, int32_t* found) {
+__device__ DpItem dp_find(const DenseArgs& a, int items, int32_t* scan, float* scan_keys, DpItem* found) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.num_seqs + kThreads - 1) / kThreads;
-    const int b0 = min(tid * per, a.num_seqs), b1 = min(b0 + per, a.num_seqs);
+    // up to 32 sequences every warp finds it by itself, a lane a sequence
+    const bool few = a.num_seqs <= 32;
+    const int per = (a.num_seqs + kThreads - 1) / kThreads, at = few ? lane : tid;
+    const int b0 = min(at * per, a.num_seqs), b1 = min(b0 + per, a.num_seqs);
     int mine = 0;
+    float keys = 0.f;
+    DpItem it{};
     for (int b = b0; b < b1; ++b) {
         bool bad;
-        mine += dp_tiles<kAlt>(a, b, bad);
+        float k;
+        mine += dp_tiles<kAlt>(a, b, it, k, bad);
+        keys += k;
         if (bad && blockIdx.x == 0) atomicOr(a.err, kErrBadMetadata);
     }
     int incl = mine;
@@ -194,31 +230,71 @@ __device__ DpItem dp_find(const DenseArgs& a, int index, int items, int32_t* sca
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) scan[warp] = incl;
-    if (tid == 0) found[0] = -1;
-    __syncthreads();
-    int before = incl - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+    int before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
+    if (!few) {
+        if (lane == 31) scan[warp] = incl;
+        if (lane == 0) scan_keys[warp] = keys;
+        if (tid == 0) found->b = -1;
+        __syncthreads();
+        total = 0;
+        keys = 0.f;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += scan[w];
+            total += scan[w];
+            keys += scan_keys[w];
+        }
     }
     // more tiles than the host's row counts allow for: the first of them go without
     if (total > items && blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrBadMetadata);
-    int want = total - 1 - index - before;
-    if (index < total && want >= 0 && want < mine) {
+    total = min(total, items);
+    const int all = total * a.H, whole = all / a.places * a.places, rest = all - whole;
+    const int nsplit = dp_split(rest, a.places, total > 0 ? keys / total : 0.f, a.parts_most);
+    const int g = blockIdx.x, r = g - whole;
+    if (g == 0 && tid == 0) *a.split_head = make_int2(nsplit > 1 ? rest : 0, nsplit);
+    const int item = r < 0 ? g : whole + r / nsplit;
+    int want = total - 1 - item / a.H - before;
+    const bool here = item < all && want >= 0 && want < mine;  // one thread (few: one lane of each warp)
+    if (here) {
         for (int b = b0; b < b1; ++b) {
             bool bad;
-            const int t = dp_tiles<kAlt>(a, b, bad);
+            float k;
+            const int t = dp_tiles<kAlt>(a, b, it, k, bad);
             if (want < t) {
-                found[1] = want;
-                found[0] = b;
+                it.b = b;
+                it.tile = want;
+                it.h = item % a.H;
+                it.nsplit = r < 0 ? 1 : nsplit;
+                it.split = r < 0 ? 0 : r % nsplit;
+                it.part = r;
+                it.item = item - whole;
+                if (!few) *found = it;
+                if (it.nsplit > 1 && it.split == 0) a.split_items[it.item] = make_int4(b, want, it.h, 0);
                 break;
             }
             want -= t;
         }
     }
+    if (few) {
+        const uint32_t who = __ballot_sync(0xffffffffu, here);
+        const int from = who ? __ffs(who) - 1 : 0;
+        DpItem x;
+        x.b = who ? __shfl_sync(0xffffffffu, it.b, from) : -1;
+        x.tile = __shfl_sync(0xffffffffu, it.tile, from);
+        x.h = __shfl_sync(0xffffffffu, it.h, from);
+        x.c0 = __shfl_sync(0xffffffffu, it.c0, from);
+        x.n = __shfl_sync(0xffffffffu, it.n, from);
+        x.L = __shfl_sync(0xffffffffu, it.L, from);
+        x.split = __shfl_sync(0xffffffffu, it.split, from);
+        x.nsplit = __shfl_sync(0xffffffffu, it.nsplit, from);
+        x.part = __shfl_sync(0xffffffffu, it.part, from);
+        x.item = __shfl_sync(0xffffffffu, it.item, from);
+        __syncthreads();
+        return x;
+    }
     __syncthreads();
-    return DpItem{found[0], found[1]};
+    return *found;
 }
 
 // What an item covers.
@@ -231,12 +307,13 @@ struct DpWork {
 };
 
 template <bool kAlt, int NK>
-__device__ __forceinline__ DpWork dp_work(const DenseArgs& a, const DpItem& it, int split, int nsplit) {
+__device__ __forceinline__ DpWork dp_work(const DenseArgs& a, const DpItem& it) {
     DpWork w;
+    const int split = it.split, nsplit = it.nsplit;
     w.b = it.b;
-    w.c0 = a.cu_rows[it.b];
-    w.n = a.cu_rows[it.b + 1] - w.c0;
-    w.L = a.cache_lens[it.b];
+    w.c0 = it.c0;
+    w.n = it.n;
+    w.L = it.L;
     w.P = 128 / a.G;
     w.i0 = it.tile * w.P * (kAlt ? 1 : 2);
     const int p0 = w.L - w.n;
@@ -324,7 +401,7 @@ template <int kParts, int kForm, bool kAlt>
 __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                     const __grid_constant__ CUtensorMap k_map,
                                                                     const __grid_constant__ CUtensorMap v_map,
-                                                                    const DenseArgs a, int nsplit) {
+                                                                    const DenseArgs a, int items) {
     constexpr bool kWide = kForm == kDpInt, kF16 = kForm == kDpF16;
     using Cfg = DpCfg<kParts, kForm>;
     constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2, kSAt = Cfg::kSAt;
@@ -332,20 +409,16 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     using Smem = DpSmem<kParts, kForm>;
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.H, split = blockIdx.x / a.H % nsplit, index = blockIdx.x / (a.H * nsplit);
-    const DpItem item = dp_find<kAlt, kDpThreads>(a, index, gridDim.x / (a.H * nsplit), sm.scan, sm.found);
-    if (item.b < 0) return;
-    const DpWork w = dp_work<kAlt, NK>(a, item, split, nsplit);
-
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be scheduled: it waits for this grid
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sm.full[0][s], 1);
             mbar_init(&sm.full[1][s], 1);
-            mbar_init(&sm.empty[s], kAlt ? 1 : max(1, (w.count[0] > 0) + (w.count[1] > 0)));  // the stages that read it
+            mbar_init(&sm.empty[s], kAlt ? 1 : 2);  // the stages' issuers (one with fewer tiles lets the others pass)
         }
         for (int s = 0; s < kDpScaleSlots; ++s) {
             mbar_init(&sm.sc_full[s], 1);
-            mbar_init(&sm.sc_empty[s], 4 * max(1, (w.count[0] > 0) + (w.count[1] > 0)));
+            mbar_init(&sm.sc_empty[s], 8);
         }
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.v_last, 1);
@@ -360,11 +433,19 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         }
         fence_mbar_init();
     }
+    if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &q_map : (lane == 1 ? &k_map : &v_map));
     if (warp == 9) tmem_alloc(&sm.tmem, 512);
     tc_fence_before();
-    __syncthreads();
+    const DpItem item = dp_find<kAlt, kDpThreads>(a, items, sm.scan, sm.scan_keys, &sm.found);  // (with block barriers)
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
+    if (item.b < 0) {
+        __syncthreads();
+        if (warp == 9) tmem_dealloc(tmem, 512);
+        return;
+    }
+    const int h = item.h;
+    const DpWork w = dp_work<kAlt, NK>(a, item);
     // the value tile that holds the end of the sequence, if its last rows are nobody's
     const int v_end = w.L / NK;
     const bool fix = w.L % NK != 0 && v_end >= w.first && v_end < w.first + w.total;
@@ -467,7 +548,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         } else if (warp == 9 || warp == 11) {
             // ---------------- matrix instructions of stage s, one thread
             const int s = warp == 9 ? 0 : 1;
-            if (lane == 0 && w.count[s] > 0) {
+            if (lane == 0) {
                 constexpr uint32_t idesc_s = kF16 ? idesc_f16_f32(128, NK, 0) : idesc_bf16_f32(128, NK, 0, 0);
                 constexpr uint32_t idesc_o = kF16 ? idesc_f16_f32(128, kHeadDim, 1) : idesc_bf16_f32(128, kHeadDim, 0, 1);
                 const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[kAlt ? 0 : s]), 16, 1024);
@@ -490,10 +571,10 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 };
                 constexpr int kStep = kAlt ? 2 : 1;
                 const int j0 = kAlt ? s : 0, count = w.count[s], others = w.count[s ^ 1];
-                bool ok = mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, 0, a.err) && landed(j0, 0);
-                const bool issued = ok;
+                bool ok = count == 0 || (mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, 0, a.err) && landed(j0, 0));
+                const bool issued = ok && count > 0;
                 tc_fence_after();
-                if (ok) {
+                if (issued) {
                     scores(slot_k(j0), false);
                     tc_commit(&sm.empty[slot_k(j0) % kStages]);
                 }
@@ -853,6 +934,12 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             sum += (add[0].x + add[0].y) * back[0] + (add[1].x + add[1].y) * back[1];
             }
         }
+        if constexpr (kWide) {  // scales of tiles that only the other group needs
+            for (int j = count; alive && j < w.total; ++j) {
+                alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[j % kDpScaleSlots], (j / kDpScaleSlots) & 1, a.err));
+                if (alive && lane == 0) mbar_arrive(&sm.sc_empty[j % kDpScaleSlots]);
+            }
+        }
         // ---------------- epilogue
         bool have = count > 0;
         if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], 0, a.err));
@@ -893,11 +980,11 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             }
             if (s == 1) alive = false;  // group 0 writes
         }
-        if (alive && (have || nsplit > 1)) {
+        const bool split_up = item.nsplit > 1;
+        if (alive && (have || split_up)) {
             constexpr int kRows = kAlt ? 128 : 256;  // rows of an item's part
             const int64_t q_row = (static_cast<int64_t>(w.c0 + min(i, w.n - 1)) * a.H + h) * a.G + g;
-            const int64_t part_row = ((static_cast<int64_t>(index) * a.H + h) * nsplit + split) * kRows + s * 128 + m;
-            const bool split_up = nsplit > 1;
+            const int64_t part_row = static_cast<int64_t>(item.part) * kRows + s * 128 + m;
             float most = 0.f;  // f16 form: the row's largest value, in units of w x V16
             bool spoiled = kAlt && !(fabsf(sum) < INFINITY);  // a product with a value past the row's position that is not finite
             const float inv = kF16 ? vref / sum : 1.f / sum;  // (parts: O in plain units, as their join expects)
@@ -926,10 +1013,11 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
 #pragma unroll
                         for (int k = 0; k < 8; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
                     } else if (a.out_bf16) {
+                        // through the stage's query buffer (its products are done), so that whole rows leave together
                         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_row * kHeadDim + 32 * q);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            dst[k] = make_uint4(pack_bf16x2(y[8 * k] * inv, y[8 * k + 1] * inv),
+                            *(kAlt ? dst + k : reinterpret_cast<uint4*>(sm.q[s] + m * 256 + (((4 * q + k) ^ (m & 15)) << 4))) = make_uint4(pack_bf16x2(y[8 * k] * inv, y[8 * k + 1] * inv),
                                                 pack_bf16x2(y[8 * k + 2] * inv, y[8 * k + 3] * inv),
                                                 pack_bf16x2(y[8 * k + 4] * inv, y[8 * k + 5] * inv),
                                                 pack_bf16x2(y[8 * k + 6] * inv, y[8 * k + 7] * inv));
@@ -941,6 +1029,19 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     }
                     __syncwarp();  // the next load is the whole warp's
                 }
+            }
+            if (!kAlt && have && !split_up && a.out_bf16) {  // two rows at a time, 16 bytes a lane
+                __syncwarp();
+                const uint32_t rows = __ballot_sync(0xffffffffu, mine);
+#pragma unroll 4
+                for (int r = 0; r < 32; r += 2) {
+                    const int from = r + (lane >> 4), row = (warp & 3) * 32 + from;
+                    const int64_t to = __shfl_sync(0xffffffffu, q_row, from);
+                    if ((rows >> from) & 1u)
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * kHeadDim + 8 * (lane & 15)) =
+                            *reinterpret_cast<const uint4*>(sm.q[s] + row * 256 + (((lane & 15) ^ (row & 15)) << 4));
+                }
+                __syncwarp();
             }
             if (split_up && mine) *reinterpret_cast<float2*>(a.part_ml + part_row * 2) = make_float2(top, sum);
             // f16 form: a row that lives on blocks whose values are tiny beside another block's (even one that it does
@@ -981,49 +1082,58 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     }
 }
 
-// Joins the parts of split items: CTA (item, head), a warp per row at a time; the parts in order, the same every time.
-constexpr int kDjThreads = 512;
+// Joins the parts of split items: CTA x takes split item x, a warp every 4 gridDim.y-th of its rows, 4 of the 128
+// values a lane, eight parts' loads in flight: a running maximum m and sum of 2^(m_i - m) O_i in the parts' order, the
+// same every time.
+constexpr int kDjThreads = 128;
 template <bool kAlt>
-__global__ void __launch_bounds__(kDjThreads) dense_join_kernel(const DenseArgs a, int nsplit) {
-    __shared__ int32_t scan[kDjThreads / 32], found[4];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.H, index = blockIdx.x / a.H;
-    const DpItem it = dp_find<kAlt, kDjThreads>(a, index, gridDim.x / a.H, scan, found);
-    if (it.b < 0) return;
-    const int c0 = a.cu_rows[it.b], n = a.cu_rows[it.b + 1] - c0, P = 128 / a.G, i0 = it.tile * P * (kAlt ? 1 : 2);
+__global__ void __launch_bounds__(kDjThreads, 8) dense_join_kernel(const DenseArgs a) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kRows = kAlt ? 128 : 256;
-    const int64_t base = (static_cast<int64_t>(index) * a.H + h) * nsplit * kRows;
-    for (int x = blockIdx.y * (kDjThreads / 32) + warp; x < kRows; x += gridDim.y * (kDjThreads / 32)) {
-        const int s = x >> 7, m = x & 127, i = i0 + s * P + m / a.G, g = m % a.G;
-        if (m >= P * a.G || i >= n) continue;
-        auto row_of = [&](int y) { return base + static_cast<int64_t>(y) * kRows + x; };
-        float top = -INFINITY;
-        for (int y = lane; y < nsplit; y += 32) top = fmaxf(top, a.part_ml[row_of(y) * 2]);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 head = *a.split_head;  // split items, parts of each
+    const int4 it = a.split_items[blockIdx.x];
+    if (static_cast<int>(blockIdx.x) >= head.x) return;
+    const int nsplit = head.y, h = it.z;
+    const int c0 = a.cu_rows[it.x], n = a.cu_rows[it.x + 1] - c0, P = 128 / a.G, i0 = it.y * P * (kAlt ? 1 : 2);
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * nsplit * kRows;
+    for (int x = blockIdx.y * 4 + warp; x < kRows; x += gridDim.y * 4) {
+        const int s = x >> 7, m0 = x & 127, i = i0 + s * P + m0 / a.G, g = m0 % a.G;
+        if (m0 >= P * a.G || i >= n) continue;
+        float m = -INFINITY, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int y0 = 0; y0 < nsplit; y0 += 8) {
+            float4 p[8];
+            float2 ml[8];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int y0 = 0; y0 < nsplit; y0 += 32) {
-            float f = 0.f;
-            if (y0 + lane < nsplit) {
-                const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + row_of(y0 + lane) * 2);
-                f = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : dp_exp2(ml.x - top);
-                l += f * ml.y;
+            for (int u = 0; u < 8; ++u) {
+                const int64_t row = base + static_cast<int64_t>(min(y0 + u, nsplit - 1)) * kRows + x;
+                ml[u] = *reinterpret_cast<const float2*>(a.part_ml + row * 2);
+                p[u] = *reinterpret_cast<const float4*>(a.part_o + row * kHeadDim + 4 * lane);
             }
-            const int count = min(32, nsplit - y0);
-#pragma unroll 4
-            for (int y = 0; y < count; ++y) {
-                const float wt = __shfl_sync(0xffffffffu, f, y);
-                const float4 p = *reinterpret_cast<const float4*>(a.part_o + row_of(y0 + y) * kHeadDim + 4 * lane);
-                if (wt != 0.f) {
-                    v[0] = fmaf(wt, p.x, v[0]);
-                    v[1] = fmaf(wt, p.y, v[1]);
-                    v[2] = fmaf(wt, p.z, v[2]);
-                    v[3] = fmaf(wt, p.w, v[3]);
+            float top = m;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) top = fmaxf(top, ml[u].x);
+            if (m != -INFINITY) {
+                const float f = dp_exp2(m - top);
+                l *= f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= f;
+            }
+            m = top;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (y0 + u >= nsplit) break;
+                // a part without keys (maximum -inf) weighs nothing, unless its sum is NaN
+                const float w = ml[u].x == -INFINITY ? (ml[u].y == ml[u].y ? 0.f : ml[u].y) : dp_exp2(ml[u].x - m);
+                if (w != 0.f) {
+                    l = fmaf(w, ml[u].y, l);
+                    v[0] = fmaf(w, p[u].x, v[0]);
+                    v[1] = fmaf(w, p[u].y, v[1]);
+                    v[2] = fmaf(w, p[u].z, v[2]);
+                    v[3] = fmaf(w, p[u].w, v[3]);
                 }
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         const float inv = 1.f / l;
         const int64_t out = (((static_cast<int64_t>(c0 + i) * a.H + h) * a.G) + g) * kHeadDim + 4 * lane;
         if (a.out_bf16)
@@ -1036,28 +1146,52 @@ __global__ void __launch_bounds__(kDjThreads) dense_join_kernel(const DenseArgs 
 }
 
 template <int kParts, int kForm, bool kAlt>
-static cudaError_t launch_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
+static cudaError_t launch_dense_prompt(DenseArgs a, int items, cudaStream_t stream) {
     auto* kernel = dense_prompt_kernel<kParts, kForm, kAlt>;
     const size_t smem = sizeof(DpSmem<kParts, kForm>) + 1024;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(items) * a.H * nsplit, kDpThreads, smem, stream>>>(*a.q_map, *a.k_map, *a.v_map, a, nsplit);
-    if ((e = cudaGetLastError()) != cudaSuccess || (nsplit == 1)) return e;
-    dense_join_kernel<kAlt><<<dim3(static_cast<unsigned>(items) * a.H, 4), kDjThreads, 0, stream>>>(a, nsplit);
-    return cudaGetLastError();
+    a.places = std::min(device_sm_count(), kDenseMaxShares);
+    // every item, and room for the parts of the last wave's: what the rule would choose for the host's counts where
+    // there is one sequence (or window each), which they tell exactly, else two a place
+    const int64_t whole = static_cast<int64_t>(items) * a.H;
+    const float tiles = a.max_cache_len / 128.f;
+    const int rest = static_cast<int>(whole % a.places);
+    a.parts_most = 0;
+    if (kAlt || a.num_seqs == 1) {
+        int best = 1;
+        for (int n = 2; n <= 32 && rest * n <= kDenseMaxParts && tiles >= 4.f * n; ++n)
+            if (dp_cost(rest, a.places, tiles, n) < dp_cost(rest, a.places, tiles, best)) best = n;
+        if (best > 1) a.parts_most = rest * best;
+    } else if (tiles >= 8.f) {
+        a.parts_most = 2 * a.places;
+    }
+    const int64_t grid = whole + a.parts_most;
+    kernel<<<static_cast<unsigned>(grid), kDpThreads, smem, stream>>>(*a.q_map, *a.k_map, *a.v_map, a, items);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.parts_most == 0) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(static_cast<int64_t>(items) * a.H, a.places)), kAlt ? 16 : 8, 1);
+    cfg.blockDim = dim3(kDjThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dense_join_kernel<kAlt>, a);
 }
 
-cudaError_t run_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
+cudaError_t run_dense_prompt(const DenseArgs& a, int items, cudaStream_t stream) {
     if (a.kv_int8)
-        return a.out_bf16 ? launch_dense_prompt<1, kDpF16, false>(a, items, nsplit, stream)
-                          : launch_dense_prompt<3, kDpInt, false>(a, items, nsplit, stream);
-    return a.out_bf16 ? launch_dense_prompt<1, kDpBf16, false>(a, items, nsplit, stream)
-                      : launch_dense_prompt<3, kDpBf16, false>(a, items, nsplit, stream);
+        return a.out_bf16 ? launch_dense_prompt<1, kDpF16, false>(a, items, stream)
+                          : launch_dense_prompt<3, kDpInt, false>(a, items, stream);
+    return a.out_bf16 ? launch_dense_prompt<1, kDpBf16, false>(a, items, stream)
+                      : launch_dense_prompt<3, kDpBf16, false>(a, items, stream);
 }
 
-cudaError_t run_dense_window(const DenseArgs& a, int items, int nsplit, cudaStream_t stream) {
-    return a.out_bf16 ? launch_dense_prompt<1, kDpBf16, true>(a, items, nsplit, stream)
-                      : launch_dense_prompt<3, kDpBf16, true>(a, items, nsplit, stream);
+cudaError_t run_dense_window(const DenseArgs& a, int items, cudaStream_t stream) {
+    return a.out_bf16 ? launch_dense_prompt<1, kDpBf16, true>(a, items, stream)
+                      : launch_dense_prompt<3, kDpBf16, true>(a, items, stream);
 }
 
 }  // namespace msa

@@ -221,6 +221,10 @@ struct DenseArgs {
     const float* seq_k_scale;  // int8 caches: the problem's scales
     const float* seq_v_scale;
     const float2* wide_fac;    // int8 prompts, bf16 outputs: factors of the f16 copy's blocks, [H, cache_tokens / 64]
+    int places;            // prompts, windows: SMs
+    int parts_most;        // parts of split items that there is room for
+    int2* split_head;      // prompts, windows: items that are split over their keys, parts of each
+    int4* split_items;     // [places] those items
     int pairs_most;        // decode family: most (row, head) pairs of a sequence that its kernel takes
     int32_t* unit_prefix;  // [num_seqs + 1] decode family: units before each sequence
     float* part_o;         // parts of what several CTAs walk: O [.., 128], decode family [2 shares, H, 16]
@@ -229,11 +233,11 @@ struct DenseArgs {
     int err_store;         // 1: the combine stores the error word, 0: it adds to it
     uint32_t* err;
 };
+constexpr int kDenseMaxParts = 960;   // most parts of items that are split over their keys (M tiles, prompts: pairs)
 constexpr int kDenseMaxShares = 160;  // most CTAs that share the decode family's cache walk
-constexpr int kDenseMaxSplit = 32;    // most key ranges of an M tile
 // Prompt chunks (M tile pairs of 2 (128 / G) rows) and drafted windows (one M tile a sequence); items: host bound.
-cudaError_t run_dense_prompt(const DenseArgs& a, int items, int nsplit, cudaStream_t stream);
-cudaError_t run_dense_window(const DenseArgs& a, int items, int nsplit, cudaStream_t stream);
+cudaError_t run_dense_prompt(const DenseArgs& a, int items, cudaStream_t stream);
+cudaError_t run_dense_window(const DenseArgs& a, int items, cudaStream_t stream);
 int dense_decode_shares(int64_t units, int H);  // CTAs for so many blocks
 cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream);
 

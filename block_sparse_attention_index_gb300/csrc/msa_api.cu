@@ -218,18 +218,10 @@ struct DensePlan {
     bool stream = false;   // decode-family sequences of at most 16 (row, head) pairs (all of them with an int8 cache)
     bool windows = false;  // the others of the decode family, on tcgen05
     bool prompts = false;
+    bool all_prompts = false;  // the prompt kernel takes the decode family too
     int64_t window_items = 0, prompt_items = 0;  // bounds of the M tiles (prompts: pairs of them)
-    int window_split = 1, prompt_split = 1;      // key ranges an M tile is split into
     int64_t wide_slots = 0, wide_total = 0, slot_rows = 0;  // int8 prompts: sequences widened a pass, in all; rows of each
 };
-
-// Key ranges for so many CTAs: enough to fill the GPU, at least eight 128-key tiles each.
-int dense_split(int64_t ctas, int max_cache_len) {
-    const int64_t tiles = (static_cast<int64_t>(max_cache_len) + 127) / 128;
-    int64_t n = 152 / std::max<int64_t>(ctas, 1);
-    n = std::min<int64_t>(n, tiles / 8);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, msa::kDenseMaxSplit)));
-}
 
 bool decode_family(const msa_problem* p) { return p->num_decode_seqs != 0; }
 bool prefill_family(const msa_problem* p) {
@@ -238,24 +230,26 @@ bool prefill_family(const msa_problem* p) {
 
 DensePlan dense_plan(const msa_problem* p) {
     DensePlan d;
-    const int64_t H = p->num_kv_heads, G = p->group_size;
+    const int64_t G = p->group_size;
     const int64_t known = p->num_decode_seqs;  // -1: unknown
-    if (decode_family(p)) {
+    // A few short contexts beside prompt chunks ride along with the chunks: their keys are at most 32 tiles each, in what
+    // is left of a wave, where kernels of their own cost 20 us (packed prompts with one 1-row sequence: 143 us).
+    d.all_prompts = prefill_family(p) && known > 0 && known * p->num_kv_heads <= 128 && p->max_cache_len <= 4096;
+    if (decode_family(p) && !d.all_prompts) {
         const int64_t rows = static_cast<int64_t>(decode_rows_per_seq(p)), seqs = known >= 0 ? known : p->num_seqs;
         const bool one_row = known >= 0 && p->num_decode_rows == known;  // every sequence
         const bool full = known >= 0 && p->num_decode_rows == known * rows;
         d.windows = p->kv_dtype == MSA_KV_BF16 && rows * G > 16 && !one_row;
         d.stream = !(d.windows && full);
         d.window_items = seqs;
-        d.window_split = dense_split(seqs * H, p->max_cache_len);
     }
     d.prompts = prefill_family(p);
     if (d.prompts) {
-        const int64_t rows = p->total_rows - std::max(p->num_decode_rows, 0);
-        int64_t seqs = known >= 0 ? p->num_seqs - known : p->num_seqs;
-        seqs = std::max<int64_t>(1, std::min<int64_t>(seqs, p->total_rows / (msa::kDecodeMaxRows + 1)));
-        d.prompt_items = rows / (2 * (128 / G)) + seqs;
-        d.prompt_split = dense_split(d.prompt_items * H, p->max_cache_len);
+        const int64_t rows = p->total_rows - (d.all_prompts ? 0 : std::max(p->num_decode_rows, 0));
+        int64_t seqs = known >= 0 && !d.all_prompts ? p->num_seqs - known : p->num_seqs;
+        if (!d.all_prompts) seqs = std::max<int64_t>(1, std::min<int64_t>(seqs, p->total_rows / (msa::kDecodeMaxRows + 1)));
+        const int64_t pair = 2 * (128 / G);  // rows of an item
+        d.prompt_items = p->num_seqs == 1 ? (rows + pair - 1) / pair : rows / pair + seqs;
         if (p->kv_dtype == MSA_KV_INT8) {
             d.slot_rows = (static_cast<int64_t>(p->max_cache_len) + msa::kBlock - 1) / msa::kBlock * msa::kBlock;
             d.wide_total = seqs;
@@ -266,7 +260,7 @@ DensePlan dense_plan(const msa_problem* p) {
 }
 
 struct DenseLayout {
-    size_t err = 0, err_slots = 0, unit_prefix = 0, part_ml = 0, part_o = 0, wide_starts = 0, wide_k = 0, wide_v = 0,
+    size_t err = 0, err_slots = 0, unit_prefix = 0, split = 0, part_ml = 0, part_o = 0, wide_starts = 0, wide_k = 0, wide_v = 0,
            wide_ks = 0, wide_vs = 0, total = 0;
 };
 
@@ -274,13 +268,15 @@ DenseLayout dense_layout(const msa_problem* p, const DensePlan& d) {
     DenseLayout l;
     const size_t H = p->num_kv_heads;
     size_t parts = d.stream ? 2 * msa::kDenseMaxShares * H * 16 : 0;  // the three launches follow one another: one buffer
-    if (d.windows && d.window_split > 1) parts = std::max(parts, static_cast<size_t>(d.window_items) * H * d.window_split * 128);
-    if (d.prompts && d.prompt_split > 1) parts = std::max(parts, static_cast<size_t>(d.prompt_items) * H * d.prompt_split * 256);
+    if (d.windows) parts = std::max<size_t>(parts, msa::kDenseMaxParts * 128);
+    if (d.prompts) parts = std::max<size_t>(parts, msa::kDenseMaxParts * 256);
     size_t off = 256;
     l.err_slots = off;
     off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
     l.unit_prefix = off;
     off = align256(off + (static_cast<size_t>(p->num_seqs) + 1) * sizeof(int32_t));
+    l.split = off;  // the head, then the items
+    off = align256(off + (1 + msa::kDenseMaxShares) * sizeof(int4));
     l.part_ml = off;
     off = align256(off + parts * 2 * sizeof(float));
     l.part_o = off;
@@ -968,12 +964,14 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.k_map = &km;
     a.v_map = &vm;
     a.unit_prefix = reinterpret_cast<int32_t*>(ws + l.unit_prefix);
+    a.split_head = reinterpret_cast<int2*>(ws + l.split);
+    a.split_items = reinterpret_cast<int4*>(ws + l.split) + 1;
     a.part_o = reinterpret_cast<float*>(ws + l.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
     a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
     a.tile_windows = d.windows;
     a.pairs_most = d.windows ? 16 : static_cast<int>(decode_rows_per_seq(p)) * p->group_size;
-    a.only_multi_row = decode_family(p);
+    a.only_multi_row = decode_family(p) && !d.all_prompts;
     a.q = static_cast<const uint16_t*>(q);
     a.k = k_cache;
     a.v = v_cache;
@@ -1004,10 +1002,10 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
         if ((e = msa::run_dense_decode(a, msa::dense_decode_shares(seqs * tiles * blocks, p->num_kv_heads), st)) != cudaSuccess)
             return cuda_fail(e, "dense decode attention launch");
     }
-    if (d.windows && (e = msa::run_dense_window(a, static_cast<int>(d.window_items), d.window_split, st)) != cudaSuccess)
+    if (d.windows && (e = msa::run_dense_window(a, static_cast<int>(d.window_items), st)) != cudaSuccess)
         return cuda_fail(e, "dense window attention launch");
     if (d.prompts && !a.kv_int8) {
-        if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), d.prompt_split, st)) != cudaSuccess)
+        if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), st)) != cudaSuccess)
             return cuda_fail(e, "dense prompt attention launch");
     } else if (d.prompts) {
         // int8: the prompts' positions widened into the workspace, as many sequences a pass as it holds
@@ -1051,7 +1049,7 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
             wa.first_slot = static_cast<int>(first);
             e = a.out_bf16 ? msa::run_widen_f16(wa, fac, st) : msa::run_widen_kv(wa, st);
             if (e != cudaSuccess) return cuda_fail(e, "key/value widening launch");
-            if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), d.prompt_split, st)) != cudaSuccess)
+            if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), st)) != cudaSuccess)
                 return cuda_fail(e, "dense prompt attention launch");
         }
     }
