@@ -49,7 +49,7 @@
 
 namespace msa {
 
-constexpr int kDpThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 copies, 9 and 11 matrix instructions, 10 last value tile
+constexpr int kDpThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 and 10 copies, 9 and 11 matrix instructions
 constexpr int kDpQBytes = 128 * kHeadDim * 2;
 constexpr int kDpScaleSlots = 4;
 constexpr float kDpSlack = 8.f;  // log2 by which the running maximum may lag
@@ -60,8 +60,9 @@ struct DpItem {
     int b, tile, h;            // b < 0: none
     int c0, n, L;              // of the sequence: first row, rows, length
     int split, nsplit, part;   // part `split` of `nsplit`; the part's place in the workspace
-    int item;                  // of those that are split: its number
 };
+constexpr int kDpInfo = 3;     // items published ahead
+constexpr int kDpClaim = 4;    // key tiles before the end of an item's copies at which the next one is taken
 
 enum DpForm { kDpBf16 = 0, kDpInt = 1, kDpF16 = 2 };  // bf16 caches; int8: bf16 integers with scales; int8: f16 copy
 
@@ -87,12 +88,15 @@ struct __align__(1024) DpSmem {
     // phases would belong to either, and a wait that skipped one could not tell by parity that it had).
     uint64_t full[2][Cfg::kStages], empty[Cfg::kStages];
     uint64_t sc_full[kDpScaleSlots], sc_empty[kDpScaleSlots];
-    uint64_t q_full, q_turned[2], v_last;  // q_turned: a stage's queries converted (f16 form)
+    uint64_t v_last[Cfg::kStages];       // a last value tile has landed, before its tail is zeroed
+    uint64_t q_full, q_turned[2], q_empty;  // q_turned: a stage's queries converted (f16 form)
     uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
     uint32_t tmem;
     int32_t scan[kDpThreads / 32];
     float scan_keys[kDpThreads / 32];
-    DpItem found;
+    DpItem info[kDpInfo];  // the CTA's next items, published by warp 10
+    uint64_t info_full[kDpInfo], info_empty[kDpInfo];
+    uint64_t item_done;  // both issuers are through with an item
     float2 other_ml[128];  // drafted windows: maxima and sums of the second stream
 };
 static_assert(sizeof(DpSmem<1, kDpBf16>) + 1024 <= 227 * 1024, "prompt attention exceeds 227 KB of shared memory");
@@ -158,6 +162,16 @@ __device__ __forceinline__ float dp_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A barrier of the 256 softmax threads that returns the AND of p.
+__device__ __forceinline__ bool dp_sync_and(bool p) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred q, o;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.and.pred o, 1, 256, q;\n\t"
+                 "selp.u32 %0, 1, 0, o;\n\t}"
+                 : "=r"(r)
+                 : "r"(static_cast<uint32_t>(p))
+                 : "memory");
+    return r != 0;
+}
 __device__ __forceinline__ void dp_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(dst)),
@@ -204,27 +218,29 @@ __device__ __forceinline__ int dp_split(int rest, int places, float tiles, int m
     return static_cast<int>(__reduce_min_sync(0xffffffffu, mine) & 31u) + 1;
 }
 
-// The block finds its item: all sequences' tiles counted by a block-wide scan, the longest first (the last tile of a
-// sequence has the most keys).  Whole waves of items go whole; those of the last wave may be split.  Ends with every
-// thread holding the same answer.
+// The launch's items: all sequences' tiles counted by the block.  Whole waves of items go whole; those of the last wave
+// may be split.
+struct DpPlan {
+    int total, all, whole, nsplit;  // tiles; items; items that go whole; parts of the others
+    int before, mine;               // up to 32 sequences: of sequence `lane`, the tiles before it and its own
+    DpItem seq;                     // and its metadata
+};
 template <bool kAlt, int kThreads>
-__device__ DpItem dp_find(const DenseArgs& a, int items, int32_t* scan, float* scan_keys, DpItem* found) {
+__device__ DpPlan dp_plan(const DenseArgs& a, int items, int32_t* scan, float* scan_keys) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // up to 32 sequences every warp finds it by itself, a lane a sequence
-    const bool few = a.num_seqs <= 32;
+    const bool few = a.num_seqs <= 32;  // every warp counts by itself, a lane a sequence
     const int per = (a.num_seqs + kThreads - 1) / kThreads, at = few ? lane : tid;
     const int b0 = min(at * per, a.num_seqs), b1 = min(b0 + per, a.num_seqs);
-    int mine = 0;
+    DpPlan p{};
     float keys = 0.f;
-    DpItem it{};
     for (int b = b0; b < b1; ++b) {
         bool bad;
         float k;
-        mine += dp_tiles<kAlt>(a, b, it, k, bad);
+        p.mine += dp_tiles<kAlt>(a, b, p.seq, k, bad);
         keys += k;
         if (bad && blockIdx.x == 0) atomicOr(a.err, kErrBadMetadata);
     }
-    int incl = mine;
+    int incl = p.mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -232,69 +248,75 @@ __device__ DpItem dp_find(const DenseArgs& a, int items, int32_t* scan, float* s
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
-    int before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
+    p.before = incl - p.mine;
+    p.total = __shfl_sync(0xffffffffu, incl, 31);
     if (!few) {
         if (lane == 31) scan[warp] = incl;
         if (lane == 0) scan_keys[warp] = keys;
-        if (tid == 0) found->b = -1;
         __syncthreads();
-        total = 0;
+        p.total = 0;
         keys = 0.f;
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += scan[w];
-            total += scan[w];
+            if (w < warp) p.before += scan[w];
+            p.total += scan[w];
             keys += scan_keys[w];
         }
-    }
-    // more tiles than the host's row counts allow for: the first of them go without
-    if (total > items && blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrBadMetadata);
-    total = min(total, items);
-    const int all = total * a.H, whole = all / a.places * a.places, rest = all - whole;
-    const int nsplit = dp_split(rest, a.places, total > 0 ? keys / total : 0.f, a.parts_most);
-    const int g = blockIdx.x, r = g - whole;
-    if (g == 0 && tid == 0) *a.split_head = make_int2(nsplit > 1 ? rest : 0, nsplit);
-    const int item = r < 0 ? g : whole + r / nsplit;
-    int want = total - 1 - item / a.H - before;
-    const bool here = item < all && want >= 0 && want < mine;  // one thread (few: one lane of each warp)
-    if (here) {
+        // the tiles before each sequence, for the search (every CTA writes the same)
+        int before = p.before;
         for (int b = b0; b < b1; ++b) {
             bool bad;
             float k;
-            const int t = dp_tiles<kAlt>(a, b, it, k, bad);
-            if (want < t) {
-                it.b = b;
-                it.tile = want;
-                it.h = item % a.H;
-                it.nsplit = r < 0 ? 1 : nsplit;
-                it.split = r < 0 ? 0 : r % nsplit;
-                it.part = r;
-                it.item = item - whole;
-                if (!few) *found = it;
-                if (it.nsplit > 1 && it.split == 0) a.split_items[it.item] = make_int4(b, want, it.h, 0);
-                break;
-            }
-            want -= t;
+            DpItem it;
+            a.tile_prefix[b] = before;
+            before += dp_tiles<kAlt>(a, b, it, k, bad);
         }
     }
-    if (few) {
-        const uint32_t who = __ballot_sync(0xffffffffu, here);
-        const int from = who ? __ffs(who) - 1 : 0;
-        DpItem x;
-        x.b = who ? __shfl_sync(0xffffffffu, it.b, from) : -1;
-        x.tile = __shfl_sync(0xffffffffu, it.tile, from);
-        x.h = __shfl_sync(0xffffffffu, it.h, from);
-        x.c0 = __shfl_sync(0xffffffffu, it.c0, from);
-        x.n = __shfl_sync(0xffffffffu, it.n, from);
-        x.L = __shfl_sync(0xffffffffu, it.L, from);
-        x.split = __shfl_sync(0xffffffffu, it.split, from);
-        x.nsplit = __shfl_sync(0xffffffffu, it.nsplit, from);
-        x.part = __shfl_sync(0xffffffffu, it.part, from);
-        x.item = __shfl_sync(0xffffffffu, it.item, from);
-        __syncthreads();
-        return x;
+    // more tiles than the host's row counts allow for: the first of them go without
+    if (p.total > items && blockIdx.x == 0 && tid == 0) atomicOr(a.err, kErrBadMetadata);
+    p.all = min(p.total, items) * a.H;
+    p.whole = p.all / a.places * a.places;
+    const int rest = p.all - p.whole;
+    p.nsplit = dp_split(rest, a.places, p.total > 0 ? keys / p.total : 0.f, a.parts_most);
+    if (blockIdx.x == 0 && tid == 0) *a.split_head = make_int2(p.nsplit > 1 ? rest : 0, p.nsplit);
+    return p;
+}
+
+// Work g of the launch (a whole warp): its item, the longest first (the last tile of a sequence has the most keys).
+__device__ DpItem dp_find(const DenseArgs& a, const DpPlan& p, int g) {
+    const int lane = threadIdx.x & 31, r = g - p.whole;
+    DpItem x{};
+    x.b = -1;
+    const int item = r < 0 ? g : p.whole + r / p.nsplit;
+    if (item >= p.all) return x;
+    const int want = p.total - 1 - item / a.H;
+    if (a.num_seqs <= 32) {
+        const uint32_t who = __ballot_sync(0xffffffffu, want >= p.before && want < p.before + p.mine);
+        const int from = __ffs(who) - 1;
+        x.b = from;
+        x.tile = want - __shfl_sync(0xffffffffu, p.before, from);
+        x.c0 = __shfl_sync(0xffffffffu, p.seq.c0, from);
+        x.n = __shfl_sync(0xffffffffu, p.seq.n, from);
+        x.L = __shfl_sync(0xffffffffu, p.seq.L, from);
+    } else {
+        int lo = 0, hi = a.num_seqs;  // largest b with tile_prefix[b] <= want, 32 candidates at a time
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.tile_prefix[at] <= want);
+            lo += (31 - __clz(le)) * step;
+            hi = min(lo + step, hi);
+        }
+        x.b = lo;
+        x.tile = want - a.tile_prefix[lo];
+        x.c0 = a.cu_rows[lo];
+        x.n = a.cu_rows[lo + 1] - x.c0;
+        x.L = a.cache_lens[lo];
     }
-    __syncthreads();
-    return *found;
+    x.h = item % a.H;
+    x.nsplit = r < 0 ? 1 : p.nsplit;
+    x.split = r < 0 ? 0 : r % p.nsplit;
+    x.part = r;
+    if (x.nsplit > 1 && x.split == 0 && lane == 0) a.split_items[item - p.whole] = make_int4(x.b, x.tile, x.h, 0);
+    return x;
 }
 
 // What an item covers.
@@ -412,16 +434,22 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be scheduled: it waits for this grid
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.full[0][s], 1);
-            mbar_init(&sm.full[1][s], 1);
+            mbar_init(&sm.full[0][s], 2);  // two warps copy a half each
+            mbar_init(&sm.full[1][s], 2);
+            mbar_init(&sm.v_last[s], 2);
             mbar_init(&sm.empty[s], kAlt ? 1 : 2);  // the stages' issuers (one with fewer tiles lets the others pass)
         }
         for (int s = 0; s < kDpScaleSlots; ++s) {
             mbar_init(&sm.sc_full[s], 1);
             mbar_init(&sm.sc_empty[s], 8);
         }
+        for (int s = 0; s < kDpInfo; ++s) {
+            mbar_init(&sm.info_full[s], 1);
+            mbar_init(&sm.info_empty[s], 11);  // copies, two issuers, eight softmax warps
+        }
         mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.v_last, 1);
+        mbar_init(&sm.q_empty, kAlt ? 6 : 2);  // two issuers; kAlt: and group 0, whose epilogue uses the query buffers
+        mbar_init(&sm.item_done, 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.q_turned[s], 4);
             mbar_init(&sm.s_full[s], 1);
@@ -436,114 +464,185 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &q_map : (lane == 1 ? &k_map : &v_map));
     if (warp == 9) tmem_alloc(&sm.tmem, 512);
     tc_fence_before();
-    const DpItem item = dp_find<kAlt, kDpThreads>(a, items, sm.scan, sm.scan_keys, &sm.found);  // (with block barriers)
+    const DpPlan plan = dp_plan<kAlt, kDpThreads>(a, items, sm.scan, sm.scan_keys);
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    if (item.b < 0) {
-        __syncthreads();
-        if (warp == 9) tmem_dealloc(tmem, 512);
-        return;
-    }
-    const int h = item.h;
-    const DpWork w = dp_work<kAlt, NK>(a, item);
-    // the value tile that holds the end of the sequence, if its last rows are nobody's
-    const int v_end = w.L / NK;
-    const bool fix = w.L % NK != 0 && v_end >= w.first && v_end < w.first + w.total;
 
-    auto full_index = [&](int j, int kind) { return kAlt ? 2 * (j >> 1) + kind : 2 * j + kind; };  // of tile j's K (0) or V (1)
-    auto full_bar = [&](int j, int kind) { return &sm.full[kAlt ? j & 1 : 0][full_index(j, kind) % kStages]; };
+    // Every role walks the CTA's items with its own copy of each and with counts that run on over them: copies (ring slots),
+    // a stage's copies (alternate tiles), a stage's tiles, items.
+    auto next_item = [&](int k, DpItem& x) {  // item k of the CTA, false where it never came
+        if (!mbar_wait(&sm.info_full[k % kDpInfo], (k / kDpInfo) & 1, a.err)) return false;
+        x = sm.info[k % kDpInfo];
+        return true;
+    };
+    // the value tile that holds the end of the sequence, if its last rows are nobody's
+    auto last_tile = [&](const DpWork& w) {
+        const int v_end = w.L / NK;
+        return w.L % NK != 0 && v_end >= w.first && v_end < w.first + w.total ? v_end - w.first : -1;
+    };
+    // tile j's K (0) or V (1) among the copies of an item (alternate tiles: of its stage)
+    auto copy_index = [&](int j, int kind) { return kAlt ? 2 * (j >> 1) + kind : 2 * j + kind; };
+    auto full_bar = [&](int j, int n) { return &sm.full[kAlt ? j & 1 : 0][n % kStages]; };  // n: running copy index
+    // ring slots of an item's key tile j: K0 V0 K1 V1 ..., or (alternate tiles) K0 K1 V0 K2 V1 ...
+    auto slot_k = [&](int j) { return kAlt ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
+    auto slot_v = [&](const DpWork& w, int j) { return kAlt ? (j + 1 < w.total ? 2 * j + 2 : 2 * j + 1) : 2 * j + 1; };
 
     if (warp >= 8) {
         if constexpr (kParts == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 8) {
-            // ---------------- copies: queries, then K and V tiles in the order the matrix instructions take them
-            if (lane == 0) {
-                const int tiles = kAlt ? 1 : (w.count[1] > 0 ? 2 : 1);
-                mbar_arrive_expect_tx(&sm.q_full, tiles * 2 * w.P * a.G * 128);
-                for (int s = 0; s < tiles; ++s)
-                    for (int half = 0; half < 2; ++half)
-                        tma_load_3d(sm.q[s] + half * (kDpQBytes / 2), &q_map, &sm.q_full, 64 * half, h * a.G,
-                                    w.c0 + w.i0 + s * w.P);
-            }
-            int64_t row = 0;
-            int slot = 0, sent[2] = {0, 0};  // copies so far, and by barrier row
+        if (warp == 8 || warp == 10) {
+            // ---------------- copies: K and V tiles in the order the matrix instructions take them, dimensions 0-63 by warp 8
+            // (and the queries and scales), 64-127 by warp 10 (and items and last value tiles)
+            const int half = warp == 10;
+            int slot = 0, sent[2] = {0, 0}, tiles_before = 0, queries = 0;  // copies so far, by barrier row; key tiles; items
+            uint32_t fixed = 0;  // last value tiles, a bit a ring slot: how often modulo 2
             bool alive = true;
-            // a copy step i loads K tile i (if any) and V tile i - lag: the order K0 V0 K1 V1 ... (two stages a tile) or
-            // K0 K1 V0 K2 V1 ... (alternate tiles)
-            constexpr int kLag = kAlt ? 1 : 0;
-            constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
-            int64_t row_before = 0;                     // the previous batch's (a V tile may still need its last one)
-            for (int i = 0; i < w.total + kLag && alive; ++i) {
-                if (i % kBatch == 0) {
-                    row_before = row;
-                    const int64_t t = (static_cast<int64_t>(w.first) + i) * NK + lane * kBlock;
-                    row = a.cache_tokens;  // past the length: a box past the cache is zeros
-                    if (t < w.L && t < static_cast<int64_t>(w.first + w.total) * NK) {
-                        row = block_row(a.cache, w.b, t);
-                        if (row < 0) {  // page outside the pool
-                            atomicOr(a.err, kErrBadMetadata);
-                            row = a.cache_tokens;
-                        }
+            DpItem item, after;
+            auto publish = [&](int n, const DpItem& x) {  // item n of the CTA
+                int ok = 1;
+                if (lane == 0) {
+                    const int at = n % kDpInfo;
+                    if (n >= kDpInfo) ok = mbar_wait(&sm.info_empty[at], ((n / kDpInfo) - 1) & 1, a.err);
+                    if (ok) {
+                        sm.info[at] = x;
+                        mbar_arrive(&sm.info_full[at]);
                     }
                 }
-#pragma unroll
-                for (int kind = 0; kind < 2; ++kind) {  // K, V
-                    const int j = kind == 0 ? i : i - kLag;
-                    if (j < 0 || j >= w.total) continue;
-                    const int st = slot % kStages;
+                return __shfl_sync(0xffffffffu, ok, 0) != 0;
+            };
+            if (half) {
+                after = dp_find(a, plan, blockIdx.x);
+                alive = publish(0, after);
+            }
+            for (int k = 0; alive; ++k) {
+                if (half) {
+                    item = after;
+                } else {
+                    alive = __all_sync(0xffffffffu, next_item(k, item));
+                    if (!alive) break;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.info_empty[k % kDpInfo]);
+                }
+                if (item.b < 0) break;
+                const DpWork w = dp_work<kAlt, NK>(a, item);
+                const int h = item.h, fix = last_tile(w);
+                if (!half) {
                     int ok = 1;
-                    if (lane == 0 && slot >= kStages) ok = mbar_wait(&sm.empty[st], ((slot / kStages) - 1) & 1, a.err);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) {
-                        alive = false;
-                        break;
-                    }
-                    const bool old = kind == 1 && kLag == 1 && i % kBatch == 0;
-                    int64_t r[NK / kBlock];
-#pragma unroll
-                    for (int c = 0; c < NK / kBlock; ++c)
-                        r[c] = __shfl_sync(0xffffffffu, old ? row_before : row, (j % kBatch) * (NK / kBlock) + c);
                     if (lane == 0) {
-                        // the last value tile completes a barrier of its own: warp 10 zeroes its tail and passes it on
-                        uint64_t* bar = kind == 1 && fix && w.first + j == v_end ? &sm.v_last : full_bar(j, kind);
-                        mbar_arrive_expect_tx(bar, Cfg::kTile);
-#pragma unroll
-                        for (int c = 0; c < NK / kBlock; ++c)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half)
-                                tma_load_3d(sm.ring[st] + half * kHalf + c * (kBlock * 128), kind == 0 ? &k_map : &v_map, bar,
-                                            64 * half, h, static_cast<int>(r[c]));
-                        if (kWide && kind == 0) {  // the tile's scales
-                            const int e = j % kDpScaleSlots;
-                            if (j >= kDpScaleSlots && !mbar_wait(&sm.sc_empty[e], ((j / kDpScaleSlots) - 1) & 1, a.err)) ok = 0;
-                            if (ok) {
-                                const int64_t from = static_cast<int64_t>(h) * a.cache_tokens + a.cache.starts[w.b] +
-                                                     static_cast<int64_t>(w.first + j) * NK;
-                                mbar_arrive_expect_tx(&sm.sc_full[e], 2 * NK * 4);
-                                dp_bulk(sm.sc[e][0], a.k_scale + from, NK * 4, &sm.sc_full[e]);
-                                dp_bulk(sm.sc[e][1], a.v_scale + from, NK * 4, &sm.sc_full[e]);
+                        if (k > 0) ok = mbar_wait(&sm.q_full, (k - 1) & 1, a.err) && mbar_wait(&sm.q_empty, (k - 1) & 1, a.err);
+                        if (ok) {
+                            const int tiles = kAlt ? 1 : (w.i0 + w.P < w.n ? 2 : 1);
+                            mbar_arrive_expect_tx(&sm.q_full, tiles * 2 * w.P * a.G * 128);
+                            for (int s = 0; s < tiles; ++s)
+                                for (int c = 0; c < 2; ++c)
+                                    tma_load_3d(sm.q[s] + c * (kDpQBytes / 2), &q_map, &sm.q_full, 64 * c, h * a.G, w.c0 + w.i0 + s * w.P);
+                            ++queries;
+                        }
+                    }
+                    alive = __shfl_sync(0xffffffffu, ok, 0) != 0;
+                }
+                const int sent0[2] = {sent[0], sent[1]};
+                int64_t row = 0;
+                // a copy step i loads K tile i (if any) and V tile i - lag: the order K0 V0 K1 V1 ... (two stages a tile) or
+                // K0 K1 V0 K2 V1 ... (alternate tiles)
+                constexpr int kLag = kAlt ? 1 : 0;
+                constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
+                int64_t row_before = 0;                     // the previous batch's (a V tile may still need its last one)
+                const int claim_at = max(0, w.total - kDpClaim);
+                for (int i = 0; alive && (i < w.total + kLag || i == 0); ++i) {
+                    if (half && i == claim_at) {  // which CTA has which item is left to their timing, what an item holds is not
+                        int g = 0;
+                        if (lane == 0) g = gridDim.x + atomicAdd(a.next_item, 1u);
+                        after = dp_find(a, plan, __shfl_sync(0xffffffffu, g, 0));
+                        alive = publish(k + 1, after);
+                        if (!alive) break;
+                    }
+                    if (w.total == 0) break;
+                    if (i % kBatch == 0) {
+                        row_before = row;
+                        const int64_t t = (static_cast<int64_t>(w.first) + i) * NK + lane * kBlock;
+                        row = a.cache_tokens;  // past the length: a box past the cache is zeros
+                        if (t < w.L && t < static_cast<int64_t>(w.first + w.total) * NK) {
+                            row = block_row(a.cache, w.b, t);
+                            if (row < 0) {  // page outside the pool
+                                atomicOr(a.err, kErrBadMetadata);
+                                row = a.cache_tokens;
                             }
                         }
                     }
-                    ++slot;
-                    if (kAlt && (j & 1)) ++sent[1];
-                    else ++sent[0];
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) {
-                        alive = false;
-                        break;
+#pragma unroll
+                    for (int kind = 0; kind < 2; ++kind) {  // K, V
+                        const int j = kind == 0 ? i : i - kLag;
+                        if (j < 0 || j >= w.total) continue;
+                        const int st = slot % kStages;
+                        const bool old = kind == 1 && kLag == 1 && i % kBatch == 0;
+                        int64_t r[NK / kBlock];
+#pragma unroll
+                        for (int c = 0; c < NK / kBlock; ++c)
+                            r[c] = __shfl_sync(0xffffffffu, old ? row_before : row, (j % kBatch) * (NK / kBlock) + c);
+                        int ok = 1;
+                        if (lane == 0) {
+                            // the last value tile completes a barrier of its own: warp 10 zeroes its tail and passes it on
+                            const int odd = kAlt ? j & 1 : 0;
+                            uint64_t* bar = kind == 1 && j == fix ? &sm.v_last[st]
+                                                                  : full_bar(j, (odd ? sent0[1] : sent0[0]) + copy_index(j, kind));
+                            uint8_t* dst = sm.ring[st] + half * kHalf;
+                            if (slot >= kStages) ok = mbar_wait(&sm.empty[st], ((slot / kStages) - 1) & 1, a.err);
+                            if (ok) {
+                                mbar_arrive_expect_tx(bar, Cfg::kTile / 2);
+#pragma unroll
+                                for (int c = 0; c < NK / kBlock; ++c)
+                                    tma_load_3d(dst + c * (kBlock * 128), kind == 0 ? &k_map : &v_map, bar, 64 * half, h, static_cast<int>(r[c]));
+                                if (kWide && kind == 0 && !half) {  // the tile's scales
+                                    const int jt = tiles_before + j, e = jt % kDpScaleSlots;
+                                    if (jt >= kDpScaleSlots) ok = mbar_wait(&sm.sc_empty[e], ((jt / kDpScaleSlots) - 1) & 1, a.err);
+                                    if (ok) {
+                                        const int64_t from = static_cast<int64_t>(h) * a.cache_tokens + a.cache.starts[w.b] +
+                                                             static_cast<int64_t>(w.first + j) * NK;
+                                        mbar_arrive_expect_tx(&sm.sc_full[e], 2 * NK * 4);
+                                        dp_bulk(sm.sc[e][0], a.k_scale + from, NK * 4, &sm.sc_full[e]);
+                                        dp_bulk(sm.sc[e][1], a.v_scale + from, NK * 4, &sm.sc_full[e]);
+                                    }
+                                }
+                            }
+                        }
+                        ++slot;
+                        if (kAlt && (j & 1)) ++sent[1];
+                        else ++sent[0];
+                        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                            alive = false;
+                            break;
+                        }
                     }
                 }
+                if (half && fix >= 0 && alive) {  // ---- the last value tile: rows past the length become zero
+                    const int st = (2 * tiles_before + slot_v(w, fix)) % kStages;
+                    alive = __all_sync(0xffffffffu, mbar_wait(&sm.v_last[st], fixed >> st & 1, a.err));
+                    if (!alive) break;
+                    fixed ^= 1u << st;
+                    for (int x = (w.L % NK) * 16 + lane; x < NK * 16; x += 32) {
+                        const int key = x >> 4, c = x & 15;  // 16-byte chunk c & 7 of half c >> 3 (a whole row: no swizzle to undo)
+                        *reinterpret_cast<uint4*>(sm.ring[st] + (c >> 3) * kHalf + key * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        uint64_t* bar = full_bar(fix, sent0[kAlt ? fix & 1 : 0] + copy_index(fix, 1));
+                        mbar_arrive(bar);
+                        mbar_arrive(bar);
+                    }
+                }
+                tiles_before += w.total;
             }
-            if (lane == 0) {  // no copy in flight at the end (the last value tile's barrier is warp 10's to wait for)
-                mbar_wait(&sm.q_full, 0, a.err);
+            if (lane == 0 && !half) {  // no copy in flight at the end (a last value tile's barrier was warp 10's to wait for)
+                if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, a.err);
                 for (int s = 0; s < (kAlt ? 2 : 1); ++s)
                     for (int b = 0; b < kStages && b < sent[s]; ++b)
                         mbar_wait(&sm.full[s][b], ((sent[s] - 1 - b) / kStages) & 1, a.err);
                 if (kWide && alive)
-                    for (int e = 0; e < kDpScaleSlots && e < w.total; ++e)
-                        mbar_wait(&sm.sc_full[e], ((w.total - 1 - e) / kDpScaleSlots) & 1, a.err);
+                    for (int e = 0; e < kDpScaleSlots && e < tiles_before; ++e)
+                        mbar_wait(&sm.sc_full[e], ((tiles_before - 1 - e) / kDpScaleSlots) & 1, a.err);
             }
         } else if (warp == 9 || warp == 11) {
             // ---------------- matrix instructions of stage s, one thread
@@ -554,91 +653,114 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 const uint64_t qd = smem_desc_sw128(smem_u32(sm.q[kAlt ? 0 : s]), 16, 1024);
                 const uint64_t kd = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
                 const uint64_t vd = smem_desc_sw128(smem_u32(sm.ring[0]), kHalf, 1024);
-                // ring slots of key tile j: K0 V0 K1 V1 ..., or (alternate tiles) K0 K1 V0 K2 V1 ...
-                auto slot_k = [&](int j) { return kAlt ? (j == 0 ? 0 : 2 * j - 1) : 2 * j; };
-                auto slot_v = [&](int j) { return kAlt ? (j + 1 < w.total ? 2 * j + 2 : 2 * j + 1) : 2 * j + 1; };
-                auto landed = [&](int j, int kind) { return mbar_wait(full_bar(j, kind), (full_index(j, kind) / kStages) & 1, a.err); };
-                // S_s = Q_s K^T; `pass`: the other stage's turn begins while the last of them run
-                auto scores = [&](int slot, bool pass) {
-                    const uint64_t kb = kd + static_cast<uint64_t>((slot % kStages) * (Cfg::kTile >> 4));
+                constexpr int kStep = kAlt ? 2 : 1;
+                const int j0 = kAlt ? s : 0;
+                // running: ring slots, tiles of the stage, turns taken, the next copy's barrier and its phase
+                int slots = 0, tiles = 0, turns = 0, bar = 0;
+                uint32_t bar_phase = 0;
+                auto landed = [&]() { return mbar_wait(&sm.full[kAlt ? s : 0][bar], bar_phase, a.err); };
+                auto pass_copy = [&]() {
+                    if (++bar == kStages) {
+                        bar = 0;
+                        bar_phase ^= 1;
+                    }
+                };
+                bool ok = true, issued = false;
+                for (int k = 0; ok; ++k) {
+                DpItem item;
+                ok = next_item(k, item);
+                if (!ok) break;
+                mbar_arrive(&sm.info_empty[k % kDpInfo]);
+                if (item.b < 0) break;
+                const DpWork w = dp_work<kAlt, NK>(a, item);
+                const int count = s == 0 ? w.count[0] : w.count[1], others = s == 0 ? w.count[1] : w.count[0];
+                // S_s = Q_s K^T from ring slot st; `pass`: the other stage's turn begins while the last of them run
+                auto scores = [&](int st, bool last, bool pass) {
+                    const uint64_t kb = kd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        tc_mma_ss(tmem + s * 128 + kSAt, qd + static_cast<uint64_t>(((k >> 2) * (kDpQBytes / 2) + (k & 3) * 32) >> 4),
-                                  kb + static_cast<uint64_t>(((k >> 2) * kHalf + (k & 3) * 32) >> 4), idesc_s, k > 0);
-                        if (k == 5 && pass) mbar_arrive(&sm.turn[s ^ 1]);
+                    for (int i = 0; i < 8; ++i) {
+                        tc_mma_ss(tmem + s * 128 + kSAt, qd + static_cast<uint64_t>(((i >> 2) * (kDpQBytes / 2) + (i & 3) * 32) >> 4),
+                                  kb + static_cast<uint64_t>(((i >> 2) * kHalf + (i & 3) * 32) >> 4), idesc_s, i > 0);
+                        if (i == 5 && pass) mbar_arrive(&sm.turn[s ^ 1]);
                     }
                     tc_commit(&sm.s_full[s]);
+                    if (!kAlt && last) tc_commit(&sm.q_empty);  // the last products with this item's queries
+                    tc_commit(&sm.empty[st]);
                 };
-                constexpr int kStep = kAlt ? 2 : 1;
-                const int j0 = kAlt ? s : 0, count = w.count[s], others = w.count[s ^ 1];
-                bool ok = count == 0 || (mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, 0, a.err) && landed(j0, 0));
-                const bool issued = ok && count > 0;
-                tc_fence_after();
-                if (issued) {
-                    scores(slot_k(j0), false);
-                    tc_commit(&sm.empty[slot_k(j0) % kStages]);
+                // (waited for without tiles too: a barrier's phases have to be seen one by one, and the stage's group may
+                // be converting the queries)
+                ok = mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, k & 1, a.err);
+                if (!ok) break;
+                if constexpr (kAlt) mbar_arrive(&sm.q_empty);  // (seen; group 0 arrives when the products are done)
+                if (count > 0) {
+                    ok = landed();
+                    if (!ok) break;
+                    issued = true;
+                    tc_fence_after();
+                    scores(kAlt ? (slots + slot_k(j0)) % kStages : bar, count == 1, false);
+                    pass_copy();
+                } else if (!kAlt) {
+                    mbar_arrive(&sm.q_empty);
                 }
+                // the other stage is through with its last item: its turns have been taken
+                if (k > 0) ok = mbar_wait(&sm.item_done, (k - 1) & 1, a.err);
                 for (int c = 0; ok && c < count; ++c) {
                     // the stages take turns: values of tile c, scores of the next (whatever can be waited for is, first)
                     const int j = j0 + kStep * c;
+                    const uint32_t phase = (tiles + c) & 1;
                     const bool next = c + 1 < count;
-                    ok = landed(j, 1) && (!next || landed(j + kStep, 0)) && mbar_wait(&sm.p_full[s][0], c & 1, a.err);
-                    if (ok && (s == 0 ? c > 0 && c <= others : c < others)) ok = mbar_wait(&sm.turn[s], (s == 0 ? c - 1 : c) & 1, a.err);
-                    if (!ok) break;
+                    ok = landed();
+                    const int st_v = kAlt ? (slots + slot_v(w, j)) % kStages : bar;
+                    pass_copy();
+                    ok = ok && (!next || landed());
+                    const int st_k = kAlt ? (slots + slot_k(j + kStep)) % kStages : bar;
+                    if (next) pass_copy();
+                    const bool turns_now = s == 0 ? c > 0 && c <= others : c < others;
                     const bool pass = s == 0 ? c < others : c + 1 < others;
-                    const uint64_t vb = vd + static_cast<uint64_t>((slot_v(j) % kStages) * (Cfg::kTile >> 4));
+                    const uint64_t vb = vd + static_cast<uint64_t>(st_v * (Cfg::kTile >> 4));
+                    ok = ok && mbar_wait(&sm.p_full[s][0], phase, a.err);
+                    if (ok && turns_now) ok = mbar_wait(&sm.turn[s], turns++ & 1, a.err);
+                    if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int h2 = 0; h2 < NK / 64; ++h2) {  // O_s += P_s V, the second 64 keys as soon as their weights are there
                         if (h2 == 1) {
-                            ok = mbar_wait(&sm.p_full[s][1], c & 1, a.err);
+                            ok = mbar_wait(&sm.p_full[s][1], phase, a.err);
                             if (!ok) break;
                             tc_fence_after();
                         }
 #pragma unroll
                         for (int part = 0; part < kParts; ++part)
 #pragma unroll
-                            for (int k = 4 * h2; k < 4 * h2 + 4; ++k)
-                                dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + k * 8,
-                                          vb + static_cast<uint64_t>(k * 2048 >> 4), idesc_o,
-                                          !((kParts > 1 ? (c & 1) == 0 : c == 0) && part == 0 && k == 0));
+                            for (int i = 4 * h2; i < 4 * h2 + 4; ++i)
+                                dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + i * 8,
+                                          vb + static_cast<uint64_t>(i * 2048 >> 4), idesc_o,
+                                          !((kParts > 1 ? (c & 1) == 0 : c == 0) && part == 0 && i == 0));
                     }
                     if (!ok) break;
                     if (next) {
-                        scores(slot_k(j + kStep), pass);
-                        tc_commit(&sm.empty[slot_k(j + kStep) % kStages]);
+                        scores(st_k, c + 2 == count, pass);
                     } else {
                         if (pass) mbar_arrive(&sm.turn[s ^ 1]);
                         tc_commit(&sm.o_full[s]);
                     }
-                    tc_commit(&sm.empty[slot_v(j) % kStages]);
+                    tc_commit(&sm.empty[st_v]);
                 }
                 if constexpr (!kAlt) {  // tiles that only the other stage needs
-                    for (int j = w.count[s]; ok && j < w.total; ++j)
-                        for (int kind = 0; ok && kind < 2; ++kind) {
-                            ok = landed(j, kind);
-                            if (ok) mbar_arrive(&sm.empty[(2 * j + kind) % kStages]);
-                        }
+                    for (int j = 2 * count; ok && j < 2 * w.total; ++j) {
+                        ok = landed();
+                        if (ok) mbar_arrive(&sm.empty[bar]);
+                        pass_copy();
+                    }
+                }
+                slots += 2 * w.total;
+                tiles += count;
+                if (ok) mbar_arrive(&sm.item_done);
                 }
                 if (issued) {  // every matrix instruction done before tensor memory is given back
                     tc_commit(&sm.drain[s]);
                     mbar_wait(&sm.drain[s], 0, a.err);
                 }
-            }
-        } else if (warp == 10 && fix) {
-            // ---------------- last value tile: rows past the length become zero
-            const int j = v_end - w.first;
-            // its ring slot: K0 V0 K1 V1 ..., or K0 K1 V0 K2 V1 ... (the last V has no K before it)
-            const int slot = kAlt ? (j + 1 < w.total ? 2 * j + 2 : 2 * j + 1) : 2 * j + 1, st = slot % kStages;
-            if (mbar_wait(&sm.v_last, 0, a.err)) {
-                const int first = w.L - v_end * NK;
-                for (int x = first * 16 + lane; x < NK * 16; x += 32) {
-                    const int key = x >> 4, c = x & 15;  // 16-byte chunk c & 7 of half c >> 3 (a whole row: no swizzle to undo)
-                    *reinterpret_cast<uint4*>(sm.ring[st] + (c >> 3) * kHalf + key * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full_bar(j, 1));
             }
         }
     } else {
@@ -647,28 +769,36 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // ---------------- softmax group s: thread = row of M tile s
         const int s = warp >> 2, m = tid & 127;
-        const int i = w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, g = m % a.G;
-        const bool mine = m < w.P * a.G && i < w.n;
-        const int pos = w.L - w.n + min(i, w.n - 1);
-        // the tile's earliest position: key tiles up to it hide nothing
-        const int early = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P), w.n - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 (warp % 4)) << 16
         const uint32_t s_addr = tmem + s * 128 + lanes, o_addr = tmem + 256 + s * 128 + lanes;
-        const int count = w.count[s];
-        float row_f = a.scale_log2;  // factor from the row's products to the log2 domain
+        int tiles = 0, tiles_before = 0, done = 0;  // running: the stage's tiles, the items' key tiles, items the stage had tiles of
         bool alive = true;
+        for (int k = 0; alive; ++k) {
+        DpItem item;
+        alive = __all_sync(0xffffffffu, next_item(k, item));
+        if constexpr (kAlt) alive = dp_sync_and(alive);  // (the groups meet in the epilogue: both come, or neither)
+        if (!alive) break;
+        if (item.b < 0) break;
+        const DpWork w = dp_work<kAlt, NK>(a, item);
+        const int h = item.h;
+        const int pos = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, w.n - 1);
+        // the tile's earliest position: key tiles up to it hide nothing
+        const int early = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P), w.n - 1);
+        const int count = s == 0 ? w.count[0] : w.count[1];
+        float row_f = a.scale_log2;  // factor from the row's products to the log2 domain
+        if constexpr (kF16 || kAlt) alive = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, k & 1, a.err));
         if constexpr (kF16) {
             // the row's queries to f16: its largest value into [2^8, 2^9)
-            if (count > 0) alive = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, 0, a.err));
+            if (!alive) break;
             uint8_t* row = sm.q[s] + m * 128;
             auto chunk = [&](int c) { return reinterpret_cast<uint4*>(row + (c >> 3) * (kDpQBytes / 2) + (((c & 7) ^ (m & 7)) << 4)); };
             uint32_t big = 0;  // largest magnitude as bits
 #pragma unroll 4
             for (int c = 0; c < 16; ++c) {
                 const uint4 v = *chunk(c);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t qw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) big = max(big, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+                for (int e = 0; e < 4; ++e) big = max(big, max((qw[e] << 16) & 0x7fff0000u, qw[e] & 0x7fff0000u));
             }
             const uint32_t ex = min(max(big >> 23, 9u), 253u);
             const float up = __uint_as_float((262u - ex) << 23);  // 2^(8 - exponent)
@@ -729,15 +859,15 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         };
         for (int c = 0; alive && c < count; ++c) {
             const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
-            alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], c & 1, a.err));
+            alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], (tiles + c) & 1, a.err));
             if (!alive) break;
             tc_fence_after();
             if (c > 0 && (c & 1) == 0) collect();
             if constexpr (kParts > 1) {  // ---- fp32 outputs: 32 scores at a time, O in registers (the code below has no room for it)
                 const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
-                const int e = j % kDpScaleSlots;
+                const int e = (tiles_before + j) % kDpScaleSlots;
                 if constexpr (kWide) {
-                    alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], (j / kDpScaleSlots) & 1, a.err));
+                    alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], ((tiles_before + j) / kDpScaleSlots) & 1, a.err));
                     if (!alive) break;
                 }
                 // the scores of keys 32 q .. of the tile in the log2 domain (f: what is left to multiply by)
@@ -934,15 +1064,25 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             sum += (add[0].x + add[0].y) * back[0] + (add[1].x + add[1].y) * back[1];
             }
         }
+        // (the item is read again here, so that the loop over its tiles need not keep it in registers)
+        {
+        const DpItem item = sm.info[k % kDpInfo];
+        const DpWork w = dp_work<kAlt, NK>(a, item);
+        const int h = item.h, count = s == 0 ? w.count[0] : w.count[1];
+        const int i = w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, g = m % a.G;
+        const bool mine = m < w.P * a.G && i < w.n;
+        const int pos = w.L - w.n + min(i, w.n - 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.info_empty[k % kDpInfo]);
         if constexpr (kWide) {  // scales of tiles that only the other group needs
-            for (int j = count; alive && j < w.total; ++j) {
+            for (int j = tiles_before + count; alive && j < tiles_before + w.total; ++j) {
                 alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[j % kDpScaleSlots], (j / kDpScaleSlots) & 1, a.err));
                 if (alive && lane == 0) mbar_arrive(&sm.sc_empty[j % kDpScaleSlots]);
             }
         }
         // ---------------- epilogue
         bool have = count > 0;
-        if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], 0, a.err));
+        if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], done++ & 1, a.err));
         tc_fence_after();
         if (alive && have) collect();
         auto row_of_o = [&](int q, float (&y)[32]) {  // 32 values of the row
@@ -957,8 +1097,10 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         float f0 = 1.f, f1 = 0.f;
         float* other = reinterpret_cast<float*>(&sm.q[0][0]);  // [128 dims][128 rows]
         if constexpr (kAlt) {
-            // the second stream's state goes through the query buffers, once both streams' products are done
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // the second stream's state goes through the query buffers, once both streams' products are done (where a wait
+            // gave up, all 256 threads stop here together)
+            alive = dp_sync_and(alive);
+            if (!alive) break;
             if (s == 1 && have && alive) {
 #pragma unroll(kParts > 1 ? 4 : 1)
                 for (int q = 0; q < kHeadDim / 32; ++q) {
@@ -969,6 +1111,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 }
             }
             if (s == 1) sm.other_ml[m] = make_float2(have ? top : -INFINITY, have ? sum : 0.f);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the next item's queries land here)
             asm volatile("bar.sync 1, 256;" ::: "memory");
             if (s == 0 && w.count[1] > 0) {
                 const float2 ml = sm.other_ml[m];
@@ -978,10 +1121,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 sum = sum * f0 + ml.y * f1;
                 top = t2;
             }
-            if (s == 1) alive = false;  // group 0 writes
         }
         const bool split_up = item.nsplit > 1;
-        if (alive && (have || split_up)) {
+        if (alive && (have || split_up) && !(kAlt && s == 1)) {  // (kAlt: group 0 writes)
             constexpr int kRows = kAlt ? 128 : 256;  // rows of an item's part
             const int64_t q_row = (static_cast<int64_t>(w.c0 + min(i, w.n - 1)) * a.H + h) * a.G + g;
             const int64_t part_row = static_cast<int64_t>(item.part) * kRows + s * 128 + m;
@@ -1013,11 +1155,10 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
 #pragma unroll
                         for (int k = 0; k < 8; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
                     } else if (a.out_bf16) {
-                        // through the stage's query buffer (its products are done), so that whole rows leave together
                         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_row * kHeadDim + 32 * q);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            *(kAlt ? dst + k : reinterpret_cast<uint4*>(sm.q[s] + m * 256 + (((4 * q + k) ^ (m & 15)) << 4))) = make_uint4(pack_bf16x2(y[8 * k] * inv, y[8 * k + 1] * inv),
+                            dst[k] = make_uint4(pack_bf16x2(y[8 * k] * inv, y[8 * k + 1] * inv),
                                                 pack_bf16x2(y[8 * k + 2] * inv, y[8 * k + 3] * inv),
                                                 pack_bf16x2(y[8 * k + 4] * inv, y[8 * k + 5] * inv),
                                                 pack_bf16x2(y[8 * k + 6] * inv, y[8 * k + 7] * inv));
@@ -1029,19 +1170,6 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     }
                     __syncwarp();  // the next load is the whole warp's
                 }
-            }
-            if (!kAlt && have && !split_up && a.out_bf16) {  // two rows at a time, 16 bytes a lane
-                __syncwarp();
-                const uint32_t rows = __ballot_sync(0xffffffffu, mine);
-#pragma unroll 4
-                for (int r = 0; r < 32; r += 2) {
-                    const int from = r + (lane >> 4), row = (warp & 3) * 32 + from;
-                    const int64_t to = __shfl_sync(0xffffffffu, q_row, from);
-                    if ((rows >> from) & 1u)
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to * kHeadDim + 8 * (lane & 15)) =
-                            *reinterpret_cast<const uint4*>(sm.q[s] + row * 256 + (((lane & 15) ^ (row & 15)) << 4));
-                }
-                __syncwarp();
             }
             if (split_up && mine) *reinterpret_cast<float2*>(a.part_ml + part_row * 2) = make_float2(top, sum);
             // f16 form: a row that lives on blocks whose values are tiny beside another block's (even one that it does
@@ -1072,6 +1200,18 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     }
                 }
             }
+        }
+        if constexpr (kAlt) {
+            if (s == 0) {  // the query buffers are free again
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_empty);
+            }
+        }
+        tc_fence_before();
+        tiles += count;
+        tiles_before += w.total;
+        }
         }
     }
     tc_fence_before();
@@ -1166,7 +1306,7 @@ static cudaError_t launch_dense_prompt(DenseArgs a, int items, cudaStream_t stre
     } else if (tiles >= 8.f) {
         a.parts_most = 2 * a.places;
     }
-    const int64_t grid = whole + a.parts_most;
+    const int64_t grid = std::min<int64_t>(whole + a.parts_most, a.places);
     kernel<<<static_cast<unsigned>(grid), kDpThreads, smem, stream>>>(*a.q_map, *a.k_map, *a.v_map, a, items);
     if ((e = cudaGetLastError()) != cudaSuccess || a.parts_most == 0) return e;
     cudaLaunchConfig_t cfg = {};

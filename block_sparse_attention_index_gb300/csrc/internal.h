@@ -223,6 +223,8 @@ struct DenseArgs {
     const float2* wide_fac;    // int8 prompts, bf16 outputs: factors of the f16 copy's blocks, [H, cache_tokens / 64]
     int places;            // prompts, windows: SMs
     int parts_most;        // parts of split items that there is room for
+    uint32_t* next_item;   // prompts, windows: items taken beyond each CTA's first, cleared before the launch
+    int32_t* tile_prefix;  // prompts, windows: [num_seqs] tiles before each sequence (more than 32 sequences)
     int2* split_head;      // prompts, windows: items that are split over their keys, parts of each
     int4* split_items;     // [places] those items
     int pairs_most;        // decode family: most (row, head) pairs of a sequence that its kernel takes

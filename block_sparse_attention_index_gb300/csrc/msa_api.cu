@@ -964,6 +964,7 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.k_map = &km;
     a.v_map = &vm;
     a.unit_prefix = reinterpret_cast<int32_t*>(ws + l.unit_prefix);
+    a.tile_prefix = a.unit_prefix;  // (the kernels follow one another)
     a.split_head = reinterpret_cast<int2*>(ws + l.split);
     a.split_items = reinterpret_cast<int4*>(ws + l.split) + 1;
     a.part_o = reinterpret_cast<float*>(ws + l.part_o);
@@ -992,9 +993,10 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.cache_tokens = a.seq_cache_tokens = p->cache_tokens;
     a.scale_log2 = scale_log2(p);
     a.err = reinterpret_cast<uint32_t*>(ws + l.err);
-    // the decode family's combine stores the error word; before any other kernel it is cleared
+    // the decode family's combine stores the error word; before any other kernel it is cleared, and with it the counts of
+    // items taken by windows (word 1) and prompts (word 2)
     a.err_store = d.stream && !d.prompts && !d.windows;
-    if (!a.err_store && (e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    if (!a.err_store && (e = cudaMemsetAsync(ws, 0, 3 * sizeof(uint32_t), st)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
     if (d.stream) {
         const int64_t seqs = p->num_decode_seqs > 0 ? p->num_decode_seqs : p->num_seqs;
         const int64_t tiles = d.windows ? 1 : (static_cast<int64_t>(decode_rows_per_seq(p)) * p->group_size + 15) / 16;
@@ -1002,8 +1004,10 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
         if ((e = msa::run_dense_decode(a, msa::dense_decode_shares(seqs * tiles * blocks, p->num_kv_heads), st)) != cudaSuccess)
             return cuda_fail(e, "dense decode attention launch");
     }
+    a.next_item = a.err + 1;
     if (d.windows && (e = msa::run_dense_window(a, static_cast<int>(d.window_items), st)) != cudaSuccess)
         return cuda_fail(e, "dense window attention launch");
+    a.next_item = a.err + 2;
     if (d.prompts && !a.kv_int8) {
         if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), st)) != cudaSuccess)
             return cuda_fail(e, "dense prompt attention launch");
@@ -1047,6 +1051,8 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
         a.wide_fac = fac;
         for (int64_t first = 0; first < d.wide_total; first += d.wide_slots) {
             wa.first_slot = static_cast<int>(first);
+            if (first > 0 && (e = cudaMemsetAsync(a.next_item, 0, sizeof(uint32_t), st)) != cudaSuccess)
+                return cuda_fail(e, "cudaMemsetAsync");
             e = a.out_bf16 ? msa::run_widen_f16(wa, fac, st) : msa::run_widen_kv(wa, st);
             if (e != cudaSuccess) return cuda_fail(e, "key/value widening launch");
             if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), st)) != cudaSuccess)
