@@ -489,8 +489,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     auto slot_v = [&](const DpWork& w, int j) { return kAlt ? (j + 1 < w.total ? 2 * j + 2 : 2 * j + 1) : 2 * j + 1; };
 
     if (warp >= 8) {
-        if constexpr (kParts == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8 || warp == 10) {
             // ---------------- copies: K and V tiles in the order the matrix instructions take them, dimensions 0-63 by warp 8
             // (and the queries and scales), 64-127 by warp 10 (and items and last value tiles)
@@ -764,9 +763,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             }
         }
     } else {
-        // 168 x 384 registers at launch: 208 x 256 + 88 x 128, or 232 x 256 + 40 x 128
-        if constexpr (kParts == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        // 168 x 384 registers at launch: 208 x 256 + 88 x 128 (fp32 outputs, 512 rows at 32,768: 968 us; with 200 and 104
+        // 1,001, the groups spill; with 232 and 40 1,069, the copying warps do)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------- softmax group s: thread = row of M tile s
         const int s = warp >> 2, m = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 (warp % 4)) << 16
@@ -825,7 +824,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             }
         };
         if constexpr (kF16) load_fac(0, fac_next);
-        float vref = 0.f;
+        int vexp = 0;  // its exponent, biased (the factors are powers of two, 2^-118 .. 2^119; 0: none yet)
+        auto power = [](int e) { return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23); };  // 2^e, e < 128
         bool coarse = false;  // some block's values were 2^-12 or less of another's: small weights may have lost bits
         constexpr float kLift = kF16 ? 6.f : 0.f;  // f16 weights: at most 2^(6 + 8)
         float top = -INFINITY, sum = 0.f;  // maximum in use (log2 domain), sum of weights
@@ -1001,40 +1001,44 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             } else {
                 now = (NK == 128 ? fmaxf(big[0], big[NK / 64 - 1]) : big[0]) * f;
             }
-            float vnew = vref;
-            if constexpr (kF16) vnew = fmaxf(vref, fmaxf(fac_now[0].y, fac_now[1].y));  // the same for every row
+            int vnew = vexp, vblock[2] = {0, 0};
+            if constexpr (kF16) {  // the same for every row
+                vblock[0] = static_cast<int>(__float_as_uint(fac_now[0].y) >> 23);
+                vblock[1] = static_cast<int>(__float_as_uint(fac_now[1].y) >> 23);
+                vnew = max(vexp, max(vblock[0], vblock[1]));
+            }
             if (c == 0) {
                 top = now;
-            } else if (__any_sync(0xffffffffu, now > top + kDpSlack) || (kF16 && vnew > vref)) {
+            } else if (__any_sync(0xffffffffu, now > top + kDpSlack) || (kF16 && vnew > vexp)) {
                 // the maximum grew: the warp's rows of O in tensor memory (no product runs on it now: S of this tile
                 // was computed after the last one) and their sums move to the new one
                 const float next = now > top + kDpSlack ? now : top;
                 const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
-                const float ro = kF16 ? r * (vref / vnew) : r;  // (vnew > 0: every block's is)
-                if constexpr (kF16) coarse |= vref < vnew * 2.4414063e-4f;
+                const float ro = kF16 ? r * power(vexp - vnew) : r;
+                if constexpr (kF16) coarse |= vexp - vnew < -12;
                 rescale(ro);
                 sum *= r;
                 top = next;
             }
-            if constexpr (kF16) vref = vnew;
+            if constexpr (kF16) vexp = vnew;
             const float base = top == -INFINITY ? 0.f : top;
             float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
             float back[2] = {1.f, 1.f};  // f16 form: from a block's weights, in units of its values, to plain ones
             float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int h2 = 0; h2 < NK / 64; ++h2) {  // 64 keys at a time: the products with them start while the next are made
-                float unit = 1.f;  // f16 form: the block's value factor over vref
+                int unit = 0;  // f16 form: the block's value factor over the one that O is kept in, log2 (at most 0)
                 bool folded = true;
                 if constexpr (kF16) {
-                    // weight 2^(x - base + 6) times `unit`, a power of two: an exponent's addition, and taken out of the
-                    // sum again, unless it is too small for that (a block of tiny scales; the same for the whole CTA)
-                    if (fac_now[h2].y > 0.f) unit = fac_now[h2].y / vref;
-                    folded = unit >= 8.6736174e-19f;  // 2^-60
-                    coarse |= unit < 2.4414063e-4f;   // 2^-12
-                    const float up = kLift + (folded ? static_cast<float>(static_cast<int>(__float_as_uint(unit) >> 23) - 127) : 0.f);
+                    // weight 2^(x - base + 6) times 2^unit: an exponent's addition, and taken out of the sum again, unless it
+                    // is too small for that (a block of tiny scales; the same for the whole CTA)
+                    if (vblock[h2] > 0) unit = vblock[h2] - vexp;
+                    folded = unit >= -60;
+                    coarse |= unit < -12;
+                    const float up = kLift + (folded ? static_cast<float>(unit) : 0.f);
                     ff = make_float2(f * fac_now[h2].x, f * fac_now[h2].x);
                     nb = make_float2(up - base, up - base);
-                    back[h2] = folded ? 1.f / unit : 1.f;
+                    back[h2] = folded ? power(-unit) : 1.f;
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -1048,7 +1052,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     }
                     if (kF16 && !folded) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) z[k] *= unit;
+                        for (int k = 0; k < 32; ++k) z[k] *= power(unit);
                     }
                     uint32_t pk[16];
 #pragma unroll
@@ -1129,6 +1133,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             const int64_t part_row = static_cast<int64_t>(item.part) * kRows + s * 128 + m;
             float most = 0.f;  // f16 form: the row's largest value, in units of w x V16
             bool spoiled = kAlt && !(fabsf(sum) < INFINITY);  // a product with a value past the row's position that is not finite
+            const float vref = kF16 ? __uint_as_float(static_cast<uint32_t>(vexp) << 23) : 1.f;
             const float inv = kF16 ? vref / sum : 1.f / sum;  // (parts: O in plain units, as their join expects)
             if (have) {
 #pragma unroll(kParts > 1 ? 4 : 1)
@@ -1246,9 +1251,12 @@ __global__ void __launch_bounds__(kDjThreads, 8) dense_join_kernel(const DenseAr
             float2 ml[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int64_t row = base + static_cast<int64_t>(min(y0 + u, nsplit - 1)) * kRows + x;
-                ml[u] = *reinterpret_cast<const float2*>(a.part_ml + row * 2);
-                p[u] = *reinterpret_cast<const float4*>(a.part_o + row * kHeadDim + 4 * lane);
+                const int64_t row = base + static_cast<int64_t>(y0 + u) * kRows + x;
+                ml[u] = make_float2(-INFINITY, 0.f);
+                if (y0 + u < nsplit) {
+                    ml[u] = *reinterpret_cast<const float2*>(a.part_ml + row * 2);
+                    p[u] = *reinterpret_cast<const float4*>(a.part_o + row * kHeadDim + 4 * lane);
+                }
             }
             float top = m;
 #pragma unroll
