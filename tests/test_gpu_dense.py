@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 class Batch:
     """Random inputs of one batch and its problem."""
 
-    def __init__(self, seqs, H, G, int8=False, page=0, out=torch.bfloat16, scale=None, seed=0, spare_rows=0, q_gain=2.0):
+    def __init__(self, seqs, H, G, int8=False, page=0, out=torch.bfloat16, scale=None, seed=0, spare_rows=0, q_gain=2.0,
+                 lead=5):
         g = torch.Generator(device="cuda").manual_seed(seed)
         m = msa()
         self.seqs, self.H, self.G, self.out_dtype, self.int8 = seqs, H, G, out, int8
@@ -34,7 +35,7 @@ class Batch:
             self.table = self.table.cuda()
             kw.update(block_table=self.table, page_size=page)
         else:
-            self.starts, at = [], 5
+            self.starts, at = [], lead
             for _, L in seqs:
                 self.starts.append(at)
                 at += L + 3
@@ -153,6 +154,61 @@ def test_long_contexts_are_split(seqs):
 def test_many_sequences():
     Batch([(1, 1 + (37 * i) % 200) for i in range(700)], 1, 4, False, 64, torch.bfloat16).check()
     Batch([(1 + i % 12, 20 + (37 * i) % 200) for i in range(300)], 2, 3, True, 64, torch.bfloat16).check()
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("G", [6, 16])
+def test_decodes_windows_and_prompts_in_one_call(G, int8, out):
+    """Contexts long enough that each kind runs in its own kernel."""
+    seqs = [(1, 5000), (40, 4200), (1, 70), (4, 4500), (8, 8), (12, 12), (5, 300), (200, 700)]
+    Batch(seqs, 2, G, int8, 64, out, seed=G).check()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_many_sequences_of_every_kind(int8):
+    seqs = [((1, 4, 12, 7, 20)[i % 5], 20 + (37 * i) % 200) for i in range(450)]
+    Batch(seqs, 1, 8, int8, 64, torch.bfloat16).check()
+    seqs[17] = (12, 5000)  # (every kind in its own kernel)
+    Batch(seqs, 1, 8, int8, 0, torch.float32).check()
+    Batch(seqs[:40], 4, 8, int8, 0, torch.bfloat16).check()
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("int8", [False, True])
+def test_cache_rows_beyond_32_bit_offsets(n, int8):
+    """Rows from 4,200,000 on of 8 heads of 128 values: elements past 2^32."""
+    Batch([(n, 300), (n, 77)], 8, 4, int8, 0, torch.float32, lead=4_200_000).check()
+
+
+def test_int8_prompts_widened_a_few_at_a_time():
+    """The widened copy of a 2^20-token context and its neighbours is larger than one pass may hold."""
+    Batch([(40, 50), (9, 1 << 20), (1, 300), (130, 130)], 8, 1, True, 0, torch.bfloat16).check()
+    Batch([(40, 50), (9, 1 << 20), (20, 70)], 8, 1, True, 0, torch.float32).check()
+
+
+def test_sequences_may_share_pages():
+    for n in (1, 4, 40):
+        b = Batch([(n, 300), (n, 300), (n, 300)], 2, 8, n == 4, 64)
+        b.table[1, :3] = b.table[0, :3]  # a common prefix
+        b.table[2] = b.table[0]
+        b.check()
+
+
+def test_two_calls_at_once_on_two_streams():
+    m = msa()
+    batches = [Batch([(300, 6000)], 2, 16), Batch([(1, 30000), (4, 9000)], 2, 16), Batch([(64, 5000)], 2, 16, True)]
+    want = [b.run() for b in batches]
+    streams = [torch.cuda.Stream() for _ in batches]
+    got = [[] for _ in batches]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, s, g in zip(batches, streams, got):
+            with torch.cuda.stream(s):
+                g.append(m.dense_forward(b.pb, b.q, b.k, b.v))  # (a workspace of its own)
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
 
 
 @pytest.mark.parametrize("n", [1, 4, 40])
