@@ -944,6 +944,10 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     if ((s = check_ptr(q, "q")) != MSA_OK || (s = check_ptr(k_cache, "k_cache")) != MSA_OK ||
         (s = check_ptr(v_cache, "v_cache")) != MSA_OK || (s = check_ptr(out, "out")) != MSA_OK)
         return s;
+    const uintptr_t values = static_cast<uintptr_t>(p->total_rows) * p->num_kv_heads * p->group_size * msa::kHeadDim;
+    const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
+    if (q0 < o0 + values * (p->out_dtype == MSA_OUT_BF16 ? 2 : 4) && o0 < q0 + values * 2)
+        return fail(MSA_ERR_INVALID_ARG, "out overlaps q");  // (q is read again where a row is computed a second time)
     const DensePlan d = dense_plan(p);
     const DenseLayout l = dense_layout(p, d);
     if (workspace == nullptr) return fail(MSA_ERR_WORKSPACE, "workspace is null");

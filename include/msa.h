@@ -354,7 +354,9 @@ typedef struct msa_append {
  * are rows of q_out and iq_out at or past cu_rows[num_seqs].  Two positions
  * that share a cache row (a page listed twice) are the caller's error.
  * Metadata errors go to the error word in the workspace's first 4 bytes, as
- * for msa_workspace_size's workspace; a row with bad metadata is not stored. */
+ * for msa_workspace_size's workspace; a row with bad metadata is not stored.
+ * Other than q_out on q and iq_out on iq, what is written must not overlap
+ * what is read. */
 msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa_rope* rope, void* workspace,
                             size_t workspace_bytes, void* stream);
 
@@ -371,9 +373,22 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  * read of a key or value.  Cache rows past a sequence's length may hold
  * anything, NaN included.  Rows of out at or past cu_rows[num_seqs] are left
  * as they were; a sequence of no rows is skipped.
- * With fp32 outputs the softmax weights enter the products with V as three
- * bf16 parts (all 24 bits); with bf16 outputs as one part (prompt chunks) or
- * two (decode rows). */
+ *
+ * Numerics.  Scores, maxima and sums are fp32.  The softmax weights enter the
+ * products with V, bf16 caches: as three bf16 parts (2^-24) with fp32 outputs;
+ * with bf16 outputs as one (2^-9, prompt chunks) or two (2^-17, decode rows and
+ * drafted windows of up to 16 (row, head) pairs).  int8 caches: exact codes,
+ * f16 weights of one part (2^-12, bf16 outputs) or two (2^-23, fp32) for up to
+ * 8 rows a sequence, three bf16 parts for prompt chunks with fp32 outputs; with
+ * bf16 outputs prompt chunks read an f16 copy of the cache (a key or value off
+ * by 2^-12 of itself at most).  For up to 8 rows a sequence, a value whose scale
+ * is below 2^-28 of the largest value scale met before it loses weight bits.
+ *
+ * out must not overlap q or the caches.  The workspace's contents need no
+ * initialisation; calls that share one must be ordered (one stream, or events).
+ * It holds the parts of what is split over keys (up to 130 MB) and, for an int8
+ * cache with prompt chunks, the widened copy: 4 H (D + 2) bytes a position of
+ * every such sequence, as many sequences at a time as 8 GiB hold (at least one). */
 msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_cache, const void* v_cache,
                              void* out, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -91,14 +91,22 @@ def test_dense_arguments_rejected_on_host():
     assert L.msa_dense_workspace_size(C.byref(pb), None) == 1
     assert L.msa_dense_workspace_size(C.byref(_problem(head_dim=64)), C.byref(n)) == 2
     L.msa_dense_workspace_size(C.byref(pb), C.byref(n))
-    f, ws = C.c_void_p(FAKE), C.c_void_p(1 << 20)
+    f, o, ws = C.c_void_p(FAKE), C.c_void_p(FAKE + (1 << 30)), C.c_void_p(1 << 20)
     bad = C.c_void_p(FAKE + 8)
-    for args in ((None, f, f, f), (f, None, f, f), (f, f, bad, f), (f, f, f, bad)):
+    for args in ((None, f, f, o), (f, None, f, o), (f, f, bad, o), (f, f, f, bad)):
         assert L.msa_dense_forward(C.byref(pb), *args, ws, n.value, None) == 1
-    assert L.msa_dense_forward(C.byref(pb), f, f, f, f, None, n.value, None) == 3
-    assert L.msa_dense_forward(C.byref(pb), f, f, f, f, ws, n.value - 1, None) == 3
-    assert L.msa_dense_forward(C.byref(pb), f, f, f, f, C.c_void_p((1 << 20) + 128), n.value, None) == 3
-    assert L.msa_dense_forward(C.byref(_problem(group_size=17)), f, f, f, f, ws, n.value, None) == 2
+    # out must not touch q: the same, its last value, and one that begins inside it
+    values = pb.total_rows * pb.num_kv_heads * pb.group_size * 128
+    width = 2 if pb.out_dtype else 4
+    for at in (FAKE, FAKE + 2 * values - 16, FAKE - width * values + 16):
+        assert L.msa_dense_forward(C.byref(pb), f, f, f, C.c_void_p(at), ws, n.value, None) == 1
+        assert b"overlaps" in L.msa_last_error()
+    for at in (FAKE + 2 * values, FAKE - width * values):  # beside it: on to the workspace's checks
+        assert L.msa_dense_forward(C.byref(pb), f, f, f, C.c_void_p(at), None, n.value, None) == 3
+    assert L.msa_dense_forward(C.byref(pb), f, f, f, o, None, n.value, None) == 3
+    assert L.msa_dense_forward(C.byref(pb), f, f, f, o, ws, n.value - 1, None) == 3
+    assert L.msa_dense_forward(C.byref(pb), f, f, f, o, C.c_void_p((1 << 20) + 128), n.value, None) == 3
+    assert L.msa_dense_forward(C.byref(_problem(group_size=17)), f, f, f, o, ws, n.value, None) == 2
 
 
 def test_rope_tables():
