@@ -26,18 +26,32 @@
 // with fp32 outputs O_s holds two key tiles' products only and the softmax group adds them to its rows in registers.
 //
 // Drafted windows (kAlt): one M tile, and the two stages take alternate key tiles, each with its own running state.
-// Items (a tile pair and a head) are one CTA each, the longest first; those of the last wave, which would leave SMs
-// idle, are split over their keys as well (2,048 int8 rows at 8,192: 512 items on 152 SMs ended between 432 and 562 us)
-// and their parts joined by dense_join_kernel.
+//
+// One CTA per SM stays for the launch and takes items (a tile pair and a head), the longest first, as it gets through
+// them (a counter; what an item holds and how it is computed does not depend on who has it).  Barriers, tensor memory and
+// the ring of tiles run on from item to item: the next item's first copies and scores run under the last one's epilogue
+// (a CTA for each item: 890 against 813 us for 4,096 rows at 8,192, 131 against 108 for eight packed prompts of 1 to
+// 2,047 rows).  Items of the last wave, which would leave SMs idle, are split over their keys as well and their parts
+// joined by dense_join_kernel.
+//
+// K and V are copied by two warps, 64 dimensions each: a thread's copies go out at about 48 B a cycle and a slot of the
+// ring is free for one key tile's time, so with one thread the matrix instructions waited 580 of 2,900 cycles a tile for
+// them (two: 300, which is what testing two complete barriers takes).
+//
+// What bounds it: bf16, the tensor pipe (4,096 rows at 8,192, 4 x 16 heads: 1.37 TFLOP in 805 to 870 us with the clocks
+// that the power limit leaves, 1.58 to 1.70 PFLOP/s of 1.92 measured for cuBLAS in short bursts, 1.74 sustained); int8
+// with bf16 outputs, the softmax groups' instructions (0.62 TFLOP in 504 us); fp32 outputs, likewise (0.55 TFLOP, with
+// three weight parts 1.1 on the tensor cores, in 968 us); short sequences, the 4 us an item that its groups spend between
+// its last scores and the next one's first, against 1.6 us a key tile.
 //
 // int8 caches are read from a copy widened once per call.  bf16 outputs: f16 values with the scales in them, over a
 // power of two for each 64-position block (run_widen_f16), queries as f16 times a power of two for each row (converted
 // in shared memory by the softmax threads; bf16's 8 bits fit, what lies 2^-22 below the row's largest loses some) and
 // weights as one f16 (2^-12), at most 2^14: the blocks' powers of two are two scalars each for the softmax, where the
-// scales themselves, one for each key, were a third of its instructions (784 us for 2,048 rows at 8,192).  fp32 outputs:
+// scales themselves, one for each key, were a third of its instructions (784 us for 2,048 rows at 8,192, now 504).  fp32 outputs:
 // bf16 integers, exact, scales beside them (run_widen_kv); the key scale multiplies the score, the value scale the weight.
 //
-// Values that no row of the tile may see: positions past the length are zeroed in the last value tile (warp 10), so
+// Values that no row of the tile may see: positions past the length are zeroed in the last value tile (by warp 10), so
 // stale cache rows do not matter.  A later token of the same chunk meets weights of zero; if its value is not finite
 // the product is NaN, so a row whose result is not finite is computed again key by key (dp_row_again).
 #include <cuda_fp16.h>
@@ -356,7 +370,8 @@ __device__ __forceinline__ DpWork dp_work(const DenseArgs& a, const DpItem& it) 
     return w;
 }
 
-// One row again over keys [first, end), key by key (a whole warp; 4 dimensions a lane).  Used where a product with a later token's infinite or NaN value spoiled the row.
+// One row again over keys [first, end), key by key (a whole warp; 4 dimensions a lane): where a product with a later
+// token's infinite or NaN value spoiled the row, or the f16 copy's powers of two left it too few bits.
 __device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int64_t q_row, int first, int end, float (&o)[4],
                                           float& m, float& l) {
     const int lane = threadIdx.x & 31;

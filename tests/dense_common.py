@@ -14,7 +14,12 @@ Dense attention, out = sum_t w_t v_t with w = softmax(x), x_t = scale q.k_t.
     denominator.
   - a weight entering the product with v is rounded to one bf16 (2^-8), two
     (2^-16) or three (2^-24) parts; int8 caches multiply it by the value's
-    scale first (one more fp32 rounding, inside the L 2^-24).
+    scale first (one more fp32 rounding, inside the L 2^-24).  f16 forms of an
+    int8 cache: a weight is off by 2^-12, and in prompts with bf16 outputs keys
+    and values by up to 2^-12 of themselves.  Weight and value are inside the
+    2^-8 counted for one bf16 part.  The key's share, 2^-12 A of a score if all
+    128 errors had one sign, is not counted: the tests hold these outputs to
+    the tighter bound.
   - the output is rounded to its type: half a step, eps / 2 of its magnitude.
 All but the last scale with sum_t w_t |v_t|."""
 import math
