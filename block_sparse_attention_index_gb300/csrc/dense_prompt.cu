@@ -343,21 +343,24 @@ struct DpWork {
 };
 
 template <bool kAlt, int NK>
-__device__ __forceinline__ DpWork dp_work(const DenseArgs& a, const DpItem& it) {
+__device__ __forceinline__ DpWork dp_work(int P, const DpItem& it) {  // P = 128 / G
     DpWork w;
-    const int split = it.split, nsplit = it.nsplit;
     w.b = it.b;
     w.c0 = it.c0;
     w.n = it.n;
     w.L = it.L;
-    w.P = 128 / a.G;
+    w.P = P;
     w.i0 = it.tile * w.P * (kAlt ? 1 : 2);
     const int p0 = w.L - w.n;
     // keys up to the last row of each M tile
     const int end0 = p0 + min(w.n, w.i0 + w.P), end1 = p0 + min(w.n, w.i0 + 2 * w.P);
     const int all = (max(end0, end1) + NK - 1) / NK;
-    w.first = static_cast<int>(static_cast<int64_t>(all) * split / nsplit);
-    const int last = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / nsplit);
+    int last = all;
+    w.first = 0;
+    if (it.nsplit > 1) {  // (at most 2^15 tiles and 32 parts)
+        w.first = static_cast<int>(static_cast<uint32_t>(all) * it.split / it.nsplit);
+        last = static_cast<int>(static_cast<uint32_t>(all) * (it.split + 1) / it.nsplit);
+    }
     w.total = last - w.first;
     if (kAlt) {
         w.count[0] = (w.total + 1) / 2;
@@ -483,6 +486,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
+    const int P = 128 / a.G;
 
     // Every role walks the CTA's items with its own copy of each and with counts that run on over them: copies (ring slots),
     // a stage's copies (alternate tiles), a stage's tiles, items.
@@ -539,7 +543,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     if (lane == 0) mbar_arrive(&sm.info_empty[k % kDpInfo]);
                 }
                 if (item.b < 0) break;
-                const DpWork w = dp_work<kAlt, NK>(a, item);
+                const DpWork w = dp_work<kAlt, NK>(P, item);
                 const int h = item.h, fix = last_tile(w);
                 if (!half) {
                     int ok = 1;
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 if (!ok) break;
                 mbar_arrive(&sm.info_empty[k % kDpInfo]);
                 if (item.b < 0) break;
-                const DpWork w = dp_work<kAlt, NK>(a, item);
+                const DpWork w = dp_work<kAlt, NK>(P, item);
                 const int count = s == 0 ? w.count[0] : w.count[1], others = s == 0 ? w.count[1] : w.count[0];
                 // S_s = Q_s K^T from ring slot st; `pass`: the other stage's turn begins while the last of them run
                 auto scores = [&](int st, bool last, bool pass) {
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             }
         }
     } else {
-        // 168 x 384 registers at launch: 208 x 256 + 88 x 128 (fp32 outputs, 512 rows at 32,768: 968 us; with 200 and 104
+        // 168 x 384 registers at launch: 208 x 256 + 88 x 128 (fp32 outputs, 512 rows at 32,768: 958 us; with 200 and 104
         // 1,001, the groups spill; with 232 and 40 1,069, the copying warps do)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------- softmax group s: thread = row of M tile s
@@ -793,7 +797,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         if constexpr (kAlt) alive = dp_sync_and(alive);  // (the groups meet in the epilogue: both come, or neither)
         if (!alive) break;
         if (item.b < 0) break;
-        const DpWork w = dp_work<kAlt, NK>(a, item);
+        const DpWork w = dp_work<kAlt, NK>(128 / a.G, item);
         const int h = item.h;
         const int pos = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, w.n - 1);
         // the tile's earliest position: key tiles up to it hide nothing
@@ -1086,7 +1090,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         // (the item is read again here, so that the loop over its tiles need not keep it in registers)
         {
         const DpItem item = sm.info[k % kDpInfo];
-        const DpWork w = dp_work<kAlt, NK>(a, item);
+        const DpWork w = dp_work<kAlt, NK>(128 / a.G, item);
         const int h = item.h, count = s == 0 ? w.count[0] : w.count[1];
         const int i = w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, g = m % a.G;
         const bool mine = m < w.P * a.G && i < w.n;
@@ -1104,12 +1108,13 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], done++ & 1, a.err));
         tc_fence_after();
         if (alive && have) collect();
-        auto row_of_o = [&](int q, float (&y)[32]) {  // 32 values of the row
+        constexpr int kRun = 32;  // values of the row that are finished at a time
+        auto row_of_o = [&](int q, float (&y)[kRun]) {
             if constexpr (kParts > 1) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) y[k] = acc[32 * q + k];
+                for (int k = 0; k < kRun; ++k) y[k] = acc[kRun * q + k];
             } else {
-                dp_ld32(o_addr + 32 * q, y);
+                dp_ld32(o_addr + kRun * q, y);
                 tmem_ld_wait();
             }
         };
@@ -1120,13 +1125,13 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             // gave up, all 256 threads stop here together)
             alive = dp_sync_and(alive);
             if (!alive) break;
-            if (s == 1 && have && alive) {
+            if (s == 1 && have) {
 #pragma unroll(kParts > 1 ? 4 : 1)
-                for (int q = 0; q < kHeadDim / 32; ++q) {
-                    float y[32];
+                for (int q = 0; q < kHeadDim / kRun; ++q) {
+                    float y[kRun];
                     row_of_o(q, y);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) other[(32 * q + k) * 128 + m] = y[k];
+                    for (int k = 0; k < kRun; ++k) other[(kRun * q + k) * 128 + m] = y[k];
                 }
             }
             if (s == 1) sm.other_ml[m] = make_float2(have ? top : -INFINITY, have ? sum : 0.f);
@@ -1151,42 +1156,49 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             const float vref = kF16 ? __uint_as_float(static_cast<uint32_t>(vexp) << 23) : 1.f;
             const float inv = kF16 ? vref / sum : 1.f / sum;  // (parts: O in plain units, as their join expects)
             if (have) {
+                const float to = split_up ? (kF16 ? vref : 1.f) : inv;
 #pragma unroll(kParts > 1 ? 4 : 1)
-                for (int q = 0; q < kHeadDim / 32; ++q) {
-                    float y[32];
+                for (int q = 0; q < kHeadDim / kRun; ++q) {
+                    float y[kRun];
                     row_of_o(q, y);
                     if constexpr (kAlt) {
-                        if (w.count[1] > 0)
+                        if (w.count[1] > 0) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) y[k] = y[k] * f0 + other[(32 * q + k) * 128 + m] * f1;
+                            for (int k = 0; k < kRun; ++k) y[k] = y[k] * f0 + other[(kRun * q + k) * 128 + m] * f1;
+                        }
+                    }
+                    float2 zero[4] = {};  // 0 unless a value is infinite or NaN
+#pragma unroll
+                    for (int k = 0; k < kRun; k += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            zero[e] = __ffma2_rn(make_float2(y[k + 2 * e], y[k + 2 * e + 1]), make_float2(0.f, 0.f), zero[e]);
+                    spoiled |= !(((zero[0].x + zero[0].y) + (zero[1].x + zero[1].y)) + ((zero[2].x + zero[2].y) + (zero[3].x + zero[3].y)) == 0.f);
+                    if constexpr (kF16) {
+                        float big[4] = {most, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < kRun; ++k) big[k & 3] = fmaxf(big[k & 3], fabsf(y[k]));
+                        most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
                     }
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        spoiled |= !(fabsf(y[k]) < INFINITY);
-                        if constexpr (kF16) most = fmaxf(most, fabsf(y[k]));
+                    for (int k = 0; k < kRun; k += 2) {
+                        const float2 z = __fmul2_rn(make_float2(y[k], y[k + 1]), make_float2(to, to));
+                        y[k] = z.x;
+                        y[k + 1] = z.y;
                     }
-                    if (kF16 && split_up)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] *= vref;
                     if (!mine) {
                         // (a row of the tile that no query has)
-                    } else if (split_up) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 32 * q);
+                    } else if (split_up || !a.out_bf16) {
+                        float* to_row = split_up ? a.part_o + part_row * kHeadDim : static_cast<float*>(a.out) + q_row * kHeadDim;
+                        float4* dst = reinterpret_cast<float4*>(to_row + kRun * q);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    } else if (a.out_bf16) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_row * kHeadDim + 32 * q);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            dst[k] = make_uint4(pack_bf16x2(y[8 * k] * inv, y[8 * k + 1] * inv),
-                                                pack_bf16x2(y[8 * k + 2] * inv, y[8 * k + 3] * inv),
-                                                pack_bf16x2(y[8 * k + 4] * inv, y[8 * k + 5] * inv),
-                                                pack_bf16x2(y[8 * k + 6] * inv, y[8 * k + 7] * inv));
+                        for (int k = 0; k < kRun / 4; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + q_row * kHeadDim + 32 * q);
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_row * kHeadDim + kRun * q);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            dst[k] = make_float4(y[4 * k] * inv, y[4 * k + 1] * inv, y[4 * k + 2] * inv, y[4 * k + 3] * inv);
+                        for (int k = 0; k < kRun / 8; ++k)
+                            dst[k] = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                                                pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
                     }
                     __syncwarp();  // the next load is the whole warp's
                 }
