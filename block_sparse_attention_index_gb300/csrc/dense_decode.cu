@@ -40,7 +40,7 @@ constexpr int kDdConsumers = 8;
 // launched with 168 a thread (64,512), 256 x 208 + 128 x 88 = 64,512 after the split.
 constexpr int kDdThreads = 384;
 constexpr int kDdMergeWords = 32 + 4;  // half of O, m and l of a lane
-constexpr int kDdPrefix = 512;         // sequences whose unit prefix is kept in shared memory (more: in the workspace)
+constexpr int kDdPrefix = 256;         // sequences whose prefixes are kept in shared memory (more: in the workspace)
 
 // Tile i lands in stage i % kStages and completes barrier i % 16.  16 is a multiple of the consumers, so each of them
 // sees its barriers' phases one after the other (a warp that saw only some of a stage's phases could not tell them
@@ -113,9 +113,10 @@ struct DdSeq {
 
 __device__ __forceinline__ int dd_blocks(int L) { return (L + kBlock - 1) / kBlock; }
 
-// Units (blocks x tiles) of sequence b; 0 if it is not of the decode family or its metadata is bad.
-__device__ __forceinline__ int dd_units(const DenseArgs& a, int b, bool& bad) {
+// Units (blocks x tiles) and tiles of sequence b; 0 if it is not of the decode family or its metadata is bad.
+__device__ __forceinline__ int dd_units(const DenseArgs& a, int b, int& tiles, bool& bad) {
     bad = false;
+    tiles = 0;
     const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0, L = a.cache_lens[b];
     const bool placed = seq_rows_ok(a.cache, b, L, a.cache_tokens);  // (loads that need not wait for one another)
     if (n == 0 || n > kDecodeMaxRows || (a.tile_windows && n * a.G > 16)) return 0;
@@ -123,7 +124,8 @@ __device__ __forceinline__ int dd_units(const DenseArgs& a, int b, bool& bad) {
         bad = true;
         return 0;
     }
-    return dd_blocks(L) * ((n * a.G + 15) / 16);
+    tiles = (n * a.G + 15) / 16;
+    return dd_blocks(L) * tiles;
 }
 
 __device__ __forceinline__ DdSeq dd_seq(const DenseArgs& a, int b) {
@@ -137,9 +139,36 @@ __device__ __forceinline__ DdSeq dd_seq(const DenseArgs& a, int b) {
     return s;
 }
 
-// CTAs that take a share of the tiles (unit u, head h: tile u H + h): share c is tiles [total c / shares,
-// total (c + 1) / shares), none of them empty.
+// CTAs that take a share of the tiles (unit u, head h: tile u H + h).  Going on to another segment (a sequence's 16 pairs)
+// holds a CTA's warps up as some tiles would, so a segment counts for that many more: the shares divide evenly the line
+// of all tiles with dd_extra of nothing before the first of each segment, from the very first tile on.  (With even tiles,
+// of the shares of 64 short sequences those with four segments ended 10 us after those with one, 29 of 44 us, and the
+// two-segment shares of 8 ragged int8 sequences 5 us after the others, 34 of 50.)
 __device__ __forceinline__ int dd_shares(int64_t total, int grid) { return static_cast<int>(min(total, static_cast<int64_t>(grid))); }
+__device__ __forceinline__ int dd_extra(bool int8) { return int8 ? 16 : 4; }
+// Where share c begins.
+__device__ __forceinline__ int64_t dd_cut(int64_t line, int extra, int c, int shares) {
+    const int64_t n = line - extra;
+    if (n * shares < (int64_t{1} << 32)) return extra + static_cast<uint32_t>(n) * static_cast<uint32_t>(c) / static_cast<uint32_t>(shares);
+    return extra + n * c / shares;
+}
+
+// The tile at position `at` of that line (`extra` is where the next segment begins); b: its sequence, or one before it
+// that has none.
+__device__ __forceinline__ int64_t dd_tile_at(const int32_t* units, const int32_t* segs, int num_seqs, int H, int extra, int64_t at, int& b) {
+    int lo = 0, hi = num_seqs;  // largest b that begins at or before it
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int64_t>(units[mid]) * H + static_cast<int64_t>(segs[mid]) * extra <= at) lo = mid; else hi = mid;
+    }
+    b = lo;
+    const int u = units[lo], n = segs[lo + 1] - segs[lo];
+    if (n == 0) return static_cast<int64_t>(u) * H;
+    const int all = units[lo + 1] - u, blocks = n == 1 ? all : all / n, per = blocks * H + extra;
+    const int off = static_cast<int>(at - static_cast<int64_t>(u) * H - static_cast<int64_t>(segs[lo]) * extra);
+    const int mt = off < per ? 0 : off / per;
+    return static_cast<int64_t>(u + mt * blocks) * H + max(0, off - mt * per - extra);
+}
 
 // Writes two neighbouring outputs of (row, head) pair m of a sequence, heads of KV head h.
 __device__ __forceinline__ void dd_store2(const DenseArgs& a, const DdSeq& s, int h, int m, int d, float x, float y) {
@@ -162,8 +191,9 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     // [num_seqs + 1]; in the workspace every CTA writes the same values
     int32_t* prefix = a.num_seqs < kDdPrefix ? reinterpret_cast<int32_t*>(ring + Cfg::kStages * Cfg::kStageBytes + Cfg::kMergeBytes)
                                              : a.unit_prefix;
+    int32_t* segs = prefix + (a.num_seqs < kDdPrefix ? kDdPrefix : a.num_seqs + 1);  // the same of segments
     __shared__ uint64_t full[kDdFull], empty[Cfg::kStages];
-    __shared__ int warp_tot[kDdThreads / 32];
+    __shared__ int2 warp_tot[kDdThreads / 32];
     __shared__ uint32_t err;
     __shared__ float tail_w[kDdConsumers][16][kDecodeMaxRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -178,50 +208,61 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // ---- exclusive prefix of the sequences' units (a block-wide scan, kDdThreads sequences at a time)
-    int carry = 0;
+    // ---- exclusive prefixes of the sequences' units and segments (a block-wide scan, kDdThreads sequences at a time)
+    int2 carry = make_int2(0, 0);
     for (int base = 0; base < a.num_seqs; base += kDdThreads) {
         const int b = base + tid;
         bool bad = false;
-        const int units = b < a.num_seqs ? dd_units(a, b, bad) : 0;
+        int2 mine = make_int2(0, 0);
+        if (b < a.num_seqs) mine.x = dd_units(a, b, mine.y, bad);
         if (bad && blockIdx.x == 0) atomicOr(&err, kErrBadMetadata);
-        int incl = units;
+        int2 incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, incl.x, o), w = __shfl_up_sync(0xffffffffu, incl.y, o);
+            if (lane >= o) incl = make_int2(incl.x + v, incl.y + w);
         }
         if (lane == 31) warp_tot[warp] = incl;
         __syncthreads();
-        int before = 0, total = 0;
+        int2 before = make_int2(0, 0), total = make_int2(0, 0);
         for (int w = 0; w < kDdThreads / 32; ++w) {
-            if (w < warp) before += warp_tot[w];
-            total += warp_tot[w];
+            const int2 t = warp_tot[w];
+            if (w < warp) before = make_int2(before.x + t.x, before.y + t.y);
+            total = make_int2(total.x + t.x, total.y + t.y);
         }
-        if (b < a.num_seqs) prefix[b] = carry + before + incl - units;
+        if (b < a.num_seqs) {
+            prefix[b] = carry.x + before.x + incl.x - mine.x;
+            segs[b] = carry.y + before.y + incl.y - mine.y;
+        }
         __syncthreads();
-        carry += total;
+        carry = make_int2(carry.x + total.x, carry.y + total.y);
     }
-    if (tid == 0) prefix[a.num_seqs] = carry;
+    if (tid == 0) {
+        prefix[a.num_seqs] = carry.x;
+        segs[a.num_seqs] = carry.y;
+    }
     __syncthreads();
     if (blockIdx.x == 0 && a.num_seqs < kDdPrefix)
-        for (int b = tid; b <= a.num_seqs; b += kDdThreads) a.unit_prefix[b] = prefix[b];
-    // this CTA's tiles: [begin, begin + n) of all; the first is head h_off of unit u0
-    const int64_t total = static_cast<int64_t>(carry) * H;
-    const int shares = dd_shares(total, gridDim.x);  // CTAs with work
-    const bool idle = static_cast<int>(blockIdx.x) >= shares;
-    const int64_t begin = idle ? 0 : total * blockIdx.x / shares;
-    const int n_tiles = idle ? 0 : static_cast<int>(total * (blockIdx.x + 1) / shares - begin);
-    const int u0 = static_cast<int>(begin / H), h_off = static_cast<int>(begin % H), u1 = u0 + (h_off + n_tiles + H - 1) / H;
-    int first_b = 0;
-    {
-        int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= u0
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= u0) lo = mid; else hi = mid;
+        for (int b = tid; b <= a.num_seqs; b += kDdThreads) {
+            a.unit_prefix[b] = prefix[b];
+            a.unit_prefix[a.num_seqs + 1 + b] = segs[b];
         }
-        first_b = lo;
+    // this CTA's tiles: [begin, begin + n) of all; the first is head h_off of unit u0
+    const int64_t total = static_cast<int64_t>(carry.x) * H, line = total + static_cast<int64_t>(carry.y) * dd_extra(kInt8);
+    const int shares = dd_shares(total, gridDim.x);  // CTAs with work (some of them none, where segments are very short)
+    const bool idle = static_cast<int>(blockIdx.x) >= shares;
+    int first_b = 0, n_tiles = 0;
+    int64_t begin = 0;
+    if (!idle) {  // even lanes find where it begins, odd ones where it ends
+        int b;
+        const int64_t at = dd_tile_at(prefix, segs, a.num_seqs, H, dd_extra(kInt8),
+                                      dd_cut(line, dd_extra(kInt8), blockIdx.x + (lane & 1), shares), b);
+        first_b = __shfl_sync(0xffffffffu, b, 0);
+        begin = __shfl_sync(0xffffffffu, at, 0);
+        n_tiles = static_cast<int>(__shfl_sync(0xffffffffu, at, 1) - begin);
     }
+    const int u0 = static_cast<int>(begin / H), h_off = static_cast<int>(begin % H);
+    const int u1 = n_tiles == 0 ? u0 : u0 + (h_off + n_tiles + H - 1) / H;
 
     if (warp >= kDdConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -740,38 +781,41 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 
 // Joins the parts of the sequences that several CTAs walked.  CTA (x, h, z) takes a (sequence, tile), x itself where
 // they are no more than the shares (by_tile: tiles a sequence may have), else the one in which boundary x + 1 of the
-// shares is the first to fall, if any; of its (row, head) pairs every gridDim.z-th.  Four warps share a pair, each a
-// quarter of the parts, eight parts' loads in flight and 4 of the 128 values a lane: a running maximum m and sum of
-// 2^(m_i - m) O_i in the parts' order within a warp, then over the warps: the same every time.  What bounds it is the
-// chain of dependent loads (metadata, parts), so the metadata is read while the shares' CTAs still run.
-constexpr int kDcThreads = 128;
-__global__ void __launch_bounds__(kDcThreads, 8) dense_combine_kernel(const DenseArgs a, int grid, int by_tile) {
-    __shared__ float4 sum_o[4][32];
-    __shared__ float2 sum_ml[4];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
-    // ---- which parts: from the inputs alone where a thread a sequence is enough (before the wait), else from the prefix
+// shares is the first to fall, if any; of its (row, head) pairs every gridDim.z-th.  kShare warps share the parts of a
+// pair, eight parts' loads in flight and 4 of the 128 values a lane: a running maximum m
+// and sum of 2^(m_i - m) O_i in the parts' order within a warp, then over the warps: the same every time.  What bounds
+// it is the chain of dependent loads (metadata, parts), so the metadata is read while the shares' CTAs still run.
+template <int kThreads, int kShare>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) dense_combine_kernel(const DenseArgs a, int grid, int by_tile) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float4 sum_o[kWarps][32];
+    __shared__ float2 sum_ml[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y, extra = dd_extra(a.kv_int8);
+    // ---- which parts: from the inputs alone where a thread a sequence is enough (before the wait), else from the prefixes
     // that the shares' CTA 0 wrote
     int lo = by_tile > 0 ? blockIdx.x / by_tile : 0, mt = by_tile > 0 ? blockIdx.x % by_tile : 0;  // sequence, tile
-    const bool early = by_tile > 0 && a.num_seqs <= kDcThreads;
-    int begin = 0, units = 0, carry = 0;  // units before the sequence, of it, of all
+    const bool early = by_tile > 0 && a.num_seqs <= kThreads;
+    int begin = 0, units = 0, carry = 0;     // units before the sequence, of it, of all
+    int seg_begin = 0, seg_carry = 0;        // segments before it, of all
     if (early) {
-        __shared__ int sums[3][4];
+        __shared__ int sums[5][kWarps];
         bool bad;
-        const int mine = tid < a.num_seqs ? dd_units(a, tid, bad) : 0;
-        const int before = __reduce_add_sync(0xffffffffu, tid < lo ? mine : 0);
-        const int here = __reduce_add_sync(0xffffffffu, tid == lo ? mine : 0);
-        const int all = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) {
-            sums[0][warp] = before;
-            sums[1][warp] = here;
-            sums[2][warp] = all;
+        int tiles = 0;
+        const int mine = tid < a.num_seqs ? dd_units(a, tid, tiles, bad) : 0;
+        const int part[5] = {tid < lo ? mine : 0, tid == lo ? mine : 0, mine, tid < lo ? tiles : 0, tiles};
+#pragma unroll
+        for (int q = 0; q < 5; ++q) {
+            const int sum = __reduce_add_sync(0xffffffffu, part[q]);
+            if (lane == 0) sums[q][warp] = sum;
         }
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kWarps; ++q) {
             begin += sums[0][q];
             units += sums[1][q];
             carry += sums[2][q];
+            seg_begin += sums[3][q];
+            seg_carry += sums[4][q];
         }
     }
     DdSeq s{};
@@ -787,36 +831,40 @@ __global__ void __launch_bounds__(kDcThreads, 8) dense_combine_kernel(const Dens
             else if (e) atomicOr(a.err, e);
         }
     }
-    if (!early) carry = a.unit_prefix[a.num_seqs];
-    const int64_t total = static_cast<int64_t>(carry) * a.H;
+    const int32_t* segs = a.unit_prefix + a.num_seqs + 1;
+    if (!early) {
+        carry = a.unit_prefix[a.num_seqs];
+        seg_carry = segs[a.num_seqs];
+    }
+    const int64_t total = static_cast<int64_t>(carry) * a.H, line = total + static_cast<int64_t>(seg_carry) * extra;
     const int shares = dd_shares(total, grid);
     if (by_tile == 0) {
         if (static_cast<int>(blockIdx.x) + 1 >= shares) return;
-        const int cut = static_cast<int>(total * (blockIdx.x + 1) / shares / a.H);  // the unit of the boundary's tile
-        int hi = a.num_seqs;  // largest b with prefix[b] <= cut
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.unit_prefix[mid] <= cut) lo = mid; else hi = mid;
-        }
+        // the unit of the boundary's tile
+        const int cut = static_cast<int>(dd_tile_at(a.unit_prefix, segs, a.num_seqs, a.H, extra, dd_cut(line, extra, blockIdx.x + 1, shares), lo) / a.H);
+        if (cut >= a.unit_prefix[lo + 1]) return;  // (the end of all)
         mt = (cut - a.unit_prefix[lo]) / dd_blocks(a.cache_lens[lo]);
     }
     if (!early) {
         begin = a.unit_prefix[lo];
         units = a.unit_prefix[lo + 1] - begin;
+        seg_begin = segs[lo];
         s = dd_seq(a, lo);
     }
     if (units == 0 || mt >= s.tiles) return;
-    const int64_t seg0 = static_cast<int64_t>(begin + mt * s.blocks) * a.H, seg1 = seg0 + static_cast<int64_t>(s.blocks) * a.H;
-    // the shares that hold its first and last tiles: the largest c with total c / shares <= tile
-    const int first = static_cast<int>(((seg0 + 1) * shares - 1) / total), last = static_cast<int>((seg1 * shares - 1) / total);
+    const int n_seg = s.blocks * a.H;  // the segment's tiles; its place on the line, before the extra
+    const int64_t at = static_cast<int64_t>(begin) * a.H + static_cast<int64_t>(seg_begin) * extra + static_cast<int64_t>(mt) * (n_seg + extra);
+    // the shares that hold its first and last tiles: the largest c with line c / shares at or before the tile
+    const int first = static_cast<int>(((at + 1) * shares - 1) / (line - extra)), last = static_cast<int>(((at + n_seg) * shares - 1) / (line - extra));
     // one share wrote it whole; the boundary lies between two of them, or an earlier one inside it has its CTA
     if (first == last || (by_tile == 0 && first != static_cast<int>(blockIdx.x))) return;
     const int count = last - first + 1;
     // the first share's part is its second one unless the share began with it; the others' are the first of their shares
-    const int slot0 = 2 * first + (total * first / shares < seg0 ? 1 : 0);
-    const int i_begin = count * warp / 4, i_end = count * (warp + 1) / 4;
+    const int slot0 = 2 * first + (dd_cut(line, extra, first, shares) < at ? 1 : 0);
+    const int mine = warp % kShare, i_begin = count * mine / kShare, i_end = count * (mine + 1) / kShare;
     const int pairs = min(16, s.n * a.G - 16 * mt);
-    for (int pair = blockIdx.z; pair < pairs; pair += gridDim.z) {
+    constexpr int kAtOnce = kWarps / kShare;  // pairs
+    for (int pair = blockIdx.z * kAtOnce + warp / kShare; pair < pairs; pair += gridDim.z * kAtOnce) {
         float m = -INFINITY, l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
@@ -858,24 +906,29 @@ __global__ void __launch_bounds__(kDcThreads, 8) dense_combine_kernel(const Dens
             for (int u = 0; u < 8; ++u)
                 if (i0 + u < i_end) add(weight(ml[u], m), ml[u], v[u]);
         }
-        sum_o[warp][lane] = x;
-        if (lane == 0) sum_ml[warp] = make_float2(m, l);
-        __syncthreads();
-        if (warp == 0) {
-            float top = m;
+        if constexpr (kShare > 1) {
+            static_assert(kShare == 1 || kAtOnce == 1, "the warps of a pair meet in block-wide barriers");
+            sum_o[warp][lane] = x;
+            if (lane == 0) sum_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp == 0) {
+                float top = m;
 #pragma unroll
-            for (int q = 1; q < 4; ++q) top = fmaxf(top, sum_ml[q].x);
-            raise(top);
+                for (int q = 1; q < kShare; ++q) top = fmaxf(top, sum_ml[q].x);
+                raise(top);
 #pragma unroll
-            for (int q = 1; q < 4; ++q) {
-                const float2 ml = sum_ml[q];
-                add(weight(ml, m), ml, sum_o[q][lane]);
+                for (int q = 1; q < kShare; ++q) {
+                    const float2 ml = sum_ml[q];
+                    add(weight(ml, m), ml, sum_o[q][lane]);
+                }
             }
+        }
+        if (mine == 0) {
             const float inv = 1.f / l;
             dd_store2(a, s, h, 16 * mt + pair, 4 * lane, x.x * inv, x.y * inv);
             dd_store2(a, s, h, 16 * mt + pair, 4 * lane + 2, x.z * inv, x.w * inv);
         }
-        __syncthreads();
+        if constexpr (kShare > 1) __syncthreads();
     }
 }
 
@@ -883,7 +936,7 @@ template <int H, bool kInt8, int kParts>
 static cudaError_t launch_dense_decode(const DenseArgs& a, int grid, cudaStream_t stream) {
     using Cfg = DdCfg<kInt8>;
     const size_t smem = 1024 + static_cast<size_t>(Cfg::kStages) * Cfg::kStageBytes + Cfg::kMergeBytes +
-                        kDdPrefix * sizeof(int32_t);
+                        2 * kDdPrefix * sizeof(int32_t);
     auto* kernel = dense_decode_kernel<H, kInt8, kParts>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
@@ -901,11 +954,15 @@ static cudaError_t launch_dense_decode(const DenseArgs& a, int grid, cudaStream_
     // tiles or boundaries, heads, (row, head) pairs
     const int tiles = (a.pairs_most + 15) / 16, pairs = std::min(16, a.pairs_most);
     const int by_tile = a.num_seqs * tiles <= grid ? tiles : 0;
-    cfg.gridDim = dim3(static_cast<unsigned>(by_tile > 0 ? a.num_seqs * tiles : grid), static_cast<unsigned>(a.H),
-                       by_tile > 0 ? pairs : (pairs + 3) / 4);
-    cfg.blockDim = dim3(kDcThreads, 1, 1);
+    // Few parts each: a warp a pair, so that the CTAs fit at once (64 sequences of 8 heads x 4 pairs: 2,048 CTAs were two
+    // waves); many: eight warps a pair (sixteen fit two CTAs an SM, again two waves); else four.
+    const int segments = a.num_seqs * tiles, share = by_tile == 0 ? 4 : (grid >= 12 * segments ? 8 : (grid < 4 * segments ? 1 : 4));
+    cfg.gridDim = dim3(static_cast<unsigned>(by_tile > 0 ? segments : grid), static_cast<unsigned>(a.H),
+                       by_tile > 0 && share > 1 ? pairs : (pairs + 3) / 4);
+    cfg.blockDim = dim3(share == 8 ? 256 : 128, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, dense_combine_kernel, a, grid, by_tile);
+    auto* combine = share == 8 ? dense_combine_kernel<256, 8> : (share == 4 ? dense_combine_kernel<128, 4> : dense_combine_kernel<128, 1>);
+    return cudaLaunchKernelEx(&cfg, combine, a, grid, by_tile);
 }
 
 // CTAs for so many units: one a SM at most, and at least two tiles each (fewer parts to join, the same latency).

@@ -228,7 +228,7 @@ struct DenseArgs {
     int2* split_head;      // prompts, windows: items that are split over their keys, parts of each
     int4* split_items;     // [places] those items
     int pairs_most;        // decode family: most (row, head) pairs of a sequence that its kernel takes
-    int32_t* unit_prefix;  // [num_seqs + 1] decode family: units before each sequence
+    int32_t* unit_prefix;  // [2][num_seqs + 1] decode family: units, and segments, before each sequence
     float* part_o;         // parts of what several CTAs walk: O [.., 128], decode family [2 shares, H, 16]
     float* part_ml;        // and their maxima and sums [.., 2]
     uint32_t* err_slots;   // [shares] error bits of the decode family's CTAs

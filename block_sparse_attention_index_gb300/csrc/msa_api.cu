@@ -274,7 +274,7 @@ DenseLayout dense_layout(const msa_problem* p, const DensePlan& d) {
     l.err_slots = off;
     off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
     l.unit_prefix = off;
-    off = align256(off + (static_cast<size_t>(p->num_seqs) + 1) * sizeof(int32_t));
+    off = align256(off + 2 * (static_cast<size_t>(p->num_seqs) + 1) * sizeof(int32_t));
     l.split = off;  // the head, then the items
     off = align256(off + (1 + msa::kDenseMaxShares) * sizeof(int4));
     l.part_ml = off;
