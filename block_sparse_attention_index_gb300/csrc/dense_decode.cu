@@ -153,6 +153,11 @@ __device__ __forceinline__ int64_t dd_cut(int64_t line, int extra, int c, int sh
     return extra + n * c / shares;
 }
 
+__device__ __forceinline__ int dd_div(int64_t x, int64_t y) {
+    if (((x | y) >> 32) == 0) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+    return static_cast<int>(x / y);
+}
+
 // The tile at position `at` of that line (`extra` is where the next segment begins); b: its sequence, or one before it
 // that has none.
 __device__ __forceinline__ int64_t dd_tile_at(const int32_t* units, const int32_t* segs, int num_seqs, int H, int extra, int64_t at, int& b) {
@@ -819,7 +824,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) dense_combine_kerne
         }
     }
     DdSeq s{};
-    if (early) s = dd_seq(a, lo);
+    int first = 0, last = 0, slot0 = 0;
+    // the shares that hold its first and last tiles (the largest c that begins at or before the tile); the first share's part
+    // is its second one unless the share began with it, the others' are the first of their shares
+    auto find_parts = [&]() {
+        const int64_t total = static_cast<int64_t>(carry) * a.H, line = total + static_cast<int64_t>(seg_carry) * extra;
+        const int shares = dd_shares(total, grid), n_seg = s.blocks * a.H;  // the segment's tiles
+        const int64_t at = static_cast<int64_t>(begin) * a.H + static_cast<int64_t>(seg_begin) * extra + static_cast<int64_t>(mt) * (n_seg + extra);
+        first = dd_div((at + 1) * shares - 1, line - extra);
+        last = dd_div((at + n_seg) * shares - 1, line - extra);
+        slot0 = 2 * first + (dd_cut(line, extra, first, shares) < at ? 1 : 0);
+    };
+    if (early) {
+        s = dd_seq(a, lo);
+        if (units > 0 && mt < s.tiles) find_parts();
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the shares' CTAs found wrong
@@ -831,36 +850,29 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) dense_combine_kerne
             else if (e) atomicOr(a.err, e);
         }
     }
-    const int32_t* segs = a.unit_prefix + a.num_seqs + 1;
     if (!early) {
+        const int32_t* segs = a.unit_prefix + a.num_seqs + 1;
         carry = a.unit_prefix[a.num_seqs];
         seg_carry = segs[a.num_seqs];
-    }
-    const int64_t total = static_cast<int64_t>(carry) * a.H, line = total + static_cast<int64_t>(seg_carry) * extra;
-    const int shares = dd_shares(total, grid);
-    if (by_tile == 0) {
-        if (static_cast<int>(blockIdx.x) + 1 >= shares) return;
-        // the unit of the boundary's tile
-        const int cut = static_cast<int>(dd_tile_at(a.unit_prefix, segs, a.num_seqs, a.H, extra, dd_cut(line, extra, blockIdx.x + 1, shares), lo) / a.H);
-        if (cut >= a.unit_prefix[lo + 1]) return;  // (the end of all)
-        mt = (cut - a.unit_prefix[lo]) / dd_blocks(a.cache_lens[lo]);
-    }
-    if (!early) {
+        if (by_tile == 0) {
+            const int64_t total = static_cast<int64_t>(carry) * a.H, line = total + static_cast<int64_t>(seg_carry) * extra;
+            const int shares = dd_shares(total, grid);
+            if (static_cast<int>(blockIdx.x) + 1 >= shares) return;
+            // the unit of the boundary's tile
+            const int cut = static_cast<int>(dd_tile_at(a.unit_prefix, segs, a.num_seqs, a.H, extra, dd_cut(line, extra, blockIdx.x + 1, shares), lo) / a.H);
+            if (cut >= a.unit_prefix[lo + 1]) return;  // (the end of all)
+            mt = (cut - a.unit_prefix[lo]) / dd_blocks(a.cache_lens[lo]);
+        }
         begin = a.unit_prefix[lo];
         units = a.unit_prefix[lo + 1] - begin;
         seg_begin = segs[lo];
         s = dd_seq(a, lo);
     }
     if (units == 0 || mt >= s.tiles) return;
-    const int n_seg = s.blocks * a.H;  // the segment's tiles; its place on the line, before the extra
-    const int64_t at = static_cast<int64_t>(begin) * a.H + static_cast<int64_t>(seg_begin) * extra + static_cast<int64_t>(mt) * (n_seg + extra);
-    // the shares that hold its first and last tiles: the largest c with line c / shares at or before the tile
-    const int first = static_cast<int>(((at + 1) * shares - 1) / (line - extra)), last = static_cast<int>(((at + n_seg) * shares - 1) / (line - extra));
+    if (!early) find_parts();
     // one share wrote it whole; the boundary lies between two of them, or an earlier one inside it has its CTA
     if (first == last || (by_tile == 0 && first != static_cast<int>(blockIdx.x))) return;
     const int count = last - first + 1;
-    // the first share's part is its second one unless the share began with it; the others' are the first of their shares
-    const int slot0 = 2 * first + (dd_cut(line, extra, first, shares) < at ? 1 : 0);
     const int mine = warp % kShare, i_begin = count * mine / kShare, i_end = count * (mine + 1) / kShare;
     const int pairs = min(16, s.n * a.G - 16 * mt);
     constexpr int kAtOnce = kWarps / kShare;  // pairs
