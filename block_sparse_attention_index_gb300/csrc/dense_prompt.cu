@@ -30,7 +30,7 @@
 // One CTA per SM stays for the launch and takes items (a tile pair and a head), the longest first, as it gets through
 // them (a counter; what an item holds and how it is computed does not depend on who has it).  Barriers, tensor memory and
 // the ring of tiles run on from item to item: the next item's first copies and scores run under the last one's epilogue
-// (a CTA for each item: 890 against 813 us for 4,096 rows at 8,192, 131 against 108 for eight packed prompts of 1 to
+// (a CTA for each item: 890 against 813 us for 4,096 rows at 8,192, 131 against 103 for eight packed prompts of 1 to
 // 2,047 rows).  Items of the last wave, which would leave SMs idle, are split over their keys as well and their parts
 // joined by dense_join_kernel.
 //
@@ -40,15 +40,15 @@
 //
 // What bounds it: bf16, the tensor pipe (4,096 rows at 8,192, 4 x 16 heads: 1.37 TFLOP in 805 to 870 us with the clocks
 // that the power limit leaves, 1.58 to 1.70 PFLOP/s of 1.92 measured for cuBLAS in short bursts, 1.74 sustained); int8
-// with bf16 outputs, the softmax groups' instructions (0.62 TFLOP in 504 us); fp32 outputs, likewise (0.55 TFLOP, with
-// three weight parts 1.1 on the tensor cores, in 968 us); short sequences, the 4 us an item that its groups spend between
+// with bf16 outputs, the softmax groups' instructions (0.62 TFLOP in 515 us); fp32 outputs, likewise (0.55 TFLOP, with
+// three weight parts 1.1 on the tensor cores, in 958 us); short sequences, the 3.5 us an item that its groups spend between
 // its last scores and the next one's first, against 1.6 us a key tile.
 //
 // int8 caches are read from a copy widened once per call.  bf16 outputs: f16 values with the scales in them, over a
 // power of two for each 64-position block (run_widen_f16), queries as f16 times a power of two for each row (converted
 // in shared memory by the softmax threads; bf16's 8 bits fit, what lies 2^-22 below the row's largest loses some) and
 // weights as one f16 (2^-12), at most 2^14: the blocks' powers of two are two scalars each for the softmax, where the
-// scales themselves, one for each key, were a third of its instructions (784 us for 2,048 rows at 8,192, now 504).  fp32 outputs:
+// scales themselves, one for each key, were a third of its instructions (784 us for 2,048 rows at 8,192, now 515).  fp32 outputs:
 // bf16 integers, exact, scales beside them (run_widen_kv); the key scale multiplies the score, the value scale the weight.
 //
 // Values that no row of the tile may see: positions past the length are zeroed in the last value tile (by warp 10), so
