@@ -29,7 +29,8 @@
 //
 // Measured (with the combine): 4 rows at 65,536, 4 x 16 heads, 96 us, 7.08 TB/s while every SM streams (they end 77 to 86
 // us in, the combine 4 us later); 8 int8 sequences of 1,024 to 196,608, 47 us, bound by the 1,670 instructions a tile
-// and warp; 64 sequences of 3 to 4,096, 8 x 4 heads, 43 us, a third of it before the first
+// and warp, two warps a scheduler (41 % of the issue slots taken, waits on the instruction before the rest; registers
+// leave no room for a third); 64 sequences of 3 to 4,096, 8 x 4 heads, 43 us, a third of it before the first
 // tile and after the last.
 #include <algorithm>
 
