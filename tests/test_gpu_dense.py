@@ -156,6 +156,21 @@ def test_many_sequences():
     Batch([(1 + i % 12, 20 + (37 * i) % 200) for i in range(300)], 2, 3, True, 64, torch.bfloat16).check()
 
 
+@pytest.mark.parametrize("count", [2, 12, 40, 130, 150, 255, 256, 300])
+@pytest.mark.parametrize("H,int8", [(1, False), (8, False), (4, True)])
+def test_any_number_of_single_rows(count, H, int8):
+    """Shares that begin and end inside sequences, hold several, or hold none."""
+    Batch([(1, 1 + (7919 * i) % (64 if i % 3 else 2000)) for i in range(count)], H, 4, int8, 64,
+          torch.float32 if count % 4 else torch.bfloat16, seed=count).check()
+
+
+@pytest.mark.parametrize("seqs", [[(8, 900), (1, 64), (8, 8)], [(5, 20000), (8, 3000)], [(8, 70 + i) for i in range(90)]])
+def test_several_tiles_of_rows_a_sequence(seqs):
+    for int8 in (False, True):  # (G = 2: one tile; 16 with an int8 cache: up to eight)
+        for G in (2, 16):
+            Batch(seqs, 2, G, int8, 64, torch.float32, seed=G).check()
+
+
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("G", [6, 16])
