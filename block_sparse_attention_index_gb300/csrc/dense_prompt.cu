@@ -387,23 +387,30 @@ __device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int6
         if (t < end) {
             row = block_row(a.seq_cache, b, t & ~(kBlock - 1));
             row = row < 0 ? 0 : (row + (t & (kBlock - 1))) * a.H + h;
-            if (a.kv_int8) {
-                float acc = 0.f;
-                for (int i = 0; i < kHeadDim; ++i)
-                    acc = fmaf(static_cast<float>(static_cast<const int8_t*>(a.k)[row * kHeadDim + i]),
-                               __uint_as_float(static_cast<uint32_t>(a.q[q_row * kHeadDim + i]) << 16), acc);
-                x = acc * a.seq_k_scale[row] * a.scale_log2;
-            } else {
-            const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + row * kHeadDim);
             const uint4* q = reinterpret_cast<const uint4*>(a.q + q_row * kHeadDim);
             float acc = 0.f;
-            for (int i = 0; i < kHeadDim / 8; ++i) {
-                const uint4 kv = k[i], qv = q[i];
-                acc += bf16_lo(kv.x) * bf16_lo(qv.x) + bf16_hi(kv.x) * bf16_hi(qv.x) + bf16_lo(kv.y) * bf16_lo(qv.y) +
-                       bf16_hi(kv.y) * bf16_hi(qv.y) + bf16_lo(kv.z) * bf16_lo(qv.z) + bf16_hi(kv.z) * bf16_hi(qv.z) +
-                       bf16_lo(kv.w) * bf16_lo(qv.w) + bf16_hi(kv.w) * bf16_hi(qv.w);
-            }
-            x = acc * a.scale_log2;
+            if (a.kv_int8) {
+                const uint4* k = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.k) + row * kHeadDim);
+#pragma unroll 2
+                for (int i = 0; i < kHeadDim / 16; ++i) {
+                    const uint4 kv = k[i], q0 = q[2 * i], q1 = q[2 * i + 1];
+                    const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        acc = fmaf(static_cast<float>(static_cast<int8_t>(kw[e >> 2] >> (8 * (e & 3)))),
+                                   e & 1 ? bf16_hi(qw[e >> 1]) : bf16_lo(qw[e >> 1]), acc);
+                }
+                x = acc * a.seq_k_scale[row] * a.scale_log2;
+            } else {
+                const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + row * kHeadDim);
+#pragma unroll 4
+                for (int i = 0; i < kHeadDim / 8; ++i) {
+                    const uint4 kv = k[i], qv = q[i];
+                    acc += bf16_lo(kv.x) * bf16_lo(qv.x) + bf16_hi(kv.x) * bf16_hi(qv.x) + bf16_lo(kv.y) * bf16_lo(qv.y) +
+                           bf16_hi(kv.y) * bf16_hi(qv.y) + bf16_lo(kv.z) * bf16_lo(qv.z) + bf16_hi(kv.z) * bf16_hi(qv.z) +
+                           bf16_lo(kv.w) * bf16_lo(qv.w) + bf16_hi(kv.w) * bf16_hi(qv.w);
+                }
+                x = acc * a.scale_log2;
             }
         }
         float top = x;
@@ -413,28 +420,60 @@ __device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int6
         l *= f;
         for (int e = 0; e < 4; ++e) o[e] *= f;
         m = top;
-        for (int i = 0; i < 32 && u0 + i < end; ++i) {
-            const float pi = __shfl_sync(0xffffffffu, p, i);
-            const int64_t ri = __shfl_sync(0xffffffffu, row, i);
-            float v[4];
-            if (a.kv_int8) {
-                const char4 v8 = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.v) + ri * kHeadDim + 4 * lane);
-                const float f8 = a.seq_v_scale[ri];
-                v[0] = v8.x * f8;
-                v[1] = v8.y * f8;
-                v[2] = v8.z * f8;
-                v[3] = v8.w * f8;
-            } else {
-                const uint2 vw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + ri * kHeadDim + 4 * lane);
-                v[0] = bf16_lo(vw.x);
-                v[1] = bf16_hi(vw.x);
-                v[2] = bf16_lo(vw.y);
-                v[3] = bf16_hi(vw.y);
+        for (int i0 = 0; i0 < 32 && u0 + i0 < end; i0 += 8) {  // eight values in flight
+            float v[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // (past the end: row 0, not added)
+                const int64_t ri = __shfl_sync(0xffffffffu, row, i0 + i);
+                if (a.kv_int8) {
+                    const char4 v8 = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.v) + ri * kHeadDim + 4 * lane);
+                    const float f8 = a.seq_v_scale[ri];
+                    v[i][0] = v8.x * f8;
+                    v[i][1] = v8.y * f8;
+                    v[i][2] = v8.z * f8;
+                    v[i][3] = v8.w * f8;
+                } else {
+                    const uint2 vw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + ri * kHeadDim + 4 * lane);
+                    v[i][0] = bf16_lo(vw.x);
+                    v[i][1] = bf16_hi(vw.x);
+                    v[i][2] = bf16_lo(vw.y);
+                    v[i][3] = bf16_hi(vw.y);
+                }
             }
-            l += pi;
-            for (int e = 0; e < 4; ++e) o[e] = fmaf(pi, v[e], o[e]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float pi = __shfl_sync(0xffffffffu, p, i0 + i);
+                if (u0 + i0 + i >= end) break;
+                l += pi;
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(pi, v[i][e], o[e]);
+            }
         }
     }
+}
+
+// The last of the positions [first, end) whose value is not finite, -1 if all are (a whole warp).
+__device__ __noinline__ int dp_last_bad(const DenseArgs& a, int b, int h, int first, int end) {
+    int bad = -1;
+    for (int t = first + static_cast<int>(threadIdx.x & 31); t < end; t += 32) {
+        int64_t row = block_row(a.seq_cache, b, t & ~(kBlock - 1));
+        if (row < 0) continue;
+        row = (row + (t & (kBlock - 1))) * a.H + h;
+        bool is = false;
+        if (a.kv_int8) {
+            is = !(fabsf(a.seq_v_scale[row]) < INFINITY);
+        } else {
+            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v) + row * kHeadDim);
+#pragma unroll 4
+            for (int i = 0; i < kHeadDim / 8; ++i) {
+                const uint4 x = v[i];
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) is |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+            }
+        }
+        if (is) bad = t;
+    }
+    return __reduce_max_sync(0xffffffffu, bad);
 }
 
 template <int kParts, int kForm, bool kAlt>
@@ -685,95 +724,95 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 };
                 bool ok = true, issued = false;
                 for (int k = 0; ok; ++k) {
-                DpItem item;
-                ok = next_item(k, item);
-                if (!ok) break;
-                mbar_arrive(&sm.info_empty[k % kDpInfo]);
-                if (item.b < 0) break;
-                const DpWork w = dp_work<kAlt, NK>(P, item);
-                const int count = s == 0 ? w.count[0] : w.count[1], others = s == 0 ? w.count[1] : w.count[0];
-                // S_s = Q_s K^T from ring slot st; `pass`: the other stage's turn begins while the last of them run
-                auto scores = [&](int st, bool last, bool pass) {
-                    const uint64_t kb = kd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        tc_mma_ss(tmem + s * 128 + kSAt, qd + static_cast<uint64_t>(((i >> 2) * (kDpQBytes / 2) + (i & 3) * 32) >> 4),
-                                  kb + static_cast<uint64_t>(((i >> 2) * kHalf + (i & 3) * 32) >> 4), idesc_s, i > 0);
-                        if (i == 5 && pass) mbar_arrive(&sm.turn[s ^ 1]);
-                    }
-                    tc_commit(&sm.s_full[s]);
-                    if (!kAlt && last) tc_commit(&sm.q_empty);  // the last products with this item's queries
-                    tc_commit(&sm.empty[st]);
-                };
-                // (waited for without tiles too: a barrier's phases have to be seen one by one, and the stage's group may
-                // be converting the queries)
-                ok = mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, k & 1, a.err);
-                if (!ok) break;
-                if constexpr (kAlt) mbar_arrive(&sm.q_empty);  // (seen; group 0 arrives when the products are done)
-                if (count > 0) {
-                    ok = landed();
+                    DpItem item;
+                    ok = next_item(k, item);
                     if (!ok) break;
-                    issued = true;
-                    tc_fence_after();
-                    scores(kAlt ? (slots + slot_k(j0)) % kStages : bar, count == 1, false);
-                    pass_copy();
-                } else if (!kAlt) {
-                    mbar_arrive(&sm.q_empty);
-                }
-                // the other stage is through with its last item: its turns have been taken
-                if (k > 0) ok = mbar_wait(&sm.item_done, (k - 1) & 1, a.err);
-                for (int c = 0; ok && c < count; ++c) {
-                    // the stages take turns: values of tile c, scores of the next (whatever can be waited for is, first)
-                    const int j = j0 + kStep * c;
-                    const uint32_t phase = (tiles + c) & 1;
-                    const bool next = c + 1 < count;
-                    ok = landed();
-                    const int st_v = kAlt ? (slots + slot_v(w, j)) % kStages : bar;
-                    pass_copy();
-                    ok = ok && (!next || landed());
-                    const int st_k = kAlt ? (slots + slot_k(j + kStep)) % kStages : bar;
-                    if (next) pass_copy();
-                    const bool turns_now = s == 0 ? c > 0 && c <= others : c < others;
-                    const bool pass = s == 0 ? c < others : c + 1 < others;
-                    const uint64_t vb = vd + static_cast<uint64_t>(st_v * (Cfg::kTile >> 4));
-                    ok = ok && mbar_wait(&sm.p_full[s][0], phase, a.err);
-                    if (ok && turns_now) ok = mbar_wait(&sm.turn[s], turns++ & 1, a.err);
-                    if (!ok) break;
-                    tc_fence_after();
+                    mbar_arrive(&sm.info_empty[k % kDpInfo]);
+                    if (item.b < 0) break;
+                    const DpWork w = dp_work<kAlt, NK>(P, item);
+                    const int count = s == 0 ? w.count[0] : w.count[1], others = s == 0 ? w.count[1] : w.count[0];
+                    // S_s = Q_s K^T from ring slot st; `pass`: the other stage's turn begins while the last of them run
+                    auto scores = [&](int st, bool last, bool pass) {
+                        const uint64_t kb = kd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
 #pragma unroll
-                    for (int h2 = 0; h2 < NK / 64; ++h2) {  // O_s += P_s V, the second 64 keys as soon as their weights are there
-                        if (h2 == 1) {
-                            ok = mbar_wait(&sm.p_full[s][1], phase, a.err);
-                            if (!ok) break;
-                            tc_fence_after();
+                        for (int i = 0; i < 8; ++i) {
+                            tc_mma_ss(tmem + s * 128 + kSAt, qd + static_cast<uint64_t>(((i >> 2) * (kDpQBytes / 2) + (i & 3) * 32) >> 4),
+                                      kb + static_cast<uint64_t>(((i >> 2) * kHalf + (i & 3) * 32) >> 4), idesc_s, i > 0);
+                            if (i == 5 && pass) mbar_arrive(&sm.turn[s ^ 1]);
                         }
-#pragma unroll
-                        for (int part = 0; part < kParts; ++part)
-#pragma unroll
-                            for (int i = 4 * h2; i < 4 * h2 + 4; ++i)
-                                dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + i * 8,
-                                          vb + static_cast<uint64_t>(i * 2048 >> 4), idesc_o,
-                                          !((kParts > 1 ? (c & 1) == 0 : c == 0) && part == 0 && i == 0));
-                    }
+                        tc_commit(&sm.s_full[s]);
+                        if (!kAlt && last) tc_commit(&sm.q_empty);  // the last products with this item's queries
+                        tc_commit(&sm.empty[st]);
+                    };
+                    // (waited for without tiles too: a barrier's phases have to be seen one by one, and the stage's group may
+                    // be converting the queries)
+                    ok = mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, k & 1, a.err);
                     if (!ok) break;
-                    if (next) {
-                        scores(st_k, c + 2 == count, pass);
-                    } else {
-                        if (pass) mbar_arrive(&sm.turn[s ^ 1]);
-                        tc_commit(&sm.o_full[s]);
-                    }
-                    tc_commit(&sm.empty[st_v]);
-                }
-                if constexpr (!kAlt) {  // tiles that only the other stage needs
-                    for (int j = 2 * count; ok && j < 2 * w.total; ++j) {
+                    if constexpr (kAlt) mbar_arrive(&sm.q_empty);  // (seen; group 0 arrives when the products are done)
+                    if (count > 0) {
                         ok = landed();
-                        if (ok) mbar_arrive(&sm.empty[bar]);
+                        if (!ok) break;
+                        issued = true;
+                        tc_fence_after();
+                        scores(kAlt ? (slots + slot_k(j0)) % kStages : bar, count == 1, false);
                         pass_copy();
+                    } else if (!kAlt) {
+                        mbar_arrive(&sm.q_empty);
                     }
-                }
-                slots += 2 * w.total;
-                tiles += count;
-                if (ok) mbar_arrive(&sm.item_done);
+                    // the other stage is through with its last item: its turns have been taken
+                    if (k > 0) ok = mbar_wait(&sm.item_done, (k - 1) & 1, a.err);
+                    for (int c = 0; ok && c < count; ++c) {
+                        // the stages take turns: values of tile c, scores of the next (whatever can be waited for is, first)
+                        const int j = j0 + kStep * c;
+                        const uint32_t phase = (tiles + c) & 1;
+                        const bool next = c + 1 < count;
+                        ok = landed();
+                        const int st_v = kAlt ? (slots + slot_v(w, j)) % kStages : bar;
+                        pass_copy();
+                        ok = ok && (!next || landed());
+                        const int st_k = kAlt ? (slots + slot_k(j + kStep)) % kStages : bar;
+                        if (next) pass_copy();
+                        const bool turns_now = s == 0 ? c > 0 && c <= others : c < others;
+                        const bool pass = s == 0 ? c < others : c + 1 < others;
+                        const uint64_t vb = vd + static_cast<uint64_t>(st_v * (Cfg::kTile >> 4));
+                        ok = ok && mbar_wait(&sm.p_full[s][0], phase, a.err);
+                        if (ok && turns_now) ok = mbar_wait(&sm.turn[s], turns++ & 1, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int h2 = 0; h2 < NK / 64; ++h2) {  // O_s += P_s V, the second 64 keys as soon as their weights are there
+                            if (h2 == 1) {
+                                ok = mbar_wait(&sm.p_full[s][1], phase, a.err);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                                for (int i = 4 * h2; i < 4 * h2 + 4; ++i)
+                                    dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + i * 8,
+                                              vb + static_cast<uint64_t>(i * 2048 >> 4), idesc_o,
+                                              !((kParts > 1 ? (c & 1) == 0 : c == 0) && part == 0 && i == 0));
+                        }
+                        if (!ok) break;
+                        if (next) {
+                            scores(st_k, c + 2 == count, pass);
+                        } else {
+                            if (pass) mbar_arrive(&sm.turn[s ^ 1]);
+                            tc_commit(&sm.o_full[s]);
+                        }
+                        tc_commit(&sm.empty[st_v]);
+                    }
+                    if constexpr (!kAlt) {  // tiles that only the other stage needs
+                        for (int j = 2 * count; ok && j < 2 * w.total; ++j) {
+                            ok = landed();
+                            if (ok) mbar_arrive(&sm.empty[bar]);
+                            pass_copy();
+                        }
+                    }
+                    slots += 2 * w.total;
+                    tiles += count;
+                    if (ok) mbar_arrive(&sm.item_done);
                 }
                 if (issued) {  // every matrix instruction done before tensor memory is given back
                     tc_commit(&sm.drain[s]);
@@ -792,458 +831,466 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         int tiles = 0, tiles_before = 0, done = 0;  // running: the stage's tiles, the items' key tiles, items the stage had tiles of
         bool alive = true;
         for (int k = 0; alive; ++k) {
-        DpItem item;
-        alive = __all_sync(0xffffffffu, next_item(k, item));
-        if constexpr (kAlt) alive = dp_sync_and(alive);  // (the groups meet in the epilogue: both come, or neither)
-        if (!alive) break;
-        if (item.b < 0) break;
-        const DpWork w = dp_work<kAlt, NK>(128 / a.G, item);
-        const int h = item.h;
-        const int pos = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, w.n - 1);
-        // the tile's earliest position: key tiles up to it hide nothing
-        const int early = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P), w.n - 1);
-        const int count = s == 0 ? w.count[0] : w.count[1];
-        float row_f = a.scale_log2;  // factor from the row's products to the log2 domain
-        if constexpr (kF16 || kAlt) alive = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, k & 1, a.err));
-        if constexpr (kF16) {
-            // the row's queries to f16: its largest value into [2^8, 2^9)
+            DpItem item;
+            alive = __all_sync(0xffffffffu, next_item(k, item));
+            if constexpr (kAlt) alive = dp_sync_and(alive);  // (the groups meet in the epilogue: both come, or neither)
             if (!alive) break;
-            uint8_t* row = sm.q[s] + m * 128;
-            auto chunk = [&](int c) { return reinterpret_cast<uint4*>(row + (c >> 3) * (kDpQBytes / 2) + (((c & 7) ^ (m & 7)) << 4)); };
-            uint32_t big = 0;  // largest magnitude as bits
+            if (item.b < 0) break;
+            const DpWork w = dp_work<kAlt, NK>(128 / a.G, item);
+            const int h = item.h;
+            const int pos = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, w.n - 1);
+            // the tile's earliest position: key tiles up to it hide nothing
+            const int early = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P), w.n - 1);
+            const int count = s == 0 ? w.count[0] : w.count[1];
+            float row_f = a.scale_log2;  // factor from the row's products to the log2 domain
+            if constexpr (kF16 || kAlt) alive = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, k & 1, a.err));
+            if constexpr (kF16) {
+                // the row's queries to f16: its largest value into [2^8, 2^9)
+                if (!alive) break;
+                uint8_t* row = sm.q[s] + m * 128;
+                auto chunk = [&](int c) { return reinterpret_cast<uint4*>(row + (c >> 3) * (kDpQBytes / 2) + (((c & 7) ^ (m & 7)) << 4)); };
+                uint32_t big = 0;  // largest magnitude as bits
 #pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                const uint4 v = *chunk(c);
-                const uint32_t qw[4] = {v.x, v.y, v.z, v.w};
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 v = *chunk(c);
+                    const uint32_t qw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) big = max(big, max((qw[e] << 16) & 0x7fff0000u, qw[e] & 0x7fff0000u));
-            }
-            const uint32_t ex = min(max(big >> 23, 9u), 253u);
-            const float up = __uint_as_float((262u - ex) << 23);  // 2^(8 - exponent)
-            row_f *= __uint_as_float((ex - 8u) << 23);
+                    for (int e = 0; e < 4; ++e) big = max(big, max((qw[e] << 16) & 0x7fff0000u, qw[e] & 0x7fff0000u));
+                }
+                const uint32_t ex = min(max(big >> 23, 9u), 253u);
+                const float up = __uint_as_float((262u - ex) << 23);  // 2^(8 - exponent)
+                row_f *= __uint_as_float((ex - 8u) << 23);
 #pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                const uint4 v = *chunk(c);
-                *chunk(c) = make_uint4(dp_pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), dp_pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
-                                       dp_pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), dp_pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+                for (int c = 0; c < 16; ++c) {
+                    const uint4 v = *chunk(c);
+                    *chunk(c) = make_uint4(dp_pack_f16(bf16_lo(v.x) * up, bf16_hi(v.x) * up), dp_pack_f16(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                                           dp_pack_f16(bf16_lo(v.z) * up, bf16_hi(v.z) * up), dp_pack_f16(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.q_turned[s]);
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.q_turned[s]);
-        }
-        // f16 form: factors (products, value sums) of the key tile's blocks, loaded a tile ahead; the power of two that
-        // O is kept in units of (not below any value block's so far)
-        const float2* fac = kF16 ? a.wide_fac + (static_cast<int64_t>(h) * a.cache_tokens + a.cache.starts[w.b]) / kBlock : nullptr;
-        float2 fac_now[2], fac_next[2];
-        auto load_fac = [&](int c, float2 (&x)[2]) {
+            // f16 form: factors (products, value sums) of the key tile's blocks, loaded a tile ahead; the power of two that
+            // O is kept in units of (not below any value block's so far)
+            const float2* fac = kF16 ? a.wide_fac + (static_cast<int64_t>(h) * a.cache_tokens + a.cache.starts[w.b]) / kBlock : nullptr;
+            float2 fac_now[2], fac_next[2];
+            auto load_fac = [&](int c, float2 (&x)[2]) {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int blk = 2 * (w.first + c) + y;
-                x[y] = blk * kBlock < w.L ? fac[blk] : make_float2(0.f, 0.f);
-            }
-        };
-        if constexpr (kF16) load_fac(0, fac_next);
-        int vexp = 0;  // its exponent, biased (the factors are powers of two, 2^-118 .. 2^119; 0: none yet)
-        auto power = [](int e) { return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23); };  // 2^e, e < 128
-        bool coarse = false;  // some block's values were 2^-12 or less of another's: small weights may have lost bits
-        constexpr float kLift = kF16 ? 6.f : 0.f;  // f16 weights: at most 2^(6 + 8)
-        float top = -INFINITY, sum = 0.f;  // maximum in use (log2 domain), sum of weights
-        float acc[kParts > 1 ? kHeadDim : 1];  // fp32 outputs: O of the row
-        if constexpr (kParts > 1) {
-#pragma unroll
-            for (int k = 0; k < kHeadDim; ++k) acc[k] = 0.f;
-        }
-        auto rescale = [&](float r) {  // O in tensor memory times r
-#pragma unroll 1
-            for (int q = 0; q < kHeadDim / 32; ++q) {
-                float y[32];
-                dp_ld32(o_addr + 32 * q, y);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) y[k] *= r;
-                dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
-            }
-        };
-        auto collect = [&]() {  // adds the last two tiles' product to it
+                for (int y = 0; y < 2; ++y) {
+                    const int blk = 2 * (w.first + c) + y;
+                    x[y] = blk * kBlock < w.L ? fac[blk] : make_float2(0.f, 0.f);
+                }
+            };
+            if constexpr (kF16) load_fac(0, fac_next);
+            int vexp = 0;  // its exponent, biased (the factors are powers of two, 2^-118 .. 2^119; 0: none yet)
+            auto power = [](int e) { return e < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23); };  // 2^e, e < 128
+            bool coarse = false;  // some block's values were 2^-12 or less of another's: small weights may have lost bits
+            constexpr float kLift = kF16 ? 6.f : 0.f;  // f16 weights: at most 2^(6 + 8)
+            float top = -INFINITY, sum = 0.f;  // maximum in use (log2 domain), sum of weights
+            float acc[kParts > 1 ? kHeadDim : 1];  // fp32 outputs: O of the row
             if constexpr (kParts > 1) {
 #pragma unroll
-                for (int q = 0; q < kHeadDim / 16; ++q) {
-                    uint32_t y[16];
-                    tmem_ld16(o_addr + 16 * q, y);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) acc[16 * q + k] += __uint_as_float(y[k]);
-                }
+                for (int k = 0; k < kHeadDim; ++k) acc[k] = 0.f;
             }
-        };
-        for (int c = 0; alive && c < count; ++c) {
-            const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
-            alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], (tiles + c) & 1, a.err));
-            if (!alive) break;
-            tc_fence_after();
-            if (c > 0 && (c & 1) == 0) collect();
-            if constexpr (kParts > 1) {  // ---- fp32 outputs: 32 scores at a time, O in registers (the code below has no room for it)
-                const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
-                const int e = (tiles_before + j) % kDpScaleSlots;
-                if constexpr (kWide) {
-                    alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], ((tiles_before + j) / kDpScaleSlots) & 1, a.err));
-                    if (!alive) break;
-                }
-                // the scores of keys 32 q .. of the tile in the log2 domain (f: what is left to multiply by)
-                const float f = kWide || edge ? 1.f : a.scale_log2;
-                auto scores_of = [&](int q, float (&x)[32]) {
-                    dp_ld32(s_addr + kSAt + 32 * q, x);
+            auto rescale = [&](float r) {  // O in tensor memory times r
+#pragma unroll 1
+                for (int q = 0; q < kHeadDim / 32; ++q) {
+                    float y[32];
+                    dp_ld32(o_addr + 32 * q, y);
                     tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) y[k] *= r;
+                    dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
+                }
+            };
+            auto collect = [&]() {  // adds the last two tiles' product to it
+                if constexpr (kParts > 1) {
+#pragma unroll
+                    for (int q = 0; q < kHeadDim / 16; ++q) {
+                        uint32_t y[16];
+                        tmem_ld16(o_addr + 16 * q, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) acc[16 * q + k] += __uint_as_float(y[k]);
+                    }
+                }
+            };
+            for (int c = 0; alive && c < count; ++c) {
+                const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
+                alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], (tiles + c) & 1, a.err));
+                if (!alive) break;
+                tc_fence_after();
+                if (c > 0 && (c & 1) == 0) collect();
+                if constexpr (kParts > 1) {  // ---- fp32 outputs: 32 scores at a time, O in registers (the code below has no room for it)
+                    const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
+                    const int e = (tiles_before + j) % kDpScaleSlots;
                     if constexpr (kWide) {
+                        alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], ((tiles_before + j) / kDpScaleSlots) & 1, a.err));
+                        if (!alive) break;
+                    }
+                    // the scores of keys 32 q .. of the tile in the log2 domain (f: what is left to multiply by)
+                    const float f = kWide || edge ? 1.f : a.scale_log2;
+                    auto scores_of = [&](int q, float (&x)[32]) {
+                        dp_ld32(s_addr + kSAt + 32 * q, x);
+                        tmem_ld_wait();
+                        if constexpr (kWide) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 ks = *reinterpret_cast<const float4*>(&sm.sc[e][0][32 * q + k]);
-                            x[k] *= ks.x * a.scale_log2;
-                            x[k + 1] *= ks.y * a.scale_log2;
-                            x[k + 2] *= ks.z * a.scale_log2;
-                            x[k + 3] *= ks.w * a.scale_log2;
+                            for (int k = 0; k < 32; k += 4) {
+                                const float4 ks = *reinterpret_cast<const float4*>(&sm.sc[e][0][32 * q + k]);
+                                x[k] *= ks.x * a.scale_log2;
+                                x[k + 1] *= ks.y * a.scale_log2;
+                                x[k + 2] *= ks.z * a.scale_log2;
+                                x[k + 3] *= ks.w * a.scale_log2;
+                            }
                         }
-                    }
-                    if (edge) {
-                        const int seen = pos + 1 - t0 - 32 * q;
+                        if (edge) {
+                            const int seen = pos + 1 - t0 - 32 * q;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = k < seen ? (kWide ? x[k] : x[k] * a.scale_log2) : -INFINITY;
+                            for (int k = 0; k < 32; ++k) x[k] = k < seen ? (kWide ? x[k] : x[k] * a.scale_log2) : -INFINITY;
+                        }
+                    };
+                    float now = -INFINITY;
+                    if (kWide || edge) {
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q) {
+                            float x[32];
+                            scores_of(q, x);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) now = fmaxf(now, x[k]);
+                        }
+                    } else {
+                        tmem_ld_max64(s_addr + kSAt, now);
+                        tmem_ld_wait();
+                        now *= f;
                     }
-                };
-                float now = -INFINITY;
-                if (kWide || edge) {
+                    if (c == 0) {
+                        top = now;
+                    } else if (__any_sync(0xffffffffu, now > top + kDpSlack)) {
+                        const float next = now > top + kDpSlack ? now : top;
+                        const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
+#pragma unroll
+                        for (int k = 0; k < kHeadDim; ++k) acc[k] *= r;
+                        if (c & 1) rescale(r);
+                        sum *= r;
+                        top = next;
+                    }
+                    const float base = top == -INFINITY ? 0.f : top;
+                    const float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+                    float2 add = make_float2(0.f, 0.f);
 #pragma unroll 1
                     for (int q = 0; q < 2; ++q) {
                         float x[32];
                         scores_of(q, x);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) now = fmaxf(now, x[k]);
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), ff, nb);
+                            x[2 * k] = dp_exp2(y.x);
+                            x[2 * k + 1] = dp_exp2(y.y);
+                            add = __fadd2_rn(add, make_float2(x[2 * k], x[2 * k + 1]));
+                        }
+                        if constexpr (kWide) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const float4 vs = *reinterpret_cast<const float4*>(&sm.sc[e][1][32 * q + k]);
+                                // a hidden key's weight stays 0 whatever its scale is
+                                x[k] = edge && x[k] == 0.f ? 0.f : x[k] * vs.x;
+                                x[k + 1] = edge && x[k + 1] == 0.f ? 0.f : x[k + 1] * vs.y;
+                                x[k + 2] = edge && x[k + 2] == 0.f ? 0.f : x[k + 2] * vs.z;
+                                x[k + 3] = edge && x[k + 3] == 0.f ? 0.f : x[k + 3] * vs.w;
+                            }
+                        }
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                pk[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                                if (part + 1 < kParts) {
+                                    x[2 * k] -= bf16_lo(pk[k]);
+                                    x[2 * k + 1] -= bf16_hi(pk[k]);
+                                }
+                            }
+                            dp_st16(s_addr + part * 32 + 16 * q, pk);
+                        }
                     }
+                    sum += add.x + add.y;
+                    dp_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.p_full[s][0]);
+                        if constexpr (kWide) mbar_arrive(&sm.sc_empty[e]);
+                    }
+                    continue;
                 } else {
-                    tmem_ld_max64(s_addr + kSAt, now);
-                    tmem_ld_wait();
-                    now *= f;
+                float x[NK], big[NK / 64];
+#pragma unroll
+                for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
+                float f = row_f;  // x f is the score in the log2 domain (f16 form: times the block's factor)
+                if constexpr (kF16) {
+                    fac_now[0] = fac_next[0];
+                    fac_now[1] = fac_next[1];
+                    if (c + 1 < count) load_fac(c + 1, fac_next);
+                }
+                tmem_ld_wait();
+                const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
+                if (edge) {
+                    const int seen = pos + 1 - t0;
+                    if constexpr (kF16) {
+#pragma unroll
+                        for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * (f * fac_now[k >> 6].x) : -INFINITY;
+                        fac_now[0].x = fac_now[1].x = 1.f;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * f : -INFINITY;
+                    }
+                    f = 1.f;
+                }
+                float now;
+                if (edge) {  // the scores are not those that the load took the maximum of
+                    float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < NK; k += 8)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], fmaxf(x[k + z], x[k + 4 + z]));
+                    now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * f;
+                } else if constexpr (kF16) {
+                    now = fmaxf(big[0] * fac_now[0].x, big[NK / 64 - 1] * fac_now[1].x) * f;
+                } else {
+                    now = (NK == 128 ? fmaxf(big[0], big[NK / 64 - 1]) : big[0]) * f;
+                }
+                int vnew = vexp, vblock[2] = {0, 0};
+                if constexpr (kF16) {  // the same for every row
+                    vblock[0] = static_cast<int>(__float_as_uint(fac_now[0].y) >> 23);
+                    vblock[1] = static_cast<int>(__float_as_uint(fac_now[1].y) >> 23);
+                    vnew = max(vexp, max(vblock[0], vblock[1]));
                 }
                 if (c == 0) {
                     top = now;
-                } else if (__any_sync(0xffffffffu, now > top + kDpSlack)) {
+                } else if (__any_sync(0xffffffffu, now > top + kDpSlack) || (kF16 && vnew > vexp)) {
+                    // the maximum grew: the warp's rows of O in tensor memory (no product runs on it now: S of this tile
+                    // was computed after the last one) and their sums move to the new one
                     const float next = now > top + kDpSlack ? now : top;
                     const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
-#pragma unroll
-                    for (int k = 0; k < kHeadDim; ++k) acc[k] *= r;
-                    if (c & 1) rescale(r);
+                    const float ro = kF16 ? r * power(vexp - vnew) : r;
+                    if constexpr (kF16) coarse |= vexp - vnew < -12;
+                    rescale(ro);
                     sum *= r;
                     top = next;
                 }
+                if constexpr (kF16) vexp = vnew;
                 const float base = top == -INFINITY ? 0.f : top;
-                const float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
-                float2 add = make_float2(0.f, 0.f);
-#pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    float x[32];
-                    scores_of(q, x);
+                float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+                float back[2] = {1.f, 1.f};  // f16 form: from a block's weights, in units of its values, to plain ones
+                float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), ff, nb);
-                        x[2 * k] = dp_exp2(y.x);
-                        x[2 * k + 1] = dp_exp2(y.y);
-                        add = __fadd2_rn(add, make_float2(x[2 * k], x[2 * k + 1]));
-                    }
-                    if constexpr (kWide) {
-#pragma unroll
-                        for (int k = 0; k < 32; k += 4) {
-                            const float4 vs = *reinterpret_cast<const float4*>(&sm.sc[e][1][32 * q + k]);
-                            // a hidden key's weight stays 0 whatever its scale is
-                            x[k] = edge && x[k] == 0.f ? 0.f : x[k] * vs.x;
-                            x[k + 1] = edge && x[k + 1] == 0.f ? 0.f : x[k + 1] * vs.y;
-                            x[k + 2] = edge && x[k + 2] == 0.f ? 0.f : x[k + 2] * vs.z;
-                            x[k + 3] = edge && x[k + 3] == 0.f ? 0.f : x[k + 3] * vs.w;
-                        }
+                for (int h2 = 0; h2 < NK / 64; ++h2) {  // 64 keys at a time: the products with them start while the next are made
+                    int unit = 0;  // f16 form: the block's value factor over the one that O is kept in, log2 (at most 0)
+                    bool folded = true;
+                    if constexpr (kF16) {
+                        // weight 2^(x - base + 6) times 2^unit: an exponent's addition, and taken out of the sum again, unless it
+                        // is too small for that (a block of tiny scales; the same for the whole CTA)
+                        if (vblock[h2] > 0) unit = vblock[h2] - vexp;
+                        folded = unit >= -60;
+                        coarse |= unit < -12;
+                        const float up = kLift + (folded ? static_cast<float>(unit) : 0.f);
+                        ff = make_float2(f * fac_now[h2].x, f * fac_now[h2].x);
+                        nb = make_float2(up - base, up - base);
+                        back[h2] = folded ? power(-unit) : 1.f;
                     }
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part) {
-                        uint32_t pk[16];
+                    for (int q = 0; q < 2; ++q) {
+                        float* z = x + 64 * h2 + 32 * q;
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            pk[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
-                            if (part + 1 < kParts) {
-                                x[2 * k] -= bf16_lo(pk[k]);
-                                x[2 * k + 1] -= bf16_hi(pk[k]);
+                            const float2 y = __ffma2_rn(make_float2(z[2 * k], z[2 * k + 1]), ff, nb);
+                            z[2 * k] = dp_exp2(y.x);
+                            z[2 * k + 1] = dp_exp2(y.y);
+                            add[kF16 ? h2 : k & 1] = __fadd2_rn(add[kF16 ? h2 : k & 1], make_float2(z[2 * k], z[2 * k + 1]));
+                        }
+                        if (kF16 && !folded) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) z[k] *= power(unit);
+                        }
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            pk[k] = kF16 ? dp_pack_f16(z[2 * k], z[2 * k + 1]) : pack_bf16x2(z[2 * k], z[2 * k + 1]);
+                        dp_st16(s_addr + 32 * h2 + 16 * q, pk);
+                    }
+                    dp_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[s][h2]);
+                }
+                sum += (add[0].x + add[0].y) * back[0] + (add[1].x + add[1].y) * back[1];
+                }
+            }
+            // (the item is read again here, so that the loop over its tiles need not keep it in registers)
+            {
+                const DpItem item = sm.info[k % kDpInfo];
+                const DpWork w = dp_work<kAlt, NK>(128 / a.G, item);
+                const int h = item.h, count = s == 0 ? w.count[0] : w.count[1];
+                const int i = w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, g = m % a.G;
+                const bool mine = m < w.P * a.G && i < w.n;
+                const int pos = w.L - w.n + min(i, w.n - 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.info_empty[k % kDpInfo]);
+                if constexpr (kWide) {  // scales of tiles that only the other group needs
+                    for (int j = tiles_before + count; alive && j < tiles_before + w.total; ++j) {
+                        alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[j % kDpScaleSlots], (j / kDpScaleSlots) & 1, a.err));
+                        if (alive && lane == 0) mbar_arrive(&sm.sc_empty[j % kDpScaleSlots]);
+                    }
+                }
+                // ---------------- epilogue
+                bool have = count > 0;
+                if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], done++ & 1, a.err));
+                tc_fence_after();
+                if (alive && have) collect();
+                constexpr int kRun = 32;  // values of the row that are finished at a time
+                auto row_of_o = [&](int q, float (&y)[kRun]) {
+                    if constexpr (kParts > 1) {
+#pragma unroll
+                        for (int k = 0; k < kRun; ++k) y[k] = acc[kRun * q + k];
+                    } else {
+                        dp_ld32(o_addr + kRun * q, y);
+                        tmem_ld_wait();
+                    }
+                };
+                float f0 = 1.f, f1 = 0.f;
+                float* other = reinterpret_cast<float*>(&sm.q[0][0]);  // [128 dims][128 rows]
+                if constexpr (kAlt) {
+                    // the second stream's state goes through the query buffers, once both streams' products are done (where a wait
+                    // gave up, all 256 threads stop here together)
+                    alive = dp_sync_and(alive);
+                    if (!alive) break;
+                    if (s == 1 && have) {
+#pragma unroll(kParts > 1 ? 4 : 1)
+                        for (int q = 0; q < kHeadDim / kRun; ++q) {
+                            float y[kRun];
+                            row_of_o(q, y);
+#pragma unroll
+                            for (int k = 0; k < kRun; ++k) other[(kRun * q + k) * 128 + m] = y[k];
+                        }
+                    }
+                    if (s == 1) sm.other_ml[m] = make_float2(have ? top : -INFINITY, have ? sum : 0.f);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the next item's queries land here)
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    if (s == 0 && w.count[1] > 0) {
+                        const float2 ml = sm.other_ml[m];
+                        const float t2 = fmaxf(top, ml.x);
+                        f0 = top == -INFINITY ? 0.f : dp_exp2(top - t2);
+                        f1 = ml.x == -INFINITY ? 0.f : dp_exp2(ml.x - t2);
+                        sum = sum * f0 + ml.y * f1;
+                        top = t2;
+                    }
+                }
+                const bool split_up = item.nsplit > 1;
+                if (alive && (have || split_up) && !(kAlt && s == 1)) {  // (kAlt: group 0 writes)
+                    constexpr int kRows = kAlt ? 128 : 256;  // rows of an item's part
+                    const int64_t q_row = (static_cast<int64_t>(w.c0 + min(i, w.n - 1)) * a.H + h) * a.G + g;
+                    const int64_t part_row = static_cast<int64_t>(item.part) * kRows + s * 128 + m;
+                    float most = 0.f;  // f16 form: the row's largest value, in units of w x V16
+                    bool spoiled = false;  // some value of the row is not finite
+                    const float vref = kF16 ? __uint_as_float(static_cast<uint32_t>(vexp) << 23) : 1.f;
+                    const float inv = kF16 ? vref / sum : 1.f / sum;  // (parts: O in plain units, as their join expects)
+                    if (have) {
+                        const float to = split_up ? (kF16 ? vref : 1.f) : inv;
+#pragma unroll(kParts > 1 ? 4 : 1)
+                        for (int q = 0; q < kHeadDim / kRun; ++q) {
+                            float y[kRun];
+                            row_of_o(q, y);
+                            if constexpr (kAlt) {
+                                if (w.count[1] > 0) {
+#pragma unroll
+                                    for (int k = 0; k < kRun; ++k) y[k] = y[k] * f0 + other[(kRun * q + k) * 128 + m] * f1;
+                                }
+                            }
+                            float2 zero[4] = {};  // 0 unless a value is infinite or NaN
+#pragma unroll
+                            for (int k = 0; k < kRun; k += 8)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    zero[e] = __ffma2_rn(make_float2(y[k + 2 * e], y[k + 2 * e + 1]), make_float2(0.f, 0.f), zero[e]);
+                            spoiled |= !(((zero[0].x + zero[0].y) + (zero[1].x + zero[1].y)) + ((zero[2].x + zero[2].y) + (zero[3].x + zero[3].y)) == 0.f);
+                            if constexpr (kF16) {
+                                float big[4] = {most, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int k = 0; k < kRun; ++k) big[k & 3] = fmaxf(big[k & 3], fabsf(y[k]));
+                                most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+                            }
+#pragma unroll
+                            for (int k = 0; k < kRun; k += 2) {
+                                const float2 z = __fmul2_rn(make_float2(y[k], y[k + 1]), make_float2(to, to));
+                                y[k] = z.x;
+                                y[k + 1] = z.y;
+                            }
+                            if (!mine) {
+                                // (a row of the tile that no query has)
+                            } else if (split_up || !a.out_bf16) {
+                                float* to_row = split_up ? a.part_o + part_row * kHeadDim : static_cast<float*>(a.out) + q_row * kHeadDim;
+                                float4* dst = reinterpret_cast<float4*>(to_row + kRun * q);
+#pragma unroll
+                                for (int k = 0; k < kRun / 4; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                            } else {
+                                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_row * kHeadDim + kRun * q);
+#pragma unroll
+                                for (int k = 0; k < kRun / 8; ++k)
+                                    dst[k] = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                                                        pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
+                            }
+                            __syncwarp();  // the next load is the whole warp's
+                        }
+                    }
+                    if (split_up && mine) *reinterpret_cast<float2*>(a.part_ml + part_row * 2) = make_float2(top, sum);
+                    if constexpr (!kWide) {  // (bf16 integers are finite, and a hidden key's weight ignores its scale)
+                        const int keys = (w.first + (kAlt ? w.total : count)) * NK, end = min(pos + 1, keys);
+                        // only a value past the row's position makes a row wrong that is not finite (the row's own keys and
+                        // values give what the formula gives, and a sum that is not finite is theirs)
+                        spoiled = spoiled && mine && have && fabsf(sum) < INFINITY;
+                        if (__any_sync(0xffffffffu, spoiled)) {
+                            const int least = static_cast<int>(__reduce_min_sync(0xffffffffu, mine ? static_cast<uint32_t>(pos) : 0x7fffffffu));
+                            const int bad = dp_last_bad(a, w.b, h, max(least + 1, w.first * NK), min(keys, w.L));  // (every lane)
+                            spoiled = spoiled && bad > pos;
+                        }
+                        // f16 form: a row that lives on blocks whose values are tiny beside another block's (even one that it
+                        // does not see) has small weights there, off by up to 2^-25 each, L^1/2 2^-12 in units where it has
+                        // 2^10 or more when nothing was lost
+                        if (kF16 && coarse && most < 1024.f) spoiled = fabsf(sum) < INFINITY;
+                        uint32_t again = __ballot_sync(0xffffffffu, mine && spoiled && have);
+                        while (again) {  // these rows once more, by the whole warp
+                            const int from = __ffs(again) - 1;
+                            again &= again - 1;
+                            const int64_t qr = __shfl_sync(0xffffffffu, q_row, from), pr = __shfl_sync(0xffffffffu, part_row, from);
+                            float y[4], m2, l2;
+                            dp_row_again(a, w.b, h, qr, w.first * NK, __shfl_sync(0xffffffffu, end, from), y, m2, l2);
+                            const float f = split_up ? 1.f : 1.f / l2;
+                            if (split_up) {  // (in the units of the other parts' sums)
+                                constexpr float kUnits = kF16 ? 64.f : 1.f;
+                                *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + 4 * lane) =
+                                    make_float4(y[0] * kUnits, y[1] * kUnits, y[2] * kUnits, y[3] * kUnits);
+                                if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m2, l2 * kUnits);
+                            } else if (a.out_bf16) {
+                                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qr * kHeadDim + 4 * lane) =
+                                    make_uint2(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f));
+                            } else {
+                                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + qr * kHeadDim + 4 * lane) =
+                                    make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
                             }
                         }
-                        dp_st16(s_addr + part * 32 + 16 * q, pk);
                     }
                 }
-                sum += add.x + add.y;
-                dp_st_wait();
+                if constexpr (kAlt) {
+                    if (s == 0) {  // the query buffers are free again
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.q_empty);
+                    }
+                }
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sm.p_full[s][0]);
-                    if constexpr (kWide) mbar_arrive(&sm.sc_empty[e]);
-                }
-                continue;
-            } else {
-            float x[NK], big[NK / 64];
-#pragma unroll
-            for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
-            float f = row_f;  // x f is the score in the log2 domain (f16 form: times the block's factor)
-            if constexpr (kF16) {
-                fac_now[0] = fac_next[0];
-                fac_now[1] = fac_next[1];
-                if (c + 1 < count) load_fac(c + 1, fac_next);
+                tiles += count;
+                tiles_before += w.total;
             }
-            tmem_ld_wait();
-            const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
-            if (edge) {
-                const int seen = pos + 1 - t0;
-                if constexpr (kF16) {
-#pragma unroll
-                    for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * (f * fac_now[k >> 6].x) : -INFINITY;
-                    fac_now[0].x = fac_now[1].x = 1.f;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < NK; ++k) x[k] = k < seen ? x[k] * f : -INFINITY;
-                }
-                f = 1.f;
-            }
-            float now;
-            if (edge) {  // the scores are not those that the load took the maximum of
-                float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < NK; k += 8)
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], fmaxf(x[k + z], x[k + 4 + z]));
-                now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * f;
-            } else if constexpr (kF16) {
-                now = fmaxf(big[0] * fac_now[0].x, big[NK / 64 - 1] * fac_now[1].x) * f;
-            } else {
-                now = (NK == 128 ? fmaxf(big[0], big[NK / 64 - 1]) : big[0]) * f;
-            }
-            int vnew = vexp, vblock[2] = {0, 0};
-            if constexpr (kF16) {  // the same for every row
-                vblock[0] = static_cast<int>(__float_as_uint(fac_now[0].y) >> 23);
-                vblock[1] = static_cast<int>(__float_as_uint(fac_now[1].y) >> 23);
-                vnew = max(vexp, max(vblock[0], vblock[1]));
-            }
-            if (c == 0) {
-                top = now;
-            } else if (__any_sync(0xffffffffu, now > top + kDpSlack) || (kF16 && vnew > vexp)) {
-                // the maximum grew: the warp's rows of O in tensor memory (no product runs on it now: S of this tile
-                // was computed after the last one) and their sums move to the new one
-                const float next = now > top + kDpSlack ? now : top;
-                const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
-                const float ro = kF16 ? r * power(vexp - vnew) : r;
-                if constexpr (kF16) coarse |= vexp - vnew < -12;
-                rescale(ro);
-                sum *= r;
-                top = next;
-            }
-            if constexpr (kF16) vexp = vnew;
-            const float base = top == -INFINITY ? 0.f : top;
-            float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
-            float back[2] = {1.f, 1.f};  // f16 form: from a block's weights, in units of its values, to plain ones
-            float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int h2 = 0; h2 < NK / 64; ++h2) {  // 64 keys at a time: the products with them start while the next are made
-                int unit = 0;  // f16 form: the block's value factor over the one that O is kept in, log2 (at most 0)
-                bool folded = true;
-                if constexpr (kF16) {
-                    // weight 2^(x - base + 6) times 2^unit: an exponent's addition, and taken out of the sum again, unless it
-                    // is too small for that (a block of tiny scales; the same for the whole CTA)
-                    if (vblock[h2] > 0) unit = vblock[h2] - vexp;
-                    folded = unit >= -60;
-                    coarse |= unit < -12;
-                    const float up = kLift + (folded ? static_cast<float>(unit) : 0.f);
-                    ff = make_float2(f * fac_now[h2].x, f * fac_now[h2].x);
-                    nb = make_float2(up - base, up - base);
-                    back[h2] = folded ? power(-unit) : 1.f;
-                }
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float* z = x + 64 * h2 + 32 * q;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 y = __ffma2_rn(make_float2(z[2 * k], z[2 * k + 1]), ff, nb);
-                        z[2 * k] = dp_exp2(y.x);
-                        z[2 * k + 1] = dp_exp2(y.y);
-                        add[kF16 ? h2 : k & 1] = __fadd2_rn(add[kF16 ? h2 : k & 1], make_float2(z[2 * k], z[2 * k + 1]));
-                    }
-                    if (kF16 && !folded) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) z[k] *= power(unit);
-                    }
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        pk[k] = kF16 ? dp_pack_f16(z[2 * k], z[2 * k + 1]) : pack_bf16x2(z[2 * k], z[2 * k + 1]);
-                    dp_st16(s_addr + 32 * h2 + 16 * q, pk);
-                }
-                dp_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[s][h2]);
-            }
-            sum += (add[0].x + add[0].y) * back[0] + (add[1].x + add[1].y) * back[1];
-            }
-        }
-        // (the item is read again here, so that the loop over its tiles need not keep it in registers)
-        {
-        const DpItem item = sm.info[k % kDpInfo];
-        const DpWork w = dp_work<kAlt, NK>(128 / a.G, item);
-        const int h = item.h, count = s == 0 ? w.count[0] : w.count[1];
-        const int i = w.i0 + (kAlt ? 0 : s * w.P) + m / a.G, g = m % a.G;
-        const bool mine = m < w.P * a.G && i < w.n;
-        const int pos = w.L - w.n + min(i, w.n - 1);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.info_empty[k % kDpInfo]);
-        if constexpr (kWide) {  // scales of tiles that only the other group needs
-            for (int j = tiles_before + count; alive && j < tiles_before + w.total; ++j) {
-                alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[j % kDpScaleSlots], (j / kDpScaleSlots) & 1, a.err));
-                if (alive && lane == 0) mbar_arrive(&sm.sc_empty[j % kDpScaleSlots]);
-            }
-        }
-        // ---------------- epilogue
-        bool have = count > 0;
-        if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], done++ & 1, a.err));
-        tc_fence_after();
-        if (alive && have) collect();
-        constexpr int kRun = 32;  // values of the row that are finished at a time
-        auto row_of_o = [&](int q, float (&y)[kRun]) {
-            if constexpr (kParts > 1) {
-#pragma unroll
-                for (int k = 0; k < kRun; ++k) y[k] = acc[kRun * q + k];
-            } else {
-                dp_ld32(o_addr + kRun * q, y);
-                tmem_ld_wait();
-            }
-        };
-        float f0 = 1.f, f1 = 0.f;
-        float* other = reinterpret_cast<float*>(&sm.q[0][0]);  // [128 dims][128 rows]
-        if constexpr (kAlt) {
-            // the second stream's state goes through the query buffers, once both streams' products are done (where a wait
-            // gave up, all 256 threads stop here together)
-            alive = dp_sync_and(alive);
-            if (!alive) break;
-            if (s == 1 && have) {
-#pragma unroll(kParts > 1 ? 4 : 1)
-                for (int q = 0; q < kHeadDim / kRun; ++q) {
-                    float y[kRun];
-                    row_of_o(q, y);
-#pragma unroll
-                    for (int k = 0; k < kRun; ++k) other[(kRun * q + k) * 128 + m] = y[k];
-                }
-            }
-            if (s == 1) sm.other_ml[m] = make_float2(have ? top : -INFINITY, have ? sum : 0.f);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the next item's queries land here)
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (s == 0 && w.count[1] > 0) {
-                const float2 ml = sm.other_ml[m];
-                const float t2 = fmaxf(top, ml.x);
-                f0 = top == -INFINITY ? 0.f : dp_exp2(top - t2);
-                f1 = ml.x == -INFINITY ? 0.f : dp_exp2(ml.x - t2);
-                sum = sum * f0 + ml.y * f1;
-                top = t2;
-            }
-        }
-        const bool split_up = item.nsplit > 1;
-        if (alive && (have || split_up) && !(kAlt && s == 1)) {  // (kAlt: group 0 writes)
-            constexpr int kRows = kAlt ? 128 : 256;  // rows of an item's part
-            const int64_t q_row = (static_cast<int64_t>(w.c0 + min(i, w.n - 1)) * a.H + h) * a.G + g;
-            const int64_t part_row = static_cast<int64_t>(item.part) * kRows + s * 128 + m;
-            float most = 0.f;  // f16 form: the row's largest value, in units of w x V16
-            bool spoiled = kAlt && !(fabsf(sum) < INFINITY);  // a product with a value past the row's position that is not finite
-            const float vref = kF16 ? __uint_as_float(static_cast<uint32_t>(vexp) << 23) : 1.f;
-            const float inv = kF16 ? vref / sum : 1.f / sum;  // (parts: O in plain units, as their join expects)
-            if (have) {
-                const float to = split_up ? (kF16 ? vref : 1.f) : inv;
-#pragma unroll(kParts > 1 ? 4 : 1)
-                for (int q = 0; q < kHeadDim / kRun; ++q) {
-                    float y[kRun];
-                    row_of_o(q, y);
-                    if constexpr (kAlt) {
-                        if (w.count[1] > 0) {
-#pragma unroll
-                            for (int k = 0; k < kRun; ++k) y[k] = y[k] * f0 + other[(kRun * q + k) * 128 + m] * f1;
-                        }
-                    }
-                    float2 zero[4] = {};  // 0 unless a value is infinite or NaN
-#pragma unroll
-                    for (int k = 0; k < kRun; k += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            zero[e] = __ffma2_rn(make_float2(y[k + 2 * e], y[k + 2 * e + 1]), make_float2(0.f, 0.f), zero[e]);
-                    spoiled |= !(((zero[0].x + zero[0].y) + (zero[1].x + zero[1].y)) + ((zero[2].x + zero[2].y) + (zero[3].x + zero[3].y)) == 0.f);
-                    if constexpr (kF16) {
-                        float big[4] = {most, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int k = 0; k < kRun; ++k) big[k & 3] = fmaxf(big[k & 3], fabsf(y[k]));
-                        most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-                    }
-#pragma unroll
-                    for (int k = 0; k < kRun; k += 2) {
-                        const float2 z = __fmul2_rn(make_float2(y[k], y[k + 1]), make_float2(to, to));
-                        y[k] = z.x;
-                        y[k + 1] = z.y;
-                    }
-                    if (!mine) {
-                        // (a row of the tile that no query has)
-                    } else if (split_up || !a.out_bf16) {
-                        float* to_row = split_up ? a.part_o + part_row * kHeadDim : static_cast<float*>(a.out) + q_row * kHeadDim;
-                        float4* dst = reinterpret_cast<float4*>(to_row + kRun * q);
-#pragma unroll
-                        for (int k = 0; k < kRun / 4; ++k) dst[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + q_row * kHeadDim + kRun * q);
-#pragma unroll
-                        for (int k = 0; k < kRun / 8; ++k)
-                            dst[k] = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
-                                                pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
-                    }
-                    __syncwarp();  // the next load is the whole warp's
-                }
-            }
-            if (split_up && mine) *reinterpret_cast<float2*>(a.part_ml + part_row * 2) = make_float2(top, sum);
-            // f16 form: a row that lives on blocks whose values are tiny beside another block's (even one that it does
-            // not see) has small weights there, off by up to 2^-25 each, L^1/2 2^-12 in units where it has 2^10 or more
-            // when nothing was lost
-            if (kF16 && coarse && most < 1024.f) spoiled = true;
-            if constexpr (!kWide) {  // (bf16 integers are finite, and a hidden key's weight ignores its scale)
-                uint32_t again = __ballot_sync(0xffffffffu, mine && spoiled && have);
-                const int end = min(pos + 1, (w.first + (kAlt ? w.total : count)) * NK);
-                while (again) {  // these rows once more, by the whole warp
-                    const int from = __ffs(again) - 1;
-                    again &= again - 1;
-                    const int64_t qr = __shfl_sync(0xffffffffu, q_row, from), pr = __shfl_sync(0xffffffffu, part_row, from);
-                    float y[4], m2, l2;
-                    dp_row_again(a, w.b, h, qr, w.first * NK, __shfl_sync(0xffffffffu, end, from), y, m2, l2);
-                    const float f = split_up ? 1.f : 1.f / l2;
-                    if (split_up) {  // (in the units of the other parts' sums)
-                        constexpr float kUnits = kF16 ? 64.f : 1.f;
-                        *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + 4 * lane) =
-                            make_float4(y[0] * kUnits, y[1] * kUnits, y[2] * kUnits, y[3] * kUnits);
-                        if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m2, l2 * kUnits);
-                    } else if (a.out_bf16) {
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qr * kHeadDim + 4 * lane) =
-                            make_uint2(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f));
-                    } else {
-                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + qr * kHeadDim + 4 * lane) =
-                            make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
-                    }
-                }
-            }
-        }
-        if constexpr (kAlt) {
-            if (s == 0) {  // the query buffers are free again
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.q_empty);
-            }
-        }
-        tc_fence_before();
-        tiles += count;
-        tiles_before += w.total;
-        }
         }
     }
     tc_fence_before();

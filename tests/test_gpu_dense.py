@@ -302,6 +302,41 @@ def test_int8_later_tokens_do_not_reach_earlier_rows(n):
             assert not torch.isfinite(after[at:]).all(-1).any()
 
 
+@pytest.mark.parametrize("n", [1, 4, 40, 300])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_values_and_queries_that_are_not_finite_stay_where_they_belong(n, out):
+    b = Batch([(n, 400), (n, 333)], 2, 16, False, 64, out, seed=3)
+    ref, bound = b.ref()
+    rows = b.rows_of(0, torch.arange(400, device="cuda"))
+    b.v[rows[50], 1, 7] = float("inf")  # seen by every row of sequence 0: one value of head 1's outputs
+    b.q[n // 2, 3] = float("nan")       # a query head of one row: all of it
+    got = b.run()
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[:n, 16:, 7] = True
+    bad[n // 2, 3] = True
+    assert not torch.isfinite(got[bad]).any()
+    assert ((got.double() - ref).abs() <= bound)[~bad].all()
+
+
+@pytest.mark.parametrize("n", [40, 4])
+def test_many_rows_that_are_not_finite_over_a_long_context(n):
+    """Nothing is computed twice for them, and a value that only some rows of a chunk see is still told apart."""
+    b = Batch([(n, 1 << 19), (n, 333)], 1, 16, False, 0, torch.bfloat16, seed=3)
+    rows = b.rows_of(0, torch.arange(1 << 19, device="cuda"))
+    b.q[: n // 2] = float("nan")
+    b.v[rows[100], 0, 5] = float("nan")
+    got = b.run()
+    assert not torch.isfinite(got[: n // 2]).any() and not torch.isfinite(got[:n, :, 5]).any()
+    b.q[:n] = torch.randn(n, 16, 128, device="cuda").bfloat16()
+    b.v[rows[100], 0, 5] = 0
+    ref, bound = b.ref()  # (before the infinity, which the plain form would multiply by weights of zero)
+    b.v[rows[(1 << 19) - 2], 0, 9] = float("inf")  # the last two rows see it
+    got = b.run()
+    assert ((got[: n - 2].double() - ref[: n - 2]).abs() <= bound[: n - 2]).all()
+    assert not torch.isfinite(got[n - 2 : n, :, 9]).any()
+    assert ((got[n:].double() - ref[n:]).abs() <= bound[n:]).all()
+
+
 def test_rows_behind_the_last_sequence_stay():
     for seqs in ([(1, 100), (1, 30)], [(20, 100), (5, 30)], [(4, 100)]):
         b = Batch(seqs, 2, 8, spare_rows=7)
