@@ -373,81 +373,133 @@ __device__ __forceinline__ DpWork dp_work(int P, const DpItem& it) {  // P = 128
     return w;
 }
 
-// One row again over keys [first, end), key by key (a whole warp; 4 dimensions a lane): where a product with a later
-// token's infinite or NaN value spoiled the row, or the f16 copy's powers of two left it too few bits.
-__device__ __noinline__ void dp_row_again(const DenseArgs& a, int b, int h, int64_t q_row, int first, int end, float (&o)[4],
-                                          float& m, float& l) {
-    const int lane = threadIdx.x & 31;
-    o[0] = o[1] = o[2] = o[3] = l = 0.f;
-    m = -INFINITY;
-    for (int u0 = first; u0 < end; u0 += 32) {
+// Up to four rows of a warp again over keys [first, end[r]), in fp32: where a product with a later token's infinite or NaN
+// value spoiled them, or the f16 copy's powers of two left them too few bits.  The whole warp, 32 keys at a time: 16
+// lanes share a key's dot products (8 dimensions each, summed by a reduce-scatter over 16 keys), then a lane has a key's
+// scores; 4 dimensions of O a lane.  70 cycles a key and row, bound by the instructions (one row at a time, loads in the
+// order of its keys: 710).
+constexpr int kDpAgain = 4;
+struct DpAgain {
+    int64_t q_row[kDpAgain];
+    int end[kDpAgain];
+    float o[kDpAgain][4], m[kDpAgain], l[kDpAgain];
+};
+template <bool kInt8>
+__device__ __noinline__ void dp_rows_again(const DenseArgs& a, int b, int h, int first, DpAgain& g) {
+    const int lane = threadIdx.x & 31, dl = lane & 15;
+    float q[kDpAgain][8], o[kDpAgain][4], m[kDpAgain], l[kDpAgain];
+    int end[kDpAgain], last = 0;
+#pragma unroll
+    for (int r = 0; r < kDpAgain; ++r) {
+        const uint4 w = *reinterpret_cast<const uint4*>(a.q + g.q_row[r] * kHeadDim + 8 * dl);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            q[r][2 * e] = bf16_lo(ws[e]);
+            q[r][2 * e + 1] = bf16_hi(ws[e]);
+            o[r][e] = 0.f;
+        }
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        end[r] = g.end[r];
+        last = max(last, end[r]);
+    }
+    for (int u0 = first; u0 < last; u0 += 32) {
         const int t = u0 + lane;
-        float x = -INFINITY;
-        int64_t row = 0;
-        if (t < end) {
-            row = block_row(a.seq_cache, b, t & ~(kBlock - 1));
-            row = row < 0 ? 0 : (row + (t & (kBlock - 1))) * a.H + h;
-            const uint4* q = reinterpret_cast<const uint4*>(a.q + q_row * kHeadDim);
-            float acc = 0.f;
-            if (a.kv_int8) {
-                const uint4* k = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.k) + row * kHeadDim);
-#pragma unroll 2
-                for (int i = 0; i < kHeadDim / 16; ++i) {
-                    const uint4 kv = k[i], q0 = q[2 * i], q1 = q[2 * i + 1];
-                    const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w}, qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        int64_t row = 0;  // (past the last key: row 0, not added)
+        float kf = a.scale_log2, vf = 1.f;
+        if (t < last) {
+            const int64_t base = block_row(a.seq_cache, b, t & ~(kBlock - 1));
+            row = base < 0 ? 0 : (base + (t & (kBlock - 1))) * a.H + h;
+            if constexpr (kInt8) {
+                kf *= a.seq_k_scale[row];
+                vf = a.seq_v_scale[row];
+            }
+        }
+        float acc[kDpAgain][16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        acc = fmaf(static_cast<float>(static_cast<int8_t>(kw[e >> 2] >> (8 * (e & 3)))),
-                                   e & 1 ? bf16_hi(qw[e >> 1]) : bf16_lo(qw[e >> 1]), acc);
-                }
-                x = acc * a.seq_k_scale[row] * a.scale_log2;
+        for (int i = 0; i < 16; ++i) {  // keys i and 16 + i
+            const int64_t at = __shfl_sync(0xffffffffu, row, i + (lane & 16)) * kHeadDim + 8 * dl;
+            float k[8];
+            if constexpr (kInt8) {
+                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.k) + at);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) k[e] = static_cast<float>(static_cast<int8_t>((e < 4 ? w.x : w.y) >> (8 * (e & 3))));
             } else {
-                const uint4* k = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + row * kHeadDim);
-#pragma unroll 4
-                for (int i = 0; i < kHeadDim / 8; ++i) {
-                    const uint4 kv = k[i], qv = q[i];
-                    acc += bf16_lo(kv.x) * bf16_lo(qv.x) + bf16_hi(kv.x) * bf16_hi(qv.x) + bf16_lo(kv.y) * bf16_lo(qv.y) +
-                           bf16_hi(kv.y) * bf16_hi(qv.y) + bf16_lo(kv.z) * bf16_lo(qv.z) + bf16_hi(kv.z) * bf16_hi(qv.z) +
-                           bf16_lo(kv.w) * bf16_lo(qv.w) + bf16_hi(kv.w) * bf16_hi(qv.w);
-                }
-                x = acc * a.scale_log2;
+                const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k) + at);
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) k[e] = e & 1 ? bf16_hi(ws[e >> 1]) : bf16_lo(ws[e >> 1]);
+            }
+#pragma unroll
+            for (int r = 0; r < kDpAgain; ++r) {
+                float x = k[0] * q[r][0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) x = fmaf(k[e], q[r][e], x);
+                acc[r][i] = x;
             }
         }
-        float top = x;
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        top = fmaxf(top, m);
-        const float f = m == -INFINITY ? 0.f : dp_exp2(m - top), p = t < end ? dp_exp2(x - top) : 0.f;
-        l *= f;
-        for (int e = 0; e < 4; ++e) o[e] *= f;
-        m = top;
-        for (int i0 = 0; i0 < 32 && u0 + i0 < end; i0 += 8) {  // eight values in flight
-            float v[8][4];
+        float p[kDpAgain];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {  // (past the end: row 0, not added)
-                const int64_t ri = __shfl_sync(0xffffffffu, row, i0 + i);
-                if (a.kv_int8) {
-                    const char4 v8 = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.v) + ri * kHeadDim + 4 * lane);
-                    const float f8 = a.seq_v_scale[ri];
-                    v[i][0] = v8.x * f8;
-                    v[i][1] = v8.y * f8;
-                    v[i][2] = v8.z * f8;
-                    v[i][3] = v8.w * f8;
+        for (int r = 0; r < kDpAgain; ++r) {
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1)
+#pragma unroll
+                for (int i = 0; i < d; ++i) {
+                    const float send = dl & d ? acc[r][i] : acc[r][i + d], keep = dl & d ? acc[r][i + d] : acc[r][i];
+                    acc[r][i] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+                }
+            const float x = t < end[r] ? acc[r][0] * kf : -INFINITY;
+            float top = x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, m[r]);
+            const float f = m[r] == -INFINITY ? 0.f : dp_exp2(m[r] - top);
+            p[r] = t < end[r] ? dp_exp2(x - top) : 0.f;
+            l[r] *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][e] *= f;
+            m[r] = top;
+        }
+        for (int i0 = 0; i0 < 32 && u0 + i0 < last; i0 += 16) {  // sixteen values in flight
+            float v[16][4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int64_t at = __shfl_sync(0xffffffffu, row, i0 + i) * kHeadDim + 4 * lane;
+                if constexpr (kInt8) {
+                    const char4 w = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.v) + at);
+                    const float f = __shfl_sync(0xffffffffu, vf, i0 + i);
+                    v[i][0] = w.x * f;
+                    v[i][1] = w.y * f;
+                    v[i][2] = w.z * f;
+                    v[i][3] = w.w * f;
                 } else {
-                    const uint2 vw = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + ri * kHeadDim + 4 * lane);
-                    v[i][0] = bf16_lo(vw.x);
-                    v[i][1] = bf16_hi(vw.x);
-                    v[i][2] = bf16_lo(vw.y);
-                    v[i][3] = bf16_hi(vw.y);
+                    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + at);
+                    v[i][0] = bf16_lo(w.x);
+                    v[i][1] = bf16_hi(w.x);
+                    v[i][2] = bf16_lo(w.y);
+                    v[i][3] = bf16_hi(w.y);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float pi = __shfl_sync(0xffffffffu, p, i0 + i);
-                if (u0 + i0 + i >= end) break;
-                l += pi;
-                for (int e = 0; e < 4; ++e) o[e] = fmaf(pi, v[i][e], o[e]);
-            }
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+                for (int r = 0; r < kDpAgain; ++r) {
+                    const float w = __shfl_sync(0xffffffffu, p[r], i0 + i);
+                    if (u0 + i0 + i < end[r]) {
+                        l[r] += w;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[r][e] = fmaf(w, v[i][e], o[r][e]);
+                    }
+                }
         }
+    }
+#pragma unroll
+    for (int r = 0; r < kDpAgain; ++r) {
+        g.m[r] = m[r];
+        g.l[r] = l[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g.o[r][e] = o[r][e];
     }
 }
 
@@ -1259,23 +1311,33 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         if (kF16 && coarse && most < 1024.f) spoiled = fabsf(sum) < INFINITY;
                         uint32_t again = __ballot_sync(0xffffffffu, mine && spoiled && have);
                         while (again) {  // these rows once more, by the whole warp
-                            const int from = __ffs(again) - 1;
-                            again &= again - 1;
-                            const int64_t qr = __shfl_sync(0xffffffffu, q_row, from), pr = __shfl_sync(0xffffffffu, part_row, from);
-                            float y[4], m2, l2;
-                            dp_row_again(a, w.b, h, qr, w.first * NK, __shfl_sync(0xffffffffu, end, from), y, m2, l2);
-                            const float f = split_up ? 1.f : 1.f / l2;
-                            if (split_up) {  // (in the units of the other parts' sums)
-                                constexpr float kUnits = kF16 ? 64.f : 1.f;
-                                *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + 4 * lane) =
-                                    make_float4(y[0] * kUnits, y[1] * kUnits, y[2] * kUnits, y[3] * kUnits);
-                                if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m2, l2 * kUnits);
-                            } else if (a.out_bf16) {
-                                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + qr * kHeadDim + 4 * lane) =
-                                    make_uint2(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f));
-                            } else {
-                                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + qr * kHeadDim + 4 * lane) =
-                                    make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+                            DpAgain x;
+                            int64_t pr[kDpAgain];
+#pragma unroll
+                            for (int r = 0; r < kDpAgain; ++r) {  // (the last of them several times where there are fewer)
+                                const int from = __ffs(again) - 1;
+                                if (r == kDpAgain - 1 || (again & (again - 1)) != 0) again &= again - 1;
+                                x.q_row[r] = __shfl_sync(0xffffffffu, q_row, from);
+                                pr[r] = __shfl_sync(0xffffffffu, part_row, from);
+                                x.end[r] = __shfl_sync(0xffffffffu, end, from);
+                            }
+                            dp_rows_again<kF16>(a, w.b, h, w.first * NK, x);
+#pragma unroll
+                            for (int r = 0; r < kDpAgain; ++r) {
+                                const float* y = x.o[r];
+                                const int64_t at = x.q_row[r] * kHeadDim + 4 * lane;
+                                const float f = 1.f / x.l[r];
+                                if (split_up) {  // (in the units of the other parts' sums)
+                                    constexpr float kUnits = kF16 ? 64.f : 1.f;
+                                    *reinterpret_cast<float4*>(a.part_o + pr[r] * kHeadDim + 4 * lane) =
+                                        make_float4(y[0] * kUnits, y[1] * kUnits, y[2] * kUnits, y[3] * kUnits);
+                                    if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + pr[r] * 2) = make_float2(x.m[r], x.l[r] * kUnits);
+                                } else if (a.out_bf16) {
+                                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+                                        make_uint2(pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f));
+                                } else {
+                                    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+                                }
                             }
                         }
                     }
