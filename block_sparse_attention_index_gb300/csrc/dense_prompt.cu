@@ -53,7 +53,8 @@
 //
 // Values that no row of the tile may see: positions past the length are zeroed in the last value tile (by warp 10), so
 // stale cache rows do not matter.  A later token of the same chunk meets weights of zero; if its value is not finite
-// the product is NaN, so a row whose result is not finite is computed again key by key (dp_row_again).
+// the product is NaN, so a row whose result is not finite is computed again (dp_rows_again) where such a token lies past
+// it in the item's tiles.
 #include <cuda_fp16.h>
 
 #include <algorithm>
