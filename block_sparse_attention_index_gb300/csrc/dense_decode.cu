@@ -125,7 +125,7 @@ __device__ __forceinline__ int dd_units(const DenseArgs& a, int b, int& tiles, b
     tiles = 0;
     const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0, L = a.cache_lens[b];
     const bool placed = seq_rows_ok(a.cache, b, L, a.cache_tokens);  // (loads that need not wait for one another)
-    if (n == 0 || n > kDecodeMaxRows || (a.tile_windows && n * a.G > 16)) return 0;
+    if (n == 0 || n > kDecodeMaxRows || n * a.G > a.window_above) return 0;
     if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len || !placed) {
         bad = true;
         return 0;

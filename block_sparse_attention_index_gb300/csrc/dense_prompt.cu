@@ -204,7 +204,7 @@ __device__ __forceinline__ int dp_tiles(const DenseArgs& a, int b, DpItem& it, f
     const bool placed = seq_rows_ok(a.seq_cache, b, L, a.seq_cache_tokens);
     const bool here = a.cache.table != nullptr || a.cache.starts[b] >= 0;  // (else widened in another pass)
     if (n == 0) return 0;
-    if (kAlt ? n < 0 || n > kDecodeMaxRows || n * a.G <= 16 : a.only_multi_row && n > 0 && n <= kDecodeMaxRows) return 0;
+    if (kAlt ? n < 0 || n > kDecodeMaxRows || n * a.G <= a.window_above : a.only_multi_row && n > 0 && n <= kDecodeMaxRows) return 0;
     if (n < 0 || n > a.max_rows_per_seq || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len || !placed) {
         bad = true;
         return 0;

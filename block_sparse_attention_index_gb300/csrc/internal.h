@@ -212,7 +212,7 @@ struct DenseArgs {
     int64_t cache_tokens;
     float scale_log2;  // softmax scale * log2(e)
     int only_multi_row;  // 1: the prompt kernel skips decode-family sequences
-    int tile_windows;    // 1: run_dense_window takes the decode-family sequences of more than 16 (row, head) pairs
+    int window_above;    // run_dense_window takes the decode-family sequences of more (row, head) pairs than this
     const CUtensorMap* q_map;  // host copies: q as (D, H*G, rows), box 64 x G x 128 / G; the cache maps (kv_map)
     const CUtensorMap* k_map;
     const CUtensorMap* v_map;

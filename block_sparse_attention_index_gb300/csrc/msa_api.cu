@@ -216,7 +216,7 @@ Layout layout_of(const msa_problem* p) {
 // How msa_dense_forward divides a problem (host counts alone).
 struct DensePlan {
     bool stream = false;   // decode-family sequences of at most 16 (row, head) pairs (all of them with an int8 cache)
-    bool windows = false;  // the others of the decode family, on tcgen05
+    bool windows = false;  // the others of the decode family, on tcgen05 (all of it where stream is off)
     bool prompts = false;
     bool all_prompts = false;  // the prompt kernel takes the decode family too
     int64_t window_items = 0, prompt_items = 0;  // bounds of the M tiles (prompts: pairs of them)
@@ -238,6 +238,7 @@ DensePlan dense_plan(const msa_problem* p) {
     if (decode_family(p) && !d.all_prompts) {
         const int64_t rows = static_cast<int64_t>(decode_rows_per_seq(p)), seqs = known >= 0 ? known : p->num_seqs;
         const bool one_row = known >= 0 && p->num_decode_rows == known;  // every sequence
+        // (the count is a bound: shorter windows on the device are the window kernel's as well)
         const bool full = known >= 0 && p->num_decode_rows == known * rows;
         d.windows = p->kv_dtype == MSA_KV_BF16 && rows * G > 16 && !one_row;
         d.stream = !(d.windows && full);
@@ -974,7 +975,8 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.part_o = reinterpret_cast<float*>(ws + l.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
     a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
-    a.tile_windows = d.windows;
+    // (a call for full windows launches no streaming kernel: the window kernel takes the shorter ones too)
+    a.window_above = !d.windows ? INT32_MAX : (d.stream ? 16 : 0);
     a.pairs_most = d.windows ? 16 : static_cast<int>(decode_rows_per_seq(p)) * p->group_size;
     a.only_multi_row = decode_family(p) && !d.all_prompts;
     a.q = static_cast<const uint16_t*>(q);

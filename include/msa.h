@@ -377,7 +377,8 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  * Numerics.  Scores, maxima and sums are fp32.  The softmax weights enter the
  * products with V, bf16 caches: as three bf16 parts (2^-24) with fp32 outputs;
  * with bf16 outputs as one (2^-9, prompt chunks) or two (2^-17, decode rows and
- * drafted windows of up to 16 (row, head) pairs).  int8 caches: exact codes,
+ * drafted windows of up to 16 (row, head) pairs, but for those of a call whose
+ * num_decode_rows says that all windows are longer).  int8 caches: exact codes,
  * f16 weights of one part (2^-12, bf16 outputs) or two (2^-23, fp32) for up to
  * 8 rows a sequence, three bf16 parts for prompt chunks with fp32 outputs; with
  * bf16 outputs prompt chunks read an f16 copy of the cache (a key or value off
