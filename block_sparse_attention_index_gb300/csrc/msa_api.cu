@@ -246,7 +246,8 @@ DensePlan dense_plan(const msa_problem* p) {
     }
     d.prompts = prefill_family(p);
     if (d.prompts) {
-        const int64_t rows = p->total_rows - (d.all_prompts ? 0 : std::max(p->num_decode_rows, 0));
+        // (every row may be a prompt's: num_decode_rows is a bound from above, and sequences may have none)
+        const int64_t rows = p->total_rows;
         int64_t seqs = known >= 0 && !d.all_prompts ? p->num_seqs - known : p->num_seqs;
         if (!d.all_prompts) seqs = std::max<int64_t>(1, std::min<int64_t>(seqs, p->total_rows / (msa::kDecodeMaxRows + 1)));
         const int64_t pair = 2 * (128 / G);  // rows of an item

@@ -22,6 +22,15 @@ def test_windows_shorter_than_the_host_counts(count, G, int8, out):
     assert (rest[13:] == 7).all()
 
 
+@pytest.mark.parametrize("count", [0, 64, 65, 512])
+@pytest.mark.parametrize("int8", [False, True])
+def test_prompts_beside_an_over_count_of_decode_rows(count, int8):
+    seqs = [(1, 20 + 90 * i) for i in range(64)] + [(512, 600)]
+    b = Batch(seqs, 1, 16, int8, 64, torch.bfloat16)
+    b.pb.c.num_decode_rows = count
+    b.check()
+
+
 def test_a_captured_step_follows_its_rows():
     """One graph, captured for full windows, replayed for shorter ones."""
     m = msa()
