@@ -161,7 +161,9 @@ class Problem:
     page_size, with cache_tokens = rows of the page pool.  ik_heads=1: one
     index key per position shared by every KV head (ik is [T, 1, Di]).
     k_scale, v_scale (float32 [cache_tokens, H] device tensors): the key and
-    value caches are int8 with these per-(cache row, head) scales.
+    value caches are int8 with these per-(cache row, head) scales.  Scales of
+    another type, device or layout are copied, which append_cache, the writer
+    of scales, refuses.
     num_decode_rows: host count of decode-family rows ("auto": from seqs_host;
     0: unknown, the decode attention then covers every row slot).
     """
@@ -220,11 +222,13 @@ class Problem:
             raise ValueError("k_scale and v_scale go together")
         self.kv_dtype = torch.int8 if k_scale is not None else torch.bfloat16
         self.k_scale = self.v_scale = None
+        self.scales_copied = False
         if k_scale is not None:
             self.k_scale = torch.as_tensor(k_scale, dtype=torch.float32).to(self.device).contiguous()
             self.v_scale = torch.as_tensor(v_scale, dtype=torch.float32).to(self.device).contiguous()
             for t, name in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale")):
                 _need(t, name, torch.float32, self.device, (self.cache_tokens, H))
+            self.scales_copied = self.k_scale is not k_scale or self.v_scale is not v_scale
             self.c.kv_dtype = MSA_KV_INT8
             self.c.k_scale = self.k_scale.data_ptr()
             self.c.v_scale = self.v_scale.data_ptr()
@@ -423,10 +427,13 @@ def append_cache(pb: Problem, new_k, new_v, k, v, new_ik=None, ik=None, q=None, 
 
     New rows may be views of a wider projection (any row stride that is a multiple of 8).  positions: int32
     [axes, rows], or None for each row's position in its sequence.  With an int8 cache the scales go to pb.k_scale
-    and pb.v_scale.  Returns (q, iq) rotated, each None when not given."""
+    and pb.v_scale, which must be the tensors that the Problem was given, not copies of them.  Returns (q, iq) rotated, each None when not given."""
     R, H, D, Di, dev = pb.total_rows, pb.H, pb.D, pb.Di, pb.device
     pb._check_cache(k, "k", D)
     pb._check_cache(v, "v", D)
+    if pb.scales_copied:
+        raise ValueError("the Problem holds copies of k_scale and v_scale, and the cache would not get the new rows' "
+                         f"scales: give it contiguous {torch.float32} tensors on {dev}")
     ks, vs = _rows(new_k, "new_k", R, H, D, dev), _rows(new_v, "new_v", R, H, D, dev)
     ikp = ikc = qp = iqp = qo = iqo = None
     iks = qs = iqs = 0
