@@ -1375,7 +1375,9 @@ __global__ void __launch_bounds__(kDjThreads, 8) dense_join_kernel(const DenseAr
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int2 head = *a.split_head;  // split items, parts of each
     const int4 it = a.split_items[blockIdx.x];
-    if (static_cast<int>(blockIdx.x) >= head.x) return;
+    const uint32_t err = *a.err;
+    // (where a wait gave up, an item may have been left that nobody wrote down)
+    if (static_cast<int>(blockIdx.x) >= head.x || (err & kErrWaitTimeout)) return;
     const int nsplit = head.y, h = it.z;
     const int c0 = a.cu_rows[it.x], n = a.cu_rows[it.x + 1] - c0, P = 128 / a.G, i0 = it.y * P * (kAlt ? 1 : 2);
     const int64_t base = static_cast<int64_t>(blockIdx.x) * nsplit * kRows;
