@@ -378,8 +378,10 @@ __device__ __forceinline__ DpWork dp_work(int P, const DpItem& it) {  // P = 128
 // value spoiled them, or the f16 copy's powers of two left them too few bits.  The whole warp, 32 keys at a time: 16
 // lanes share a key's dot products (8 dimensions each, summed by a reduce-scatter over 16 keys), then a lane has a key's
 // scores; 4 dimensions of O a lane.  70 cycles a key and row, bound by the instructions (one row at a time, loads in the
-// order of its keys: 710).
+// order of its keys: 710).  A warp's 32 rows over 2^21 keys take 2.5 s, so the CTA's other warps
+// may wait longer for them than kWaitLimitNs: kDpAgainNs more for each key.
 constexpr int kDpAgain = 4;
+constexpr uint64_t kDpAgainNs = 8000;  // 32 rows x 70 cycles are 1.2 us; two warps a scheduler, low clocks, one stage after the other
 struct DpAgain {
     int64_t q_row[kDpAgain];
     int end[kDpAgain];
@@ -541,6 +543,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     using Smem = DpSmem<kParts, kForm>;
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.err, a.wait_ns); };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be scheduled: it waits for this grid
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
     // Every role walks the CTA's items with its own copy of each and with counts that run on over them: copies (ring slots),
     // a stage's copies (alternate tiles), a stage's tiles, items.
     auto next_item = [&](int k, DpItem& x) {  // item k of the CTA, false where it never came
-        if (!mbar_wait(&sm.info_full[k % kDpInfo], (k / kDpInfo) & 1, a.err)) return false;
+        if (!wait(&sm.info_full[k % kDpInfo], (k / kDpInfo) & 1)) return false;
         x = sm.info[k % kDpInfo];
         return true;
     };
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 int ok = 1;
                 if (lane == 0) {
                     const int at = n % kDpInfo;
-                    if (n >= kDpInfo) ok = mbar_wait(&sm.info_empty[at], ((n / kDpInfo) - 1) & 1, a.err);
+                    if (n >= kDpInfo) ok = wait(&sm.info_empty[at], ((n / kDpInfo) - 1) & 1);
                     if (ok) {
                         sm.info[at] = x;
                         mbar_arrive(&sm.info_full[at]);
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 if (!half) {
                     int ok = 1;
                     if (lane == 0) {
-                        if (k > 0) ok = mbar_wait(&sm.q_full, (k - 1) & 1, a.err) && mbar_wait(&sm.q_empty, (k - 1) & 1, a.err);
+                        if (k > 0) ok = wait(&sm.q_full, (k - 1) & 1) && wait(&sm.q_empty, (k - 1) & 1);
                         if (ok) {
                             const int tiles = kAlt ? 1 : (w.i0 + w.P < w.n ? 2 : 1);
                             mbar_arrive_expect_tx(&sm.q_full, tiles * 2 * w.P * a.G * 128);
@@ -698,7 +701,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                             uint64_t* bar = kind == 1 && j == fix ? &sm.v_last[st]
                                                                   : full_bar(j, (odd ? sent0[1] : sent0[0]) + copy_index(j, kind));
                             uint8_t* dst = sm.ring[st] + half * kHalf;
-                            if (slot >= kStages) ok = mbar_wait(&sm.empty[st], ((slot / kStages) - 1) & 1, a.err);
+                            if (slot >= kStages) ok = wait(&sm.empty[st], ((slot / kStages) - 1) & 1);
                             if (ok) {
                                 mbar_arrive_expect_tx(bar, Cfg::kTile / 2);
 #pragma unroll
@@ -706,7 +709,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                                     tma_load_3d(dst + c * (kBlock * 128), kind == 0 ? &k_map : &v_map, bar, 64 * half, h, static_cast<int>(r[c]));
                                 if (kWide && kind == 0 && !half) {  // the tile's scales
                                     const int jt = tiles_before + j, e = jt % kDpScaleSlots;
-                                    if (jt >= kDpScaleSlots) ok = mbar_wait(&sm.sc_empty[e], ((jt / kDpScaleSlots) - 1) & 1, a.err);
+                                    if (jt >= kDpScaleSlots) ok = wait(&sm.sc_empty[e], ((jt / kDpScaleSlots) - 1) & 1);
                                     if (ok) {
                                         const int64_t from = static_cast<int64_t>(h) * a.cache_tokens + a.cache.starts[w.b] +
                                                              static_cast<int64_t>(w.first + j) * NK;
@@ -728,7 +731,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 }
                 if (half && fix >= 0 && alive) {  // ---- the last value tile: rows past the length become zero
                     const int st = (2 * tiles_before + slot_v(w, fix)) % kStages;
-                    alive = __all_sync(0xffffffffu, mbar_wait(&sm.v_last[st], fixed >> st & 1, a.err));
+                    alive = __all_sync(0xffffffffu, wait(&sm.v_last[st], fixed >> st & 1));
                     if (!alive) break;
                     fixed ^= 1u << st;
                     for (int x = (w.L % NK) * 16 + lane; x < NK * 16; x += 32) {
@@ -746,13 +749,13 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 tiles_before += w.total;
             }
             if (lane == 0 && !half) {  // no copy in flight at the end (a last value tile's barrier was warp 10's to wait for)
-                if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, a.err);
+                if (queries > 0) wait(&sm.q_full, (queries - 1) & 1);
                 for (int s = 0; s < (kAlt ? 2 : 1); ++s)
                     for (int b = 0; b < kStages && b < sent[s]; ++b)
-                        mbar_wait(&sm.full[s][b], ((sent[s] - 1 - b) / kStages) & 1, a.err);
+                        wait(&sm.full[s][b], ((sent[s] - 1 - b) / kStages) & 1);
                 if (kWide && alive)
                     for (int e = 0; e < kDpScaleSlots && e < tiles_before; ++e)
-                        mbar_wait(&sm.sc_full[e], ((tiles_before - 1 - e) / kDpScaleSlots) & 1, a.err);
+                        wait(&sm.sc_full[e], ((tiles_before - 1 - e) / kDpScaleSlots) & 1);
             }
         } else if (warp == 9 || warp == 11) {
             // ---------------- matrix instructions of stage s, one thread
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 // running: ring slots, tiles of the stage, turns taken, the next copy's barrier and its phase
                 int slots = 0, tiles = 0, turns = 0, bar = 0;
                 uint32_t bar_phase = 0;
-                auto landed = [&]() { return mbar_wait(&sm.full[kAlt ? s : 0][bar], bar_phase, a.err); };
+                auto landed = [&]() { return wait(&sm.full[kAlt ? s : 0][bar], bar_phase); };
                 auto pass_copy = [&]() {
                     if (++bar == kStages) {
                         bar = 0;
@@ -799,7 +802,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     };
                     // (waited for without tiles too: a barrier's phases have to be seen one by one, and the stage's group may
                     // be converting the queries)
-                    ok = mbar_wait(kF16 ? &sm.q_turned[s] : &sm.q_full, k & 1, a.err);
+                    ok = wait(kF16 ? &sm.q_turned[s] : &sm.q_full, k & 1);
                     if (!ok) break;
                     if constexpr (kAlt) mbar_arrive(&sm.q_empty);  // (seen; group 0 arrives when the products are done)
                     if (count > 0) {
@@ -813,7 +816,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         mbar_arrive(&sm.q_empty);
                     }
                     // the other stage is through with its last item: its turns have been taken
-                    if (k > 0) ok = mbar_wait(&sm.item_done, (k - 1) & 1, a.err);
+                    if (k > 0) ok = wait(&sm.item_done, (k - 1) & 1);
                     for (int c = 0; ok && c < count; ++c) {
                         // the stages take turns: values of tile c, scores of the next (whatever can be waited for is, first)
                         const int j = j0 + kStep * c;
@@ -828,14 +831,14 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                         const bool turns_now = s == 0 ? c > 0 && c <= others : c < others;
                         const bool pass = s == 0 ? c < others : c + 1 < others;
                         const uint64_t vb = vd + static_cast<uint64_t>(st_v * (Cfg::kTile >> 4));
-                        ok = ok && mbar_wait(&sm.p_full[s][0], phase, a.err);
-                        if (ok && turns_now) ok = mbar_wait(&sm.turn[s], turns++ & 1, a.err);
+                        ok = ok && wait(&sm.p_full[s][0], phase);
+                        if (ok && turns_now) ok = wait(&sm.turn[s], turns++ & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int h2 = 0; h2 < NK / 64; ++h2) {  // O_s += P_s V, the second 64 keys as soon as their weights are there
                             if (h2 == 1) {
-                                ok = mbar_wait(&sm.p_full[s][1], phase, a.err);
+                                ok = wait(&sm.p_full[s][1], phase);
                                 if (!ok) break;
                                 tc_fence_after();
                             }
@@ -869,7 +872,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 }
                 if (issued) {  // every matrix instruction done before tensor memory is given back
                     tc_commit(&sm.drain[s]);
-                    mbar_wait(&sm.drain[s], 0, a.err);
+                    wait(&sm.drain[s], 0);
                 }
             }
         }
@@ -896,7 +899,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             const int early = w.L - w.n + min(w.i0 + (kAlt ? 0 : s * w.P), w.n - 1);
             const int count = s == 0 ? w.count[0] : w.count[1];
             float row_f = a.scale_log2;  // factor from the row's products to the log2 domain
-            if constexpr (kF16 || kAlt) alive = __all_sync(0xffffffffu, mbar_wait(&sm.q_full, k & 1, a.err));
+            if constexpr (kF16 || kAlt) alive = __all_sync(0xffffffffu, wait(&sm.q_full, k & 1));
             if constexpr (kF16) {
                 // the row's queries to f16: its largest value into [2^8, 2^9)
                 if (!alive) break;
@@ -970,7 +973,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             };
             for (int c = 0; alive && c < count; ++c) {
                 const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
-                alive = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s], (tiles + c) & 1, a.err));
+                alive = __all_sync(0xffffffffu, wait(&sm.s_full[s], (tiles + c) & 1));
                 if (!alive) break;
                 tc_fence_after();
                 if (c > 0 && (c & 1) == 0) collect();
@@ -978,7 +981,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
                     const int e = (tiles_before + j) % kDpScaleSlots;
                     if constexpr (kWide) {
-                        alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[e], ((tiles_before + j) / kDpScaleSlots) & 1, a.err));
+                        alive = __all_sync(0xffffffffu, wait(&sm.sc_full[e], ((tiles_before + j) / kDpScaleSlots) & 1));
                         if (!alive) break;
                     }
                     // the scores of keys 32 q .. of the tile in the log2 domain (f: what is left to multiply by)
@@ -1191,13 +1194,13 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 if (lane == 0) mbar_arrive(&sm.info_empty[k % kDpInfo]);
                 if constexpr (kWide) {  // scales of tiles that only the other group needs
                     for (int j = tiles_before + count; alive && j < tiles_before + w.total; ++j) {
-                        alive = __all_sync(0xffffffffu, mbar_wait(&sm.sc_full[j % kDpScaleSlots], (j / kDpScaleSlots) & 1, a.err));
+                        alive = __all_sync(0xffffffffu, wait(&sm.sc_full[j % kDpScaleSlots], (j / kDpScaleSlots) & 1));
                         if (alive && lane == 0) mbar_arrive(&sm.sc_empty[j % kDpScaleSlots]);
                     }
                 }
                 // ---------------- epilogue
                 bool have = count > 0;
-                if (alive && have) alive = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[s], done++ & 1, a.err));
+                if (alive && have) alive = __all_sync(0xffffffffu, wait(&sm.o_full[s], done++ & 1));
                 tc_fence_after();
                 if (alive && have) collect();
                 constexpr int kRun = 32;  // values of the row that are finished at a time
@@ -1439,6 +1442,7 @@ static cudaError_t launch_dense_prompt(DenseArgs a, int items, cudaStream_t stre
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     a.places = std::min(device_sm_count(), kDenseMaxShares);
+    a.wait_ns = kWaitLimitNs + kDpAgainNs * static_cast<uint64_t>(a.max_cache_len);
     // every item, and room for the parts of the last wave's: what the rule would choose for the host's counts where
     // there is one sequence (or window each), which they tell exactly, else two a place
     const int64_t whole = static_cast<int64_t>(items) * a.H;

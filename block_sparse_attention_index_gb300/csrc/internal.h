@@ -222,6 +222,7 @@ struct DenseArgs {
     const float* seq_v_scale;
     const float2* wide_fac;    // int8 prompts, bf16 outputs: factors of the f16 copy's blocks, [H, cache_tokens / 64]
     int places;            // prompts, windows: SMs
+    uint64_t wait_ns;      // prompts, windows: limit of a wait
     int parts_most;        // parts of split items that there is room for
     uint32_t* next_item;   // prompts, windows: items taken beyond each CTA's first, cleared before the launch
     int32_t* tile_prefix;  // prompts, windows: [num_seqs] tiles before each sequence (more than 32 sequences)

@@ -37,3 +37,24 @@ def test_split_items_are_not_joined_after_a_wait_gave_up():
     torch.cuda.synchronize()
     assert m.error_word(ws) == 0
     assert torch.isfinite(out[:39]).all() and torch.isnan(out[39]).all() and not (out == 7).all(-1).any()
+
+
+def test_work_that_outlasts_a_wait_is_waited_for():
+    """Rows that are computed again over 2^21 positions take a CTA 2.5 s or more, while its other warps wait for their
+    next item."""
+    m = msa()
+    L, n = 1 << 21, 640
+    b = Batch([(n, L)], 8, 16, False, 0, torch.bfloat16, seed=2)
+    at = b.starts[0]
+    b.v[at + L - 1] = float("nan")  # the last row sees it; the 15 rows of its tiles before it are computed again
+    got = b.run()
+    assert torch.isnan(got[n - 1]).all()
+    assert torch.isfinite(got[:n - 1]).all()
+    # weights to 2^-8 each, half a step of bf16, the sums' 2 L 2^-24 as in 64 bits' bound (of |values| of the same size)
+    for row, head in ((n - 2, 0), (n - 16, 77), (n - 17, 127), (0, 5), (n // 2, 40)):
+        h, end = head // 16, at + L - n + row + 1
+        x = (b.k[at:end, h].double() @ b.q[row, head].double()) * b.scale
+        w = torch.softmax(x, 0)
+        v = b.v[at:end, h].double()
+        ref, bound = w @ v, (w @ v.abs()) * (2.0 ** -8 + 2.0 ** -12) + 2.0 ** -8 * (w @ v).abs()
+        assert ((got[row, head].double() - ref).abs() <= bound).all()
