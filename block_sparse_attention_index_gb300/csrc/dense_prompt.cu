@@ -458,7 +458,7 @@ __device__ __noinline__ void dp_rows_again(const DenseArgs& a, int b, int h, int
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             top = fmaxf(top, m[r]);
             const float f = m[r] == -INFINITY ? 0.f : dp_exp2(m[r] - top);
-            p[r] = t < end[r] ? dp_exp2(x - top) : 0.f;
+            p[r] = t < end[r] ? dp_exp2(x - (top == -INFINITY ? 0.f : top)) : 0.f;  // (no score above -inf so far: weights of 0)
             l[r] *= f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[r][e] *= f;
