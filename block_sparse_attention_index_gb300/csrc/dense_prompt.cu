@@ -106,7 +106,7 @@ struct __align__(1024) DpSmem {
     uint64_t v_last[Cfg::kStages];       // a last value tile has landed, before its tail is zeroed
     uint64_t q_full, q_turned[2], q_empty;  // q_turned: a stage's queries converted (f16 form)
     uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
-    uint32_t tmem;
+    uint32_t tmem, lost;  // lost: some block of the f16 copy has lost bits
     int32_t scan[kDpThreads / 32];
     float scan_keys[kDpThreads / 32];
     DpItem info[kDpInfo];  // the CTA's next items, published by warp 10
@@ -531,6 +531,22 @@ __device__ __noinline__ int dp_last_bad(const DenseArgs& a, int b, int h, int fi
     return __reduce_max_sync(0xffffffffu, bad);
 }
 
+// How far apart the value factors of an item's blocks are, log2 (blocks of zeros left out); 127 if some key or value of
+// one has lost bits (a whole warp).
+__device__ __noinline__ int dp_apart(const float2* fac, int first, int end) {
+    int most = 0, least = 255, lost = 0;
+    for (int b = first + static_cast<int>(threadIdx.x & 31); b < end; b += 32) {
+        const float2 f = fac[b];
+        const int e = static_cast<int>(__float_as_uint(f.y) >> 23);
+        lost |= static_cast<int>(__float_as_uint(f.x) & 1u);
+        most = max(most, e);
+        if (e > 0) least = min(least, e);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    return __any_sync(0xffffffffu, lost) ? 127 : most - least;
+}
+
 template <int kParts, int kForm, bool kAlt>
 __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                     const __grid_constant__ CUtensorMap k_map,
@@ -574,6 +590,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
         }
         fence_mbar_init();
     }
+    if (kF16 && tid == 0) sm.lost = *a.wide_lost;
     if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &q_map : (lane == 1 ? &k_map : &v_map));
     if (warp == 9) tmem_alloc(&sm.tmem, 512);
     tc_fence_before();
@@ -1309,10 +1326,17 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                             const int bad = dp_last_bad(a, w.b, h, max(least + 1, w.first * NK), min(keys, w.L));  // (every lane)
                             spoiled = spoiled && bad > pos;
                         }
-                        // f16 form: a row that lives on blocks whose values are tiny beside another block's (even one that it
-                        // does not see) has small weights there, off by up to 2^-25 each, L^1/2 2^-12 in units where it has
-                        // 2^10 or more when nothing was lost
-                        if (kF16 && coarse && most < 1024.f) spoiled = fabsf(sum) < INFINITY;
+                        // f16 form: a row that lives on blocks whose values are tiny (2^-12) beside another block's (even one
+                        // that it does not see) has small weights there, off by up to 2^-25 each, L^1/2 2^-12 in units where
+                        // it has 2^10 or more when nothing was lost.  Further apart (2^-22), or where keys or values of a
+                        // block have lost bits to another's of the block, they may be all that a row sees (or that one of its
+                        // values has: codes of 0 in the large ones), so every row of the tile is computed again.
+                        if constexpr (kF16) {
+                            if (coarse || sm.lost) {
+                                const int apart = dp_apart(fac, 2 * w.first, min(2 * (w.first + count), (w.L + kBlock - 1) / kBlock));
+                                if (apart > 22 || (apart > 12 && most < 1024.f)) spoiled = fabsf(sum) < INFINITY;
+                            }
+                        }
                         uint32_t again = __ballot_sync(0xffffffffu, mine && spoiled && have);
                         while (again) {  // these rows once more, by the whole warp
                             DpAgain x;

@@ -175,7 +175,7 @@ struct WidenArgs {
     uint32_t* err;
 };
 cudaError_t run_widen_kv(const WidenArgs& a, cudaStream_t stream);
-cudaError_t run_widen_f16(const WidenArgs& a, float2* fac, cudaStream_t stream);
+cudaError_t run_widen_f16(const WidenArgs& a, float2* fac, uint32_t* any_lost, cudaStream_t stream);
 
 // Cache writer: the new rows of a call, rotated and stored (msa_append, msa_rope of the ABI).
 struct AppendArgs {
@@ -221,6 +221,7 @@ struct DenseArgs {
     const float* seq_k_scale;  // int8 caches: the problem's scales
     const float* seq_v_scale;
     const float2* wide_fac;    // int8 prompts, bf16 outputs: factors of the f16 copy's blocks, [H, cache_tokens / 64]
+    const uint32_t* wide_lost; // and whether some block's keys or values have lost bits
     int places;            // prompts, windows: SMs
     uint64_t wait_ns;      // prompts, windows: limit of a wait
     int parts_most;        // parts of split items that there is room for

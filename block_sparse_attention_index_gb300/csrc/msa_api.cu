@@ -1001,9 +1001,9 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.scale_log2 = scale_log2(p);
     a.err = reinterpret_cast<uint32_t*>(ws + l.err);
     // the decode family's combine stores the error word; before any other kernel it is cleared, and with it the counts of
-    // items taken by windows (word 1) and prompts (word 2)
+    // items taken by windows (word 1) and prompts (word 2), and what the f16 copy lost (word 3)
     a.err_store = d.stream && !d.prompts && !d.windows;
-    if (!a.err_store && (e = cudaMemsetAsync(ws, 0, 3 * sizeof(uint32_t), st)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    if (!a.err_store && (e = cudaMemsetAsync(ws, 0, 4 * sizeof(uint32_t), st)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
     if (d.stream) {
         const int64_t seqs = p->num_decode_seqs > 0 ? p->num_decode_seqs : p->num_seqs;
         const int64_t tiles = d.windows ? 1 : (static_cast<int64_t>(decode_rows_per_seq(p)) * p->group_size + 15) / 16;
@@ -1056,11 +1056,12 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
         a.v_scale = wa.vsw;
         float2* fac = reinterpret_cast<float2*>(wa.ksw);  // (the f16 copy has its scales in it)
         a.wide_fac = fac;
+        a.wide_lost = a.err + 3;
         for (int64_t first = 0; first < d.wide_total; first += d.wide_slots) {
             wa.first_slot = static_cast<int>(first);
             if (first > 0 && (e = cudaMemsetAsync(a.next_item, 0, sizeof(uint32_t), st)) != cudaSuccess)
                 return cuda_fail(e, "cudaMemsetAsync");
-            e = a.out_bf16 ? msa::run_widen_f16(wa, fac, st) : msa::run_widen_kv(wa, st);
+            e = a.out_bf16 ? msa::run_widen_f16(wa, fac, a.err + 3, st) : msa::run_widen_kv(wa, st);
             if (e != cudaSuccess) return cuda_fail(e, "key/value widening launch");
             if ((e = msa::run_dense_prompt(a, static_cast<int>(d.prompt_items), st)) != cudaSuccess)
                 return cuda_fail(e, "dense prompt attention launch");

@@ -147,14 +147,17 @@ __global__ void __launch_bounds__(kWidenThreads) widen_kv_kernel(const WidenArgs
 }
 
 // The same for outputs of 16 bits in the dense attention: f16 values with the scales in them, over a power of two for
-// each 64-position block and head (so that nothing overflows and the block's values keep f16's 11 bits; a key is
-// then off by 2^-12 of itself at random, about a tenth of what the output's own rounding is).  fac[h][block] = (the
-// power of two to multiply key products by, the one to multiply the value sums by).  CTA: a block, all heads.
-__global__ void __launch_bounds__(kWidenThreads) widen_f16_kernel(const WidenArgs a, float2* fac) {
+// each 64-position block and head (so that nothing overflows).  A scale down to 2^-22 of that power of two keeps f16's
+// 11 bits: a key or value is off by 2^-11 of itself at most.  Below, small codes have fewer bits or none (a token whose
+// scale is 2^22 times its neighbours', which the rows before it must not notice).  fac[h][block] = (the power of two to
+// multiply key products by, its lowest bit set, 2^-23 of it, if some key or value of the block has lost bits, and
+// *any_lost too; the one to multiply the value sums by, 0 for values that are all 0).  CTA: a block, all heads.
+__global__ void __launch_bounds__(kWidenThreads) widen_f16_kernel(const WidenArgs a, float2* fac, uint32_t* any_lost) {
     extern __shared__ int32_t slot_of[];  // [num_seqs]
     __shared__ int32_t warp_tot[kWidenThreads / 32];
     __shared__ float scale[2][kBlock * 8];  // key and value scales of the block, [position][head]
     __shared__ float top[2][8];             // their powers of two
+    __shared__ bool zero[2][8], lost[2][8]; // all scales are 0; some scale is too far below
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.num_seqs, H = a.H;
     widen_slots(a, slot_of, warp_tot);
     const int blocks = a.slot_rows / kBlock;
@@ -177,20 +180,31 @@ __global__ void __launch_bounds__(kWidenThreads) widen_f16_kernel(const WidenArg
         __syncthreads();
         for (int c = warp; c < 2 * H; c += kWidenThreads / 32) {  // a warp a (kind, head): the largest finite scale
             const int kind = c / H, h = c - kind * H;
-            float m = 0.f;
+            float most = 0.f, least = INFINITY;  // (of the scales that are not zero)
             for (int pos = lane; pos < kBlock; pos += 32) {
                 const float x = fabsf(scale[kind][pos * H + h]);
-                if (x < INFINITY) m = fmaxf(m, x);
+                if (x < INFINITY) most = fmaxf(most, x);
+                if (x > 0.f) least = fminf(least, x);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(most));  // (positive: ordered as their bits)
+            least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least)));
             // the next power of two, in [2^-110, 2^127]: 256 / it and it / 256 are normal numbers
-            const uint32_t bits = (__float_as_uint(m) + 0x007FFFFFu) & 0x7F800000u;
-            if (lane == 0) top[kind][h] = __uint_as_float(min(max(bits, 17u << 23), 0x7F000000u));
+            const uint32_t bits = (m + 0x007FFFFFu) & 0x7F800000u;
+            const float power = __uint_as_float(min(max(bits, 17u << 23), 0x7F000000u));
+            if (lane == 0) {
+                top[kind][h] = power;
+                zero[kind][h] = m == 0u;
+                lost[kind][h] = least < power * 2.384185791015625e-7f;  // 2^-22
+            }
         }
         __syncthreads();
         const int64_t dst = (static_cast<int64_t>(slot) * blocks + blk) * kBlock;
-        if (tid < H) fac[tid * wide_blocks + dst / kBlock] = make_float2(top[0][tid] / 256.f, top[1][tid] / 256.f);
+        if (tid < H) {
+            const uint32_t bad = lost[0][tid] || lost[1][tid];
+            fac[tid * wide_blocks + dst / kBlock] = make_float2(__uint_as_float(__float_as_uint(top[0][tid] / 256.f) | bad),
+                                                                zero[1][tid] ? 0.f : top[1][tid] / 256.f);
+            if (bad) *any_lost = 1u;
+        }
         const uint8_t* in[2] = {a.k8 + src * H * kHeadDim, a.v8 + src * H * kHeadDim};
         uint16_t* out[2] = {a.kw + dst * H * kHeadDim, a.vw + dst * H * kHeadDim};
         for (int c0 = tid; c0 < chunks; c0 += kWidenBatch * kWidenThreads) {
@@ -228,11 +242,11 @@ __global__ void __launch_bounds__(kWidenThreads) widen_f16_kernel(const WidenArg
     }
 }
 
-cudaError_t run_widen_f16(const WidenArgs& a, float2* fac, cudaStream_t stream) {
+cudaError_t run_widen_f16(const WidenArgs& a, float2* fac, uint32_t* any_lost, cudaStream_t stream) {
     const int64_t units = static_cast<int64_t>(a.num_seqs) * (a.slot_rows / kBlock);
     const int64_t cap = 4 * static_cast<int64_t>(device_sm_count());
     const int grid = static_cast<int>(units < cap ? (units > 0 ? units : 1) : cap);
-    widen_f16_kernel<<<grid, kWidenThreads, static_cast<size_t>(a.num_seqs) * sizeof(int32_t), stream>>>(a, fac);
+    widen_f16_kernel<<<grid, kWidenThreads, static_cast<size_t>(a.num_seqs) * sizeof(int32_t), stream>>>(a, fac, any_lost);
     return cudaGetLastError();
 }
 

@@ -9,6 +9,37 @@ from test_gpu_dense import Batch
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("n,L", [(9, 9), (40, 60), (200, 300)])
+@pytest.mark.parametrize("value,rest", [(2.0 ** 40, 1.0), (1.0, 2.0 ** -40), (2.0 ** 20, 1.0), (2.0 ** 24, 1.0), (2.0 ** 30, 1.0)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_int8_prompts_behind_which_a_far_larger_value_lies(n, L, value, rest, out):
+    """The last token's value scale leaves those of the tokens before it, in the same block, far behind."""
+    b = Batch([(n, L), (n, L)], 2, 16, True, 0, out, seed=n)
+    rows = b.rows_of(0, torch.arange(L, device="cuda"))
+    b.pb.v_scale[rows] *= rest
+    b.pb.v_scale[rows[-1]] *= value / rest
+    b.check()
+
+
+@pytest.mark.parametrize("n,L", [(9, 9), (40, 60), (200, 300)])
+@pytest.mark.parametrize("key,rest", [(2.0 ** 60, 1.0), (2.0 ** 24, 1.0), (1.0, 2.0 ** -50)])
+def test_int8_prompts_behind_which_a_far_larger_key_lies(n, L, key, rest):
+    """The same of the keys; the rows that do not see it must not tell.  (In the last row the large key's score is
+    far above or below all others, and rounding decides nothing.)"""
+    b = Batch([(n, L), (n, L)], 2, 16, True, 0, torch.bfloat16, seed=n)
+    if rest != 1:  # tiny keys whose scores matter: queries that are large in turn
+        b.q[:n] *= 2.0 ** 50
+    rows = b.rows_of(0, torch.arange(L, device="cuda"))
+    b.pb.k_scale[rows] *= rest
+    b.pb.k_scale[rows[-1]] *= key / rest
+    ref, bound = b.ref()
+    got = b.run()
+    keep = torch.ones(2 * n, dtype=torch.bool, device="cuda")
+    keep[n - 1] = False
+    assert torch.isfinite(got).all()
+    assert ((got.double() - ref).abs() <= bound)[keep].all()
+
+
 @pytest.mark.parametrize("n", [1, 4, 40])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("first", [32, 70, 128])
