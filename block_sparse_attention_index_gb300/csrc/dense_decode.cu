@@ -22,7 +22,8 @@
 // power of two for each row (its largest value in [2^8, 2^9): bf16's 8 bits fit; what lies 2^-22 below the row's
 // largest loses bits).  The key scale multiplies the score and the value scale the weight.  A weight is 2^14 2^(x - m)
 // times the value scale over a power of two not below any of the scales so far, in one f16 part (2^-12; bf16
-// outputs) or two (2^-23; fp32): at most 2^14, and full precision down to 2^-28 of the largest.
+// outputs) or two (2^-23; fp32): at most 2^14.  A tile with a scale below 2^-14 of that power of two (one far larger may
+// be a drafted token's that earlier rows do not see) is summed key by key in fp32 instead: seldom, and six times slower.
 //
 // Where a sequence begins and ends inside one CTA, the CTA writes its output; else each CTA leaves its part (O, m,
 // l) in the workspace, at most two a CTA, and dense_combine_kernel joins them.
@@ -191,6 +192,36 @@ __device__ __forceinline__ void dd_store2(const DenseArgs& a, const DdSeq& s, in
         *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o) = make_float2(x, y);
 }
 
+// int8 tiles whose value scales reach below this part of the largest so far (or of a later token's, which rows before it
+// must not notice): f16 weights would have too few bits, so their keys are added one by one.
+constexpr float kDdApart = 6.103515625e-05f;  // 2^-14
+
+// O += weights x values of the keys of an int8 tile up to `last`, in fp32.  The weights lie over the stage's keys, [16][64];
+// o: the lane's 16 x 4 accumulators, in units of 1 / vinv; pos: its rows' positions in the block.
+template <int kPlane>
+static __device__ __noinline__ void dd_add_by_key(uint8_t* stage, int last, int2 pos, float* o, float vinv) {
+    const float* weights = reinterpret_cast<const float*>(stage);
+    const float* scales = reinterpret_cast<const float*>(stage + 2 * kPlane + 256);
+    const int lane = threadIdx.x & 31, grp = lane >> 2, tig = lane & 3;
+    for (int key = 0; key < last; ++key) {
+        const float v = scales[key] * vinv;
+        const uint8_t* row = stage + kPlane + key * 128 + 4 * tig;
+        for (int e = 0; e < 2; ++e) {
+            if (key > (e ? pos.y : pos.x)) continue;
+            const float w = weights[(grp + 8 * e) * kBlock + key] * v;
+            for (int chunk = 0; chunk < 8; ++chunk) {  // (dims as the lane's columns have them)
+                const char4 x = *reinterpret_cast<const char4*>(row + ((chunk ^ (key & 7)) << 4));
+                float* y = o + 8 * chunk + 2 * e;
+                y[0] = fmaf(w, x.x, y[0]);
+                y[4] = fmaf(w, x.y, y[4]);
+                y[1] = fmaf(w, x.z, y[1]);
+                y[5] = fmaf(w, x.w, y[5]);
+            }
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
+}
+
 template <int H, bool kInt8, int kParts>
 __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __grid_constant__ CUtensorMap k_map,
                                                                     const __grid_constant__ CUtensorMap v_map,
@@ -206,7 +237,8 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
     __shared__ uint64_t full[kDdFull], empty[Cfg::kStages];
     __shared__ int2 warp_tot[kDdThreads / 32];
     __shared__ uint32_t err;
-    __shared__ float tail_w[kDdConsumers][16][kDecodeMaxRows];
+    constexpr int kTailWarps = kInt8 ? 1 : kDdConsumers;  // (bf16 caches alone need it)
+    __shared__ float tail_w[kTailWarps][16][kDecodeMaxRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < kDdFull; ++s) mbar_init(&full[s], Cfg::kBarArrivals);
@@ -507,21 +539,39 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
                     top[e] = fmaxf(top[e], mrun[e]);
                 }
-                bool grew = top[0] > mrun[0] || top[1] > mrun[1];
+                bool grew = top[0] > mrun[0] || top[1] > mrun[1], apart = false;
                 float vnew = vref;
                 if constexpr (kInt8) {
-                    float big = 0.f;
+                    float big[8], low[8];
 #pragma unroll
-                    for (int nt = 0; nt < 8; ++nt) big = fmaxf(big, fmaxf(fabsf(vs[nt].x), fabsf(vs[nt].y)));
-                    if (big > vref && big < INFINITY) {  // the next power of two, at most 2^127
-                        vnew = __uint_as_float(min((__float_as_uint(big) + 0x007FFFFFu) & 0x7F800000u, 0x7F000000u));
+                    for (int nt = 0; nt < 8; ++nt) {
+                        big[nt] = fmaxf(fabsf(vs[nt].x), fabsf(vs[nt].y));
+                        low[nt] = fminf(fabsf(vs[nt].x), fabsf(vs[nt].y));
+                    }
+#pragma unroll
+                    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+                        for (int nt = 0; nt < d; ++nt) {
+                            big[nt] = fmaxf(big[nt], big[nt + d]);
+                            low[nt] = fminf(low[nt], low[nt + d]);
+                        }
+                    if (big[0] > vref && big[0] < INFINITY) {  // the next power of two, at most 2^127
+                        vnew = __uint_as_float(min((__float_as_uint(big[0]) + 0x007FFFFFu) & 0x7F800000u, 0x7F000000u));
                         grew = true;
                     }
+                    grew |= low[0] < vref * kDdApart;
                 }
                 if (__any_sync(0xffffffffu, grew)) {
                     if constexpr (kInt8) {  // the same in every lane
                         vnew = fmaxf(vnew, __shfl_xor_sync(0xffffffffu, vnew, 1));
                         vnew = fmaxf(vnew, __shfl_xor_sync(0xffffffffu, vnew, 2));
+                        bool below = false;
+#pragma unroll
+                        for (int nt = 0; nt < 8; ++nt) {
+                            below |= vs[nt].x != 0.f && fabsf(vs[nt].x) < vnew * kDdApart;
+                            below |= vs[nt].y != 0.f && fabsf(vs[nt].y) < vnew * kDdApart;
+                        }
+                        apart = __any_sync(0xffffffffu, below);
                     }
                     const float fv = kInt8 ? (vnew > 0.f ? vref / vnew : 1.f) : 1.f;
 #pragma unroll
@@ -557,6 +607,22 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     lrun[1] += sum[1].x + sum[1].y;
                 }
                 if constexpr (kInt8) {
+                    if (apart) {
+                        float* weights = reinterpret_cast<float*>(stage);  // (the keys are done with)
+                        float t[64];                                        // O goes through local memory here alone
+#pragma unroll
+                        for (int x = 0; x < 64; ++x) {
+                            if (x < 32) weights[(grp + 8 * ((x & 3) >> 1)) * kBlock + (x >> 2) * 8 + 2 * tig + (x & 1)] = c[x >> 2][x & 3];
+                            t[x] = o[x >> 2][x & 3];
+                        }
+                        __syncwarp();
+                        dd_add_by_key<Cfg::kPlane>(stage, min(kBlock, s.L - t0), make_int2(pos[0] - t0, pos[1] - t0), t, vinv);
+#pragma unroll
+                        for (int x = 0; x < 64; ++x) o[x >> 2][x & 3] = t[x];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&empty[st]);
+                        continue;
+                    }
                     if (edge) {  // a hidden key's weight stays 0 whatever its scale is
 #pragma unroll
                         for (int nt = 0; nt < 8; ++nt)
@@ -588,7 +654,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                         for (int e = 0; e < 4; ++e) {
                             const int key = nt * 8 + 2 * tig + (e & 1);
                             if (key >= first) {
-                                if (key < last) tail_w[warp][grp + 8 * (e >> 1)][key - first] = c[nt][e];
+                                if (key < last) tail_w[warp % kTailWarps][grp + 8 * (e >> 1)][key - first] = c[nt][e];
                                 c[nt][e] = 0.f;
                             }
                         }
@@ -597,7 +663,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             if (t0 + key > pos[e]) continue;
-                            const float w = tail_w[warp][grp + 8 * e][key - first];
+                            const float w = tail_w[warp % kTailWarps][grp + 8 * e][key - first];
 #pragma unroll
                             for (int nt = 0; nt < 16; ++nt) {
                                 const int chunk = nt & 7;

@@ -382,8 +382,9 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  * f16 weights of one part (2^-12, bf16 outputs) or two (2^-23, fp32) for up to
  * 8 rows a sequence, three bf16 parts for prompt chunks with fp32 outputs; with
  * bf16 outputs prompt chunks read an f16 copy of the cache (a key or value off
- * by 2^-12 of itself at most).  For up to 8 rows a sequence, a value whose scale
- * is below 2^-28 of the largest value scale met before it loses weight bits.
+ * by 2^-12 of itself at most).  For up to 8 rows a sequence, 64 positions with a
+ * value scale below 2^-14 of the largest of theirs and of those met before are
+ * summed in fp32.
  *
  * out must not overlap q or the caches.  The workspace's contents need no
  * initialisation; calls that share one must be ordered (one stream, or events).

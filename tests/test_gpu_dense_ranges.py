@@ -40,6 +40,20 @@ def test_int8_prompts_behind_which_a_far_larger_key_lies(n, L, key, rest):
     assert ((got.double() - ref).abs() <= bound)[keep].all()
 
 
+@pytest.mark.parametrize("n", [2, 3, 8])
+@pytest.mark.parametrize("L", [8, 64, 66, 300])
+@pytest.mark.parametrize("G", [2, 16])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_int8_windows_whose_later_values_are_far_larger(n, L, G, out):
+    for later in (2.0 ** 20, 2.0 ** 40, 2.0 ** 90, 2.0 ** -40):
+        b = Batch([(n, L), (n, L)], 4, G, True, 0, out, seed=n)
+        rows = b.rows_of(0, torch.arange(L, device="cuda"))
+        b.pb.v_scale[rows[L - n + 1:]] *= later
+        b.check()
+        b.pb.v_scale[rows[:L - n + 1]] = 0  # nothing but the later ones
+        b.check()
+
+
 @pytest.mark.parametrize("n", [1, 4, 40])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("first", [32, 70, 128])
