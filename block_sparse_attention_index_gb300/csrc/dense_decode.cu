@@ -222,6 +222,21 @@ static __device__ __noinline__ void dd_add_by_key(uint8_t* stage, int last, int2
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
 }
 
+// t += what was set aside, in t's units.  Both: the lane's 16 x 4 accumulators, the maxima of its two rows and the power
+// of two that the value scales are divided by, none of which fall.
+constexpr int kDdAside = 512;  // tiles of a warp: 2,048 additions, 1.2e-4
+static __device__ __noinline__ void dd_join_aside(const float* aside, float* t, bool some) {
+    if (!some) return;
+    const float unit = t[66] > 0.f ? aside[66] / t[66] : 1.f;
+    for (int e = 0; e < 2; ++e) {
+        const float f = aside[64 + e] == -INFINITY ? 0.f : dd_exp2(aside[64 + e] - t[64 + e]) * unit;
+        for (int x = 2 * e; x < 64; x += 4) {
+            t[x] = fmaf(aside[x], f, t[x]);
+            t[x + 1] = fmaf(aside[x + 1], f, t[x + 1]);
+        }
+    }
+}
+
 template <int H, bool kInt8, int kParts>
 __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __grid_constant__ CUtensorMap k_map,
                                                                     const __grid_constant__ CUtensorMap v_map,
@@ -391,7 +406,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
         const int grp = lane >> 2, tig = lane & 3, h = warp % H;
         // int8, bf16 outputs: the keys keep their bias and the accumulators begin at -1152 sum q (its cancellation costs
         // some 1e-5 of a score's spread, far below the outputs' rounding; fp32 outputs take the bias off)
-        constexpr bool kBiased = kInt8 && kParts == 1;
+        constexpr bool kBiased = kInt8 && kParts == 1, kAside = kInt8 && kParts == 1;
         bool alive = true;
         int i = (warp - static_cast<int>(begin % kDdConsumers)) & (kDdConsumers - 1), b = first_b;
         for (int cur = 0; cur < n_tiles;) {
@@ -460,8 +475,32 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
             float o[16][4], mrun[2] = {-INFINITY, -INFINITY}, lrun[2] = {0.f, 0.f};
 #pragma unroll
             for (int nt = 0; nt < 16; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+            float aside[kAside ? 67 : 1];  // O, maxima and unit of the tiles before (in local memory)
+            int since = 0;                  // tiles since
+            bool some = false;              // whether there were any
 
             for (; i < end; i += kDdConsumers) {
+                if constexpr (kAside) {
+                    if (since++ == kDdAside) {
+                        float t[67];
+#pragma unroll
+                        for (int x = 0; x < 64; ++x) t[x] = o[x >> 2][x & 3];
+                        t[64] = mrun[0];
+                        t[65] = mrun[1];
+                        t[66] = vref;
+                        dd_join_aside(aside, t, some);
+#pragma unroll
+                        for (int x = 0; x < 64; ++x) {
+                            aside[x] = t[x];
+                            o[x >> 2][x & 3] = 0.f;
+                        }
+                        aside[64] = mrun[0];
+                        aside[65] = mrun[1];
+                        aside[66] = vref;
+                        some = true;
+                        since = 1;
+                    }
+                }
                 const int st = i % Cfg::kStages, j = u0 + (i + h_off) / H - seg0, t0 = j * kBlock;
                 if (alive) alive = mbar_wait(&full[i % kDdFull], (i / kDdFull) & 1, &err);
                 if (!alive) continue;
@@ -684,8 +723,10 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
                     __syncwarp();
                 }
-                // O += P V, 16 keys a step.  The tensor cores cut what an addition loses (a bias of about 2^-25 each,
-                // 1.5e-4 after 33,280 keys), so with fp32 outputs a tile is summed by itself and then added to O.
+                // O += P V, 16 keys a step.  The tensor cores cut what an addition loses instead of rounding it (a bias of
+                // about 2^-25 each, 1.5e-4 after 33,280 keys), so a tile is summed by itself and then added to O; int8
+                // caches with bf16 outputs, where that would cost 8 % (46.3 against 42.9 us for 8 ragged sequences), set
+                // O aside every so many tiles instead.
                 uint32_t pa[4][kParts][4];
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -706,7 +747,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                             }
                         }
                     }
-                constexpr bool kApart = kParts == (kInt8 ? 2 : 3);  // fp32 outputs: a tile's product by itself
+                constexpr bool kApart = !kAside;  // a tile's product by itself
                 if constexpr (kInt8) {
 #pragma unroll
                     for (int n4 = 0; n4 < 4; ++n4) {
@@ -733,7 +774,11 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 #pragma unroll
                             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) o[4 * n4 + n][e] += t[n][e];
+                                for (int e = 0; e < 4; e += 2) {
+                                    const float2 x = __fadd2_rn(make_float2(o[4 * n4 + n][e], o[4 * n4 + n][e + 1]), make_float2(t[n][e], t[n][e + 1]));
+                                    o[4 * n4 + n][e] = x.x;
+                                    o[4 * n4 + n][e + 1] = x.y;
+                                }
                         }
                     }
                 } else {
@@ -762,7 +807,11 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
 #pragma unroll
                             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) o[4 * n4 + n][e] += t[n][e];
+                                for (int e = 0; e < 4; e += 2) {
+                                    const float2 x = __fadd2_rn(make_float2(o[4 * n4 + n][e], o[4 * n4 + n][e + 1]), make_float2(t[n][e], t[n][e + 1]));
+                                    o[4 * n4 + n][e] = x.x;
+                                    o[4 * n4 + n][e + 1] = x.y;
+                                }
                         }
                     }
                 }
@@ -770,6 +819,19 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                 if (lane == 0) mbar_arrive(&empty[st]);
             }
 
+            if constexpr (kAside) {
+                if (some) {
+                    float t[67];
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) t[x] = o[x >> 2][x & 3];
+                    t[64] = mrun[0];
+                    t[65] = mrun[1];
+                    t[66] = vref;
+                    dd_join_aside(aside, t, true);
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) o[x >> 2][x & 3] = t[x];
+                }
+            }
             if constexpr (kInt8) {
 #pragma unroll
                 for (int nt = 0; nt < 16; ++nt)

@@ -73,3 +73,37 @@ def test_scores_of_minus_infinity_weigh_nothing(first, out, n):
         live = n - 1
     got = b.run()
     assert ((got.double() - ref).abs() <= 2.5 * 2.0 ** -8 * most)[:live].all()
+
+
+C = 1 + 2.0 ** -7  # a value whose sums need every bit
+
+
+def long_batch(B, n, G, int8, length=1 << 21, H=8, seed=1):
+    """B sequences that share one cache of `length` positions; every value is C."""
+    m = msa()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    kw = {}
+    if int8:
+        k = torch.randint(-127, 128, (length, H, 128), generator=g, device="cuda", dtype=torch.int8)
+        v = torch.full((length, H, 128), 1, device="cuda", dtype=torch.int8)
+        kw = {"k_scale": torch.full((length, H), 1 / 64, device="cuda"), "v_scale": torch.full((length, H), C, device="cuda")}
+    else:
+        k = torch.randn(length, H, 128, generator=g, device="cuda", dtype=torch.bfloat16)
+        v = torch.full((length, H, 128), C, device="cuda", dtype=torch.bfloat16)
+    pb = m.Problem(H, G, [(n, length)] * B, "cuda", out_dtype=torch.bfloat16, cache_tokens=length, cache_starts=[0] * B, **kw)
+    q = torch.randn(B * n, H * G, 128, generator=g, device="cuda", dtype=torch.bfloat16)
+    return m, pb, q, k, v
+
+
+@pytest.mark.parametrize("B,n,G,int8", [(160, 1, 4, False), (160, 1, 4, True), (19, 4, 16, True)])
+def test_the_longest_contexts_do_not_drift(B, n, G, int8):
+    """Every value is C, so every output is, whatever the weights are.  A CTA walks all 2^21 positions.  Rounded
+    weights differ from the summed ones at random (2^-8 L^-1/2 of the sum) and the sums of 32 bits are off by less
+    than 2^-10, together below half a step of bf16 (2^-8), so the output is C itself; sums that lose something in the
+    same direction 10^5 times are not."""
+    m, pb, q, k, v = long_batch(B, n, G, int8)
+    ws = pb.dense_workspace()
+    out = m.dense_forward(pb, q, k, v, workspace=ws)
+    torch.cuda.synchronize()
+    assert m.error_word(ws) == 0
+    assert (out.float() == C).all(), (out.float().min().item(), out.float().max().item())
