@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kDdThreads, 1) dense_decode_kernel(const __gri
                     __syncwarp();
                 }
                 // O += P V, 16 keys a step.  The tensor cores cut what an addition loses instead of rounding it (a bias of
-                // about 2^-25 each, 1.5e-4 after 33,280 keys), so a tile is summed by itself and then added to O; int8
+                // about 2^-24 each, 1.5e-4 after 33,280 keys), so a tile is summed by itself and then added to O; int8
                 // caches with bf16 outputs, where that would cost 8 % (46.3 against 42.9 us for 8 ragged sequences), set
                 // O aside every so many tiles instead.
                 uint32_t pa[4][kParts][4];

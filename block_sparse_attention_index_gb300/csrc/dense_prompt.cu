@@ -22,8 +22,10 @@
 //
 // With bf16 outputs a weight enters P V as one bf16 (2^-9 relative, at random, about the output's own rounding); with
 // fp32 outputs as three parts (2^-24), NK = 64 then, so that the parts fit over S.  The tensor cores cut what an
-// addition loses instead of rounding it, a bias of about 2^-25 per addition (1.5e-4 after 33,280 keys, measured), so
-// with fp32 outputs O_s holds two key tiles' products only and the softmax group adds them to its rows in registers.
+// addition loses instead of rounding it, a bias of about 2^-24 per addition of 16 keys (1.5e-4 after 33,280 keys,
+// measured), so with fp32 outputs O_s holds two key tiles' products only and the softmax group adds them to its rows in
+// registers; with bf16 outputs (whose half step is 2^-8) 256 tiles' products, which the group then adds to a sum in the
+// workspace.
 //
 // Drafted windows (kAlt): one M tile, and the two stages take alternate key tiles, each with its own running state.
 //
@@ -78,6 +80,10 @@ struct DpItem {
 };
 constexpr int kDpInfo = 3;     // items published ahead
 constexpr int kDpClaim = 4;    // key tiles before the end of an item's copies at which the next one is taken
+
+// Key tiles whose products O is summed over in tensor memory before they are added to the row's sum.
+template <int kParts>
+constexpr int kDpRun = kParts > 1 ? 2 : kDenseRunKeys / 128;
 
 enum DpForm { kDpBf16 = 0, kDpInt = 1, kDpF16 = 2 };  // bf16 caches; int8: bf16 integers with scales; int8: f16 copy
 
@@ -531,6 +537,48 @@ __device__ __noinline__ int dp_last_bad(const DenseArgs& a, int b, int h, int fi
     return __reduce_max_sync(0xffffffffu, bad);
 }
 
+// bf16 outputs: the row's sum over earlier runs of tiles lies in the workspace, [128 dims, maximum, value exponent][row] of
+// the CTA's stage.  Adds O in tensor memory to it (`first`: there was none) or, `back`, it to O (a whole warp, a row a
+// thread), in units of the present maximum and value exponent.
+constexpr int kDpAsideRows = kHeadDim + 2;
+__device__ __forceinline__ void dp_aside(float* base, uint32_t o_addr, float top, int vexp, bool first, bool back) {
+    float* aside = base + (static_cast<int64_t>(blockIdx.x) * 2 + (threadIdx.x >> 7)) * (kDpAsideRows * 128) + (threadIdx.x & 127);
+    float f = 0.f;
+    if (!first) {
+        const float then = aside[kHeadDim * 128];
+        const int e = static_cast<int>(aside[(kHeadDim + 1) * 128]) - vexp;
+        f = then == -INFINITY || e < -126 ? 0.f : dp_exp2(then - top) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    }
+#pragma unroll 1
+    for (int q = 0; q < kHeadDim / 32; ++q) {
+        float y[32];
+        dp_ld32(o_addr + 32 * q, y);
+        tmem_ld_wait();
+        if (!first) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y[k] = fmaf(aside[(32 * q + k) * 128], f, y[k]);
+        }
+        if (back) {
+            dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) aside[(32 * q + k) * 128] = y[k];
+        }
+    }
+    if (back) {
+        dp_st_wait();
+    } else {
+        aside[kHeadDim * 128] = top;
+        aside[(kHeadDim + 1) * 128] = static_cast<float>(vexp);
+    }
+}
+
+// The same as a call, which is what the kernel on bf16 caches runs faster with (8 packed prompts 106 us, inline 108), and
+// the one on the f16 copy slower (2,048 rows at 8,192 531, inline 518).
+__device__ __noinline__ void dp_aside_call(float* base, uint32_t o_addr, float top, int vexp, bool first, bool back) {
+    dp_aside(base, o_addr, top, vexp, first, back);
+}
+
 // How far apart the value factors of an item's blocks are, log2 (blocks of zeros left out); 127 if some key or value of
 // one has lost bits (a whole warp).
 __device__ __noinline__ int dp_apart(const float2* fac, int first, int end) {
@@ -865,7 +913,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                                 for (int i = 4 * h2; i < 4 * h2 + 4; ++i)
                                     dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + i * 8,
                                               vb + static_cast<uint64_t>(i * 2048 >> 4), idesc_o,
-                                              !((kParts > 1 ? (c & 1) == 0 : c == 0) && part == 0 && i == 0));
+                                              !(c % kDpRun<kParts> == 0 && part == 0 && i == 0));
                         }
                         if (!ok) break;
                         if (next) {
@@ -988,12 +1036,20 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                     }
                 }
             };
+            auto aside = [&](bool first, bool back) {
+                if constexpr (kF16) dp_aside(a.aside, o_addr, top, vexp, first, back);
+                else dp_aside_call(a.aside, o_addr, top, vexp, first, back);
+            };
             for (int c = 0; alive && c < count; ++c) {
                 const int j = kAlt ? 2 * c + s : c, t0 = (w.first + j) * NK;
                 alive = __all_sync(0xffffffffu, wait(&sm.s_full[s], (tiles + c) & 1));
                 if (!alive) break;
                 tc_fence_after();
-                if (c > 0 && (c & 1) == 0) collect();
+                if constexpr (kParts > 1) {
+                    if (c > 0 && c % kDpRun<kParts> == 0) collect();
+                } else {
+                    if (c > 0 && c % kDpRun<kParts> == 0) aside(c == kDpRun<kParts>, false);
+                }
                 if constexpr (kParts > 1) {  // ---- fp32 outputs: 32 scores at a time, O in registers (the code below has no room for it)
                     const bool edge = t0 + NK > early + 1;  // some key is hidden from some row of the tile
                     const int e = (tiles_before + j) % kDpScaleSlots;
@@ -1220,6 +1276,9 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
                 if (alive && have) alive = __all_sync(0xffffffffu, wait(&sm.o_full[s], done++ & 1));
                 tc_fence_after();
                 if (alive && have) collect();
+                if constexpr (kParts == 1) {
+                    if (alive && count > kDpRun<kParts>) aside(false, true);
+                }
                 constexpr int kRun = 32;  // values of the row that are finished at a time
                 auto row_of_o = [&](int q, float (&y)[kRun]) {
                     if constexpr (kParts > 1) {

@@ -233,11 +233,13 @@ struct DenseArgs {
     int32_t* unit_prefix;  // [2][num_seqs + 1] decode family: units, and segments, before each sequence
     float* part_o;         // parts of what several CTAs walk: O [.., 128], decode family [2 shares, H, 16]
     float* part_ml;        // and their maxima and sums [.., 2]
+    float* aside;          // prompts, windows with bf16 outputs: sums over earlier keys [places][2][130][128]
     uint32_t* err_slots;   // [shares] error bits of the decode family's CTAs
     int err_store;         // 1: the combine stores the error word, 0: it adds to it
     uint32_t* err;
 };
 constexpr int kDenseMaxParts = 960;   // most parts of items that are split over their keys (M tiles, prompts: pairs)
+constexpr int kDenseRunKeys = 256 * 128;  // prompts, windows with bf16 outputs: keys that are summed in tensor memory at a time
 constexpr int kDenseMaxShares = 160;  // most CTAs that share the decode family's cache walk
 // Prompt chunks (M tile pairs of 2 (128 / G) rows) and drafted windows (one M tile a sequence); items: host bound.
 cudaError_t run_dense_prompt(const DenseArgs& a, int items, cudaStream_t stream);

@@ -262,7 +262,7 @@ DensePlan dense_plan(const msa_problem* p) {
 }
 
 struct DenseLayout {
-    size_t err = 0, err_slots = 0, unit_prefix = 0, split = 0, part_ml = 0, part_o = 0, wide_starts = 0, wide_k = 0, wide_v = 0,
+    size_t err = 0, err_slots = 0, unit_prefix = 0, split = 0, part_ml = 0, part_o = 0, aside = 0, wide_starts = 0, wide_k = 0, wide_v = 0,
            wide_ks = 0, wide_vs = 0, total = 0;
 };
 
@@ -283,6 +283,9 @@ DenseLayout dense_layout(const msa_problem* p, const DensePlan& d) {
     off = align256(off + parts * 2 * sizeof(float));
     l.part_o = off;
     off = align256(off + parts * msa::kHeadDim * sizeof(float));
+    l.aside = off;
+    if ((d.windows || d.prompts) && p->out_dtype == MSA_OUT_BF16 && p->max_cache_len > msa::kDenseRunKeys)
+        off = align256(off + static_cast<size_t>(msa::kDenseMaxShares) * 2 * 128 * (msa::kHeadDim + 2) * sizeof(float));
     if (d.wide_slots > 0) {
         const size_t rows = static_cast<size_t>(d.wide_slots * d.slot_rows);
         l.wide_starts = off;
@@ -975,6 +978,7 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     a.split_items = reinterpret_cast<int4*>(ws + l.split) + 1;
     a.part_o = reinterpret_cast<float*>(ws + l.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+    a.aside = reinterpret_cast<float*>(ws + l.aside);
     a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
     // (a call for full windows launches no streaming kernel: the window kernel takes the shorter ones too)
     a.window_above = !d.windows ? INT32_MAX : (d.stream ? 16 : 0);

@@ -388,7 +388,9 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  *
  * out must not overlap q or the caches.  The workspace's contents need no
  * initialisation; calls that share one must be ordered (one stream, or events).
- * It holds the parts of what is split over keys (up to 130 MB) and, for an int8
+ * It holds the parts of what is split over keys (up to 130 MB), for prompt chunks
+ * and drafted windows with bf16 outputs and contexts above 32,768 positions the
+ * rows' sums of earlier keys (22 MB), and, for an int8
  * cache with prompt chunks, the widened copy: 4 H (D + 2) bytes a position of
  * every such sequence, as many sequences at a time as 8 GiB hold (at least one). */
 msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_cache, const void* v_cache,
