@@ -23,7 +23,8 @@
 // largest loses bits).  The key scale multiplies the score and the value scale the weight.  A weight is 2^14 2^(x - m)
 // times the value scale over a power of two not below any of the scales so far, in one f16 part (2^-12; bf16
 // outputs) or two (2^-23; fp32): at most 2^14.  A tile with a scale below 2^-14 of that power of two (one far larger may
-// be a drafted token's that earlier rows do not see) is summed key by key in fp32 instead: seldom, and six times slower.
+// be a drafted token's that earlier rows do not see) is summed key by key in fp32 instead, nine times slower (377 us
+// where all tiles of the 43 us below are such, 68 us where one of 50 is).
 //
 // Where a sequence begins and ends inside one CTA, the CTA writes its output; else each CTA leaves its part (O, m,
 // l) in the workspace, at most two a CTA, and dense_combine_kernel joins them.
@@ -203,21 +204,30 @@ static __device__ __noinline__ void dd_add_by_key(uint8_t* stage, int last, int2
     const float* weights = reinterpret_cast<const float*>(stage);
     const float* scales = reinterpret_cast<const float*>(stage + 2 * kPlane + 256);
     const int lane = threadIdx.x & 31, grp = lane >> 2, tig = lane & 3;
-    for (int key = 0; key < last; ++key) {
-        const float v = scales[key] * vinv;
-        const uint8_t* row = stage + kPlane + key * 128 + 4 * tig;
-        for (int e = 0; e < 2; ++e) {
-            if (key > (e ? pos.y : pos.x)) continue;
-            const float w = weights[(grp + 8 * e) * kBlock + key] * v;
-            for (int chunk = 0; chunk < 8; ++chunk) {  // (dims as the lane's columns have them)
-                const char4 x = *reinterpret_cast<const char4*>(row + ((chunk ^ (key & 7)) << 4));
-                float* y = o + 8 * chunk + 2 * e;
-                y[0] = fmaf(w, x.x, y[0]);
-                y[4] = fmaf(w, x.y, y[4]);
-                y[1] = fmaf(w, x.z, y[1]);
-                y[5] = fmaf(w, x.w, y[5]);
+    const float* w0 = weights + grp * kBlock;
+    const float* w1 = w0 + 8 * kBlock;
+    for (int chunk = 0; chunk < 8; ++chunk) {  // (dims as the lane's columns have them)
+        float* y = o + 8 * chunk;
+        float a[8] = {y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]};
+#pragma unroll 4
+        for (int key = 0; key < last; ++key) {
+            const char4 x = *reinterpret_cast<const char4*>(stage + kPlane + key * 128 + ((chunk ^ (key & 7)) << 4) + 4 * tig);
+            const float v = scales[key] * vinv, f0 = w0[key] * v, f1 = w1[key] * v;
+            if (key <= pos.x) {
+                a[0] = fmaf(f0, x.x, a[0]);
+                a[1] = fmaf(f0, x.y, a[1]);
+                a[2] = fmaf(f0, x.z, a[2]);
+                a[3] = fmaf(f0, x.w, a[3]);
+            }
+            if (key <= pos.y) {
+                a[4] = fmaf(f1, x.x, a[4]);
+                a[5] = fmaf(f1, x.y, a[5]);
+                a[6] = fmaf(f1, x.z, a[6]);
+                a[7] = fmaf(f1, x.w, a[7]);
             }
         }
+        y[0] = a[0], y[4] = a[1], y[1] = a[2], y[5] = a[3];
+        y[2] = a[4], y[6] = a[5], y[3] = a[6], y[7] = a[7];
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
 }
