@@ -233,8 +233,12 @@ DensePlan dense_plan(const msa_problem* p) {
     const int64_t G = p->group_size;
     const int64_t known = p->num_decode_seqs;  // -1: unknown
     // A few short contexts beside prompt chunks ride along with the chunks: their keys are at most 32 tiles each, in what
-    // is left of a wave, where kernels of their own cost 20 us (packed prompts with one 1-row sequence: 143 us).
-    d.all_prompts = prefill_family(p) && known > 0 && known * p->num_kv_heads <= 128 && p->max_cache_len <= 4096;
+    // is left of a wave, where kernels of their own cost 15 to 20 us.  With and without, in us, 4 x 16 heads, single rows
+    // beside a chunk of 512 (one row beside 130 at 500: 19 and 33): bf16 1 at 2,000 37 and 53, 32 at 4,000 99 and 134.
+    // int8 caches, whose contexts are then widened too: 1 at 4,000 79 and 98, 8 at 2,000 78 and 70, 32 at 4,000 206 and
+    // 146, so only where they are 8,192 positions in all.
+    d.all_prompts = prefill_family(p) && known > 0 && known * p->num_kv_heads <= 128 && p->max_cache_len <= 4096 &&
+                    (p->kv_dtype != MSA_KV_INT8 || known * p->max_cache_len <= 8192);
     if (decode_family(p) && !d.all_prompts) {
         const int64_t rows = static_cast<int64_t>(decode_rows_per_seq(p)), seqs = known >= 0 ? known : p->num_seqs;
         const bool one_row = known >= 0 && p->num_decode_rows == known;  // every sequence
