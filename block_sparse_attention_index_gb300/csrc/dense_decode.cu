@@ -3,8 +3,8 @@
 // in one pass: a running maximum m, sum l and unnormalised output O per (row, query head), rescaled by
 // 2^(m - m') when the maximum grows, and the parts of a sequence that several CTAs walk joined by the same rule.
 //
-// Bound by memory: each cached position is H x 512 bytes (264 with an int8 cache) that are read once for all query
-// heads of the sequence's rows.  The cache is split over its length: one CTA per SM takes an even share of all
+// Bound by memory: each cached position is H x 512 bytes (264 with an int8 cache) that are read once for 16 (row, query
+// head) pairs (more: bf16 windows are the window kernel's; int8 windows read the cache once for every 16).  The cache is split over its length: one CTA per SM takes an even share of all
 // 64-position blocks of all sequences (from the lengths on the device, so ragged batches balance) and streams them
 // through a ring of shared-memory stages, one (block, KV head) tile of K and V each, by TMA boxes issued by two
 // producer warps.  Heads of a block are neighbours in the ring, so memory is read in whole 64 H-row runs.  Eight
@@ -21,19 +21,19 @@
 // keys, and the second product's pairs of keys come from transposed loads of byte pairs.  Queries become f16 times a
 // power of two for each row (its largest value in [2^8, 2^9): bf16's 8 bits fit; what lies 2^-22 below the row's
 // largest loses bits).  The key scale multiplies the score and the value scale the weight.  A weight is 2^14 2^(x - m)
-// times the value scale over a power of two not below any of the scales so far, in one f16 part (2^-12; bf16
-// outputs) or two (2^-23; fp32): at most 2^14.  A tile with a scale below 2^-14 of that power of two (one far larger may
+// times the value scale over a power of two not below any of the scales so far, in one f16 part (2^-11; bf16
+// outputs) or two (2^-22; fp32): at most 2^14.  A tile with a scale below 2^-14 of that power of two (one far larger may
 // be a drafted token's that earlier rows do not see) is summed key by key in fp32 instead, nine times slower (377 us
 // where all tiles of the 43 us below are such, 68 us where one of 50 is).
 //
 // Where a sequence begins and ends inside one CTA, the CTA writes its output; else each CTA leaves its part (O, m,
 // l) in the workspace, at most two a CTA, and dense_combine_kernel joins them.
 //
-// Measured (with the combine): 4 rows at 65,536, 4 x 16 heads, 96 us, 7.08 TB/s while every SM streams (they end 77 to 86
-// us in, the combine 4 us later); 8 int8 sequences of 1,024 to 196,608, 47 us, bound by the 1,670 instructions a tile
-// and warp, two warps a scheduler (41 % of the issue slots taken, waits on the instruction before the rest; registers
-// leave no room for a third); 64 sequences of 3 to 4,096, 8 x 4 heads, 43 us, a third of it before the first
-// tile and after the last.
+// Measured (with the combine): 4 rows at 65,536, 4 x 16 heads, 92 us called back to back, 95 as a graph of one call
+// (whose start nothing overlaps), 7.08 TB/s while every SM streams (they end 77 to 86 us in, the combine 4 us later); 8
+// int8 sequences of 1,024 to 196,608, 43 and 46 us, bound by the 1,730 instructions a tile and warp, two warps a scheduler
+// (42 % of the issue slots taken, waits on the instruction before the rest; registers leave no room for a third); 64
+// sequences of 3 to 4,096, 8 x 4 heads, 37 and 40 us, a third of it before the first tile and after the last.
 #include <algorithm>
 
 #include <cuda_fp16.h>

@@ -20,7 +20,9 @@
 // sums and bf16 weights carry without loss); the group that owns O then multiplies it in tensor memory.  So most tiles
 // rescale nothing.
 //
-// With bf16 outputs a weight enters P V as one bf16 (2^-9 relative, at random, about the output's own rounding); with
+// With bf16 outputs a weight enters P V as one bf16, 2^-8 of itself off at most and at random: in the 2-norm 1.66e-3 to
+// 1.8e-3 of the outputs with their own rounding, which alone is 1.65e-3.  (A row with two keys may be off by 4.5e-3, more
+// than fp32 outputs allow and less than a step of bf16, 7.8e-3 at 1.)  With
 // fp32 outputs as three parts (2^-24), NK = 64 then, so that the parts fit over S.  The tensor cores cut what an
 // addition loses instead of rounding it, a bias of about 2^-24 per addition of 16 keys (1.5e-4 after 33,280 keys,
 // measured), so with fp32 outputs O_s holds two key tiles' products only and the softmax group adds them to its rows in
@@ -40,18 +42,20 @@
 // ring is free for one key tile's time, so with one thread the matrix instructions waited 580 of 2,900 cycles a tile for
 // them (two: 300, which is what testing two complete barriers takes).
 //
-// What bounds it: bf16, the tensor pipe (4,096 rows at 8,192, 4 x 16 heads: 1.37 TFLOP in 805 to 870 us with the clocks
-// that the power limit leaves, 1.58 to 1.70 PFLOP/s of 1.92 measured for cuBLAS in short bursts, 1.74 sustained); int8
-// with bf16 outputs, the softmax groups' instructions (0.62 TFLOP in 515 us); fp32 outputs, likewise (0.55 TFLOP, with
-// three weight parts 1.1 on the tensor cores, in 958 us); short sequences, the 3.5 us an item that its groups spend between
+// What bounds it: bf16, the tensor pipe (4,096 rows at 8,192, 4 x 16 heads: 1.37 TFLOP in 800 to 880 us with the clocks
+// that the power limit leaves, 1.56 to 1.71 PFLOP/s of 1.92 measured for cuBLAS in short bursts, 1.74 sustained); int8
+// with bf16 outputs, the softmax groups' instructions (0.62 TFLOP in 518 us); fp32 outputs, likewise (0.55 TFLOP, with
+// three weight parts 1.1 on the tensor cores, in 965 us); short sequences, the 3.5 us an item that its groups spend between
 // its last scores and the next one's first, against 1.6 us a key tile.
 //
 // int8 caches are read from a copy widened once per call.  bf16 outputs: f16 values with the scales in them, over a
 // power of two for each 64-position block (run_widen_f16), queries as f16 times a power of two for each row (converted
 // in shared memory by the softmax threads; bf16's 8 bits fit, what lies 2^-22 below the row's largest loses some) and
-// weights as one f16 (2^-12), at most 2^14: the blocks' powers of two are two scalars each for the softmax, where the
-// scales themselves, one for each key, were a third of its instructions (784 us for 2,048 rows at 8,192, now 515).  fp32 outputs:
+// weights as one f16 (2^-11), at most 2^14: the blocks' powers of two are two scalars each for the softmax, where the
+// scales themselves, one for each key, were a third of its instructions (784 us for 2,048 rows at 8,192, now 518).  fp32 outputs:
 // bf16 integers, exact, scales beside them (run_widen_kv); the key scale multiplies the score, the value scale the weight.
+// The rounded keys cost the outputs 1.75e-3 where their own rounding is 1.65e-3 (2-norm), with even keys as with one
+// channel 16 times the others.  Rows whose blocks' scales lie too far apart for f16 are computed again, as below.
 //
 // Values that no row of the tile may see: positions past the length are zeroed in the last value tile (by warp 10), so
 // stale cache rows do not matter.  A later token of the same chunk meets weights of zero; if its value is not finite
@@ -942,7 +946,7 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_prompt_kernel(const __gri
             }
         }
     } else {
-        // 168 x 384 registers at launch: 208 x 256 + 88 x 128 (fp32 outputs, 512 rows at 32,768: 958 us; with 200 and 104
+        // 168 x 384 registers at launch: 208 x 256 + 88 x 128 (fp32 outputs, 512 rows at 32,768: 965 us; with 200 and 104
         // 1,001, the groups spill; with 232 and 40 1,069, the copying warps do)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------- softmax group s: thread = row of M tile s

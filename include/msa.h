@@ -369,22 +369,34 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  *                   over t = 0 .. p
  * for decode rows, drafted windows and prompt chunks (packed sequences of
  * different lengths, each with its cached prefix) in one call; contiguous or
- * paged caches, bf16 or int8 with scales.  Rows of a sequence share each
- * read of a key or value.  Cache rows past a sequence's length may hold
+ * paged caches, bf16 or int8 with scales.  Up to 16 (row, head) pairs of a
+ * sequence share each read of a key or value, and with a bf16 cache all rows of a
+ * drafted window or a tile of a prompt chunk do (int8: a window reads the cache
+ * once for every 16 pairs).  Cache rows past a sequence's length may hold
  * anything, NaN included.  Rows of out at or past cu_rows[num_seqs] are left
  * as they were; a sequence of no rows is skipped.
  *
- * Numerics.  Scores, maxima and sums are fp32.  The softmax weights enter the
- * products with V, bf16 caches: as three bf16 parts (2^-24) with fp32 outputs;
- * with bf16 outputs as one (2^-9, prompt chunks) or two (2^-17, decode rows and
- * drafted windows of up to 16 (row, head) pairs, but for those of a call whose
- * num_decode_rows says that all windows are longer).  int8 caches: exact codes,
- * f16 weights of one part (2^-12, bf16 outputs) or two (2^-23, fp32) for up to
- * 8 rows a sequence, three bf16 parts for prompt chunks with fp32 outputs; with
- * bf16 outputs prompt chunks read an f16 copy of the cache (a key or value off
- * by 2^-12 of itself at most).  For up to 8 rows a sequence, 64 positions with a
- * value scale below 2^-14 of the largest of theirs and of those met before are
- * summed in fp32.
+ * Numerics.  Scores, maxima and sums are fp32.  A rounding below is half a step at
+ * most.  The softmax weights enter the products with V, bf16 caches: as three bf16
+ * parts (2^-24) with fp32 outputs; with bf16 outputs as one (2^-8, prompt chunks
+ * and larger windows) or two (2^-16, decode rows and drafted windows of up to 16
+ * (row, head) pairs, but for those of a call whose num_decode_rows says that all
+ * windows are longer).  int8 caches: exact codes, f16 weights of one part (2^-11,
+ * bf16 outputs) or two (2^-22, fp32) for up to 8 rows a sequence, three bf16 parts
+ * for prompt chunks with fp32 outputs; with bf16 outputs prompt chunks read an f16
+ * copy of the cache, a key or value off by 2^-11 of itself at most, a score by
+ * 2^-11 softmax_scale sum_d |q_d k_d|.  Which of these a row gets depends on the
+ * call: short contexts beside prompt chunks (at most 128 (sequence, KV head) pairs
+ * and max_cache_len 4,096; int8: 8,192 positions in all) are computed as the
+ * chunks are.  The same call gives the same bits every time.
+ * A later token's key, value or scale, of any size, infinite or NaN, does not
+ * reach the rows before it.  An infinite value that a row does see makes outputs
+ * infinite or NaN.  int8 caches, up to 8 rows a sequence: 64 positions with a value
+ * scale below 2^-14 of the largest of theirs and of those met before are summed
+ * in fp32.  Prompt chunks: rows that a later token's value would spoil, and int8
+ * rows that meet scales more than 2^22 apart in 64 positions, are computed again
+ * in fp32 (about 70 clocks a key and row).  The kernel's waits, some two seconds
+ * elsewhere, may take 8 us a position of max_cache_len longer for these.
  *
  * out must not overlap q or the caches.  The workspace's contents need no
  * initialisation; calls that share one must be ordered (one stream, or events).
