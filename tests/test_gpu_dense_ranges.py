@@ -108,3 +108,18 @@ def test_the_longest_contexts_do_not_drift(B, n, G, int8):
     torch.cuda.synchronize()
     assert m.error_word(ws) == 0
     assert (out.float() == C).all(), (out.float().min().item(), out.float().max().item())
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_int8_values_that_are_all_zero(n, out):
+    """Scales of zero everywhere, and everywhere but in the last, or the first, few positions."""
+    for keep in (slice(0, 0), slice(295, 300), slice(0, 3)):
+        b = Batch([(n, 300), (n, 200)], 2, 16, True, 64, out, seed=n)
+        rows = b.rows_of(0, torch.arange(300, device="cuda"))
+        kept = b.pb.v_scale[rows[keep]].clone()
+        b.pb.v_scale[rows] = 0
+        b.pb.v_scale[rows[keep]] = kept
+        b.check()
+        if keep.stop == 0:
+            assert (b.run()[:n] == 0).all()
