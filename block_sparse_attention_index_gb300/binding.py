@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libmsa_gb300.so")
 MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_WORKSPACE, MSA_ERR_CUDA, MSA_ERR_INTERNAL = range(6)
 MSA_OUT_F32, MSA_OUT_BF16 = 0, 1
 MSA_KV_BF16, MSA_KV_INT8 = 0, 1
+MSA_IK_BF16, MSA_IK_INT8 = 0, 1
 ERR_WAIT_TIMEOUT, ERR_BAD_METADATA, ERR_TMEM_ALLOC = 1, 2, 4
 
 EXPORTED = [
@@ -45,6 +46,8 @@ class MsaProblem(C.Structure):
         ("cache_starts", C.c_void_p), ("block_table", C.c_void_p), ("block_table_stride", C.c_int32),
         ("page_size", C.c_int32), ("index_key_heads", C.c_int32), ("kv_dtype", C.c_int32),
         ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("num_decode_rows", C.c_int32),
+        ("ik_dtype", C.c_int32), ("ik_exp", C.c_void_p), ("num_groups", C.c_int32), ("max_shared_len", C.c_int32),
+        ("max_group_rows", C.c_int32), ("group_starts", C.c_void_p), ("group_shared", C.c_void_p),
     ]
 
 
@@ -59,7 +62,7 @@ class MsaAppend(C.Structure):
     """Mirror of struct msa_append."""
     _fields_ = [(n, C.c_void_p) for n in ("k", "v", "ik", "q", "iq")] + \
         [(n, C.c_int64) for n in ("k_stride", "v_stride", "ik_stride", "q_stride", "iq_stride")] + \
-        [(n, C.c_void_p) for n in ("k_cache", "v_cache", "ik_cache", "k_scale", "v_scale", "q_out", "iq_out")]
+        [(n, C.c_void_p) for n in ("k_cache", "v_cache", "ik_cache", "k_scale", "v_scale", "ik_exp", "q_out", "iq_out")]
 
 
 class MsaError(RuntimeError):
@@ -166,12 +169,19 @@ class Problem:
     of scales, refuses.
     num_decode_rows: host count of decode-family rows ("auto": from seqs_host;
     0: unknown, the decode attention then covers every row slot).
+    ik_exp (int8 [cache_tokens, KH] device tensor): the index-key cache is
+    int8 codes, each head of a position times 2^ik_exp.  Must be the tensor
+    itself (right type, device and layout), as append_cache writes it.
+    shared: groups of neighbouring sequences, from the first on, whose block
+    tables begin alike: [(sequences, positions), ...], the positions that lie
+    in the same cache rows, before every row of the group.  forward and
+    dense_forward then read them once a group; the results are the same.
     """
 
     def __init__(self, H, G, seqs_host, device, top_k=16, scale=None, out_dtype=torch.float32,
                  cache_starts=None, cache_tokens=None, D=128, Di=64, S=64, num_decode_seqs="auto",
                  block_table=None, page_size=0, ik_heads=0, k_scale=None, v_scale=None,
-                 num_decode_rows="auto"):
+                 num_decode_rows="auto", ik_exp=None, shared=None):
         self.H, self.G, self.D, self.Di, self.S, self.top_k = H, G, D, Di, S, top_k
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
@@ -232,6 +242,29 @@ class Problem:
             self.c.kv_dtype = MSA_KV_INT8
             self.c.k_scale = self.k_scale.data_ptr()
             self.c.v_scale = self.v_scale.data_ptr()
+        self.ik_dtype, self.ik_exp = torch.bfloat16, ik_exp
+        if ik_exp is not None:
+            _need(ik_exp, "ik_exp", torch.int8, self.device, (self.cache_tokens, self.KH))
+            self.ik_dtype, self.c.ik_dtype, self.c.ik_exp = torch.int8, MSA_IK_INT8, ik_exp.data_ptr()
+        self.shared = [] if shared is None else [(int(n), int(s)) for n, s in shared]
+        if self.shared:
+            self._set_groups(rows, lens)
+
+    def _set_groups(self, rows, lens):
+        starts, most = [0], 1
+        for count, positions in self.shared:
+            first, last = starts[-1], starts[-1] + count
+            if count < 1 or last > len(rows):
+                raise ValueError("shared must name between 1 and all of the sequences, in order")
+            if positions < 0 or any(lens[b] - rows[b] < positions for b in range(first, last)):
+                raise ValueError("the shared positions of a group must lie before every row of its sequences")
+            most = max(most, sum(rows[first:last]))
+            starts.append(last)
+        self.group_starts = torch.tensor(starts, dtype=torch.int32, device=self.device)
+        self.group_shared = torch.tensor([s for _, s in self.shared], dtype=torch.int32, device=self.device)
+        self.c.num_groups, self.c.max_group_rows = len(self.shared), most
+        self.c.max_shared_len = max(s for _, s in self.shared)
+        self.c.group_starts, self.c.group_shared = self.group_starts.data_ptr(), self.group_shared.data_ptr()
 
     @property
     def max_cache_len(self):
@@ -272,7 +305,7 @@ class Problem:
         _need(iq, "iq", torch.bfloat16, self.device, (self.total_rows, self.H, self.Di))
 
     def _check_cache(self, t, name, width, heads=None):
-        dtype = self.kv_dtype if name in ("k", "v") else torch.bfloat16
+        dtype = self.kv_dtype if name in ("k", "v") else self.ik_dtype
         _need(t, name, dtype, self.device, (self.cache_tokens, self.H if heads is None else heads, width))
 
     def _check_sel(self, sel, nsel):
@@ -427,7 +460,8 @@ def append_cache(pb: Problem, new_k, new_v, k, v, new_ik=None, ik=None, q=None, 
 
     New rows may be views of a wider projection (any row stride that is a multiple of 8).  positions: int32
     [axes, rows], or None for each row's position in its sequence.  With an int8 cache the scales go to pb.k_scale
-    and pb.v_scale, which must be the tensors that the Problem was given, not copies of them.  Returns (q, iq) rotated, each None when not given."""
+    and pb.v_scale, which must be the tensors that the Problem was given, not copies of them; with int8 index keys their
+    exponents go to pb.ik_exp.  Returns (q, iq) rotated, each None when not given."""
     R, H, D, Di, dev = pb.total_rows, pb.H, pb.D, pb.Di, pb.device
     pb._check_cache(k, "k", D)
     pb._check_cache(v, "v", D)
@@ -462,7 +496,7 @@ def append_cache(pb: Problem, new_k, new_v, k, v, new_ik=None, ik=None, q=None, 
     elif positions is not None:
         raise ValueError("positions need a rope")
     a = MsaAppend(new_k.data_ptr(), new_v.data_ptr(), ikp, qp, iqp, ks, vs, iks, qs, iqs, k.data_ptr(), v.data_ptr(), ikc,
-                  pb.c.k_scale, pb.c.v_scale, qo, iqo)
+                  pb.c.k_scale, pb.c.v_scale, pb.c.ik_exp if ikc else None, qo, iqo)
     ws = torch.empty(APPEND_WORKSPACE_BYTES, dtype=torch.uint8, device=dev) if workspace is None else workspace
     _need(ws, "workspace", torch.uint8, dev)
     with _on(dev):

@@ -1,0 +1,1017 @@
+// Attention over every cached position for decode rows and drafted windows (1 to 8 rows a sequence) of a batch in which
+// groups of sequences share a prefix: the prefix is read once for all rows of the group.
+//   out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m),  x_t = scale log2(e) q.k_t over t <= p
+// A softmax over a set of keys splits into parts (O, m, l: unnormalised sum, maximum, sum of weights) over any division
+// of the keys, joined by weights 2^(m_i - m).  Here the keys of a row are divided into
+//   the group's shared positions [0, S)     one item for up to 2 x 128 (row, head) pairs of the group and a KV head
+//   the sequence's own positions [S, L - n) one item for the sequence's (row, head) pairs and a KV head
+//   the n rows' own positions [L - n, p]    at most 8 keys, in fp32 by the kernel that joins the parts
+// so that the first two have no causal edge: every row of an item sees every key of it, and no value of a later token is
+// ever multiplied with.
+//
+// dense_shared_kernel.  An item is an M tile of 128 rows (row = neighbouring query rows x G heads; a sequence's n G rows
+// leave the others of the tile empty) or two of them, and its keys in tiles of NK:
+//   S[128, NK] = Q K^T     operands from shared memory (TMA, 128-byte swizzle), S in tensor memory
+//   P = 2^(x - m)          a thread a row, written over S (m is raised only where it would grow by more than 8)
+//   O[128, 128] += P V     P from tensor memory, V as it lies
+// Two stages of 128 columns of S and of O: two M tiles that take turns on the tensor pipe, or one M tile whose stages
+// take alternate key tiles.  One CTA per SM; all items' key tiles lie on a line, item after item, that is cut into even
+// shares (an item counts for kDsExtra tiles more, what going on to another one costs); a CTA's shares of items leave
+// their parts in the workspace.
+//
+// dense_shared_join.  A CTA takes a row and a KV head: the row's own keys, then the parts, whose places follow from the
+// same line by arithmetic (slot = item + CTA, which is different for every pair of them that meets, as both ascend along
+// the line).  Parts lie [dim / 4][row][4], so that the rows of a tile are stored and loaded in whole lines.
+//
+// Numerics.  bf16 outputs: weights as one bf16 (2^-8 at most, at random), and at most 32,768 keys to a part, as the
+// tensor cores cut what an addition loses instead of rounding it (2^-24 an addition of 16 keys).  fp32 outputs: weights
+// as three bf16 parts, NK = 64, O taken from tensor memory every second tile and summed in registers.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tensor_rows.cuh"
+
+namespace msa {
+
+constexpr int kDsThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 and 10 copies, 9 and 11 matrix instructions
+constexpr int kDsQBytes = 128 * kHeadDim * 2;
+constexpr int kDsPartKeys = 32768;  // most keys of a part
+constexpr int kDsExtra = 3;         // tiles that an item counts for besides its own
+constexpr int kDsInfo = 4;          // items published ahead
+constexpr float kDsSlack = 8.f;     // log2 by which the running maximum may lag
+
+// A CTA's share of an item.
+struct DsItem {
+    int b;             // sequence whose table is read; < 0: no more items
+    int row, rows;     // first query row of the item, query rows of its entry from there on
+    int h, key, end;   // KV head; first key of the share; end of the entry's keys
+    int tiles, pair;   // key tiles; two M tiles (or one, the stages on alternate key tiles)
+    int cap;           // rows of a stage's part
+    int64_t part;      // first row of its parts in the workspace
+};
+
+template <int kParts>
+struct DsCfg {
+    static constexpr int NK = kParts == 1 ? 128 : 64;
+    static constexpr int kTile = NK * kHeadDim * 2;  // bytes of a K or V tile
+    static constexpr int kStages = 5 * (128 / NK);
+    static constexpr int kSAt = kParts == 1 ? 0 : 64;  // column of S in its 128 (as in the prompt kernel: P's parts from 0 on)
+    static constexpr int kRun = kDsPartKeys / NK;      // most tiles of a part
+};
+
+template <int kParts>
+struct __align__(1024) DsSmem {
+    using Cfg = DsCfg<kParts>;
+    uint8_t q[2][kDsQBytes];
+    uint8_t ring[Cfg::kStages][Cfg::kTile];
+    // Copies landed: of pairs [0], of the two stages on alternate tiles [1], [2], each counted by itself, so that an issuer
+    // sees all phases of the barriers that it waits for.
+    uint64_t full[3][Cfg::kStages], empty[Cfg::kStages];
+    uint64_t v_last[Cfg::kStages];  // a last value tile has landed, before its tail is zeroed (by ring slot: a copier may be items ahead)
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
+    uint64_t info_full[kDsInfo], info_empty[kDsInfo], item_done;
+    DsItem info[kDsInfo];
+    uint32_t tmem, err;
+    int64_t scan_line[kDsThreads / 32];
+    int32_t scan_items[kDsThreads / 32];
+};
+static_assert(sizeof(DsSmem<1>) + 1024 <= 227 * 1024, "shared-prefix attention exceeds 227 KB of shared memory");
+static_assert(sizeof(DsSmem<3>) + 1024 <= 227 * 1024, "shared-prefix attention (fp32) exceeds 227 KB of shared memory");
+
+// Entries of the line: the groups, then the sequences.  The query rows [row, row + rows) see all keys [key, end).
+struct DsEntry {
+    int b, row, rows, key, end;
+};
+
+// The shared positions of group g in whole blocks (0 where its metadata is bad), its sequences and rows.
+__device__ __forceinline__ int ds_group(const SharedArgs& a, int g, DsEntry& x, int& last, bool& bad) {
+    const int b0 = a.group_starts[g], b1 = a.group_starts[g + 1], S = a.group_shared[g];
+    bad = b0 < 0 || b1 < b0 || b1 > a.num_seqs || S < 0 || S > a.max_shared_len;
+    if (bad) return 0;
+    const int c0 = a.cu_rows[b0], c1 = a.cu_rows[b1];
+    bad = c0 < 0 || c1 < c0 || c1 > a.total_rows || c1 - c0 > a.max_group_rows;
+    if (bad) return 0;
+    x = DsEntry{b0, c0, c1 - c0, 0, S & ~(kBlock - 1)};
+    last = b1;
+    return x.end;
+}
+
+// The shared positions of sequence b, in whole blocks, and its group (-1: none).
+__device__ __forceinline__ int ds_shared_of(const SharedArgs& a, int b, int& g) {
+    int lo = 0, hi = a.num_groups;  // largest group that begins at or before b
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_starts[mid] <= b) lo = mid; else hi = mid;
+    }
+    g = -1;
+    DsEntry x;
+    int last;
+    bool bad;
+    const int S = ds_group(a, lo, x, last, bad);
+    if (bad || b < x.b || b >= last || S == 0) return 0;
+    g = lo;
+    return S;
+}
+
+// Sequence b; rows = 0: it has none, or its metadata is bad.
+__device__ __forceinline__ DsEntry ds_seq(const SharedArgs& a, int b, int& g, bool& bad) {
+    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0, L = a.cache_lens[b];
+    const int S = ds_shared_of(a, b, g);
+    bad = n < 0 || n > min(a.max_rows_per_seq, kDecodeMaxRows) || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
+          L - n < S;
+    if (n == 0) bad = false;
+    if (bad || n == 0) return DsEntry{b, 0, 0, 0, 0};
+    return DsEntry{b, c0, n, S, L - n};
+}
+
+// How an entry lies on the line: `units` items a head (of up to two M tiles), each `chunks` parts of up to `run` tiles.
+struct DsSize {
+    int tiles, chunks, units, unit;  // key tiles; parts they make; items a head; an item's length on the line
+};
+__device__ __forceinline__ DsSize ds_size(const SharedArgs& a, const DsEntry& x, int NK) {
+    DsSize s{};
+    if (x.rows == 0 || x.end <= x.key) return s;
+    const int run = kDsPartKeys / NK, P = 128 / a.G, mt = (x.rows + P - 1) / P;
+    s.tiles = (x.end - x.key + NK - 1) / NK;
+    s.chunks = (s.tiles + run - 1) / run;
+    s.units = (mt + 1) / 2;
+    s.unit = s.tiles + s.chunks * kDsExtra;
+    return s;
+}
+__device__ __forceinline__ DsEntry ds_entry(const SharedArgs& a, int e, bool& bad) {
+    if (e >= a.num_groups) {
+        int g;
+        return ds_seq(a, e - a.num_groups, g, bad);
+    }
+    DsEntry x{};
+    int last;
+    ds_group(a, e, x, last, bad);
+    return x;
+}
+
+// CTAs that share a line, and where share c begins (the largest c whose share begins at or before a place: ds_owner).
+__host__ __device__ __forceinline__ int ds_shares(int64_t line, int grid) {
+    const int64_t n = line / (kDsExtra + 2);
+    return static_cast<int>(n < 1 ? 1 : (n < grid ? n : grid));
+}
+__device__ __forceinline__ int64_t ds_cut(int64_t line, int c, int shares) { return line * c / shares; }
+__device__ __forceinline__ int ds_owner(int64_t line, int64_t at, int shares) {
+    return static_cast<int>(((at + 1) * shares - 1) / line);
+}
+
+template <int kParts>
+__global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                    const __grid_constant__ CUtensorMap k_map,
+                                                                    const __grid_constant__ CUtensorMap v_map,
+                                                                    const SharedArgs a) {
+    using Cfg = DsCfg<kParts>;
+    using Smem = DsSmem<kParts>;
+    constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2, kSAt = Cfg::kSAt, kRun = Cfg::kRun;
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.err); };
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            for (int k = 0; k < 3; ++k) mbar_init(&sm.full[k][s], 2);  // two warps copy a half each
+            mbar_init(&sm.empty[s], 2);                                // both issuers (alternate tiles: one, and the copier for the other)
+            mbar_init(&sm.v_last[s], 2);
+        }
+        for (int s = 0; s < kDsInfo; ++s) {
+            mbar_init(&sm.info_full[s], 1);
+            mbar_init(&sm.info_empty[s], 11);  // a copier, two issuers, eight softmax warps
+        }
+        mbar_init(&sm.item_done, 2);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.q_full[s], 1);
+            mbar_init(&sm.q_empty[s], 2);
+            mbar_init(&sm.s_full[s], 1);
+            mbar_init(&sm.p_full[s][0], 4);
+            mbar_init(&sm.p_full[s][1], 4);
+            mbar_init(&sm.o_full[s], 1);
+            mbar_init(&sm.turn[s], 1);
+            mbar_init(&sm.drain[s], 1);
+        }
+        sm.err = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &q_map : (lane == 1 ? &k_map : &v_map));
+    if (warp == 9) tmem_alloc(&sm.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t tmem = sm.tmem;
+    // ---- places of the entries on the line, and parts before each (a block-wide scan; every CTA stores the same)
+    const int entries = a.num_groups + a.num_seqs;
+    int64_t line = 0;
+    int parts = 0;
+    for (int base = 0; base < entries; base += kDsThreads) {
+        const int e = base + tid;
+        int64_t mine = 0;
+        int items = 0;
+        if (e < entries) {
+            bool bad;
+            const DsEntry x = ds_entry(a, e, bad);
+            const DsSize s = ds_size(a, x, NK);
+            mine = static_cast<int64_t>(a.H) * s.units * s.unit;
+            items = a.H * s.units * s.chunks;
+            if (blockIdx.x == 0) {
+                if (e >= a.num_groups && x.rows > 0)  // the rows' own positions, which the join reads
+                    bad |= block_row(a.cache, x.b, x.end & ~(kBlock - 1)) < 0 ||
+                           block_row(a.cache, x.b, (x.end + x.rows - 1) & ~(kBlock - 1)) < 0;
+                if (bad) atomicOr(&sm.err, kErrBadMetadata);
+            }
+        }
+        int64_t incl = mine;
+        int incl_items = items;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, static_cast<long long>(incl), o);
+            const int w = __shfl_up_sync(0xffffffffu, incl_items, o);
+            if (lane >= o) {
+                incl += v;
+                incl_items += w;
+            }
+        }
+        if (lane == 31) {
+            sm.scan_line[warp] = incl;
+            sm.scan_items[warp] = incl_items;
+        }
+        __syncthreads();
+        int64_t before = line;
+        int before_items = parts;
+        for (int w = 0; w < kDsThreads / 32; ++w) {
+            if (w < warp) {
+                before += sm.scan_line[w];
+                before_items += sm.scan_items[w];
+            }
+            line += sm.scan_line[w];
+            parts += sm.scan_items[w];
+        }
+        if (e < entries) {
+            a.line[e] = before + incl - mine;
+            a.items[e] = before_items + incl_items - items;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        a.line[entries] = line;
+        a.items[entries] = parts;
+    }
+    __syncthreads();
+    const int group_parts = a.items[a.num_groups];
+    if (group_parts > a.group_parts_most || parts - group_parts > a.seq_parts_most) {  // more than the host's bounds allow for
+        if (tid == 0) atomicOr(&sm.err, kErrBadMetadata);
+        line = 0;
+    }
+    const int shares = ds_shares(line, gridDim.x);
+    const bool idle = line == 0 || static_cast<int>(blockIdx.x) >= shares;
+    const int P = 128 / a.G;
+
+    auto next_item = [&](int k, DsItem& x) {  // item k of the CTA, false where it never came
+        if (!wait(&sm.info_full[k % kDsInfo], (k / kDsInfo) & 1)) return false;
+        x = sm.info[k % kDsInfo];
+        return true;
+    };
+    auto passed = [&](int k) { mbar_arrive(&sm.info_empty[k % kDsInfo]); };
+    auto count_of = [](const DsItem& x, int s) { return x.pair ? x.tiles : (x.tiles + 1 - s) / 2; };  // key tiles of stage s
+
+    if (idle) {
+        // nothing to do
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8 || warp == 10) {
+            // ---------------- copies: K and V tiles, dimensions 0-63 by warp 8 (and the queries), 64-127 by warp 10 (which
+            // also finds the items, and clears the end of a last value tile)
+            const int half = warp == 10;
+            int slot = 0, sent[3] = {0, 0, 0}, q_used[2] = {0, 0};  // copies in all and by barrier row; items by query buffer
+            uint32_t fixed = 0;  // last value tiles, a bit a ring slot: how often modulo 2
+            bool alive = true;
+            // the CTA's walk along the line
+            int64_t at = ds_cut(line, blockIdx.x, shares);
+            const int64_t stop = ds_cut(line, blockIdx.x + 1, shares);
+            int e = 0;
+            DsEntry x{};
+            DsSize sz{};
+            int64_t e_line = 0, e_next = -1;
+            if (half) {
+                int lo = 0, hi = entries;  // the last entry that begins at or before it
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (a.line[mid] <= at) lo = mid; else hi = mid;
+                }
+                e = lo - 1;
+            }
+            auto find = [&]() {
+                DsItem it{};
+                it.b = -1;
+                while (at < stop) {
+                    while (at >= e_next) {
+                        ++e;
+                        e_line = a.line[e];
+                        e_next = a.line[e + 1];
+                        if (at < e_next) {
+                            bool bad;
+                            x = ds_entry(a, e, bad);
+                            sz = ds_size(a, x, NK);
+                        }
+                    }
+                    const int off = static_cast<int>(at - e_line), uh = off / sz.unit, o = off - uh * sz.unit;
+                    const int h = uh / sz.units, u = uh - h * sz.units;
+                    const int ch = min(o / (kRun + kDsExtra), sz.chunks - 1), oc = o - ch * (kRun + kDsExtra);
+                    const int tiles = min(kRun, sz.tiles - ch * kRun);
+                    const int64_t begin = at - oc, end = begin + kDsExtra + tiles;
+                    const int64_t upto = min(end, stop);
+                    const int t0 = max(0, oc - kDsExtra), t1 = static_cast<int>(upto - begin) - kDsExtra;
+                    at = upto;
+                    if (t1 <= t0) continue;
+                    const bool group = e < a.num_groups;
+                    it.b = x.b;
+                    it.row = x.row + u * 2 * P;
+                    it.rows = x.rows - u * 2 * P;
+                    it.h = h;
+                    it.key = x.key + (ch * kRun + t0) * NK;
+                    it.end = x.end;
+                    it.tiles = t1 - t0;
+                    it.pair = it.rows > P;
+                    it.cap = group ? a.group_rows : a.seq_rows;
+                    const int64_t place = a.items[e] + uh * sz.chunks + ch + static_cast<int>(blockIdx.x);
+                    it.part = group ? place * 2 * a.group_rows : a.seq_part0 + (place - group_parts) * 2 * a.seq_rows;
+                    break;
+                }
+                return it;
+            };
+            auto publish = [&](int n, const DsItem& item) {
+                int ok = 1;
+                if (lane == 0) {
+                    if (n >= kDsInfo) ok = wait(&sm.info_empty[n % kDsInfo], ((n / kDsInfo) - 1) & 1);
+                    if (ok) {
+                        sm.info[n % kDsInfo] = item;
+                        mbar_arrive(&sm.info_full[n % kDsInfo]);
+                    }
+                }
+                return __shfl_sync(0xffffffffu, ok, 0) != 0;
+            };
+            DsItem item, after;
+            if (half) {
+                after = find();
+                alive = publish(0, after);
+            }
+            for (int k = 0; alive; ++k) {
+                if (half) {
+                    item = after;
+                    if (item.b < 0) break;
+                    after = find();  // (ahead of this item's copies)
+                    alive = publish(k + 1, after);
+                    if (!alive) break;
+                } else {
+                    alive = __all_sync(0xffffffffu, next_item(k, item));
+                    if (!alive) break;
+                    __syncwarp();
+                    if (lane == 0) passed(k);
+                    if (item.b < 0) break;
+                    int ok = 1;
+                    if (lane == 0) {
+                        for (int s = 0; s < (item.pair ? 2 : 1); ++s) {
+                            const int buf = item.pair ? s : k & 1, used = buf ? q_used[1] : q_used[0];
+                            if (used > 0) ok = ok && wait(&sm.q_empty[buf], (used - 1) & 1);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(&sm.q_full[buf], 2 * P * a.G * 128);
+                            for (int c = 0; c < 2; ++c)
+                                tma_load_3d(sm.q[buf] + c * (kDsQBytes / 2), &q_map, &sm.q_full[buf], 64 * c, item.h * a.G, item.row + s * P);
+                            if (buf) ++q_used[1];
+                            else ++q_used[0];
+                        }
+                    }
+                    alive = __shfl_sync(0xffffffffu, ok, 0) != 0;
+                }
+                // the value tile that holds the end of the keys, if its last block is not wholly theirs
+                const int fix = item.end % kBlock != 0 && item.key + item.tiles * NK >= item.end ? item.tiles - 1 : -1;
+                constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
+                int64_t row = 0;
+                int fix_slot = 0, fix_row = 0, fix_copy = 0;
+                for (int j = 0; alive && j < item.tiles; ++j) {
+                    if (j % kBatch == 0) {
+                        const int t = item.key + j * NK + lane * kBlock;
+                        row = a.cache_tokens;  // past the end: a box past the cache is zeros
+                        if (lane < NK / kBlock * (item.tiles - j) && t < item.end) {
+                            row = block_row(a.cache, item.b, t);
+                            if (row < 0) {  // page outside the pool
+                                atomicOr(&sm.err, kErrBadMetadata);
+                                row = a.cache_tokens;
+                            }
+                        }
+                    }
+                    const int set = item.pair ? 0 : 1 + (j & 1);
+#pragma unroll
+                    for (int kind = 0; kind < 2; ++kind) {  // K, V
+                        const int st = slot % kStages, copy = set == 0 ? sent[0] : (set == 1 ? sent[1] : sent[2]);
+                        int64_t r[NK / kBlock];
+#pragma unroll
+                        for (int c = 0; c < NK / kBlock; ++c) r[c] = __shfl_sync(0xffffffffu, row, (j % kBatch) * (NK / kBlock) + c);
+                        int ok = 1;
+                        if (lane == 0) {
+                            uint64_t* bar = kind == 1 && j == fix ? &sm.v_last[st] : &sm.full[set][copy % kStages];
+                            if (slot >= kStages) ok = wait(&sm.empty[st], ((slot / kStages) - 1) & 1);
+                            if (ok) {
+                                if (set > 0 && !half) mbar_arrive(&sm.empty[st]);  // (for the stage that does not take the tile)
+                                mbar_arrive_expect_tx(bar, Cfg::kTile / 2);
+#pragma unroll
+                                for (int c = 0; c < NK / kBlock; ++c)
+                                    tma_load_3d(sm.ring[st] + half * kHalf + c * (kBlock * 128), kind == 0 ? &k_map : &v_map, bar, 64 * half,
+                                                item.h, static_cast<int>(r[c]));
+                            }
+                        }
+                        fix_slot = st;
+                        fix_row = set;
+                        fix_copy = copy;
+                        ++slot;
+                        if (set == 0) ++sent[0];
+                        else if (set == 1) ++sent[1];
+                        else ++sent[2];
+                        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+                            alive = false;
+                            break;
+                        }
+                    }
+                }
+                if (half && fix >= 0 && alive) {  // ---- values past the end become zero (they may be anything; the last copy is theirs)
+                    alive = __all_sync(0xffffffffu, wait(&sm.v_last[fix_slot], fixed >> fix_slot & 1));
+                    if (!alive) break;
+                    fixed ^= 1u << fix_slot;
+                    for (int y = (item.end - item.key - fix * NK) * 16 + lane; y < NK * 16; y += 32) {
+                        const int key = y >> 4, c = y & 15;  // (a whole row: no swizzle to undo)
+                        *reinterpret_cast<uint4*>(sm.ring[fix_slot] + (c >> 3) * kHalf + key * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        uint64_t* bar = &sm.full[fix_row][fix_copy % kStages];
+                        mbar_arrive(bar);
+                        mbar_arrive(bar);
+                    }
+                }
+            }
+            if (lane == 0 && !half) {  // no copy in flight at the end (a last value tile's barrier was warp 10's to wait for)
+                for (int s = 0; s < 2; ++s) {
+                    const int used = s ? q_used[1] : q_used[0];
+                    if (used > 0) wait(&sm.q_full[s], (used - 1) & 1);
+                }
+#pragma unroll
+                for (int s = 0; s < 3; ++s)
+                    for (int b = 0; b < kStages && b < sent[s]; ++b) wait(&sm.full[s][b], ((sent[s] - 1 - b) / kStages) & 1);
+            }
+        } else {
+            // ---------------- matrix instructions of stage s, one thread
+            const int s = warp == 9 ? 0 : 1;
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(128, NK, 0, 0), idesc_o = idesc_bf16_f32(128, kHeadDim, 0, 1);
+                const uint64_t qd0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024), qd1 = smem_desc_sw128(smem_u32(sm.q[1]), 16, 1024);
+                const uint64_t kd = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
+                const uint64_t vd = smem_desc_sw128(smem_u32(sm.ring[0]), kHalf, 1024);
+                // running: ring slots, the stage's tiles, turns taken, copies seen of pairs and of alternate tiles, query buffers
+                int slots = 0, tiles = 0, turns = 0, seen[2] = {0, 0}, q_used[2] = {0, 0};
+                bool ok = true, issued = false;
+                for (int k = 0; ok; ++k) {
+                    DsItem item;
+                    ok = next_item(k, item);
+                    if (!ok) break;
+                    passed(k);
+                    if (item.b < 0) break;
+                    const int count = count_of(item, s), step = item.pair ? 1 : 2, j0 = item.pair ? 0 : s;
+                    const bool pair = item.pair;
+                    const int row = pair ? 0 : 1 + s;
+                    auto landed = [&]() {  // the stage's next copy
+                        int& n = pair ? seen[0] : seen[1];
+                        const bool r = wait(&sm.full[row][n % kStages], (n / kStages) & 1);
+                        ++n;
+                        return r;
+                    };
+                    auto at = [&](int j, int kind) { return (slots + 2 * j + kind) % kStages; };
+                    const int b0 = pair ? 0 : k & 1, b1 = pair ? 1 : k & 1;  // query buffers of the item
+                    const uint64_t qd = (pair ? s : k & 1) ? qd1 : qd0;
+                    auto free_q = [&](bool products) {
+                        for (int b = b0; b <= b1; ++b) {
+                            if (products) tc_commit(&sm.q_empty[b]);
+                            else mbar_arrive(&sm.q_empty[b]);
+                        }
+                    };
+                    for (int b = b0; b <= b1 && ok; ++b) {
+                        int& n = b ? q_used[1] : q_used[0];
+                        ok = wait(&sm.q_full[b], n & 1);
+                        ++n;
+                    }
+                    if (!ok) break;
+                    // S_s = Q K^T from ring slot st; `pass`: the other stage's turn begins while the last of them run
+                    auto scores = [&](int st, bool last, bool pass) {
+                        const uint64_t kb = kd + static_cast<uint64_t>(st * (Cfg::kTile >> 4));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            tc_mma_ss(tmem + s * 128 + kSAt, qd + static_cast<uint64_t>(((i >> 2) * (kDsQBytes / 2) + (i & 3) * 32) >> 4),
+                                      kb + static_cast<uint64_t>(((i >> 2) * kHalf + (i & 3) * 32) >> 4), idesc_s, i > 0);
+                            if (i == 5 && pass) mbar_arrive(&sm.turn[s ^ 1]);
+                        }
+                        tc_commit(&sm.s_full[s]);
+                        if (last) free_q(true);  // the last products with this item's queries
+                        tc_commit(&sm.empty[st]);
+                    };
+                    if (count > 0) {
+                        ok = landed();
+                        if (!ok) break;
+                        issued = true;
+                        tc_fence_after();
+                        scores(at(j0, 0), count == 1, false);
+                    } else {
+                        free_q(false);
+                    }
+                    // the other stage is through with its last item: its turns have been taken
+                    if (k > 0) ok = wait(&sm.item_done, (k - 1) & 1);
+                    for (int c = 0; ok && c < count; ++c) {
+                        // pairs take turns: values of tile c, scores of the next (whatever can be waited for is, first)
+                        const int j = j0 + step * c;
+                        const uint32_t phase = (tiles + c) & 1;
+                        const bool next = c + 1 < count, pass = pair && (s == 0 || next);
+                        ok = landed();
+                        const int st_v = at(j, 1), st_k = at(j + step, 0);
+                        if (pair && next) ok = ok && landed();
+                        const uint64_t vb = vd + static_cast<uint64_t>(st_v * (Cfg::kTile >> 4));
+                        ok = ok && wait(&sm.p_full[s][0], phase);
+                        if (ok && pair && (s == 1 || c > 0)) ok = wait(&sm.turn[s], turns++ & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int h2 = 0; h2 < NK / 64; ++h2) {  // O_s += P_s V, the second 64 keys as soon as their weights are there
+                            if (h2 == 1) {
+                                ok = wait(&sm.p_full[s][1], phase);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+#pragma unroll
+                            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                                for (int i = 4 * h2; i < 4 * h2 + 4; ++i)
+                                    dp_mma_ts(tmem + 256 + s * 128, tmem + s * 128 + part * (NK / 2) + i * 8,
+                                              vb + static_cast<uint64_t>(i * 2048 >> 4), idesc_o,
+                                              !((kParts > 1 ? c % 2 == 0 : c == 0) && part == 0 && i == 0));
+                        }
+                        if (!ok) break;
+                        if (!pair && next) {  // the values' slot back before the next keys are waited for
+                            tc_commit(&sm.empty[st_v]);
+                            ok = landed();
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        if (next) {
+                            scores(st_k, c + 2 == count, pass);
+                        } else {
+                            if (pass) mbar_arrive(&sm.turn[s ^ 1]);
+                            tc_commit(&sm.o_full[s]);
+                        }
+                        if (pair || !next) tc_commit(&sm.empty[st_v]);
+                    }
+                    slots += 2 * item.tiles;
+                    tiles += count;
+                    if (ok) mbar_arrive(&sm.item_done);
+                }
+                if (issued) {  // every matrix instruction done before tensor memory is given back
+                    tc_commit(&sm.drain[s]);
+                    wait(&sm.drain[s], 0);
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        // 168 x 384 registers at launch: 208 x 256 + 88 x 128
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // ---------------- softmax group s: thread = row of its M tile
+        const int s = warp >> 2, m = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 (warp % 4)) << 16
+        const uint32_t s_addr = tmem + s * 128 + lanes, o_addr = tmem + 256 + s * 128 + lanes;
+        int tiles = 0, done = 0;  // running: the stage's tiles, items it had tiles of
+        bool alive = true;
+        for (int k = 0; alive; ++k) {
+            DsItem item;
+            alive = __all_sync(0xffffffffu, next_item(k, item));
+            if (!alive) break;
+            __syncwarp();
+            if (lane == 0) passed(k);
+            if (item.b < 0) break;
+            const int count = count_of(item, s);
+            const int rows = min(item.rows - (item.pair ? s * P : 0), P) * a.G;  // of the M tile
+            const bool mine = m < rows, busy = (m & ~31) < rows;                 // busy: some row of the warp is
+            float top = -INFINITY, sum = 0.f;         // maximum in use (log2 domain), sum of weights
+            float acc[kParts > 1 ? kHeadDim : 1];     // fp32 outputs: O of the row
+            if constexpr (kParts > 1) {
+#pragma unroll
+                for (int d = 0; d < kHeadDim; ++d) acc[d] = 0.f;
+            }
+            auto rescale = [&](float r) {  // O in tensor memory times r
+#pragma unroll 1
+                for (int q = 0; q < kHeadDim / 32; ++q) {
+                    float y[32];
+                    dp_ld32(o_addr + 32 * q, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int d = 0; d < 32; ++d) y[d] *= r;
+                    dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(y));
+                }
+            };
+            auto collect = [&]() {  // adds the last two tiles' product to it
+                if constexpr (kParts > 1) {
+#pragma unroll
+                    for (int q = 0; q < kHeadDim / 16; ++q) {
+                        uint32_t y[16];
+                        tmem_ld16(o_addr + 16 * q, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int d = 0; d < 16; ++d) acc[16 * q + d] += __uint_as_float(y[d]);
+                    }
+                }
+            };
+            for (int c = 0; alive && c < count; ++c) {
+                const int t0 = item.key + (item.pair ? c : 2 * c + s) * NK;
+                alive = __all_sync(0xffffffffu, wait(&sm.s_full[s], (tiles + c) & 1));
+                if (!alive) break;
+                if (!busy) {  // (the tile's other warps have rows)
+                    if (lane == 0) {
+                        mbar_arrive(&sm.p_full[s][0]);
+                        if constexpr (NK == 128) mbar_arrive(&sm.p_full[s][1]);
+                    }
+                    continue;
+                }
+                tc_fence_after();
+                if (kParts > 1 && c > 0 && c % 2 == 0) collect();
+                const bool edge = t0 + NK > item.end;
+                const int seen = item.end - t0;  // keys of the tile
+                auto raise = [&](float now) {  // the maximum in use is now's or within kDsSlack of it
+                    if (c == 0) {
+                        top = now;
+                    } else if (__any_sync(0xffffffffu, now > top + kDsSlack)) {
+                        // the warp's rows of O move to the new maximum (no product runs on it now: S of this tile was computed
+                        // after the last one), and their sums
+                        const float next = now > top + kDsSlack ? now : top;
+                        const float r = top == -INFINITY ? (next == -INFINITY ? 1.f : 0.f) : dp_exp2(top - next);
+                        if constexpr (kParts > 1) {
+#pragma unroll
+                            for (int d = 0; d < kHeadDim; ++d) acc[d] *= r;
+                            if (c & 1) rescale(r);
+                        } else {
+                            rescale(r);
+                        }
+                        sum *= r;
+                        top = next;
+                    }
+                };
+                if constexpr (kParts > 1) {  // ---- 32 scores at a time, O in registers
+                    float now = -INFINITY;
+                    auto scores_of = [&](int q, float (&x)[32]) {
+                        dp_ld32(s_addr + kSAt + 32 * q, x);
+                        tmem_ld_wait();
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = 32 * q + i < seen ? x[i] * a.scale_log2 : -INFINITY;
+                        }
+                    };
+                    const float f = edge ? 1.f : a.scale_log2;  // what is left to multiply by
+                    if (edge) {
+#pragma unroll 1
+                        for (int q = 0; q < 2; ++q) {
+                            float x[32];
+                            scores_of(q, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) now = fmaxf(now, x[i]);
+                        }
+                    } else {
+                        tmem_ld_max64(s_addr + kSAt, now);
+                        tmem_ld_wait();
+                        now *= f;
+                    }
+                    raise(now);
+                    const float base = top == -INFINITY ? 0.f : top;
+                    const float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+                    float2 add = make_float2(0.f, 0.f);
+#pragma unroll 1
+                    for (int q = 0; q < 2; ++q) {
+                        float x[32];
+                        scores_of(q, x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), ff, nb);
+                            x[2 * i] = dp_exp2(y.x);
+                            x[2 * i + 1] = dp_exp2(y.y);
+                            add = __fadd2_rn(add, make_float2(x[2 * i], x[2 * i + 1]));
+                        }
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                pk[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                                if (part + 1 < kParts) {
+                                    x[2 * i] -= bf16_lo(pk[i]);
+                                    x[2 * i + 1] -= bf16_hi(pk[i]);
+                                }
+                            }
+                            dp_st16(s_addr + part * 32 + 16 * q, pk);
+                        }
+                    }
+                    sum += add.x + add.y;
+                    dp_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[s][0]);
+                } else {
+                    float x[NK], big[NK / 64];
+#pragma unroll
+                    for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
+                    float f = a.scale_log2;
+                    tmem_ld_wait();
+                    float now;
+                    if (edge) {  // keys past the end; the scores are then not those that the load took the maximum of
+#pragma unroll
+                        for (int i = 0; i < NK; ++i) x[i] = i < seen ? x[i] * f : -INFINITY;
+                        f = 1.f;
+                        float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < NK; i += 4)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], x[i + z]);
+                        now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                    } else {
+                        now = fmaxf(big[0], big[NK / 64 - 1]) * f;
+                    }
+                    raise(now);
+                    const float base = top == -INFINITY ? 0.f : top;
+                    const float2 ff = make_float2(f, f), nb = make_float2(-base, -base);
+                    float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int h2 = 0; h2 < NK / 64; ++h2) {  // 64 keys at a time: the products with them start while the next are made
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float* z = x + 64 * h2 + 32 * q;
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 y = __ffma2_rn(make_float2(z[2 * i], z[2 * i + 1]), ff, nb);
+                                z[2 * i] = dp_exp2(y.x);
+                                z[2 * i + 1] = dp_exp2(y.y);
+                                add[i & 1] = __fadd2_rn(add[i & 1], make_float2(z[2 * i], z[2 * i + 1]));
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(z[2 * i], z[2 * i + 1]);
+                            dp_st16(s_addr + 32 * h2 + 16 * q, pk);
+                        }
+                        dp_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.p_full[s][h2]);
+                    }
+                    sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
+                }
+            }
+            if (alive && count > 0) alive = __all_sync(0xffffffffu, wait(&sm.o_full[s], done++ & 1));
+            tiles += count;
+            if (!alive) break;
+            if (!busy) continue;
+            // ---------------- the part: O, maximum, sum
+            tc_fence_after();
+            const int64_t row0 = item.part + s * item.cap;
+            float4* dst = reinterpret_cast<float4*>(a.part_o) + row0 * (kHeadDim / 4) + m;
+            if (count > 0) {
+                collect();
+#pragma unroll(kParts > 1 ? 4 : 1)
+                for (int q = 0; q < kHeadDim / 32; ++q) {
+                    float y[32];
+                    if constexpr (kParts > 1) {
+#pragma unroll
+                        for (int d = 0; d < 32; ++d) y[d] = acc[32 * q + d];
+                    } else {
+                        dp_ld32(o_addr + 32 * q, y);
+                        tmem_ld_wait();
+                    }
+                    if (mine) {
+#pragma unroll
+                        for (int d = 0; d < 8; ++d)
+                            dst[static_cast<int64_t>(8 * q + d) * item.cap] = make_float4(y[4 * d], y[4 * d + 1], y[4 * d + 2], y[4 * d + 3]);
+                    }
+                    __syncwarp();  // the next load is the whole warp's
+                }
+            }
+            tc_fence_before();
+            if (mine) *reinterpret_cast<float2*>(a.part_ml + (row0 + m) * 2) = make_float2(count > 0 ? top : -INFINITY, count > 0 ? sum : 0.f);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0) a.err_slots[blockIdx.x] = sm.err;
+}
+
+// Joins the parts of a row's pairs of KV head h with the row's own keys.  CTA (row, h, z): quarter, half or all of the 128
+// dimensions, a thread 4 of them of one query head.
+template <bool kInt8>
+__global__ void __launch_bounds__(512) dense_shared_join(const SharedArgs a, int grid, int NK) {
+    __shared__ float own[kMaxGroup][kDecodeMaxRows];  // scores of the row's own keys (log2 domain)
+    __shared__ int64_t own_row[kDecodeMaxRows];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, h = blockIdx.y, r = blockIdx.x;
+    // ---- the row's sequence: the last that begins at or before it, 32 candidates at a time
+    int lo = 0, hi = a.num_seqs;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.cu_rows[at] <= r);
+        const int last = le ? 31 - __clz(le) : 0;
+        lo += last * step;
+        hi = min(lo + step, hi);
+    }
+    int g;
+    bool bad;
+    const DsEntry x = ds_seq(a, lo, g, bad);
+    bool there = x.rows > 0 && r >= x.row && r < x.row + x.rows;
+    const int keys = there ? r - x.row + 1 : 0;  // its own: x.end .. x.end + keys - 1
+    if (tid < kDecodeMaxRows) {
+        int64_t row = 0;
+        if (tid < keys) {
+            const int t = x.end + tid;
+            row = block_row(a.cache, x.b, t & ~(kBlock - 1));
+            if (row >= 0) row = (row + (t & (kBlock - 1))) * a.H + h;
+        }
+        own_row[tid] = row;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (r == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the CTAs found wrong
+        uint32_t e = 0;
+        for (int c = lane; c < grid; c += 32) e |= a.err_slots[c];
+        e = __reduce_or_sync(0xffffffffu, e);
+        if (lane == 0) *a.err = e;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kDecodeMaxRows; ++i) there &= own_row[i] >= 0;
+    if (!there) return;
+    const int entries = a.num_groups + a.num_seqs, group_parts = a.items[a.num_groups];
+    const int64_t line = a.line[entries];
+    if (group_parts > a.group_parts_most || a.items[entries] - group_parts > a.seq_parts_most) return;
+    const int64_t q_row = (static_cast<int64_t>(r) * a.H + h) * a.G;
+    for (int i = warp; i < a.G * keys; i += warps) {
+        const int gh = i / keys, key = i - gh * keys;
+        const uint2 qw = *reinterpret_cast<const uint2*>(a.q + (q_row + gh) * kHeadDim + 4 * lane);
+        float k[4], f = a.scale_log2;
+        if constexpr (kInt8) {
+            const char4 w = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.k) + own_row[key] * kHeadDim + 4 * lane);
+            k[0] = w.x, k[1] = w.y, k[2] = w.z, k[3] = w.w;
+            f *= a.k_scale[own_row[key]];
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.k) + own_row[key] * kHeadDim + 4 * lane);
+            k[0] = bf16_lo(w.x), k[1] = bf16_hi(w.x), k[2] = bf16_lo(w.y), k[3] = bf16_hi(w.y);
+        }
+        float y = fmaf(bf16_lo(qw.x), k[0], fmaf(bf16_hi(qw.x), k[1], fmaf(bf16_lo(qw.y), k[2], bf16_hi(qw.y) * k[3])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (lane == 0) own[gh][key] = y * f;
+    }
+    __syncthreads();
+    const int d4s = kHeadDim / 4 / gridDim.z, gh = tid % a.G, d4 = tid / a.G + blockIdx.z * d4s;
+    if (tid >= a.G * d4s) return;
+    float top = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < keys; ++i) top = fmaxf(top, own[gh][i]);
+    for (int i = 0; i < keys; ++i) {
+        const float y = own[gh][i], w = top == -INFINITY ? (y == y ? 0.f : y) : dp_exp2(y - top);
+        float v[4];
+        if constexpr (kInt8) {
+            const char4 c = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.v) + own_row[i] * kHeadDim + 4 * d4);
+            const float f = a.v_scale[own_row[i]];
+            v[0] = c.x * f, v[1] = c.y * f, v[2] = c.z * f, v[3] = c.w * f;
+        } else {
+            const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + own_row[i] * kHeadDim + 4 * d4);
+            v[0] = bf16_lo(c.x), v[1] = bf16_hi(c.x), v[2] = bf16_lo(c.y), v[3] = bf16_hi(c.y);
+        }
+        sum += w;
+        o.x = fmaf(w, v[0], o.x);
+        o.y = fmaf(w, v[1], o.y);
+        o.z = fmaf(w, v[2], o.z);
+        o.w = fmaf(w, v[3], o.w);
+    }
+    // ---- parts of entry e, eight at a time
+    const int shares = ds_shares(line, grid), P = 128 / a.G;
+    auto join = [&](int e, const DsEntry& y, bool group) {
+        const DsSize s = ds_size(a, y, NK);
+        if (s.units == 0) return;
+        const int run = kDsPartKeys / NK, i = r - y.row, tile = i / P, u = tile / 2, uh = h * s.units + u;
+        const bool pair = y.rows - u * 2 * P > P;
+        const int cap = group ? a.group_rows : a.seq_rows, m = (i - tile * P) * a.G + gh;
+        const int stages = pair ? 1 : 2, s0 = pair ? tile & 1 : 0;
+        for (int ch = 0; ch < s.chunks; ++ch) {
+            const int64_t begin = a.line[e] + static_cast<int64_t>(uh) * s.unit + ch * (run + kDsExtra) + kDsExtra;
+            const int tiles = min(run, s.tiles - ch * run);
+            const int c0 = ds_owner(line, begin, shares), c1 = ds_owner(line, begin + tiles - 1, shares);
+            const int64_t place = a.items[e] + uh * s.chunks + ch + c0;
+            const int64_t row0 = (group ? place * 2 * cap : a.seq_part0 + (place - group_parts) * 2 * cap) + s0 * cap;
+            const int count = (c1 - c0 + 1) * stages, step = pair ? 2 * cap : cap;
+            for (int i0 = 0; i0 < count; i0 += 8) {
+                float4 v[8];
+                float2 ml[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int64_t at = row0 + static_cast<int64_t>(min(i0 + q, count - 1)) * step;
+                    ml[q] = *reinterpret_cast<const float2*>(a.part_ml + (at + m) * 2);
+                    v[q] = reinterpret_cast<const float4*>(a.part_o)[at * (kHeadDim / 4) + static_cast<int64_t>(d4) * cap + m];
+                }
+                float most = top;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) most = fmaxf(most, ml[q].x);
+                const float f = top == -INFINITY ? 0.f : dp_exp2(top - most);
+                if (top != -INFINITY) {
+                    sum *= f;
+                    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                }
+                top = most;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (i0 + q >= count) continue;
+                    // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
+                    const float w = ml[q].x == -INFINITY ? (ml[q].y == ml[q].y ? 0.f : ml[q].y) : dp_exp2(ml[q].x - top);
+                    if (w != 0.f) {
+                        sum = fmaf(w, ml[q].y, sum);
+                        o.x = fmaf(w, v[q].x, o.x);
+                        o.y = fmaf(w, v[q].y, o.y);
+                        o.z = fmaf(w, v[q].z, o.z);
+                        o.w = fmaf(w, v[q].w, o.w);
+                    }
+                }
+            }
+        }
+    };
+    if (g >= 0) {
+        DsEntry y{};
+        int last;
+        bool no;
+        ds_group(a, g, y, last, no);
+        join(g, y, true);
+    }
+    join(a.num_groups + lo, x, false);
+    const float inv = 1.f / sum;
+    const int64_t at = (q_row + gh) * kHeadDim + 4 * d4;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+template <int kParts>
+static cudaError_t launch_shared(const SharedArgs& a, int grid, cudaStream_t stream) {
+    const size_t smem = sizeof(DsSmem<kParts>) + 1024;
+    auto* kernel = dense_shared_kernel<kParts>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kDsThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, *a.q_map, *a.k_map, *a.v_map, a)) != cudaSuccess) return e;
+    // few rows: the dimensions over several CTAs
+    const int64_t blocks = static_cast<int64_t>(a.total_rows) * a.H;
+    const int z = blocks * 4 <= 2 * device_sm_count() ? 4 : (blocks * 2 <= 2 * device_sm_count() ? 2 : 1);
+    const int threads = (a.G * (kHeadDim / 4 / z) + 31) / 32 * 32;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.total_rows), static_cast<unsigned>(a.H), static_cast<unsigned>(z));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    auto* join = a.kv_int8 ? dense_shared_join<true> : dense_shared_join<false>;
+    return cudaLaunchKernelEx(&cfg, join, a, grid, DsCfg<kParts>::NK);
+}
+
+SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int total_rows, int max_rows_per_seq, int max_group_rows,
+                             int max_shared_len, int max_cache_len) {
+    SharedRoom r;
+    const int64_t P = 128 / G, units = total_rows / (2 * P) + num_groups;
+    auto chunks = [](int64_t keys) { return (keys + kDsPartKeys - 1) / kDsPartKeys; };
+    r.grid = std::min(device_sm_count(), kDenseMaxShares);
+    r.group_parts = max_shared_len < kBlock ? 0 : units * H * chunks(max_shared_len);
+    r.seq_parts = static_cast<int64_t>(num_seqs) * H * chunks(max_cache_len);
+    r.group_rows = static_cast<int>(std::min(P, static_cast<int64_t>(max_group_rows)) * G);
+    r.seq_rows = std::min(max_rows_per_seq, kDecodeMaxRows) * G;
+    r.seq_part0 = (r.group_parts > 0 ? (r.group_parts + kDenseMaxShares) * 2 * r.group_rows : 0);
+    r.rows = r.seq_part0 + (r.seq_parts + kDenseMaxShares) * 2 * r.seq_rows;
+    return r;
+}
+
+cudaError_t run_dense_shared(const SharedArgs& a, int grid, cudaStream_t stream) {
+    return a.out_bf16 ? launch_shared<1>(a, grid, stream) : launch_shared<3>(a, grid, stream);
+}
+
+}  // namespace msa

@@ -247,6 +247,44 @@ cudaError_t run_dense_window(const DenseArgs& a, int items, cudaStream_t stream)
 int dense_decode_shares(int64_t units, int H);  // CTAs for so many blocks
 cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream);
 
+// Attention over every cached position for a decode family whose groups of sequences share a prefix.
+struct SharedArgs {
+    const uint16_t* q;
+    const void* k;
+    const void* v;
+    const float* k_scale;  // int8 caches: [T, H]
+    const float* v_scale;
+    void* out;
+    const int32_t* cu_rows;
+    const int32_t* cache_lens;
+    const int32_t* group_starts;  // [num_groups + 1]
+    const int32_t* group_shared;  // [num_groups]
+    CacheRows cache;
+    int num_seqs, num_groups, H, G, total_rows, max_rows_per_seq, max_group_rows, max_shared_len, max_cache_len, kv_int8, out_bf16;
+    int64_t cache_tokens;
+    float scale_log2;          // softmax scale * log2(e)
+    const CUtensorMap* q_map;  // host copies: q as (D, H*G, rows), box 64 x G x 128 / G; the caches (kv_map)
+    const CUtensorMap* k_map;
+    const CUtensorMap* v_map;
+    int64_t* line;             // [num_groups + num_seqs + 1] places of the groups and the sequences on the line of key tiles
+    int32_t* items;            // the same of the parts that the line's items make
+    int64_t group_parts_most, seq_parts_most;  // parts that there is room for, beside one a CTA
+    int group_rows, seq_rows;  // rows of a part's stage: of a group's items, of a sequence's
+    int64_t seq_part0;         // first row of the sequences' parts
+    float* part_o;             // [rows of a stage: dim / 4][row][4]
+    float* part_ml;            // [rows][2] maximum (log2 domain) and sum
+    uint32_t* err_slots;       // [grid]
+    uint32_t* err;             // stored by the join
+};
+struct SharedRoom {
+    int grid = 0;  // CTAs
+    int64_t group_parts = 0, seq_parts = 0, seq_part0 = 0, rows = 0;
+    int group_rows = 0, seq_rows = 0;
+};
+SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int total_rows, int max_rows_per_seq, int max_group_rows,
+                             int max_shared_len, int max_cache_len);
+cudaError_t run_dense_shared(const SharedArgs& a, int grid, cudaStream_t stream);
+
 // Allocation-free decode attention: scratch in a file-scope device array
 // sized for at most kNoAllocMaxPairs (sequence, KV head) pairs per call.
 constexpr int kNoAllocMaxPairs = 32;

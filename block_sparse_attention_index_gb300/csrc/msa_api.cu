@@ -36,6 +36,24 @@ constexpr int64_t kMaxCacheLen = int64_t(1) << 21;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Groups of sequences that share a prefix.
+msa_status check_groups(const msa_problem* p) {
+    if (p->num_groups < 0 || p->num_groups > p->num_seqs)
+        return fail(MSA_ERR_INVALID_ARG, "num_groups must lie in [0, num_seqs] (got %d)", p->num_groups);
+    if (p->num_groups == 0) return MSA_OK;
+    if (!p->group_starts || !p->group_shared) return fail(MSA_ERR_INVALID_ARG, "group_starts or group_shared is null");
+    if ((reinterpret_cast<uintptr_t>(p->group_starts) & 3u) || (reinterpret_cast<uintptr_t>(p->group_shared) & 3u))
+        return fail(MSA_ERR_INVALID_ARG, "group_starts or group_shared is not 4-byte aligned");
+    if (p->max_shared_len < 0 || p->max_shared_len > p->max_cache_len)
+        return fail(MSA_ERR_INVALID_ARG, "max_shared_len must lie in [0, max_cache_len] (got %d)", p->max_shared_len);
+    if (p->max_group_rows < 1 || p->max_group_rows > p->total_rows)
+        return fail(MSA_ERR_INVALID_ARG, "max_group_rows must lie in [1, total_rows] (got %d)", p->max_group_rows);
+    if (p->block_table == nullptr) return fail(MSA_ERR_UNSUPPORTED, "groups that share a prefix need a block table");
+    if (p->max_rows_per_seq > msa::kDecodeMaxRows)
+        return fail(MSA_ERR_UNSUPPORTED, "groups that share a prefix need sequences of at most 8 rows (max_rows_per_seq <= 8)");
+    return MSA_OK;
+}
+
 // Host-side validation shared by every entry point.
 msa_status check_problem(const msa_problem* p) {
     if (p == nullptr) return fail(MSA_ERR_INVALID_ARG, "problem is null");
@@ -95,7 +113,13 @@ msa_status check_problem(const msa_problem* p) {
             return fail(MSA_ERR_INVALID_ARG, "block_table_stride * page_size < max_cache_len");
         if (reinterpret_cast<uintptr_t>(p->block_table) & 3u) return fail(MSA_ERR_INVALID_ARG, "block_table misaligned");
     }
-    return MSA_OK;
+    if (p->ik_dtype != MSA_IK_BF16 && p->ik_dtype != MSA_IK_INT8)
+        return fail(MSA_ERR_INVALID_ARG, "ik_dtype must be MSA_IK_BF16 or MSA_IK_INT8 (got %d)", p->ik_dtype);
+    if (p->ik_dtype == MSA_IK_INT8) {
+        if (!p->ik_exp) return fail(MSA_ERR_INVALID_ARG, "int8 index keys need ik_exp");
+        if (!aligned16(p->ik_exp)) return fail(MSA_ERR_INVALID_ARG, "ik_exp is not 16-byte aligned");
+    }
+    return check_groups(p);
 }
 
 msa_status check_ptr(const void* ptr, const char* name) {
@@ -307,6 +331,34 @@ DenseLayout dense_layout(const msa_problem* p, const DensePlan& d) {
     return l;
 }
 
+// Groups that share a prefix: msa_dense_forward runs on kernels of its own.
+bool dense_shared(const msa_problem* p) { return p->num_groups > 0 && p->kv_dtype == MSA_KV_BF16; }
+
+struct SharedLayout {
+    msa::SharedRoom room;
+    size_t err = 0, err_slots = 0, line = 0, items = 0, part_ml = 0, part_o = 0, total = 0;
+};
+
+SharedLayout shared_layout(const msa_problem* p) {
+    SharedLayout l;
+    l.room = msa::dense_shared_room(p->num_seqs, p->num_groups, p->num_kv_heads, p->group_size, p->total_rows, p->max_rows_per_seq,
+                                    p->max_group_rows, p->max_shared_len, p->max_cache_len);
+    const size_t entries = static_cast<size_t>(p->num_groups) + p->num_seqs + 1, rows = static_cast<size_t>(l.room.rows);
+    size_t off = 256;
+    l.err_slots = off;
+    off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
+    l.line = off;
+    off = align256(off + entries * sizeof(int64_t));
+    l.items = off;
+    off = align256(off + entries * sizeof(int32_t));
+    l.part_ml = off;
+    off = align256(off + rows * 2 * sizeof(float));
+    l.part_o = off;
+    off = align256(off + rows * msa::kHeadDim * sizeof(float));
+    l.total = off;
+    return l;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -467,6 +519,7 @@ msa_status msa_index_scores(const msa_problem* p, const void* iq, const void* ik
         (s = check_ptr(scores, "scores")) != MSA_OK)
         return s;
     if (ld < p->max_cache_len) return fail(MSA_ERR_INVALID_ARG, "ld < max_cache_len");
+    if (p->ik_dtype != MSA_IK_BF16) return fail(MSA_ERR_UNSUPPORTED, "int8 index keys");
     cudaError_t e = msa::run_index_scores(staged_args(p), static_cast<const uint16_t*>(iq),
                                           static_cast<const uint16_t*>(ik_cache), scores, ld,
                                           static_cast<cudaStream_t>(stream));
@@ -718,6 +771,7 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
         return fail(MSA_ERR_INVALID_ARG, "sel_out and nsel_out must both be given or both be null");
     if (sel_out && ((s = check_ptr(sel_out, "sel_out")) != MSA_OK || (s = check_ptr(nsel_out, "nsel_out")) != MSA_OK))
         return s;
+    if (p->ik_dtype != MSA_IK_BF16) return fail(MSA_ERR_UNSUPPORTED, "int8 index keys");
     if (n_events < 0 || n_events > 5) return fail(MSA_ERR_INVALID_ARG, "n_events must be in [0, 5]");
     Layout l;
     if ((s = check_workspace(p, workspace, workspace_bytes, &l)) != MSA_OK) return s;
@@ -879,6 +933,7 @@ msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa
         return s;
     if ((a->q && a->q_out == a->q && a->q_stride != HG * D) || (a->iq && a->iq_out == a->iq && a->iq_stride != H * Di))
         return fail(MSA_ERR_INVALID_ARG, "q and iq can be rotated in place only where their rows are contiguous");
+    if (a->ik && p->ik_dtype != MSA_IK_BF16) return fail(MSA_ERR_UNSUPPORTED, "int8 index keys");
     const bool i8 = p->kv_dtype == MSA_KV_INT8;
     if (i8 != (a->k_scale != nullptr) || i8 != (a->v_scale != nullptr))
         return fail(MSA_ERR_INVALID_ARG, "k_scale and v_scale are given for an int8 cache and for no other");
@@ -941,8 +996,70 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes) {
     msa_status s = check_problem(p);
     if (s != MSA_OK) return s;
     if (!bytes) return fail(MSA_ERR_INVALID_ARG, "bytes is null");
-    *bytes = dense_layout(p, dense_plan(p)).total;
+    *bytes = dense_shared(p) ? shared_layout(p).total : dense_layout(p, dense_plan(p)).total;
     return MSA_OK;
+}
+
+static msa_status check_dense_workspace(const void* workspace, size_t bytes, size_t needed) {
+    if (workspace == nullptr) return fail(MSA_ERR_WORKSPACE, "workspace is null");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (bytes < needed) return fail(MSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, needed);
+    return MSA_OK;
+}
+
+// msa_dense_forward of a batch with groups (arguments checked but for the workspace).
+static msa_status dense_shared_forward(const msa_problem* p, const void* q, const void* k_cache, const void* v_cache, void* out,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t st) {
+    const SharedLayout l = shared_layout(p);
+    msa_status s = check_dense_workspace(workspace, workspace_bytes, l.total);
+    if (s != MSA_OK) return s;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const uint32_t G = p->group_size;
+    CUtensorMap qm, km, vm;
+    if ((s = kv_map(&km, p, k_cache, "k_cache")) != MSA_OK || (s = kv_map(&vm, p, v_cache, "v_cache")) != MSA_OK ||
+        (s = make_map(&qm, q, 128, static_cast<uint64_t>(p->num_kv_heads) * G, p->total_rows, 64, G, 128 / G, "q")) != MSA_OK)
+        return s;
+    msa::SharedArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = k_cache;
+    a.v = v_cache;
+    a.kv_int8 = p->kv_dtype == MSA_KV_INT8;
+    a.k_scale = a.kv_int8 ? p->k_scale : nullptr;
+    a.v_scale = a.kv_int8 ? p->v_scale : nullptr;
+    a.out = out;
+    a.out_bf16 = p->out_dtype == MSA_OUT_BF16;
+    a.cu_rows = p->cu_rows;
+    a.cache_lens = p->cache_lens;
+    a.group_starts = p->group_starts;
+    a.group_shared = p->group_shared;
+    a.cache = cache_rows_of(p);
+    a.num_seqs = p->num_seqs;
+    a.num_groups = p->num_groups;
+    a.H = p->num_kv_heads;
+    a.G = p->group_size;
+    a.total_rows = p->total_rows;
+    a.max_rows_per_seq = p->max_rows_per_seq;
+    a.max_group_rows = p->max_group_rows;
+    a.max_shared_len = p->max_shared_len;
+    a.max_cache_len = p->max_cache_len;
+    a.cache_tokens = p->cache_tokens;
+    a.scale_log2 = scale_log2(p);
+    a.q_map = &qm;
+    a.k_map = &km;
+    a.v_map = &vm;
+    a.line = reinterpret_cast<int64_t*>(ws + l.line);
+    a.items = reinterpret_cast<int32_t*>(ws + l.items);
+    a.group_parts_most = l.room.group_parts;
+    a.seq_parts_most = l.room.seq_parts;
+    a.group_rows = l.room.group_rows;
+    a.seq_rows = l.room.seq_rows;
+    a.seq_part0 = l.room.seq_part0;
+    a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+    a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
+    a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
+    a.err = reinterpret_cast<uint32_t*>(ws + l.err);
+    const cudaError_t e = msa::run_dense_shared(a, l.room.grid, st);
+    return e == cudaSuccess ? MSA_OK : cuda_fail(e, "shared-prefix attention launch");
 }
 
 msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_cache, const void* v_cache, void* out,
@@ -957,13 +1074,11 @@ msa_status msa_dense_forward(const msa_problem* p, const void* q, const void* k_
     const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(out);
     if (q0 < o0 + values * (p->out_dtype == MSA_OUT_BF16 ? 2 : 4) && o0 < q0 + values * 2)
         return fail(MSA_ERR_INVALID_ARG, "out overlaps q");  // (q is read again where a row is computed a second time)
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dense_shared(p)) return dense_shared_forward(p, q, k_cache, v_cache, out, workspace, workspace_bytes, st);
     const DensePlan d = dense_plan(p);
     const DenseLayout l = dense_layout(p, d);
-    if (workspace == nullptr) return fail(MSA_ERR_WORKSPACE, "workspace is null");
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(MSA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-    if (workspace_bytes < l.total)
-        return fail(MSA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, l.total);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((s = check_dense_workspace(workspace, workspace_bytes, l.total)) != MSA_OK) return s;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaError_t e;
     msa::DenseArgs a{};

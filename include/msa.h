@@ -89,6 +89,9 @@ enum { MSA_OUT_F32 = 0, MSA_OUT_BF16 = 1 };
 /* Element type of the key and value caches (msa_problem.kv_dtype). */
 enum { MSA_KV_BF16 = 0, MSA_KV_INT8 = 1 };
 
+/* Element type of the index-key cache (msa_problem.ik_dtype). */
+enum { MSA_IK_BF16 = 0, MSA_IK_INT8 = 1 };
+
 /* One batch: B sequences, each with n_b >= 1 query rows and a cache of L_b
  * tokens (n_b <= L_b).  Host fields size grids and workspaces; device
  * fields are read by the kernels. */
@@ -150,6 +153,32 @@ typedef struct msa_problem {
      * launches work that exits at once.  Library mechanics: the pages have
      * no counterpart. */
     int32_t num_decode_rows;
+    /* Index-key cache element type (the pages have no counterpart).
+     * MSA_IK_BF16 (0): ik is bf16.  MSA_IK_INT8 (1): ik is int8 codes of the
+     * same shape with a power of two for each (cache row, index head),
+     *     ik[t, h, d] = ik8[row, h, d] * 2^ik_exp[row, h]
+     * (exactly a bf16 value; -128 stands for a key that is not finite, whose
+     * score is NaN and is passed over in a block's maximum).  ik_exp is device
+     * int8 [cache_tokens, H] (H -> 1 with a shared index key), 16-byte aligned.
+     * Read by msa_forward and msa_index_scores, written by msa_append_cache. */
+    int32_t ik_dtype;
+    const int8_t* ik_exp;
+    /* Groups of sequences that share a prefix (optional, num_groups = 0:
+     * none; the pages have no counterpart).  Group g is the sequences
+     * group_starts[g] .. group_starts[g+1]-1; the first group_shared[g]
+     * positions of each of them lie in the same cache rows (their block
+     * tables begin alike), and every row lies past them (L_b - n_b >=
+     * group_shared[g]).  A statement about the caches, not an option: results
+     * are those of the same call without groups, msa_dense_forward and
+     * msa_forward read what is shared (whole 64-position blocks of it, by the
+     * block table of the group's first sequence) once for the group's rows
+     * instead of once a sequence.  With groups: a block table, and sequences
+     * of 1 to 8 rows only (max_rows_per_seq <= 8). */
+    int32_t num_groups;          /* at most num_seqs                            */
+    int32_t max_shared_len;      /* >= every group_shared (host bound), <= max_cache_len */
+    int32_t max_group_rows;      /* >= the rows of every group (host bound)     */
+    const int32_t* group_starts; /* device [num_groups + 1], ascending, within [0, num_seqs] */
+    const int32_t* group_shared; /* device [num_groups]                         */
 } msa_problem;
 
 /* Human-readable name of a status code (static string).  Library mechanics:
@@ -338,6 +367,7 @@ typedef struct msa_append {
     void* ik_cache;
     float* k_scale; /* MSA_KV_INT8: [cache_tokens, H], written; else NULL    */
     float* v_scale;
+    int8_t* ik_exp; /* MSA_IK_INT8 and ik given: [cache_tokens, KH], written; else NULL */
     void* q_out;    /* [total_rows, H*G, D] bf16, contiguous; may be q itself when q_stride = H*G*D */
     void* iq_out;   /* [total_rows, H, Di] bf16, contiguous; may be iq likewise                      */
 } msa_append;
@@ -350,7 +380,11 @@ typedef struct msa_append {
  *   scale = max_d |y_d| / 127,   code_d = round-to-nearest-even(y_d / scale)
  * (clamped to [-127, 127]; zero codes for a zero head; a head that holds a
  * NaN or an infinity gets a NaN or infinite scale and zero codes, which read
- * back as NaN).  Cache rows of other positions are left as they were, and so
+ * back as NaN).  Index keys of MSA_IK_INT8:
+ *   e = the smallest integer >= -126 with max_d |y_d| <= 127 2^e,
+ *   code_d = round-to-nearest-even(y_d / 2^e)
+ * (-126 for a zero head, -128 and zero codes for one that holds a NaN or an
+ * infinity).  Cache rows of other positions are left as they were, and so
  * are rows of q_out and iq_out at or past cu_rows[num_seqs].  Two positions
  * that share a cache row (a page listed twice) are the caller's error.
  * Metadata errors go to the error word in the workspace's first 4 bytes, as
