@@ -2,24 +2,26 @@
 // groups of sequences share a prefix: the prefix is read once for all rows of the group.
 //   out = sum_t 2^(x_t - m) v_t / sum_t 2^(x_t - m),  x_t = scale log2(e) q.k_t over t <= p
 // A softmax over a set of keys splits into parts (O, m, l: unnormalised sum, maximum, sum of weights) over any division
-// of the keys, joined by weights 2^(m_i - m).  Here a row's keys are divided into its group's shared positions [0, S),
-// which are this file's, and its sequence's own [S, p], which the streaming kernel of decode rows takes (dense_decode.cuh:
-// 16 rows are all that share those, and its warps take a tile of keys each, where a tile of 128 rows would leave seven
-// eighths of the softmax threads without a row: 2 to 3 us a tile of 128 keys and CTA, against 0.6).  Every row of a group
-// sees all shared positions: no edge, and no later token's value is ever multiplied with.
+// of the keys, joined by weights 2^(m_i - m).  Here the keys of a row are divided into
+//   the group's shared positions [0, S)     one item for up to 2 x 128 (row, head) pairs of the group and a KV head
+//   the sequence's own positions [S, L - n) one item for the sequence's (row, head) pairs and a KV head
+//   the n rows' own positions [L - n, p]    at most 8 keys, in fp32 by the kernel that joins the parts
+// so that the first two have no causal edge: every row of an item sees every key of it, and no value of a later token is
+// ever multiplied with.
 //
-// dense_shared_kernel.  An item is an M tile of 128 rows (row = neighbouring query rows x G heads of a KV head) or two of
-// them, and its keys in tiles of NK:
+// dense_shared_kernel.  An item is an M tile of 128 rows (row = neighbouring query rows x G heads; a sequence's n G rows
+// leave the others of the tile empty) or two of them, and its keys in tiles of NK:
 //   S[128, NK] = Q K^T     operands from shared memory (TMA, 128-byte swizzle), S in tensor memory
 //   P = 2^(x - m)          a thread a row, written over S (m is raised only where it would grow by more than 8)
 //   O[128, 128] += P V     P from tensor memory, V as it lies
 // Two stages of 128 columns of S and of O: two M tiles that take turns on the tensor pipe, or one M tile whose stages
 // take alternate key tiles.  One CTA per SM; all items' key tiles lie on a line, item after item, that is cut into even
-// shares (going on to another item counts as some tiles); a CTA's shares of items leave their parts in the workspace.
+// shares (an item counts for kDsExtra tiles more, what going on to another one costs); a CTA's shares of items leave
+// their parts in the workspace.
 //
-// dense_shared_join.  A CTA takes a row and a KV head: the places of its parts follow from the two kernels' lines by
-// arithmetic (slot = item + CTA, which is different for every pair of them that meets, as both ascend along the line).
-// This kernel's parts lie [dim / 4][row][4], so that the rows of a tile are stored and loaded in whole lines.
+// dense_shared_join.  A CTA takes a row and a KV head: the row's own keys, then the parts, whose places follow from the
+// same line by arithmetic (slot = item + CTA, which is different for every pair of them that meets, as both ascend along
+// the line).  Parts lie [dim / 4][row][4], so that the rows of a tile are stored and loaded in whole lines.
 //
 // Numerics.  bf16 outputs: weights as one bf16 (2^-8 at most, at random), and at most 32,768 keys to a part, as the
 // tensor cores cut what an addition loses instead of rounding it (2^-24 an addition of 16 keys).  fp32 outputs: weights
@@ -27,31 +29,26 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "dense_decode.cuh"
-#include "groups.cuh"
 #include "internal.h"
 #include "tensor_rows.cuh"
 
 namespace msa {
 
-constexpr int kDsThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 and 10 copies (10: items too), 9 and 11 matrix instructions
+constexpr int kDsThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 and 10 copies, 9 and 11 matrix instructions
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
 constexpr int kDsPartKeys = 32768;  // most keys of a part
-// What lies on the line, in about 0.3 us: a key tile of two M tiles 1.5 us (the tensor pipe), of one 1.2 (its copies), and
-// going on to another item 2.5.
-constexpr int kDsPairTile = 5, kDsTile = 4, kDsExtra = 8;
-constexpr int kDsBatch = 8;         // items published at a time, two batches deep
+constexpr int kDsExtra = 3;         // tiles that an item counts for besides its own
+constexpr int kDsInfo = 4;          // items published ahead
 constexpr float kDsSlack = 8.f;     // log2 by which the running maximum may lag
 
 // A CTA's share of an item.
 struct DsItem {
     int b;             // sequence whose table is read; < 0: no more items
-    int row, rows;     // first query row of the item, query rows of its group from there on
-    int h, key, end;   // KV head; first key of the share; end of the group's keys
-    int tiles, pair;   // key tiles; two M tiles, or one whose stages take alternate key tiles
+    int row, rows;     // first query row of the item, query rows of its entry from there on
+    int h, key, end;   // KV head; first key of the share; end of the entry's keys
+    int tiles, pair;   // key tiles; two M tiles (or one, the stages on alternate key tiles)
+    int cap;           // rows of a stage's part
     int64_t part;      // first row of its parts in the workspace
-
-    __device__ __forceinline__ int count(int s) const { return pair ? tiles : (tiles + 1 - s) / 2; }  // key tiles of stage s
 };
 
 template <int kParts>
@@ -60,6 +57,7 @@ struct DsCfg {
     static constexpr int kTile = NK * kHeadDim * 2;  // bytes of a K or V tile
     static constexpr int kStages = 5 * (128 / NK);
     static constexpr int kSAt = kParts == 1 ? 0 : 64;  // column of S in its 128 (as in the prompt kernel: P's parts from 0 on)
+    static constexpr int kRun = kDsPartKeys / NK;      // most tiles of a part
 };
 
 template <int kParts>
@@ -67,14 +65,14 @@ struct __align__(1024) DsSmem {
     using Cfg = DsCfg<kParts>;
     uint8_t q[2][kDsQBytes];
     uint8_t ring[Cfg::kStages][Cfg::kTile];
-    // Copies landed: of pairs [0], of the stages on alternate tiles [1], [2], each counted by itself, so that an issuer sees
-    // all phases of the barriers that it waits for.
+    // Copies landed: of pairs [0], of the two stages on alternate tiles [1], [2], each counted by itself, so that an issuer
+    // sees all phases of the barriers that it waits for.
     uint64_t full[3][Cfg::kStages], empty[Cfg::kStages];
+    uint64_t v_last[Cfg::kStages];  // a last value tile has landed, before its tail is zeroed (by ring slot: a copier may be items ahead)
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
-    uint64_t info_full[2], info_empty[2], pair_done;
-    DsItem info[2][kDsBatch];
-    int32_t next;  // the CTA's first item
+    uint64_t info_full[kDsInfo], info_empty[kDsInfo], item_done;
+    DsItem info[kDsInfo];
     uint32_t tmem, err;
     int64_t scan_line[kDsThreads / 32];
     int32_t scan_items[kDsThreads / 32];
@@ -82,84 +80,85 @@ struct __align__(1024) DsSmem {
 static_assert(sizeof(DsSmem<1>) + 1024 <= 227 * 1024, "shared-prefix attention exceeds 227 KB of shared memory");
 static_assert(sizeof(DsSmem<3>) + 1024 <= 227 * 1024, "shared-prefix attention (fp32) exceeds 227 KB of shared memory");
 
-// What the join has to know of a row.
-struct DsRow {
-    int seq, group;             // seq < 0: it is no row, or its sequence's metadata is bad; group < 0: none
-    int row, rows;              // its sequence's first row, rows
-    int group_row, group_rows;  // its group's
-    int shared, blocks;         // shared positions; blocks of its own
+// Entries of the line: the groups, then the sequences.  The query rows [row, row + rows) see all keys [key, end).
+struct DsEntry {
+    int b, row, rows, key, end;
 };
-static_assert(sizeof(DsRow) == kDsRowBytes, "records of the rows");
 
-// How a group lies on the line: its keys in `chunks`, each of them for the `units` items (of up to two M tiles) of every KV
-// head one after the other.  These read the same keys, or the same tokens, and neighbours on the line run at the same time on
-// neighbouring CTAs, so that all but the first find them in L2: chunks are about as long as a CTA's share of the line (64
-// rows at 32,768, 4 items a head: 276 MB were read from DRAM with the items' keys whole, 182 with chunks; 167 are needed).
-struct DsSize {
-    int tiles, chunks, units, heads, weight;  // key tiles; chunks; items a head; KV heads; a key tile's length on the line
+// The shared positions of group g in whole blocks (0 where its metadata is bad), its sequences and rows.
+__device__ __forceinline__ int ds_group(const SharedArgs& a, int g, DsEntry& x, int& last, bool& bad) {
+    const int b0 = a.group_starts[g], b1 = a.group_starts[g + 1], S = a.group_shared[g];
+    bad = b0 < 0 || b1 < b0 || b1 > a.num_seqs || S < 0 || S > a.max_shared_len;
+    if (bad) return 0;
+    const int c0 = a.cu_rows[b0], c1 = a.cu_rows[b1];
+    bad = c0 < 0 || c1 < c0 || c1 > a.total_rows || c1 - c0 > a.max_group_rows;
+    if (bad) return 0;
+    x = DsEntry{b0, c0, c1 - c0, 0, S & ~(kBlock - 1)};
+    last = b1;
+    return x.end;
+}
 
-    __device__ __forceinline__ int start(int ch) const { return tiles * ch / chunks; }  // (2^15 tiles and 160 chunks at most)
-    __device__ __forceinline__ int length(int ch) const { return start(ch + 1) - start(ch); }
-    __device__ __forceinline__ int parts() const { return chunks * heads * units; }
-    __device__ __forceinline__ int64_t all() const { return static_cast<int64_t>(heads * units) * (tiles * weight + chunks * kDsExtra); }
-    // Where chunk ch begins, and where the tiles of its item u of head h do, after the item's kDsExtra.
-    __device__ __forceinline__ int64_t begin(int ch) const { return static_cast<int64_t>(heads * units) * (start(ch) * weight + ch * kDsExtra); }
-    __device__ __forceinline__ int64_t place(int h, int ch, int u) const {
-        return begin(ch) + static_cast<int64_t>(h * units + u) * (length(ch) * weight + kDsExtra) + kDsExtra;
+// The shared positions of sequence b, in whole blocks, and its group (-1: none).
+__device__ __forceinline__ int ds_shared_of(const SharedArgs& a, int b, int& g) {
+    int lo = 0, hi = a.num_groups;  // largest group that begins at or before b
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.group_starts[mid] <= b) lo = mid; else hi = mid;
     }
-    __device__ __forceinline__ int part(int h, int ch, int u) const { return (ch * heads + h) * units + u; }
+    g = -1;
+    DsEntry x;
+    int last;
+    bool bad;
+    const int S = ds_group(a, lo, x, last, bad);
+    if (bad || b < x.b || b >= last || S == 0) return 0;
+    g = lo;
+    return S;
+}
+
+// Sequence b; rows = 0: it has none, or its metadata is bad.
+__device__ __forceinline__ DsEntry ds_seq(const SharedArgs& a, int b, int& g, bool& bad) {
+    const int c0 = a.cu_rows[b], n = a.cu_rows[b + 1] - c0, L = a.cache_lens[b];
+    const int S = ds_shared_of(a, b, g);
+    bad = n < 0 || n > min(a.max_rows_per_seq, kDecodeMaxRows) || c0 < 0 || c0 + n > a.total_rows || L < n || L > a.max_cache_len ||
+          L - n < S;
+    if (n == 0) bad = false;
+    if (bad || n == 0) return DsEntry{b, 0, 0, 0, 0};
+    return DsEntry{b, c0, n, S, L - n};
+}
+
+// How an entry lies on the line: `units` items a head (of up to two M tiles), each `chunks` parts of up to `run` tiles.
+struct DsSize {
+    int tiles, chunks, units, unit;  // key tiles; parts they make; items a head; an item's length on the line
 };
-__device__ __forceinline__ DsSize ds_size(const SharedArgs& a, int rows, int keys, int NK, int share) {
+__device__ __forceinline__ DsSize ds_size(const SharedArgs& a, const DsEntry& x, int NK) {
     DsSize s{};
-    if (rows <= 0 || keys <= 0) return s;
-    const int run = kDsPartKeys / NK, P = 128 / a.G, mt = (rows + P - 1) / P;
-    s.tiles = (keys + NK - 1) / NK;
-    s.weight = mt > 1 ? kDsPairTile : kDsTile;
+    if (x.rows == 0 || x.end <= x.key) return s;
+    const int run = kDsPartKeys / NK, P = 128 / a.G, mt = (x.rows + P - 1) / P;
+    s.tiles = (x.end - x.key + NK - 1) / NK;
+    s.chunks = (s.tiles + run - 1) / run;
     s.units = (mt + 1) / 2;
-    s.heads = a.H;
-    s.chunks = max((s.tiles + run - 1) / run, (s.tiles * s.weight + share / 2) / share);
+    s.unit = s.tiles + s.chunks * kDsExtra;
     return s;
+}
+__device__ __forceinline__ DsEntry ds_entry(const SharedArgs& a, int e, bool& bad) {
+    if (e >= a.num_groups) {
+        int g;
+        return ds_seq(a, e - a.num_groups, g, bad);
+    }
+    DsEntry x{};
+    int last;
+    ds_group(a, e, x, last, bad);
+    return x;
 }
 
 // CTAs that share a line, and where share c begins (the largest c whose share begins at or before a place: ds_owner).
 __host__ __device__ __forceinline__ int ds_shares(int64_t line, int grid) {
-    const int64_t n = line / (kDsExtra + 2 * kDsTile);
+    const int64_t n = line / (kDsExtra + 2);
     return static_cast<int>(n < 1 ? 1 : (n < grid ? n : grid));
 }
-__device__ __forceinline__ int64_t ds_cut(int64_t line, int c, int shares) {
-    if (line < INT32_MAX / 256) return static_cast<uint32_t>(line) * static_cast<uint32_t>(c) / static_cast<uint32_t>(shares);
-    return line * c / shares;
-}
+__device__ __forceinline__ int64_t ds_cut(int64_t line, int c, int shares) { return line * c / shares; }
 __device__ __forceinline__ int ds_owner(int64_t line, int64_t at, int shares) {
-    const int64_t x = (at + 1) * shares - 1;
-    if (line < INT32_MAX / 256) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(line));
-    return static_cast<int>(x / line);
-}
-
-// Leaves the records of sequence b's rows.
-__device__ __noinline__ void ds_record(const SharedArgs& a, int b) {
-    const int c0 = a.groups.cu_rows[b], c1 = a.groups.cu_rows[b + 1], L = a.cache_lens[b], n = c1 - c0;
-    DsRow r{};
-    r.seq = -1;
-    // every row gets a record, whatever the row counts are: rows of no sequence from the first or the last
-    if (b == 0)
-        for (int i = 0; i < min(c0, a.groups.total_rows); ++i) a.rows[i] = r;
-    if (b == a.groups.num_seqs - 1)
-        for (int i = max(c1, 0); i < a.groups.total_rows; ++i) a.rows[i] = r;
-    const int S = shared_of(a.groups, b, r.group);
-    if (n >= 1 && n <= min(a.max_rows_per_seq, kDecodeMaxRows) && c0 >= 0 && c1 <= a.groups.total_rows && L <= a.max_cache_len && L - n >= S) {
-        r.seq = b;
-        r.row = c0;
-        r.rows = n;
-        r.shared = S;
-        r.blocks = (L + kBlock - 1) / kBlock - S / kBlock;
-        Group x;
-        if (r.group >= 0 && group_at(a.groups, r.group, x)) {
-            r.group_row = x.row;
-            r.group_rows = x.rows;
-        }
-    }
-    for (int i = max(c0, 0); i < min(c1, a.groups.total_rows); ++i) a.rows[i] = r;
+    return static_cast<int>(((at + 1) * shares - 1) / line);
 }
 
 template <int kParts>
@@ -169,7 +168,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                                                                     const SharedArgs a) {
     using Cfg = DsCfg<kParts>;
     using Smem = DsSmem<kParts>;
-    constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2, kSAt = Cfg::kSAt;
+    constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2, kSAt = Cfg::kSAt, kRun = Cfg::kRun;
     extern __shared__ uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -178,11 +177,14 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
         for (int s = 0; s < kStages; ++s) {
             for (int k = 0; k < 3; ++k) mbar_init(&sm.full[k][s], 2);  // two warps copy a half each
             mbar_init(&sm.empty[s], 2);                                // both issuers (alternate tiles: one, and the copier for the other)
+            mbar_init(&sm.v_last[s], 2);
         }
-        mbar_init(&sm.pair_done, 2);
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kDsInfo; ++s) {
             mbar_init(&sm.info_full[s], 1);
             mbar_init(&sm.info_empty[s], 11);  // a copier, two issuers, eight softmax warps
+        }
+        mbar_init(&sm.item_done, 2);
+        for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.q_full[s], 1);
             mbar_init(&sm.q_empty[s], 2);
             mbar_init(&sm.s_full[s], 1);
@@ -193,7 +195,6 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
             mbar_init(&sm.drain[s], 1);
         }
         sm.err = 0;
-        sm.next = 0;
         fence_mbar_init();
     }
     if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &q_map : (lane == 1 ? &k_map : &v_map));
@@ -204,56 +205,28 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = sm.tmem;
-    // ---- places of the groups on the line, and parts before each (a block-wide scan; every CTA stores the same)
-    const int num = a.groups.num, P = 128 / a.G;
-    const bool few = num <= kDsThreads;  // a thread a group
-    Group mine{};
-    bool my_bad = false;
-    if (few && tid < num) my_bad = !group_at(a.groups, tid, mine);
-    auto group_of = [&](int g, bool& bad) {
-        if (few) {
-            bad = my_bad;
-            return mine;
-        }
-        Group x;
-        bad = !group_at(a.groups, g, x);
-        return x;
-    };
+    // ---- places of the entries on the line, and parts before each (a block-wide scan; every CTA stores the same)
+    const int entries = a.num_groups + a.num_seqs;
     int64_t line = 0;
-    for (int g = tid; g < num; g += kDsThreads) {
-        bool bad;
-        const Group x = group_of(g, bad);
-        const DsSize s = ds_size(a, x.rows, x.shared, NK, INT32_MAX);
-        line += static_cast<int64_t>(a.H) * s.units * (s.tiles * s.weight + kDsExtra);
-        if (bad && blockIdx.x == 0) atomicOr(&sm.err, kErrBadMetadata);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) line += __shfl_xor_sync(0xffffffffu, static_cast<long long>(line), o);
-    if (lane == 0) sm.scan_line[warp] = line;
-    if (tid < kDsBatch) sm.info[0][tid].b = -1;
-    __syncthreads();
-    line = 0;
-    for (int w = 0; w < kDsThreads / 32; ++w) line += sm.scan_line[w];
-    const int share = static_cast<int>(max(int64_t{kDsExtra + 2 * kDsTile}, min(line / gridDim.x, int64_t{INT32_MAX / 2})));  // about
-    __syncthreads();
-    line = 0;
-    int parts = 0, my_items = 0, my_count = 0;
-    int64_t my_line = 0;
-    DsSize my_size{};
-    for (int base = 0; base < num; base += kDsThreads) {
-        const int g = base + tid;
-        int64_t length = 0;
+    int parts = 0;
+    for (int base = 0; base < entries; base += kDsThreads) {
+        const int e = base + tid;
+        int64_t mine = 0;
         int items = 0;
-        if (g < num) {
+        if (e < entries) {
             bool bad;
-            const Group x = group_of(g, bad);
-            my_size = ds_size(a, x.rows, x.shared, NK, share);
-            if (my_size.units > 0) {
-                length = my_size.all();
-                items = my_size.parts();
+            const DsEntry x = ds_entry(a, e, bad);
+            const DsSize s = ds_size(a, x, NK);
+            mine = static_cast<int64_t>(a.H) * s.units * s.unit;
+            items = a.H * s.units * s.chunks;
+            if (blockIdx.x == 0) {
+                if (e >= a.num_groups && x.rows > 0)  // the rows' own positions, which the join reads
+                    bad |= block_row(a.cache, x.b, x.end & ~(kBlock - 1)) < 0 ||
+                           block_row(a.cache, x.b, (x.end + x.rows - 1) & ~(kBlock - 1)) < 0;
+                if (bad) atomicOr(&sm.err, kErrBadMetadata);
             }
         }
-        int64_t incl = length;
+        int64_t incl = mine;
         int incl_items = items;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -279,185 +252,128 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
             line += sm.scan_line[w];
             parts += sm.scan_items[w];
         }
-        if (g < num) {
-            my_line = before + incl - length;
-            my_items = before_items + incl_items - items;
-            my_count = items;
-            a.line[g] = my_line;
-            a.items[g] = my_items;
+        if (e < entries) {
+            a.line[e] = before + incl - mine;
+            a.items[e] = before_items + incl_items - items;
         }
         __syncthreads();
     }
     if (tid == 0) {
-        a.line[num] = line;
-        a.line[num + 1] = share;
-        a.items[num] = parts;
+        a.line[entries] = line;
+        a.items[entries] = parts;
     }
-    if (parts > a.parts_most) {  // more than the host's bounds allow for
+    __syncthreads();
+    const int group_parts = a.items[a.num_groups];
+    if (group_parts > a.group_parts_most || parts - group_parts > a.seq_parts_most) {  // more than the host's bounds allow for
         if (tid == 0) atomicOr(&sm.err, kErrBadMetadata);
         line = 0;
     }
     const int shares = ds_shares(line, gridDim.x);
     const bool idle = line == 0 || static_cast<int>(blockIdx.x) >= shares;
-    // ---- the CTA's share of the line.  Its items are numbered as their parts are, from the one that holds its beginning on.
-    const int64_t from = idle ? 0 : ds_cut(line, blockIdx.x, shares), stop = idle ? 0 : ds_cut(line, blockIdx.x + 1, shares);
-    auto first_item = [&](const DsSize& sz, int items, int64_t at_line) {
-        const int64_t o = from - at_line;
-        int ch = min(static_cast<int>(o * sz.chunks / sz.all()), sz.chunks - 1);
-        while (ch > 0 && sz.begin(ch) > o) --ch;
-        while (ch + 1 < sz.chunks && sz.begin(ch + 1) <= o) ++ch;
-        const int length = sz.length(ch) * sz.weight + kDsExtra, off = static_cast<int>(o - sz.begin(ch));
-        const int hu = min(off / length, sz.heads * sz.units - 1);
-        // (a tile is the CTA's in whose share it begins: the item's last may have)
-        return items + sz.part(0, ch, hu) + (off - hu * length > length - sz.weight ? 1 : 0);
-    };
-    auto item_of = [&](int part, const Group& x, const DsSize& sz, int items, int64_t at_line) {
-        DsItem it{};
-        it.b = -1;
-        const int at = part - items, ch_h = at / sz.units, u = at - ch_h * sz.units, ch = ch_h / sz.heads, h = ch_h - ch * sz.heads;
-        const int64_t begin = at_line + sz.place(h, ch, u), last = min(stop, begin + sz.length(ch) * sz.weight);
-        const int t0 = from > begin ? static_cast<int>(from - begin + sz.weight - 1) / sz.weight : 0;
-        const int t1 = last > begin ? static_cast<int>(last - begin + sz.weight - 1) / sz.weight : 0;
-        if (t1 <= t0) return it;
-        it.b = x.first;
-        it.row = x.row + u * 2 * P;
-        it.rows = x.rows - u * 2 * P;
-        it.h = h;
-        it.key = (sz.start(ch) + t0) * NK;
-        it.end = x.shared;
-        it.tiles = t1 - t0;
-        it.pair = it.rows > P;
-        it.part = (static_cast<int64_t>(part) + blockIdx.x) * 2 * a.stage_rows;
-        return it;
-    };
-    if (few && !idle) {  // the first items, by the threads that have their entries
-        if (my_count > 0 && from >= my_line && from < my_line + my_size.all())
-            sm.next = first_item(my_size, my_items, my_line);
-        __syncthreads();
-        const int next = sm.next;
-        for (int part = max(my_items, next); part < min(my_items + my_count, next + kDsBatch); ++part)
-            sm.info[0][part - next] = item_of(part, mine, my_size, my_items, my_line);
-    }
-    __syncthreads();
+    const int P = 128 / a.G;
 
     auto next_item = [&](int k, DsItem& x) {  // item k of the CTA, false where it never came
-        const int n = k / kDsBatch;
-        if (k % kDsBatch == 0 && !wait(&sm.info_full[n & 1], (n >> 1) & 1)) return false;
-        x = sm.info[n & 1][k % kDsBatch];
+        if (!wait(&sm.info_full[k % kDsInfo], (k / kDsInfo) & 1)) return false;
+        x = sm.info[k % kDsInfo];
         return true;
     };
-    auto passed = [&](int k, const DsItem& x) {  // (one thread of the role) the item has been read: the last of its batch
-        if (k % kDsBatch == kDsBatch - 1 || x.b < 0) mbar_arrive(&sm.info_empty[(k / kDsBatch) & 1]);
-    };
+    auto passed = [&](int k) { mbar_arrive(&sm.info_empty[k % kDsInfo]); };
+    auto count_of = [](const DsItem& x, int s) { return x.pair ? x.tiles : (x.tiles + 1 - s) / 2; };  // key tiles of stage s
 
-    // (the records: by the softmax groups, which wait for their first products anyway)
-    if (warp < 8)
-        for (int b = blockIdx.x + tid * gridDim.x; b < a.groups.num_seqs; b += 256 * gridDim.x) ds_record(a, b);
     if (idle) {
         // nothing to do
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8 || warp == 10) {
-            // ---------------- copies: K and V tiles, dimensions 0-63 by warp 8 (and the queries), 64-127 by warp 10 (and items)
+            // ---------------- copies: K and V tiles, dimensions 0-63 by warp 8 (and the queries), 64-127 by warp 10 (which
+            // also finds the items, and clears the end of a last value tile)
             const int half = warp == 10;
             int slot = 0, sent[3] = {0, 0, 0}, q_used[2] = {0, 0};  // copies in all and by barrier row; items by query buffer
-            int next = sm.next;
-            bool more = true;  // items beyond the published ones
-            // the last of table[0 .. num] that is at most x, 32 candidates at a time (a whole warp)
-            auto last_of = [&](auto* table, auto x) {
-                int lo = 0, hi = num;
+            uint32_t fixed = 0;  // last value tiles, a bit a ring slot: how often modulo 2
+            bool alive = true;
+            // the CTA's walk along the line
+            int64_t at = ds_cut(line, blockIdx.x, shares);
+            const int64_t stop = ds_cut(line, blockIdx.x + 1, shares);
+            int e = 0;
+            DsEntry x{};
+            DsSize sz{};
+            int64_t e_line = 0, e_next = -1;
+            if (half) {
+                int lo = 0, hi = entries;  // the last entry that begins at or before it
                 while (hi - lo > 1) {
-                    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-                    const uint32_t le = __ballot_sync(0xffffffffu, at < hi && table[at] <= x);
-                    lo += (31 - __clz(le)) * step;
-                    hi = min(lo + step, hi);
+                    const int mid = (lo + hi) >> 1;
+                    if (a.line[mid] <= at) lo = mid; else hi = mid;
                 }
-                return lo;
-            };
-            if (half && !few) {
-                const int lo = last_of(a.line, from);
-                Group x;
-                group_at(a.groups, lo, x);
-                next = first_item(ds_size(a, x.rows, x.shared, NK, share), a.items[lo], a.line[lo]);
+                e = lo - 1;
             }
-            auto publish = [&](int n) {  // batch n: a lane an item
-                int ok = 1;
-                if (lane == 0 && n >= 2) ok = wait(&sm.info_empty[n & 1], ((n >> 1) - 1) & 1);
-                if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+            auto find = [&]() {
                 DsItem it{};
                 it.b = -1;
-                if (n == 0 && few) {
-                    if (lane < kDsBatch) it = sm.info[0][lane];
-                } else {
-                    const int part = next + lane;
-                    // the num of the items: among the 32 from the first one's on, or found one by one
-                    const int e0 = last_of(a.items, min(next, parts - 1));
-                    const int begins = e0 + lane <= num ? a.items[e0 + lane] : INT32_MAX;
-                    int lo = e0;
-                    bool found = false;
-                    for (int i = 0; i < kDsBatch; ++i) {
-                        const int n_le = __popc(__ballot_sync(0xffffffffu, begins <= next + i));
-                        if (lane == i) {
-                            lo = e0 + n_le - 1;
-                            found = n_le < 32;
+                while (at < stop) {
+                    while (at >= e_next) {
+                        ++e;
+                        e_line = a.line[e];
+                        e_next = a.line[e + 1];
+                        if (at < e_next) {
+                            bool bad;
+                            x = ds_entry(a, e, bad);
+                            sz = ds_size(a, x, NK);
                         }
                     }
-                    if (lane < kDsBatch && part < parts) {
-                        if (!found) {
-                            lo = e0;
-                            for (int hi = num; hi - lo > 1;) {
-                                const int mid = (lo + hi) >> 1;
-                                if (a.items[mid] <= part) lo = mid; else hi = mid;
-                            }
-                        }
-                        Group x;
-                        group_at(a.groups, lo, x);
-                        it = item_of(part, x, ds_size(a, x.rows, x.shared, NK, share), a.items[lo], a.line[lo]);
+                    const int off = static_cast<int>(at - e_line), uh = off / sz.unit, o = off - uh * sz.unit;
+                    const int h = uh / sz.units, u = uh - h * sz.units;
+                    const int ch = min(o / (kRun + kDsExtra), sz.chunks - 1), oc = o - ch * (kRun + kDsExtra);
+                    const int tiles = min(kRun, sz.tiles - ch * kRun);
+                    const int64_t begin = at - oc, end = begin + kDsExtra + tiles;
+                    const int64_t upto = min(end, stop);
+                    const int t0 = max(0, oc - kDsExtra), t1 = static_cast<int>(upto - begin) - kDsExtra;
+                    at = upto;
+                    if (t1 <= t0) continue;
+                    const bool group = e < a.num_groups;
+                    it.b = x.b;
+                    it.row = x.row + u * 2 * P;
+                    it.rows = x.rows - u * 2 * P;
+                    it.h = h;
+                    it.key = x.key + (ch * kRun + t0) * NK;
+                    it.end = x.end;
+                    it.tiles = t1 - t0;
+                    it.pair = it.rows > P;
+                    it.cap = group ? a.group_rows : a.seq_rows;
+                    const int64_t place = a.items[e] + uh * sz.chunks + ch + static_cast<int>(blockIdx.x);
+                    it.part = group ? place * 2 * a.group_rows : a.seq_part0 + (place - group_parts) * 2 * a.seq_rows;
+                    break;
+                }
+                return it;
+            };
+            auto publish = [&](int n, const DsItem& item) {
+                int ok = 1;
+                if (lane == 0) {
+                    if (n >= kDsInfo) ok = wait(&sm.info_empty[n % kDsInfo], ((n / kDsInfo) - 1) & 1);
+                    if (ok) {
+                        sm.info[n % kDsInfo] = item;
+                        mbar_arrive(&sm.info_full[n % kDsInfo]);
                     }
                 }
-                more = __popc(__ballot_sync(0xffffffffu, it.b >= 0)) == kDsBatch;
-                next += kDsBatch;
-                if (lane < kDsBatch) sm.info[n & 1][lane] = it;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.info_full[n & 1]);
-                return true;
-            };
-            constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
-            // the cache row of the lane's block of tiles j0 .. of an item, loaded before they are needed
-            auto rows_of = [&](const DsItem& x, int j0) {
-                int64_t row = a.cache_tokens;  // past the end: a box past the cache is zeros
-                const int t = x.key + j0 * NK + lane * kBlock;
-                if (x.b >= 0 && lane < NK / kBlock * (x.tiles - j0) && t < x.end) {
-                    row = block_row(a.cache, x.b, t);
-                    if (row < 0) {  // page outside the pool
-                        atomicOr(&sm.err, kErrBadMetadata);
-                        row = a.cache_tokens;
-                    }
-                }
-                return row;
-            };
-            bool alive = true;
-            // the item at k, and the first cache rows of the one behind it (loaded an item ahead; none where the batch with it
-            // is not there yet)
-            auto item_at = [&](int k, DsItem& x) {
-                if (half) {
-                    x = sm.info[(k / kDsBatch) & 1][k % kDsBatch];
-                    return true;
-                }
-                if (!__all_sync(0xffffffffu, next_item(k, x))) return false;
-                __syncwarp();
-                if (lane == 0) passed(k, x);
-                return true;
+                return __shfl_sync(0xffffffffu, ok, 0) != 0;
             };
             DsItem item, after;
-            if (half) alive = publish(0);
-            if (alive) alive = item_at(0, item);
-            int64_t row_next = alive ? rows_of(item, 0) : 0;
-            for (int k = 0; alive && item.b >= 0; ++k) {
-                int64_t row = row_next;
-                // the next batch in the middle of this one: its place is free by then
-                if (half && k % kDsBatch == kDsBatch / 2 && more && !publish(k / kDsBatch + 1)) break;
-                if (!half) {
+            if (half) {
+                after = find();
+                alive = publish(0, after);
+            }
+            for (int k = 0; alive; ++k) {
+                if (half) {
+                    item = after;
+                    if (item.b < 0) break;
+                    after = find();  // (ahead of this item's copies)
+                    alive = publish(k + 1, after);
+                    if (!alive) break;
+                } else {
+                    alive = __all_sync(0xffffffffu, next_item(k, item));
+                    if (!alive) break;
+                    __syncwarp();
+                    if (lane == 0) passed(k);
+                    if (item.b < 0) break;
                     int ok = 1;
                     if (lane == 0) {
                         for (int s = 0; s < (item.pair ? 2 : 1); ++s) {
@@ -472,15 +388,23 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                         }
                     }
                     alive = __shfl_sync(0xffffffffu, ok, 0) != 0;
-                    if (!alive) break;
                 }
-                alive = item_at(k + 1, after);
-                if (!alive) break;
-                row_next = item.tiles > kBatch ? rows_of(item, kBatch) : rows_of(after, 0);
+                // the value tile that holds the end of the keys, if its last block is not wholly theirs
+                const int fix = item.end % kBlock != 0 && item.key + item.tiles * NK >= item.end ? item.tiles - 1 : -1;
+                constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
+                int64_t row = 0;
+                int fix_slot = 0, fix_row = 0, fix_copy = 0;
                 for (int j = 0; alive && j < item.tiles; ++j) {
-                    if (j > 0 && j % kBatch == 0) {
-                        row = row_next;
-                        row_next = j + kBatch < item.tiles ? rows_of(item, j + kBatch) : rows_of(after, 0);
+                    if (j % kBatch == 0) {
+                        const int t = item.key + j * NK + lane * kBlock;
+                        row = a.cache_tokens;  // past the end: a box past the cache is zeros
+                        if (lane < NK / kBlock * (item.tiles - j) && t < item.end) {
+                            row = block_row(a.cache, item.b, t);
+                            if (row < 0) {  // page outside the pool
+                                atomicOr(&sm.err, kErrBadMetadata);
+                                row = a.cache_tokens;
+                            }
+                        }
                     }
                     const int set = item.pair ? 0 : 1 + (j & 1);
 #pragma unroll
@@ -491,7 +415,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                         for (int c = 0; c < NK / kBlock; ++c) r[c] = __shfl_sync(0xffffffffu, row, (j % kBatch) * (NK / kBlock) + c);
                         int ok = 1;
                         if (lane == 0) {
-                            uint64_t* bar = &sm.full[set][copy % kStages];
+                            uint64_t* bar = kind == 1 && j == fix ? &sm.v_last[st] : &sm.full[set][copy % kStages];
                             if (slot >= kStages) ok = wait(&sm.empty[st], ((slot / kStages) - 1) & 1);
                             if (ok) {
                                 if (set > 0 && !half) mbar_arrive(&sm.empty[st]);  // (for the stage that does not take the tile)
@@ -502,6 +426,9 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                                                 item.h, static_cast<int>(r[c]));
                             }
                         }
+                        fix_slot = st;
+                        fix_row = set;
+                        fix_copy = copy;
                         ++slot;
                         if (set == 0) ++sent[0];
                         else if (set == 1) ++sent[1];
@@ -512,9 +439,24 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                         }
                     }
                 }
-                item = after;
+                if (half && fix >= 0 && alive) {  // ---- values past the end become zero (they may be anything; the last copy is theirs)
+                    alive = __all_sync(0xffffffffu, wait(&sm.v_last[fix_slot], fixed >> fix_slot & 1));
+                    if (!alive) break;
+                    fixed ^= 1u << fix_slot;
+                    for (int y = (item.end - item.key - fix * NK) * 16 + lane; y < NK * 16; y += 32) {
+                        const int key = y >> 4, c = y & 15;  // (a whole row: no swizzle to undo)
+                        *reinterpret_cast<uint4*>(sm.ring[fix_slot] + (c >> 3) * kHalf + key * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        uint64_t* bar = &sm.full[fix_row][fix_copy % kStages];
+                        mbar_arrive(bar);
+                        mbar_arrive(bar);
+                    }
+                }
             }
-            if (lane == 0 && !half) {  // no copy in flight at the end
+            if (lane == 0 && !half) {  // no copy in flight at the end (a last value tile's barrier was warp 10's to wait for)
                 for (int s = 0; s < 2; ++s) {
                     const int used = s ? q_used[1] : q_used[0];
                     if (used > 0) wait(&sm.q_full[s], (used - 1) & 1);
@@ -531,17 +473,17 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                 const uint64_t qd0 = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024), qd1 = smem_desc_sw128(smem_u32(sm.q[1]), 16, 1024);
                 const uint64_t kd = smem_desc_sw128(smem_u32(sm.ring[0]), 16, 1024);
                 const uint64_t vd = smem_desc_sw128(smem_u32(sm.ring[0]), kHalf, 1024);
-                // running: ring slots, the stage's tiles, turns taken, pairs, copies seen of pairs and of alternate tiles, query buffers
-                int slots = 0, tiles = 0, turns = 0, pairs = 0, seen[2] = {0, 0}, q_used[2] = {0, 0};
+                // running: ring slots, the stage's tiles, turns taken, copies seen of pairs and of alternate tiles, query buffers
+                int slots = 0, tiles = 0, turns = 0, seen[2] = {0, 0}, q_used[2] = {0, 0};
                 bool ok = true, issued = false;
                 for (int k = 0; ok; ++k) {
                     DsItem item;
                     ok = next_item(k, item);
                     if (!ok) break;
-                    passed(k, item);
+                    passed(k);
                     if (item.b < 0) break;
+                    const int count = count_of(item, s), step = item.pair ? 1 : 2, j0 = item.pair ? 0 : s;
                     const bool pair = item.pair;
-                    const int count = item.count(s), step = pair ? 1 : 2, j0 = pair ? 0 : s;
                     const int row = pair ? 0 : 1 + s;
                     auto landed = [&]() {  // the stage's next copy
                         int& n = pair ? seen[0] : seen[1];
@@ -586,8 +528,8 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                     } else {
                         free_q(false);
                     }
-                    // the other stage is through with its last pair: its turns have been taken
-                    if (pair && pairs > 0) ok = wait(&sm.pair_done, (pairs - 1) & 1);
+                    // the other stage is through with its last item: its turns have been taken
+                    if (k > 0) ok = wait(&sm.item_done, (k - 1) & 1);
                     for (int c = 0; ok && c < count; ++c) {
                         // pairs take turns: values of tile c, scores of the next (whatever can be waited for is, first)
                         const int j = j0 + step * c;
@@ -633,10 +575,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                     }
                     slots += 2 * item.tiles;
                     tiles += count;
-                    if (pair) {
-                        ++pairs;
-                        if (ok) mbar_arrive(&sm.pair_done);
-                    }
+                    if (ok) mbar_arrive(&sm.item_done);
                 }
                 if (issued) {  // every matrix instruction done before tensor memory is given back
                     tc_commit(&sm.drain[s]);
@@ -659,11 +598,10 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
             alive = __all_sync(0xffffffffu, next_item(k, item));
             if (!alive) break;
             __syncwarp();
-            if (lane == 0) passed(k, item);
+            if (lane == 0) passed(k);
             if (item.b < 0) break;
-            const bool pair = item.pair;
-            const int count = item.count(s);
-            const int rows = min(item.rows - (pair ? s * P : 0), P) * a.G;       // of the M tile
+            const int count = count_of(item, s);
+            const int rows = min(item.rows - (item.pair ? s * P : 0), P) * a.G;  // of the M tile
             const bool mine = m < rows, busy = (m & ~31) < rows;                 // busy: some row of the warp is
             float top = -INFINITY, sum = 0.f;         // maximum in use (log2 domain), sum of weights
             float acc[kParts > 1 ? kHeadDim : 1];     // fp32 outputs: O of the row
@@ -695,7 +633,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                 }
             };
             for (int c = 0; alive && c < count; ++c) {
-                const int t0 = item.key + (pair ? c : 2 * c + s) * NK;
+                const int t0 = item.key + (item.pair ? c : 2 * c + s) * NK;
                 alive = __all_sync(0xffffffffu, wait(&sm.s_full[s], (tiles + c) & 1));
                 if (!alive) break;
                 if (!busy) {  // (the tile's other warps have rows)
@@ -841,7 +779,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
             if (!busy) continue;
             // ---------------- the part: O, maximum, sum
             tc_fence_after();
-            const int64_t row0 = item.part + s * a.stage_rows;
+            const int64_t row0 = item.part + s * item.cap;
             float4* dst = reinterpret_cast<float4*>(a.part_o) + row0 * (kHeadDim / 4) + m;
             if (count > 0) {
                 collect();
@@ -858,7 +796,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                     if (mine) {
 #pragma unroll
                         for (int d = 0; d < 8; ++d)
-                            dst[static_cast<int64_t>(8 * q + d) * a.stage_rows] = make_float4(y[4 * d], y[4 * d + 1], y[4 * d + 2], y[4 * d + 3]);
+                            dst[static_cast<int64_t>(8 * q + d) * item.cap] = make_float4(y[4 * d], y[4 * d + 1], y[4 * d + 2], y[4 * d + 3]);
                     }
                     __syncwarp();  // the next load is the whole warp's
                 }
@@ -877,177 +815,160 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
     if (tid == 0) a.err_slots[blockIdx.x] = sm.err;
 }
 
-// Joins the parts of a row's pairs of KV head h.  CTA (row, h, z): a share of the 128 dimensions, a thread 4 kD4 of them of
-// one query head.  kDjList parts at a time: one warp finds where they are, the threads fetch their maxima and sums together,
-// then every thread what has a weight, eight in flight.  What bounds it is that chain of loads.
-constexpr int kDjThreads = 128;
-constexpr int kDjList = 64;
-struct DjPart {
-    int64_t row, at;  // query head 0: its row for maximum and sum, its first four dimensions of O (in fours)
-    int run;          // fours from one run of four dimensions to the next: the rows of a stage; own positions 1
-    int first, end;   // query heads that it has
-};
-template <int kD4>
-__global__ void __launch_bounds__(kDjThreads, 5) dense_shared_join(const __grid_constant__ SharedArgs a, int grid, int own_grid, int NK) {
-    __shared__ DjPart part[kDjList];
-    __shared__ float2 part_ml[kDjList][kMaxGroup];  // maximum and sum
-    __shared__ int found;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y, r = blockIdx.x;
+// Joins the parts of a row's pairs of KV head h with the row's own keys.  CTA (row, h, z): quarter, half or all of the 128
+// dimensions, a thread 4 of them of one query head.
+template <bool kInt8>
+__global__ void __launch_bounds__(512) dense_shared_join(const SharedArgs a, int grid, int NK) {
+    __shared__ float own[kMaxGroup][kDecodeMaxRows];  // scores of the row's own keys (log2 domain)
+    __shared__ int64_t own_row[kDecodeMaxRows];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, h = blockIdx.y, r = blockIdx.x;
+    // ---- the row's sequence: the last that begins at or before it, 32 candidates at a time
+    int lo = 0, hi = a.num_seqs;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.cu_rows[at] <= r);
+        const int last = le ? 31 - __clz(le) : 0;
+        lo += last * step;
+        hi = min(lo + step, hi);
+    }
+    int g;
+    bool bad;
+    const DsEntry x = ds_seq(a, lo, g, bad);
+    bool there = x.rows > 0 && r >= x.row && r < x.row + x.rows;
+    const int keys = there ? r - x.row + 1 : 0;  // its own: x.end .. x.end + keys - 1
+    if (tid < kDecodeMaxRows) {
+        int64_t row = 0;
+        if (tid < keys) {
+            const int t = x.end + tid;
+            row = block_row(a.cache, x.b, t & ~(kBlock - 1));
+            if (row >= 0) row = (row + (t & (kBlock - 1))) * a.H + h;
+        }
+        own_row[tid] = row;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int32_t* segs = a.own_units + a.groups.num_seqs + 1;
-    if (r == 0 && h == 0 && blockIdx.z == 0 && warp == 1) {  // what the CTAs found wrong
+    if (r == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the CTAs found wrong
         uint32_t e = 0;
         for (int c = lane; c < grid; c += 32) e |= a.err_slots[c];
-        for (int c = lane; c < own_grid; c += 32) e |= a.own_err_slots[c];
         e = __reduce_or_sync(0xffffffffu, e);
         if (lane == 0) *a.err = e;
     }
-    const int64_t line = a.line[a.groups.num];
-    const int share = static_cast<int>(a.line[a.groups.num + 1]), all_parts = a.items[a.groups.num];
-    const int64_t own_units = a.own_units[a.groups.num_seqs], own_segs = segs[a.groups.num_seqs];
-    const DsRow w = a.rows[r];
-    // (sequences whose rows overlap may have written a record together: nothing is read outside the buffers all the same)
-    if (w.seq < 0 || w.seq >= a.groups.num_seqs || w.group >= a.groups.num || w.rows > kDecodeMaxRows || r < w.row || r - w.row >= w.rows) return;
-    if (all_parts > a.parts_most) return;
-    constexpr int kD4s = kHeadDim / 4 / kD4;  // threads a query head, all CTAs of the row together
-    const int per = kD4s / gridDim.z;
-    const bool busy = tid < a.G * per;
-    const int gh = busy ? tid % a.G : 0, d4 = (busy ? tid / a.G : 0) + blockIdx.z * per;  // the thread's: d4 + i kD4s
-    const DsSize size = ds_size(a, w.group >= 0 ? w.group_rows : 0, w.shared, NK, share);
-    const int chunks = size.units > 0 ? size.chunks : 0;
-    float top = -INFINITY, sum = 0.f;
-    float4 o[kD4];
+    __syncthreads();
 #pragma unroll
-    for (int d = 0; d < kD4; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // what is to be listed: a lane a chunk of the group's, then two tiles of 16 (row, head) pairs of its own positions
-    for (int n0 = 0, n = kDjList; n == kDjList; n0 += kDjList) {  // parts n0 .. of the row's
-        if (warp == 0) {
-            int before = 0;
-            for (int c0 = 0; c0 < chunks + 2 && before < n0 + kDjList; c0 += 32) {
-                const int c = c0 + lane, i = r - w.row;
-                int count = 0;
-                int64_t step = 0;
-                DjPart x{0, 0, 1, 0, a.G};
-                if (c < chunks) {
-                    const int at = r - w.group_row, P = 128 / a.G, tile = at / P, u = tile / 2, shares = ds_shares(line, grid);
-                    const bool pair = w.group_rows - u * 2 * P > P;
-                    const int64_t t0 = a.line[w.group] + size.place(h, c, u);
-                    const int from = ds_owner(line, t0, shares), to = ds_owner(line, t0 + (size.length(c) - 1) * size.weight, shares);
-                    const int64_t place = static_cast<int64_t>(a.items[w.group]) + size.part(h, c, u) + from;
-                    const int64_t row0 = place * 2 * a.stage_rows + (pair ? (tile & 1) * a.stage_rows : 0);
-                    count = (to - from + 1) * (pair ? 1 : 2);
-                    step = pair ? 2 * a.stage_rows : a.stage_rows;
-                    x.row = row0 + (at - tile * P) * a.G;
-                    x.at = row0 * (kHeadDim / 4) + (at - tile * P) * a.G;
-                    x.run = a.stage_rows;
-                    if (at < 0 || at >= w.group_rows || row0 < 0 || row0 + static_cast<int64_t>(count) * step > a.part_rows) count = 0;
-                } else if (c < chunks + 2) {
-                    const int mt = i * a.G / 16 + c - chunks, tiles = (w.rows * a.G + 15) / 16, first = mt * 16 - i * a.G;
-                    x.first = max(0, first);
-                    x.end = min(a.G, first + 16);
-                    if (mt < tiles && x.first < x.end && w.blocks > 0) {
-                        const int extra = dd_extra(a.kv_int8);
-                        const int64_t total = own_units * a.H, own_line = total + own_segs * extra;
-                        const int shares = dd_shares(total, own_grid), n_seg = w.blocks * a.H, seg = segs[w.seq] + mt;
-                        const int64_t at = static_cast<int64_t>(a.own_units[w.seq]) * a.H + static_cast<int64_t>(segs[w.seq]) * extra +
-                                           static_cast<int64_t>(mt) * (n_seg + extra);
-                        const int from = dd_div((at + 1) * shares - 1, own_line - extra), to = dd_div((at + n_seg) * shares - 1, own_line - extra);
-                        const int64_t row0 = ((static_cast<int64_t>(seg) + from) * a.H + h) * 16;
-                        count = to - from + 1;
-                        step = 16 * a.H;
-                        x.row = row0 - first;
-                        x.at = x.row * (kHeadDim / 4);
-                        if (row0 < 0 || row0 + (count - 1) * step + 16 > a.own_rows) count = 0;
+    for (int i = 0; i < kDecodeMaxRows; ++i) there &= own_row[i] >= 0;
+    if (!there) return;
+    const int entries = a.num_groups + a.num_seqs, group_parts = a.items[a.num_groups];
+    const int64_t line = a.line[entries];
+    if (group_parts > a.group_parts_most || a.items[entries] - group_parts > a.seq_parts_most) return;
+    const int64_t q_row = (static_cast<int64_t>(r) * a.H + h) * a.G;
+    for (int i = warp; i < a.G * keys; i += warps) {
+        const int gh = i / keys, key = i - gh * keys;
+        const uint2 qw = *reinterpret_cast<const uint2*>(a.q + (q_row + gh) * kHeadDim + 4 * lane);
+        float k[4], f = a.scale_log2;
+        if constexpr (kInt8) {
+            const char4 w = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.k) + own_row[key] * kHeadDim + 4 * lane);
+            k[0] = w.x, k[1] = w.y, k[2] = w.z, k[3] = w.w;
+            f *= a.k_scale[own_row[key]];
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.k) + own_row[key] * kHeadDim + 4 * lane);
+            k[0] = bf16_lo(w.x), k[1] = bf16_hi(w.x), k[2] = bf16_lo(w.y), k[3] = bf16_hi(w.y);
+        }
+        float y = fmaf(bf16_lo(qw.x), k[0], fmaf(bf16_hi(qw.x), k[1], fmaf(bf16_lo(qw.y), k[2], bf16_hi(qw.y) * k[3])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (lane == 0) own[gh][key] = y * f;
+    }
+    __syncthreads();
+    const int d4s = kHeadDim / 4 / gridDim.z, gh = tid % a.G, d4 = tid / a.G + blockIdx.z * d4s;
+    if (tid >= a.G * d4s) return;
+    float top = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < keys; ++i) top = fmaxf(top, own[gh][i]);
+    for (int i = 0; i < keys; ++i) {
+        const float y = own[gh][i], w = top == -INFINITY ? (y == y ? 0.f : y) : dp_exp2(y - top);
+        float v[4];
+        if constexpr (kInt8) {
+            const char4 c = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(a.v) + own_row[i] * kHeadDim + 4 * d4);
+            const float f = a.v_scale[own_row[i]];
+            v[0] = c.x * f, v[1] = c.y * f, v[2] = c.z * f, v[3] = c.w * f;
+        } else {
+            const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.v) + own_row[i] * kHeadDim + 4 * d4);
+            v[0] = bf16_lo(c.x), v[1] = bf16_hi(c.x), v[2] = bf16_lo(c.y), v[3] = bf16_hi(c.y);
+        }
+        sum += w;
+        o.x = fmaf(w, v[0], o.x);
+        o.y = fmaf(w, v[1], o.y);
+        o.z = fmaf(w, v[2], o.z);
+        o.w = fmaf(w, v[3], o.w);
+    }
+    // ---- parts of entry e, eight at a time
+    const int shares = ds_shares(line, grid), P = 128 / a.G;
+    auto join = [&](int e, const DsEntry& y, bool group) {
+        const DsSize s = ds_size(a, y, NK);
+        if (s.units == 0) return;
+        const int run = kDsPartKeys / NK, i = r - y.row, tile = i / P, u = tile / 2, uh = h * s.units + u;
+        const bool pair = y.rows - u * 2 * P > P;
+        const int cap = group ? a.group_rows : a.seq_rows, m = (i - tile * P) * a.G + gh;
+        const int stages = pair ? 1 : 2, s0 = pair ? tile & 1 : 0;
+        for (int ch = 0; ch < s.chunks; ++ch) {
+            const int64_t begin = a.line[e] + static_cast<int64_t>(uh) * s.unit + ch * (run + kDsExtra) + kDsExtra;
+            const int tiles = min(run, s.tiles - ch * run);
+            const int c0 = ds_owner(line, begin, shares), c1 = ds_owner(line, begin + tiles - 1, shares);
+            const int64_t place = a.items[e] + uh * s.chunks + ch + c0;
+            const int64_t row0 = (group ? place * 2 * cap : a.seq_part0 + (place - group_parts) * 2 * cap) + s0 * cap;
+            const int count = (c1 - c0 + 1) * stages, step = pair ? 2 * cap : cap;
+            for (int i0 = 0; i0 < count; i0 += 8) {
+                float4 v[8];
+                float2 ml[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int64_t at = row0 + static_cast<int64_t>(min(i0 + q, count - 1)) * step;
+                    ml[q] = *reinterpret_cast<const float2*>(a.part_ml + (at + m) * 2);
+                    v[q] = reinterpret_cast<const float4*>(a.part_o)[at * (kHeadDim / 4) + static_cast<int64_t>(d4) * cap + m];
+                }
+                float most = top;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) most = fmaxf(most, ml[q].x);
+                const float f = top == -INFINITY ? 0.f : dp_exp2(top - most);
+                if (top != -INFINITY) {
+                    sum *= f;
+                    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+                }
+                top = most;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (i0 + q >= count) continue;
+                    // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
+                    const float w = ml[q].x == -INFINITY ? (ml[q].y == ml[q].y ? 0.f : ml[q].y) : dp_exp2(ml[q].x - top);
+                    if (w != 0.f) {
+                        sum = fmaf(w, ml[q].y, sum);
+                        o.x = fmaf(w, v[q].x, o.x);
+                        o.y = fmaf(w, v[q].y, o.y);
+                        o.z = fmaf(w, v[q].z, o.z);
+                        o.w = fmaf(w, v[q].w, o.w);
                     }
                 }
-                int incl = count;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, incl, d);
-                    if (lane >= d) incl += v;
-                }
-                const int first = before + incl - count;
-                for (int q = max(0, n0 - first); q < min(count, n0 + kDjList - first); ++q) {
-                    DjPart y = x;
-                    y.row += q * step;
-                    y.at += q * step * (kHeadDim / 4);
-                    part[first + q - n0] = y;
-                }
-                before += __shfl_sync(0xffffffffu, incl, 31);
-            }
-            if (lane == 0) found = min(kDjList, before - n0);
-        }
-        __syncthreads();
-        n = found;
-        for (int i = tid; i < n * a.G; i += kDjThreads) {
-            const int q = i / a.G, gq = i - q * a.G;
-            const DjPart x = part[q];
-            const float* ml = x.run > 1 ? a.part_ml : a.own_ml;
-            part_ml[q][gq] = gq >= x.first && gq < x.end ? *reinterpret_cast<const float2*>(ml + (x.row + gq) * 2) : make_float2(-INFINITY, 0.f);
-        }
-        __syncthreads();
-        float most = top;
-        for (int i = 0; i < n; ++i) most = fmaxf(most, part_ml[i][gh].x);
-        if (most > top) {
-            const float f = top == -INFINITY ? 0.f : dp_exp2(top - most);
-            if (top != -INFINITY) {
-                sum *= f;
-#pragma unroll
-                for (int d = 0; d < kD4; ++d) o[d] = make_float4(o[d].x * f, o[d].y * f, o[d].z * f, o[d].w * f);
-            }
-            top = most;
-        }
-        constexpr int kAtOnce = 8 / (kD4 > 2 ? 2 : 1);
-        for (int i0 = 0; i0 < n; i0 += kAtOnce) {
-            float4 v[kAtOnce][kD4];
-            float f[kAtOnce], l[kAtOnce];
-#pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
-                const int i = min(i0 + q, n - 1);
-                const float2 ml = part_ml[i][gh];
-                // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
-                f[q] = i0 + q >= n ? 0.f : (ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : dp_exp2(ml.x - top));
-                l[q] = ml.y;
-                const DjPart x = part[i];
-#pragma unroll
-                for (int d = 0; d < kD4; ++d) {
-                    const int c = d4 + d * kD4s;
-                    const float4* src = x.run > 1 ? reinterpret_cast<const float4*>(a.part_o) + x.at + gh + static_cast<int64_t>(c) * x.run
-                                                  : reinterpret_cast<const float4*>(a.own_o) + x.at + gh * (kHeadDim / 4) + c;
-                    if (f[q] != 0.f) v[q][d] = *src;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < kAtOnce; ++q) {
-                if (f[q] == 0.f) continue;
-                sum = fmaf(f[q], l[q], sum);
-#pragma unroll
-                for (int d = 0; d < kD4; ++d) {
-                    o[d].x = fmaf(f[q], v[q][d].x, o[d].x);
-                    o[d].y = fmaf(f[q], v[q][d].y, o[d].y);
-                    o[d].z = fmaf(f[q], v[q][d].z, o[d].z);
-                    o[d].w = fmaf(f[q], v[q][d].w, o[d].w);
-                }
             }
         }
-        __syncthreads();  // before the list is made again
+    };
+    if (g >= 0) {
+        DsEntry y{};
+        int last;
+        bool no;
+        ds_group(a, g, y, last, no);
+        join(g, y, true);
     }
-    if (!busy) return;
+    join(a.num_groups + lo, x, false);
     const float inv = 1.f / sum;
-#pragma unroll
-    for (int d = 0; d < kD4; ++d) {
-        const int64_t at = ((static_cast<int64_t>(r) * a.H + h) * a.G + gh) * kHeadDim + 4 * (d4 + d * kD4s);
-        if (a.out_bf16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-                make_uint2(pack_bf16x2(o[d].x * inv, o[d].y * inv), pack_bf16x2(o[d].z * inv, o[d].w * inv));
-        else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o[d].x * inv, o[d].y * inv, o[d].z * inv, o[d].w * inv);
-    }
+    const int64_t at = (q_row + gh) * kHeadDim + 4 * d4;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
 template <int kParts>
-static cudaError_t launch_shared(const SharedArgs& a, const DenseArgs& own, int grid, int own_grid, cudaStream_t stream) {
+static cudaError_t launch_shared(const SharedArgs& a, int grid, cudaStream_t stream) {
     const size_t smem = sizeof(DsSmem<kParts>) + 1024;
     auto* kernel = dense_shared_kernel<kParts>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
@@ -1063,33 +984,34 @@ static cudaError_t launch_shared(const SharedArgs& a, const DenseArgs& own, int 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, *a.q_map, *a.k_map, *a.v_map, a)) != cudaSuccess) return e;
-    if ((e = run_dense_decode_own(own, own_grid, stream)) != cudaSuccess) return e;
-    // few rows: the dimensions over two or four CTAs a row and head, while all CTAs run at once (five an SM)
-    const int64_t blocks = static_cast<int64_t>(a.groups.total_rows) * a.H, places = 5 * device_sm_count();
-    const int z = blocks * 4 <= places ? 4 : (blocks * 2 <= places ? 2 : 1);
-    cfg.gridDim = dim3(static_cast<unsigned>(a.groups.total_rows), static_cast<unsigned>(a.H), static_cast<unsigned>(z));
-    cfg.blockDim = dim3(kDjThreads, 1, 1);
+    // few rows: the dimensions over several CTAs
+    const int64_t blocks = static_cast<int64_t>(a.total_rows) * a.H;
+    const int z = blocks * 4 <= 2 * device_sm_count() ? 4 : (blocks * 2 <= 2 * device_sm_count() ? 2 : 1);
+    const int threads = (a.G * (kHeadDim / 4 / z) + 31) / 32 * 32;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.total_rows), static_cast<unsigned>(a.H), static_cast<unsigned>(z));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = 0;
-    auto* join = z == 4 ? dense_shared_join<1> : z == 2 ? dense_shared_join<2> : dense_shared_join<4>;
-    return cudaLaunchKernelEx(&cfg, join, a, grid, own_grid, DsCfg<kParts>::NK);
+    auto* join = a.kv_int8 ? dense_shared_join<true> : dense_shared_join<false>;
+    return cudaLaunchKernelEx(&cfg, join, a, grid, DsCfg<kParts>::NK);
 }
 
-SharedRoom dense_shared_room(const GroupArgs& g, int H, int G, int max_rows_per_seq) {
+SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int total_rows, int max_rows_per_seq, int max_group_rows,
+                             int max_shared_len, int max_cache_len) {
     SharedRoom r;
-    const int64_t P = 128 / G, units = g.total_rows / (2 * P) + g.num;
-    // (chunks are at least half a share long where there are more of them than the longest parts make)
-    r.parts = g.max_shared_len < kBlock ? 0 : units * H * ((g.max_shared_len + kDsPartKeys - 1) / kDsPartKeys) + 2 * kDenseMaxShares;
-    r.stage_rows = std::max(2, static_cast<int>(std::min(P, static_cast<int64_t>(g.max_rows)) * G));  // (1 is the mark of own positions)
-    r.rows = (r.parts + kDenseMaxShares) * 2 * r.stage_rows;
-    const int64_t line = units * H * (((g.max_shared_len + 63) / 64) * kDsPairTile + kDsExtra);
-    r.grid = ds_shares(line, std::min(device_sm_count(), kDenseMaxShares));
-    const int64_t tiles = (static_cast<int64_t>(std::min(max_rows_per_seq, kDecodeMaxRows)) * G + 15) / 16;
-    r.own_rows = (g.num_seqs * tiles + kDenseMaxShares) * H * 16;
+    const int64_t P = 128 / G, units = total_rows / (2 * P) + num_groups;
+    auto chunks = [](int64_t keys) { return (keys + kDsPartKeys - 1) / kDsPartKeys; };
+    r.grid = std::min(device_sm_count(), kDenseMaxShares);
+    r.group_parts = max_shared_len < kBlock ? 0 : units * H * chunks(max_shared_len);
+    r.seq_parts = static_cast<int64_t>(num_seqs) * H * chunks(max_cache_len);
+    r.group_rows = static_cast<int>(std::min(P, static_cast<int64_t>(max_group_rows)) * G);
+    r.seq_rows = std::min(max_rows_per_seq, kDecodeMaxRows) * G;
+    r.seq_part0 = (r.group_parts > 0 ? (r.group_parts + kDenseMaxShares) * 2 * r.group_rows : 0);
+    r.rows = r.seq_part0 + (r.seq_parts + kDenseMaxShares) * 2 * r.seq_rows;
     return r;
 }
 
-cudaError_t run_dense_shared(const SharedArgs& a, const DenseArgs& own, int grid, int own_grid, cudaStream_t stream) {
-    return a.out_bf16 ? launch_shared<1>(a, own, grid, own_grid, stream) : launch_shared<3>(a, own, grid, own_grid, stream);
+cudaError_t run_dense_shared(const SharedArgs& a, int grid, cudaStream_t stream) {
+    return a.out_bf16 ? launch_shared<1>(a, grid, stream) : launch_shared<3>(a, grid, stream);
 }
 
 }  // namespace msa

@@ -197,14 +197,6 @@ struct AppendArgs {
 };
 cudaError_t run_append_cache(const AppendArgs& a, cudaStream_t stream);
 
-// Groups of neighbouring sequences whose first positions lie in the same cache rows.
-struct GroupArgs {
-    const int32_t* starts;  // [num + 1] first sequence of each
-    const int32_t* shared;  // [num] positions
-    const int32_t* cu_rows;
-    int num, num_seqs, total_rows, max_rows, max_shared_len;
-};
-
 // Attention over every cached position.
 struct DenseArgs {
     const uint16_t* q;
@@ -242,7 +234,6 @@ struct DenseArgs {
     float* part_o;         // parts of what several CTAs walk: O [.., 128], decode family [2 shares, H, 16]
     float* part_ml;        // and their maxima and sums [.., 2]
     float* aside;          // prompts, windows with bf16 outputs: sums over earlier keys [places][2][130][128]
-    GroupArgs groups;      // run_dense_decode_own
     uint32_t* err_slots;   // [shares] error bits of the decode family's CTAs
     int err_store;         // 1: the combine stores the error word, 0: it adds to it
     uint32_t* err;
@@ -255,46 +246,44 @@ cudaError_t run_dense_prompt(const DenseArgs& a, int items, cudaStream_t stream)
 cudaError_t run_dense_window(const DenseArgs& a, int items, cudaStream_t stream);
 int dense_decode_shares(int64_t units, int H);  // CTAs for so many blocks
 cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream);
-// The decode family's positions behind what its groups share; the parts go to part_o [segment + share, H, 16].
-cudaError_t run_dense_decode_own(const DenseArgs& a, int shares, cudaStream_t stream);
 
-struct DsRow;  // (dense_shared.cu)
-constexpr int kDsRowBytes = 32;
-// Attention over every cached position for a decode family whose groups of sequences share a prefix: the shared positions,
-// and the join with the parts of the others (run_dense_decode_own).
+// Attention over every cached position for a decode family whose groups of sequences share a prefix.
 struct SharedArgs {
-    GroupArgs groups;
-    const int32_t* cache_lens;
+    const uint16_t* q;
+    const void* k;
+    const void* v;
+    const float* k_scale;  // int8 caches: [T, H]
+    const float* v_scale;
     void* out;
+    const int32_t* cu_rows;
+    const int32_t* cache_lens;
+    const int32_t* group_starts;  // [num_groups + 1]
+    const int32_t* group_shared;  // [num_groups]
     CacheRows cache;
-    int H, G, max_rows_per_seq, max_cache_len, kv_int8, out_bf16;
+    int num_seqs, num_groups, H, G, total_rows, max_rows_per_seq, max_group_rows, max_shared_len, max_cache_len, kv_int8, out_bf16;
     int64_t cache_tokens;
     float scale_log2;          // softmax scale * log2(e)
     const CUtensorMap* q_map;  // host copies: q as (D, H*G, rows), box 64 x G x 128 / G; the caches (kv_map)
     const CUtensorMap* k_map;
     const CUtensorMap* v_map;
-    int64_t* line;             // [groups + 2] places of the groups on the line of key tiles; a CTA's share of it
-    int32_t* items;            // [groups + 1] the same of the parts that the line's items make
-    int64_t parts_most;        // parts that there is room for, beside one a CTA
-    int stage_rows;            // rows of a part's stage
-    int64_t part_rows;         // rows of all parts
-    DsRow* rows;               // [total_rows]
-    float* part_o;             // [stages][dim / 4][row][4]
+    int64_t* line;             // [num_groups + num_seqs + 1] places of the groups and the sequences on the line of key tiles
+    int32_t* items;            // the same of the parts that the line's items make
+    int64_t group_parts_most, seq_parts_most;  // parts that there is room for, beside one a CTA
+    int group_rows, seq_rows;  // rows of a part's stage: of a group's items, of a sequence's
+    int64_t seq_part0;         // first row of the sequences' parts
+    float* part_o;             // [rows of a stage: dim / 4][row][4]
     float* part_ml;            // [rows][2] maximum (log2 domain) and sum
-    const int32_t* own_units;  // of run_dense_decode_own: unit_prefix
-    const float* own_o;        // its parts [segment + share, H, 16][dim]
-    const float* own_ml;
-    int64_t own_rows;
-    const uint32_t* own_err_slots;
     uint32_t* err_slots;       // [grid]
     uint32_t* err;             // stored by the join
 };
 struct SharedRoom {
-    int grid = 0, stage_rows = 0;                // CTAs
-    int64_t parts = 0, rows = 0, own_rows = 0;
+    int grid = 0;  // CTAs
+    int64_t group_parts = 0, seq_parts = 0, seq_part0 = 0, rows = 0;
+    int group_rows = 0, seq_rows = 0;
 };
-SharedRoom dense_shared_room(const GroupArgs& g, int H, int G, int max_rows_per_seq);
-cudaError_t run_dense_shared(const SharedArgs& a, const DenseArgs& own, int grid, int own_grid, cudaStream_t stream);
+SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int total_rows, int max_rows_per_seq, int max_group_rows,
+                             int max_shared_len, int max_cache_len);
+cudaError_t run_dense_shared(const SharedArgs& a, int grid, cudaStream_t stream);
 
 // Allocation-free decode attention: scratch in a file-scope device array
 // sized for at most kNoAllocMaxPairs (sequence, KV head) pairs per call.

@@ -334,50 +334,27 @@ DenseLayout dense_layout(const msa_problem* p, const DensePlan& d) {
 // Groups that share a prefix: msa_dense_forward runs on kernels of its own.
 bool dense_shared(const msa_problem* p) { return p->num_groups > 0 && p->kv_dtype == MSA_KV_BF16; }
 
-msa::GroupArgs groups_of(const msa_problem* p) {
-    msa::GroupArgs g{};
-    g.starts = p->group_starts;
-    g.shared = p->group_shared;
-    g.cu_rows = p->cu_rows;
-    g.num = p->num_groups;
-    g.num_seqs = p->num_seqs;
-    g.total_rows = p->total_rows;
-    g.max_rows = p->max_group_rows;
-    g.max_shared_len = p->max_shared_len;
-    return g;
-}
-
 struct SharedLayout {
     msa::SharedRoom room;
-    size_t err = 0, err_slots = 0, own_err_slots = 0, line = 0, items = 0, units = 0, rows = 0, part_ml = 0, part_o = 0, own_ml = 0,
-           own_o = 0, total = 0;
+    size_t err = 0, err_slots = 0, line = 0, items = 0, part_ml = 0, part_o = 0, total = 0;
 };
 
 SharedLayout shared_layout(const msa_problem* p) {
     SharedLayout l;
-    l.room = msa::dense_shared_room(groups_of(p), p->num_kv_heads, p->group_size, p->max_rows_per_seq);
-    const size_t rows = static_cast<size_t>(l.room.rows), own = static_cast<size_t>(l.room.own_rows);
+    l.room = msa::dense_shared_room(p->num_seqs, p->num_groups, p->num_kv_heads, p->group_size, p->total_rows, p->max_rows_per_seq,
+                                    p->max_group_rows, p->max_shared_len, p->max_cache_len);
+    const size_t entries = static_cast<size_t>(p->num_groups) + p->num_seqs + 1, rows = static_cast<size_t>(l.room.rows);
     size_t off = 256;
     l.err_slots = off;
     off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
-    l.own_err_slots = off;
-    off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
     l.line = off;
-    off = align256(off + (static_cast<size_t>(p->num_groups) + 2) * sizeof(int64_t));
+    off = align256(off + entries * sizeof(int64_t));
     l.items = off;
-    off = align256(off + (static_cast<size_t>(p->num_groups) + 1) * sizeof(int32_t));
-    l.units = off;
-    off = align256(off + 2 * (static_cast<size_t>(p->num_seqs) + 1) * sizeof(int32_t));
-    l.rows = off;
-    off = align256(off + static_cast<size_t>(p->total_rows) * msa::kDsRowBytes);
+    off = align256(off + entries * sizeof(int32_t));
     l.part_ml = off;
     off = align256(off + rows * 2 * sizeof(float));
     l.part_o = off;
     off = align256(off + rows * msa::kHeadDim * sizeof(float));
-    l.own_ml = off;
-    off = align256(off + own * 2 * sizeof(float));
-    l.own_o = off;
-    off = align256(off + own * msa::kHeadDim * sizeof(float));
     l.total = off;
     return l;
 }
@@ -1043,16 +1020,28 @@ static msa_status dense_shared_forward(const msa_problem* p, const void* q, cons
         (s = make_map(&qm, q, 128, static_cast<uint64_t>(p->num_kv_heads) * G, p->total_rows, 64, G, 128 / G, "q")) != MSA_OK)
         return s;
     msa::SharedArgs a{};
-    a.groups = groups_of(p);
-    a.cache_lens = p->cache_lens;
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = k_cache;
+    a.v = v_cache;
+    a.kv_int8 = p->kv_dtype == MSA_KV_INT8;
+    a.k_scale = a.kv_int8 ? p->k_scale : nullptr;
+    a.v_scale = a.kv_int8 ? p->v_scale : nullptr;
     a.out = out;
+    a.out_bf16 = p->out_dtype == MSA_OUT_BF16;
+    a.cu_rows = p->cu_rows;
+    a.cache_lens = p->cache_lens;
+    a.group_starts = p->group_starts;
+    a.group_shared = p->group_shared;
     a.cache = cache_rows_of(p);
+    a.num_seqs = p->num_seqs;
+    a.num_groups = p->num_groups;
     a.H = p->num_kv_heads;
     a.G = p->group_size;
+    a.total_rows = p->total_rows;
     a.max_rows_per_seq = p->max_rows_per_seq;
+    a.max_group_rows = p->max_group_rows;
+    a.max_shared_len = p->max_shared_len;
     a.max_cache_len = p->max_cache_len;
-    a.kv_int8 = p->kv_dtype == MSA_KV_INT8;
-    a.out_bf16 = p->out_dtype == MSA_OUT_BF16;
     a.cache_tokens = p->cache_tokens;
     a.scale_log2 = scale_log2(p);
     a.q_map = &qm;
@@ -1060,53 +1049,16 @@ static msa_status dense_shared_forward(const msa_problem* p, const void* q, cons
     a.v_map = &vm;
     a.line = reinterpret_cast<int64_t*>(ws + l.line);
     a.items = reinterpret_cast<int32_t*>(ws + l.items);
-    a.parts_most = l.room.parts;
-    a.stage_rows = l.room.stage_rows;
-    a.part_rows = l.room.rows;
-    a.rows = reinterpret_cast<msa::DsRow*>(ws + l.rows);
+    a.group_parts_most = l.room.group_parts;
+    a.seq_parts_most = l.room.seq_parts;
+    a.group_rows = l.room.group_rows;
+    a.seq_rows = l.room.seq_rows;
+    a.seq_part0 = l.room.seq_part0;
     a.part_o = reinterpret_cast<float*>(ws + l.part_o);
     a.part_ml = reinterpret_cast<float*>(ws + l.part_ml);
     a.err_slots = reinterpret_cast<uint32_t*>(ws + l.err_slots);
     a.err = reinterpret_cast<uint32_t*>(ws + l.err);
-    // the positions behind what is shared
-    msa::DenseArgs own{};
-    own.groups = a.groups;
-    own.q = static_cast<const uint16_t*>(q);
-    own.k = k_cache;
-    own.v = v_cache;
-    own.kv_int8 = a.kv_int8;
-    own.k_scale = a.kv_int8 ? p->k_scale : nullptr;
-    own.v_scale = a.kv_int8 ? p->v_scale : nullptr;
-    own.out = out;
-    own.out_bf16 = a.out_bf16;
-    own.cu_rows = p->cu_rows;
-    own.cache_lens = p->cache_lens;
-    own.cache = a.cache;
-    own.num_seqs = p->num_seqs;
-    own.H = a.H;
-    own.G = a.G;
-    own.total_rows = p->total_rows;
-    own.max_rows_per_seq = p->max_rows_per_seq;
-    own.max_cache_len = p->max_cache_len;
-    own.cache_tokens = p->cache_tokens;
-    own.scale_log2 = a.scale_log2;
-    own.window_above = INT32_MAX;
-    own.k_map = &km;
-    own.v_map = &vm;
-    own.unit_prefix = reinterpret_cast<int32_t*>(ws + l.units);
-    own.part_o = reinterpret_cast<float*>(ws + l.own_o);
-    own.part_ml = reinterpret_cast<float*>(ws + l.own_ml);
-    own.err_slots = reinterpret_cast<uint32_t*>(ws + l.own_err_slots);
-    own.err = a.err;
-    a.own_units = own.unit_prefix;
-    a.own_o = own.part_o;
-    a.own_ml = own.part_ml;
-    a.own_rows = l.room.own_rows;
-    a.own_err_slots = own.err_slots;
-    const int64_t tiles = (static_cast<int64_t>(decode_rows_per_seq(p)) * p->group_size + 15) / 16;
-    const int64_t blocks = (p->max_cache_len + msa::kBlock - 1) / msa::kBlock;
-    const int own_grid = msa::dense_decode_shares(p->num_seqs * tiles * blocks, p->num_kv_heads);
-    const cudaError_t e = msa::run_dense_shared(a, own, l.room.grid, own_grid, st);
+    const cudaError_t e = msa::run_dense_shared(a, l.room.grid, st);
     return e == cudaSuccess ? MSA_OK : cuda_fail(e, "shared-prefix attention launch");
 }
 

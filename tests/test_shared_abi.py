@@ -34,12 +34,12 @@ def test_groups_checked_on_host(over, status):
 
 
 def test_the_dense_workspace_holds_the_parts():
-    """Two parts of max_group_rows x G rows for each item of a group's prefix, 16 rows for each head and sequence,
-    520 bytes a row."""
+    """Two parts of max_group_rows x G rows for each item of a group's prefix, two of max_rows_per_seq x G for each of a
+    sequence's own positions, 520 bytes a row."""
     import block_sparse_attention_index_gb300 as m
     L, n = m.lib(), C.c_size_t(0)
     assert L.msa_dense_workspace_size(C.byref(_groups()), C.byref(n)) == 0
-    rows = 2 * (2 * 4 * 2 * 16) + 3 * 4 * 16
+    rows = 2 * (2 * 4 * 2 * 16) + 3 * 4 * 2 * 16
     assert n.value >= rows * 520
     f, o, ws = C.c_void_p(FAKE), C.c_void_p(2 * FAKE), C.c_void_p(1 << 20)
     p = _groups()
