@@ -37,7 +37,7 @@ namespace msa {
 constexpr int kDsThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 and 10 copies, 9 and 11 matrix instructions
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
 constexpr int kDsPartKeys = 32768;  // most keys of a part
-constexpr int kDsExtra = 3;         // tiles that an item counts for besides its own
+constexpr int kDsExtra = 2;         // tiles that an item counts for besides its own
 constexpr int kDsInfo = 4;          // items published ahead
 constexpr float kDsSlack = 8.f;     // log2 by which the running maximum may lag
 
@@ -365,9 +365,6 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                 if (half) {
                     item = after;
                     if (item.b < 0) break;
-                    after = find();  // (ahead of this item's copies)
-                    alive = publish(k + 1, after);
-                    if (!alive) break;
                 } else {
                     alive = __all_sync(0xffffffffu, next_item(k, item));
                     if (!alive) break;
@@ -395,6 +392,11 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                 int64_t row = 0;
                 int fix_slot = 0, fix_row = 0, fix_copy = 0;
                 for (int j = 0; alive && j < item.tiles; ++j) {
+                    if (half && j == min(2, item.tiles - 1)) {  // the next item (its search takes loads: behind the first copies)
+                        after = find();
+                        alive = publish(k + 1, after);
+                        if (!alive) break;
+                    }
                     if (j % kBatch == 0) {
                         const int t = item.key + j * NK + lane * kBlock;
                         row = a.cache_tokens;  // past the end: a box past the cache is zeros
@@ -817,8 +819,8 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
 
 // Joins the parts of a row's pairs of KV head h with the row's own keys.  CTA (row, h, z): quarter, half or all of the 128
 // dimensions, a thread 4 of them of one query head.
-template <bool kInt8>
-__global__ void __launch_bounds__(512) dense_shared_join(const SharedArgs a, int grid, int NK) {
+template <bool kInt8, int kResident>
+__global__ void __launch_bounds__(512, kResident) dense_shared_join(const SharedArgs a, int grid, int NK) {
     __shared__ float own[kMaxGroup][kDecodeMaxRows];  // scores of the row's own keys (log2 domain)
     __shared__ int64_t own_row[kDecodeMaxRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, h = blockIdx.y, r = blockIdx.x;
@@ -901,7 +903,7 @@ __global__ void __launch_bounds__(512) dense_shared_join(const SharedArgs a, int
         o.z = fmaf(w, v[2], o.z);
         o.w = fmaf(w, v[3], o.w);
     }
-    // ---- parts of entry e, eight at a time
+    // ---- parts of entry e, some at a time
     const int shares = ds_shares(line, grid), P = 128 / a.G;
     auto join = [&](int e, const DsEntry& y, bool group) {
         const DsSize s = ds_size(a, y, NK);
@@ -917,18 +919,19 @@ __global__ void __launch_bounds__(512) dense_shared_join(const SharedArgs a, int
             const int64_t place = a.items[e] + uh * s.chunks + ch + c0;
             const int64_t row0 = (group ? place * 2 * cap : a.seq_part0 + (place - group_parts) * 2 * cap) + s0 * cap;
             const int count = (c1 - c0 + 1) * stages, step = pair ? 2 * cap : cap;
-            for (int i0 = 0; i0 < count; i0 += 8) {
-                float4 v[8];
-                float2 ml[8];
+            constexpr int kAtOnce = kResident > 1 ? 4 : 8;
+            for (int i0 = 0; i0 < count; i0 += kAtOnce) {
+                float4 v[kAtOnce];
+                float2 ml[kAtOnce];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < kAtOnce; ++q) {
                     const int64_t at = row0 + static_cast<int64_t>(min(i0 + q, count - 1)) * step;
                     ml[q] = *reinterpret_cast<const float2*>(a.part_ml + (at + m) * 2);
                     v[q] = reinterpret_cast<const float4*>(a.part_o)[at * (kHeadDim / 4) + static_cast<int64_t>(d4) * cap + m];
                 }
                 float most = top;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) most = fmaxf(most, ml[q].x);
+                for (int q = 0; q < kAtOnce; ++q) most = fmaxf(most, ml[q].x);
                 const float f = top == -INFINITY ? 0.f : dp_exp2(top - most);
                 if (top != -INFINITY) {
                     sum *= f;
@@ -936,7 +939,7 @@ __global__ void __launch_bounds__(512) dense_shared_join(const SharedArgs a, int
                 }
                 top = most;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < kAtOnce; ++q) {
                     if (i0 + q >= count) continue;
                     // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
                     const float w = ml[q].x == -INFINITY ? (ml[q].y == ml[q].y ? 0.f : ml[q].y) : dp_exp2(ml[q].x - top);
@@ -991,7 +994,10 @@ static cudaError_t launch_shared(const SharedArgs& a, int grid, cudaStream_t str
     cfg.gridDim = dim3(static_cast<unsigned>(a.total_rows), static_cast<unsigned>(a.H), static_cast<unsigned>(z));
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = 0;
-    auto* join = a.kv_int8 ? dense_shared_join<true> : dense_shared_join<false>;
+    // two CTAs an SM where they are more than the SMs (256 rows of 4 x 16 heads: 30 us for 58; few rows are slower by 1 to 2)
+    const bool many = blocks > device_sm_count();
+    auto* join = a.kv_int8 ? (many ? dense_shared_join<true, 2> : dense_shared_join<true, 1>)
+                           : (many ? dense_shared_join<false, 2> : dense_shared_join<false, 1>);
     return cudaLaunchKernelEx(&cfg, join, a, grid, DsCfg<kParts>::NK);
 }
 
