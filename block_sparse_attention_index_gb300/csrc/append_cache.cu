@@ -3,6 +3,8 @@
 //   angle_j = 2 pi frac(x turns_j / 2^64),  x = the row's position on axis_j
 //   y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin      for the pair (a, b) of j
 //   bf16 cache: y rounded;  int8: scale = max |y| / 127, codes = rint(y / scale)
+//   int8 index keys: the least e with max |y| <= 127 2^e, codes = rint(y 2^-e): a power of two, so that a code read back
+//   is a bf16 value exactly and the index scores are the same whichever kernel computes them
 // x turns_j is a 64-bit product modulo one turn, so the phase of a far
 // position is as exact as a near one's (fp32 angles lose 0.1 rad at 2^21);
 // its upper 32 bits, as a signed number of half turns, feed sincospi.
@@ -92,6 +94,24 @@ __device__ __forceinline__ uint2 ap_codes(const float (&y)[8], float scale) {
         c[w] = __byte_perm(__byte_perm(__float_as_uint(t[4 * w]), __float_as_uint(t[4 * w + 1]), 0x0040),
                            __byte_perm(__float_as_uint(t[4 * w + 2]), __float_as_uint(t[4 * w + 3]), 0x0040), 0x5410);
     return make_uint2(c[0], c[1]);
+}
+
+// The power of two of an index head from its largest magnitude as bits (not finite: -128): 127 is 1.984375 2^6.
+__device__ __forceinline__ int ap_index_exp(uint32_t top) {
+    if (top >= 0x7f800000u) return -128;
+    return max(static_cast<int>(top >> 23) - 133 + ((top & 0x7fffffu) > 0x7e0000u ? 1 : 0), -126);
+}
+
+// 8 codes of y 2^-e, which is exact and at most 127.
+__device__ __forceinline__ uint2 ap_index_codes(const float (&y)[8], int e) {
+    const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = __float_as_uint(fmaf(y[i], f, 12582912.f));  // 1.5 2^23: an integer in the low bits
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+    return make_uint2(w[0], w[1]);
 }
 
 __global__ void __launch_bounds__(kApThreads, 3) append_cache_kernel(const AppendArgs a, int rows_per_cta, int team) {
@@ -284,9 +304,22 @@ __global__ void __launch_bounds__(kApThreads, 3) append_cache_kernel(const Appen
                         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(k == 1 ? a.k_cache : a.v_cache) + o * kHeadDim + at) = code;
                         if (at == 0) (k == 1 ? a.k_scale : a.v_scale)[o] = scale;
                     }
+                } else if (k == 4 && a.ik_exp != nullptr) {  // the 8 lanes of an index head
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    if (there && row.cache >= 0) {
+                        const int e = ap_index_exp(top);
+                        const int64_t o = row.cache * a.KH + head;
+                        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.ik_cache) + o * kIndexDim + at) =
+                            e == -128 ? make_uint2(0u, 0u) : ap_index_codes(y, e);
+                        if (at == 0) a.ik_exp[o] = static_cast<int8_t>(e);
+                    }
                 } else if (there && (k == 3 || row.cache >= 0)) {
                     uint16_t* dst = k == 3 ? a.iq_out + (r * H + head) * kIndexDim
-                                  : k == 4 ? a.ik_cache + (row.cache * a.KH + head) * kIndexDim
+                                  : k == 4 ? static_cast<uint16_t*>(a.ik_cache) + (row.cache * a.KH + head) * kIndexDim
                                            : static_cast<uint16_t*>(k == 1 ? a.k_cache : a.v_cache) + (row.cache * H + head) * kHeadDim;
                     *reinterpret_cast<uint4*>(dst + at) =
                         turned ? make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),

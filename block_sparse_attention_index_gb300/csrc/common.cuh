@@ -61,6 +61,11 @@ __device__ __forceinline__ void i8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_
     hi = __byte_perm(__float_as_uint(f2), __float_as_uint(f3), 0x7632);
 }
 
+// 2^e of an index key's 8-bit exponent; -128 stands for a key that is not finite.
+__device__ __forceinline__ float index_power(int e) {
+    return e < -126 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
 // One 64-key x 128-dim int8 tile, as TMA lands it with 128-byte swizzle at
 // area + upper, rewritten in place as the bf16 layout the MMAs read: dims
 // 0-63 at area, dims 64-127 at area + upper, each a [key][64 dims] tile with

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kClThreads, 2) decode_cluster_kernel(const __g
         b = blockIdx.z / a.rows_per_seq;
         row_in_seq = blockIdx.z - b * a.rows_per_seq;
     }
-    const int row_slot = b * a.rows_per_seq + row_in_seq;  // the row's pooled-score slot
+    const int row_slot = a.pooled_by_row ? a.cu_rows[b] + row_in_seq : b * a.rows_per_seq + row_in_seq;  // the row's pooled-score slot
 
     // ---- prologue: only inputs that no earlier kernel of the step writes
     const int nrows = a.cu_rows[b + 1] - a.cu_rows[b];

@@ -1,0 +1,413 @@
+// Index scan of the decode family with the block max-pool fused in (as decode_scan.cu), for index keys of 8 bits, and for
+// batches whose groups of sequences share a prefix:
+//     m_j = max_{t in block j, t <= p}  iq[r,h,:] . ik[t,h,:],   ik = code 2^e (8 bits) or bf16
+//
+// Work unit = one 64-position block with all its index heads: of a group's shared positions, for all rows of the group, or
+// of a sequence's own, for its 1 to 8 rows.  The units lie on a line, groups first, a unit for as long as it takes; one CTA
+// per SM takes an even share and streams it through a ring of shared-memory stages (TMA boxes of 64 positions of a head,
+// completing an mbarrier), consumer warp w owns stage w.  Dot products run on mma.sync m16n8k16: A = 16 positions x 16 of
+// the dimensions, held in registers for a whole head, B = eight query rows, taken one group of eight after the other.
+//
+// The order of the dimensions inside a dot product is free: lane `tig` of a row takes the 16 dimensions 16 tig .., which
+// are one 16-byte load of codes, or two of bf16, and two of the queries.  Codes become bf16 exactly (11 instructions for 4);
+// their power of two multiplies the finished scores, position by position, before the maximum: exact too, so that integer
+// scores stay exact and every kernel that reads these keys finds the same maxima.
+//
+// Bound by memory: 65 bytes a position and head with codes, 128 without; a group's are read once instead of once a
+// sequence.  With many rows the products take over: eight rows of a head and a block are 16 mma and about 80 other
+// instructions.
+#include "common.cuh"
+#include "internal.h"
+
+namespace msa {
+
+template <int H, bool kShared, bool kInt8>
+struct IxCfg {
+    static constexpr int kKeyHeads = kShared ? 1 : H;
+    static constexpr int kRowBytes = kInt8 ? kIndexDim : 2 * kIndexDim;
+    static constexpr int kHeadBytes = kBlock * kRowBytes;  // [64 positions][64 dims]
+    static constexpr int kUnitBytes = kKeyHeads * kHeadBytes;
+    static constexpr int kStages = kUnitBytes >= 65536 ? 3 : (kUnitBytes >= 32768 ? 6 : (kUnitBytes >= 16384 ? 10 : 12));  // <= 192 KB of ring
+    static constexpr int kThreads = 32 * (kStages + 1);  // a consumer a stage, and the producer
+};
+
+__device__ __forceinline__ uint4 ix_lds(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void ix_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Entry e of the line: a group's shared positions or (behind the groups) a sequence's own.
+struct IxEntry {
+    int b;            // sequence whose table is read
+    int row, rows;    // query rows
+    int first, units; // blocks [first, first + units)
+    int last;         // position of row 0 (groups: past all of them)
+    int weight;       // of a unit on the line
+};
+
+// Group g; nothing of it is shared where its metadata is bad.
+__device__ __forceinline__ IxEntry ix_group(const IndexScanArgs& a, int g, int& end, bool& bad) {
+    IxEntry x{};
+    const int b0 = a.group_starts[g], b1 = a.group_starts[g + 1], S = a.group_shared[g];
+    end = 0;
+    bad = b0 < 0 || b1 < b0 || b1 > a.num_seqs || S < 0 || S > a.max_shared_len;
+    if (bad) return x;
+    const int c0 = a.cu_rows[b0], c1 = a.cu_rows[b1];
+    bad = c0 < 0 || c1 < c0 || c1 > a.total_rows || c1 - c0 > a.max_group_rows;
+    if (bad) return x;
+    end = b1;
+    x.b = b0;
+    x.row = c0;
+    x.rows = c1 - c0;
+    x.units = x.rows > 0 ? S / kBlock : 0;
+    x.last = 1 << 30;
+    x.weight = 1 + x.rows / 128;  // (about 100 rows of 4 heads take as long as the block's copy)
+    return x;
+}
+
+// Sequence b: no units where it has no rows of this family or its metadata is bad (the attention that follows reports it).
+__device__ __forceinline__ IxEntry ix_seq(const IndexScanArgs& a, int b) {
+    IxEntry x{};
+    const int r = a.cu_rows[b], n = a.cu_rows[b + 1] - r, L = a.cache_lens[b];
+    int shared = 0;
+    if (a.num_groups > 0) {
+        int lo = 0, hi = a.num_groups, end;  // the last group that begins at or before b
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.group_starts[mid] <= b) lo = mid; else hi = mid;
+        }
+        bool bad;
+        const IxEntry g = ix_group(a, lo, end, bad);
+        if (b >= g.b && b < end) shared = g.units;
+    }
+    x.weight = 1;
+    if (n < 1 || n > kDecodeMaxRows || n > a.rows_per_seq || r < 0 || r + n > a.total_rows || L < n || L > a.max_cache_len ||
+        L - n < shared * kBlock || !seq_rows_ok(a.cache, b, L, a.cache_tokens))
+        return x;
+    x.b = b;
+    x.row = r;
+    x.rows = n;
+    x.first = shared;
+    x.units = (L + kBlock - 1) / kBlock - shared;
+    x.last = L - n;
+    return x;
+}
+__device__ __forceinline__ IxEntry ix_entry(const IndexScanArgs& a, int e) {
+    if (e >= a.num_groups) return ix_seq(a, e - a.num_groups);
+    int end;
+    bool bad;
+    return ix_group(a, e, end, bad);
+}
+
+// A warp's place among the CTA's units.
+struct IxPlace {
+    int e = -1, k = 0;  // entry, unit of it
+    int at = 0;         // place on the line
+    IxEntry x{};
+};
+
+template <int H, bool kShared, bool kInt8>
+__global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_scan_kernel(const __grid_constant__ CUtensorMap ik_map,
+                                                                                         const IndexScanArgs a) {
+    using Cfg = IxCfg<H, kShared, kInt8>;
+    constexpr int kStages = Cfg::kStages, kWarps = Cfg::kThreads / 32, KH = Cfg::kKeyHeads;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Cfg::kUnitBytes);
+    uint64_t* empty = full + kStages;
+    int32_t* line = reinterpret_cast<int32_t*>(empty + kStages);  // [entries + 1] places of the entries
+    __shared__ int warp_tot[kWarps];
+    __shared__ uint32_t err;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, entries = a.num_groups + a.num_seqs;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        fence_mbar_init();
+        prefetch_tmap(&ik_map);
+        err = 0;
+    }
+    __syncthreads();
+    // (a programmatic dependent of what precedes it: inputs are read, and anything is written, from here on)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0)  // words that the kernels behind this one count in
+        for (int i = tid; i < a.n_clear; i += Cfg::kThreads) a.clear_words[i] = 0;
+    // exclusive sums over `count` values, in order, kThreads at a time; returns the sum
+    auto scan = [&](int count, auto value, int32_t* to) {
+        int carry = 0;
+        for (int base = 0; base < count; base += Cfg::kThreads) {
+            const int i = base + tid, mine = i < count ? value(i) : 0;
+            int incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane == 31) warp_tot[warp] = incl;
+            __syncthreads();
+            int before = carry;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += warp_tot[w];
+                carry += warp_tot[w];
+            }
+            if (i < count) to[i] = before + incl - mine;
+            __syncthreads();
+        }
+        return carry;
+    };
+    const int total = scan(entries, [&](int e) {
+        const IxEntry x = ix_entry(a, e);
+        return x.units * x.weight;
+    }, line);
+    if (tid == 0) line[entries] = total;
+    if (blockIdx.x == 0) {
+        if (a.drow_prefix != nullptr) {  // rows of the decode family before each sequence, for the attention's grid
+            const int rows = scan(a.num_seqs, [&](int b) {
+                const int n = a.cu_rows[b + 1] - a.cu_rows[b];
+                return n >= 1 && n <= kDecodeMaxRows ? n : 0;
+            }, a.drow_prefix);
+            if (tid == 0) a.drow_prefix[a.num_seqs] = rows;
+        }
+        for (int g = tid; g < a.num_groups; g += Cfg::kThreads) {
+            int end;
+            bool bad;
+            ix_group(a, g, end, bad);
+            if (bad) atomicOr(&err, kErrBadMetadata);
+        }
+        for (int b = tid; b < a.num_seqs && a.num_groups > 0; b += Cfg::kThreads) {  // rows before the end of what is shared
+            const int n = a.cu_rows[b + 1] - a.cu_rows[b];
+            if (n >= 1 && n <= kDecodeMaxRows && ix_seq(a, b).rows == 0) atomicOr(&err, kErrBadMetadata);
+        }
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int from = static_cast<int>(static_cast<int64_t>(total) * blockIdx.x / gridDim.x);
+    const int to = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+    // the first unit that begins in the share, and `steps` units on
+    IxPlace place;
+    auto enter = [&](int e) {
+        place.e = e;
+        place.x = ix_entry(a, e);
+    };
+    auto advance = [&](int steps) {
+        place.k += steps;
+        while (place.k >= place.x.units) {
+            if (place.e + 1 >= entries) {
+                place.at = INT32_MAX;
+                return;
+            }
+            place.k -= place.x.units;
+            enter(place.e + 1);
+        }
+        place.at = line[place.e] + place.k * place.x.weight;
+    };
+    if (from < to) {
+        int lo = 0, hi = entries;  // the last entry that begins at or before the share
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (line[mid] <= from) lo = mid; else hi = mid;
+        }
+        enter(lo);
+        advance((from - line[lo] + place.x.weight - 1) / place.x.weight);
+    } else {
+        place.at = INT32_MAX;
+    }
+
+    if (warp == kStages) {
+        // ---------------- producer: one lane streams units into the ring
+        if (lane == 0) {
+            int i = 0;
+            for (; place.at < to; ++i, advance(1)) {
+                const int s = i % kStages;
+                if (i >= kStages && !mbar_wait(&empty[s], ((i / kStages) - 1) & 1, &err)) break;
+                mbar_arrive_expect_tx(&full[s], Cfg::kUnitBytes);
+                int64_t row = block_row(a.cache, place.x.b, static_cast<int64_t>(place.x.first + place.k) * kBlock);
+                if (row < 0) {  // page outside the pool
+                    atomicOr(&err, kErrBadMetadata);
+                    row = 0;
+                }
+                // whole boxes: what lies past the sequence is masked, past the cache zeros
+#pragma unroll
+                for (int h = 0; h < KH; ++h)
+                    tma_load_3d(ring + s * Cfg::kUnitBytes + h * Cfg::kHeadBytes, &ik_map, &full[s], 0, h, static_cast<int>(row));
+            }
+            // no copy in flight when the CTA ends
+            for (int s = 0; s < kStages && s < i; ++s) mbar_wait(&full[s], ((i - 1 - s) / kStages) & 1, &err);
+        }
+    } else {
+        // ---------------- consumer warp `warp` owns stage `warp`.  Lane (grp, tig) = (lane / 4, lane % 4): of the products' B,
+        // column grp; of the accumulators, positions 16 mt + grp and + 8, columns 2 tig and 2 tig + 1.
+        const int grp = lane >> 2, tig = lane & 3;
+        const uint32_t stage = smem_u32(ring + warp * Cfg::kUnitBytes);
+        // codes: the heads' exponents of positions lane and lane + 32, loaded a unit ahead
+        constexpr int kWords = (KH + 3) / 4;
+        uint32_t ex[2][kWords];
+        auto load_exps = [&]() {
+            if constexpr (kInt8) {
+                if (place.at >= to) return;
+                const int64_t row = block_row(a.cache, place.x.b, static_cast<int64_t>(place.x.first + place.k) * kBlock);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int64_t t = max(row, int64_t{0}) + lane + 32 * y;
+                    const int8_t* src = a.ik_exp + t * KH;
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) ex[y][w] = 0;
+                    if (t >= a.cache_tokens) continue;
+                    if constexpr (KH == 1) ex[y][0] = static_cast<uint8_t>(*src);
+                    else if constexpr (KH == 2) ex[y][0] = *reinterpret_cast<const uint16_t*>(src);
+                    else {
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w) ex[y][w] = reinterpret_cast<const uint32_t*>(src)[w];
+                    }
+                }
+            }
+        };
+        if (place.at < to) advance(warp);
+        load_exps();
+        for (int i = 0; place.at < to; ++i) {
+            const IxEntry x = place.x;
+            const int j = x.first + place.k;
+            uint32_t now[2][kWords];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) now[y][w] = ex[y][w];
+            advance(kStages);
+            load_exps();
+            if (!mbar_wait(&full[warp], i & 1, &err)) break;
+            // columns: kShared one head's, (row, query head) pairs; else the rows of query head h
+            const int columns = kShared ? x.rows * H : x.rows;
+            const int64_t slot = a.by_row ? x.row : static_cast<int64_t>(x.b) * a.rows_per_seq;  // of row 0 among the pooled scores
+#pragma unroll 1
+            for (int h = 0; h < KH; ++h) {
+                uint32_t ka[4][4][4];  // A: [16 positions][16 of the lanes' dims]
+                float power[4][2];
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = mt * 16 + grp + 8 * e;
+                        const uint32_t at = stage + h * Cfg::kHeadBytes + row * Cfg::kRowBytes;
+                        if constexpr (kInt8) {
+                            const uint4 w = ix_lds(at + ((tig ^ ((row >> 1) & 3)) << 4));  // (64-byte swizzle)
+                            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) i8x4_to_bf16x4(ws[kk], ka[mt][kk][e], ka[mt][kk][2 + e]);
+                        } else {
+                            const uint4 w0 = ix_lds(at + (((2 * tig) ^ (row & 7)) << 4)), w1 = ix_lds(at + (((2 * tig + 1) ^ (row & 7)) << 4));
+                            ka[mt][0][e] = w0.x, ka[mt][0][2 + e] = w0.y;
+                            ka[mt][1][e] = w0.z, ka[mt][1][2 + e] = w0.w;
+                            ka[mt][2][e] = w1.x, ka[mt][2][2 + e] = w1.y;
+                            ka[mt][3][e] = w1.z, ka[mt][3][2 + e] = w1.w;
+                        }
+                    }
+                }
+                if constexpr (kInt8) {
+                    // the lane's two positions' powers, then those of the accumulators' positions from their lanes
+                    float mine[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t word = kWords > 1 && h >= 4 ? now[y][kWords - 1] : now[y][0];
+                        mine[y] = index_power(static_cast<int8_t>(word >> (8 * (h & 3))));
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) power[mt][e] = __shfl_sync(0xffffffffu, mine[mt >> 1], (mt & 1) * 16 + grp + 8 * e);
+                }
+                for (int c0 = 0; c0 < columns; c0 += 8) {
+                    const int col = min(c0 + grp, columns - 1);
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        a.iq + (static_cast<int64_t>(x.row) * H + (kShared ? col : static_cast<int64_t>(col) * H + h)) * kIndexDim + 16 * tig);
+                    const uint4 q0 = src[0], q1 = src[1];
+                    const uint32_t qb[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                    float c[4][4];
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt) c[mt][0] = c[mt][1] = c[mt][2] = c[mt][3] = 0.f;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt) ix_mma(c[mt], ka[mt][kk], qb[2 * kk], qb[2 * kk + 1]);
+                    // the lane's columns: rows' visible positions of the block
+                    float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int ce = c0 + 2 * tig + e, seen = x.last + (kShared ? ce / H : ce) + 1 - j * kBlock;
+#pragma unroll
+                        for (int mt = 0; mt < 4; ++mt) {
+                            const int t = mt * 16 + grp;
+                            const float y0 = kInt8 ? c[mt][e] * power[mt][0] : c[mt][e], y1 = kInt8 ? c[mt][2 + e] * power[mt][1] : c[mt][2 + e];
+                            if (t < seen) m[e] = fmaxf(m[e], y0);
+                            if (t + 8 < seen) m[e] = fmaxf(m[e], y1);
+                        }
+                    }
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+                        m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], o));
+                    }
+                    if (grp < 2) {  // lanes 0-3 store the even columns, 4-7 the odd ones
+                        const int ce = c0 + 2 * tig + grp, i_row = kShared ? ce / H : ce;
+                        if (ce < columns && x.last + i_row + 1 > j * kBlock)
+                            a.pooled[(kShared ? slot * H + ce : (slot + ce) * H + h) * a.max_blocks + j] = grp ? m[1] : m[0];
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[warp]);  // stage reusable
+        }
+    }
+    // What was found wrong, into the header that CTA 0 has cleared long since (its first act, this one's last).
+    __syncthreads();
+    if (tid == 0 && err != 0) atomicOr(a.err, err);
+}
+
+template <int H, bool kShared, bool kInt8>
+static cudaError_t launch_index_scan(const IndexScanArgs& a, cudaStream_t stream) {
+    using Cfg = IxCfg<H, kShared, kInt8>;
+    const size_t smem = 1024 + static_cast<size_t>(Cfg::kStages) * Cfg::kUnitBytes + 2 * Cfg::kStages * sizeof(uint64_t) +
+                        static_cast<size_t>(a.num_groups + a.num_seqs + 1) * sizeof(int32_t);
+    auto* kernel = index_scan_kernel<H, kShared, kInt8>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+    int64_t grid = device_sm_count();
+    if (a.unit_bound < grid) grid = a.unit_bound > 0 ? a.unit_bound : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, *a.ik_map, a);
+}
+
+template <int H>
+static cudaError_t launch_index_scan_h(const IndexScanArgs& a, cudaStream_t stream) {
+    if constexpr (H > 1) {
+        if (a.ik_shared) return a.ik_exp ? launch_index_scan<H, true, true>(a, stream) : launch_index_scan<H, true, false>(a, stream);
+    }
+    return a.ik_exp ? launch_index_scan<H, false, true>(a, stream) : launch_index_scan<H, false, false>(a, stream);
+}
+
+cudaError_t run_index_scan(const IndexScanArgs& a, cudaStream_t stream) {
+    switch (a.H) {
+        case 1: return launch_index_scan_h<1>(a, stream);
+        case 2: return launch_index_scan_h<2>(a, stream);
+        case 4: return launch_index_scan_h<4>(a, stream);
+        case 8: return launch_index_scan_h<8>(a, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace msa

@@ -68,6 +68,30 @@ struct ScanArgs {
     uint32_t* err;
 };
 
+// The same for index keys of 8 bits, and for groups of sequences that share a prefix.
+struct IndexScanArgs {
+    const CUtensorMap* ik_map;  // ik as (Di, KH, tokens), box 64 x 1 x 64; int8 codes: bytes, 64-byte swizzle
+    int H, ik_shared;
+    const uint16_t* iq;
+    const int8_t* ik_exp;       // int8 codes: [T, KH]; else nullptr
+    const int32_t* cu_rows;
+    const int32_t* cache_lens;
+    const int32_t* group_starts;  // [num_groups + 1]
+    const int32_t* group_shared;  // [num_groups]
+    CacheRows cache;
+    int num_seqs, num_groups, total_rows, max_cache_len, max_shared_len, max_group_rows, max_blocks;
+    int rows_per_seq;      // pooled row slots per sequence
+    int by_row;            // 1: row r's pooled scores lie at slot r (every sequence is of the decode family)
+    int64_t cache_tokens;
+    int64_t unit_bound;    // upper bound of the number of work units
+    float* pooled;         // [slots, H, max_blocks]
+    int32_t* clear_words;
+    int n_clear;
+    int32_t* drow_prefix;  // nullable
+    uint32_t* err;
+};
+cudaError_t run_index_scan(const IndexScanArgs& a, cudaStream_t stream);
+
 struct DecodeAttendArgs {
     const CUtensorMap* k_map;  // host copies, passed by value to the kernel
     const CUtensorMap* v_map;
@@ -75,6 +99,7 @@ struct DecodeAttendArgs {
     const float* pooled;       // fused path: pooled scores [B * RS, H, max_blocks] (nullptr when sel is given)
     int max_blocks;
     int rows_per_seq;          // RS: pooled slot of row i of sequence b = b * RS + i; grid z = B * RS slots
+    int pooled_by_row;         // 1: pooled slot of row r = r
     const int32_t* drow_prefix;  // fused path, nullable: grid z = decode-family row z, its sequence found in
                                  // this prefix of rows per sequence (written by the scan)
     int decode_rows;             // with drow_prefix: the grid's z extent (host count of decode-family rows)
@@ -101,6 +126,7 @@ struct DecodeAttendArgs {
 
 struct StagedArgs {
     int H, G, top_k, num_seqs, total_rows, max_cache_len;
+    const int8_t* ik_exp;  // int8 index keys: [T, KH]; else nullptr
     int ik_shared;  // index keys per position: 1 (shared) or H
     int64_t cache_tokens;
     const int32_t* cu_rows;
@@ -110,7 +136,8 @@ struct StagedArgs {
 
 struct PrefillIndexArgs {
     const CUtensorMap* iq_map;  // iq as (Di, H, rows)
-    const CUtensorMap* ik_map;  // ik as (Di, KH, tokens), box 64 x 1 x 256 (64 x 1 x 64 when paged)
+    const CUtensorMap* ik_map;  // ik as (Di, KH, tokens), box 64 x 1 x 256 (64 x 1 x 64 when paged); int8 codes: bytes, 64-byte swizzle
+    const int8_t* ik_exp;       // int8 codes: [T, KH]; else nullptr
     int ik_shared;              // KH = 1: every head reads key head 0
     const int32_t* cu_rows;
     const int32_t* cache_lens;
@@ -181,9 +208,9 @@ cudaError_t run_widen_f16(const WidenArgs& a, float2* fac, uint32_t* any_lost, c
 struct AppendArgs {
     const uint16_t *k, *v, *ik, *q, *iq;
     int64_t k_stride, v_stride, ik_stride, q_stride, iq_stride;  // elements
-    void *k_cache, *v_cache;
-    uint16_t* ik_cache;
+    void *k_cache, *v_cache, *ik_cache;
     float *k_scale, *v_scale;
+    int8_t* ik_exp;  // int8 index keys: [T, KH]; else nullptr
     uint16_t *q_out, *iq_out;
     int rope_dim, rope_index_dim, axes, interleaved;
     const uint64_t *turns, *index_turns;
@@ -295,7 +322,7 @@ cudaError_t run_decode_attend(const DecodeAttendArgs& a, cudaStream_t stream);  
 // Cluster form (combine through distributed shared memory); after_scan: launch
 // as a programmatic dependent of the index scan that precedes it.
 cudaError_t run_decode_cluster(const DecodeAttendArgs& a, bool after_scan, cudaStream_t stream);
-cudaError_t run_index_scores(const StagedArgs& a, const uint16_t* iq, const uint16_t* ik, float* scores,
+cudaError_t run_index_scores(const StagedArgs& a, const uint16_t* iq, const void* ik, float* scores,
                              int64_t ld, cudaStream_t stream);
 cudaError_t run_select_blocks(const StagedArgs& a, const float* scores, int64_t ld, int32_t* sel, int32_t* nsel,
                               cudaStream_t stream);

@@ -375,9 +375,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // 3-D tensor (d0 innermost, contiguous) of bf16 (elem_bytes 2) or one-byte
 // elements with a box of b0 x b1 x b2 and 128-byte swizzle (b0 * elem_bytes
-// must be 128).
+// must be 128; 64 with the 64-byte one).
 msa_status make_map(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
-                    uint32_t b1, uint32_t b2, const char* name, int elem_bytes = 2) {
+                    uint32_t b1, uint32_t b2, const char* name, int elem_bytes = 2,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     auto enc = tensor_map_encoder();
     if (!enc) return fail(MSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
     cuuint64_t dims[3] = {d0, d1, d2};
@@ -386,7 +387,7 @@ msa_status make_map(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1
     cuuint32_t es[3] = {1, 1, 1};
     const CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     CUresult r = enc(map, dt, 3, const_cast<void*>(base), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(MSA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with %d", name, int(r));
     return MSA_OK;
@@ -402,6 +403,7 @@ msa::StagedArgs staged_args(const msa_problem* p) {
     a.max_cache_len = p->max_cache_len;
     a.cache_tokens = p->cache_tokens;
     a.ik_shared = ik_shared(p);
+    a.ik_exp = p->ik_dtype == MSA_IK_INT8 ? p->ik_exp : nullptr;
     a.cu_rows = p->cu_rows;
     a.cache_lens = p->cache_lens;
     a.cache = cache_rows_of(p);
@@ -436,6 +438,14 @@ msa_status kv_map(CUtensorMap* map, const msa_problem* p, const void* base, cons
     const uint64_t T = p->cache_tokens, H = p->num_kv_heads;
     if (p->kv_dtype == MSA_KV_INT8) return make_map(map, base, 128, H, T, 128, 1, 64, name, 1);
     return make_map(map, base, 128, H, T, 64, 1, 64, name);
+}
+
+// Index-key cache map: boxes of 64 dims x `positions`, bf16 or codes.
+msa_status ik_map(CUtensorMap* map, const msa_problem* p, const void* base, uint32_t positions) {
+    const uint64_t T = p->cache_tokens, KH = ik_shared(p) ? 1 : p->num_kv_heads;
+    if (p->ik_dtype == MSA_IK_INT8)
+        return make_map(map, base, 64, KH, T, 64, 1, positions, "ik_cache", 1, CU_TENSOR_MAP_SWIZZLE_64B);
+    return make_map(map, base, 64, KH, T, 64, 1, positions, "ik_cache");
 }
 
 // The decode attention's grid covers the host's count of decode-family rows
@@ -519,9 +529,7 @@ msa_status msa_index_scores(const msa_problem* p, const void* iq, const void* ik
         (s = check_ptr(scores, "scores")) != MSA_OK)
         return s;
     if (ld < p->max_cache_len) return fail(MSA_ERR_INVALID_ARG, "ld < max_cache_len");
-    if (p->ik_dtype != MSA_IK_BF16) return fail(MSA_ERR_UNSUPPORTED, "int8 index keys");
-    cudaError_t e = msa::run_index_scores(staged_args(p), static_cast<const uint16_t*>(iq),
-                                          static_cast<const uint16_t*>(ik_cache), scores, ld,
+    cudaError_t e = msa::run_index_scores(staged_args(p), static_cast<const uint16_t*>(iq), ik_cache, scores, ld,
                                           static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MSA_OK : cuda_fail(e, "index scores launch");
 }
@@ -756,6 +764,38 @@ int32_t msa_forward_launches(const msa_problem* p) {
     return (decode_family(p) ? 2 : 0) + (prefill_family(p) ? (widen_plan(p, true).on ? 3 : 2) : 0);
 }
 
+// The scan of int8 index keys and of groups that share a prefix, from the other one's arguments.
+static msa::IndexScanArgs index_scan_args(const msa_problem* p, const msa::ScanArgs& a) {
+    msa::IndexScanArgs x{};
+    x.ik_map = a.ik_map;
+    x.H = a.H;
+    x.ik_shared = a.ik_shared;
+    x.iq = a.iq;
+    x.ik_exp = p->ik_dtype == MSA_IK_INT8 ? p->ik_exp : nullptr;
+    x.cu_rows = a.cu_rows;
+    x.cache_lens = a.cache_lens;
+    x.group_starts = p->group_starts;
+    x.group_shared = p->group_shared;
+    x.cache = a.cache;
+    x.num_seqs = a.num_seqs;
+    x.num_groups = p->num_groups;
+    x.total_rows = a.total_rows;
+    x.max_cache_len = a.max_cache_len;
+    x.max_shared_len = p->max_shared_len;
+    x.max_group_rows = p->max_group_rows;
+    x.max_blocks = a.max_blocks;
+    x.rows_per_seq = a.rows_per_seq;
+    x.by_row = p->num_groups > 0;  // (then every sequence is of the decode family)
+    x.cache_tokens = a.cache_tokens;
+    x.unit_bound = a.unit_bound;
+    x.pooled = a.pooled;
+    x.clear_words = a.clear_words;
+    x.n_clear = a.n_clear;
+    x.drow_prefix = a.drow_prefix;
+    x.err = a.err;
+    return x;
+}
+
 msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* iq, const void* k_cache,
                               const void* v_cache, const void* ik_cache, void* out, int32_t* sel_out,
                               int32_t* nsel_out, void* workspace, size_t workspace_bytes, void* stream,
@@ -771,7 +811,6 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
         return fail(MSA_ERR_INVALID_ARG, "sel_out and nsel_out must both be given or both be null");
     if (sel_out && ((s = check_ptr(sel_out, "sel_out")) != MSA_OK || (s = check_ptr(nsel_out, "nsel_out")) != MSA_OK))
         return s;
-    if (p->ik_dtype != MSA_IK_BF16) return fail(MSA_ERR_UNSUPPORTED, "int8 index keys");
     if (n_events < 0 || n_events > 5) return fail(MSA_ERR_INVALID_ARG, "n_events must be in [0, 5]");
     Layout l;
     if ((s = check_workspace(p, workspace, workspace_bytes, &l)) != MSA_OK) return s;
@@ -782,8 +821,7 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
     const bool dec = decode_family(p), pre = prefill_family(p);
     int32_t* sel = sel_out ? sel_out : reinterpret_cast<int32_t*>(ws + l.sel);
     int32_t* nsel = nsel_out ? nsel_out : reinterpret_cast<int32_t*>(ws + l.nsel);
-    const uint64_t T = p->cache_tokens, H = p->num_kv_heads;
-    const uint64_t KH = ik_shared(p) ? 1 : H;  // index-key heads per position
+    const uint64_t H = p->num_kv_heads;
     const int max_blocks = static_cast<int>((p->max_cache_len + msa::kBlock - 1) / msa::kBlock);
 
     CUtensorMap km, vm, qm, iqm, ikm;
@@ -791,11 +829,10 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
     if (pre) {
         if ((s = make_map(&iqm, iq, 64, H, p->total_rows, 64, 1, 128, "iq")) != MSA_OK) return s;
         // a whole 256-position tile per box, or one box per 64-position block when paged
-        const uint32_t box = p->block_table == nullptr ? 256 : 64;
-        if ((s = make_map(&ikm, ik_cache, 64, KH, T, 64, 1, box, "ik_cache")) != MSA_OK) return s;
+        if ((s = ik_map(&ikm, p, ik_cache, p->block_table == nullptr ? 256 : 64)) != MSA_OK) return s;
     }
     CUtensorMap ik_scan;
-    if (dec && (s = make_map(&ik_scan, ik_cache, 64, KH, T, 64, 1, 64, "ik_cache")) != MSA_OK) return s;
+    if (dec && (s = ik_map(&ik_scan, p, ik_cache, 64)) != MSA_OK) return s;
     if ((s = marks.mark(0)) != MSA_OK) return s;
     cudaError_t e;
     if (dec) {
@@ -821,10 +858,15 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
         sa.n_clear = static_cast<int>(l.header_bytes / sizeof(int32_t));
         sa.drow_prefix = compact_decode_grid(p) ? reinterpret_cast<int32_t*>(ws + l.drow_prefix) : nullptr;
         sa.err = reinterpret_cast<uint32_t*>(ws + l.err);
-        if ((e = msa::run_decode_scan(sa, st)) != cudaSuccess) return cuda_fail(e, "decode scan launch");
+        if (p->num_groups > 0 || p->ik_dtype == MSA_IK_INT8)
+            e = msa::run_index_scan(index_scan_args(p, sa), st);
+        else
+            e = msa::run_decode_scan(sa, st);
+        if (e != cudaSuccess) return cuda_fail(e, "decode scan launch");
         if ((s = marks.mark(1)) != MSA_OK) return s;
         msa::DecodeAttendArgs da = decode_args(p, &km, &vm, q, out, ws, l);
         da.pooled = sa.pooled;
+        da.pooled_by_row = p->num_groups > 0;
         da.max_blocks = max_blocks;
         da.sel_out = sel;
         da.nsel_out = nsel;
@@ -841,6 +883,7 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
         msa::PrefillIndexArgs ia{};
         ia.iq_map = &iqm;
         ia.ik_map = &ikm;
+        ia.ik_exp = p->ik_dtype == MSA_IK_INT8 ? p->ik_exp : nullptr;
         ia.cu_rows = p->cu_rows;
         ia.cache_lens = p->cache_lens;
         ia.cache = cache_rows_of(p);
@@ -933,7 +976,10 @@ msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa
         return s;
     if ((a->q && a->q_out == a->q && a->q_stride != HG * D) || (a->iq && a->iq_out == a->iq && a->iq_stride != H * Di))
         return fail(MSA_ERR_INVALID_ARG, "q and iq can be rotated in place only where their rows are contiguous");
-    if (a->ik && p->ik_dtype != MSA_IK_BF16) return fail(MSA_ERR_UNSUPPORTED, "int8 index keys");
+    const bool ik8 = a->ik && p->ik_dtype == MSA_IK_INT8;
+    if (ik8 != (a->ik_exp != nullptr))
+        return fail(MSA_ERR_INVALID_ARG, "ik_exp is given with index keys of 8 bits and with no others");
+    if (!aligned16(a->ik_exp)) return fail(MSA_ERR_INVALID_ARG, "ik_exp is not 16-byte aligned");
     const bool i8 = p->kv_dtype == MSA_KV_INT8;
     if (i8 != (a->k_scale != nullptr) || i8 != (a->v_scale != nullptr))
         return fail(MSA_ERR_INVALID_ARG, "k_scale and v_scale are given for an int8 cache and for no other");
@@ -957,7 +1003,8 @@ msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa
     x.iq_stride = a->iq_stride;
     x.k_cache = a->k_cache;
     x.v_cache = a->v_cache;
-    x.ik_cache = static_cast<uint16_t*>(a->ik_cache);
+    x.ik_cache = a->ik_cache;
+    x.ik_exp = a->ik_exp;
     x.k_scale = a->k_scale;
     x.v_scale = a->v_scale;
     x.q_out = static_cast<uint16_t*>(a->q_out);

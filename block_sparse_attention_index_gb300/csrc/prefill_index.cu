@@ -22,6 +22,10 @@
 // at positions <= p; the local block J is forced and needs no score.
 // Scores are never written to memory.
 //
+// Index keys of 8 bits (codes with a power of two a position): the tiles land as codes in a ring of their own, and four more
+// warps write them as bf16, exactly, into the ring that the products read, with the power of two in them: a thread two
+// positions, 3.75 instructions a value, a quarter of what the epilogue of a tile takes, beside which they run.
+//
 // Warp roles: warps 0-7 epilogue (two per TMEM lane quarter, each taking two
 // of a tile's four blocks), warp 8 TMA producer, warp 9 MMA issuer and
 // tensor-memory owner.
@@ -37,9 +41,17 @@ constexpr int kIdxStages = 4;     // index-key tile ring
 constexpr int kIdxTileBytes = kIdxCols * kIndexDim * 2;  // 32 KB
 constexpr int kIdxABytes = kIdxRows * kIndexDim * 2;     // 16 KB
 
+constexpr int kIdxCodeStages = 3;                          // ring of 8-bit tiles
+constexpr int kIdxCodeBytes = kIdxCols * kIndexDim;        // 16 KB
+// 8-bit keys: the same ten warps, four that convert.
+constexpr int kIdxThreadsInt8 = 448;
+
+template <bool kInt8>
 struct __align__(1024) IndexSmem {
     uint8_t b[kIdxStages][kIdxTileBytes];
     uint8_t a[kIdxABytes];
+    uint8_t codes[kInt8 ? kIdxCodeStages : 1][kInt8 ? kIdxCodeBytes : 16];
+    uint64_t code_full[kIdxCodeStages], code_empty[kIdxCodeStages];
     uint64_t full[kIdxStages];
     uint64_t empty[kIdxStages];
     uint64_t a_full;
@@ -145,11 +157,13 @@ __device__ __forceinline__ void sort16_asc(int (&v)[16]) {
 // decode attention.  A no-op in an ordinary launch.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-__global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __grid_constant__ CUtensorMap iq_map,
+template <bool kInt8>
+__global__ void __launch_bounds__(kInt8 ? kIdxThreadsInt8 : kIdxThreads, 1) prefill_index_kernel(const __grid_constant__ CUtensorMap iq_map,
                                                                        const __grid_constant__ CUtensorMap ik_map,
                                                                        const PrefillIndexArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    IndexSmem& sm = *reinterpret_cast<IndexSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using Smem = IndexSmem<kInt8>;
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y;
 
@@ -177,8 +191,12 @@ __global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __g
             }
         }
         for (int s = 0; s < kIdxStages; ++s) {
-            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.full[s], kInt8 ? 4 : 1);  // (the converting warps, or the producer)
             mbar_init(&sm.empty[s], 1);
+        }
+        for (int s = 0; s < kIdxCodeStages; ++s) {
+            mbar_init(&sm.code_full[s], 1);
+            mbar_init(&sm.code_empty[s], 4);
         }
         mbar_init(&sm.a_full, 1);
         for (int s = 0; s < 2; ++s) {
@@ -200,6 +218,12 @@ __global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __g
     const uint32_t tmem = sm.tmem_base;
     const int n0 = sm.n0, n1 = sm.n1;  // this split's tiles
 
+    // tiles land in the ring of codes, or straight in the products'
+    constexpr int kRing = kInt8 ? kIdxCodeStages : kIdxStages, kLand = kInt8 ? kIdxCodeBytes : kIdxTileBytes;
+    uint64_t* const land_full = kInt8 ? sm.code_full : sm.full;
+    uint64_t* const land_empty = kInt8 ? sm.code_empty : sm.empty;
+    uint8_t* const land = kInt8 ? sm.codes[0] : sm.b[0];
+
     if (warp == 8) {
         // ---------------- TMA producer
         if (lane == 0) {
@@ -211,12 +235,12 @@ __global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __g
             int armed = 0;  // ring positions armed so far
             for (int n = n0; n < n1; ++n) {
                 const int i = n - n0;  // ring position
-                const int s = i % kIdxStages;
-                if (i >= kIdxStages && !mbar_wait(&sm.empty[s], ((i / kIdxStages) - 1) & 1, a.err)) break;
+                const int s = i % kRing;
+                if (i >= kRing && !mbar_wait(&land_empty[s], ((i / kRing) - 1) & 1, a.err)) break;
                 armed = i + 1;
                 if (a.cache.table == nullptr) {  // contiguous: the tile is one 256-position box
-                    mbar_arrive_expect_tx(&sm.full[s], kIdxTileBytes);
-                    tma_load_3d(sm.b[s], &ik_map, &sm.full[s], 0, key_head,
+                    mbar_arrive_expect_tx(&land_full[s], kLand);
+                    tma_load_3d(land + s * kLand, &ik_map, &land_full[s], 0, key_head,
                                 static_cast<int>(a.cache.starts[sm.seq] + static_cast<int64_t>(n) * kIdxCols));
                     continue;
                 }
@@ -237,18 +261,18 @@ __global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __g
                         ++nbox;
                     }
                 }
-                mbar_arrive_expect_tx(&sm.full[s], nbox * (kIdxTileBytes / (kIdxCols / kBlock)));
+                mbar_arrive_expect_tx(&land_full[s], nbox * (kLand / (kIdxCols / kBlock)));
 #pragma unroll
                 for (int qq = 0; qq < kIdxCols / kBlock; ++qq)
                     if (rows[qq] >= 0)
-                        tma_load_3d(sm.b[s] + qq * (kIdxTileBytes / (kIdxCols / kBlock)), &ik_map, &sm.full[s], 0, key_head,
+                        tma_load_3d(land + s * kLand + qq * (kLand / (kIdxCols / kBlock)), &ik_map, &land_full[s], 0, key_head,
                                     static_cast<int>(rows[qq]));
             }
             // no copy of this lane may still be in flight when the CTA ends (after a timed-out
             // wait elsewhere, too): wait, bounded, for the last phase armed on every slot
             mbar_wait(&sm.a_full, 0, a.err);
-            for (int s = 0; s < kIdxStages && s < armed; ++s)
-                mbar_wait(&sm.full[s], ((s + kIdxStages * ((armed - 1 - s) / kIdxStages)) / kIdxStages) & 1, a.err);
+            for (int s = 0; s < kRing && s < armed; ++s)
+                mbar_wait(&land_full[s], ((s + kRing * ((armed - 1 - s) / kRing)) / kRing) & 1, a.err);
         }
     } else if (warp == 9) {
         // ---------------- MMA issuer
@@ -279,6 +303,65 @@ __global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __g
                 mbar_wait(&sm.drain, 0, a.err);
             }
         }
+    } else if (kInt8 && warp >= 10) {
+        if constexpr (kInt8) {
+            // ---------------- codes to bf16: warps 10-13, positions t and t + 128 of a tile a thread
+            {
+                const int t = tid - 10 * 32, kh = a.ik_shared ? 1 : a.H, key_head = a.ik_shared ? 0 : h;
+                // exponents, a tile ahead
+                auto exps_of = [&](int n, int (&e)[2]) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int p = n * kIdxCols + t + 128 * y;
+                        e[y] = 0;
+                        if (n >= n1 || p >= sm.L) continue;
+                        const int64_t row = block_row(a.cache, sm.seq, p & ~(kBlock - 1));
+                        if (row >= 0) e[y] = a.ik_exp[(row + (p & (kBlock - 1))) * kh + key_head];
+                    }
+                };
+                int next[2];
+                exps_of(n0, next);
+                for (int n = n0; n < n1; ++n) {
+                    const int i = n - n0, from = i % kIdxCodeStages, s = i % kIdxStages;
+                    const float power[2] = {index_power(next[0]), index_power(next[1])};
+                    exps_of(n + 1, next);
+                    const bool ok = mbar_wait(&sm.code_full[from], (i / kIdxCodeStages) & 1, a.err) &&
+                                    (i < kIdxStages || mbar_wait(&sm.empty[s], ((i / kIdxStages) - 1) & 1, a.err));
+                    if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int row = t + 128 * y;
+                        const uint8_t* src = sm.codes[from] + row * kIndexDim;  // (64-byte swizzle)
+                        uint8_t* dst = sm.b[s] + row * 2 * kIndexDim;            // (128-byte swizzle)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ ((row >> 1) & 3)) << 4));
+                            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t u = ws[x] ^ 0x80808080u;
+                                float f[4];
+                                f[0] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540)) - 8388736.f) * power[y];
+                                f[1] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7541)) - 8388736.f) * power[y];
+                                f[2] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7542)) - 8388736.f) * power[y];
+                                f[3] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7543)) - 8388736.f) * power[y];
+                                o[2 * x] = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x7632);
+                                o[2 * x + 1] = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x7632);
+                            }
+                            *reinterpret_cast<uint4*>(dst + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(dst + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sm.full[s]);
+                        mbar_arrive(&sm.code_empty[from]);
+                    }
+                }
+            }
+        }
     } else {
         // ---------------- epilogue: warps w and w+4 share TMEM lane quarter w; a thread
         // owns one row and half of each tile's blocks (blocks 2 half, 2 half + 1)
@@ -303,6 +386,7 @@ __global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __g
                 float m;  // the block's pooled score: the maximum of its 64 columns, taken by the TMEM load
                 tmem_ld_max64(lane_addr + acc * kIdxCols + jb * kBlock, m);
                 tmem_ld_wait();
+                if constexpr (kInt8) m = fmaxf(m, -INFINITY);  // (a block whose keys are all not finite comes last)
                 if (!live || j >= J) continue;  // the local block is forced; later blocks are in the future
                 insert_top(best, block_key(m, j));
             }
@@ -397,13 +481,16 @@ __global__ void __launch_bounds__(kIdxThreads, 1) prefill_index_kernel(const __g
 }
 
 cudaError_t run_prefill_index(const PrefillIndexArgs& a, bool after_decode, cudaStream_t stream) {
-    const size_t smem = sizeof(IndexSmem) + 1024;
-    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(prefill_index_kernel), smem);
+    const bool int8 = a.ik_exp != nullptr;
+    const size_t smem = (int8 ? sizeof(IndexSmem<true>) : sizeof(IndexSmem<false>)) + 1024;
+    static_assert(sizeof(IndexSmem<true>) + 1024 <= 227 * 1024, "prompt indexer exceeds 227 KB of shared memory");
+    auto* kernel = int8 ? prefill_index_kernel<true> : prefill_index_kernel<false>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     const int tiles = (a.total_rows + kIdxRows - 1) / kIdxRows + a.num_seqs;  // upper bound
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(tiles, a.H, a.nsplit);
-    cfg.blockDim = dim3(kIdxThreads, 1, 1);
+    cfg.blockDim = dim3(int8 ? kIdxThreadsInt8 : kIdxThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -413,7 +500,7 @@ cudaError_t run_prefill_index(const PrefillIndexArgs& a, bool after_decode, cuda
     // only behind the decode attention, whose outputs this kernel does not read; as the
     // first kernel of a call it would overlap whatever the caller wrote iq or ik with
     cfg.numAttrs = after_decode ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, prefill_index_kernel, *a.iq_map, *a.ik_map, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, *a.iq_map, *a.ik_map, a);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }

@@ -25,8 +25,9 @@ __device__ __forceinline__ bool row_position(const StagedArgs& a, int r, int& b,
 }
 
 // grid (rows, H): one CTA per (row, head)
+template <bool kInt8>
 __global__ void __launch_bounds__(kStagedThreads) index_scores_kernel(StagedArgs a, const uint16_t* __restrict__ iq,
-                                                                      const uint16_t* __restrict__ ik,
+                                                                      const void* __restrict__ ik,
                                                                       float* __restrict__ scores, int64_t ld) {
     const int h = blockIdx.y, r = blockIdx.x;
     int b, p;
@@ -47,7 +48,22 @@ __global__ void __launch_bounds__(kStagedThreads) index_scores_kernel(StagedArgs
         const int64_t row0 = ok && t <= p ? block_row(a.cache, b, t & ~int64_t{kBlock - 1}) : -1;
         if (row0 >= 0) {  // (a page outside the pool leaves -inf)
             const int kh = a.ik_shared ? 1 : a.H;  // index-key heads per position
-            const uint16_t* kp = ik + ((row0 + (t & (kBlock - 1))) * kh + (a.ik_shared ? 0 : h)) * kIndexDim;
+            const int64_t key = (row0 + (t & (kBlock - 1))) * kh + (a.ik_shared ? 0 : h);
+            const uint16_t* kp = static_cast<const uint16_t*>(ik) + key * kIndexDim;
+            if constexpr (kInt8) {
+                const int8_t* cp = static_cast<const int8_t*>(ik) + key * kIndexDim;
+                s = 0.f;
+#pragma unroll
+                for (int c = 0; c < kIndexDim / 16; ++c) {
+                    const int4 w = *reinterpret_cast<const int4*>(cp + c * 16);
+                    const int ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        s = fmaf(q[c * 16 + e], static_cast<float>(static_cast<int8_t>(ws[e >> 2] >> (8 * (e & 3)))), s);
+                }
+                out[t] = s * index_power(a.ik_exp[key]);
+                continue;
+            }
             s = 0.f;
 #pragma unroll
             for (int c = 0; c < kIndexDim / 8; ++c) {
@@ -92,10 +108,11 @@ __global__ void __launch_bounds__(kStagedThreads) select_blocks_kernel(StagedArg
     if (threadIdx.x == 0) nsel[static_cast<int64_t>(r) * a.H + h] = n;
 }
 
-cudaError_t run_index_scores(const StagedArgs& a, const uint16_t* iq, const uint16_t* ik, float* scores, int64_t ld,
+cudaError_t run_index_scores(const StagedArgs& a, const uint16_t* iq, const void* ik, float* scores, int64_t ld,
                              cudaStream_t stream) {
     dim3 grid(a.total_rows, a.H);
-    index_scores_kernel<<<grid, kStagedThreads, 0, stream>>>(a, iq, ik, scores, ld);
+    if (a.ik_exp != nullptr) index_scores_kernel<true><<<grid, kStagedThreads, 0, stream>>>(a, iq, ik, scores, ld);
+    else index_scores_kernel<false><<<grid, kStagedThreads, 0, stream>>>(a, iq, ik, scores, ld);
     return cudaGetLastError();
 }
 
