@@ -61,6 +61,15 @@ __device__ __forceinline__ void i8x4_to_bf16x4(uint32_t w, uint32_t& lo, uint32_
     hi = __byte_perm(__float_as_uint(f2), __float_as_uint(f3), 0x7632);
 }
 
+// Bytes 0 and 2 of w, signed, as two bf16 values: a byte's lower seven bits v under the exponent of 128 read as 128 + v,
+// its sign bit there as 128 or 256, and the difference of the two is the byte, exactly.  (Three instructions for two
+// values; the other bytes are those of w >> 8.)
+__device__ __forceinline__ uint32_t i8_even_to_bf16(uint32_t w) {
+    const uint32_t v = (w & 0x007F007Fu) | 0x43004300u, s = (w & 0x00800080u) | 0x43004300u;
+    __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&s));
+    return *reinterpret_cast<uint32_t*>(&r);
+}
+
 // 2^e of an index key's 8-bit exponent; -128 stands for a key that is not finite.
 __device__ __forceinline__ float index_power(int e) {
     return e < -126 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);

@@ -9,7 +9,7 @@
 // the dimensions, held in registers for a whole head, B = eight query rows, taken one group of eight after the other.
 //
 // The order of the dimensions inside a dot product is free: lane `tig` of a row takes the 16 dimensions 16 tig .., which
-// are one 16-byte load of codes, or two of bf16, and two of the queries.  Codes become bf16 exactly (11 instructions for 4);
+// are one 16-byte load of codes, or two of bf16, and two of the queries.  Codes become bf16 exactly (7 instructions for 4);
 // their power of two multiplies the finished scores, position by position, before the maximum: exact too, so that integer
 // scores stay exact and every kernel that reads these keys finds the same maxima.
 //
@@ -27,7 +27,7 @@ struct IxCfg {
     static constexpr int kRowBytes = kInt8 ? kIndexDim : 2 * kIndexDim;
     static constexpr int kHeadBytes = kBlock * kRowBytes;  // [64 positions][64 dims]
     static constexpr int kUnitBytes = kKeyHeads * kHeadBytes;
-    static constexpr int kStages = kUnitBytes >= 65536 ? 3 : (kUnitBytes >= 32768 ? 6 : (kUnitBytes >= 16384 ? 10 : 12));  // <= 192 KB of ring
+    static constexpr int kStages = kUnitBytes >= 65536 ? 3 : (kUnitBytes >= 32768 ? 6 : (kUnitBytes >= 16384 ? 11 : 12));  // <= 192 KB of ring
     static constexpr int kThreads = 32 * (kStages + 1);  // a consumer a stage, and the producer
 };
 
@@ -299,7 +299,10 @@ __global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_s
                             const uint4 w = ix_lds(at + ((tig ^ ((row >> 1) & 3)) << 4));  // (64-byte swizzle)
                             const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) i8x4_to_bf16x4(ws[kk], ka[mt][kk][e], ka[mt][kk][2 + e]);
+                            for (int kk = 0; kk < 4; ++kk) {  // dims 0 and 2, 1 and 3 of the four
+                                ka[mt][kk][e] = i8_even_to_bf16(ws[kk]);
+                                ka[mt][kk][2 + e] = i8_even_to_bf16(ws[kk] >> 8);
+                            }
                         } else {
                             const uint4 w0 = ix_lds(at + (((2 * tig) ^ (row & 7)) << 4)), w1 = ix_lds(at + (((2 * tig + 1) ^ (row & 7)) << 4));
                             ka[mt][0][e] = w0.x, ka[mt][0][2 + e] = w0.y;
@@ -327,7 +330,15 @@ __global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_s
                     const uint4* src = reinterpret_cast<const uint4*>(
                         a.iq + (static_cast<int64_t>(x.row) * H + (kShared ? col : static_cast<int64_t>(col) * H + h)) * kIndexDim + 16 * tig);
                     const uint4 q0 = src[0], q1 = src[1];
-                    const uint32_t qb[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                    uint32_t qb[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                    if constexpr (kInt8) {  // in the codes' order
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t even = __byte_perm(qb[2 * kk], qb[2 * kk + 1], 0x5410), odd = __byte_perm(qb[2 * kk], qb[2 * kk + 1], 0x7632);
+                            qb[2 * kk] = even;
+                            qb[2 * kk + 1] = odd;
+                        }
+                    }
                     float c[4][4];
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt) c[mt][0] = c[mt][1] = c[mt][2] = c[mt][3] = 0.f;
