@@ -34,7 +34,8 @@
 
 namespace msa {
 
-constexpr int kDsThreads = 384;  // softmax groups: warps 0-3, 4-7; 8 and 10 copies, 9 and 11 matrix instructions
+// Softmax groups: warps 0-3, 4-7; 8 and 10 copies, 9 and 11 matrix instructions; int8 caches: 12-15 make bf16 of the codes.
+constexpr int kDsThreads = 384, kDsThreadsInt8 = 512;
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
 constexpr int kDsPartKeys = 32768;  // most keys of a part
 constexpr int kDsExtra = 2;         // tiles that an item counts for besides its own
@@ -51,20 +52,28 @@ struct DsItem {
     int64_t part;      // first row of its parts in the workspace
 };
 
-template <int kParts>
+template <int kParts, bool kInt8>
 struct DsCfg {
     static constexpr int NK = kParts == 1 ? 128 : 64;
     static constexpr int kTile = NK * kHeadDim * 2;  // bytes of a K or V tile
-    static constexpr int kStages = 5 * (128 / NK);
+    static constexpr int kStages = (kInt8 ? 3 : 5) * (128 / NK);
+    static constexpr int kCodes = 3 * (128 / NK);  // int8: tiles of codes in flight
+    // int8: tiles whose scales are kept.  When tile t is converted its slot has been given back by the values of tile t - 2
+    // (64-key tiles: t - 4 at the latest), whose softmax is then done.
+    static constexpr int kScales = 8;
+    static constexpr int kThreads = kInt8 ? kDsThreadsInt8 : kDsThreads;
     static constexpr int kSAt = kParts == 1 ? 0 : 64;  // column of S in its 128 (as in the prompt kernel: P's parts from 0 on)
     static constexpr int kRun = kDsPartKeys / NK;      // most tiles of a part
 };
 
-template <int kParts>
+template <int kParts, bool kInt8>
 struct __align__(1024) DsSmem {
-    using Cfg = DsCfg<kParts>;
+    using Cfg = DsCfg<kParts, kInt8>;
     uint8_t q[2][kDsQBytes];
     uint8_t ring[Cfg::kStages][Cfg::kTile];
+    uint8_t codes[kInt8 ? Cfg::kCodes : 1][kInt8 ? Cfg::kTile / 2 : 16];
+    float sc[kInt8 ? Cfg::kScales : 1][2][kInt8 ? Cfg::NK : 4];  // scales of a tile's keys and values
+    uint64_t code_full[Cfg::kCodes], code_empty[Cfg::kCodes];
     // Copies landed: of pairs [0], of the two stages on alternate tiles [1], [2], each counted by itself, so that an issuer
     // sees all phases of the barriers that it waits for.
     uint64_t full[3][Cfg::kStages], empty[Cfg::kStages];
@@ -74,11 +83,13 @@ struct __align__(1024) DsSmem {
     uint64_t info_full[kDsInfo], info_empty[kDsInfo], item_done;
     DsItem info[kDsInfo];
     uint32_t tmem, err;
-    int64_t scan_line[kDsThreads / 32];
-    int32_t scan_items[kDsThreads / 32];
+    int64_t scan_line[Cfg::kThreads / 32];
+    int32_t scan_items[Cfg::kThreads / 32];
 };
-static_assert(sizeof(DsSmem<1>) + 1024 <= 227 * 1024, "shared-prefix attention exceeds 227 KB of shared memory");
-static_assert(sizeof(DsSmem<3>) + 1024 <= 227 * 1024, "shared-prefix attention (fp32) exceeds 227 KB of shared memory");
+static_assert(sizeof(DsSmem<1, false>) + 1024 <= 227 * 1024, "shared-prefix attention exceeds 227 KB of shared memory");
+static_assert(sizeof(DsSmem<3, false>) + 1024 <= 227 * 1024, "shared-prefix attention (fp32) exceeds 227 KB of shared memory");
+static_assert(sizeof(DsSmem<1, true>) + 1024 <= 227 * 1024, "shared-prefix attention (int8) exceeds 227 KB of shared memory");
+static_assert(sizeof(DsSmem<3, true>) + 1024 <= 227 * 1024, "shared-prefix attention (int8, fp32) exceeds 227 KB of shared memory");
 
 // Entries of the line: the groups, then the sequences.  The query rows [row, row + rows) see all keys [key, end).
 struct DsEntry {
@@ -161,13 +172,14 @@ __device__ __forceinline__ int ds_owner(int64_t line, int64_t at, int shares) {
     return static_cast<int>(((at + 1) * shares - 1) / line);
 }
 
-template <int kParts>
-__global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __grid_constant__ CUtensorMap q_map,
+template <int kParts, bool kInt8>
+__global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_shared_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                     const __grid_constant__ CUtensorMap k_map,
                                                                     const __grid_constant__ CUtensorMap v_map,
                                                                     const SharedArgs a) {
-    using Cfg = DsCfg<kParts>;
-    using Smem = DsSmem<kParts>;
+    using Cfg = DsCfg<kParts, kInt8>;
+    using Smem = DsSmem<kParts, kInt8>;
+    constexpr int kThreads = Cfg::kThreads, kCodes = Cfg::kCodes;
     constexpr int NK = Cfg::NK, kStages = Cfg::kStages, kHalf = Cfg::kTile / 2, kSAt = Cfg::kSAt, kRun = Cfg::kRun;
     extern __shared__ uint8_t smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -175,13 +187,17 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, &sm.err); };
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            for (int k = 0; k < 3; ++k) mbar_init(&sm.full[k][s], 2);  // two warps copy a half each
+            for (int k = 0; k < 3; ++k) mbar_init(&sm.full[k][s], kInt8 ? 4 : 2);  // two warps copy a half each (int8: four convert)
             mbar_init(&sm.empty[s], 2);                                // both issuers (alternate tiles: one, and the copier for the other)
             mbar_init(&sm.v_last[s], 2);
         }
         for (int s = 0; s < kDsInfo; ++s) {
             mbar_init(&sm.info_full[s], 1);
-            mbar_init(&sm.info_empty[s], 11);  // a copier, two issuers, eight softmax warps
+            mbar_init(&sm.info_empty[s], kInt8 ? 15 : 11);  // a copier, two issuers, eight softmax warps, four that convert
+        }
+        for (int s = 0; s < kCodes; ++s) {
+            mbar_init(&sm.code_full[s], 2);
+            mbar_init(&sm.code_empty[s], 4);
         }
         mbar_init(&sm.item_done, 2);
         for (int s = 0; s < 2; ++s) {
@@ -209,7 +225,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
     const int entries = a.num_groups + a.num_seqs;
     int64_t line = 0;
     int parts = 0;
-    for (int base = 0; base < entries; base += kDsThreads) {
+    for (int base = 0; base < entries; base += kThreads) {
         const int e = base + tid;
         int64_t mine = 0;
         int items = 0;
@@ -244,7 +260,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
         __syncthreads();
         int64_t before = line;
         int before_items = parts;
-        for (int w = 0; w < kDsThreads / 32; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) {
                 before += sm.scan_line[w];
                 before_items += sm.scan_items[w];
@@ -283,7 +299,8 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
     if (idle) {
         // nothing to do
     } else if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (kInt8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8 || warp == 10) {
             // ---------------- copies: K and V tiles, dimensions 0-63 by warp 8 (and the queries), 64-127 by warp 10 (which
             // also finds the items, and clears the end of a last value tile)
@@ -386,8 +403,8 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                     }
                     alive = __shfl_sync(0xffffffffu, ok, 0) != 0;
                 }
-                // the value tile that holds the end of the keys, if its last block is not wholly theirs
-                const int fix = item.end % kBlock != 0 && item.key + item.tiles * NK >= item.end ? item.tiles - 1 : -1;
+                // the value tile that holds the end of the keys, if its last block is not wholly theirs (codes are finite)
+                const int fix = !kInt8 && item.end % kBlock != 0 && item.key + item.tiles * NK >= item.end ? item.tiles - 1 : -1;
                 constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
                 int64_t row = 0;
                 int fix_slot = 0, fix_row = 0, fix_copy = 0;
@@ -416,7 +433,18 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
 #pragma unroll
                         for (int c = 0; c < NK / kBlock; ++c) r[c] = __shfl_sync(0xffffffffu, row, (j % kBatch) * (NK / kBlock) + c);
                         int ok = 1;
-                        if (lane == 0) {
+                        if (kInt8 && lane == 0) {  // a block of codes each, if the tile has two
+                            const int at = slot % kCodes;
+                            if (slot >= kCodes) ok = wait(&sm.code_empty[at], ((slot / kCodes) - 1) & 1);
+                            if (ok && half >= NK / kBlock) {
+                                mbar_arrive(&sm.code_full[at]);
+                            } else if (ok) {
+                                mbar_arrive_expect_tx(&sm.code_full[at], kBlock * kHeadDim);
+                                tma_load_3d(sm.codes[at] + half * (kBlock * kHeadDim), kind == 0 ? &k_map : &v_map, &sm.code_full[at], 0, item.h,
+                                            static_cast<int>(half < NK / kBlock ? r[half < NK / kBlock ? half : 0] : 0));
+                            }
+                        }
+                        if (!kInt8 && lane == 0) {
                             uint64_t* bar = kind == 1 && j == fix ? &sm.v_last[st] : &sm.full[set][copy % kStages];
                             if (slot >= kStages) ok = wait(&sm.empty[st], ((slot / kStages) - 1) & 1);
                             if (ok) {
@@ -463,9 +491,82 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                     const int used = s ? q_used[1] : q_used[0];
                     if (used > 0) wait(&sm.q_full[s], (used - 1) & 1);
                 }
+                if constexpr (kInt8) {
+                    for (int b = 0; b < kCodes && b < slot; ++b) wait(&sm.code_full[b], ((slot - 1 - b) / kCodes) & 1);
+                } else {
 #pragma unroll
-                for (int s = 0; s < 3; ++s)
-                    for (int b = 0; b < kStages && b < sent[s]; ++b) wait(&sm.full[s][b], ((sent[s] - 1 - b) / kStages) & 1);
+                    for (int s = 0; s < 3; ++s)
+                        for (int b = 0; b < kStages && b < sent[s]; ++b) wait(&sm.full[s][b], ((sent[s] - 1 - b) / kStages) & 1);
+                }
+            }
+        } else if (kInt8 && warp >= 12) {
+            // ---------------- codes to bf16, exactly: a thread a key (64-key tiles: half a key), which also puts its scales down
+            const int t = tid - 384, key = t % NK, piece = t / NK;
+            int slot = 0, tiles = 0, sent[3] = {0, 0, 0};
+            bool alive = true;
+            for (int k = 0; alive; ++k) {
+                DsItem item;
+                alive = __all_sync(0xffffffffu, next_item(k, item));
+                if (!alive) break;
+                __syncwarp();
+                if (lane == 0) passed(k);
+                if (item.b < 0) break;
+                // scales of the thread's key in tile j (zeros past the end: their weights are zero whatever lies there)
+                auto scales_of = [&](int j) {
+                    const int p = item.key + j * NK + key;
+                    float2 y = make_float2(0.f, 0.f);
+                    if (j < item.tiles && p < item.end) {
+                        const int64_t row = block_row(a.cache, item.b, p & ~(kBlock - 1));
+                        if (row >= 0) {
+                            const int64_t at = (row + (p & (kBlock - 1))) * a.H + item.h;
+                            y = make_float2(a.k_scale[at], a.v_scale[at]);
+                        }
+                    }
+                    return y;
+                };
+                float2 next = scales_of(0);
+                for (int j = 0; alive && j < item.tiles; ++j, ++tiles) {
+                    const int set = item.pair ? 0 : 1 + (j & 1);
+                    if (piece == 0) {
+                        sm.sc[tiles % Cfg::kScales][0][key] = next.x;
+                        sm.sc[tiles % Cfg::kScales][1][key] = next.y;
+                    }
+                    next = scales_of(j + 1);
+#pragma unroll 1
+                    for (int kind = 0; kind < 2; ++kind, ++slot) {
+                        const int st = slot % kStages, from = slot % kCodes, copy = set == 0 ? sent[0] : (set == 1 ? sent[1] : sent[2]);
+                        const bool ok = wait(&sm.code_full[from], (slot / kCodes) & 1) && (slot < kStages || wait(&sm.empty[st], ((slot / kStages) - 1) & 1));
+                        alive = __all_sync(0xffffffffu, ok);
+                        if (!alive) break;
+                        if (set > 0 && t == 0) mbar_arrive(&sm.empty[st]);  // (for the stage that does not take the tile)
+                        const uint8_t* src = sm.codes[from] + key * kHeadDim;
+                        uint8_t* dst = sm.ring[st] + key * 128;
+#pragma unroll 2
+                        for (int c = piece * (NK / 16); c < (piece + 1) * (NK / 16); ++c) {  // 16 dims
+                            const uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ (key & 7)) << 4));
+                            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                            uint32_t o[8];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t even = i8_even_to_bf16(ws[x]), odd = i8_even_to_bf16(ws[x] >> 8);
+                                o[2 * x] = __byte_perm(even, odd, 0x5410);
+                                o[2 * x + 1] = __byte_perm(even, odd, 0x7632);
+                            }
+                            uint8_t* to = dst + (c >> 2) * kHalf;  // (64 dims a half)
+                            *reinterpret_cast<uint4*>(to + (((2 * (c & 3)) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sm.full[set][copy % kStages]);
+                            mbar_arrive(&sm.code_empty[from]);
+                        }
+                        if (set == 0) ++sent[0];
+                        else if (set == 1) ++sent[1];
+                        else ++sent[2];
+                    }
+                }
             }
         } else {
             // ---------------- matrix instructions of stage s, one thread
@@ -587,13 +688,14 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
             __syncwarp();
         }
     } else {
-        // 168 x 384 registers at launch: 208 x 256 + 88 x 128
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // 168 x 384 registers at launch: 208 x 256 + 88 x 128; int8 128 x 512: 192 x 256 + 64 x 256
+        if constexpr (kInt8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------- softmax group s: thread = row of its M tile
         const int s = warp >> 2, m = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 (warp % 4)) << 16
         const uint32_t s_addr = tmem + s * 128 + lanes, o_addr = tmem + 256 + s * 128 + lanes;
-        int tiles = 0, done = 0;  // running: the stage's tiles, items it had tiles of
+        int tiles = 0, done = 0, before = 0;  // running: the stage's tiles, items it had tiles of, key tiles of earlier items
         bool alive = true;
         for (int k = 0; alive; ++k) {
             DsItem item;
@@ -647,6 +749,8 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                 }
                 tc_fence_after();
                 if (kParts > 1 && c > 0 && c % 2 == 0) collect();
+                // int8: scales of the tile's keys and values
+                const auto& sc = sm.sc[kInt8 ? (before + (item.pair ? c : 2 * c + s)) % Cfg::kScales : 0];
                 const bool edge = t0 + NK > item.end;
                 const int seen = item.end - t0;  // keys of the tile
                 auto raise = [&](float now) {  // the maximum in use is now's or within kDsSlack of it
@@ -673,13 +777,23 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                     auto scores_of = [&](int q, float (&x)[32]) {
                         dp_ld32(s_addr + kSAt + 32 * q, x);
                         tmem_ld_wait();
+                        if constexpr (kInt8) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(&sc[0][32 * q + i]);
+                                x[i] *= f.x;
+                                x[i + 1] *= f.y;
+                                x[i + 2] *= f.z;
+                                x[i + 3] *= f.w;
+                            }
+                        }
                         if (edge) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) x[i] = 32 * q + i < seen ? x[i] * a.scale_log2 : -INFINITY;
                         }
                     };
                     const float f = edge ? 1.f : a.scale_log2;  // what is left to multiply by
-                    if (edge) {
+                    if (kInt8 || edge) {
 #pragma unroll 1
                         for (int q = 0; q < 2; ++q) {
                             float x[32];
@@ -687,6 +801,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
 #pragma unroll
                             for (int i = 0; i < 32; ++i) now = fmaxf(now, x[i]);
                         }
+                        now *= f;
                     } else {
                         tmem_ld_max64(s_addr + kSAt, now);
                         tmem_ld_wait();
@@ -706,6 +821,16 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                             x[2 * i] = dp_exp2(y.x);
                             x[2 * i + 1] = dp_exp2(y.y);
                             add = __fadd2_rn(add, make_float2(x[2 * i], x[2 * i + 1]));
+                        }
+                        if constexpr (kInt8) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 v = *reinterpret_cast<const float4*>(&sc[1][32 * q + i]);
+                                x[i] *= v.x;
+                                x[i + 1] *= v.y;
+                                x[i + 2] *= v.z;
+                                x[i + 3] *= v.w;
+                            }
                         }
 #pragma unroll
                         for (int part = 0; part < kParts; ++part) {
@@ -732,6 +857,15 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                     for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
                     float f = a.scale_log2;
                     tmem_ld_wait();
+                    if constexpr (kInt8) {
+#pragma unroll
+                        for (int i = 0; i < NK; i += 4) {
+                            const float4 ks = *reinterpret_cast<const float4*>(&sc[0][i]);
+                            const float2 y0 = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ks.x, ks.y));
+                            const float2 y1 = __fmul2_rn(make_float2(x[i + 2], x[i + 3]), make_float2(ks.z, ks.w));
+                            x[i] = y0.x, x[i + 1] = y0.y, x[i + 2] = y1.x, x[i + 3] = y1.y;
+                        }
+                    }
                     float now;
                     if (edge) {  // keys past the end; the scores are then not those that the load took the maximum of
 #pragma unroll
@@ -743,6 +877,13 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
 #pragma unroll
                             for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], x[i + z]);
                         now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+                    } else if constexpr (kInt8) {
+                        float y[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                        for (int i = 4; i < NK; i += 4)
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], x[i + z]);
+                        now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * f;
                     } else {
                         now = fmaxf(big[0], big[NK / 64 - 1]) * f;
                     }
@@ -763,6 +904,15 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
                                 z[2 * i + 1] = dp_exp2(y.y);
                                 add[i & 1] = __fadd2_rn(add[i & 1], make_float2(z[2 * i], z[2 * i + 1]));
                             }
+                            if constexpr (kInt8) {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 vs = *reinterpret_cast<const float4*>(&sc[1][64 * h2 + 32 * q + i]);
+                                    const float2 y0 = __fmul2_rn(make_float2(z[i], z[i + 1]), make_float2(vs.x, vs.y));
+                                    const float2 y1 = __fmul2_rn(make_float2(z[i + 2], z[i + 3]), make_float2(vs.z, vs.w));
+                                    z[i] = y0.x, z[i + 1] = y0.y, z[i + 2] = y1.x, z[i + 3] = y1.y;
+                                }
+                            }
 #pragma unroll
                             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(z[2 * i], z[2 * i + 1]);
                             dp_st16(s_addr + 32 * h2 + 16 * q, pk);
@@ -777,6 +927,7 @@ __global__ void __launch_bounds__(kDsThreads, 1) dense_shared_kernel(const __gri
             }
             if (alive && count > 0) alive = __all_sync(0xffffffffu, wait(&sm.o_full[s], done++ & 1));
             tiles += count;
+            before += item.tiles;
             if (!alive) break;
             if (!busy) continue;
             // ---------------- the part: O, maximum, sum
@@ -970,15 +1121,15 @@ __global__ void __launch_bounds__(512, kResident) dense_shared_join(const Shared
         *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
-template <int kParts>
+template <int kParts, bool kInt8>
 static cudaError_t launch_shared(const SharedArgs& a, int grid, cudaStream_t stream) {
-    const size_t smem = sizeof(DsSmem<kParts>) + 1024;
-    auto* kernel = dense_shared_kernel<kParts>;
+    const size_t smem = sizeof(DsSmem<kParts, kInt8>) + 1024;
+    auto* kernel = dense_shared_kernel<kParts, kInt8>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kDsThreads, 1, 1);
+    cfg.blockDim = dim3(DsCfg<kParts, kInt8>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -998,7 +1149,7 @@ static cudaError_t launch_shared(const SharedArgs& a, int grid, cudaStream_t str
     const bool many = blocks > device_sm_count();
     auto* join = a.kv_int8 ? (many ? dense_shared_join<true, 2> : dense_shared_join<true, 1>)
                            : (many ? dense_shared_join<false, 2> : dense_shared_join<false, 1>);
-    return cudaLaunchKernelEx(&cfg, join, a, grid, DsCfg<kParts>::NK);
+    return cudaLaunchKernelEx(&cfg, join, a, grid, DsCfg<kParts, kInt8>::NK);
 }
 
 SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int total_rows, int max_rows_per_seq, int max_group_rows,
@@ -1017,7 +1168,8 @@ SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int tot
 }
 
 cudaError_t run_dense_shared(const SharedArgs& a, int grid, cudaStream_t stream) {
-    return a.out_bf16 ? launch_shared<1>(a, grid, stream) : launch_shared<3>(a, grid, stream);
+    if (a.kv_int8) return a.out_bf16 ? launch_shared<1, true>(a, grid, stream) : launch_shared<3, true>(a, grid, stream);
+    return a.out_bf16 ? launch_shared<1, false>(a, grid, stream) : launch_shared<3, false>(a, grid, stream);
 }
 
 }  // namespace msa

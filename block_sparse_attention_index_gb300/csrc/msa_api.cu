@@ -332,7 +332,7 @@ DenseLayout dense_layout(const msa_problem* p, const DensePlan& d) {
 }
 
 // Groups that share a prefix: msa_dense_forward runs on kernels of its own.
-bool dense_shared(const msa_problem* p) { return p->num_groups > 0 && p->kv_dtype == MSA_KV_BF16; }
+bool dense_shared(const msa_problem* p) { return p->num_groups > 0; }
 
 struct SharedLayout {
     msa::SharedRoom room;

@@ -157,6 +157,37 @@ def test_int8_caches(out):
     SharedBatch(seqs, [(4, 640), (2, 128)], 2, 16, out=out, int8=True).check()
 
 
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("H,G", [(1, 1), (2, 4), (4, 16)])
+def test_int8_caches_over_many_tiles(H, G, out):
+    """Groups of one M tile, of two and of an odd number, prefixes that end inside a tile of 128 keys, own positions of any
+    length: every ring slot and scale slot is used again."""
+    rows = 128 // G
+    most = min(8, rows)
+    groups, seqs = [], []
+    for tiles, S in ((1, 1984), (2, 2112), (3, 1280)):
+        n = min(rows * tiles // most + (tiles > 1), 40)
+        seqs += behind(S, [(37 * i) % 700 for i in range(n)], most)
+        groups.append((n, S))
+    SharedBatch(seqs + [(most, 1500), (1, 130)], groups, H, G, out=out, int8=True, seed=3).check()
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_int8_parts_of_a_long_prefix(out):
+    SharedBatch(behind(40000, [0, 100, 33000], 1), [(3, 40000)], 1, 16, out=out, int8=True).check()
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_int8_scales_past_the_end_do_not_matter(out):
+    a = SharedBatch(behind(256, [1, 70, 129, 190], 1) + [(1, 3)], [(4, 256)], 2, 16, out=out, int8=True)
+    used = torch.zeros(a.T, dtype=torch.bool, device="cuda")
+    for b, (n, L) in enumerate(a.seqs):
+        used[a.rows_of(b, torch.arange(L, device="cuda"))] = True
+    a.k_scale[~used] = float("nan")
+    a.v_scale[~used] = float("inf")
+    a.check()
+
+
 def test_the_same_call_gives_the_same_bits():
     a = SharedBatch(behind(8192, [100 * i for i in range(20)], 2), [(20, 8192)], 4, 16)
     first, ws = a.run(), a.workspace()
