@@ -38,7 +38,8 @@ namespace msa {
 constexpr int kDsThreads = 384, kDsThreadsInt8 = 512;
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
 constexpr int kDsPartKeys = 32768;  // most keys of a part
-constexpr int kDsExtra = 2;         // tiles that an item counts for besides its own
+// Lengths on the line: a key tile of one M tile, of two, and what an item counts for besides (going on to another one).
+constexpr int kDsSingle = 4, kDsPair = 6, kDsExtra = 8;
 constexpr int kDsInfo = 4;          // items published ahead
 constexpr float kDsSlack = 8.f;     // log2 by which the running maximum may lag
 
@@ -77,12 +78,14 @@ struct __align__(1024) DsSmem {
     // Copies landed: of pairs [0], of the two stages on alternate tiles [1], [2], each counted by itself, so that an issuer
     // sees all phases of the barriers that it waits for.
     uint64_t full[3][Cfg::kStages], empty[Cfg::kStages];
-    uint64_t v_last[Cfg::kStages];  // a last value tile has landed, before its tail is zeroed (by ring slot: a copier may be items ahead)
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];  // P: by halves of the key tile
-    uint64_t info_full[kDsInfo], info_empty[kDsInfo], item_done;
+    uint64_t info_full[kDsInfo], info_empty[kDsInfo], item_done[2];
     DsItem info[kDsInfo];
     uint32_t tmem, err;
+    int group_parts;   // parts of all groups
+    int first;         // the entry where the CTA's share begins, and what is known of it
+    SharedEntry first_entry;
     int64_t scan_line[Cfg::kThreads / 32];
     int32_t scan_items[Cfg::kThreads / 32];
 };
@@ -139,16 +142,17 @@ __device__ __forceinline__ DsEntry ds_seq(const SharedArgs& a, int b, int& g, bo
 
 // How an entry lies on the line: `units` items a head (of up to two M tiles), each `chunks` parts of up to `run` tiles.
 struct DsSize {
-    int tiles, chunks, units, unit;  // key tiles; parts they make; items a head; an item's length on the line
+    int tiles, chunks, units, unit, w;  // key tiles; parts they make; items a head; an item's length on the line, a tile's
 };
 __device__ __forceinline__ DsSize ds_size(const SharedArgs& a, const DsEntry& x, int NK) {
     DsSize s{};
     if (x.rows == 0 || x.end <= x.key) return s;
-    const int run = kDsPartKeys / NK, P = 128 / a.G, mt = (x.rows + P - 1) / P;
+    const int run = kDsPartKeys / NK, P = 128 / a.G, mt = x.rows <= P ? 1 : (x.rows + P - 1) / P;
     s.tiles = (x.end - x.key + NK - 1) / NK;
     s.chunks = (s.tiles + run - 1) / run;
     s.units = (mt + 1) / 2;
-    s.unit = s.tiles + s.chunks * kDsExtra;
+    s.w = mt > 1 ? kDsPair : kDsSingle;
+    s.unit = s.tiles * s.w + s.chunks * kDsExtra;
     return s;
 }
 __device__ __forceinline__ DsEntry ds_entry(const SharedArgs& a, int e, bool& bad) {
@@ -162,14 +166,46 @@ __device__ __forceinline__ DsEntry ds_entry(const SharedArgs& a, int e, bool& ba
     return x;
 }
 
+// Tiles of a part that begin before x on the line from its first tile on.
+__device__ __forceinline__ int ds_tiles_before(int x, int w) {
+    return x <= 0 ? 0 : (w == kDsPair ? (x + kDsPair - 1) / kDsPair : (x + kDsSingle - 1) / kDsSingle);
+}
+
 // CTAs that share a line, and where share c begins (the largest c whose share begins at or before a place: ds_owner).
-__host__ __device__ __forceinline__ int ds_shares(int64_t line, int grid) {
-    const int64_t n = line / (kDsExtra + 2);
+__device__ __forceinline__ int ds_shares(int64_t line, int grid) {
+    const int64_t n = line / (kDsExtra + 2 * kDsPair);  // (no share is then without a tile of an item that goes through it)
     return static_cast<int>(n < 1 ? 1 : (n < grid ? n : grid));
 }
 __device__ __forceinline__ int64_t ds_cut(int64_t line, int c, int shares) { return line * c / shares; }
 __device__ __forceinline__ int ds_owner(int64_t line, int64_t at, int shares) {
     return static_cast<int>(((at + 1) * shares - 1) / line);
+}
+__device__ __forceinline__ SharedEntry ds_load(const SharedEntry* p) {
+    SharedEntry y;
+    reinterpret_cast<int4*>(&y)[0] = reinterpret_cast<const int4*>(p)[0];
+    reinterpret_cast<int4*>(&y)[1] = reinterpret_cast<const int4*>(p)[1];
+    return y;
+}
+
+__device__ __forceinline__ uint4 ds_ld_shared(uint32_t at) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    return w;
+}
+// x[i] times the 32 floats at `at` (the loads first: one behind another they would each take their latency).
+__device__ __forceinline__ void ds_times32(float* x, uint32_t at) {
+    uint4 f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = ds_ld_shared(at + 16 * i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 y0 = __fmul2_rn(make_float2(x[4 * i], x[4 * i + 1]), make_float2(__uint_as_float(f[i].x), __uint_as_float(f[i].y)));
+        const float2 y1 = __fmul2_rn(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(__uint_as_float(f[i].z), __uint_as_float(f[i].w)));
+        x[4 * i] = y0.x, x[4 * i + 1] = y0.y, x[4 * i + 2] = y1.x, x[4 * i + 3] = y1.y;
+    }
+}
+__device__ __forceinline__ void ds_st_shared(uint32_t at, uint4 w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
 }
 
 template <int kParts, bool kInt8>
@@ -189,7 +225,6 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
         for (int s = 0; s < kStages; ++s) {
             for (int k = 0; k < 3; ++k) mbar_init(&sm.full[k][s], kInt8 ? 4 : 2);  // two warps copy a half each (int8: four convert)
             mbar_init(&sm.empty[s], 2);                                // both issuers (alternate tiles: one, and the copier for the other)
-            mbar_init(&sm.v_last[s], 2);
         }
         for (int s = 0; s < kDsInfo; ++s) {
             mbar_init(&sm.info_full[s], 1);
@@ -199,8 +234,8 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             mbar_init(&sm.code_full[s], 2);
             mbar_init(&sm.code_empty[s], 4);
         }
-        mbar_init(&sm.item_done, 2);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(&sm.item_done[s], 2);
             mbar_init(&sm.q_full[s], 1);
             mbar_init(&sm.q_empty[s], 2);
             mbar_init(&sm.s_full[s], 1);
@@ -223,18 +258,22 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
     const uint32_t tmem = sm.tmem;
     // ---- places of the entries on the line, and parts before each (a block-wide scan; every CTA stores the same)
     const int entries = a.num_groups + a.num_seqs;
-    int64_t line = 0;
-    int parts = 0;
+    int64_t line = 0, len = 0;
+    int parts = 0, e_mine = -1;
+    SharedEntry y{};  // the thread's entry of the last round
     for (int base = 0; base < entries; base += kThreads) {
         const int e = base + tid;
-        int64_t mine = 0;
         int items = 0;
+        len = 0;
+        e_mine = -1;
         if (e < entries) {
             bool bad;
             const DsEntry x = ds_entry(a, e, bad);
             const DsSize s = ds_size(a, x, NK);
-            mine = static_cast<int64_t>(a.H) * s.units * s.unit;
+            len = static_cast<int64_t>(a.H) * s.units * s.unit;
             items = a.H * s.units * s.chunks;
+            e_mine = e;
+            y = SharedEntry{0, 0, x.b, x.row, x.rows, x.key, x.end};
             if (blockIdx.x == 0) {
                 if (e >= a.num_groups && x.rows > 0)  // the rows' own positions, which the join reads
                     bad |= block_row(a.cache, x.b, x.end & ~(kBlock - 1)) < 0 ||
@@ -242,7 +281,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                 if (bad) atomicOr(&sm.err, kErrBadMetadata);
             }
         }
-        int64_t incl = mine;
+        int64_t incl = len;
         int incl_items = items;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -268,24 +307,35 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             line += sm.scan_line[w];
             parts += sm.scan_items[w];
         }
+        y.line = before + incl - len;
+        y.parts = before_items + incl_items - items;
         if (e < entries) {
-            a.line[e] = before + incl - mine;
-            a.items[e] = before_items + incl_items - items;
+            a.entries[e] = y;
+            if (e == a.num_groups) sm.group_parts = y.parts;
         }
         __syncthreads();
     }
-    if (tid == 0) {
-        a.line[entries] = line;
-        a.items[entries] = parts;
-    }
-    __syncthreads();
-    const int group_parts = a.items[a.num_groups];
+    if (tid == 0) a.entries[entries] = SharedEntry{line, parts, 0, 0, 0, 0, 0};
+    const int group_parts = sm.group_parts;  // (a problem has a sequence)
     if (group_parts > a.group_parts_most || parts - group_parts > a.seq_parts_most) {  // more than the host's bounds allow for
         if (tid == 0) atomicOr(&sm.err, kErrBadMetadata);
         line = 0;
     }
     const int shares = ds_shares(line, gridDim.x);
     const bool idle = line == 0 || static_cast<int>(blockIdx.x) >= shares;
+    const int64_t from = ds_cut(line, blockIdx.x, shares);
+    // the entry where the share begins
+    if (!idle && e_mine >= 0 && y.line <= from && from < y.line + len) {
+        sm.first = e_mine;
+        sm.first_entry = y;
+    }
+    for (int e = tid; !idle && e < (entries - 1) / kThreads * kThreads; e += kThreads) {  // (earlier rounds')
+        if (a.entries[e].line <= from && from < a.entries[e + 1].line) {
+            sm.first = e;
+            sm.first_entry = ds_load(a.entries + e);
+        }
+    }
+    __syncthreads();
     const int P = 128 / a.G;
 
     auto next_item = [&](int k, DsItem& x) {  // item k of the CTA, false where it never came
@@ -294,71 +344,76 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
         return true;
     };
     auto passed = [&](int k) { mbar_arrive(&sm.info_empty[k % kDsInfo]); };
-    auto count_of = [](const DsItem& x, int s) { return x.pair ? x.tiles : (x.tiles + 1 - s) / 2; };  // key tiles of stage s
+    // One M tile: stage s takes every second key tile, of item k from tile (s + k) % 2 on.
+    auto first_of = [](const DsItem& x, int k, int s) { return x.pair ? 0 : (s + k) & 1; };
+    auto count_of = [](const DsItem& x, int k, int s) { return x.pair ? x.tiles : (x.tiles + 1 - ((s + k) & 1)) / 2; };
 
     if (idle) {
         // nothing to do
     } else if (warp >= 8) {
-        if constexpr (kInt8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (kInt8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 8 || warp == 10) {
             // ---------------- copies: K and V tiles, dimensions 0-63 by warp 8 (and the queries), 64-127 by warp 10 (which
-            // also finds the items, and clears the end of a last value tile)
+            // also finds the items)
             const int half = warp == 10;
             int slot = 0, sent[3] = {0, 0, 0}, q_used[2] = {0, 0};  // copies in all and by barrier row; items by query buffer
-            uint32_t fixed = 0;  // last value tiles, a bit a ring slot: how often modulo 2
             bool alive = true;
-            // the CTA's walk along the line
-            int64_t at = ds_cut(line, blockIdx.x, shares);
+            // The CTA's walk along the line, item after item (of one KV head h, unit u and part ch of the entry's keys; `at`
+            // lies `on` tiles behind the item's beginning); the entry after the present one is loaded ahead.
+            int64_t at = from;
             const int64_t stop = ds_cut(line, blockIdx.x + 1, shares);
-            int e = 0;
-            DsEntry x{};
-            DsSize sz{};
-            int64_t e_line = 0, e_next = -1;
+            int e = sm.first, h = 0, u = 0, ch = 0, on = 0;
+            SharedEntry x = sm.first_entry, ahead = x;
+            DsSize sz = ds_size(a, DsEntry{x.b, x.row, x.rows, x.key, x.end}, NK);
             if (half) {
-                int lo = 0, hi = entries;  // the last entry that begins at or before it
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.line[mid] <= at) lo = mid; else hi = mid;
-                }
-                e = lo - 1;
+                ahead = ds_load(a.entries + e + 1);
+                const int off = static_cast<int>(at - x.line), uh = off / sz.unit, o = off - uh * sz.unit;
+                h = uh / sz.units;
+                u = uh - h * sz.units;
+                ch = min(o / (kRun * sz.w + kDsExtra), sz.chunks - 1);
+                on = o - ch * (kRun * sz.w + kDsExtra);
             }
             auto find = [&]() {
                 DsItem it{};
                 it.b = -1;
                 while (at < stop) {
-                    while (at >= e_next) {
+                    while (sz.units == 0) {  // an entry without items (the line goes on: there is another)
+                        x = ahead;
                         ++e;
-                        e_line = a.line[e];
-                        e_next = a.line[e + 1];
-                        if (at < e_next) {
-                            bool bad;
-                            x = ds_entry(a, e, bad);
-                            sz = ds_size(a, x, NK);
+                        ahead = ds_load(a.entries + min(e + 1, entries));
+                        sz = ds_size(a, DsEntry{x.b, x.row, x.rows, x.key, x.end}, NK);
+                    }
+                    const int tiles = min(kRun, sz.tiles - ch * kRun), len = min(kDsExtra + tiles * sz.w - on, static_cast<int>(min(stop - at, INT64_C(1) << 30)));
+                    const int t0 = ds_tiles_before(on - kDsExtra, sz.w), t1 = ds_tiles_before(on + len - kDsExtra, sz.w);
+                    const bool some = t1 > t0;
+                    if (some) {
+                        const bool group = e < a.num_groups;
+                        it.b = x.b;
+                        it.row = x.row + u * 2 * P;
+                        it.rows = x.rows - u * 2 * P;
+                        it.h = h;
+                        it.key = x.key + (ch * kRun + t0) * NK;
+                        it.end = x.end;
+                        it.tiles = t1 - t0;
+                        it.pair = it.rows > P;
+                        it.cap = group ? a.group_rows : a.seq_rows;
+                        const int64_t place = x.parts + (h * sz.units + u) * sz.chunks + ch + static_cast<int>(blockIdx.x);
+                        it.part = group ? place * 2 * a.group_rows : a.seq_part0 + (place - group_parts) * 2 * a.seq_rows;
+                    }
+                    at += len;
+                    on = 0;  // (the share ends here if the item does not)
+                    if (++ch == sz.chunks) {
+                        ch = 0;
+                        if (++u == sz.units) {
+                            u = 0;
+                            if (++h == a.H) {
+                                h = 0;
+                                sz.units = 0;
+                            }
                         }
                     }
-                    const int off = static_cast<int>(at - e_line), uh = off / sz.unit, o = off - uh * sz.unit;
-                    const int h = uh / sz.units, u = uh - h * sz.units;
-                    const int ch = min(o / (kRun + kDsExtra), sz.chunks - 1), oc = o - ch * (kRun + kDsExtra);
-                    const int tiles = min(kRun, sz.tiles - ch * kRun);
-                    const int64_t begin = at - oc, end = begin + kDsExtra + tiles;
-                    const int64_t upto = min(end, stop);
-                    const int t0 = max(0, oc - kDsExtra), t1 = static_cast<int>(upto - begin) - kDsExtra;
-                    at = upto;
-                    if (t1 <= t0) continue;
-                    const bool group = e < a.num_groups;
-                    it.b = x.b;
-                    it.row = x.row + u * 2 * P;
-                    it.rows = x.rows - u * 2 * P;
-                    it.h = h;
-                    it.key = x.key + (ch * kRun + t0) * NK;
-                    it.end = x.end;
-                    it.tiles = t1 - t0;
-                    it.pair = it.rows > P;
-                    it.cap = group ? a.group_rows : a.seq_rows;
-                    const int64_t place = a.items[e] + uh * sz.chunks + ch + static_cast<int>(blockIdx.x);
-                    it.part = group ? place * 2 * a.group_rows : a.seq_part0 + (place - group_parts) * 2 * a.seq_rows;
-                    break;
+                    if (some) break;
                 }
                 return it;
             };
@@ -403,17 +458,9 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                     }
                     alive = __shfl_sync(0xffffffffu, ok, 0) != 0;
                 }
-                // the value tile that holds the end of the keys, if its last block is not wholly theirs (codes are finite)
-                const int fix = !kInt8 && item.end % kBlock != 0 && item.key + item.tiles * NK >= item.end ? item.tiles - 1 : -1;
                 constexpr int kBatch = 32 / (NK / kBlock);  // tiles whose cache rows the lanes hold
                 int64_t row = 0;
-                int fix_slot = 0, fix_row = 0, fix_copy = 0;
                 for (int j = 0; alive && j < item.tiles; ++j) {
-                    if (half && j == min(2, item.tiles - 1)) {  // the next item (its search takes loads: behind the first copies)
-                        after = find();
-                        alive = publish(k + 1, after);
-                        if (!alive) break;
-                    }
                     if (j % kBatch == 0) {
                         const int t = item.key + j * NK + lane * kBlock;
                         row = a.cache_tokens;  // past the end: a box past the cache is zeros
@@ -425,7 +472,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                             }
                         }
                     }
-                    const int set = item.pair ? 0 : 1 + (j & 1);
+                    const int set = item.pair ? 0 : 1 + ((j + k) & 1);
 #pragma unroll
                     for (int kind = 0; kind < 2; ++kind) {  // K, V
                         const int st = slot % kStages, copy = set == 0 ? sent[0] : (set == 1 ? sent[1] : sent[2]);
@@ -445,7 +492,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                             }
                         }
                         if (!kInt8 && lane == 0) {
-                            uint64_t* bar = kind == 1 && j == fix ? &sm.v_last[st] : &sm.full[set][copy % kStages];
+                            uint64_t* bar = &sm.full[set][copy % kStages];
                             if (slot >= kStages) ok = wait(&sm.empty[st], ((slot / kStages) - 1) & 1);
                             if (ok) {
                                 if (set > 0 && !half) mbar_arrive(&sm.empty[st]);  // (for the stage that does not take the tile)
@@ -456,9 +503,6 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                                                 item.h, static_cast<int>(r[c]));
                             }
                         }
-                        fix_slot = st;
-                        fix_row = set;
-                        fix_copy = copy;
                         ++slot;
                         if (set == 0) ++sent[0];
                         else if (set == 1) ++sent[1];
@@ -468,25 +512,13 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                             break;
                         }
                     }
-                }
-                if (half && fix >= 0 && alive) {  // ---- values past the end become zero (they may be anything; the last copy is theirs)
-                    alive = __all_sync(0xffffffffu, wait(&sm.v_last[fix_slot], fixed >> fix_slot & 1));
-                    if (!alive) break;
-                    fixed ^= 1u << fix_slot;
-                    for (int y = (item.end - item.key - fix * NK) * 16 + lane; y < NK * 16; y += 32) {
-                        const int key = y >> 4, c = y & 15;  // (a whole row: no swizzle to undo)
-                        *reinterpret_cast<uint4*>(sm.ring[fix_slot] + (c >> 3) * kHalf + key * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        uint64_t* bar = &sm.full[fix_row][fix_copy % kStages];
-                        mbar_arrive(bar);
-                        mbar_arrive(bar);
+                    if (half && alive && j == min(1, item.tiles - 1)) {  // the next item, behind the first copies
+                        after = find();
+                        alive = publish(k + 1, after);
                     }
                 }
             }
-            if (lane == 0 && !half) {  // no copy in flight at the end (a last value tile's barrier was warp 10's to wait for)
+            if (lane == 0 && !half) {  // no copy in flight at the end
                 for (int s = 0; s < 2; ++s) {
                     const int used = s ? q_used[1] : q_used[0];
                     if (used > 0) wait(&sm.q_full[s], (used - 1) & 1);
@@ -511,26 +543,33 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                 __syncwarp();
                 if (lane == 0) passed(k);
                 if (item.b < 0) break;
-                // scales of the thread's key in tile j (zeros past the end: their weights are zero whatever lies there)
+                // Scales of the thread's key in tile j (zeros past the end: their weights are zero whatever lies there); the lanes
+                // hold the cache rows of the next 32 blocks.
+                constexpr int kBatch = 32 / (NK / kBlock);
+                int64_t row = -1;
+                auto rows_from = [&](int j) {
+                    const int p = item.key + j * NK + lane * kBlock;
+                    row = j < item.tiles && p < item.end ? block_row(a.cache, item.b, p) : -1;
+                };
                 auto scales_of = [&](int j) {
+                    const int64_t r = __shfl_sync(0xffffffffu, row, (j % kBatch) * (NK / kBlock) + key / kBlock);
                     const int p = item.key + j * NK + key;
                     float2 y = make_float2(0.f, 0.f);
-                    if (j < item.tiles && p < item.end) {
-                        const int64_t row = block_row(a.cache, item.b, p & ~(kBlock - 1));
-                        if (row >= 0) {
-                            const int64_t at = (row + (p & (kBlock - 1))) * a.H + item.h;
-                            y = make_float2(a.k_scale[at], a.v_scale[at]);
-                        }
+                    if (j < item.tiles && p < item.end && r >= 0) {
+                        const int64_t at = (r + (key & (kBlock - 1))) * a.H + item.h;
+                        y = make_float2(a.k_scale[at], a.v_scale[at]);
                     }
                     return y;
                 };
+                rows_from(0);
                 float2 next = scales_of(0);
                 for (int j = 0; alive && j < item.tiles; ++j, ++tiles) {
-                    const int set = item.pair ? 0 : 1 + (j & 1);
+                    const int set = item.pair ? 0 : 1 + ((j + k) & 1);
                     if (piece == 0) {
                         sm.sc[tiles % Cfg::kScales][0][key] = next.x;
                         sm.sc[tiles % Cfg::kScales][1][key] = next.y;
                     }
+                    if ((j + 1) % kBatch == 0) rows_from(j + 1);
                     next = scales_of(j + 1);
 #pragma unroll 1
                     for (int kind = 0; kind < 2; ++kind, ++slot) {
@@ -539,22 +578,30 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                         alive = __all_sync(0xffffffffu, ok);
                         if (!alive) break;
                         if (set > 0 && t == 0) mbar_arrive(&sm.empty[st]);  // (for the stage that does not take the tile)
-                        const uint8_t* src = sm.codes[from] + key * kHeadDim;
-                        uint8_t* dst = sm.ring[st] + key * 128;
-#pragma unroll 2
-                        for (int c = piece * (NK / 16); c < (piece + 1) * (NK / 16); ++c) {  // 16 dims
-                            const uint4 w = *reinterpret_cast<const uint4*>(src + ((c ^ (key & 7)) << 4));
-                            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                            uint32_t o[8];
+                        // (64-key tiles: a half of the dimensions a thread)
+                        const uint32_t x16 = (key & 7) << 4;
+                        uint32_t src = smem_u32(sm.codes[from]) + key * kHeadDim, dst = smem_u32(sm.ring[st]) + key * 128 + piece * kHalf;
+#pragma unroll 1
+                        for (int c0 = piece * (NK / 16); c0 < (piece + 1) * (NK / 16); c0 += 4, dst += kHalf) {  // 64 dims
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const uint32_t even = i8_even_to_bf16(ws[x]), odd = i8_even_to_bf16(ws[x] >> 8);
-                                o[2 * x] = __byte_perm(even, odd, 0x5410);
-                                o[2 * x + 1] = __byte_perm(even, odd, 0x7632);
+                            for (int i = 0; i < 4; i += 2) {
+                                uint4 w[2];
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) w[n] = ds_ld_shared(src + (((c0 + i + n) << 4) ^ x16));
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    const uint32_t ws[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+                                    uint32_t o[8];
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        const uint32_t even = i8_even_to_bf16(ws[x]), odd = i8_even_to_bf16(ws[x] >> 8);
+                                        o[2 * x] = __byte_perm(even, odd, 0x5410);
+                                        o[2 * x + 1] = __byte_perm(even, odd, 0x7632);
+                                    }
+                                    ds_st_shared(dst + ((2 * (i + n)) << 4 ^ x16), make_uint4(o[0], o[1], o[2], o[3]));
+                                    ds_st_shared(dst + ((2 * (i + n) + 1) << 4 ^ x16), make_uint4(o[4], o[5], o[6], o[7]));
+                                }
                             }
-                            uint8_t* to = dst + (c >> 2) * kHalf;  // (64 dims a half)
-                            *reinterpret_cast<uint4*>(to + (((2 * (c & 3)) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
@@ -585,7 +632,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                     if (!ok) break;
                     passed(k);
                     if (item.b < 0) break;
-                    const int count = count_of(item, s), step = item.pair ? 1 : 2, j0 = item.pair ? 0 : s;
+                    const int count = count_of(item, k, s), step = item.pair ? 1 : 2, j0 = first_of(item, k, s);
                     const bool pair = item.pair;
                     const int row = pair ? 0 : 1 + s;
                     auto landed = [&]() {  // the stage's next copy
@@ -631,8 +678,10 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                     } else {
                         free_q(false);
                     }
-                    // the other stage is through with its last item: its turns have been taken
-                    if (k > 0) ok = wait(&sm.item_done, (k - 1) & 1);
+                    // The other stage is through with the item before the last one (no barrier is then two phases behind), and for
+                    // turns with the last one (its turns have been taken).
+                    if (k > 1) ok = wait(&sm.item_done[k & 1], ((k >> 1) - 1) & 1);
+                    if (pair && k > 0) ok = ok && wait(&sm.item_done[(k - 1) & 1], ((k - 1) >> 1) & 1);
                     for (int c = 0; ok && c < count; ++c) {
                         // pairs take turns: values of tile c, scores of the next (whatever can be waited for is, first)
                         const int j = j0 + step * c;
@@ -678,7 +727,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                     }
                     slots += 2 * item.tiles;
                     tiles += count;
-                    if (ok) mbar_arrive(&sm.item_done);
+                    if (ok) mbar_arrive(&sm.item_done[k & 1]);
                 }
                 if (issued) {  // every matrix instruction done before tensor memory is given back
                     tc_commit(&sm.drain[s]);
@@ -688,14 +737,14 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             __syncwarp();
         }
     } else {
-        // 168 x 384 registers at launch: 208 x 256 + 88 x 128; int8 128 x 512: 192 x 256 + 64 x 256
-        if constexpr (kInt8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // 168 x 384 registers at launch: 200 x 256 + 104 x 128; int8 128 x 512: 184 x 256 + 72 x 256
+        if constexpr (kInt8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---------------- softmax group s: thread = row of its M tile
         const int s = warp >> 2, m = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // (32 (warp % 4)) << 16
         const uint32_t s_addr = tmem + s * 128 + lanes, o_addr = tmem + 256 + s * 128 + lanes;
-        int tiles = 0, done = 0, before = 0;  // running: the stage's tiles, items it had tiles of, key tiles of earlier items
+        int tiles = 0, done = 0, before = 0, single = 0;  // running: the stage's tiles, items it had tiles of; key tiles of earlier items; the stage's of one M tile
         bool alive = true;
         for (int k = 0; alive; ++k) {
             DsItem item;
@@ -704,7 +753,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             __syncwarp();
             if (lane == 0) passed(k);
             if (item.b < 0) break;
-            const int count = count_of(item, s);
+            const int count = count_of(item, k, s), j0 = first_of(item, k, s), step = item.pair ? 1 : 2;
             const int rows = min(item.rows - (item.pair ? s * P : 0), P) * a.G;  // of the M tile
             const bool mine = m < rows, busy = (m & ~31) < rows;                 // busy: some row of the warp is
             float top = -INFINITY, sum = 0.f;         // maximum in use (log2 domain), sum of weights
@@ -737,9 +786,24 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                 }
             };
             for (int c = 0; alive && c < count; ++c) {
-                const int t0 = item.key + (item.pair ? c : 2 * c + s) * NK;
+                const int t0 = item.key + (j0 + step * c) * NK;
                 alive = __all_sync(0xffffffffu, wait(&sm.s_full[s], (tiles + c) & 1));
                 if (!alive) break;
+                const bool edge = t0 + NK > item.end;
+                const int seen = item.end - t0;  // keys of the tile
+                if (!kInt8 && edge && item.end % kBlock != 0) {
+                    // Values past the end, which may be anything, become zero up to the end of their block (past the cache a copy
+                    // fills with zeros).  One M tile: groups end with a block.
+                    const int copy = 2 * (single + c) + 1, slot = (2 * (before + j0 + step * c) + 1) % kStages;
+                    alive = __all_sync(0xffffffffu, wait(&sm.full[1 + s][copy % kStages], (copy / kStages) & 1));
+                    if (!alive) break;
+                    for (int y = seen * 16 + m; y < (seen + kBlock - 1) / kBlock * kBlock * 16; y += 128) {
+                        const int key = y >> 4, part = y & 15;  // (a whole row: no swizzle to undo)
+                        *reinterpret_cast<uint4*>(sm.ring[slot] + (part >> 3) * kHalf + key * 128 + (part & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
                 if (!busy) {  // (the tile's other warps have rows)
                     if (lane == 0) {
                         mbar_arrive(&sm.p_full[s][0]);
@@ -750,9 +814,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                 tc_fence_after();
                 if (kParts > 1 && c > 0 && c % 2 == 0) collect();
                 // int8: scales of the tile's keys and values
-                const auto& sc = sm.sc[kInt8 ? (before + (item.pair ? c : 2 * c + s)) % Cfg::kScales : 0];
-                const bool edge = t0 + NK > item.end;
-                const int seen = item.end - t0;  // keys of the tile
+                const uint32_t k_sc = smem_u32(sm.sc[kInt8 ? (before + j0 + step * c) % Cfg::kScales : 0][0]), v_sc = k_sc + NK * 4;
                 auto raise = [&](float now) {  // the maximum in use is now's or within kDsSlack of it
                     if (c == 0) {
                         top = now;
@@ -778,14 +840,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                         dp_ld32(s_addr + kSAt + 32 * q, x);
                         tmem_ld_wait();
                         if constexpr (kInt8) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(&sc[0][32 * q + i]);
-                                x[i] *= f.x;
-                                x[i + 1] *= f.y;
-                                x[i + 2] *= f.z;
-                                x[i + 3] *= f.w;
-                            }
+                            ds_times32(x, k_sc + 128 * q);
                         }
                         if (edge) {
 #pragma unroll
@@ -823,14 +878,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                             add = __fadd2_rn(add, make_float2(x[2 * i], x[2 * i + 1]));
                         }
                         if constexpr (kInt8) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 v = *reinterpret_cast<const float4*>(&sc[1][32 * q + i]);
-                                x[i] *= v.x;
-                                x[i + 1] *= v.y;
-                                x[i + 2] *= v.z;
-                                x[i + 3] *= v.w;
-                            }
+                            ds_times32(x, v_sc + 128 * q);
                         }
 #pragma unroll
                         for (int part = 0; part < kParts; ++part) {
@@ -852,32 +900,31 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[s][0]);
                 } else {
+                    float f = a.scale_log2;
+                    if (edge) {  // keys past the end: the tile's scores as they are to be go back to where they are read from
+#pragma unroll 1
+                        for (int q = 0; q < NK / 32; ++q) {
+                            float x[32];
+                            dp_ld32(s_addr + 32 * q, x);
+                            tmem_ld_wait();
+                            if constexpr (kInt8) ds_times32(x, k_sc + 128 * q);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                x[i] = 32 * q + i < seen ? x[i] * f : -INFINITY;
+                            }
+                            dp_st32(s_addr + 32 * q, reinterpret_cast<const uint32_t*>(x));
+                        }
+                        dp_st_wait();
+                        f = 1.f;
+                    }
                     float x[NK], big[NK / 64];
 #pragma unroll
                     for (int q = 0; q < NK / 64; ++q) dp_ld64_max(s_addr + 64 * q, x + 64 * q, big[q]);
-                    float f = a.scale_log2;
                     tmem_ld_wait();
-                    if constexpr (kInt8) {
-#pragma unroll
-                        for (int i = 0; i < NK; i += 4) {
-                            const float4 ks = *reinterpret_cast<const float4*>(&sc[0][i]);
-                            const float2 y0 = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(ks.x, ks.y));
-                            const float2 y1 = __fmul2_rn(make_float2(x[i + 2], x[i + 3]), make_float2(ks.z, ks.w));
-                            x[i] = y0.x, x[i + 1] = y0.y, x[i + 2] = y1.x, x[i + 3] = y1.y;
-                        }
-                    }
                     float now;
-                    if (edge) {  // keys past the end; the scores are then not those that the load took the maximum of
+                    if (kInt8 && !edge) {
 #pragma unroll
-                        for (int i = 0; i < NK; ++i) x[i] = i < seen ? x[i] * f : -INFINITY;
-                        f = 1.f;
-                        float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int i = 0; i < NK; i += 4)
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) y[z] = fmaxf(y[z], x[i + z]);
-                        now = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                    } else if constexpr (kInt8) {
+                        for (int q = 0; q < NK / 32; ++q) ds_times32(x + 32 * q, k_sc + 128 * q);
                         float y[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
                         for (int i = 4; i < NK; i += 4)
@@ -905,13 +952,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                                 add[i & 1] = __fadd2_rn(add[i & 1], make_float2(z[2 * i], z[2 * i + 1]));
                             }
                             if constexpr (kInt8) {
-#pragma unroll
-                                for (int i = 0; i < 32; i += 4) {
-                                    const float4 vs = *reinterpret_cast<const float4*>(&sc[1][64 * h2 + 32 * q + i]);
-                                    const float2 y0 = __fmul2_rn(make_float2(z[i], z[i + 1]), make_float2(vs.x, vs.y));
-                                    const float2 y1 = __fmul2_rn(make_float2(z[i + 2], z[i + 3]), make_float2(vs.z, vs.w));
-                                    z[i] = y0.x, z[i + 1] = y0.y, z[i + 2] = y1.x, z[i + 3] = y1.y;
-                                }
+                                ds_times32(z, v_sc + 256 * h2 + 128 * q);
                             }
 #pragma unroll
                             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(z[2 * i], z[2 * i + 1]);
@@ -928,6 +969,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             if (alive && count > 0) alive = __all_sync(0xffffffffu, wait(&sm.o_full[s], done++ & 1));
             tiles += count;
             before += item.tiles;
+            if (!item.pair) single += count;
             if (!alive) break;
             if (!busy) continue;
             // ---------------- the part: O, maximum, sum
@@ -998,24 +1040,15 @@ __global__ void __launch_bounds__(512, kResident) dense_shared_join(const Shared
         }
         own_row[tid] = row;
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (r == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the CTAs found wrong
-        uint32_t e = 0;
-        for (int c = lane; c < grid; c += 32) e |= a.err_slots[c];
-        e = __reduce_or_sync(0xffffffffu, e);
-        if (lane == 0) *a.err = e;
-    }
     __syncthreads();
+    // ---- the row's own keys, while the parts are still being made (what came before dense_shared_kernel is done: its CTAs
+    // wait for that before they let this kernel begin)
 #pragma unroll
     for (int i = 0; i < kDecodeMaxRows; ++i) there &= own_row[i] >= 0;
-    if (!there) return;
-    const int entries = a.num_groups + a.num_seqs, group_parts = a.items[a.num_groups];
-    const int64_t line = a.line[entries];
-    if (group_parts > a.group_parts_most || a.items[entries] - group_parts > a.seq_parts_most) return;
+    const int own_keys = there ? keys : 0;
     const int64_t q_row = (static_cast<int64_t>(r) * a.H + h) * a.G;
-    for (int i = warp; i < a.G * keys; i += warps) {
-        const int gh = i / keys, key = i - gh * keys;
+    for (int i = warp; i < a.G * own_keys; i += warps) {
+        const int gh = i / own_keys, key = i - gh * own_keys;
         const uint2 qw = *reinterpret_cast<const uint2*>(a.q + (q_row + gh) * kHeadDim + 4 * lane);
         float k[4], f = a.scale_log2;
         if constexpr (kInt8) {
@@ -1033,11 +1066,12 @@ __global__ void __launch_bounds__(512, kResident) dense_shared_join(const Shared
     }
     __syncthreads();
     const int d4s = kHeadDim / 4 / gridDim.z, gh = tid % a.G, d4 = tid / a.G + blockIdx.z * d4s;
-    if (tid >= a.G * d4s) return;
+    if (tid >= a.G * d4s) there = false;
     float top = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < keys; ++i) top = fmaxf(top, own[gh][i]);
-    for (int i = 0; i < keys; ++i) {
+    const int mine = there ? own_keys : 0;
+    for (int i = 0; i < mine; ++i) top = fmaxf(top, own[gh][i]);
+    for (int i = 0; i < mine; ++i) {
         const float y = own[gh][i], w = top == -INFINITY ? (y == y ? 0.f : y) : dp_exp2(y - top);
         float v[4];
         if constexpr (kInt8) {
@@ -1054,20 +1088,33 @@ __global__ void __launch_bounds__(512, kResident) dense_shared_join(const Shared
         o.z = fmaf(w, v[2], o.z);
         o.w = fmaf(w, v[3], o.w);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (r == 0 && h == 0 && blockIdx.z == 0 && warp == 0) {  // what the CTAs found wrong
+        uint32_t e = 0;
+        for (int c = lane; c < grid; c += 32) e |= a.err_slots[c];
+        e = __reduce_or_sync(0xffffffffu, e);
+        if (lane == 0) *a.err = e;
+    }
+    if (!there) return;
+    const int entries = a.num_groups + a.num_seqs, group_parts = a.entries[a.num_groups].parts;
+    const int64_t line = a.entries[entries].line;
+    if (group_parts > a.group_parts_most || a.entries[entries].parts - group_parts > a.seq_parts_most) return;
     // ---- parts of entry e, some at a time
     const int shares = ds_shares(line, grid), P = 128 / a.G;
     auto join = [&](int e, const DsEntry& y, bool group) {
         const DsSize s = ds_size(a, y, NK);
         if (s.units == 0) return;
+        const SharedEntry at = ds_load(a.entries + e);
         const int run = kDsPartKeys / NK, i = r - y.row, tile = i / P, u = tile / 2, uh = h * s.units + u;
         const bool pair = y.rows - u * 2 * P > P;
         const int cap = group ? a.group_rows : a.seq_rows, m = (i - tile * P) * a.G + gh;
         const int stages = pair ? 1 : 2, s0 = pair ? tile & 1 : 0;
         for (int ch = 0; ch < s.chunks; ++ch) {
-            const int64_t begin = a.line[e] + static_cast<int64_t>(uh) * s.unit + ch * (run + kDsExtra) + kDsExtra;
+            const int64_t begin = at.line + static_cast<int64_t>(uh) * s.unit + ch * (run * s.w + kDsExtra) + kDsExtra;
             const int tiles = min(run, s.tiles - ch * run);
-            const int c0 = ds_owner(line, begin, shares), c1 = ds_owner(line, begin + tiles - 1, shares);
-            const int64_t place = a.items[e] + uh * s.chunks + ch + c0;
+            const int c0 = ds_owner(line, begin, shares), c1 = ds_owner(line, begin + (tiles - 1) * s.w, shares);
+            const int64_t place = at.parts + uh * s.chunks + ch + c0;
             const int64_t row0 = (group ? place * 2 * cap : a.seq_part0 + (place - group_parts) * 2 * cap) + s0 * cap;
             const int count = (c1 - c0 + 1) * stages, step = pair ? 2 * cap : cap;
             constexpr int kAtOnce = kResident > 1 ? 4 : 8;

@@ -274,6 +274,13 @@ cudaError_t run_dense_window(const DenseArgs& a, int items, cudaStream_t stream)
 int dense_decode_shares(int64_t units, int H);  // CTAs for so many blocks
 cudaError_t run_dense_decode(const DenseArgs& a, int shares, cudaStream_t stream);
 
+// A group or sequence on the line of key tiles: where it begins, parts before it, and its rows [row, row + rows), which see
+// all keys [key, end) of the table of sequence b.
+struct __align__(16) SharedEntry {
+    int64_t line;
+    int32_t parts, b, row, rows, key, end;
+};
+
 // Attention over every cached position for a decode family whose groups of sequences share a prefix.
 struct SharedArgs {
     const uint16_t* q;
@@ -293,8 +300,7 @@ struct SharedArgs {
     const CUtensorMap* q_map;  // host copies: q as (D, H*G, rows), box 64 x G x 128 / G; the caches (kv_map)
     const CUtensorMap* k_map;
     const CUtensorMap* v_map;
-    int64_t* line;             // [num_groups + num_seqs + 1] places of the groups and the sequences on the line of key tiles
-    int32_t* items;            // the same of the parts that the line's items make
+    SharedEntry* entries;      // [num_groups + num_seqs + 1] groups, sequences, the line's length and parts
     int64_t group_parts_most, seq_parts_most;  // parts that there is room for, beside one a CTA
     int group_rows, seq_rows;  // rows of a part's stage: of a group's items, of a sequence's
     int64_t seq_part0;         // first row of the sequences' parts

@@ -336,7 +336,7 @@ bool dense_shared(const msa_problem* p) { return p->num_groups > 0; }
 
 struct SharedLayout {
     msa::SharedRoom room;
-    size_t err = 0, err_slots = 0, line = 0, items = 0, part_ml = 0, part_o = 0, total = 0;
+    size_t err = 0, err_slots = 0, entries = 0, part_ml = 0, part_o = 0, total = 0;
 };
 
 SharedLayout shared_layout(const msa_problem* p) {
@@ -347,10 +347,8 @@ SharedLayout shared_layout(const msa_problem* p) {
     size_t off = 256;
     l.err_slots = off;
     off = align256(off + msa::kDenseMaxShares * sizeof(uint32_t));
-    l.line = off;
-    off = align256(off + entries * sizeof(int64_t));
-    l.items = off;
-    off = align256(off + entries * sizeof(int32_t));
+    l.entries = off;
+    off = align256(off + entries * sizeof(msa::SharedEntry));
     l.part_ml = off;
     off = align256(off + rows * 2 * sizeof(float));
     l.part_o = off;
@@ -1094,8 +1092,7 @@ static msa_status dense_shared_forward(const msa_problem* p, const void* q, cons
     a.q_map = &qm;
     a.k_map = &km;
     a.v_map = &vm;
-    a.line = reinterpret_cast<int64_t*>(ws + l.line);
-    a.items = reinterpret_cast<int32_t*>(ws + l.items);
+    a.entries = reinterpret_cast<msa::SharedEntry*>(ws + l.entries);
     a.group_parts_most = l.room.group_parts;
     a.seq_parts_most = l.room.seq_parts;
     a.group_rows = l.room.group_rows;
