@@ -39,7 +39,7 @@ constexpr int kDsThreads = 384, kDsThreadsInt8 = 512;
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
 constexpr int kDsPartKeys = 32768;  // most keys of a part
 // Lengths on the line: a key tile of one M tile, of two, and what an item counts for besides (going on to another one).
-constexpr int kDsSingle = 4, kDsPair = 6, kDsExtra = 8;
+constexpr int kDsSingle = 2, kDsPair = 3, kDsExtra = 2;
 constexpr int kDsInfo = 4;          // items published ahead
 constexpr float kDsSlack = 8.f;     // log2 by which the running maximum may lag
 
@@ -1010,10 +1010,10 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
     if (tid == 0) a.err_slots[blockIdx.x] = sm.err;
 }
 
-// Joins the parts of a row's pairs of KV head h with the row's own keys.  CTA (row, h, z): quarter, half or all of the 128
+// Joins the parts of a row's pairs of KV head h with the row's own keys.  CTA (row, h, z): a quarter or half of the 128
 // dimensions, a thread 4 of them of one query head.
 template <bool kInt8, int kResident>
-__global__ void __launch_bounds__(512, kResident) dense_shared_join(const SharedArgs a, int grid, int NK) {
+__global__ void __launch_bounds__(256, kResident) dense_shared_join(const SharedArgs a, int grid, int NK) {
     __shared__ float own[kMaxGroup][kDecodeMaxRows];  // scores of the row's own keys (log2 domain)
     __shared__ int64_t own_row[kDecodeMaxRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, h = blockIdx.y, r = blockIdx.x;
@@ -1185,17 +1185,17 @@ static cudaError_t launch_shared(const SharedArgs& a, int grid, cudaStream_t str
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, *a.q_map, *a.k_map, *a.v_map, a)) != cudaSuccess) return e;
-    // few rows: the dimensions over several CTAs
+    // the dimensions over two CTAs, over four of few rows (one: 78 us for 75 where 73 rows of 8 x 5 heads are joined)
     const int64_t blocks = static_cast<int64_t>(a.total_rows) * a.H;
-    const int z = blocks * 4 <= 2 * device_sm_count() ? 4 : (blocks * 2 <= 2 * device_sm_count() ? 2 : 1);
+    const int z = blocks * 4 <= 2 * device_sm_count() ? 4 : 2;
     const int threads = (a.G * (kHeadDim / 4 / z) + 31) / 32 * 32;
     cfg.gridDim = dim3(static_cast<unsigned>(a.total_rows), static_cast<unsigned>(a.H), static_cast<unsigned>(z));
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = 0;
-    // two CTAs an SM where they are more than the SMs (256 rows of 4 x 16 heads: 30 us for 58; few rows are slower by 1 to 2)
+    // four CTAs an SM where they are many (three or five: 3% to 8% more at 73 and 256 rows); few take more loads at once
     const bool many = blocks > device_sm_count();
-    auto* join = a.kv_int8 ? (many ? dense_shared_join<true, 2> : dense_shared_join<true, 1>)
-                           : (many ? dense_shared_join<false, 2> : dense_shared_join<false, 1>);
+    auto* join = a.kv_int8 ? (many ? dense_shared_join<true, 4> : dense_shared_join<true, 1>)
+                           : (many ? dense_shared_join<false, 4> : dense_shared_join<false, 1>);
     return cudaLaunchKernelEx(&cfg, join, a, grid, DsCfg<kParts, kInt8>::NK);
 }
 
