@@ -39,7 +39,7 @@ constexpr int kDsThreads = 384, kDsThreadsInt8 = 512;
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
 constexpr int kDsPartKeys = 32768;  // most keys of a part
 // Lengths on the line: a key tile of one M tile, of two, and what an item counts for besides (going on to another one).
-constexpr int kDsSingle = 2, kDsPair = 3, kDsExtra = 2;
+constexpr int kDsSingle = 2, kDsPair = 3, kDsExtra = 3;
 constexpr int kDsInfo = 4;          // items published ahead
 constexpr float kDsSlack = 8.f;     // log2 by which the running maximum may lag
 
@@ -1012,40 +1012,49 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
 
 // Joins the parts of a row's pairs of KV head h with the row's own keys.  CTA (row, h, z): a quarter or half of the 128
 // dimensions, a thread 4 of them of one query head.
+struct DsRun {  // parts of a row's M tile that lie behind one another: `count` of `cap` rows, `step` rows apart
+    int64_t row0;
+    int count, step, cap, m;  // m: row of its first head in a part
+};
+
 template <bool kInt8, int kResident>
 __global__ void __launch_bounds__(256, kResident) dense_shared_join(const SharedArgs a, int grid, int NK) {
     __shared__ float own[kMaxGroup][kDecodeMaxRows];  // scores of the row's own keys (log2 domain)
     __shared__ int64_t own_row[kDecodeMaxRows];
+    __shared__ DsRun runs[32];
+    __shared__ int row_keys, num_runs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, h = blockIdx.y, r = blockIdx.x;
-    // ---- the row's sequence: the last that begins at or before it, 32 candidates at a time
-    int lo = 0, hi = a.num_seqs;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.cu_rows[at] <= r);
-        const int last = le ? 31 - __clz(le) : 0;
-        lo += last * step;
-        hi = min(lo + step, hi);
-    }
-    int g;
-    bool bad;
-    const DsEntry x = ds_seq(a, lo, g, bad);
-    bool there = x.rows > 0 && r >= x.row && r < x.row + x.rows;
-    const int keys = there ? r - x.row + 1 : 0;  // its own: x.end .. x.end + keys - 1
-    if (tid < kDecodeMaxRows) {
+    // Where everything lies is found out by one warp (by all of them: 1,360 instructions a warp, and 37 us for 32 at 256 rows
+    // of 4 x 16 heads, by itself).
+    int lo = 0, g = -1, own_keys = 0;
+    DsEntry x{};
+    if (warp == 0) {  // ---- the row's sequence: the last that begins at or before it, 32 candidates at a time
+        int hi = a.num_seqs;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const uint32_t le = __ballot_sync(0xffffffffu, at < hi && a.cu_rows[at] <= r);
+            const int last = le ? 31 - __clz(le) : 0;
+            lo += last * step;
+            hi = min(lo + step, hi);
+        }
+        bool bad;
+        x = ds_seq(a, lo, g, bad);
+        const int keys = x.rows > 0 && r >= x.row && r < x.row + x.rows ? r - x.row + 1 : 0;  // its own: x.end .. x.end + keys - 1
         int64_t row = 0;
-        if (tid < keys) {
-            const int t = x.end + tid;
+        if (lane < keys) {
+            const int t = x.end + lane;
             row = block_row(a.cache, x.b, t & ~(kBlock - 1));
             if (row >= 0) row = (row + (t & (kBlock - 1))) * a.H + h;
         }
-        own_row[tid] = row;
+        own_keys = __any_sync(0xffffffffu, row < 0) ? 0 : keys;
+        if (lane < own_keys) own_row[lane] = row;
+        if (lane == 0) row_keys = own_keys;
     }
     __syncthreads();
+    own_keys = row_keys;
+    bool there = own_keys > 0;
     // ---- the row's own keys, while the parts are still being made (what came before dense_shared_kernel is done: its CTAs
     // wait for that before they let this kernel begin)
-#pragma unroll
-    for (int i = 0; i < kDecodeMaxRows; ++i) there &= own_row[i] >= 0;
-    const int own_keys = there ? keys : 0;
     const int64_t q_row = (static_cast<int64_t>(r) * a.H + h) * a.G;
     for (int i = warp; i < a.G * own_keys; i += warps) {
         const int gh = i / own_keys, key = i - gh * own_keys;
@@ -1096,36 +1105,64 @@ __global__ void __launch_bounds__(256, kResident) dense_shared_join(const Shared
         e = __reduce_or_sync(0xffffffffu, e);
         if (lane == 0) *a.err = e;
     }
-    if (!there) return;
-    const int entries = a.num_groups + a.num_seqs, group_parts = a.entries[a.num_groups].parts;
-    const int64_t line = a.entries[entries].line;
-    if (group_parts > a.group_parts_most || a.entries[entries].parts - group_parts > a.seq_parts_most) return;
-    // ---- parts of entry e, some at a time
-    const int shares = ds_shares(line, grid), P = 128 / a.G;
-    auto join = [&](int e, const DsEntry& y, bool group) {
-        const DsSize s = ds_size(a, y, NK);
-        if (s.units == 0) return;
-        const SharedEntry at = ds_load(a.entries + e);
-        const int run = kDsPartKeys / NK, i = r - y.row, tile = i / P, u = tile / 2, uh = h * s.units + u;
-        const bool pair = y.rows - u * 2 * P > P;
-        const int cap = group ? a.group_rows : a.seq_rows, m = (i - tile * P) * a.G + gh;
-        const int stages = pair ? 1 : 2, s0 = pair ? tile & 1 : 0;
-        for (int ch = 0; ch < s.chunks; ++ch) {
-            const int64_t begin = at.line + static_cast<int64_t>(uh) * s.unit + ch * (run * s.w + kDsExtra) + kDsExtra;
-            const int tiles = min(run, s.tiles - ch * run);
-            const int c0 = ds_owner(line, begin, shares), c1 = ds_owner(line, begin + (tiles - 1) * s.w, shares);
-            const int64_t place = at.parts + uh * s.chunks + ch + c0;
-            const int64_t row0 = (group ? place * 2 * cap : a.seq_part0 + (place - group_parts) * 2 * cap) + s0 * cap;
-            const int count = (c1 - c0 + 1) * stages, step = pair ? 2 * cap : cap;
+    if (own_keys == 0) return;
+    // ---- the parts, some runs and parts at a time
+    const int groups = a.num_groups, entries = groups + a.num_seqs;
+    int chunk = 0;  // (warp 0: the next part of the group's keys, then of the sequence's)
+    auto make_runs = [&]() {
+        const SharedEntry total = ds_load(a.entries + entries);
+        const int group_parts = a.entries[groups].parts;
+        int n = -1;
+        if (group_parts <= a.group_parts_most && total.parts - group_parts <= a.seq_parts_most) {
+            const int P = 128 / a.G, shares = ds_shares(total.line, grid), run = kDsPartKeys / NK;
+            DsSize sg{};
+            SharedEntry eg{};
+            if (g >= 0) {
+                eg = ds_load(a.entries + g);
+                sg = ds_size(a, DsEntry{eg.b, eg.row, eg.rows, eg.key, eg.end}, NK);
+            }
+            const DsSize ss = ds_size(a, x, NK);
+            n = min(sg.chunks + ss.chunks - chunk, 32);
+            const bool group = chunk + lane < sg.chunks;
+            const SharedEntry y = group ? eg : ds_load(a.entries + groups + lo);
+            const DsSize s = group ? sg : ss;
+            const int ch = chunk + lane - (group ? 0 : sg.chunks);
+            if (lane < n) {
+                const int i = r - y.row, tile = i < P ? 0 : i / P, u = tile / 2, uh = h * s.units + u;
+                const bool pair = y.rows - u * 2 * P > P;
+                DsRun out;
+                out.cap = group ? a.group_rows : a.seq_rows;
+                out.m = (i - tile * P) * a.G;
+                const int64_t begin = y.line + static_cast<int64_t>(uh) * s.unit + ch * (run * s.w + kDsExtra) + kDsExtra;
+                const int tiles = min(run, s.tiles - ch * run);
+                const int c0 = ds_owner(total.line, begin, shares), c1 = ds_owner(total.line, begin + (tiles - 1) * s.w, shares);
+                const int64_t place = y.parts + uh * s.chunks + ch + c0;
+                out.row0 = (group ? place * 2 * out.cap : a.seq_part0 + (place - group_parts) * 2 * out.cap) + (pair ? tile & 1 : 0) * out.cap;
+                out.count = (c1 - c0 + 1) * (pair ? 1 : 2);  // (one M tile: both stages' parts)
+                out.step = pair ? 2 * out.cap : out.cap;
+                runs[lane] = out;
+            }
+            chunk += n;
+            if (chunk < sg.chunks + ss.chunks) n |= 1 << 8;  // more to come
+        }
+        if (lane == 0) num_runs = n;
+    };
+    do {
+        if (warp == 0) make_runs();
+        __syncthreads();
+        if (num_runs < 0) return;
+        for (int k = 0; k < (num_runs & 255) && there; ++k) {
+            const DsRun run = runs[k];
+            const int m = run.m + gh;
             constexpr int kAtOnce = kResident > 1 ? 4 : 8;
-            for (int i0 = 0; i0 < count; i0 += kAtOnce) {
+            for (int i0 = 0; i0 < run.count; i0 += kAtOnce) {
                 float4 v[kAtOnce];
                 float2 ml[kAtOnce];
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q) {
-                    const int64_t at = row0 + static_cast<int64_t>(min(i0 + q, count - 1)) * step;
+                    const int64_t at = run.row0 + static_cast<int64_t>(min(i0 + q, run.count - 1)) * run.step;
                     ml[q] = *reinterpret_cast<const float2*>(a.part_ml + (at + m) * 2);
-                    v[q] = reinterpret_cast<const float4*>(a.part_o)[at * (kHeadDim / 4) + static_cast<int64_t>(d4) * cap + m];
+                    v[q] = reinterpret_cast<const float4*>(a.part_o)[at * (kHeadDim / 4) + static_cast<int64_t>(d4) * run.cap + m];
                 }
                 float most = top;
 #pragma unroll
@@ -1138,7 +1175,7 @@ __global__ void __launch_bounds__(256, kResident) dense_shared_join(const Shared
                 top = most;
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q) {
-                    if (i0 + q >= count) continue;
+                    if (i0 + q >= run.count) continue;
                     // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
                     const float w = ml[q].x == -INFINITY ? (ml[q].y == ml[q].y ? 0.f : ml[q].y) : dp_exp2(ml[q].x - top);
                     if (w != 0.f) {
@@ -1151,15 +1188,10 @@ __global__ void __launch_bounds__(256, kResident) dense_shared_join(const Shared
                 }
             }
         }
-    };
-    if (g >= 0) {
-        DsEntry y{};
-        int last;
-        bool no;
-        ds_group(a, g, y, last, no);
-        join(g, y, true);
-    }
-    join(a.num_groups + lo, x, false);
+        if (num_runs < 256) break;
+        __syncthreads();  // before the runs are others
+    } while (true);
+    if (!there) return;
     const float inv = 1.f / sum;
     const int64_t at = (q_row + gh) * kHeadDim + 4 * d4;
     if (a.out_bf16)
