@@ -62,7 +62,7 @@ class MsaAppend(C.Structure):
     """Mirror of struct msa_append."""
     _fields_ = [(n, C.c_void_p) for n in ("k", "v", "ik", "q", "iq")] + \
         [(n, C.c_int64) for n in ("k_stride", "v_stride", "ik_stride", "q_stride", "iq_stride")] + \
-        [(n, C.c_void_p) for n in ("k_cache", "v_cache", "ik_cache", "k_scale", "v_scale", "ik_exp", "q_out", "iq_out")]
+        [(n, C.c_void_p) for n in ("k_cache", "v_cache", "ik_cache", "k_scale", "v_scale", "q_out", "iq_out", "ik_exp")]
 
 
 class MsaError(RuntimeError):
@@ -496,7 +496,7 @@ def append_cache(pb: Problem, new_k, new_v, k, v, new_ik=None, ik=None, q=None, 
     elif positions is not None:
         raise ValueError("positions need a rope")
     a = MsaAppend(new_k.data_ptr(), new_v.data_ptr(), ikp, qp, iqp, ks, vs, iks, qs, iqs, k.data_ptr(), v.data_ptr(), ikc,
-                  pb.c.k_scale, pb.c.v_scale, pb.c.ik_exp if ikc else None, qo, iqo)
+                  pb.c.k_scale, pb.c.v_scale, qo, iqo, pb.c.ik_exp if ikc else None)
     ws = torch.empty(APPEND_WORKSPACE_BYTES, dtype=torch.uint8, device=dev) if workspace is None else workspace
     _need(ws, "workspace", torch.uint8, dev)
     with _on(dev):

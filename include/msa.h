@@ -367,9 +367,9 @@ typedef struct msa_append {
     void* ik_cache;
     float* k_scale; /* MSA_KV_INT8: [cache_tokens, H], written; else NULL    */
     float* v_scale;
-    int8_t* ik_exp; /* MSA_IK_INT8 and ik given: [cache_tokens, KH], written; else NULL */
     void* q_out;    /* [total_rows, H*G, D] bf16, contiguous; may be q itself when q_stride = H*G*D */
     void* iq_out;   /* [total_rows, H, Di] bf16, contiguous; may be iq likewise                      */
+    int8_t* ik_exp; /* MSA_IK_INT8 and ik given: [cache_tokens, KH], written; else NULL */
 } msa_append;
 
 /* Rotates the new rows (rope NULL: no rotation) and stores them in the
