@@ -15,9 +15,19 @@
 //   P = 2^(x - m)          a thread a row, written over S (m is raised only where it would grow by more than 8)
 //   O[128, 128] += P V     P from tensor memory, V as it lies
 // Two stages of 128 columns of S and of O: two M tiles that take turns on the tensor pipe, or one M tile whose stages
-// take alternate key tiles.  One CTA per SM; all items' key tiles lie on a line, item after item, that is cut into even
-// shares (an item counts for kDsExtra tiles more, what going on to another one costs); a CTA's shares of items leave
-// their parts in the workspace.
+// take alternate key tiles (the first of an item in turn: items of one tile keep both busy).  One CTA per SM; all items'
+// key tiles lie on a line, item after item, that is cut into even shares; a CTA's shares of items leave their parts in the
+// workspace.  On the line a tile of two M tiles is half as long again as one of a single M tile (1.55 us for 1.0 to 1.4
+// measured), and going on to another item counts for one and a half tiles (tiles of equal length: 3% slower at 256
+// sequences, 11% with several groups; one or two tiles an item: up to 4% slower).
+// The next item is walked to, not divided out: those loads and divisions stood before the copies of a short item (1 to 2 us).
+// Values past the end of a sequence become zero by the softmax warps, as the copying warp cannot go on while it waits for
+// them.  Both together: 157 for 168 us at 256 sequences of one to four tiles.
+//
+// int8 caches.  The tiles land as codes, and four more warps write them as bf16, exactly (7 instructions for 4), into the
+// ring that the products read; a key's scale multiplies its scores and a value's the weights, after their sum.  The codes
+// of a tile become bf16 once for all rows of an item.  A thread's 128 scores take 64 products and no reducing load then:
+// 2.9 us a tile of two M tiles for 1.55; the scales are loaded 32 at a time (one by one as used: 64 for 60 us).
 //
 // dense_shared_join.  A CTA takes a row and a KV head: the row's own keys, then the parts, whose places follow from the
 // same line by arithmetic (slot = item + CTA, which is different for every pair of them that meets, as both ascend along
@@ -26,6 +36,13 @@
 // Numerics.  bf16 outputs: weights as one bf16 (2^-8 at most, at random), and at most 32,768 keys to a part, as the
 // tensor cores cut what an addition loses instead of rounding it (2^-24 an addition of 16 keys).  fp32 outputs: weights
 // as three bf16 parts, NK = 64, O taken from tensor memory every second tile and summed in registers.
+//
+// Bound by the tensor pipe where many rows share (two M tiles: 1.55 us a tile of 128 keys for 1.3 at the pipe's rate), by
+// the chain of one tile's scores, weights and products elsewhere (2.7 us a stage: own positions go at 48 KB a us and SM,
+// about HBM's rate over all SMs), and by its beginning: 5 us to the first copy, 7 to 8 to the first scores.
+// Measured, whole calls of 4 x 16 heads: 64 sequences behind 32,768 positions and 100 to 2,000 of their own, 86 us (prefix
+// once and own positions: 24.6 us of memory, 35.8 of products; without `shared` 408 us); 256 behind 8,192, 138 us; 8 behind
+// 1,984, 19 us; int8, 32 behind 16,384, 57 us; 16 behind 8,192 with fp32 outputs, 36.5 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -38,7 +55,7 @@ namespace msa {
 constexpr int kDsThreads = 384, kDsThreadsInt8 = 512;
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
 constexpr int kDsPartKeys = 32768;  // most keys of a part
-// Lengths on the line: a key tile of one M tile, of two, and what an item counts for besides (going on to another one).
+// Lengths on the line, in half tiles: a key tile of one M tile, of two, and what an item counts for besides.
 constexpr int kDsSingle = 2, kDsPair = 3, kDsExtra = 3;
 constexpr int kDsInfo = 4;          // items published ahead
 constexpr float kDsSlack = 8.f;     // log2 by which the running maximum may lag

@@ -16,6 +16,9 @@
 // Bound by memory: 65 bytes a position and head with codes, 128 without; a group's are read once instead of once a
 // sequence.  With many rows the products take over: eight rows of a head and a block are 16 mma and about 80 other
 // instructions.
+//
+// Measured by itself, cold caches: 4 x 65,536 positions of 4 heads in codes, 24.6 us (68 MB; bf16 keys, twice the bytes, take
+// decode_scan 25); 32 rows that share 65,536 positions, bf16, 26.9 us.  Eleven stages of 16 KB (8 and 12: within 1%).
 #include "common.cuh"
 #include "internal.h"
 

@@ -168,12 +168,15 @@ typedef struct msa_problem {
      * group_starts[g] .. group_starts[g+1]-1; the first group_shared[g]
      * positions of each of them lie in the same cache rows (their block
      * tables begin alike), and every row lies past them (L_b - n_b >=
-     * group_shared[g]).  A statement about the caches, not an option: results
-     * are those of the same call without groups, msa_dense_forward and
-     * msa_forward read what is shared (whole 64-position blocks of it, by the
-     * block table of the group's first sequence) once for the group's rows
-     * instead of once a sequence.  With groups: a block table, and sequences
-     * of 1 to 8 rows only (max_rows_per_seq <= 8). */
+     * group_shared[g]).  A statement about the caches, not an option: outputs
+     * are the formula's with or without it.  msa_dense_forward and msa_forward
+     * read what is shared (whole 64-position blocks of it, by the block table
+     * of the group's first sequence, which needs one even if it has no rows)
+     * once for the group's rows instead of once a sequence; the other entry
+     * points do not look at groups.  With groups: a block table, and sequences
+     * of at most 8 rows (max_rows_per_seq <= 8).  A group that breaks its
+     * bounds, or a row before the end of its group's shared positions, is bad
+     * metadata. */
     int32_t num_groups;          /* at most num_seqs                            */
     int32_t max_shared_len;      /* >= every group_shared (host bound), <= max_cache_len */
     int32_t max_group_rows;      /* >= the rows of every group (host bound)     */
@@ -395,7 +398,11 @@ msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa
                             size_t workspace_bytes, void* stream);
 
 /* Bytes of scratch that msa_dense_forward needs for problem p (host only;
- * same conventions and error word as msa_workspace_size). */
+ * same conventions and error word as msa_workspace_size).  With groups it grows
+ * with the parts that the host's bounds allow for: about 1 KB for each
+ * (sequence, KV head, up to 32,768 of max_cache_len positions, row, query head
+ * of the group) and for each (shared row, query head, 32,768 of
+ * max_shared_len). */
 msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
 
 /* Attention over every cached position (top_k plays no part):
@@ -432,9 +439,14 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  * in fp32 (about 70 clocks a key and row).  The kernel's waits, some two seconds
  * elsewhere, may take 8 us a position of max_cache_len longer for these.
  *
+ * Groups (num_groups > 0): keys and values that a group shares are read once for
+ * every 256 / G of its rows.  Weights enter the products with V as one bf16 part
+ * (2^-8, bf16 outputs) or three (fp32), with an int8 cache times the value's scale,
+ * beside exact codes; a row's and its window's own positions are fp32.
+ *
  * out must not overlap q or the caches.  The workspace's contents need no
  * initialisation; calls that share one must be ordered (one stream, or events).
- * It holds the parts of what is split over keys (up to 130 MB), for prompt chunks
+ * It holds the parts of what is split over keys (up to 130 MB without groups), for prompt chunks
  * and drafted windows with bf16 outputs and contexts above 32,768 positions the
  * rows' sums of earlier keys (22 MB), and, for an int8
  * cache with prompt chunks, the widened copy: 4 H (D + 2) bytes a position of
