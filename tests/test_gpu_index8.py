@@ -105,6 +105,12 @@ def test_long_contexts():
     Sparse([(20, 70000)], 4, 16, 64).both()
 
 
+@pytest.mark.parametrize("H,ik_heads", [(1, 0), (2, 0), (2, 1), (8, 0), (8, 1)])
+def test_every_stage_is_used_again(H, ik_heads):
+    """20 units of 64 positions a multiprocessor and more, for rings of up to 12."""
+    Sparse([(1, 262144), (2, 100001), (8, 50000)], H, 2, 64, ik_heads=ik_heads).both()
+
+
 def test_many_sequences():
     Sparse([(1 + i % 3, 3 + (i * 37) % 700) for i in range(500)], 2, 4, 64).both()
 

@@ -104,6 +104,12 @@ def test_long_prefix(index8):
     Batch(behind(131072, [700, 5, 3000], 2), [(3, 131072)], 4, 16, page=256, index8=index8).check()
 
 
+@pytest.mark.parametrize("H,ik_heads", [(1, 0), (2, 0), (8, 0), (8, 1)])
+@pytest.mark.parametrize("index8", [False, True])
+def test_every_stage_is_used_again(H, ik_heads, index8):
+    Batch(behind(262144, [700, 5, 90000], 3) + [(1, 60000)], [(3, 262144)], H, 2, page=256, ik_heads=ik_heads, index8=index8).check()
+
+
 def test_int8_keys_and_values():
     Batch(behind(2048, [0, 100, 63]), [(3, 2048)], 4, 16, index8=True, kv_int8=True).check()
 
