@@ -25,7 +25,7 @@
 // Index keys of 8 bits (codes with a power of two a position): the tiles land as codes in a ring of their own, and four more
 // warps write them as bf16, exactly, into the ring that the products read, with the power of two in them: a thread two
 // positions, 3.75 instructions a value, a quarter of what the epilogue of a tile takes, beside which they run.
-// Measured: 1,024 rows behind 16,384 positions, 4 heads, 46 us by itself.
+// Measured: 1,024 rows behind 16,384 positions, 4 heads, 46 us by itself (bf16 keys: 31).
 //
 // Warp roles: warps 0-7 epilogue (two per TMEM lane quarter, each taking two
 // of a tile's four blocks), warp 8 TMA producer, warp 9 MMA issuer and
