@@ -113,6 +113,11 @@ def test_a_thousand_samples_of_one_prompt():
     SharedBatch(behind(512, [(i * 29) % 64 for i in range(1000)]), [(1000, 512)], 1, 4).check()
 
 
+@pytest.mark.parametrize("int8", [False, True])
+def test_the_most_sequences_and_groups(int8):
+    SharedBatch([(1 + i % 2, 67 + (i * 37) % 150) for i in range(4096)], [(1, 64)] * 4096, 1, 2, int8=int8).check()
+
+
 @pytest.mark.parametrize("out", [BF16, FP32])
 def test_tokens_that_a_row_does_not_see(out):
     """Positions past a sequence's length, and its later tokens, may hold NaN or infinities."""

@@ -110,6 +110,11 @@ def test_every_stage_is_used_again(H, ik_heads, index8):
     Batch(behind(262144, [700, 5, 90000], 3) + [(1, 60000)], [(3, 262144)], H, 2, page=256, ik_heads=ik_heads, index8=index8).check()
 
 
+@pytest.mark.parametrize("index8", [False, True])
+def test_the_most_sequences_and_groups(index8):
+    Batch([(1 + i % 2, 67 + (i * 37) % 150) for i in range(4096)], [(1, 64)] * 4096, 2, 2, index8=index8).check()
+
+
 def test_int8_keys_and_values():
     Batch(behind(2048, [0, 100, 63]), [(3, 2048)], 4, 16, index8=True, kv_int8=True).check()
 
