@@ -381,21 +381,25 @@ def forward(pb: Problem, q, iq, k, v, ik, out=None, sel=None, nsel=None, workspa
     pb._check_cache(k, "k", pb.D)
     pb._check_cache(v, "v", pb.D)
     pb._check_cache(ik, "ik", pb.Di, pb.KH)
-    out = pb.new_out() if out is None else out
-    _need(out, "out", pb.out_dtype, pb.device, (pb.total_rows, pb.H * pb.G, pb.D))
+    if out is None:
+        out = pb.new_out()
+    else:
+        _need(out, "out", pb.out_dtype, pb.device, (pb.total_rows, pb.H * pb.G, pb.D))
     if sel is None:
         sel, nsel = pb.new_sel()
-    pb._check_sel(sel, nsel)
-    ws = pb.workspace() if workspace is None else workspace
-    args = (C.byref(pb.c), _ptr(q), _ptr(iq), _ptr(k), _ptr(v), _ptr(ik), _ptr(out), _ptr(sel), _ptr(nsel),
-            _ptr(ws), ws.numel(), _stream(pb.device))
-    if events:
-        if any(e is not None and not e.cuda_event for e in events):
-            raise ValueError("record each torch.cuda.Event once before passing it (torch creates events lazily)")
-        arr = (C.c_void_p * len(events))(*[C.c_void_p(e.cuda_event) if e is not None else None for e in events])
-        _check(_lib.msa_forward_marked(*args, arr, len(events)))
     else:
-        _check(_lib.msa_forward(*args))
+        pb._check_sel(sel, nsel)
+    ws = pb.workspace() if workspace is None else workspace
+    args = (pb._ref, q.data_ptr(), iq.data_ptr(), k.data_ptr(), v.data_ptr(), ik.data_ptr(), out.data_ptr(), sel.data_ptr(),
+            nsel.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(pb.device.index))
+    with _on(pb.device):
+        if events:
+            if any(e is not None and not e.cuda_event for e in events):
+                raise ValueError("record each torch.cuda.Event once before passing it (torch creates events lazily)")
+            arr = (C.c_void_p * len(events))(*[C.c_void_p(e.cuda_event) if e is not None else None for e in events])
+            _check(_lib.msa_forward_marked(*args, arr, len(events)))
+        else:
+            _check(_lib.msa_forward(*args))
     return out, sel, nsel
 
 
