@@ -4,7 +4,8 @@
 //   y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin      for the pair (a, b) of j
 //   bf16 cache: y rounded;  int8: scale = max |y| / 127, codes = rint(y / scale)
 //   int8 index keys: the least e with max |y| <= 127 2^e, codes = rint(y 2^-e): a power of two, so that a code read back
-//   is a bf16 value exactly and the index scores are the same whichever kernel computes them
+//   is a bf16 value exactly and the index scores are the same whichever kernel computes them.  A head with a value so near to
+//   a half that fp32 may be on its other side (1.5 % of them) is rotated again in 64 bits when the CTA's rows are done.
 // x turns_j is a 64-bit product modulo one turn, so the phase of a far
 // position is as exact as a near one's (fp32 angles lose 0.1 rad at 2^21);
 // its upper 32 bits, as a signed number of half turns, feed sincospi.
@@ -26,8 +27,8 @@
 // a value so near a half that the product could round the other way.
 //
 // Measured: 4,096 rows of 4 x 16 heads into an int8 cache, 45 us (155 MB: 3.4 TB/s, 55 % of the issue slots taken; four
-// CTAs an SM instead of three spill: 51 us); 8 paged rows, 8.5 us, of which an empty launch is about 7.5.  Index keys of 8
-// bits change neither.
+// CTAs an SM instead of three spill: 51 us); 8 paged rows, 8.5 us, of which an empty launch is about 7.5.  With index
+// keys of 8 bits 44 us and the same (their 64-bit rotations; 40 without).
 #include "common.cuh"
 #include "internal.h"
 
@@ -38,6 +39,7 @@ constexpr int kApWarps = kApThreads / 32;
 constexpr int kApRows = 16;   // most rows a CTA takes at a time
 constexpr int kApPairs = kHeadDim / 2 + kIndexDim / 2;
 constexpr int kApBatch = 4;   // pairs of query heads that a warp loads before it stores any
+constexpr float kApNear = 1.f / 8192;  // index codes: how near to a half counts as near
 constexpr int kApCheckRows = 256;  // up to so many rows CTA 0 alone reports bad metadata (and stores the error word)
 
 struct ApRow {
@@ -115,7 +117,44 @@ __device__ __forceinline__ uint2 ap_index_codes(const float (&y)[8], int e) {
     return make_uint2(w[0], w[1]);
 }
 
+// An index head's codes and exponent from a rotation in 64 bits: a warp, two values a lane.
+__device__ __forceinline__ void ap_index_again(const AppendArgs& a, const ApRow& row, int head, int lane) {
+    const uint16_t* src = a.ik + row.r * a.ik_stride + head * kIndexDim;
+    const int half = a.rope_index_dim / 2;
+    double y[2];
+    unsigned long long top = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int d = 2 * lane + i;
+        y[i] = __uint_as_float(static_cast<uint32_t>(src[d]) << 16);
+        if (d < a.rope_index_dim) {
+            const bool lower = a.interleaved ? i == 0 : d < half;
+            const int pair = a.interleaved ? lane : (lower ? d : d - half), other = a.interleaved ? d ^ 1 : (lower ? d + half : d - half);
+            int ax = a.index_axis ? a.index_axis[pair] : 0;
+            if (ax < 0 || ax >= a.axes) ax = 0;
+            const int64_t where = a.positions ? a.positions[static_cast<int64_t>(ax) * a.total_rows + row.r] : row.pos;
+            const uint64_t phase = static_cast<uint64_t>(where) * a.index_turns[pair];
+            const double z = __uint_as_float(static_cast<uint32_t>(src[other]) << 16);
+            double s, c;
+            sincospi(static_cast<double>(static_cast<int64_t>(phase)) * 1.0842021724855044e-19, &s, &c);  // 2^-63
+            y[i] = y[i] * c + (lower ? -z : z) * s;
+        }
+        top = max(top, static_cast<unsigned long long>(__double_as_longlong(fabs(y[i]))));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = max(static_cast<int>(top >> 52) - 1029 + ((top & 0xFFFFFFFFFFFFFull) > 0xFC00000000000ull ? 1 : 0), -126);
+    const double f = __longlong_as_double(static_cast<long long>(1023 - e) << 52);
+    const uint32_t lo = __double2int_rn(y[0] * f) & 0xff, hi = __double2int_rn(y[1] * f) & 0xff;
+    const int64_t o = row.cache * a.KH + head;
+    *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.ik_cache) + o * kIndexDim + 2 * lane) = static_cast<uint16_t>(lo | hi << 8);
+    if (lane == 0) a.ik_exp[o] = static_cast<int8_t>(e);
+}
+
+template <bool kCodes>
 __global__ void __launch_bounds__(kApThreads, 3) append_cache_kernel(const AppendArgs a, int rows_per_cta, int team) {
+    __shared__ int again;  // index heads that are to be rotated in 64 bits, and which: 8 i + head
+    __shared__ uint16_t again_of[kCodes ? kApRows * 8 : 1];
     __shared__ ApRow row_of[kApRows];
     __shared__ __align__(16) float2 turn[kApRows][kApPairs];  // (cos, sin) of the head pairs, then of the index pairs
     __shared__ uint32_t err;
@@ -168,6 +207,7 @@ __global__ void __launch_bounds__(kApThreads, 3) append_cache_kernel(const Appen
             if (other0 < others) ov = load_other(my_team, other0);
         }
         __syncthreads();  // the last rows' tasks are done with the shared arrays
+        if (kCodes && tid == 0) again = 0;
         if (a.num_seqs <= kApThreads) {
             if (tid < rows_per_cta) row_of[tid] = ApRow{-1, 0, -1};
             int c0 = 0, c1 = 0, L = 0;
@@ -305,19 +345,30 @@ __global__ void __launch_bounds__(kApThreads, 3) append_cache_kernel(const Appen
                         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(k == 1 ? a.k_cache : a.v_cache) + o * kHeadDim + at) = code;
                         if (at == 0) (k == 1 ? a.k_scale : a.v_scale)[o] = scale;
                     }
-                } else if (k == 4 && a.ik_exp != nullptr) {  // the 8 lanes of an index head
+                } else if (kCodes && k == 4) {  // the 8 lanes of an index head
                     uint32_t top = 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    bool near = false;
                     if (there && row.cache >= 0) {
                         const int e = ap_index_exp(top);
                         const int64_t o = row.cache * a.KH + head;
                         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.ik_cache) + o * kIndexDim + at) =
                             e == -128 ? make_uint2(0u, 0u) : ap_index_codes(y, e);
                         if (at == 0) a.ik_exp[o] = static_cast<int8_t>(e);
+                        // A value so near to a half, or a maximum to where the exponent changes, that the fp32 rotation may be on
+                        // its other side (an angle and its cosine off by 2.2e-7, two roundings, 254 steps at most: 9e-5 of one).
+                        if (turned && e != -128) {
+                            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), most = __uint_as_float(top) * f;
+                            near = fabsf(most - 127.f) < kApNear || fabsf(most - 63.5f) < kApNear;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) near |= fabsf(y[c] * f - rintf(y[c] * f)) > 0.5f - kApNear;
+                        }
                     }
+                    const uint32_t who = __ballot_sync(0xffffffffu, near);
+                    if (at == 0 && (who >> lane & 0xffu)) again_of[atomicAdd(&again, 1)] = static_cast<uint16_t>(8 * i + head);
                 } else if (there && (k == 3 || row.cache >= 0)) {
                     uint16_t* dst = k == 3 ? a.iq_out + (r * H + head) * kIndexDim
                                   : k == 4 ? static_cast<uint16_t*>(a.ik_cache) + (row.cache * a.KH + head) * kIndexDim
@@ -329,6 +380,10 @@ __global__ void __launch_bounds__(kApThreads, 3) append_cache_kernel(const Appen
                 }
                 __syncwarp();
             }
+        }
+        if constexpr (kCodes) {
+            __syncthreads();
+            for (int w = warp; w < again; w += kApWarps) ap_index_again(a, row_of[again_of[w] >> 3], again_of[w] & 7, lane);
         }
     }
     // Few rows: CTA 0 looks at every row once more and stores the word, so that no kernel has to clear it first.
@@ -360,7 +415,8 @@ cudaError_t run_append_cache(const AppendArgs& a, cudaStream_t stream) {
     const int64_t need = (static_cast<int64_t>(a.total_rows) + rows - 1) / rows, cap = places;
     // warps that share a row (4,096 rows of 4 x 16 heads: 55, 49, 47 and 45 us with 1, 2, 4 and 8; 2,300 rows of 8 x 5: 31, 31, 29, 31)
     const int team = rows > 1 ? 4 : kApWarps;
-    append_cache_kernel<<<static_cast<unsigned>(need < cap ? need : cap), kApThreads, 0, stream>>>(a, rows, team);
+    auto* kernel = a.ik_exp ? append_cache_kernel<true> : append_cache_kernel<false>;
+    kernel<<<static_cast<unsigned>(need < cap ? need : cap), kApThreads, 0, stream>>>(a, rows, team);
     return cudaGetLastError();
 }
 

@@ -387,7 +387,7 @@ typedef struct msa_append {
  *   e = the smallest integer >= -126 with max_d |y_d| <= 127 2^e,
  *   code_d = round-to-nearest-even(y_d / 2^e)
  * (-126 for a zero head, -128 and zero codes for one that holds a NaN or an
- * infinity).  Cache rows of other positions are left as they were, and so
+ * infinity; e and the codes are those of the rotation in 64 bits).  Cache rows of other positions are left as they were, and so
  * are rows of q_out and iq_out at or past cu_rows[num_seqs].  Two positions
  * that share a cache row (a page listed twice) are the caller's error.
  * Metadata errors go to the error word in the workspace's first 4 bytes, as

@@ -230,6 +230,32 @@ def test_append(H, ik_heads, page, rope):
     assert (codes[others] == 55).all() and (exp[others] == 77).all()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("axes", [1, 3])
+@pytest.mark.parametrize("dim", [32, 64])
+def test_codes_of_a_rotation_in_64_bits(interleaved, axes, dim):
+    """Codes and exponents are those of the rotation in 64 bits (one in 32 bits chooses the other neighbour of about one value
+    in a million; the reference's angles, 1e-11 off, of one in a thousand millions)."""
+    m = msa()
+    g = torch.Generator(device="cuda").manual_seed(axes)
+    R, H = 1200, 4
+    exp = torch.zeros(R, H, dtype=torch.int8, device="cuda")
+    codes = torch.zeros(R, H, 64, dtype=torch.int8, device="cuda")
+    pb = m.Problem(H, 1, [(R, R)], "cuda", ik_exp=exp)
+    k, v = (torch.zeros(R, H, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    new = torch.randn(R, H, 128, generator=g, device="cuda").bfloat16()
+    ik = torch.randn(R, H, 64, generator=g, device="cuda").bfloat16()
+    where = torch.randint(1, 20000, (axes, R), generator=g, device="cuda", dtype=torch.int32)
+    axis = [j % axes for j in range(dim // 2)] if axes > 1 else None
+    r = m.Rope(dim, dim, theta=1e4, axes=axes, axis=axis, index_axis=axis, interleaved=interleaved)
+    m.append_cache(pb, new, new, k, v, new_ik=ik, ik=codes, rope=r, positions=where)
+    y = rotate_ref(ik, dim, where, interleaved=interleaved, axis=axis)
+    _, e = quantised(y)
+    want = torch.round(y * ((1023 - e.long()) << 52).view(torch.float64)[..., None])
+    assert torch.equal(exp.double(), e)
+    assert torch.equal(codes.double(), want)
+
+
 def test_append_values_at_the_ends_of_the_range():
     m = msa()
     inf, nan = float("inf"), float("nan")
