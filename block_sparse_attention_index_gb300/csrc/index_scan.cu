@@ -195,10 +195,8 @@ __global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_s
             ix_group(a, g, end, bad);
             if (bad) atomicOr(&err, kErrBadMetadata);
         }
-        for (int b = tid; b < a.num_seqs && a.num_groups > 0; b += Cfg::kThreads) {  // rows before the end of what is shared
-            const int n = a.cu_rows[b + 1] - a.cu_rows[b];
-            if (n >= 1 && n <= kDecodeMaxRows && ix_seq(a, b).rows == 0) atomicOr(&err, kErrBadMetadata);
-        }
+        for (int b = tid; b < a.num_seqs && a.num_groups > 0; b += Cfg::kThreads)  // more rows than the bound, rows before the end of what is shared
+            if (a.cu_rows[b + 1] != a.cu_rows[b] && ix_seq(a, b).rows == 0) atomicOr(&err, kErrBadMetadata);
     }
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

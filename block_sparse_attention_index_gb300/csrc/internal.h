@@ -84,7 +84,7 @@ struct IndexScanArgs {
     int by_row;            // 1: row r's pooled scores lie at slot r (every sequence is of the decode family)
     int64_t cache_tokens;
     int64_t unit_bound;    // upper bound of the number of work units
-    float* pooled;         // [slots, H, max_blocks]
+    float* pooled;         // [slots, H, max_blocks]; slots: num_seqs x rows_per_seq, by_row: total_rows
     int32_t* clear_words;
     int n_clear;
     int32_t* drow_prefix;  // nullable

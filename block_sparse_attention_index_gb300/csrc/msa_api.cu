@@ -207,7 +207,8 @@ Layout layout_of(const msa_problem* p) {
     l.header_bytes = off;
     off = align256(off);
     l.pooled = off;
-    off = align256(off + B * RS * H * MB * sizeof(float));
+    // a slot for each row slot of a sequence; with groups for each row, whatever the device's cu_rows say
+    off = align256(off + (p->num_groups > 0 ? R : B * RS) * H * MB * sizeof(float));
     l.partials = off;  // none: decode partials are combined on chip (thread-block clusters)
     l.sel = off;
     off = align256(off + R * H * K * sizeof(int32_t));

@@ -1,0 +1,59 @@
+"""Device metadata that breaks the host's bounds, in batches with groups: it is
+reported, and nothing outside the workspace is written."""
+import pytest
+import torch
+
+from gpu_common import msa
+from test_gpu_shared_sparse import Batch, behind
+
+pytestmark = pytest.mark.gpu
+
+
+def guarded(pb, size):
+    """A workspace with 4 MB behind it that nobody may write."""
+    store = torch.full((size + (4 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    return store[:size], store[size:]
+
+
+def forward(a, pb):
+    """(error word, guard untouched, out)"""
+    m = msa()
+    ws, guard = guarded(pb, pb.workspace_size())
+    out = torch.full_like(pb.new_out(), float("nan"))
+    m.forward(pb, a.q, a.iq, a.k, a.v, a.ik, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    return m.error_word(ws), bool((guard == 0xA5).all()), out
+
+
+@pytest.mark.parametrize("index8", [False, True])
+@pytest.mark.parametrize("starts", [[0, 1, 64], [0, 3, 6], [0, 33, 34], [0, 1, 9], [0, 63, 64]])
+def test_more_rows_than_the_host_says(starts, index8):
+    """Two sequences of one row each for the host, rows behind them; the device gives them more."""
+    a = Batch(behind(4096, [100, 300]), [(2, 4096)], 4, 8, index8=index8, spare_rows=62)
+    pb = a.problem(True)
+    pb.c.max_group_rows = 64
+    pb.cu_rows.copy_(torch.tensor(starts, dtype=torch.int32))
+    word, intact, _ = forward(a, pb)
+    assert intact and word == msa().ERR_BAD_METADATA
+
+
+@pytest.mark.parametrize("first", [5, 50, 62])
+def test_rows_that_begin_later(first):
+    """Rows before the first sequence: its scores lie at its rows' slots all the same."""
+    a = Batch(behind(4096, [100, 300]), [(2, 4096)], 4, 8, spare_rows=62)
+    pb = a.problem(True)
+    pb.cu_rows.copy_(torch.tensor([first, first + 1, first + 2], dtype=torch.int32))
+    word, intact, out = forward(a, pb)
+    assert intact and word == 0
+    b = a.problem(False)
+    b.cu_rows.copy_(pb.cu_rows)
+    assert torch.equal(out[first:first + 2], forward(a, b)[2][first:first + 2])
+    assert torch.isnan(out[:first]).all() and torch.isnan(out[first + 2:]).all()
+
+
+def test_rows_past_the_total():
+    a = Batch(behind(1280, [100, 300], 2), [(2, 1280)], 2, 8)
+    pb = a.problem(True)
+    pb.cu_rows.copy_(torch.tensor([1, 3, 5], dtype=torch.int32))
+    word, intact, _ = forward(a, pb)
+    assert intact and word == msa().ERR_BAD_METADATA
