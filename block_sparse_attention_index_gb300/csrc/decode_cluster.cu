@@ -125,6 +125,20 @@ __global__ void __launch_bounds__(kClThreads, 2) decode_cluster_kernel(const __g
     const int H = a.H, G = a.G;
     const int h = blockIdx.y;
     int b, row_in_seq;
+    // What the scan's CTAs found wrong goes into the error word by one CTA, which loads it when it may and looks at it as its
+    // last act.
+    static_assert(kScanMostCtas <= 2 * kClThreads, "two words a thread");
+    const bool reports = !kSelGiven && blockIdx.z == 0 && h == 0 && rank == 0;
+    uint32_t found[2] = {0, 0};
+    auto load_found = [&]() {
+        if (!reports) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (tid + i * kClThreads < a.scan_ctas) found[i] = a.scan_found[tid + i * kClThreads];
+    };
+    auto report_found = [&]() {
+        if (!kSelGiven && (found[0] | found[1]) != 0) atomicOr(a.err, found[0] | found[1]);
+    };
     if (a.drow_prefix != nullptr) {
         // compact grid (fused path): blockIdx.z is a decode-family row; its sequence comes from
         // the prefix of rows the index scan wrote, so this wait comes first
@@ -133,7 +147,11 @@ __global__ void __launch_bounds__(kClThreads, 2) decode_cluster_kernel(const __g
         const int total = a.drow_prefix[B];
         if (z == 0 && h == 0 && rank == 0 && tid == 0 && total > static_cast<int>(gridDim.z))
             atomicOr(a.err, kErrBadMetadata);  // the host's row count is below the device metadata's
-        if (z >= total) return;  // a host count above the device's: nothing to do
+        if (z >= total) {  // a host count above the device's: nothing to do
+            load_found();
+            report_found();
+            return;
+        }
         int lo = 0, hi = B;  // largest b with drow_prefix[b] <= z
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -150,7 +168,12 @@ __global__ void __launch_bounds__(kClThreads, 2) decode_cluster_kernel(const __g
     // ---- prologue: only inputs that no earlier kernel of the step writes
     const int nrows = a.cu_rows[b + 1] - a.cu_rows[b];
     // not a decode-family sequence, or no such row (the whole cluster returns)
-    if (nrows < 1 || nrows > kDecodeMaxRows || row_in_seq >= nrows) return;
+    if (nrows < 1 || nrows > kDecodeMaxRows || row_in_seq >= nrows) {
+        if (reports) pdl_wait();
+        load_found();
+        report_found();
+        return;
+    }
     const int r = a.cu_rows[b] + row_in_seq;
     const int L = a.cache_lens[b];
     // nrows > rows_per_seq: more rows than the grid and the pooled scores have slots for
@@ -182,12 +205,14 @@ __global__ void __launch_bounds__(kClThreads, 2) decode_cluster_kernel(const __g
     // a given count of kept blocks (the same in every thread of the cluster)
     const int nsel_given = kSelGiven && meta_ok ? a.nsel_in[static_cast<int64_t>(r) * H + h] : 1;
     pdl_wait();  // the index scan (pooled scores, error word) is complete and visible
+    load_found();
     // A kernel launched after this one as a programmatic dependent may start now.  The
     // scan's header clears (tickets of the prompt indexer) have landed by this point;
     // a dependent that reads anything this grid writes waits for it to finish first.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!meta_ok) {
         if (tid == 0 && rank == 0) atomicOr(a.err, kErrBadMetadata);
+        report_found();
         return;  // the whole cluster returns: before any cluster barrier
     }
     if (nsel_given < 1 || nsel_given > a.top_k) {
@@ -557,6 +582,7 @@ __global__ void __launch_bounds__(kClThreads, 2) decode_cluster_kernel(const __g
         mbar_wait(&sm.bar_k, k_armed & 1, nullptr);  // the last K phase armed (the earlier ones completed)
         mbar_wait(&sm.bar_v, late_phase, nullptr);
     }
+    report_found();
 }
 
 // Shared memory a CTA asks for: what it uses, or (one CTA per SM) more than half of an SM's

@@ -90,9 +90,11 @@ __global__ void __launch_bounds__(ScanCfg<H, kShared>::kThreads, 1) decode_scan_
     uint64_t* empty = full + Cfg::kStages;
     int32_t* prefix = reinterpret_cast<int32_t*>(empty + Cfg::kStages);  // [num_seqs + 1]
     __shared__ int warp_tot[Cfg::kThreads / 32];
+    __shared__ uint32_t err;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
+        err = 0;
         for (int s = 0; s < Cfg::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -172,7 +174,10 @@ __global__ void __launch_bounds__(ScanCfg<H, kShared>::kThreads, 1) decode_scan_
     const int64_t u0 = total * blockIdx.x / gridDim.x;
     const int64_t u1 = total * (blockIdx.x + 1) / gridDim.x;
     const int n = static_cast<int>(u1 - u0);
-    if (n <= 0) return;
+    if (n <= 0) {
+        if (tid == 0) a.found[blockIdx.x] = 0;
+        return;
+    }
     int b0 = 0;
     {
         int lo = 0, hi = a.num_seqs;  // largest b with prefix[b] <= u0
@@ -195,14 +200,14 @@ __global__ void __launch_bounds__(ScanCfg<H, kShared>::kThreads, 1) decode_scan_
                 const int j = static_cast<int>(u - prefix[b]);
                 const int npos = max(0, min(kBlock, st.L - j * kBlock));
                 const int s = i % Cfg::kStages;
-                if (i >= Cfg::kStages && !mbar_wait(&empty[s], ((i / Cfg::kStages) - 1) & 1, a.err)) break;
+                if (i >= Cfg::kStages && !mbar_wait(&empty[s], ((i / Cfg::kStages) - 1) & 1, &err)) break;
                 if (npos > 0) {
                     // whole 64-position boxes; rows past the sequence are masked by the consumer
                     // and rows past the cache are zero-filled by the copy engine
                     mbar_arrive_expect_tx(&full[s], Cfg::kUnitBytes);
                     int64_t row = block_row(a.cache, b, static_cast<int64_t>(j) * kBlock);
                     if (row < 0) {  // page outside the pool
-                        atomicOr(a.err, kErrBadMetadata);
+                        atomicOr(&err, kErrBadMetadata);
                         row = 0;
                     }
                     const int tok = static_cast<int>(row);
@@ -217,9 +222,8 @@ __global__ void __launch_bounds__(ScanCfg<H, kShared>::kThreads, 1) decode_scan_
             // no copy of this lane may still be in flight when the CTA ends (after a timed-out
             // wait of a consumer, too): wait, bounded, for the last phase armed on every stage
             for (int s = 0; s < Cfg::kStages && s < armed; ++s)
-                mbar_wait(&full[s], ((s + Cfg::kStages * ((armed - 1 - s) / Cfg::kStages)) / Cfg::kStages) & 1, a.err);
+                mbar_wait(&full[s], ((s + Cfg::kStages * ((armed - 1 - s) / Cfg::kStages)) / Cfg::kStages) & 1, &err);
         }
-        return;
     }
 
     // ---------------- consumer warp `warp` owns stage `warp`
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(ScanCfg<H, kShared>::kThreads, 1) decode_scan_
     int b = b0;
     ScanSeqState st;
     const uint32_t stage = smem_u32(ring + warp * Cfg::kUnitBytes);
-    for (int i = warp; i < n; i += Cfg::kStages) {
+    for (int i = warp; warp < Cfg::kConsumers && i < n; i += Cfg::kStages) {
         const int64_t u = u0 + i;
         scan_locate(a, prefix, u, b, st);
         // this lane's B column: row grp of the sequence (if it exists)
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(ScanCfg<H, kShared>::kThreads, 1) decode_scan_
         const int last0 = st.L - st.n + 2 * tig + 1 - j * kBlock;
         const int npos0 = 2 * tig < st.n ? max(0, min(kBlock, last0)) : 0;
         const int npos1 = 2 * tig + 1 < st.n ? max(0, min(kBlock, last0 + 1)) : 0;
-        if (!mbar_wait(&full[warp], (i / Cfg::kStages) & 1, a.err)) break;
+        if (!mbar_wait(&full[warp], (i / Cfg::kStages) & 1, &err)) break;
         if constexpr (kShared) {
             // one key tile for every head: the B columns are the (row, head) pairs,
             // column c = h * n + i, eight per pass
@@ -366,6 +370,8 @@ __global__ void __launch_bounds__(ScanCfg<H, kShared>::kThreads, 1) decode_scan_
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[warp]);  // stage reusable
     }
+    __syncthreads();
+    if (tid == 0) a.found[blockIdx.x] = err;  // what was found wrong
 }
 
 template <int H, bool kShared>
@@ -375,10 +381,8 @@ static cudaError_t launch_scan(const ScanArgs& a, cudaStream_t stream) {
                         static_cast<size_t>(a.num_seqs + 1) * sizeof(int32_t);
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(decode_scan_kernel<H, kShared>), smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = device_sm_count();
-    if (a.unit_bound < grid) grid = a.unit_bound > 0 ? a.unit_bound : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(scan_grid(a.unit_bound)), 1, 1);
     cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

@@ -408,9 +408,8 @@ __global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_s
             if (lane == 0) mbar_arrive(&empty[s]);  // stage reusable
         }
     }
-    // What was found wrong, into the header that CTA 0 has cleared long since (its first act, this one's last).
     __syncthreads();
-    if (tid == 0 && err != 0) atomicOr(a.err, err);
+    if (tid == 0) a.found[blockIdx.x] = err;  // what was found wrong
 }
 
 template <int H, bool kShared, bool kInt8>
@@ -421,10 +420,8 @@ static cudaError_t launch_index_scan(const IndexScanArgs& a, cudaStream_t stream
     auto* kernel = index_scan_kernel<H, kShared, kInt8>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
-    int64_t grid = device_sm_count();
-    if (a.unit_bound < grid) grid = a.unit_bound > 0 ? a.unit_bound : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(scan_grid(a.unit_bound)), 1, 1);
     cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

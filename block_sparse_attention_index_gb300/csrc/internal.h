@@ -45,6 +45,9 @@ __device__ __forceinline__ bool seq_rows_ok(const CacheRows& c, int b, int L, in
 // unnormalised output O[16][128], running max m[16] (log2 domain), sum l[16].
 constexpr int kPartialFloats = 16 * 128 + 16 + 16;
 
+constexpr int kScanMostCtas = 256;  // most CTAs of a scan
+int scan_grid(int64_t unit_bound);  // CTAs for so many work units
+
 struct ScanArgs {
     const CUtensorMap* ik_map;  // ik as (Di, KH, tokens), box 64 x 1 x 64, host copy
     int H;
@@ -65,7 +68,8 @@ struct ScanArgs {
     int32_t* clear_words; // zeroed by the scan (tickets of the attention kernel)
     int n_clear;
     int32_t* drow_prefix; // nullable: [B + 1] prefix of decode-family rows per sequence, written by CTA 0
-    uint32_t* err;
+    uint32_t* found;      // [grid] error bits, a word a CTA: the attention kernel that follows brings them together (the
+                          // error word itself is cleared by CTA 0, maybe after another CTA's last act)
 };
 
 // The same for index keys of 8 bits, and for groups of sequences that share a prefix.
@@ -88,7 +92,7 @@ struct IndexScanArgs {
     int32_t* clear_words;
     int n_clear;
     int32_t* drow_prefix;  // nullable
-    uint32_t* err;
+    uint32_t* found;       // [grid] error bits, as in ScanArgs
 };
 cudaError_t run_index_scan(const IndexScanArgs& a, cudaStream_t stream);
 
@@ -121,6 +125,8 @@ struct DecodeAttendArgs {
     int32_t* tickets;          // [B, H], zero on entry
     int32_t* sel_out;          // nullable
     int32_t* nsel_out;         // nullable
+    const uint32_t* scan_found;  // fused path: [scan_ctas] what the scan's CTAs found wrong
+    int scan_ctas;
     uint32_t* err;
 };
 

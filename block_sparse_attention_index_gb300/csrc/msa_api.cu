@@ -148,7 +148,7 @@ msa::CacheRows cache_rows_of(const msa_problem* p) {
 }
 
 struct Layout {
-    size_t err = 0, tickets = 0, idx_tickets = 0, pooled = 0, partials = 0, sel = 0, nsel = 0, idx_cand = 0,
+    size_t err = 0, scan_found = 0, tickets = 0, idx_tickets = 0, pooled = 0, partials = 0, sel = 0, nsel = 0, idx_cand = 0,
            drow_prefix = 0, wide_starts = 0, wide_k = 0, wide_v = 0, wide_ks = 0, wide_vs = 0, total = 0;
     size_t header_bytes = 0;  // error word + tickets, cleared at the start of a call
 };
@@ -206,6 +206,8 @@ Layout layout_of(const msa_problem* p) {
     off += (static_cast<size_t>(index_tile_bound(p)) * H) * sizeof(int32_t);
     l.header_bytes = off;
     off = align256(off);
+    l.scan_found = off;
+    off = align256(off + msa::kScanMostCtas * sizeof(uint32_t));
     l.pooled = off;
     // a slot for each row slot of a sequence; with groups for each row, whatever the device's cu_rows say
     off = align256(off + (p->num_groups > 0 ? R : B * RS) * H * MB * sizeof(float));
@@ -467,6 +469,11 @@ int msa::device_sm_count() {
         c = v > 0 ? v : 1;
     }
     return c;
+}
+
+int msa::scan_grid(int64_t unit_bound) {
+    const int64_t most = std::min(device_sm_count(), kScanMostCtas);
+    return static_cast<int>(std::max<int64_t>(1, std::min(unit_bound, most)));
 }
 
 cudaError_t msa::ensure_smem_limit(const void* kernel, size_t bytes) {
@@ -791,7 +798,7 @@ static msa::IndexScanArgs index_scan_args(const msa_problem* p, const msa::ScanA
     x.clear_words = a.clear_words;
     x.n_clear = a.n_clear;
     x.drow_prefix = a.drow_prefix;
-    x.err = a.err;
+    x.found = a.found;
     return x;
 }
 
@@ -856,7 +863,7 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
         sa.clear_words = reinterpret_cast<int32_t*>(ws + l.err);
         sa.n_clear = static_cast<int>(l.header_bytes / sizeof(int32_t));
         sa.drow_prefix = compact_decode_grid(p) ? reinterpret_cast<int32_t*>(ws + l.drow_prefix) : nullptr;
-        sa.err = reinterpret_cast<uint32_t*>(ws + l.err);
+        sa.found = reinterpret_cast<uint32_t*>(ws + l.scan_found);
         if (p->num_groups > 0 || p->ik_dtype == MSA_IK_INT8)
             e = msa::run_index_scan(index_scan_args(p, sa), st);
         else
@@ -866,6 +873,8 @@ msa_status msa_forward_marked(const msa_problem* p, const void* q, const void* i
         msa::DecodeAttendArgs da = decode_args(p, &km, &vm, q, out, ws, l);
         da.pooled = sa.pooled;
         da.pooled_by_row = p->num_groups > 0;
+        da.scan_found = sa.found;
+        da.scan_ctas = msa::scan_grid(sa.unit_bound);
         da.max_blocks = max_blocks;
         da.sel_out = sel;
         da.nsel_out = nsel;
