@@ -100,7 +100,7 @@ struct __align__(1024) DsSmem {
     uint64_t info_full[kDsInfo], info_empty[kDsInfo], item_done[2];
     DsItem info[kDsInfo];
     uint32_t tmem, err;
-    int group_parts;   // parts of all groups
+    int64_t group_parts;  // parts of all groups
     int first;         // the entry where the CTA's share begins, and what is known of it
     SharedEntry first_entry;
     int64_t scan_line[Cfg::kThreads / 32];
@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
     const uint32_t tmem = sm.tmem;
     // ---- places of the entries on the line, and parts before each (a block-wide scan; every CTA stores the same)
     const int entries = a.num_groups + a.num_seqs;
-    int64_t line = 0, len = 0;
-    int parts = 0, e_mine = -1;
+    int64_t line = 0, len = 0, parts = 0;
+    int e_mine = -1;
     SharedEntry y{};  // the thread's entry of the last round
     for (int base = 0; base < entries; base += kThreads) {
         const int e = base + tid;
@@ -314,8 +314,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             sm.scan_items[warp] = incl_items;
         }
         __syncthreads();
-        int64_t before = line;
-        int before_items = parts;
+        int64_t before = line, before_items = parts;
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) {
                 before += sm.scan_line[w];
@@ -325,16 +324,19 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             parts += sm.scan_items[w];
         }
         y.line = before + incl - len;
-        y.parts = before_items + incl_items - items;
+        y.parts = static_cast<int32_t>(before_items + incl_items - items);
         if (e < entries) {
             a.entries[e] = y;
-            if (e == a.num_groups) sm.group_parts = y.parts;
+            if (e == a.num_groups) sm.group_parts = before_items + incl_items - items;
         }
         __syncthreads();
     }
-    if (tid == 0) a.entries[entries] = SharedEntry{line, parts, 0, 0, 0, 0, 0};
-    const int group_parts = sm.group_parts;  // (a problem has a sequence)
-    if (group_parts > a.group_parts_most || parts - group_parts > a.seq_parts_most) {  // more than the host's bounds allow for
+    // More parts than the host's bounds allow for, as groups that overlap can make (their starts do not ascend): nothing is done.
+    // (Sums over a warp's entries are below 2^31, over all of them maybe not.)
+    const int64_t group_parts = sm.group_parts;  // (a problem has a sequence)
+    const bool over = group_parts > a.group_parts_most || parts - group_parts > a.seq_parts_most;
+    if (tid == 0) a.entries[entries] = SharedEntry{line, static_cast<int32_t>(parts), over ? -1 : 0, 0, 0, 0, 0};
+    if (over) {
         if (tid == 0) atomicOr(&sm.err, kErrBadMetadata);
         line = 0;
     }
@@ -1130,7 +1132,7 @@ __global__ void __launch_bounds__(256, kResident) dense_shared_join(const Shared
         const SharedEntry total = ds_load(a.entries + entries);
         const int group_parts = a.entries[groups].parts;
         int n = -1;
-        if (group_parts <= a.group_parts_most && total.parts - group_parts <= a.seq_parts_most) {
+        if (total.b >= 0) {  // (not more than the host's bounds allow for)
             const int P = 128 / a.G, shares = ds_shares(total.line, grid), run = kDsPartKeys / NK;
             DsSize sg{};
             SharedEntry eg{};

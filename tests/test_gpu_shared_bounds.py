@@ -57,3 +57,38 @@ def test_rows_past_the_total():
     pb.cu_rows.copy_(torch.tensor([1, 3, 5], dtype=torch.int32))
     word, intact, _ = forward(a, pb)
     assert intact and word == msa().ERR_BAD_METADATA
+
+
+@pytest.mark.parametrize("starts", [[0, 3, 0, 3], [0, 3, 2, 3], [3, 0, 0, 3], [1, 0, 3, 1], [0, 3, -1, 3], [0, 4, 0, 3],
+                                    [0, 2 ** 31 - 1, 0, 3]])
+@pytest.mark.parametrize("index8", [False, True])
+def test_groups_that_do_not_ascend(starts, index8):
+    """Three groups whose starts go down again: some of them overlap."""
+    a = Batch(behind(1280, [100, 300, 5], 2), [(1, 1280), (1, 1280), (1, 1280)], 2, 8, index8=index8)
+    pb = a.problem(True)
+    pb.c.max_group_rows = 6
+    pb.group_starts.copy_(torch.tensor(starts, dtype=torch.int32))
+    word, intact, _ = forward(a, pb)
+    assert intact and word == msa().ERR_BAD_METADATA
+    ws, guard = guarded(pb, pb.dense_workspace_size())
+    msa().dense_forward(pb, a.q, a.k, a.v, workspace=ws)
+    torch.cuda.synchronize()
+    assert bool((guard == 0xA5).all()) and msa().error_word(ws) == msa().ERR_BAD_METADATA
+
+
+def test_more_parts_than_the_host_allows_for():
+    """64 groups that overlap, each of 64 rows and two parts: the workspace has room for those of 64 rows in all."""
+    seqs = behind(33000, [i for i in range(64)])
+    a = Batch(seqs, [(1, 33000)] * 64, 1, 16)
+    pb = a.problem(True)
+    pb.c.max_group_rows = 64
+    ws, guard = guarded(pb, pb.dense_workspace_size())
+    good = msa().dense_forward(pb, a.q, a.k, a.v, workspace=ws).clone()
+    torch.cuda.synchronize()
+    assert msa().error_word(ws) == 0 and bool((guard == 0xA5).all()) and torch.isfinite(good).all()
+    pb.group_starts.copy_(torch.tensor([64 * (i % 2) for i in range(65)], dtype=torch.int32))
+    msa().dense_forward(pb, a.q, a.k, a.v, workspace=ws)
+    torch.cuda.synchronize()
+    assert msa().error_word(ws) == msa().ERR_BAD_METADATA and bool((guard == 0xA5).all())
+    word, intact, _ = forward(a, pb)
+    assert intact and word == msa().ERR_BAD_METADATA
