@@ -1194,16 +1194,15 @@ __global__ void __launch_bounds__(256, kResident) dense_shared_join(const Shared
                 top = most;
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q) {
-                    if (i0 + q >= run.count) continue;
-                    // a part with no key (maximum -inf) weighs nothing, unless its sum is NaN
-                    const float w = ml[q].x == -INFINITY ? (ml[q].y == ml[q].y ? 0.f : ml[q].y) : dp_exp2(ml[q].x - top);
-                    if (w != 0.f) {
-                        sum = fmaf(w, ml[q].y, sum);
-                        o.x = fmaf(w, v[q].x, o.x);
-                        o.y = fmaf(w, v[q].y, o.y);
-                        o.z = fmaf(w, v[q].z, o.z);
-                        o.w = fmaf(w, v[q].w, o.w);
-                    }
+                    // A part without a key, or with none above -inf, says nothing (nor is its O read), unless its sum is NaN.  Any
+                    // other counts, also with a weight that is 0 in fp32: an infinite value in it shows.
+                    if (i0 + q >= run.count || (ml[q].x == -INFINITY && ml[q].y == ml[q].y)) continue;
+                    const float w = ml[q].x == -INFINITY ? ml[q].y : dp_exp2(ml[q].x - top);
+                    sum = fmaf(w, ml[q].y, sum);
+                    o.x = fmaf(w, v[q].x, o.x);
+                    o.y = fmaf(w, v[q].y, o.y);
+                    o.z = fmaf(w, v[q].z, o.z);
+                    o.w = fmaf(w, v[q].w, o.w);
                 }
             }
         }
