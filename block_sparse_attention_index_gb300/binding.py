@@ -342,6 +342,7 @@ def _attend(fn, pb: Problem, q, k, v, sel, nsel, out=None, workspace=None):
     out = pb.new_out() if out is None else out
     _need(out, "out", pb.out_dtype, pb.device, (pb.total_rows, pb.H * pb.G, pb.D))
     ws = pb.workspace() if workspace is None else workspace
+    _need(ws, "workspace", torch.uint8, pb.device)
     _check(fn(C.byref(pb.c), _ptr(q), _ptr(k), _ptr(v), _ptr(sel), _ptr(nsel), _ptr(out), _ptr(ws),
               ws.numel(), _stream(pb.device)))
     return out
@@ -390,6 +391,7 @@ def forward(pb: Problem, q, iq, k, v, ik, out=None, sel=None, nsel=None, workspa
     else:
         pb._check_sel(sel, nsel)
     ws = pb.workspace() if workspace is None else workspace
+    _need(ws, "workspace", torch.uint8, pb.device)
     args = (pb._ref, q.data_ptr(), iq.data_ptr(), k.data_ptr(), v.data_ptr(), ik.data_ptr(), out.data_ptr(), sel.data_ptr(),
             nsel.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(pb.device.index))
     with _on(pb.device):
