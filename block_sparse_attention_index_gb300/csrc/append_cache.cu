@@ -143,9 +143,10 @@ __device__ __forceinline__ void ap_index_again(const AppendArgs& a, const ApRow&
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = max(static_cast<int>(top >> 52) - 1029 + ((top & 0xFFFFFFFFFFFFFull) > 0xFC00000000000ull ? 1 : 0), -126);
+    const bool finite = top < 0x7FF0000000000000ull;
+    const int e = finite ? max(static_cast<int>(top >> 52) - 1029 + ((top & 0xFFFFFFFFFFFFFull) > 0xFC00000000000ull ? 1 : 0), -126) : -128;
     const double f = __longlong_as_double(static_cast<long long>(1023 - e) << 52);
-    const uint32_t lo = __double2int_rn(y[0] * f) & 0xff, hi = __double2int_rn(y[1] * f) & 0xff;
+    const uint32_t lo = finite ? __double2int_rn(y[0] * f) & 0xff : 0, hi = finite ? __double2int_rn(y[1] * f) & 0xff : 0;
     const int64_t o = row.cache * a.KH + head;
     *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.ik_cache) + o * kIndexDim + 2 * lane) = static_cast<uint16_t>(lo | hi << 8);
     if (lane == 0) a.ik_exp[o] = static_cast<int8_t>(e);
@@ -360,6 +361,8 @@ __global__ void __launch_bounds__(kApThreads, 3) append_cache_kernel(const Appen
                         if (at == 0) a.ik_exp[o] = static_cast<int8_t>(e);
                         // A value so near to a half, or a maximum to where the exponent changes, that the fp32 rotation may be on
                         // its other side (an angle and its cosine off by 2.2e-7, two roundings, 254 steps at most: 9e-5 of one).
+                        // So may a head that is not finite in 32 bits: two values near 3.4e38 are turned past them.
+                        near = turned && e == -128;
                         if (turned && e != -128) {
                             const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), most = __uint_as_float(top) * f;
                             near = fabsf(most - 127.f) < kApNear || fabsf(most - 63.5f) < kApNear;
