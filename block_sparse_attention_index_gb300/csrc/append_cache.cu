@@ -4,8 +4,9 @@
 //   y_a = x_a cos - x_b sin,  y_b = x_b cos + x_a sin      for the pair (a, b) of j
 //   bf16 cache: y rounded;  int8: scale = max |y| / 127, codes = rint(y / scale)
 //   int8 index keys: the least e with max |y| <= 127 2^e, codes = rint(y 2^-e): a power of two, so that a code read back
-//   is a bf16 value exactly and the index scores are the same whichever kernel computes them.  A head with a value so near to
-//   a half that fp32 may be on its other side (1.5 % of them) is rotated again in 64 bits when the CTA's rows are done.
+//   is a bf16 value exactly.  A head with a value so near to a half that fp32 may be on its other side (1.5 % of them), or
+//   one past 32 bits' range, is rotated again in 64 bits when the CTA's rows are done: codes and exponents are whole numbers that
+//   decide which blocks are kept, and are the definition's, not one of two neighbours (as int8 keys' codes may be).
 // x turns_j is a 64-bit product modulo one turn, so the phase of a far
 // position is as exact as a near one's (fp32 angles lose 0.1 rad at 2^21);
 // its upper 32 bits, as a signed number of half turns, feed sincospi.

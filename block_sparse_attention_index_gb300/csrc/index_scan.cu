@@ -11,8 +11,8 @@
 //
 // The order of the dimensions inside a dot product is free: lane `tig` of a row takes the 16 dimensions 16 tig .., which
 // are one 16-byte load of codes, or two of bf16, and two of the queries.  Codes become bf16 exactly (7 instructions for 4);
-// their power of two multiplies the finished scores, position by position, before the maximum: exact too, so that integer
-// scores stay exact and every kernel that reads these keys finds the same maxima.
+// their power of two multiplies the finished scores, position by position, before the maximum: exact too, so that sums that
+// are exact in 32 bits stay so (others differ in their last bits between kernels that add in another order).
 //
 // Bound by memory: 65 bytes a position and head with codes, 128 without; a group's are read once instead of once a
 // sequence.  With many rows the products take over: eight rows of a head and a block are 16 mma and about 80 other

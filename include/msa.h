@@ -157,8 +157,14 @@ typedef struct msa_problem {
      * MSA_IK_BF16 (0): ik is bf16.  MSA_IK_INT8 (1): ik is int8 codes of the
      * same shape with a power of two for each (cache row, index head),
      *     ik[t, h, d] = ik8[row, h, d] * 2^ik_exp[row, h]
-     * (exactly a bf16 value; -128 stands for a key that is not finite, whose
-     * score is NaN and is passed over in a block's maximum).  ik_exp is device
+     * (exactly a bf16 value, but for |code| >= 64 with 2^122, which is past
+     * bf16: infinite for prompt chunks, the number itself elsewhere.  -128
+     * stands for a key that is not finite, whose score is NaN and is passed
+     * over in a block's maximum).  Scores are sums of 64 products in fp32,
+     * whose order differs between decode rows, prompt chunks and
+     * msa_index_scores, as with bf16 keys: they agree to 2^-17 of
+     * sum_d |iq_d ik_d|, and exactly where the sums are exact, so blocks
+     * that are nearer than that may be chosen differently.  ik_exp is device
      * int8 [cache_tokens, H] (H -> 1 with a shared index key), 16-byte aligned.
      * Read by msa_forward and msa_index_scores, written by msa_append_cache. */
     int32_t ik_dtype;
@@ -387,7 +393,8 @@ typedef struct msa_append {
  *   e = the smallest integer >= -126 with max_d |y_d| <= 127 2^e,
  *   code_d = round-to-nearest-even(y_d / 2^e)
  * (-126 for a zero head, -128 and zero codes for one that holds a NaN or an
- * infinity; e and the codes are those of the rotation in 64 bits).  Cache rows of other positions are left as they were, and so
+ * infinity; e and the codes are those of the rotation in 64 bits, as they decide
+ * which blocks are kept; those of int8 keys may be the other neighbour of a half).  Cache rows of other positions are left as they were, and so
  * are rows of q_out and iq_out at or past cu_rows[num_seqs].  Two positions
  * that share a cache row (a page listed twice) are the caller's error.
  * Metadata errors go to the error word in the workspace's first 4 bytes, as
