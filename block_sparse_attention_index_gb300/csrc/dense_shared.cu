@@ -33,8 +33,8 @@
 // same line by arithmetic (slot = item + CTA, which is different for every pair of them that meets, as both ascend along
 // the line).  Parts lie [dim / 4][row][4], so that the rows of a tile are stored and loaded in whole lines.
 //
-// Numerics.  bf16 outputs: weights as one bf16 (2^-8 at most, at random), and at most 32,768 keys to a part, as the
-// tensor cores cut what an addition loses instead of rounding it (2^-24 an addition of 16 keys).  fp32 outputs: weights
+// Numerics.  bf16 outputs: weights as one bf16 (2^-8 at most, at random), and at most 32,768 keys to a sum in tensor memory (longer
+// ones are added up in the CTA's part), as the tensor cores cut what an addition loses instead of rounding it (2^-24 an addition of 16 keys).  fp32 outputs: weights
 // as three bf16 parts, NK = 64, O taken from tensor memory every second tile and summed in registers.
 //
 // Bound by the tensor pipe where many rows share (two M tiles: 1.55 us a tile of 128 keys for 1.3 at the pipe's rate), by
@@ -54,7 +54,7 @@ namespace msa {
 // Softmax groups: warps 0-3, 4-7; 8 and 10 copies, 9 and 11 matrix instructions; int8 caches: 12-15 make bf16 of the codes.
 constexpr int kDsThreads = 384, kDsThreadsInt8 = 512;
 constexpr int kDsQBytes = 128 * kHeadDim * 2;
-constexpr int kDsPartKeys = 32768;  // most keys of a part
+constexpr int kDsPartKeys = 32768;  // most keys of a sum in tensor memory
 // Lengths on the line, in half tiles: a key tile of one M tile, of two, and what an item counts for besides.
 constexpr int kDsSingle = 2, kDsPair = 3, kDsExtra = 3;
 constexpr int kDsInfo = 4;          // items published ahead
@@ -67,6 +67,7 @@ struct DsItem {
     int h, key, end;   // KV head; first key of the share; end of the entry's keys
     int tiles, pair;   // key tiles; two M tiles (or one, the stages on alternate key tiles)
     int cap;           // rows of a stage's part
+    int more;          // 1: earlier keys of the item are in its parts already
     int64_t part;      // first row of its parts in the workspace
 };
 
@@ -81,7 +82,7 @@ struct DsCfg {
     static constexpr int kScales = 8;
     static constexpr int kThreads = kInt8 ? kDsThreadsInt8 : kDsThreads;
     static constexpr int kSAt = kParts == 1 ? 0 : 64;  // column of S in its 128 (as in the prompt kernel: P's parts from 0 on)
-    static constexpr int kRun = kDsPartKeys / NK;      // most tiles of a part
+    static constexpr int kRun = kDsPartKeys / NK;      // most tiles of a sum
 };
 
 template <int kParts, bool kInt8>
@@ -157,9 +158,9 @@ __device__ __forceinline__ DsEntry ds_seq(const SharedArgs& a, int b, int& g, bo
     return DsEntry{b, c0, n, S, L - n};
 }
 
-// How an entry lies on the line: `units` items a head (of up to two M tiles), each `chunks` parts of up to `run` tiles.
+// How an entry lies on the line: `units` items a head (of up to two M tiles), each `chunks` pieces of up to `run` tiles.
 struct DsSize {
-    int tiles, chunks, units, unit, w;  // key tiles; parts they make; items a head; an item's length on the line, a tile's
+    int tiles, chunks, units, unit, w;  // key tiles; pieces they make; items a head; an item's length on the line, a tile's
 };
 __device__ __forceinline__ DsSize ds_size(const SharedArgs& a, const DsEntry& x, int NK) {
     DsSize s{};
@@ -183,7 +184,7 @@ __device__ __forceinline__ DsEntry ds_entry(const SharedArgs& a, int e, bool& ba
     return x;
 }
 
-// Tiles of a part that begin before x on the line from its first tile on.
+// Tiles of a piece that begin before x on the line from its first tile on.
 __device__ __forceinline__ int ds_tiles_before(int x, int w) {
     return x <= 0 ? 0 : (w == kDsPair ? (x + kDsPair - 1) / kDsPair : (x + kDsSingle - 1) / kDsSingle);
 }
@@ -223,6 +224,47 @@ __device__ __forceinline__ void ds_times32(float* x, uint32_t at) {
 }
 __device__ __forceinline__ void ds_st_shared(uint32_t at, uint4 w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+
+// A later piece of an item's keys: its O (tensor memory), maximum and sum are added to what this thread has stored of the
+// earlier ones, so that parts are as many as items and CTAs, however long the keys.  A piece without a key above -inf says
+// nothing, unless its sum is NaN.  By the whole warp.
+__device__ __forceinline__ void ds_add_piece(uint32_t o_addr, float4* dst, int cap, float2* ml, bool mine, float top, float sum) {
+    const float2 was = mine ? *ml : make_float2(-INFINITY, 0.f);
+    const bool before = was.x != -INFINITY || was.y != was.y, now = mine && (top != -INFINITY || sum != sum);
+    const float most = fmaxf(was.x, top);
+    const float f0 = was.x == -INFINITY ? was.y : dp_exp2(was.x - most), f1 = top == -INFINITY ? sum : dp_exp2(top - most);
+#pragma unroll 1
+    for (int q = 0; q < kHeadDim / 32; ++q) {
+        float y[32];
+        dp_ld32(o_addr + 32 * q, y);
+        tmem_ld_wait();
+        if (before && now) {
+            float4 o[8];  // (the loads first: each behind a store would take its latency, 11 us at three groups)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[d] = dst[static_cast<int64_t>(8 * q + d) * cap];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                y[4 * d] = fmaf(o[d].x, f0, y[4 * d] * f1);
+                y[4 * d + 1] = fmaf(o[d].y, f0, y[4 * d + 1] * f1);
+                y[4 * d + 2] = fmaf(o[d].z, f0, y[4 * d + 2] * f1);
+                y[4 * d + 3] = fmaf(o[d].w, f0, y[4 * d + 3] * f1);
+            }
+        }
+        if (now) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d)
+                dst[static_cast<int64_t>(8 * q + d) * cap] = make_float4(y[4 * d], y[4 * d + 1], y[4 * d + 2], y[4 * d + 3]);
+        }
+        __syncwarp();  // the next load is the whole warp's
+    }
+    if (now) *ml = before ? make_float2(most, fmaf(was.y, f0, sum * f1)) : make_float2(top, sum);
+}
+
+// Few items have more than one piece: a call where registers are short (fp32 outputs 37.3 us, inline 38.0; int8 57.3 and 58.3;
+// 64 sequences in bf16 88.8, inline 79.7).
+__device__ __noinline__ void ds_call_add_piece(uint32_t o_addr, float4* dst, int cap, float2* ml, bool mine, float top, float sum) {
+    ds_add_piece(o_addr, dst, cap, ml, mine, top, sum);
 }
 
 template <int kParts, bool kInt8>
@@ -288,7 +330,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             const DsEntry x = ds_entry(a, e, bad);
             const DsSize s = ds_size(a, x, NK);
             len = static_cast<int64_t>(a.H) * s.units * s.unit;
-            items = a.H * s.units * s.chunks;
+            items = a.H * s.units;
             e_mine = e;
             y = SharedEntry{0, 0, x.b, x.row, x.rows, x.key, x.end};
             if (blockIdx.x == 0) {
@@ -378,11 +420,12 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             const int half = warp == 10;
             int slot = 0, sent[3] = {0, 0, 0}, q_used[2] = {0, 0};  // copies in all and by barrier row; items by query buffer
             bool alive = true;
-            // The CTA's walk along the line, item after item (of one KV head h, unit u and part ch of the entry's keys; `at`
-            // lies `on` tiles behind the item's beginning); the entry after the present one is loaded ahead.
+            // The CTA's walk along the line, piece after piece (of one KV head h, unit u and piece ch of the entry's keys; `at`
+            // lies `on` tiles behind its beginning; `more`: the item has parts of this CTA); the entry after the present one
+            // is loaded ahead.
             int64_t at = from;
             const int64_t stop = ds_cut(line, blockIdx.x + 1, shares);
-            int e = sm.first, h = 0, u = 0, ch = 0, on = 0;
+            int e = sm.first, h = 0, u = 0, ch = 0, on = 0, more = 0;
             SharedEntry x = sm.first_entry, ahead = x;
             DsSize sz = ds_size(a, DsEntry{x.b, x.row, x.rows, x.key, x.end}, NK);
             if (half) {
@@ -417,13 +460,15 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                         it.tiles = t1 - t0;
                         it.pair = it.rows > P;
                         it.cap = group ? a.group_rows : a.seq_rows;
-                        const int64_t place = x.parts + (h * sz.units + u) * sz.chunks + ch + static_cast<int>(blockIdx.x);
+                        it.more = more;
+                        more = 1;
+                        const int64_t place = x.parts + (h * sz.units + u) + static_cast<int>(blockIdx.x);
                         it.part = group ? place * 2 * a.group_rows : a.seq_part0 + (place - group_parts) * 2 * a.seq_rows;
                     }
                     at += len;
                     on = 0;  // (the share ends here if the item does not)
                     if (++ch == sz.chunks) {
-                        ch = 0;
+                        ch = more = 0;
                         if (++u == sz.units) {
                             u = 0;
                             if (++h == a.H) {
@@ -995,8 +1040,20 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
             tc_fence_after();
             const int64_t row0 = item.part + s * item.cap;
             float4* dst = reinterpret_cast<float4*>(a.part_o) + row0 * (kHeadDim / 4) + m;
+            float2* ml = reinterpret_cast<float2*>(a.part_ml + (row0 + m) * 2);
+            if (count > 0) collect();
+            if (item.more) {  // a later piece: from tensor memory, whatever the form
+                if constexpr (kParts > 1) {
+#pragma unroll
+                    for (int q = 0; q < kHeadDim / 32; ++q) dp_st32(o_addr + 32 * q, reinterpret_cast<const uint32_t*>(acc + 32 * q));
+                    dp_st_wait();
+                }
+                constexpr auto add = kParts > 1 || kInt8 ? ds_call_add_piece : ds_add_piece;
+                add(o_addr, dst, item.cap, ml, mine, count > 0 ? top : -INFINITY, count > 0 ? sum : 0.f);
+                tc_fence_before();
+                continue;
+            }
             if (count > 0) {
-                collect();
 #pragma unroll(kParts > 1 ? 4 : 1)
                 for (int q = 0; q < kHeadDim / 32; ++q) {
                     float y[32];
@@ -1016,7 +1073,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
                 }
             }
             tc_fence_before();
-            if (mine) *reinterpret_cast<float2*>(a.part_ml + (row0 + m) * 2) = make_float2(count > 0 ? top : -INFINITY, count > 0 ? sum : 0.f);
+            if (mine) *ml = make_float2(count > 0 ? top : -INFINITY, count > 0 ? sum : 0.f);
         }
     }
     __syncwarp();
@@ -1031,7 +1088,7 @@ __global__ void __launch_bounds__(kInt8 ? kDsThreadsInt8 : kDsThreads, 1) dense_
 
 // Joins the parts of a row's pairs of KV head h with the row's own keys.  CTA (row, h, z): a quarter or half of the 128
 // dimensions, a thread 4 of them of one query head.
-struct DsRun {  // parts of a row's M tile that lie behind one another: `count` of `cap` rows, `step` rows apart
+struct DsRun {  // parts of a row's M tile that lie behind one another: `count` of `cap` rows, `step` rows apart (none: 0)
     int64_t row0;
     int count, step, cap, m;  // m: row of its first head in a part
 };
@@ -1040,8 +1097,8 @@ template <bool kInt8, int kResident>
 __global__ void __launch_bounds__(256, kResident) dense_shared_join(const SharedArgs a, int grid, int NK) {
     __shared__ float own[kMaxGroup][kDecodeMaxRows];  // scores of the row's own keys (log2 domain)
     __shared__ int64_t own_row[kDecodeMaxRows];
-    __shared__ DsRun runs[32];
-    __shared__ int row_keys, num_runs;
+    __shared__ DsRun runs[2];  // of the group's keys, of the sequence's own
+    __shared__ int row_keys;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, h = blockIdx.y, r = blockIdx.x;
     // Where everything lies is found out by one warp (by all of them: 1,360 instructions a warp, and 37 us for 32 at 256 rows
     // of 4 x 16 heads, by itself).
@@ -1125,90 +1182,75 @@ __global__ void __launch_bounds__(256, kResident) dense_shared_join(const Shared
         if (lane == 0) *a.err = e;
     }
     if (own_keys == 0) return;
-    // ---- the parts, some runs and parts at a time
+    // ---- the parts, those of the group's keys and then those of the sequence's
     const int groups = a.num_groups, entries = groups + a.num_seqs;
-    int chunk = 0;  // (warp 0: the next part of the group's keys, then of the sequence's)
-    auto make_runs = [&]() {
-        const SharedEntry total = ds_load(a.entries + entries);
+    if (warp == 0) {
+        const bool group = lane == 0;
+        const SharedEntry total = ds_load(a.entries + entries), y = ds_load(a.entries + (group && g >= 0 ? g : groups + lo));
         const int group_parts = a.entries[groups].parts;
-        int n = -1;
-        if (total.b >= 0) {  // (not more than the host's bounds allow for)
-            const int P = 128 / a.G, shares = ds_shares(total.line, grid), run = kDsPartKeys / NK;
-            DsSize sg{};
-            SharedEntry eg{};
-            if (g >= 0) {
-                eg = ds_load(a.entries + g);
-                sg = ds_size(a, DsEntry{eg.b, eg.row, eg.rows, eg.key, eg.end}, NK);
+        if (lane < 2) {
+            DsRun out{};
+            if (total.b < 0) {
+                out.count = -1;  // more than the host's bounds allow for
+            } else if (!group || g >= 0) {
+                const DsSize s = ds_size(a, DsEntry{y.b, y.row, y.rows, y.key, y.end}, NK);
+                const int i = r - y.row;
+                if (s.units > 0 && i >= 0 && i < y.rows) {  // (rows outside: cu_rows does not ascend)
+                    const int P = 128 / a.G, shares = ds_shares(total.line, grid);
+                    const int tile = i < P ? 0 : i / P, u = tile / 2, uh = h * s.units + u;
+                    const bool pair = y.rows - u * 2 * P > P;
+                    out.cap = group ? a.group_rows : a.seq_rows;
+                    out.m = (i - tile * P) * a.G;
+                    const int64_t begin = y.line + static_cast<int64_t>(uh) * s.unit;
+                    // the CTAs of its first and last tiles
+                    const int c0 = ds_owner(total.line, begin + kDsExtra, shares), c1 = ds_owner(total.line, begin + s.unit - s.w, shares);
+                    const int64_t place = y.parts + uh + c0;
+                    out.row0 = (group ? place * 2 * out.cap : a.seq_part0 + (place - group_parts) * 2 * out.cap) + (pair ? tile & 1 : 0) * out.cap;
+                    out.count = (c1 - c0 + 1) * (pair ? 1 : 2);  // (one M tile: both stages' parts)
+                    out.step = pair ? 2 * out.cap : out.cap;
+                }
             }
-            const DsSize ss = ds_size(a, x, NK);
-            n = min(sg.chunks + ss.chunks - chunk, 32);
-            const bool group = chunk + lane < sg.chunks;
-            const SharedEntry y = group ? eg : ds_load(a.entries + groups + lo);
-            const DsSize s = group ? sg : ss;
-            const int ch = chunk + lane - (group ? 0 : sg.chunks);
-            if (lane < n) {
-                const int i = r - y.row, tile = i < P ? 0 : i / P, u = tile / 2, uh = h * s.units + u;
-                const bool pair = y.rows - u * 2 * P > P;
-                DsRun out;
-                out.cap = group ? a.group_rows : a.seq_rows;
-                out.m = (i - tile * P) * a.G;
-                const int64_t begin = y.line + static_cast<int64_t>(uh) * s.unit + ch * (run * s.w + kDsExtra) + kDsExtra;
-                const int tiles = min(run, s.tiles - ch * run);
-                const int c0 = ds_owner(total.line, begin, shares), c1 = ds_owner(total.line, begin + (tiles - 1) * s.w, shares);
-                const int64_t place = y.parts + uh * s.chunks + ch + c0;
-                out.row0 = (group ? place * 2 * out.cap : a.seq_part0 + (place - group_parts) * 2 * out.cap) + (pair ? tile & 1 : 0) * out.cap;
-                out.count = (c1 - c0 + 1) * (pair ? 1 : 2);  // (one M tile: both stages' parts)
-                out.step = pair ? 2 * out.cap : out.cap;
-                runs[lane] = out;
-            }
-            chunk += n;
-            if (chunk < sg.chunks + ss.chunks) n |= 1 << 8;  // more to come
+            runs[lane] = out;
         }
-        if (lane == 0) num_runs = n;
-    };
-    do {
-        if (warp == 0) make_runs();
-        __syncthreads();
-        if (num_runs < 0) return;
-        for (int k = 0; k < (num_runs & 255) && there; ++k) {
-            const DsRun run = runs[k];
-            const int m = run.m + gh;
-            constexpr int kAtOnce = kResident > 1 ? 4 : 8;
-            for (int i0 = 0; i0 < run.count; i0 += kAtOnce) {
-                float4 v[kAtOnce];
-                float2 ml[kAtOnce];
+    }
+    __syncthreads();
+    if (runs[0].count < 0) return;
+    for (int k = 0; k < 2 && there; ++k) {
+        const DsRun run = runs[k];
+        const int m = run.m + gh;
+        constexpr int kAtOnce = kResident > 1 ? 4 : 8;
+        for (int i0 = 0; i0 < run.count; i0 += kAtOnce) {
+            float4 v[kAtOnce];
+            float2 ml[kAtOnce];
 #pragma unroll
-                for (int q = 0; q < kAtOnce; ++q) {
-                    const int64_t at = run.row0 + static_cast<int64_t>(min(i0 + q, run.count - 1)) * run.step;
-                    ml[q] = *reinterpret_cast<const float2*>(a.part_ml + (at + m) * 2);
-                    v[q] = reinterpret_cast<const float4*>(a.part_o)[at * (kHeadDim / 4) + static_cast<int64_t>(d4) * run.cap + m];
-                }
-                float most = top;
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int64_t at = run.row0 + static_cast<int64_t>(min(i0 + q, run.count - 1)) * run.step;
+                ml[q] = *reinterpret_cast<const float2*>(a.part_ml + (at + m) * 2);
+                v[q] = reinterpret_cast<const float4*>(a.part_o)[at * (kHeadDim / 4) + static_cast<int64_t>(d4) * run.cap + m];
+            }
+            float most = top;
 #pragma unroll
-                for (int q = 0; q < kAtOnce; ++q) most = fmaxf(most, ml[q].x);
-                const float f = top == -INFINITY ? 0.f : dp_exp2(top - most);
-                if (top != -INFINITY) {
-                    sum *= f;
-                    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-                }
-                top = most;
+            for (int q = 0; q < kAtOnce; ++q) most = fmaxf(most, ml[q].x);
+            const float f = top == -INFINITY ? 0.f : dp_exp2(top - most);
+            if (top != -INFINITY) {
+                sum *= f;
+                o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+            }
+            top = most;
 #pragma unroll
-                for (int q = 0; q < kAtOnce; ++q) {
-                    // A part without a key, or with none above -inf, says nothing (nor is its O read), unless its sum is NaN.  Any
-                    // other counts, also with a weight that is 0 in fp32: an infinite value in it shows.
-                    if (i0 + q >= run.count || (ml[q].x == -INFINITY && ml[q].y == ml[q].y)) continue;
-                    const float w = ml[q].x == -INFINITY ? ml[q].y : dp_exp2(ml[q].x - top);
-                    sum = fmaf(w, ml[q].y, sum);
-                    o.x = fmaf(w, v[q].x, o.x);
-                    o.y = fmaf(w, v[q].y, o.y);
-                    o.z = fmaf(w, v[q].z, o.z);
-                    o.w = fmaf(w, v[q].w, o.w);
-                }
+            for (int q = 0; q < kAtOnce; ++q) {
+                // A part without a key, or with none above -inf, says nothing (nor is its O read), unless its sum is NaN.  Any
+                // other counts, also with a weight that is 0 in fp32: an infinite value in it shows.
+                if (i0 + q >= run.count || (ml[q].x == -INFINITY && ml[q].y == ml[q].y)) continue;
+                const float w = ml[q].x == -INFINITY ? ml[q].y : dp_exp2(ml[q].x - top);
+                sum = fmaf(w, ml[q].y, sum);
+                o.x = fmaf(w, v[q].x, o.x);
+                o.y = fmaf(w, v[q].y, o.y);
+                o.z = fmaf(w, v[q].z, o.z);
+                o.w = fmaf(w, v[q].w, o.w);
             }
         }
-        if (num_runs < 256) break;
-        __syncthreads();  // before the runs are others
-    } while (true);
+    }
     if (!there) return;
     const float inv = 1.f / sum;
     const int64_t at = (q_row + gh) * kHeadDim + 4 * d4;
@@ -1241,22 +1283,23 @@ static cudaError_t launch_shared(const SharedArgs& a, int grid, cudaStream_t str
     const int threads = (a.G * (kHeadDim / 4 / z) + 31) / 32 * 32;
     cfg.gridDim = dim3(static_cast<unsigned>(a.total_rows), static_cast<unsigned>(a.H), static_cast<unsigned>(z));
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    // four CTAs an SM where they are many (three or five: 3% to 8% more at 73 and 256 rows); few take more loads at once
+    // four CTAs an SM where they are many (three or five: 3% to 8% more at 73 and 256 rows); few take more loads at once, and
+    // shared memory that they do not use, so that an SM need not divide it anew behind the first kernel (fp32, 16 rows: 37.0 and
+    // 36.2 us; 73 rows, which are many: 70.8 and 72.0)
     const bool many = blocks > device_sm_count();
+    cfg.dynamicSmemBytes = many ? 0 : 40000;
     auto* join = a.kv_int8 ? (many ? dense_shared_join<true, 4> : dense_shared_join<true, 1>)
                            : (many ? dense_shared_join<false, 4> : dense_shared_join<false, 1>);
     return cudaLaunchKernelEx(&cfg, join, a, grid, DsCfg<kParts, kInt8>::NK);
 }
 
 SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int total_rows, int max_rows_per_seq, int max_group_rows,
-                             int max_shared_len, int max_cache_len) {
+                             int max_shared_len) {
     SharedRoom r;
     const int64_t P = 128 / G, units = total_rows / (2 * P) + num_groups;
-    auto chunks = [](int64_t keys) { return (keys + kDsPartKeys - 1) / kDsPartKeys; };
     r.grid = std::min(device_sm_count(), kDenseMaxShares);
-    r.group_parts = max_shared_len < kBlock ? 0 : units * H * chunks(max_shared_len);
-    r.seq_parts = static_cast<int64_t>(num_seqs) * H * chunks(max_cache_len);
+    r.group_parts = max_shared_len < kBlock ? 0 : units * H;
+    r.seq_parts = static_cast<int64_t>(num_seqs) * H;
     r.group_rows = static_cast<int>(std::min(P, static_cast<int64_t>(max_group_rows)) * G);
     r.seq_rows = std::min(max_rows_per_seq, kDecodeMaxRows) * G;
     r.seq_part0 = (r.group_parts > 0 ? (r.group_parts + kDenseMaxShares) * 2 * r.group_rows : 0);

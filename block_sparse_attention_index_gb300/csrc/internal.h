@@ -321,7 +321,7 @@ struct SharedRoom {
     int group_rows = 0, seq_rows = 0;
 };
 SharedRoom dense_shared_room(int num_seqs, int num_groups, int H, int G, int total_rows, int max_rows_per_seq, int max_group_rows,
-                             int max_shared_len, int max_cache_len);
+                             int max_shared_len);
 cudaError_t run_dense_shared(const SharedArgs& a, int grid, cudaStream_t stream);
 
 // Allocation-free decode attention: scratch in a file-scope device array

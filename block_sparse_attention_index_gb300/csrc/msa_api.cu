@@ -345,7 +345,7 @@ struct SharedLayout {
 SharedLayout shared_layout(const msa_problem* p) {
     SharedLayout l;
     l.room = msa::dense_shared_room(p->num_seqs, p->num_groups, p->num_kv_heads, p->group_size, p->total_rows, p->max_rows_per_seq,
-                                    p->max_group_rows, p->max_shared_len, p->max_cache_len);
+                                    p->max_group_rows, p->max_shared_len);
     const size_t entries = static_cast<size_t>(p->num_groups) + p->num_seqs + 1, rows = static_cast<size_t>(l.room.rows);
     size_t off = 256;
     l.err_slots = off;

@@ -407,9 +407,8 @@ msa_status msa_append_cache(const msa_problem* p, const msa_append* a, const msa
 /* Bytes of scratch that msa_dense_forward needs for problem p (host only;
  * same conventions and error word as msa_workspace_size).  With groups it grows
  * with the parts that the host's bounds allow for: about 1 KB for each
- * (sequence, KV head, up to 32,768 of max_cache_len positions, row, query head
- * of the group) and for each (shared row, query head, 32,768 of
- * max_shared_len). */
+ * (sequence, KV head, query head of it, row of max_rows_per_seq) and for each
+ * (row, query head), whatever the lengths, beside up to 43 MB. */
 msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
 
 /* Attention over every cached position (top_k plays no part):
