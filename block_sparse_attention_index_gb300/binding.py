@@ -175,7 +175,11 @@ class Problem:
     shared: groups of neighbouring sequences, from the first on, whose block
     tables begin alike: [(sequences, positions), ...], the positions that lie
     in the same cache rows, before every row of the group.  forward and
-    dense_forward then read them once a group; the results are the same.
+    dense_forward then read them once a group.  Results are the formula's as
+    without: forward's the same bits wherever index scores are exact;
+    dense_forward's weights have fewer bits with bf16 outputs (2^-8, where
+    decode rows have 2^-16 and 2^-11 over int8 caches without groups; with
+    fp32 outputs the same 2^-24).
     """
 
     def __init__(self, H, G, seqs_host, device, top_k=16, scale=None, out_dtype=torch.float32,

@@ -33,9 +33,12 @@
 // same line by arithmetic (slot = item + CTA, which is different for every pair of them that meets, as both ascend along
 // the line).  Parts lie [dim / 4][row][4], so that the rows of a tile are stored and loaded in whole lines.
 //
-// Numerics.  bf16 outputs: weights as one bf16 (2^-8 at most, at random), and at most 32,768 keys to a sum in tensor memory (longer
-// ones are added up in the CTA's part), as the tensor cores cut what an addition loses instead of rounding it (2^-24 an addition of 16 keys).  fp32 outputs: weights
-// as three bf16 parts, NK = 64, O taken from tensor memory every second tile and summed in registers.
+// Numerics.  bf16 outputs: weights as one bf16 (2^-8 at most, at random), as prompt chunks have them and decode rows without
+// groups have not (two parts; int8 caches: f16).  Two parts here are 71 us for 57 at 32 sequences over an int8 cache, whose
+// error against the formula they lower from 2.4e-3 to 1.7e-3 in the norm, the output's own rounding (a cached value is off by
+// up to 1/254 of its head's largest).  At most 32,768 keys to a sum in tensor memory (longer ones are added up in the CTA's
+// part), as the tensor cores cut what an addition loses instead of rounding it (2^-24 an addition of 16 keys).  fp32 outputs:
+// weights as three bf16 parts, NK = 64, O taken from tensor memory every second tile and summed in registers.
 //
 // Bound by the tensor pipe where many rows share (two M tiles: 1.55 us a tile of 128 keys for 1.3 at the pipe's rate), by
 // the chain of one tile's scores, weights and products elsewhere (2.7 us a stage: own positions go at 48 KB a us and SM,

@@ -174,8 +174,9 @@ typedef struct msa_problem {
      * group_starts[g] .. group_starts[g+1]-1; the first group_shared[g]
      * positions of each of them lie in the same cache rows (their block
      * tables begin alike), and every row lies past them (L_b - n_b >=
-     * group_shared[g]).  A statement about the caches, not an option: outputs
-     * are the formula's with or without it.  msa_dense_forward and msa_forward
+     * group_shared[g]).  A statement about the caches: outputs are the
+     * formula's with or without it, to the numerics of msa_dense_forward,
+     * whose weights have fewer bits with bf16 outputs.  msa_dense_forward and msa_forward
      * read what is shared (whole 64-position blocks of it, by the block table
      * of the group's first sequence, which needs one even if it has no rows)
      * once for the group's rows instead of once a sequence; the other entry
@@ -438,7 +439,8 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  * chunks are.  The same call gives the same bits every time.
  * A later token's key, value or scale, of any size, infinite or NaN, does not
  * reach the rows before it.  An infinite value that a row does see makes outputs
- * infinite or NaN.  int8 caches, up to 8 rows a sequence: 64 positions with a value
+ * infinite or NaN (without groups, one whose weight is below 2^-126 of the row's
+ * largest may not where its keys were split).  int8 caches, up to 8 rows a sequence: 64 positions with a value
  * scale below 2^-14 of the largest of theirs and of those met before are summed
  * in fp32.  Prompt chunks: rows that a later token's value would spoil, and int8
  * rows that meet scales more than 2^22 apart in 64 positions, are computed again
@@ -447,8 +449,10 @@ msa_status msa_dense_workspace_size(const msa_problem* p, size_t* bytes);
  *
  * Groups (num_groups > 0): keys and values that a group shares are read once for
  * every 256 / G of its rows.  Weights enter the products with V as one bf16 part
- * (2^-8, bf16 outputs) or three (fp32), with an int8 cache times the value's scale,
- * beside exact codes; a row's and its window's own positions are fp32.
+ * (2^-8, bf16 outputs; fewer bits than decode rows have without groups) or three
+ * (fp32), with an int8 cache times the value's scale, beside exact codes; a row's and
+ * its window's own positions are fp32.  Every row of the batch is computed so, also
+ * those of sequences without a group.
  *
  * out must not overlap q or the caches.  The workspace's contents need no
  * initialisation; calls that share one must be ordered (one stream, or events).
