@@ -55,6 +55,8 @@ __device__ __forceinline__ void ix_mma(float (&c)[4], const uint32_t (&a)[4], ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr uint32_t kLineMost = 1u << 30;  // longer than any batch's line
+
 // Entry e of the line: a group's shared positions or (behind the groups) a sequence's own.
 struct IxEntry {
     int b;            // sequence whose table is read
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_s
         for (int i = tid; i < a.n_clear; i += Cfg::kThreads) a.clear_words[i] = 0;
     // exclusive sums over `count` values, in order, kThreads at a time; returns the sum
     auto scan = [&](int count, auto value, int32_t* to) {
-        int64_t carry = 0;
+        uint32_t carry = 0;
         for (int base = 0; base < count; base += Cfg::kThreads) {
             const int i = base + tid, mine = i < count ? value(i) : 0;
             int incl = mine;
@@ -166,10 +168,10 @@ __global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_s
             }
             if (lane == 31) warp_tot[warp] = incl;
             __syncthreads();
-            int64_t before = carry;
+            uint32_t before = carry;
             for (int w = 0; w < kWarps; ++w) {
                 if (w < warp) before += warp_tot[w];
-                carry += warp_tot[w];
+                carry = min(carry + warp_tot[w], kLineMost);
             }
             if (i < count) to[i] = static_cast<int32_t>(before + incl - mine);
             __syncthreads();
@@ -179,18 +181,18 @@ __global__ void __launch_bounds__(IxCfg<H, kShared, kInt8>::kThreads, 1) index_s
     // The line of a batch within the host's bounds is shorter than 2^30 (4,096 sequences of 2^15 blocks, 2^15 rows of groups).
     // Groups that overlap, as their starts or cu_rows do not ascend, may make it longer (of 32 neighbours every second at
     // most is such a group: a warp's sum is below 2^31): nothing is scanned then.
-    const int64_t length = scan(entries, [&](int e) {
+    const uint32_t length = scan(entries, [&](int e) {
         const IxEntry x = ix_entry(a, e);
         return x.units * x.weight;
     }, line);
-    const int total = length > INT32_MAX ? 0 : static_cast<int>(length);
+    const int total = length >= kLineMost ? 0 : static_cast<int>(length);
     if (tid == 0) {
         line[entries] = total;
-        if (total != length) atomicOr(&err, kErrBadMetadata);
+        if (length >= kLineMost) atomicOr(&err, kErrBadMetadata);
     }
     if (blockIdx.x == 0) {
         if (a.drow_prefix != nullptr) {  // rows of the decode family before each sequence, for the attention's grid
-            const int64_t rows = scan(a.num_seqs, [&](int b) {
+            const uint32_t rows = scan(a.num_seqs, [&](int b) {
                 const int n = a.cu_rows[b + 1] - a.cu_rows[b];
                 return n >= 1 && n <= kDecodeMaxRows ? n : 0;
             }, a.drow_prefix);

@@ -92,3 +92,23 @@ def test_more_parts_than_the_host_allows_for():
     assert msa().error_word(ws) == msa().ERR_BAD_METADATA and bool((guard == 0xA5).all())
     word, intact, _ = forward(a, pb)
     assert intact and word == msa().ERR_BAD_METADATA
+
+
+def test_a_line_longer_than_any_batch():
+    """256 groups that overlap, each of 4,096 rows and 2^15 blocks: 2^31 and more units of time in all."""
+    m = msa()
+    B, n, most = 512, 8, 1 << 21
+    table = torch.zeros(B, most // 64, dtype=torch.int32, device="cuda")
+    pb = m.Problem(1, 1, [(n, 264)] * B, "cuda", block_table=table, page_size=64, cache_tokens=64, shared=[(1, 256)] * B)
+    pb.c.max_cache_len = pb.c.max_shared_len = most
+    pb.c.max_group_rows = B * n
+    pb.group_starts.copy_(torch.tensor([B * (i % 2) for i in range(B + 1)], dtype=torch.int32))
+    pb.group_shared.fill_(most)
+    q = torch.zeros(B * n, 1, 128, dtype=torch.bfloat16, device="cuda")
+    iq = torch.zeros(B * n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(64, 1, 128, dtype=torch.bfloat16, device="cuda")
+    ik = torch.zeros(64, 1, 64, dtype=torch.bfloat16, device="cuda")
+    ws, guard = guarded(pb, pb.workspace_size())
+    m.forward(pb, q, iq, k, k, ik, workspace=ws)
+    torch.cuda.synchronize()
+    assert m.error_word(ws) == m.ERR_BAD_METADATA and bool((guard == 0xA5).all())
