@@ -179,7 +179,9 @@ class Problem:
     without: forward's the same bits wherever index scores are exact;
     dense_forward's weights have fewer bits with bf16 outputs (2^-8, where
     decode rows have 2^-16 and 2^-11 over int8 caches without groups; with
-    fp32 outputs the same 2^-24).
+    fp32 outputs the same 2^-24).  dense_forward is slower with groups than
+    without where little is shared (2 sequences behind 512 positions: 16 us
+    for 11; int8 caches with long positions of their own: up to 2.5 times).
     """
 
     def __init__(self, H, G, seqs_host, device, top_k=16, scale=None, out_dtype=torch.float32,

@@ -43,9 +43,11 @@
 // Bound by the tensor pipe where many rows share (two M tiles: 1.55 us a tile of 128 keys for 1.3 at the pipe's rate), by
 // the chain of one tile's scores, weights and products elsewhere (2.7 us a stage: own positions go at 48 KB a us and SM,
 // about HBM's rate over all SMs), and by its beginning: 5 us to the first copy, 7 to 8 to the first scores.
-// Measured, whole calls of 4 x 16 heads: 64 sequences behind 32,768 positions and 100 to 2,000 of their own, 86 us (prefix
-// once and own positions: 24.6 us of memory, 35.8 of products; without `shared` 408 us); 256 behind 8,192, 138 us; 8 behind
-// 1,984, 19 us; int8, 32 behind 16,384, 57 us; 16 behind 8,192 with fp32 outputs, 36.5 us.
+// Measured, whole calls of 4 x 16 heads: 64 sequences behind 32,768 positions and 100 to 2,000 of their own, 81 us (prefix
+// once and own positions: 24.6 us of memory, 35.8 of products; without groups 408 us); 256 behind 8,192, 132 us; 8 behind
+// 1,984, 18.5 us (17.7); int8, 32 behind 16,384, 57 us (96); 16 behind 8,192 with fp32 outputs, 36.4 us (46).  Where little
+// is shared the calls take longer than without groups: 6 us of beginning and join (int8 10), and own positions cost, for what
+// they cost there, 1.05 (bf16), 1.5 (fp32 outputs), 2.4 (int8) and 3 times (int8, fp32 outputs).
 #include <algorithm>
 
 #include "common.cuh"

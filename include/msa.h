@@ -181,7 +181,8 @@ typedef struct msa_problem {
      * of the group's first sequence, which needs one even if it has no rows)
      * once for the group's rows instead of once a sequence; the other entry
      * points do not look at groups.  With groups: a block table, and sequences
-     * of at most 8 rows (max_rows_per_seq <= 8).  A group that breaks its
+     * of at most 8 rows (max_rows_per_seq <= 8; a batch that also holds prompt
+     * chunks is two calls, or goes without groups).  A group that breaks its
      * bounds, or a row before the end of its group's shared positions, is bad
      * metadata. */
     int32_t num_groups;          /* at most num_seqs                            */
